@@ -66,7 +66,9 @@ WORKLOAD_TEXT = ("exact-attention hot path: long-context causal prefill B2 H32 N
 NOMINAL_HBM_GBS = 8000.0
 PROFILES = os.path.join(ROOT, "profiles")
 KERNEL_SOURCES = {
-    "prefill": ["exact_attention_33_gb300/csrc/prefill.cu", "exact_attention_33_gb300/csrc/ptx.cuh",
+    "prefill": ["exact_attention_33_gb300/csrc/prefill.cu",
+                "exact_attention_33_gb300/csrc/prefill_kernel.cuh",
+                "exact_attention_33_gb300/csrc/ptx.cuh",
                 "exact_attention_33_gb300/csrc/fa_internal.h",
                 "exact_attention_33_gb300/csrc/checks.cuh"],
     "decode": ["exact_attention_33_gb300/csrc/decode.cu", "exact_attention_33_gb300/csrc/ptx.cuh",

@@ -1,7 +1,7 @@
 """Exact attention for GB300 (sm_103a): thin Python binding of libfa.so.
 
 Every function here only marshals torch tensors into the C ABI declared in
-``include/fa.h`` (device pointers, sizes, the current CUDA stream) and checks
+``include/fa.h`` and ``include/fa_window.h`` (device pointers, sizes, the current CUDA stream) and checks
 the returned status; all arithmetic runs in the library's CUDA kernels.  There
 is no fallback: if ``libfa.so`` is missing or a call fails, an exception is
 raised.
@@ -25,6 +25,9 @@ __all__ = [
     "fa_fwd_splitkv", "fa_fwd_splitkv_workspace_size", "fa_fwd_fp8", "fa_fwd_varlen_fp8",
     "fa_bwd", "fa_bwd_varlen", "fa_bwd_workspace_size",
     "fa_decode_paged", "fa_decode_paged_noalloc", "fa_decode_workspace_size",
+    "fa_fwd_window", "fa_fwd_varlen_window", "fa_fwd_paged_window", "fa_decode_paged_window",
+    "fa_decode_window_workspace_size", "fa_bwd_window", "fa_bwd_varlen_window",
+    "fa_bwd_window_workspace_size",
     "fa_status_string", "fa_device_status", "fa_last_device_status", "new_workspace",
     "FA_WORKSPACE_HEADER_BYTES",
     "fa_version", "FA_DEV_TIMEOUT", "FA_DEV_BAD_BLOCK", "FA_DEV_BAD_CTX", "FA_DEV_BAD_SEQLEN",
@@ -103,6 +106,26 @@ def load_library() -> ctypes.CDLL:
         lib.fa_decode_paged_noalloc.argtypes = [vp, vp, vp, vp, i, vp, i, i, i, i, i, i, i, f,
                                                 vp, vp, vp]
         lib.fa_decode_paged_noalloc.restype = i
+        lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp]
+        lib.fa_fwd_window.restype = i
+        lib.fa_fwd_varlen_window.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
+        lib.fa_fwd_varlen_window.restype = i
+        lib.fa_fwd_paged_window.argtypes = [vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, i, i,
+                                            f, i, i, vp, vp, vp]
+        lib.fa_fwd_paged_window.restype = i
+        lib.fa_decode_window_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+        lib.fa_decode_window_workspace_size.restype = sz
+        lib.fa_decode_paged_window.argtypes = [vp, vp, vp, vp, i, vp, i, i, i, i, i, i, i, f, i, i,
+                                               vp, vp, vp, sz, vp]
+        lib.fa_decode_paged_window.restype = i
+        lib.fa_bwd_window_workspace_size.argtypes = [i, i, i, i, i, i, i]
+        lib.fa_bwd_window_workspace_size.restype = sz
+        lib.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i,
+                                      vp, sz, vp]
+        lib.fa_bwd_window.restype = i
+        lib.fa_bwd_varlen_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i,
+                                             i, f, i, i, vp, sz, vp]
+        lib.fa_bwd_varlen_window.restype = i
         lib.fa_status_string.argtypes = [i]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i]
@@ -589,3 +612,232 @@ def fa_decode_paged_noalloc(q, k_pool, v_pool, block_table, ctx_lens, max_ctx_le
     if rc != FA_OK:
         raise FaError("fa_decode_paged_noalloc", rc)
     return out, lse
+
+
+# ------------------------------------------------------- windowed attention
+#
+# A query at position p of its sequence sees key j <= p when j > p - window
+# or j < sinks (include/fa_window.h).
+
+def _check_window(window, sinks):
+    window, sinks = int(window), int(sinks)
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1 and sinks at least 0")
+    limit = 0x7FFFFFFF   # every sequence is shorter
+    return min(window, limit), min(sinks, limit)
+
+
+class _Launch:
+    """``with _Launch(stream, dev) as handle``: the call's device is current,
+    and so is ``stream`` where one is given, so that what the call allocates
+    (outputs, workspace) belongs to the stream that it runs on."""
+
+    __slots__ = ("context", "stream", "device")
+
+    def __init__(self, stream, device):
+        cuda = _torch().cuda
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream must be a stream of {device}")
+        self.context = cuda.device(device) if stream is None else cuda.stream(stream)
+        self.stream, self.device = stream, device
+
+    def __enter__(self):
+        self.context.__enter__()
+        return _stream_handle(self.stream, self.device)
+
+    def __exit__(self, *exc):
+        return self.context.__exit__(*exc)
+
+
+def fa_fwd_window(q, k, v, window, sinks=0, scale=None, out=None, lse=None, want_lse=True,
+                  stream=None):
+    """Dense causal prefill over the last ``window`` keys and the first
+    ``sinks`` keys.  q [B,N,H,d], k/v [B,N,Hkv,d] bf16 CUDA tensors.
+
+    Returns (out [B,N,H,d] bf16, lse [B,H,N] fp32 or None).
+    """
+    _check_bf16_cuda("q", q, 4)
+    dev = q.device
+    for name, t in (("k", k), ("v", v)):
+        _check_bf16_cuda(name, t, 4, dev)
+    window, sinks = _check_window(window, sinks)
+    B, N, H, d = q.shape
+    Hkv = k.shape[2]
+    if k.shape != (B, N, Hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [B, N, Hkv, d] matching q")
+    with _Launch(stream, dev) as handle:
+        out, lse = _outputs(q.shape, (B, H, N), out, lse, want_lse, dev)
+        rc = load_library().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H,
+                                          Hkv, N, d, _scale(scale, d), window, sinks,
+                                          handle)
+    if rc != FA_OK:
+        raise FaError("fa_fwd_window", rc)
+    return out, lse
+
+
+def fa_fwd_varlen_window(q, k, v, cu_seqlens, max_seqlen, window, sinks=0, scale=None, out=None,
+                         lse=None, want_lse=True, stream=None):
+    """Packed causal prefill over each sequence's last ``window`` and first
+    ``sinks`` keys.  q [T,H,d], k/v [T,Hkv,d], cu_seqlens int32 [S+1] on device.
+
+    Returns (out [T,H,d] bf16, lse [H,T] fp32 or None).
+    """
+    _check_bf16_cuda("q", q, 3)
+    dev = q.device
+    for name, t in (("k", k), ("v", v)):
+        _check_bf16_cuda(name, t, 3, dev)
+    _check_int32("cu_seqlens", cu_seqlens, dev)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets")
+    window, sinks = _check_window(window, sinks)
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (T, Hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, d] matching q")
+    with _Launch(stream, dev) as handle:
+        out, lse = _outputs(q.shape, (H, T), out, lse, want_lse, dev)
+        rc = load_library().fa_fwd_varlen_window(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
+            cu_seqlens.numel() - 1, T, int(max_seqlen), H, Hkv, d, _scale(scale, d), window, sinks,
+            handle)
+    if rc != FA_OK:
+        raise FaError("fa_fwd_varlen_window", rc)
+    return out, lse
+
+
+def fa_fwd_paged_window(q, k_pool, v_pool, block_table, ctx_lens, cu_seqlens_q, max_seqlen_q,
+                        max_ctx_len, window, sinks=0, scale=None, out=None, lse=None,
+                        want_lse=True, stream=None):
+    """:func:`fa_fwd_paged` (causal) over each query's last ``window`` keys and
+    the first ``sinks`` keys.  Blocks behind the window of a chunk's first
+    query, but for those of the sinks, are not read and may have been freed."""
+    _check_bf16_cuda("q", q, 3)
+    dev = q.device
+    num_blocks, block_size, Hkv, dp = _check_pools(k_pool, v_pool, dev)
+    _check_int32("block_table", block_table, dev, ndim=2)
+    batch = block_table.shape[0]
+    _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
+    _check_int32("cu_seqlens_q", cu_seqlens_q, dev, numel=batch + 1)
+    window, sinks = _check_window(window, sinks)
+    Tq, H, d = q.shape
+    if dp != d:
+        raise ValueError("the pools' head size must match q")
+    with _Launch(stream, dev) as handle:
+        out, lse = _outputs(q.shape, (H, Tq), out, lse, want_lse, dev)
+        rc = load_library().fa_fwd_paged_window(
+            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), block_table.shape[1],
+            _ptr(ctx_lens), _ptr(cu_seqlens_q), batch, Tq, int(max_seqlen_q), int(max_ctx_len), H,
+            Hkv, d, block_size, num_blocks, _scale(scale, d), window, sinks, _ptr(out), _ptr(lse),
+            handle)
+    if rc != FA_OK:
+        raise FaError("fa_fwd_paged_window", rc)
+    return out, lse
+
+
+def fa_decode_window_workspace_size(batch, H, Hkv, d, max_ctx_len, window, sinks=0,
+                                    block_size=16) -> int:
+    window, sinks = _check_window(window, sinks)
+    return int(load_library().fa_decode_window_workspace_size(batch, H, Hkv, d, max_ctx_len,
+                                                              block_size, window, sinks))
+
+
+def fa_decode_paged_window(q, k_pool, v_pool, block_table, ctx_lens, max_ctx_len, window, sinks=0,
+                           scale=None, out=None, lse=None, workspace=None, want_lse=True,
+                           stream=None):
+    """:func:`fa_decode_paged` over the last ``window`` keys and the first
+    ``sinks`` keys of each sequence; other blocks are not read."""
+    dev, batch, H, Hkv, d, num_blocks, block_size = _decode_args(q, k_pool, v_pool,
+                                                                 block_table, ctx_lens)
+    window, sinks = _check_window(window, sinks)
+    with _Launch(stream, dev) as handle:
+        need = 0 if workspace is not None else fa_decode_window_workspace_size(
+            batch, H, Hkv, d, max_ctx_len, window, sinks, block_size)
+        workspace = _workspace(workspace, need, dev, 256, zero=True)
+        out, lse = _outputs(q.shape, (batch, H), out, lse, want_lse, dev)
+        rc = load_library().fa_decode_paged_window(
+            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), block_table.shape[1],
+            _ptr(ctx_lens), int(max_ctx_len), batch, H, Hkv, d, block_size, num_blocks,
+            _scale(scale, d), window, sinks, _ptr(out), _ptr(lse), _ptr(workspace),
+            workspace.numel(), handle)
+    if rc != FA_OK:
+        raise FaError("fa_decode_paged_window", rc)
+    return out, lse
+
+
+def fa_bwd_window_workspace_size(B, H, Hkv, N, d, window, sinks=0) -> int:
+    """Bytes of workspace of :func:`fa_bwd_window`, or, with B sequences of at
+    most N rows, of :func:`fa_bwd_varlen_window`."""
+    window, sinks = _check_window(window, sinks)
+    return int(load_library().fa_bwd_window_workspace_size(B, H, Hkv, N, d, window, sinks))
+
+
+def _check_bwd(q, k, v, out, dout, ndim):
+    """Checks the inputs of a backward call."""
+    _check_bf16_cuda("q", q, ndim)
+    for name, t in (("k", k), ("v", v), ("out", out), ("dout", dout)):
+        _check_bf16_cuda(name, t, ndim, q.device)
+    if k.shape != (*q.shape[:-2], k.shape[-2], q.shape[-1]) or v.shape != k.shape \
+            or out.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("out and dout must have the shape of q; k and v its shape with Hkv heads")
+
+
+def _grads(q, k, v, dq, dk, dv):
+    """The gradients' tensors: the caller's, checked, or new ones."""
+    torch = _torch()
+    grads = []
+    for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if g is None:
+            g = torch.empty_like(like)
+        else:
+            _check_tensor(name, g, like.shape, torch.bfloat16, q.device)
+        grads.append(g)
+    return grads
+
+
+def fa_bwd_window(q, k, v, out, lse, dout, window, sinks=0, scale=None, dq=None, dk=None, dv=None,
+                  workspace=None, stream=None):
+    """Gradient of :func:`fa_fwd_window`.  q, out, dout [B,N,H,d]; k, v
+    [B,N,Hkv,d] bf16 CUDA tensors; lse [B,H,N] fp32.  Returns (dq, dk, dv)."""
+    _check_bwd(q, k, v, out, dout, 4)
+    window, sinks = _check_window(window, sinks)
+    dev, (B, N, H, d), Hkv = q.device, q.shape, k.shape[2]
+    _check_tensor("lse", lse, (B, H, N), _torch().float32, dev)
+    with _Launch(stream, dev) as handle:
+        dq, dk, dv = _grads(q, k, v, dq, dk, dv)
+        need = 0 if workspace is not None else fa_bwd_window_workspace_size(
+            B, H, Hkv, N, d, window, sinks)
+        workspace = _workspace(workspace, need, dev)
+        rc = load_library().fa_bwd_window(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
+            _ptr(dv), B, H, Hkv, N, d, _scale(scale, d), window, sinks, _ptr(workspace),
+            workspace.numel(), handle)
+    if rc != FA_OK:
+        raise FaError("fa_bwd_window", rc)
+    return dq, dk, dv
+
+
+def fa_bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window, sinks=0,
+                         scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradient of :func:`fa_fwd_varlen_window`.  q, out, dout [T,H,d]; k, v
+    [T,Hkv,d] bf16 CUDA tensors; lse [H,T] fp32; cu_seqlens int32 [S+1].
+    Returns (dq, dk, dv); rows outside every sequence are left as they were."""
+    _check_bwd(q, k, v, out, dout, 3)
+    window, sinks = _check_window(window, sinks)
+    dev, (T, H, d), Hkv = q.device, q.shape, k.shape[1]
+    _check_tensor("lse", lse, (H, T), _torch().float32, dev)
+    _check_int32("cu_seqlens", cu_seqlens, dev)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets")
+    S = cu_seqlens.numel() - 1
+    with _Launch(stream, dev) as handle:
+        dq, dk, dv = _grads(q, k, v, dq, dk, dv)
+        need = 0 if workspace is not None else fa_bwd_window_workspace_size(
+            S, H, Hkv, min(int(max_seqlen), T), d, window, sinks)
+        workspace = _workspace(workspace, need, dev)
+        rc = load_library().fa_bwd_varlen_window(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
+            _ptr(dv), _ptr(cu_seqlens), S, T, int(max_seqlen), H, Hkv, d, _scale(scale, d), window,
+            sinks, _ptr(workspace), workspace.numel(), handle)
+    if rc != FA_OK:
+        raise FaError("fa_bwd_varlen_window", rc)
+    return dq, dk, dv

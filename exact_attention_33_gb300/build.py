@@ -26,7 +26,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libfa_checked.so")
-SOURCES = ["fa_api.cu", "prefill.cu", "decode.cu", "backward.cu"]
+SOURCES = ["fa_api.cu", "prefill.cu", "prefill_window.cu", "decode.cu", "backward.cu",
+           "backward_window.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -63,7 +64,8 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
     os.makedirs(build_dir, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))]
-    deps.append(os.path.join(PKG, "..", "include", "fa.h"))
+    inc = os.path.join(PKG, "..", "include")
+    deps += [os.path.join(inc, h) for h in os.listdir(inc)]
     if not force and os.path.exists(lib):
         lib_t = os.path.getmtime(lib)
         if all(os.path.getmtime(d) <= lib_t for d in deps):

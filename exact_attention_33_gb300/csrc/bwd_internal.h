@@ -33,6 +33,8 @@ struct BwdParams {
   unsigned int *work;         // workspace: work counters of the dQ [0] and dK/dV [1] kernels
                               // (zeroed by the preprocess kernel)
   int num_ctas;               // CTAs of a persistent kernel (the SM count)
+  int window, sinks;          // windowed kernels only: query i sees key j <= i when
+                              // j > i - window or j < sinks
 };
 
 }  // namespace fa

@@ -21,6 +21,11 @@
 // The work is bound by HBM reads of K and V; the tensor-core ops are a small
 // fraction of the issue slots.
 //
+// A windowed call (WIN) reads the blocks of the sinks and of the window alone
+// and masks the hidden tokens of the first window block and the last sink
+// block as it masks slots past the context; its splits run over the blocks
+// that are read.
+//
 // decode_combine_kernel: one CTA per (sequence, query head) merges the
 // partial states: M = max m_i, L = sum 2^(m_i - M) l_i,
 // o = sum 2^(m_i - M) o_i / L, lse = (M + log2 L) ln 2.  A row gets 1, 4 or
@@ -59,12 +64,27 @@ __device__ __forceinline__ uint32_t swz_off(int token, int col) {
   return chunk * (kDecodeBlock * 128) + token * 128 + ((unit ^ (token & 7)) << 4);
 }
 
-// Keep the bf16 halves of x whose token index is below n_valid.
-__device__ __forceinline__ uint32_t keep_tokens(uint32_t x, int tok_lo, int n_valid) {
-  const uint32_t lo = (tok_lo < n_valid) ? 0x0000FFFFu : 0u;
-  const uint32_t hi = (tok_lo + 1 < n_valid) ? 0xFFFF0000u : 0u;
-  return x & (lo | hi);
+// Keep the bf16 halves of x whose token is not hidden.
+__device__ __forceinline__ uint32_t keep_tokens(uint32_t x, bool hide_lo, bool hide_hi) {
+  return x & ((hide_lo ? 0u : 0x0000FFFFu) | (hide_hi ? 0u : 0xFFFF0000u));
 }
+
+// The cache blocks that a windowed query (at position ctx - 1) reads: the
+// first nsb blocks (sinks) and those from block wb0 on, nvb in all, counted
+// in that order.  The window starts at key lo.
+struct WindowBlocks {
+  int nsb, wb0, nvb, lo;
+  __device__ __forceinline__ WindowBlocks(int ctx, int window, int sinks) {
+    lo = max(0, ctx - window);
+    const int nb = (ctx + kDecodeBlock - 1) / kDecodeBlock;
+    nsb = min((sinks + kDecodeBlock - 1) / kDecodeBlock, nb);
+    wb0 = lo / kDecodeBlock;
+    if (wb0 <= nsb) nsb = wb0 = 0;  // no block lies between
+    nvb = nsb + nb - wb0;
+  }
+  // block of the sequence that is the v-th to be read
+  __device__ __forceinline__ int logical(int v) const { return v < nsb ? v : v - nsb + wb0; }
+};
 
 // One warp's pass over a range of keys: the unnormalised O^T accumulator of
 // the group's query heads (m16n8 accumulator layout: rows are the head
@@ -82,14 +102,17 @@ constexpr int kRangeOk = 0, kRangeBadBlock = 1, kRangeFailed = 2;
 // sequence b and KV head kvh through its own ring of TMA stages at `smem`
 // (DecodeLayout<D>::kBytes, 1024-byte aligned) and leaves its state in st.
 // Lane i holds the physical id of logical block t0 / 16 + i in my_blk (-1
-// when it could not be read).  Returns kRangeBadBlock (nothing loaded,
+// when it could not be read).  WIN: t0 and t1 count the keys of the blocks
+// that the windowed query reads (wb), and the hidden ones among them are
+// masked like those past the context of ctx keys.  Returns kRangeBadBlock (nothing loaded,
 // status raised) when a block id of the range is outside the pool,
 // kRangeFailed when a wait gave up (copies in flight are drained before it
 // returns).
-template <int D, int NT>
+template <int D, int NT, bool WIN>
 __device__ __forceinline__ int decode_range(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                             const DecodeParams &p, int b, int kvh, int t0, int t1,
-                                            int my_blk, uint8_t *smem, WarpRange<D, NT> &st) {
+                                            int my_blk, uint8_t *smem, WarpRange<D, NT> &st,
+                                            const WindowBlocks &wb, int ctx) {
   using L = DecodeLayout<D>;
   constexpr int S = kDecodeStages;
   constexpr int KC = D / 16;  // 16-wide k chunks of the head dimension
@@ -183,7 +206,13 @@ __device__ __forceinline__ int decode_range(const CUtensorMap &tm_k, const CUten
     if (!ok) break;
     const uint32_t kb = smem_u32(smem + st * L::kStageBytes);
     const uint32_t vb = kb + L::kBlockBytes;
-    const int n_valid = min(kDecodeBlock, t1 - (t0 + i * kDecodeBlock));
+    const int base = WIN ? wb.logical(t0 / kDecodeBlock + i) * kDecodeBlock : t0 + i * kDecodeBlock;
+    const int n_valid = min(kDecodeBlock, (WIN ? ctx : t1) - base);
+    // windowed: tokens [hid0, hid1) of the block lie between sinks and window
+    const int hid0 = WIN ? max(0, p.sinks - base) : 0;
+    const int hid1 = WIN ? wb.lo - base : 0;
+    const bool masked = n_valid < kDecodeBlock || (WIN && hid0 < hid1);
+    auto hidden = [&](int tok) { return tok >= n_valid || (WIN && tok >= hid0 && tok < hid1); };
 
     // S^T = K Q^T
     float s[NT][4];
@@ -200,11 +229,11 @@ __device__ __forceinline__ int decode_range(const CUtensorMap &tm_k, const CUten
         mma_m16n8k16_bf16(s[nt], a0, a1, a2, a3, qf[nt][kc][0], qf[nt][kc][1]);
     }
     // rows of the accumulator are tokens grp and grp + 8
-    if (n_valid < kDecodeBlock) {
+    if (masked) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (grp >= n_valid) s[nt][0] = s[nt][1] = -CUDART_INF_F;
-        if (grp + 8 >= n_valid) s[nt][2] = s[nt][3] = -CUDART_INF_F;
+        if (hidden(grp)) s[nt][0] = s[nt][1] = -CUDART_INF_F;
+        if (hidden(grp + 8)) s[nt][2] = s[nt][3] = -CUDART_INF_F;
       }
     }
     // column-wise (per query head) online softmax
@@ -239,12 +268,12 @@ __device__ __forceinline__ int decode_range(const CUtensorMap &tm_k, const CUten
     for (int mt = 0; mt < KC; ++mt) {
       uint32_t a0, a1, a2, a3;
       ldmatrix_x4_trans(vb + swz_off(v_tok, mt * 16 + v_col), a0, a1, a2, a3);
-      if (n_valid < kDecodeBlock) {
-        // never let a stale slot past the context reach the accumulator
-        a0 = keep_tokens(a0, 2 * quad, n_valid);
-        a1 = keep_tokens(a1, 2 * quad, n_valid);
-        a2 = keep_tokens(a2, 8 + 2 * quad, n_valid);
-        a3 = keep_tokens(a3, 8 + 2 * quad, n_valid);
+      if (masked) {
+        // never let a stale slot past the context, or a hidden one, reach the accumulator
+        a0 = keep_tokens(a0, hidden(2 * quad), hidden(2 * quad + 1));
+        a1 = keep_tokens(a1, hidden(2 * quad), hidden(2 * quad + 1));
+        a2 = keep_tokens(a2, hidden(8 + 2 * quad), hidden(9 + 2 * quad));
+        a3 = keep_tokens(a3, hidden(8 + 2 * quad), hidden(9 + 2 * quad));
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -276,7 +305,7 @@ __device__ __forceinline__ int decode_range(const CUtensorMap &tm_k, const CUten
   return kRangeFailed;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool WIN>
 __global__ void __launch_bounds__(32)
     decode_split_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
@@ -292,19 +321,25 @@ __global__ void __launch_bounds__(32)
   // not used.
   const int lb0 = split * (p.split_tokens / kDecodeBlock);
   int my_blk = -1;
-  if (lane < p.split_tokens / kDecodeBlock && lb0 + lane < p.max_blocks_per_seq) {
-    const size_t tidx = static_cast<size_t>(b) * p.max_blocks_per_seq + lb0 + lane;
+  auto read_block_id = [&](int lb) {
+    const size_t tidx = static_cast<size_t>(b) * p.max_blocks_per_seq + lb;
     if (in_bounds(tidx, 1, static_cast<size_t>(p.batch) * p.max_blocks_per_seq, p.status))
       my_blk = p.block_table[tidx];
-  }
+  };
+  if (!WIN && lane < p.split_tokens / kDecodeBlock && lb0 + lane < p.max_blocks_per_seq)
+    read_block_id(lb0 + lane);
   const int ctx = checked_load(p.ctx_lens, b, p.batch, p.status);
   if (ctx < 0 || ctx > p.max_ctx_len || ctx > p.max_blocks_per_seq * kDecodeBlock) {
     if (split == 0 && kvh == 0 && lane == 0) raise_status(p.status, FA_DEV_BAD_CTX);
     return;
   }
+  const WindowBlocks wb(ctx, p.window, p.sinks);
+  const int keys = WIN ? wb.nvb * kDecodeBlock : ctx;  // keys of the blocks to be read
   const int t0 = split * p.split_tokens;
-  if (t0 >= ctx) return;
-  const int t1 = min(ctx, t0 + p.split_tokens);
+  if (t0 >= keys) return;
+  const int t1 = min(keys, t0 + p.split_tokens);
+  // (which blocks a window reads depends on the context length)
+  if (WIN && lane < (t1 - t0) / kDecodeBlock) read_block_id(wb.logical(lb0 + lane));
   const int G = p.group;
   // partial-state rows of the call: [batch, H, max_splits]
   const size_t part_rows = static_cast<size_t>(p.batch) * p.H * p.max_splits;
@@ -314,7 +349,8 @@ __global__ void __launch_bounds__(32)
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   WarpRange<D, NT> st;
-  const int rc = decode_range<D, NT>(tm_k, tm_v, p, b, kvh, t0, t1, my_blk, smem, st);
+  const int rc =
+      decode_range<D, NT, WIN>(tm_k, tm_v, p, b, kvh, t0, t1, my_blk, smem, st, wb, ctx);
   if (rc == kRangeBadBlock) {
     // Leave a neutral partial state so that the combine ignores this split.
     for (int g = 0; g < G; ++g) {
@@ -396,7 +432,8 @@ __global__ void __launch_bounds__(32 * combine_cta_warps<W>())
   const int b = row_live ? gw / p.H : 0;
   int ctx = row_live ? checked_load(p.ctx_lens, b, p.batch, status) : 0;
   if (ctx < 0 || ctx > p.max_ctx_len || ctx > p.max_blocks_per_seq * kDecodeBlock) ctx = 0;
-  const int ns = (ctx + p.split_tokens - 1) / p.split_tokens;
+  const int keys = p.window > 0 ? WindowBlocks(ctx, p.window, p.sinks).nvb * kDecodeBlock : ctx;
+  const int ns = (keys + p.split_tokens - 1) / p.split_tokens;
   const size_t row0 = static_cast<size_t>(gw) * p.max_splits;
   const size_t part_rows = static_cast<size_t>(p.batch) * p.H * p.max_splits;
   pdl_wait_primary();  // the split grid's partial states are complete from here on
@@ -525,11 +562,11 @@ static cudaError_t launch_combine(const DecodeParams &p, int grid, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, decode_combine_kernel<D, W>, p);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool WIN>
 static cudaError_t launch_decode_t(const CUtensorMap &tk, const CUtensorMap &tv,
                                    const DecodeParams &p, cudaStream_t stream) {
   using L = DecodeLayout<D>;
-  auto kern = decode_split_kernel<D, NT>;
+  auto kern = decode_split_kernel<D, NT, WIN>;
   // The shared-memory attribute is per device: set it once on each device
   // (one bit per device id; ids past 63 set it on every launch).
   static std::atomic<unsigned long long> attr_set{0};
@@ -553,13 +590,20 @@ static cudaError_t launch_decode_t(const CUtensorMap &tk, const CUtensorMap &tv,
   return launch_combine<D, 1>(p, (rows + 3) / 4, stream);
 }
 
+template <int D, int NT>
+static cudaError_t launch_decode_w(const CUtensorMap &tk, const CUtensorMap &tv,
+                                   const DecodeParams &p, cudaStream_t stream) {
+  return p.window > 0 ? launch_decode_t<D, NT, true>(tk, tv, p, stream)
+                      : launch_decode_t<D, NT, false>(tk, tv, p, stream);
+}
+
 cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeParams &p,
                           int d, cudaStream_t stream) {
   const bool two = p.group > 8;
-  if (d == 64) return two ? launch_decode_t<64, 2>(tk, tv, p, stream)
-                          : launch_decode_t<64, 1>(tk, tv, p, stream);
-  return two ? launch_decode_t<128, 2>(tk, tv, p, stream)
-             : launch_decode_t<128, 1>(tk, tv, p, stream);
+  if (d == 64) return two ? launch_decode_w<64, 2>(tk, tv, p, stream)
+                          : launch_decode_w<64, 1>(tk, tv, p, stream);
+  return two ? launch_decode_w<128, 2>(tk, tv, p, stream)
+             : launch_decode_w<128, 1>(tk, tv, p, stream);
 }
 
 }  // namespace fa

@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "../../include/fa.h"
+#include "../../include/fa_window.h"
 #include "bwd_internal.h"
 #include "fa_internal.h"
 #include "ptx.cuh"
@@ -28,10 +29,17 @@ cudaError_t launch_prefill(const CUtensorMap &tq, const CUtensorMap &tk, const C
                            const CUtensorMap &tv1, const CUtensorMap &to, const PrefillParams &p,
                            int d, bool causal, int kind, int grid, cudaStream_t stream,
                            int qtiles = 2);
+cudaError_t launch_prefill_window(const CUtensorMap &tq, const CUtensorMap &tk,
+                                  const CUtensorMap &tv, const CUtensorMap &tv1,
+                                  const CUtensorMap &to, const PrefillParams &p, int d, int kind,
+                                  int grid, cudaStream_t stream);
 cudaError_t launch_prefill_split_combine(const PrefillParams &p, int d, cudaStream_t stream);
 cudaError_t launch_bwd(const CUtensorMap &tq, const CUtensorMap &tdo, const CUtensorMap &tk,
                        const CUtensorMap &tv, const BwdParams &p, int d, bool causal,
                        cudaStream_t stream);
+cudaError_t launch_bwd_window(const CUtensorMap &tq, const CUtensorMap &tdo, const CUtensorMap &tk,
+                              const CUtensorMap &tv, const BwdParams &p, int d,
+                              cudaStream_t stream);
 cudaError_t launch_prefill_fp8(const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, const CUtensorMap &to,
                                const PrefillParams &p, bool causal, int grid,
@@ -108,6 +116,24 @@ int make_pool_map(CUtensorMap *map, const void *base, int d, int heads, long lon
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// The keys a causal query sees: all up to its own (window 0), or the last
+// `window` of them and the first `sinks` keys of the sequence.
+struct WindowSpec {
+  int window = 0;
+  int sinks = 0;
+};
+
+// The window arguments of a call, checked.
+bool window_ok(int window, int sinks) { return window >= 1 && sinks >= 0; }
+
+// No sequence is longer than `longest` keys: a longer window or more sinks
+// than that see the same keys (and positions less a window stay in int).
+WindowSpec clamp_window(WindowSpec w, int longest) {
+  if (w.window > 0) w.window = std::min(w.window, std::max(1, longest));
+  w.sinks = std::min(w.sinks, std::max(0, longest));
+  return w;
 }
 
 bool scale_ok(float s) { return std::isfinite(s) && s > 0.f; }
@@ -207,6 +233,16 @@ SplitWs split_ws(int B, int H, int N, int d, int requested) {
 
 size_t split_ws_bytes(const SplitWs &w) { return FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes; }
 
+// Keys of the cache blocks that a decode call reads at most: every one up to
+// max_ctx_len, or whole blocks of the sinks and of the window (whose first
+// and last keys may lie anywhere in their blocks).
+int window_keys(WindowSpec w, int max_ctx_len) {
+  if (w.window == 0) return max_ctx_len;
+  auto blocks = [](long long keys) { return (keys + kDecodeBlock - 1) / kDecodeBlock; };
+  const long long read = blocks(w.sinks) + blocks(w.window + kDecodeBlock - 1LL);
+  return static_cast<int>(std::min<long long>(max_ctx_len, read * kDecodeBlock));
+}
+
 struct DecodeWs {
   int split_tokens;
   int max_splits;
@@ -293,11 +329,11 @@ int fa_selftest_wait_timeout(int *wait_result, fa_stream_t stream) {
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// Dense prefill; `call` (or null) is the control block of a split-KV
-// workspace whose call runs this kernel alone.
+// Dense prefill, causal or not or windowed; `call` (or null) is the control
+// block of a split-KV workspace whose call runs this kernel alone.
 static int fwd_dense(const void *q, const void *k, const void *v, void *out, float *lse, int B,
                      int H, int Hkv, int N, int d, float scale, int causal, fa_stream_t stream,
-                     CallStatus *call) {
+                     CallStatus *call, WindowSpec win = {}) {
   if (!q || !k || !v || !out) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
     return FA_ERR_INVALID_ARG;
@@ -309,9 +345,9 @@ static int fwd_dense(const void *q, const void *k, const void *v, void *out, flo
   if (B == 0 || N == 0) return FA_OK;
   // With an even GQA group a CTA holds two query heads of one KV group over
   // the same 128 rows (both tiles share every K/V stage and key tile);
-  // otherwise two consecutive 128-row tiles of one head.
+  // otherwise two consecutive 128-row tiles of one head (windowed: one tile).
   const bool head_pairs = (H / Hkv) % 2 == 0;
-  const int rows = head_pairs ? kPrefillBM : kPrefillRowsPerCta;  // rows per work item
+  const int rows = head_pairs || win.window ? kPrefillBM : kPrefillRowsPerCta;  // per work item
   const long long pairs = (N + rows - 1) / rows;
   const long long grid = pairs * B * (head_pairs ? H / 2 : H);
   if (grid > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
@@ -343,10 +379,17 @@ static int fwd_dense(const void *q, const void *k, const void *v, void *out, flo
   p.scale_log2 = scale * kLog2e;
   p.v_descale = 1.f;
   p.causal = causal;
-  p.prefetch_ahead = std::max(0, sm_count());  // one CTA per SM
-  cudaError_t e = launch_prefill(tq, tk, tv, tv, to, p, d, causal != 0,
-                                 head_pairs ? kKindDenseHeads : kKindDense,
-                                 static_cast<int>(grid), reinterpret_cast<cudaStream_t>(stream));
+  // CTAs resident at once: one per SM, two of the windowed one-tile layout
+  p.prefetch_ahead = std::max(0, sm_count()) * (win.window && !head_pairs ? 2 : 1);
+  const int kind = head_pairs ? kKindDenseHeads : kKindDense;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  win = clamp_window(win, N);
+  p.window = win.window;
+  p.sinks = win.sinks;
+  cudaError_t e = win.window ? launch_prefill_window(tq, tk, tv, tv, to, p, d, kind,
+                                                     static_cast<int>(grid), st)
+                             : launch_prefill(tq, tk, tv, tv, to, p, d, causal != 0, kind,
+                                              static_cast<int>(grid), st);
   if (e == cudaSuccess && call != nullptr)
     e = launch_call_status(call, p.dev_status, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
@@ -357,11 +400,17 @@ int fa_fwd(const void *q, const void *k, const void *v, void *out, float *lse, i
   return fwd_dense(q, k, v, out, lse, B, H, Hkv, N, d, scale, causal, stream, nullptr);
 }
 
+int fa_fwd_window(const void *q, const void *k, const void *v, void *out, float *lse, int B, int H,
+                  int Hkv, int N, int d, float scale, int window, int sinks, fa_stream_t stream) {
+  if (!window_ok(window, sinks)) return FA_ERR_INVALID_ARG;
+  return fwd_dense(q, k, v, out, lse, B, H, Hkv, N, d, scale, 1, stream, nullptr, {window, sinks});
+}
+
 // Packed varlen prefill, bf16 or (fp8) e4m3 codes with per-tensor descales.
 static int fwd_varlen(const void *q, const void *k, const void *v, void *out, float *lse,
                       const int32_t *cu_seqlens, int num_seqs, int total_tokens, int max_seqlen,
                       int H, int Hkv, int d, float scale, int causal, fa_stream_t stream, bool fp8,
-                      float q_descale, float k_descale, float v_descale) {
+                      float q_descale, float k_descale, float v_descale, WindowSpec win = {}) {
   if (!q || !k || !v || !out || !cu_seqlens) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
     return FA_ERR_INVALID_ARG;
@@ -382,7 +431,9 @@ static int fwd_varlen(const void *q, const void *k, const void *v, void *out, fl
   // and longer sequences pair two consecutive 128-row tiles of one head (the
   // fp8 kernel has the two-tile layouts only).
   constexpr int kRowsOne = 0, kRowPairs = 1, kHeadPairs = 2;
-  const bool short_seqs = !fp8 && static_cast<long long>(total_tokens) < 4096LL * num_seqs;
+  // Windowed work items are short whatever the length: one tile per CTA.
+  const bool short_seqs =
+      win.window || (!fp8 && static_cast<long long>(total_tokens) < 4096LL * num_seqs);
   const int layout = ((H / Hkv) % 2 == 0) ? kHeadPairs : (short_seqs ? kRowsOne : kRowPairs);
   const int qtiles = layout == kRowsOne ? 1 : 2;
   const int rows = layout == kRowPairs ? 2 * kPrefillBM : kPrefillBM;  // rows per work item
@@ -429,6 +480,14 @@ static int fwd_varlen(const void *q, const void *k, const void *v, void *out, fl
   p.prefetch_ahead = std::max(0, sm_count()) * (qtiles == 1 ? 2 : 1);  // CTAs resident at once
   const int kind = layout == kHeadPairs ? kKindVarlenHeads : kKindVarlen;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  win = clamp_window(win, max_seqlen);
+  p.window = win.window;
+  p.sinks = win.sinks;
+  if (win.window)
+    return launch_prefill_window(tq, tk, tv, tv, to, p, d, kind, static_cast<int>(grid), st) ==
+                   cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
   cudaError_t e = fp8 ? launch_prefill_fp8(tq, tk, tv, to, p, causal != 0, static_cast<int>(grid), st,
                                            kind, d)
                       : launch_prefill(tq, tk, tv, tv, to, p, d, causal != 0, kind,
@@ -441,6 +500,15 @@ int fa_fwd_varlen(const void *q, const void *k, const void *v, void *out, float 
                   int H, int Hkv, int d, float scale, int causal, fa_stream_t stream) {
   return fwd_varlen(q, k, v, out, lse, cu_seqlens, num_seqs, total_tokens, max_seqlen, H, Hkv, d,
                     scale, causal, stream, false, 1.f, 1.f, 1.f);
+}
+
+int fa_fwd_varlen_window(const void *q, const void *k, const void *v, void *out, float *lse,
+                         const int32_t *cu_seqlens, int num_seqs, int total_tokens, int max_seqlen,
+                         int H, int Hkv, int d, float scale, int window, int sinks,
+                         fa_stream_t stream) {
+  if (!window_ok(window, sinks)) return FA_ERR_INVALID_ARG;
+  return fwd_varlen(q, k, v, out, lse, cu_seqlens, num_seqs, total_tokens, max_seqlen, H, Hkv, d,
+                    scale, 1, stream, false, 1.f, 1.f, 1.f, {window, sinks});
 }
 
 int fa_fwd_varlen_fp8(const void *q, const void *k, const void *v, void *out, float *lse,
@@ -506,9 +574,16 @@ size_t fa_bwd_workspace_size(int B, int H, int N) {
   return 2 * static_cast<size_t>(B) * H * npad * sizeof(float) + kBwdCounterBytes;
 }
 
-int fa_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse,
-           const void *dout, void *dq, void *dk, void *dv, int B, int H, int Hkv, int N, int d,
-           float scale, int causal, void *workspace, size_t workspace_bytes, fa_stream_t stream) {
+size_t fa_bwd_window_workspace_size(int B, int H, int Hkv, int N, int d, int window, int sinks) {
+  if (!window_ok(window, sinks) || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  return fa_bwd_workspace_size(B, H, N);
+}
+
+// Gradient of dense attention, causal or not or windowed.
+static int bwd_dense(const void *q, const void *k, const void *v, const void *out,
+                     const float *lse, const void *dout, void *dq, void *dk, void *dv, int B,
+                     int H, int Hkv, int N, int d, float scale, int causal, void *workspace,
+                     size_t workspace_bytes, fa_stream_t stream, WindowSpec win) {
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
   for (const void *ptr : {q, k, v, out, dout, static_cast<const void *>(dq),
                           static_cast<const void *>(dk), static_cast<const void *>(dv)})
@@ -555,16 +630,40 @@ int fa_bwd(const void *q, const void *k, const void *v, const void *out, const f
   p.N = N;
   p.scale = scale;
   p.scale_log2 = scale * kLog2e;
-  cudaError_t e = launch_bwd(tq, tdo, tk, tv, p, d, causal != 0,
-                             reinterpret_cast<cudaStream_t>(stream));
+  win = clamp_window(win, p.N);
+  p.window = win.window;
+  p.sinks = win.sinks;
+  // where every query sees its own key alone, its weight is 1 whatever the
+  // score: dQ and dK are 0, without the rounding of dP - D
+  if (win.window == 1 && (win.sinks == 0 || p.N == 1)) p.scale = 0.f;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = win.window ? launch_bwd_window(tq, tdo, tk, tv, p, d, st)
+                             : launch_bwd(tq, tdo, tk, tv, p, d, causal != 0, st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-int fa_bwd_varlen(const void *q, const void *k, const void *v, const void *out, const float *lse,
-                  const void *dout, void *dq, void *dk, void *dv, const int32_t *cu_seqlens,
-                  int num_seqs, int total_tokens, int max_seqlen, int H, int Hkv, int d,
-                  float scale, int causal, void *workspace, size_t workspace_bytes,
-                  fa_stream_t stream) {
+int fa_bwd(const void *q, const void *k, const void *v, const void *out, const float *lse,
+           const void *dout, void *dq, void *dk, void *dv, int B, int H, int Hkv, int N, int d,
+           float scale, int causal, void *workspace, size_t workspace_bytes, fa_stream_t stream) {
+  return bwd_dense(q, k, v, out, lse, dout, dq, dk, dv, B, H, Hkv, N, d, scale, causal, workspace,
+                   workspace_bytes, stream, {});
+}
+
+int fa_bwd_window(const void *q, const void *k, const void *v, const void *out, const float *lse,
+                  const void *dout, void *dq, void *dk, void *dv, int B, int H, int Hkv, int N,
+                  int d, float scale, int window, int sinks, void *workspace,
+                  size_t workspace_bytes, fa_stream_t stream) {
+  if (!window_ok(window, sinks)) return FA_ERR_INVALID_ARG;
+  return bwd_dense(q, k, v, out, lse, dout, dq, dk, dv, B, H, Hkv, N, d, scale, 1, workspace,
+                   workspace_bytes, stream, {window, sinks});
+}
+
+// Gradient of a packed batch, causal or not or windowed.
+static int bwd_varlen(const void *q, const void *k, const void *v, const void *out,
+                      const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                      const int32_t *cu_seqlens, int num_seqs, int total_tokens, int max_seqlen,
+                      int H, int Hkv, int d, float scale, int causal, void *workspace,
+                      size_t workspace_bytes, fa_stream_t stream, WindowSpec win) {
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv || !cu_seqlens)
     return FA_ERR_INVALID_ARG;
   for (const void *ptr : {q, k, v, out, dout, static_cast<const void *>(dq),
@@ -619,9 +718,36 @@ int fa_bwd_varlen(const void *q, const void *k, const void *v, const void *out, 
   p.cu_seqlens = cu_seqlens;
   p.total_tokens = total_tokens;
   p.longest_first = num_seqs <= kBwdOrderMaxSeqs;
-  cudaError_t e = launch_bwd(tq, tdo, tk, tv, p, d, causal != 0,
-                             reinterpret_cast<cudaStream_t>(stream));
+  win = clamp_window(win, p.N);
+  p.window = win.window;
+  p.sinks = win.sinks;
+  // where every query sees its own key alone, its weight is 1 whatever the
+  // score: dQ and dK are 0, without the rounding of dP - D
+  if (win.window == 1 && (win.sinks == 0 || p.N == 1)) p.scale = 0.f;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = win.window ? launch_bwd_window(tq, tdo, tk, tv, p, d, st)
+                             : launch_bwd(tq, tdo, tk, tv, p, d, causal != 0, st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_bwd_varlen(const void *q, const void *k, const void *v, const void *out, const float *lse,
+                  const void *dout, void *dq, void *dk, void *dv, const int32_t *cu_seqlens,
+                  int num_seqs, int total_tokens, int max_seqlen, int H, int Hkv, int d,
+                  float scale, int causal, void *workspace, size_t workspace_bytes,
+                  fa_stream_t stream) {
+  return bwd_varlen(q, k, v, out, lse, dout, dq, dk, dv, cu_seqlens, num_seqs, total_tokens,
+                    max_seqlen, H, Hkv, d, scale, causal, workspace, workspace_bytes, stream, {});
+}
+
+int fa_bwd_varlen_window(const void *q, const void *k, const void *v, const void *out,
+                         const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                         const int32_t *cu_seqlens, int num_seqs, int total_tokens, int max_seqlen,
+                         int H, int Hkv, int d, float scale, int window, int sinks,
+                         void *workspace, size_t workspace_bytes, fa_stream_t stream) {
+  if (!window_ok(window, sinks)) return FA_ERR_INVALID_ARG;
+  return bwd_varlen(q, k, v, out, lse, dout, dq, dk, dv, cu_seqlens, num_seqs, total_tokens,
+                    max_seqlen, H, Hkv, d, scale, 1, workspace, workspace_bytes, stream,
+                    {window, sinks});
 }
 
 size_t fa_fwd_splitkv_workspace_size(int B, int H, int N, int d, int num_splits) {
@@ -694,11 +820,13 @@ int fa_fwd_splitkv(const void *q, const void *k, const void *v, void *out, float
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-int fa_fwd_paged(const void *q, const void *k_pool, const void *v_pool,
-                 const int32_t *block_table, int max_blocks_per_seq, const int32_t *ctx_lens,
-                 const int32_t *cu_seqlens_q, int batch, int total_q, int max_seqlen_q,
-                 int max_ctx_len, int H, int Hkv, int d, int block_size, int num_blocks,
-                 float scale, int causal, void *out, float *lse, fa_stream_t stream) {
+// Query chunks over a paged KV cache, causal or not or windowed.
+static int fwd_paged(const void *q, const void *k_pool, const void *v_pool,
+                     const int32_t *block_table, int max_blocks_per_seq, const int32_t *ctx_lens,
+                     const int32_t *cu_seqlens_q, int batch, int total_q, int max_seqlen_q,
+                     int max_ctx_len, int H, int Hkv, int d, int block_size, int num_blocks,
+                     float scale, int causal, void *out, float *lse, fa_stream_t stream,
+                     WindowSpec win) {
   if (!q || !k_pool || !v_pool || !block_table || !ctx_lens || !cu_seqlens_q || !out)
     return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
@@ -718,9 +846,10 @@ int fa_fwd_paged(const void *q, const void *k_pool, const void *v_pool,
   if (static_cast<long long>(num_blocks) * block_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (batch == 0 || total_q == 0 || max_seqlen_q == 0) return FA_OK;
   if (max_seqlen_q > total_q) max_seqlen_q = total_q;
-  // with an even GQA group, two query heads of one KV group per CTA (as in fa_fwd)
+  // with an even GQA group, two query heads of one KV group per CTA (as in
+  // fa_fwd); otherwise a pair of row tiles, or one windowed tile
   const bool head_pairs = (H / Hkv) % 2 == 0;
-  const int rows = head_pairs ? kPrefillBM : kPrefillRowsPerCta;  // query rows per work item
+  const int rows = head_pairs || win.window ? kPrefillBM : kPrefillRowsPerCta;  // per work item
   const long long pairs = (max_seqlen_q + rows - 1) / rows;
   const long long grid = pairs * batch * (head_pairs ? H / 2 : H);
   if (grid > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
@@ -757,10 +886,38 @@ int fa_fwd_paged(const void *q, const void *k_pool, const void *v_pool,
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.max_ctx_len = max_ctx_len;
   p.num_blocks = num_blocks;
-  cudaError_t e = launch_prefill(tq, tk, tv, tv1, to, p, d, causal != 0,
-                                 head_pairs ? kKindPagedHeads : kKindPaged,
-                                 static_cast<int>(grid), reinterpret_cast<cudaStream_t>(stream));
+  const int kind = head_pairs ? kKindPagedHeads : kKindPaged;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  win = clamp_window(win, max_ctx_len);
+  p.window = win.window;
+  p.sinks = win.sinks;
+  cudaError_t e = win.window ? launch_prefill_window(tq, tk, tv, tv1, to, p, d, kind,
+                                                     static_cast<int>(grid), st)
+                             : launch_prefill(tq, tk, tv, tv1, to, p, d, causal != 0, kind,
+                                              static_cast<int>(grid), st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_fwd_paged(const void *q, const void *k_pool, const void *v_pool,
+                 const int32_t *block_table, int max_blocks_per_seq, const int32_t *ctx_lens,
+                 const int32_t *cu_seqlens_q, int batch, int total_q, int max_seqlen_q,
+                 int max_ctx_len, int H, int Hkv, int d, int block_size, int num_blocks,
+                 float scale, int causal, void *out, float *lse, fa_stream_t stream) {
+  return fwd_paged(q, k_pool, v_pool, block_table, max_blocks_per_seq, ctx_lens, cu_seqlens_q,
+                   batch, total_q, max_seqlen_q, max_ctx_len, H, Hkv, d, block_size, num_blocks,
+                   scale, causal, out, lse, stream, {});
+}
+
+int fa_fwd_paged_window(const void *q, const void *k_pool, const void *v_pool,
+                        const int32_t *block_table, int max_blocks_per_seq,
+                        const int32_t *ctx_lens, const int32_t *cu_seqlens_q, int batch,
+                        int total_q, int max_seqlen_q, int max_ctx_len, int H, int Hkv, int d,
+                        int block_size, int num_blocks, float scale, int window, int sinks,
+                        void *out, float *lse, fa_stream_t stream) {
+  if (!window_ok(window, sinks)) return FA_ERR_INVALID_ARG;
+  return fwd_paged(q, k_pool, v_pool, block_table, max_blocks_per_seq, ctx_lens, cu_seqlens_q,
+                   batch, total_q, max_seqlen_q, max_ctx_len, H, Hkv, d, block_size, num_blocks,
+                   scale, 1, out, lse, stream, {window, sinks});
 }
 
 size_t fa_decode_workspace_size(int batch, int H, int Hkv, int d, int max_ctx_len,
@@ -772,11 +929,20 @@ size_t fa_decode_workspace_size(int batch, int H, int Hkv, int d, int max_ctx_le
   return FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes;
 }
 
-int fa_decode_paged(const void *q, const void *k_pool, const void *v_pool,
-                    const int32_t *block_table, int max_blocks_per_seq, const int32_t *ctx_lens,
-                    int max_ctx_len, int batch, int H, int Hkv, int d, int block_size,
-                    int num_blocks, float scale, void *out, float *lse, void *workspace,
-                    size_t workspace_bytes, fa_stream_t stream) {
+size_t fa_decode_window_workspace_size(int batch, int H, int Hkv, int d, int max_ctx_len,
+                                       int block_size, int window, int sinks) {
+  if (!window_ok(window, sinks) || max_ctx_len < 0) return 0;
+  return fa_decode_workspace_size(batch, H, Hkv, d, window_keys({window, sinks}, max_ctx_len),
+                                  block_size);
+}
+
+// Paged decode, over every key or a window.
+static int decode_paged(const void *q, const void *k_pool, const void *v_pool,
+                        const int32_t *block_table, int max_blocks_per_seq,
+                        const int32_t *ctx_lens, int max_ctx_len, int batch, int H, int Hkv, int d,
+                        int block_size, int num_blocks, float scale, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, fa_stream_t stream,
+                        WindowSpec win) {
   if (!q || !k_pool || !v_pool || !block_table || !ctx_lens || !out) return FA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
     return FA_ERR_INVALID_ARG;
@@ -795,7 +961,8 @@ int fa_decode_paged(const void *q, const void *k_pool, const void *v_pool,
   if (batch > 65535 || Hkv > 65535) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_blocks) * block_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (batch == 0) return FA_OK;
-  const DecodeWs w = decode_ws(batch, H, Hkv, d, max_ctx_len);
+  win = clamp_window(win, max_ctx_len);
+  const DecodeWs w = decode_ws(batch, H, Hkv, d, window_keys(win, max_ctx_len));
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes)
     return FA_ERR_WORKSPACE;
@@ -830,8 +997,32 @@ int fa_decode_paged(const void *q, const void *k_pool, const void *v_pool,
   p.split_tokens = w.split_tokens;
   p.max_splits = w.max_splits;
   p.scale_log2 = scale * kLog2e;
+  p.window = win.window;
+  p.sinks = win.sinks;
   cudaError_t e = launch_decode(tk, tv, p, d, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_decode_paged(const void *q, const void *k_pool, const void *v_pool,
+                    const int32_t *block_table, int max_blocks_per_seq, const int32_t *ctx_lens,
+                    int max_ctx_len, int batch, int H, int Hkv, int d, int block_size,
+                    int num_blocks, float scale, void *out, float *lse, void *workspace,
+                    size_t workspace_bytes, fa_stream_t stream) {
+  return decode_paged(q, k_pool, v_pool, block_table, max_blocks_per_seq, ctx_lens, max_ctx_len,
+                      batch, H, Hkv, d, block_size, num_blocks, scale, out, lse, workspace,
+                      workspace_bytes, stream, {});
+}
+
+int fa_decode_paged_window(const void *q, const void *k_pool, const void *v_pool,
+                           const int32_t *block_table, int max_blocks_per_seq,
+                           const int32_t *ctx_lens, int max_ctx_len, int batch, int H, int Hkv,
+                           int d, int block_size, int num_blocks, float scale, int window,
+                           int sinks, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, fa_stream_t stream) {
+  if (!window_ok(window, sinks)) return FA_ERR_INVALID_ARG;
+  return decode_paged(q, k_pool, v_pool, block_table, max_blocks_per_seq, ctx_lens, max_ctx_len,
+                      batch, H, Hkv, d, block_size, num_blocks, scale, out, lse, workspace,
+                      workspace_bytes, stream, {window, sinks});
 }
 
 }  // extern "C"

@@ -95,6 +95,10 @@ struct PrefillParams {
   // item (its own + prefetch_ahead), the one that starts about a wave later
   // (0: none)
   int prefetch_ahead;
+  // windowed kernels only: the query at position i sees key j <= i when
+  // j > i - window or j < sinks
+  int window;
+  int sinks;
   // split kind only: partial states
   int num_splits;
   float *o_part;   // fp32 [splits, B, N, H, d]
@@ -132,6 +136,8 @@ struct DecodeParams {
   int split_tokens;         // multiple of kDecodeBlock
   int max_splits;
   float scale_log2;
+  int window;               // 0: every key; else the query (at ctx - 1) sees the last `window`
+  int sinks;                // keys and the first `sinks` ones
 };
 
 }  // namespace fa

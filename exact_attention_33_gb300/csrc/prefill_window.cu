@@ -1,0 +1,53 @@
+// prefill_window.cu - windowed instantiations of the prefill kernel: a query
+// at position i sees key j <= i when j > i - window or j < sinks.  A CTA
+// streams the key tiles of the sinks and those from the window of its first
+// row to its diagonal, so the work grows with N (window + sinks) instead of
+// N^2.  Only the first window tile, the diagonal tile and the last sink tile
+// hold masked scores.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fa_internal.h"
+#include "prefill_kernel.cuh"
+
+namespace fa {
+
+template <int D>
+static cudaError_t launch_prefill_window_d(const CUtensorMap &tq, const CUtensorMap &tk,
+                                           const CUtensorMap &tv, const CUtensorMap &tv1,
+                                           const CUtensorMap &to, const PrefillParams &p, int kind,
+                                           int grid, cudaStream_t stream) {
+  switch (kind) {
+    case kKindDenseHeads:
+      return launch_prefill_t<D, true, kKindDenseHeads, false, 2, true>(tq, tk, tv, tv1, to, p, grid,
+                                                                       stream);
+    case kKindVarlenHeads:
+      return launch_prefill_t<D, true, kKindVarlenHeads, false, 2, true>(tq, tk, tv, tv1, to, p,
+                                                                        grid, stream);
+    case kKindPagedHeads:
+      return launch_prefill_t<D, true, kKindPagedHeads, false, 2, true>(tq, tk, tv, tv1, to, p, grid,
+                                                                       stream);
+    case kKindDense:
+      return launch_prefill_t<D, true, kKindDense, false, 1, true>(tq, tk, tv, tv1, to, p, grid,
+                                                                  stream);
+    case kKindVarlen:
+      return launch_prefill_t<D, true, kKindVarlen, false, 1, true>(tq, tk, tv, tv1, to, p, grid,
+                                                                   stream);
+    default:
+      return launch_prefill_t<D, true, kKindPaged, false, 1, true>(tq, tk, tv, tv1, to, p, grid,
+                                                                  stream);
+  }
+}
+
+// Head-pair kinds run two heads of a KV group over the same 128 rows per CTA;
+// the others one query tile per CTA, so that every tile of a CTA has the same
+// key tiles.
+cudaError_t launch_prefill_window(const CUtensorMap &tq, const CUtensorMap &tk,
+                                  const CUtensorMap &tv, const CUtensorMap &tv1,
+                                  const CUtensorMap &to, const PrefillParams &p, int d, int kind,
+                                  int grid, cudaStream_t stream) {
+  return d == 64 ? launch_prefill_window_d<64>(tq, tk, tv, tv1, to, p, kind, grid, stream)
+                 : launch_prefill_window_d<128>(tq, tk, tv, tv1, to, p, kind, grid, stream);
+}
+
+}  // namespace fa
