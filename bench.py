@@ -71,7 +71,9 @@ KERNEL_SOURCES = {
                 "exact_attention_33_gb300/csrc/ptx.cuh",
                 "exact_attention_33_gb300/csrc/fa_internal.h",
                 "exact_attention_33_gb300/csrc/checks.cuh"],
-    "decode": ["exact_attention_33_gb300/csrc/decode.cu", "exact_attention_33_gb300/csrc/ptx.cuh",
+    "decode": ["exact_attention_33_gb300/csrc/decode.cu",
+               "exact_attention_33_gb300/csrc/decode_common.cuh",
+               "exact_attention_33_gb300/csrc/ptx.cuh",
                "exact_attention_33_gb300/csrc/fa_internal.h",
                "exact_attention_33_gb300/csrc/checks.cuh"],
 }

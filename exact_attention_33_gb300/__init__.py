@@ -1,7 +1,7 @@
 """Exact attention for GB300 (sm_103a): thin Python binding of libfa.so.
 
 Every function here only marshals torch tensors into the C ABI declared in
-``include/fa.h`` and ``include/fa_window.h`` (device pointers, sizes, the current CUDA stream) and checks
+``include/fa.h``, ``fa_window.h`` and ``fa_kvcache.h`` (device pointers, sizes, the current CUDA stream) and checks
 the returned status; all arithmetic runs in the library's CUDA kernels.  There
 is no fallback: if ``libfa.so`` is missing or a call fails, an exception is
 raised.
@@ -27,7 +27,7 @@ __all__ = [
     "fa_decode_paged", "fa_decode_paged_noalloc", "fa_decode_workspace_size",
     "fa_fwd_window", "fa_fwd_varlen_window", "fa_fwd_paged_window", "fa_decode_paged_window",
     "fa_decode_window_workspace_size", "fa_bwd_window", "fa_bwd_varlen_window",
-    "fa_bwd_window_workspace_size",
+    "fa_bwd_window_workspace_size", "fa_cache_append_fp8", "fa_decode_paged_fp8",
     "fa_status_string", "fa_device_status", "fa_last_device_status", "new_workspace",
     "FA_WORKSPACE_HEADER_BYTES",
     "fa_version", "FA_DEV_TIMEOUT", "FA_DEV_BAD_BLOCK", "FA_DEV_BAD_CTX", "FA_DEV_BAD_SEQLEN",
@@ -126,6 +126,13 @@ def load_library() -> ctypes.CDLL:
         lib.fa_bwd_varlen_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i,
                                              i, f, i, i, vp, sz, vp]
         lib.fa_bwd_varlen_window.restype = i
+        i64 = ctypes.c_int64
+        lib.fa_cache_append_fp8.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp, i, vp, vp, i, i,
+                                            i, i, i, i, i, vp]
+        lib.fa_cache_append_fp8.restype = i
+        lib.fa_decode_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, i, i, i, i, i, i, i, f,
+                                            i, i, vp, vp, vp, sz, vp]
+        lib.fa_decode_paged_fp8.restype = i
         lib.fa_status_string.argtypes = [i]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i]
@@ -736,7 +743,8 @@ def fa_fwd_paged_window(q, k_pool, v_pool, block_table, ctx_lens, cu_seqlens_q, 
 
 def fa_decode_window_workspace_size(batch, H, Hkv, d, max_ctx_len, window, sinks=0,
                                     block_size=16) -> int:
-    window, sinks = _check_window(window, sinks)
+    """Bytes of workspace of a decode call with this window (0: every key)."""
+    window, sinks = _check_cache_window(window, sinks)
     return int(load_library().fa_decode_window_workspace_size(batch, H, Hkv, d, max_ctx_len,
                                                               block_size, window, sinks))
 
@@ -841,3 +849,110 @@ def fa_bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window
     if rc != FA_OK:
         raise FaError("fa_bwd_varlen_window", rc)
     return dq, dk, dv
+
+
+# ------------------------------------------------------------ 8-bit KV cache
+#
+# Pools [num_blocks,16,Hkv,d] of e4m3 codes with one fp32 scale per block and
+# KV head (include/fa_kvcache.h).
+
+def _check_cache(k_pool, v_pool, k_scale, v_scale, dev):
+    _check_fp8("k_pool", k_pool, 4, dev)
+    _check_fp8("v_pool", v_pool, 4, dev)
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("k_pool and v_pool must have the same shape [num_blocks,16,Hkv,d]")
+    num_blocks, _, Hkv, _ = k_pool.shape
+    f32 = _torch().float32
+    _check_tensor("k_scale", k_scale, (num_blocks, Hkv), f32, dev)
+    _check_tensor("v_scale", v_scale, (num_blocks, Hkv), f32, dev)
+    return k_pool.shape
+
+
+def _check_cache_window(window, sinks):
+    if int(window) == 0 and int(sinks) == 0:
+        return 0, 0
+    return _check_window(window, sinks)
+
+
+def _check_token_rows(name, t, Hkv, d):
+    """bf16 rows [T, Hkv, d] whose tokens may lie apart (a view of a fused
+    projection); returns the token stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    if t.dim() != 3 or t.shape[1:] != (Hkv, d) or (t.numel() and t.stride()[1:] != (d, 1)):
+        raise ValueError(f"{name} must be [T, {Hkv}, {d}] with the heads of a token dense")
+    stride = t.stride(0) if t.shape[0] > 1 else Hkv * d
+    if stride < Hkv * d or stride % 8:
+        raise ValueError(f"{name}: tokens must lie a multiple of 8 elements apart, not overlapping")
+    return stride
+
+
+def fa_cache_append_fp8(k, v, k_pool, v_pool, k_scale, v_scale, block_table, ctx_lens, cu_seqlens,
+                        max_new, stream=None):
+    """Quantise new keys and values and write them into an 8-bit cache.
+
+    k, v [T,Hkv,d] bf16 (tokens may lie apart: views of a fused projection);
+    pools [num_blocks,16,Hkv,d] uint8/e4m3 and scales [num_blocks,Hkv] fp32,
+    written in place; block_table int32 [batch,max_blocks]; ctx_lens int32
+    [batch], the new tokens counted; cu_seqlens int32 [batch+1]: sequence b's
+    new tokens; max_new bounds their number per sequence.  Returns None.
+    """
+    torch = _torch()
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor")
+    dev = k.device
+    num_blocks, block_size, Hkv, d = _check_cache(k_pool, v_pool, k_scale, v_scale, dev)
+    k_stride = _check_token_rows("k", k, Hkv, d)
+    v_stride = _check_token_rows("v", v, Hkv, d)
+    if v.shape[0] != k.shape[0] or v.device != dev:
+        raise ValueError("k and v must have the same tokens on one device")
+    _check_int32("block_table", block_table, dev, ndim=2)
+    batch = block_table.shape[0]
+    _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
+    _check_int32("cu_seqlens", cu_seqlens, dev, numel=batch + 1)
+    with _Launch(stream, dev) as handle:
+        rc = load_library().fa_cache_append_fp8(
+            _ptr(k), _ptr(v), k_stride, v_stride, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
+            _ptr(v_scale), _ptr(block_table), block_table.shape[1], _ptr(ctx_lens),
+            _ptr(cu_seqlens), batch, k.shape[0], int(max_new), Hkv, d, block_size, num_blocks,
+            handle)
+    if rc != FA_OK:
+        raise FaError("fa_cache_append_fp8", rc)
+
+
+def fa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_lens, max_ctx_len,
+                        window=0, sinks=0, scale=None, out=None, lse=None, workspace=None,
+                        want_lse=True, stream=None):
+    """Paged GQA flash-decoding over an 8-bit cache, every key (window 0) or
+    the last ``window`` and the first ``sinks``.
+
+    q [batch,H,d] bf16; pools and scales as in :func:`fa_cache_append_fp8`.
+    Returns (out [batch,H,d] bf16, lse [batch,H] fp32 or None).
+    """
+    _check_bf16_cuda("q", q, 3)
+    dev = q.device
+    num_blocks, block_size, Hkv, dp = _check_cache(k_pool, v_pool, k_scale, v_scale, dev)
+    batch, H, d = q.shape
+    if dp != d:
+        raise ValueError("the pools' head size must match q")
+    _check_int32("block_table", block_table, dev, ndim=2)
+    if block_table.shape[0] != batch:
+        raise ValueError("block_table must have one row per sequence of q")
+    _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
+    window, sinks = _check_cache_window(window, sinks)
+    with _Launch(stream, dev) as handle:
+        need = 0
+        if workspace is None:
+            need = fa_decode_window_workspace_size(batch, H, Hkv, d, max_ctx_len, window, sinks,
+                                                   block_size)
+        workspace = _workspace(workspace, need, dev, 256, zero=True)
+        out, lse = _outputs(q.shape, (batch, H), out, lse, want_lse, dev)
+        rc = load_library().fa_decode_paged_fp8(
+            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+            block_table.shape[1], _ptr(ctx_lens), int(max_ctx_len), batch, H, Hkv, d, block_size,
+            num_blocks, _scale(scale, d), window, sinks, _ptr(out), _ptr(lse), _ptr(workspace),
+            workspace.numel(), handle)
+    if rc != FA_OK:
+        raise FaError("fa_decode_paged_fp8", rc)
+    return out, lse

@@ -38,6 +38,7 @@
 
 #include <atomic>
 
+#include "decode_common.cuh"
 #include "fa_internal.h"
 #include "ptx.cuh"
 #include "checks.cuh"
@@ -68,23 +69,6 @@ __device__ __forceinline__ uint32_t swz_off(int token, int col) {
 __device__ __forceinline__ uint32_t keep_tokens(uint32_t x, bool hide_lo, bool hide_hi) {
   return x & ((hide_lo ? 0u : 0x0000FFFFu) | (hide_hi ? 0u : 0xFFFF0000u));
 }
-
-// The cache blocks that a windowed query (at position ctx - 1) reads: the
-// first nsb blocks (sinks) and those from block wb0 on, nvb in all, counted
-// in that order.  The window starts at key lo.
-struct WindowBlocks {
-  int nsb, wb0, nvb, lo;
-  __device__ __forceinline__ WindowBlocks(int ctx, int window, int sinks) {
-    lo = max(0, ctx - window);
-    const int nb = (ctx + kDecodeBlock - 1) / kDecodeBlock;
-    nsb = min((sinks + kDecodeBlock - 1) / kDecodeBlock, nb);
-    wb0 = lo / kDecodeBlock;
-    if (wb0 <= nsb) nsb = wb0 = 0;  // no block lies between
-    nvb = nsb + nb - wb0;
-  }
-  // block of the sequence that is the v-th to be read
-  __device__ __forceinline__ int logical(int v) const { return v < nsb ? v : v - nsb + wb0; }
-};
 
 // One warp's pass over a range of keys: the unnormalised O^T accumulator of
 // the group's query heads (m16n8 accumulator layout: rows are the head
@@ -562,6 +546,19 @@ static cudaError_t launch_combine(const DecodeParams &p, int grid, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, decode_combine_kernel<D, W>, p);
 }
 
+template <int D>
+static cudaError_t launch_combine_d(const DecodeParams &p, cudaStream_t stream) {
+  const int rows = p.batch * p.H;
+  if (p.max_splits > kCombineManySplits)
+    return launch_combine<D, kCombineWarpsMany>(p, rows, stream);
+  if (p.max_splits > kCombineFewSplits) return launch_combine<D, kCombineWarps>(p, rows, stream);
+  return launch_combine<D, 1>(p, (rows + 3) / 4, stream);
+}
+
+cudaError_t launch_decode_combine(const DecodeParams &p, int d, cudaStream_t stream) {
+  return d == 64 ? launch_combine_d<64>(p, stream) : launch_combine_d<128>(p, stream);
+}
+
 template <int D, int NT, bool WIN>
 static cudaError_t launch_decode_t(const CUtensorMap &tk, const CUtensorMap &tv,
                                    const DecodeParams &p, cudaStream_t stream) {
@@ -582,12 +579,7 @@ static cudaError_t launch_decode_t(const CUtensorMap &tk, const CUtensorMap &tv,
   dim3 grid(p.max_splits, p.Hkv, p.batch);
   kern<<<grid, 32, L::kSmemAlloc, stream>>>(tk, tv, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int rows = p.batch * p.H;
-  if (p.max_splits > kCombineManySplits)
-    return launch_combine<D, kCombineWarpsMany>(p, rows, stream);
-  if (p.max_splits > kCombineFewSplits) return launch_combine<D, kCombineWarps>(p, rows, stream);
-  return launch_combine<D, 1>(p, (rows + 3) / 4, stream);
+  return e == cudaSuccess ? launch_combine_d<D>(p, stream) : e;
 }
 
 template <int D, int NT>

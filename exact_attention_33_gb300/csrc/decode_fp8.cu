@@ -1,0 +1,455 @@
+// decode_fp8.cu - paged GQA flash-decoding over a cache of e4m3 codes with a
+// scale for each (16-token block, KV head), every key or a window with sinks.
+//
+// The plan of decode.cu: one warp per (sequence, KV head, split of the keys),
+// blocks fetched with TMA into a ring of shared-memory stages, partial
+// (m, l, o) states merged by decode_combine_kernel.  A step takes two blocks
+// (32 tokens), since a block is half as large here.  With ks, vs the scales
+// of token j's block and c = scale log2(e):
+//   x_j = (q . code_j) ks c,  p_j = 2^(x_j - m),  l = sum p_j,
+//   o = sum p_j vs code'_j,   out = o / l.
+// The codes become fp16 exactly (one conversion for two codes), so both
+// products run on m16n8k16 fp16 MMAs with fp32 sums:
+//   S^T [16 tokens x 8 heads] += K [16 x 16 of d] Q^T.  Which of d's values
+//     stand in which k-slots is free as long as K and Q agree, so a thread
+//     takes 32 (d = 64: 16) consecutive codes of a row and feeds them to the
+//     MMAs four at a time: whole 16-byte reads, no shuffles.  Q is scaled per
+//     head by a power of two that puts its largest value at 2^10..2^11, so
+//     fp16 keeps bf16's bits down to 2^-25 of it; ks and c are applied to S.
+//   O^T [16 of d x 8 heads] += V^T P^T.  V's rows come through a transposing
+//     16-bit ldmatrix, whose elements are pairs of codes: the two halves of a
+//     pair are the accumulator rows g and g + 8, so row g of tile u is
+//     d = 16 u + 2 g, and row g + 8 the next one.
+// vs goes into the weights: o is kept relative to mo, the running maximum of
+// x_j + log2 vs, so the fp16 weights 2^(x_j + log2 vs - mo) are at most 1
+// whatever the scales, and each is rounded to 11 bits (2^-12 of itself).
+// Bound by HBM: half of decode.cu's bytes for the same products.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "cache_internal.h"
+#include "checks.cuh"
+#include "decode_common.cuh"
+#include "fa_internal.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kStepBlocks = 2;   // blocks of a step
+constexpr int kF8Stages = 4;     // steps in flight per warp
+
+template <int D>
+struct DecodeF8Layout {
+  static constexpr int kBlockBytes = kDecodeBlock * D;  // one KV head of one block
+  static constexpr int kHalfBytes = kStepBlocks * kBlockBytes;  // K (or V) of a step
+  static constexpr int kStageBytes = 2 * kHalfBytes;            // K then V
+  static constexpr int kBar = kF8Stages * kStageBytes;
+  static constexpr int kMisc = kBar + kF8Stages * 8;
+  static constexpr int kBytes = kMisc + 16;
+  static constexpr int kSmemAlloc = kBytes + 1024;
+};
+
+// Byte offset of 16-byte unit u of row t of a block (rows of D bytes in the
+// swizzle of that width: 128 or 64).
+template <int D>
+__device__ __forceinline__ uint32_t f8_off(int t, int u) {
+  if constexpr (D == 128) return t * 128 + ((u ^ (t & 7)) << 4);
+  return t * 64 + ((u ^ ((t >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+// 2^e with e clamped to the normal range
+__device__ __forceinline__ float pow2_clamped(int e) {
+  return __int_as_float((min(max(e, -126), 127) + 127) << 23);
+}
+
+}  // namespace
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32)
+    decode_fp8_split_kernel(const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
+                            const CacheScales sc) {
+  using L = DecodeF8Layout<D>;
+  constexpr int S = kF8Stages;
+  constexpr int W = D / 16;       // words of a K row per thread, MMAs over d
+  constexpr int U = D / 16;       // 16-byte units of a V row, accumulator tiles
+  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x;
+  const int quad = lane & 3, grp = lane >> 2;
+  pdl_launch_dependents();
+
+  // Without a window the block ids are read together with the context length
+  // (one memory round trip); ids past the context are not used.
+  const int lb0 = split * (p.split_tokens / kDecodeBlock);
+  int my_blk = -1;
+  auto read_block_id = [&](int lb) {
+    const size_t tidx = static_cast<size_t>(b) * p.max_blocks_per_seq + lb;
+    if (in_bounds(tidx, 1, static_cast<size_t>(p.batch) * p.max_blocks_per_seq, p.status))
+      my_blk = p.block_table[tidx];
+  };
+  const bool windowed = p.window > 0;
+  if (!windowed && lane < p.split_tokens / kDecodeBlock && lb0 + lane < p.max_blocks_per_seq)
+    read_block_id(lb0 + lane);
+  const int ctx = checked_load(p.ctx_lens, b, p.batch, p.status);
+  if (ctx < 0 || ctx > p.max_ctx_len ||
+      ctx > p.max_blocks_per_seq * static_cast<long long>(kDecodeBlock)) {
+    if (split == 0 && kvh == 0 && lane == 0) raise_status(p.status, FA_DEV_BAD_CTX);
+    return;
+  }
+  const WindowBlocks wb(ctx, windowed ? p.window : ctx, p.sinks);
+  const int nblk = min(wb.nvb - lb0, p.split_tokens / kDecodeBlock);  // this split's, <= 32
+  if (nblk <= 0) return;
+  if (windowed && lane < nblk) read_block_id(wb.logical(lb0 + lane));
+  const int G = p.group;
+  // partial-state rows of the call: [batch, H, max_splits]
+  const size_t part_rows = static_cast<size_t>(p.batch) * p.H * p.max_splits;
+  const size_t part_row = static_cast<size_t>(b) * p.H + static_cast<size_t>(kvh) * G;
+
+  if (__any_sync(0xffffffffu, lane < nblk && (my_blk < 0 || my_blk >= p.num_blocks))) {
+    if (lane == 0) raise_status(p.status, FA_DEV_BAD_BLOCK);
+    // a neutral partial state, so that the combine ignores this split
+    for (int g = 0; g < G; ++g) {
+      const size_t row = (part_row + g) * p.max_splits + split;
+      if (!in_bounds(row, 1, part_rows, p.status)) continue;
+      for (int c = lane; c < D; c += 32) p.o_part[row * D + c] = 0.f;
+      if (lane == 0) {
+        p.ml_part[row * 2 + 0] = -CUDART_INF_F;
+        p.ml_part[row * 2 + 1] = 0.f;
+      }
+    }
+    return;
+  }
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBar);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc);
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  __syncwarp();
+
+  const int steps = (nblk + kStepBlocks - 1) / kStepBlocks;
+  int issued = 0;
+  // lanes 0 .. 3 copy K and V of the step's two blocks (lane = 2 * block + v)
+  auto issue = [&](int i) {
+    const int st = i % S;
+    const int in_step = min(kStepBlocks, nblk - i * kStepBlocks);
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], in_step * 2 * L::kBlockBytes);
+    __syncwarp();
+    const int phys = __shfl_sync(0xffffffffu, my_blk, (i * kStepBlocks + (lane >> 1)) & 31);
+    if (lane < 2 * in_step) {
+      uint8_t *dst = smem + st * L::kStageBytes + (lane & 1) * L::kHalfBytes +
+                     (lane >> 1) * L::kBlockBytes;
+      tma_load_3d(dst, (lane & 1) ? &tm_v : &tm_k, &full[st], 0, kvh, phys * kDecodeBlock);
+    }
+    issued = i + 1;
+  };
+  for (int i = 0; i < min(S, steps); ++i) issue(i);
+
+  // this lane's block's scales: ks times the softmax scale, log2 of vs
+  float my_ks = 0.f, my_lv = 0.f;
+  if (lane < nblk) {
+    const size_t sidx = static_cast<size_t>(my_blk) * p.Hkv + kvh;
+    const size_t n = static_cast<size_t>(p.num_blocks) * p.Hkv;
+    my_ks = checked_load(sc.k, sidx, n, p.status) * p.scale_log2;
+    my_lv = __log2f(checked_load(sc.v, sidx, n, p.status));
+  }
+
+  // Q^T fragments: column n is query head kvh * G + n; word w of a thread
+  // holds d = 4 W quad + 4 w .. + 3 of its row, as K's words do.
+  uint32_t qf[NT][W][2];
+  float cq[NT][2];  // 2^-e of the heads of this thread's accumulator columns
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int n = nt * 8 + grp;
+    const bool valid =
+        n < G && in_bounds((part_row + n) * D, D, static_cast<size_t>(p.batch) * p.H * D, p.status);
+    const uint4 *qrow = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
+                                                        (part_row + (valid ? n : 0)) * D + 4 * W * quad);
+    uint32_t raw[2 * W];
+#pragma unroll
+    for (int c = 0; c < W / 2; ++c) {
+      const uint4 x = valid ? qrow[c] : make_uint4(0u, 0u, 0u, 0u);
+      raw[4 * c] = x.x;
+      raw[4 * c + 1] = x.y;
+      raw[4 * c + 2] = x.z;
+      raw[4 * c + 3] = x.w;
+    }
+    uint32_t top = 0;  // largest magnitude of the row, bf16 bits
+#pragma unroll
+    for (int c = 0; c < 2 * W; ++c)
+      top = max(top, max(raw[c] & 0x7FFFu, (raw[c] >> 16) & 0x7FFFu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // exponent that takes the row to [2^10, 2^11); rows with an infinity or
+    // NaN (or all zero) stay as they are
+    const int ex = static_cast<int>(top >> 7);
+    const int e = (ex == 0 || ex == 255) ? 0 : 10 - (ex - 127);
+    // (two factors: the power itself may exceed fp32's)
+    const float f0 = pow2_clamped(e / 2), f1 = pow2_clamped(e - e / 2);
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float2 x = bf16x2_to_float2(raw[2 * w + t]);
+        qf[nt][w][t] = pack_f16x2(x.x * f0 * f1, x.y * f0 * f1);
+      }
+    // column n of this thread's accumulators is head 8 nt + 2 quad + cc
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc)
+      cq[nt][cc] = pow2_clamped(-__shfl_sync(0xffffffffu, e, (2 * quad + cc) * 4));
+  }
+
+  float acc[NT][U][4];
+  float m[NT][2], mo[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[nt][u][x] = 0.f;
+    m[nt][0] = m[nt][1] = mo[nt][0] = mo[nt][1] = -CUDART_INF_F;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+
+  bool ok = true;
+  for (int i = 0; i < steps; ++i) {
+    const int st = i % S;
+    ok = mbar_wait(&full[st], (i / S) & 1, abort_flag, p.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const uint32_t kb = smem_u32(smem + st * L::kStageBytes);
+    const uint32_t vb = kb + L::kHalfBytes;
+
+    float s[NT][kStepBlocks][4];
+#pragma unroll
+    for (int t = 0; t < kStepBlocks; ++t) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[nt][t][x] = 0.f;
+      // rows grp and grp + 8 of the block, 4 W codes each
+      uint32_t lo[W], hi[W];
+#pragma unroll
+      for (int c = 0; c < W / 4; ++c) {
+        const int u = quad * (W / 4) + c;
+        const uint4 a = lds128(kb + t * L::kBlockBytes + f8_off<D>(grp, u));
+        const uint4 d = lds128(kb + t * L::kBlockBytes + f8_off<D>(grp + 8, u));
+        lo[4 * c] = a.x, lo[4 * c + 1] = a.y, lo[4 * c + 2] = a.z, lo[4 * c + 3] = a.w;
+        hi[4 * c] = d.x, hi[4 * c + 1] = d.y, hi[4 * c + 2] = d.z, hi[4 * c + 3] = d.w;
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint32_t a0 = e4m3x2_to_f16x2(lo[w]), a1 = e4m3x2_to_f16x2(hi[w]);
+        const uint32_t a2 = e4m3x2_hi_to_f16x2(lo[w]), a3 = e4m3x2_hi_to_f16x2(hi[w]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_m16n8k16_f16(s[nt][t], a0, a1, a2, a3, qf[nt][w][0], qf[nt][w][1]);
+      }
+    }
+
+    // Token masks of the step's blocks: slots past the context (all of them
+    // for a block the step lacks) and, windowed, those between sinks and window.
+    int n_valid[kStepBlocks], hid0[kStepBlocks], hid1[kStepBlocks];
+    float ks[kStepBlocks], lv[kStepBlocks];
+    bool masked = false;
+#pragma unroll
+    for (int t = 0; t < kStepBlocks; ++t) {
+      const int vblk = i * kStepBlocks + t;
+      const int base = wb.logical(lb0 + vblk) * kDecodeBlock;
+      n_valid[t] = vblk < nblk ? min(kDecodeBlock, ctx - base) : 0;
+      hid0[t] = windowed ? max(0, p.sinks - base) : 0;
+      hid1[t] = windowed ? wb.lo - base : 0;
+      masked = masked || n_valid[t] < kDecodeBlock || hid0[t] < hid1[t];
+      ks[t] = __shfl_sync(0xffffffffu, my_ks, vblk & 31);
+      lv[t] = __shfl_sync(0xffffffffu, my_lv, vblk & 31);
+    }
+    auto hidden = [&](int t, int tok) {
+      return tok >= n_valid[t] || (tok >= hid0[t] && tok < hid1[t]);
+    };
+    // scores in log2 units; rows of the accumulator are tokens grp and grp + 8
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int t = 0; t < kStepBlocks; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[nt][t][x] *= ks[t] * cq[nt][x & 1];
+    if (masked) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int t = 0; t < kStepBlocks; ++t) {
+          if (hidden(t, grp)) s[nt][t][0] = s[nt][t][1] = -CUDART_INF_F;
+          if (hidden(t, grp + 8)) s[nt][t][2] = s[nt][t][3] = -CUDART_INF_F;
+        }
+    }
+    // column-wise (per query head) online softmax
+    uint32_t pb[NT][kStepBlocks][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[kStepBlocks][4];
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        float m_new = m[nt][cc], mo_new = mo[nt][cc];
+#pragma unroll
+        for (int t = 0; t < kStepBlocks; ++t) {
+          float mx = fmaxf(s[nt][t][cc], s[nt][t][2 + cc]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          m_new = fmaxf(m_new, mx);
+          mo_new = fmaxf(mo_new, mx + lv[t]);
+        }
+        // (nothing seen yet: both references stay finite, every weight is 0)
+        const float m_use = (m_new == -CUDART_INF_F) ? 0.f : m_new;
+        const float mo_use = (mo_new == -CUDART_INF_F) ? 0.f : mo_new;
+        const float alpha = ex2(mo[nt][cc] - mo_use);
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < kStepBlocks; ++t) {
+          const float p0 = ex2(s[nt][t][cc] - m_use), p1 = ex2(s[nt][t][2 + cc] - m_use);
+          sum += p0 + p1;
+          // a weight and its block's scale, relative to mo
+          w[t][cc] = ex2(s[nt][t][cc] + (lv[t] - mo_use));
+          w[t][2 + cc] = ex2(s[nt][t][2 + cc] + (lv[t] - mo_use));
+        }
+        l[nt][cc] = fmaf(l[nt][cc], ex2(m[nt][cc] - m_use), sum);
+        m[nt][cc] = m_new;
+        mo[nt][cc] = mo_new;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          acc[nt][u][cc] *= alpha;
+          acc[nt][u][2 + cc] *= alpha;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kStepBlocks; ++t) {
+        pb[nt][t][0] = movmatrix_trans(pack_f16x2(w[t][0], w[t][1]));
+        pb[nt][t][1] = movmatrix_trans(pack_f16x2(w[t][2], w[t][3]));
+      }
+    }
+    // O^T += V^T P^T: matrix mi of the transposing load holds tokens
+    // 8 mi .. + 7 of the step's 32, 16 values of d as pairs
+    const int mi = lane >> 3, mr = lane & 7;
+    const uint32_t vrow = vb + (mi >> 1) * L::kBlockBytes;
+    const int vtok = mr + 8 * (mi & 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t r[4];
+      ldmatrix_x4_trans(vrow + f8_off<D>(vtok, u), r[0], r[1], r[2], r[3]);
+#pragma unroll
+      for (int t = 0; t < kStepBlocks; ++t) {
+        uint32_t a[2][2];  // [token half][even or odd value of the pair]
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t x = r[2 * t + hf];  // codes (tok, d), (tok, d + 1), (tok + 1, d), (tok + 1, d + 1)
+          if (masked) {
+            // never let a stale or hidden slot reach the accumulator
+            const int tok = 8 * hf + 2 * quad;
+            x &= (hidden(t, tok) ? 0u : 0x0000FFFFu) | (hidden(t, tok + 1) ? 0u : 0xFFFF0000u);
+          }
+          const uint32_t y = __byte_perm(x, 0, 0x3120);  // (tok, d), (tok + 1, d), then d + 1
+          a[hf][0] = e4m3x2_to_f16x2(y);
+          a[hf][1] = e4m3x2_hi_to_f16x2(y);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_m16n8k16_f16(acc[nt][u], a[0][0], a[0][1], a[1][0], a[1][1], pb[nt][t][0],
+                           pb[nt][t][1]);
+      }
+    }
+    __syncwarp();
+    if (i + S < steps) {
+      if (lane < 2 * kStepBlocks) fence_proxy_async_smem();
+      issue(i + S);
+    }
+  }
+
+  if (!ok) {
+    // drain copies still in flight before the CTA releases its shared memory
+    if (lane == 0)
+      for (int i = max(0, issued - S); i < issued; ++i)
+        mbar_drain(&full[i % S], (i / S) & 1, p.status);
+    __syncwarp();
+    return;
+  }
+  // write the partial state of every query head of the group
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc) {
+      float lt = l[nt][cc];
+      lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+      lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+      lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+      const int g = nt * 8 + 2 * quad + cc;
+      if (g >= G) continue;
+      const size_t row = (part_row + g) * p.max_splits + split;
+      if (!in_bounds(row, 1, part_rows, p.status)) continue;
+      if (grp == 0) {
+        p.ml_part[row * 2 + 0] = m[nt][cc];
+        p.ml_part[row * 2 + 1] = lt;
+      }
+      // o back from its own reference to m's
+      const float f = (mo[nt][cc] == -CUDART_INF_F) ? 0.f : exp2f(mo[nt][cc] - m[nt][cc]);
+      float2 *orow = reinterpret_cast<float2 *>(p.o_part + row * D);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        orow[u * 8 + grp] = make_float2(acc[nt][u][cc] * f, acc[nt][u][2 + cc] * f);
+    }
+}
+
+template <int D, int NT>
+static cudaError_t launch_decode_fp8_t(const CUtensorMap &tk, const CUtensorMap &tv,
+                                       const DecodeParams &p, const CacheScales &sc,
+                                       cudaStream_t stream) {
+  using L = DecodeF8Layout<D>;
+  auto kern = decode_fp8_split_kernel<D, NT>;
+  // the shared-memory attribute is per device: set once on each (one bit per
+  // device id; ids past 63 set it on every launch)
+  static std::atomic<unsigned long long> attr_set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (bit == 0ull || (attr_set.load(std::memory_order_acquire) & bit) == 0ull) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
+    if (e != cudaSuccess) return e;
+    attr_set.fetch_or(bit, std::memory_order_release);
+  }
+  kern<<<dim3(p.max_splits, p.Hkv, p.batch), 32, L::kSmemAlloc, stream>>>(tk, tv, p, sc);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_decode_combine(p, D, stream) : e;
+}
+
+cudaError_t launch_decode_fp8(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeParams &p,
+                              const CacheScales &sc, int d, cudaStream_t stream) {
+  const bool two = p.group > 8;
+  if (d == 64) return two ? launch_decode_fp8_t<64, 2>(tk, tv, p, sc, stream)
+                          : launch_decode_fp8_t<64, 1>(tk, tv, p, sc, stream);
+  return two ? launch_decode_fp8_t<128, 2>(tk, tv, p, sc, stream)
+             : launch_decode_fp8_t<128, 1>(tk, tv, p, sc, stream);
+}
+
+}  // namespace fa

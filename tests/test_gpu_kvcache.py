@@ -1,0 +1,394 @@
+"""The 8-bit paged cache: the quantising write (bit for bit), attention over
+it for single tokens against 64-bit arithmetic, and a serving run of both."""
+import math
+
+import numpy as np
+import pytest
+
+import cache_reference as cr
+import window_reference as ref
+from exact_attention_33_gb300 import workloads as W
+from gpu_helpers import assert_device_clean, torch_mod
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    from exact_attention_33_gb300.build import build
+    build()
+    import exact_attention_33_gb300 as fa_mod
+    fa_mod.fa_device_status(clear=True)
+    return fa_mod
+
+
+def dev(a, dtype=None):
+    torch = torch_mod()
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def bf16(a):
+    return dev(a, torch_mod().bfloat16)
+
+
+def cu_of(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+
+class Cache:
+    """A cache on the device beside its NumPy twin."""
+
+    def __init__(self, ctx, Hkv, d, seed, width=None):
+        rng = np.random.default_rng(seed)
+        self.table, blocks = cr.tables(ctx, seed, width=width)
+        self.pool, self.scale = {}, {}
+        for x in "kv":
+            # every finite code, so also those of stale slots
+            codes = rng.integers(0, 256, (blocks, 16, Hkv, d)).astype(np.uint8)
+            codes[(codes & 0x7F) == 0x7F] = 0x3A
+            self.pool[x] = codes
+            self.scale[x] = np.exp2(rng.integers(-9, -4, (blocks, Hkv))).astype(np.float32)
+        self.dpool = {x: dev(self.pool[x]) for x in "kv"}
+        self.dscale = {x: dev(self.scale[x]) for x in "kv"}
+        self.dtable = dev(self.table)
+
+    def args(self):
+        return self.dpool["k"], self.dpool["v"], self.dscale["k"], self.dscale["v"], self.dtable
+
+    def append(self, fa, k, v, ctx, new, **more):
+        for x, t in (("k", k), ("v", v)):
+            cr.append(t, self.pool[x], self.scale[x], self.table, ctx, new)
+        kd, vd = more.pop("tensors", None) or (bf16(k), bf16(v))
+        fa.fa_cache_append_fp8(kd, vd, *self.args(), dev(np.int32(ctx)), dev(cu_of(new)),
+                               max(max(new), 1), **more)
+
+    def check(self, what=""):
+        for x in "kv":
+            assert np.array_equal(self.dscale[x].cpu().numpy(), self.scale[x]), f"{what} {x} scale"
+            got = self.dpool[x].cpu().numpy()
+            nan = (got & 0x7F) == 0x7F
+            assert np.array_equal(nan, (self.pool[x] & 0x7F) == 0x7F), f"{what} {x} NaN"
+            assert np.array_equal(got[~nan], self.pool[x][~nan]), f"{what} {x} codes"
+
+    def rows(self, x, b, ctx):
+        """Keys or values of sequence b in 64 bits, [ctx, Hkv, d], on the device."""
+        blocks = self.table[b, : (ctx + 15) // 16]
+        return dev(cr.real(self.pool[x][blocks], self.scale[x][blocks]).reshape(
+            -1, *self.pool[x].shape[2:])[:ctx])
+
+
+# ------------------------------------------------------------------ the write
+
+APPEND = [
+    ([1], [1], 1, 64),
+    ([16, 17, 32], [16, 17, 16], 2, 128),
+    ([5, 40, 100, 16, 31], [1, 1, 1, 1, 1], 8, 128),    # single tokens, one begins a block
+    ([7, 90, 64], [0, 33, 1], 3, 64),                     # a sequence without new tokens
+    ([300, 1000], [257, 999], 2, 64),
+    ([50] * 40, [3] * 40, 1, 128),
+]
+
+
+@pytest.mark.parametrize("ctx,new,Hkv,d", APPEND)
+def test_append(fa, ctx, new, Hkv, d):
+    rng = np.random.default_rng(len(ctx) + d)
+    c = Cache(ctx, Hkv, d, seed=sum(ctx))
+    t = sum(new)
+    # magnitudes from far below to far above what the blocks hold
+    mag = np.exp2(rng.integers(-12, 9, (t, Hkv, 1))).astype(np.float32)
+    c.append(fa, cr.bf16(rng, t, Hkv, d) * mag, cr.bf16(rng, t, Hkv, d), ctx, new)
+    assert_device_clean()
+    c.check()
+
+
+def test_append_extremes(fa):
+    """Zeros, bf16's smallest and largest values, infinities and NaN, and
+    amax at the border of a power of two."""
+    Hkv, d = 2, 64
+    rows = np.zeros((48, Hkv, d), dtype=np.float32)
+    rows[1, 0, 0] = 2.0 ** -133          # subnormal: a scale of 2^-100
+    rows[16, 0, :4] = 448, -448, 0.1, 3e-3
+    rows[16, 1, :4] = 450, 1, -0.5, 1e-5  # just above the border
+    rows[32, 0, :5] = math.inf, -math.inf, math.nan, 7.0, -3.0
+    rows[33, 1, :2] = 3.3895314e38, 1e30
+    c = Cache([48], Hkv, d, seed=1)
+    c.append(fa, rows, -rows, [48], [48])
+    assert_device_clean()
+    c.check()
+    assert c.scale["k"][c.table[0, 0]].tolist() == [2.0 ** -100] * 2
+    assert c.scale["k"][c.table[0, 1]].tolist() == [1.0, 2.0]
+    assert c.scale["k"][c.table[0, 2], 0] == 2.0 ** -6
+
+
+def test_append_token_by_token(fa):
+    """A block filled one token at a time, its scale growing on the way, and
+    an older scale that is no power of two."""
+    rng = np.random.default_rng(3)
+    Hkv, d = 3, 128
+    c = Cache([40], Hkv, d, seed=4)
+    c.append(fa, *(cr.bf16(rng, 5, Hkv, d) for _ in "kv"), [5], [5])
+    for x in "kv":  # as another writer might have left it
+        c.scale[x][c.table[0, 0]] = np.float32([0.0037, 0.02, 3.0])
+        c.dscale[x].copy_(dev(c.scale[x]))
+    for n in range(6, 41):
+        grow = np.float32(2.0 ** ((n % 7) * 2 - 6))
+        c.append(fa, *(cr.bf16(rng, 1, Hkv, d) * grow for _ in "kv"), [n], [1])
+        c.check(f"token {n}")
+    assert_device_clean()
+
+
+def test_append_from_a_fused_projection(fa):
+    """k and v as views of one [T, (H + 2 Hkv) d] tensor."""
+    torch = torch_mod()
+    rng = np.random.default_rng(5)
+    H, Hkv, d, ctx = 4, 2, 64, [30, 77]
+    qkv = cr.bf16(rng, sum(ctx), H + 2 * Hkv, d)
+    t = bf16(qkv)
+    c = Cache(ctx, Hkv, d, seed=6)
+    c.append(fa, qkv[:, H:H + Hkv], qkv[:, H + Hkv:], ctx, ctx,
+             tensors=(t[:, H:H + Hkv], t[:, H + Hkv:]))
+    assert_device_clean()
+    c.check()
+
+
+def test_append_reports_bad_arguments_of_the_device(fa):
+    """A bad context length, a bad block id and a bad offset each skip what
+    they concern; the sequences beside them are written."""
+    torch = torch_mod()
+    rng = np.random.default_rng(7)
+    Hkv, d, ctx, new = 2, 64, [20, 33, 18, 40], [20, 3, 2, 8]
+    c = Cache(ctx, Hkv, d, seed=8)
+    k, v = (cr.bf16(rng, sum(new), Hkv, d) for _ in "kv")
+    good, bad = [1], {0: "block", 2: "ctx"}
+    bad_table = c.table.copy()
+    bad_table[0, 1] = 10 ** 6
+    lens, cu = np.int32(ctx), cu_of(new)
+    lens[2] = 1                       # fewer than its new tokens
+    want = c.table[0, 0]
+    # the twin: sequence 0's first block, sequence 1 and sequence 3
+    for x, t in (("k", k), ("v", v)):
+        cr.append(t[:16], c.pool[x], c.scale[x], c.table[:1], [16], [16])
+        cr.append(t[20:23], c.pool[x], c.scale[x], c.table[1:2], [33], [3])
+        cr.append(t[25:], c.pool[x], c.scale[x], c.table[3:], [40], [8])
+    fa.fa_cache_append_fp8(bf16(k), bf16(v), *c.args()[:4], dev(bad_table), dev(lens), dev(cu), 20)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_DEV_BAD_BLOCK | fa.FA_DEV_BAD_CTX
+    c.check()
+    # more new tokens than max_new says: reported, nothing of it written
+    fa.fa_cache_append_fp8(bf16(-k), bf16(v), *c.args(), dev(np.int32(ctx)), dev(cu), 2)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_DEV_BAD_SEQLEN
+    cr.append(-k[23:25], c.pool["k"], c.scale["k"], c.table[2:3], [18], [2])
+    cr.append(v[23:25], c.pool["v"], c.scale["v"], c.table[2:3], [18], [2])
+    c.check("max_new")
+
+
+# ------------------------------------------------------------------ single tokens
+
+def check_decode(out, lse, q, c, ctx, window, sinks, what):
+    H, Hkv = q.shape[1], c.pool["k"].shape[2]
+    for b, n in enumerate(ctx):
+        k, v = c.rows("k", b, n), c.rows("v", b, n)
+        for h in range(H):
+            kv = h // (H // Hkv)
+            o, l, tol = cr.decode_rows(q[b:b + 1, h].double(), k[:, kv], v[:, kv], window, sinks)
+            ref.assert_within(out[b:b + 1, h], o, tol, f"{what} seq {b} head {h}")
+            ref.assert_lse(lse[b:b + 1, h], l, f"{what} seq {b} head {h}")
+
+
+DECODE = [
+    ([1], 1, 1, 64, 0, 0),
+    ([5, 16, 17, 0, 300], 4, 2, 128, 0, 0),
+    ([700, 33, 1024], 8, 1, 64, 0, 0),
+    ([1000, 999, 31, 32], 6, 2, 128, 0, 0),
+    ([2000, 1], 32, 2, 128, 0, 0),               # group of 16
+    ([47, 48, 49], 9, 1, 64, 0, 0),
+    ([3000], 7, 1, 128, 0, 0),
+    ([700, 33, 1024], 8, 1, 64, 100, 20),
+    ([640, 641, 655, 656], 2, 2, 64, 64, 16),
+    ([1000, 40], 4, 2, 128, 1, 0),
+    ([5000, 130], 16, 2, 128, 4096, 64),
+    ([300, 40], 3, 1, 64, 10000, 2),
+]
+
+
+@pytest.mark.parametrize("ctx,H,Hkv,d,window,sinks", DECODE)
+def test_decode(fa, ctx, H, Hkv, d, window, sinks):
+    """Stale and hidden slots hold NaN codes; blocks without a visible key
+    have no table entry."""
+    torch = torch_mod()
+    c = Cache(ctx, Hkv, d, seed=20 + d)
+    table = c.table.copy()
+    for b, n in enumerate(ctx):
+        for blk in range((n + 15) // 16):
+            hidden = [t for t in range(blk * 16, blk * 16 + 16)
+                      if t >= n or (window and t < n - window and t >= sinks)]
+            for x in "kv":
+                c.dpool[x][int(c.table[b, blk]), [t % 16 for t in hidden]] = 0x7F
+            if len(hidden) == 16:
+                table[b, blk] = -5
+    q = bf16(cr.bf16(np.random.default_rng(d), len(ctx), H, d))
+    out, lse = fa.fa_decode_paged_fp8(q, *c.args()[:4], dev(table), dev(np.int32(ctx)), max(ctx),
+                                      window, sinks)
+    assert_device_clean()
+    check_decode(out, lse, q, c, ctx, window, sinks, "decode")
+
+
+def test_decode_scales_far_apart(fa):
+    """Scales over fifty powers of two, zeros, and queries of any size: the
+    block that matters may be the one with the smallest scale."""
+    ctx, H, Hkv, d = [200, 96], 4, 2, 64
+    rng = np.random.default_rng(30)
+    for case in range(4):
+        c = Cache(ctx, Hkv, d, seed=31 + case)
+        blocks = c.pool["k"].shape[0]
+        if case == 0:
+            c.scale["v"][:] = np.exp2(rng.integers(-40, 10, (blocks, Hkv)))
+        elif case == 1:  # the heavy keys' values are small
+            c.scale["k"][:] = np.exp2(rng.integers(-12, -3, (blocks, Hkv)))
+            c.scale["v"][:] = 2.0 ** -20 / c.scale["k"] ** 3
+        elif case == 2:
+            c.scale["v"][::2] = 0.0
+            c.scale["k"][:] = 0.013 * rng.random((blocks, Hkv))
+        for x in "kv":
+            c.scale[x] = c.scale[x].astype(np.float32)
+            c.dscale[x].copy_(dev(c.scale[x]))
+        q = cr.bf16(rng, 2, H, d)
+        if case == 3:
+            q = q * np.float32([[[1e-30], [2.0 ** -120], [0.0], [100.0]]])
+        q = bf16(q)
+        out, lse = fa.fa_decode_paged_fp8(q, *c.args(), dev(np.int32(ctx)), 200)
+        assert_device_clean()
+        check_decode(out, lse, q, c, ctx, 0, 0, f"case {case}")
+
+
+def test_decode_reports_and_recovers(fa):
+    torch = torch_mod()
+    ctx, H, Hkv, d = [100, 200, 64], 4, 2, 128
+    c = Cache(ctx, Hkv, d, seed=40)
+    table, lens = c.table.copy(), np.int32(ctx)
+    table[0, 6], lens[2] = c.pool["k"].shape[0], -1
+    q = bf16(cr.bf16(np.random.default_rng(41), 3, H, d))
+    ws = fa.new_workspace(fa.fa_decode_window_workspace_size(3, H, Hkv, d, 200, 0, 0))
+    out, lse = fa.fa_decode_paged_fp8(q, *c.args()[:4], dev(table), dev(lens), 200, workspace=ws)
+    torch.cuda.synchronize()
+    bits = fa.FA_DEV_BAD_BLOCK | fa.FA_DEV_BAD_CTX
+    assert fa.fa_last_device_status(ws) == bits and fa.fa_device_status(clear=True) == bits
+    check_decode(out[1:2], lse[1:2], q[1:2], _Only(c, 1), [200], 0, 0, "beside")
+    out, lse = fa.fa_decode_paged_fp8(q, *c.args(), dev(np.int32(ctx)), 200, workspace=ws)
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_status(ws) == 0
+    check_decode(out, lse, q, c, ctx, 0, 0, "after")
+
+
+class _Only:
+    """One sequence of a cache."""
+
+    def __init__(self, c, b):
+        self.pool, self.rows = c.pool, lambda x, _, n: c.rows(x, b, n)
+
+
+# ------------------------------------------------------------------ together
+
+def test_serving_run(fa):
+    """Prompts written into the cache, then tokens one by one: write, attend;
+    the step is captured into a graph and replayed on another stream."""
+    torch = torch_mod()
+    rng = np.random.default_rng(50)
+    H, Hkv, d, prompts, steps = 8, 2, 64, [37, 100, 1], 20
+    final = [n + steps for n in prompts]
+    c = Cache(final, Hkv, d, seed=51)
+    S = len(prompts)
+    c.append(fa, *(cr.bf16(rng, sum(prompts), Hkv, d) for _ in "kv"), prompts, prompts)
+    c.check("prompts")
+    for window, sinks in ((0, 0), (40, 4)):
+        q, k, v = (bf16(cr.bf16(rng, S, h, d)) for h in (H, Hkv, Hkv))
+        lens, cu = dev(np.int32(prompts)), dev(cu_of([1] * S))
+        ws = fa.new_workspace(fa.fa_decode_window_workspace_size(S, H, Hkv, d, max(final), window,
+                                                                 sinks))
+
+        def step():
+            fa.fa_cache_append_fp8(k, v, *c.args(), lens, cu, 1)
+            return fa.fa_decode_paged_fp8(q, *c.args(), lens, max(final), window, sinks,
+                                          workspace=ws)
+        lens.add_(1)
+        ctx = [n + 1 for n in prompts]
+        eager = step()  # also the one-time set-up outside the capture
+        for x, t in (("k", k), ("v", v)):
+            cr.append(t.float().cpu().numpy(), c.pool[x], c.scale[x], c.table, ctx, [1] * S)
+        check_decode(*eager, q, c, ctx, window, sinks, "eager")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            captured = step()
+        side = torch.cuda.Stream()
+        for _ in range(steps // 2 - 1):
+            ctx = [n + 1 for n in ctx]
+            lens.add_(1)
+            new = {x: cr.bf16(rng, S, h, d) for x, h in (("q", H), ("k", Hkv), ("v", Hkv))}
+            for t, x in ((q, "q"), (k, "k"), (v, "v")):
+                t.copy_(bf16(new[x]))
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                graph.replay()
+            torch.cuda.current_stream().wait_stream(side)
+            for x in "kv":
+                cr.append(new[x], c.pool[x], c.scale[x], c.table, ctx, [1] * S)
+            c.check(f"window {window} context {ctx}")
+            check_decode(*captured, q, c, ctx, window, sinks, f"context {ctx}")
+        prompts = ctx
+    assert_device_clean()
+
+
+def test_two_calls_at_once(fa):
+    """Decode calls on two streams with workspaces of their own."""
+    torch = torch_mod()
+    ctx, H, Hkv, d = [900, 1100], 8, 2, 128
+    c = Cache(ctx, Hkv, d, seed=60)
+    rng = np.random.default_rng(61)
+    qs = [bf16(cr.bf16(rng, 2, H, d)) for _ in range(2)]
+    lens = dev(np.int32(ctx))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[] for _ in range(2)]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            outs[i].append(fa.fa_decode_paged_fp8(qs[i], *c.args(), lens, 1100, stream=s))
+    torch.cuda.synchronize()
+    assert_device_clean()
+    for i in range(2):
+        check_decode(*outs[i][0], qs[i], c, ctx, 0, 0, f"stream {i}")
+        for o, l in outs[i][1:]:
+            assert torch.equal(o, outs[i][0][0]) and torch.equal(l, outs[i][0][1])
+
+
+def test_binding_refuses(fa):
+    torch = torch_mod()
+    c = Cache([40], 2, 64, seed=70)
+    q = bf16(np.zeros((1, 4, 64), np.float32))
+    lens = dev(np.int32([40]))
+    for window, sinks in ((-1, 0), (0, 3), (5, -1)):
+        with pytest.raises(ValueError):
+            fa.fa_decode_paged_fp8(q, *c.args(), lens, 40, window, sinks)
+    kp, vp, ks, vs, table = c.args()
+    with pytest.raises(ValueError):
+        fa.fa_decode_paged_fp8(q, kp, vp, ks[:-1], vs, table, lens, 40)
+    with pytest.raises(ValueError):
+        fa.fa_decode_paged_fp8(q, kp.float(), vp, ks, vs, table, lens, 40)
+    with pytest.raises(ValueError):
+        fa.fa_decode_paged_fp8(q, kp, vp, ks.double(), vs, table, lens, 40)
+    with pytest.raises(fa.FaError):
+        fa.fa_decode_paged_fp8(q, *c.args(), lens, 4000)
+    k = bf16(np.zeros((40, 2, 64), np.float32))
+    cu = dev(np.int32([0, 40]))
+    with pytest.raises(ValueError):
+        fa.fa_cache_append_fp8(k.transpose(1, 2), k, *c.args(), lens, cu, 40)
+    with pytest.raises(ValueError):
+        fa.fa_cache_append_fp8(k[:, :, :32], k, *c.args(), lens, cu, 40)
+    with pytest.raises(ValueError):
+        fa.fa_cache_append_fp8(k, k[:-1], *c.args(), lens, cu, 40)
+    with pytest.raises(ValueError):
+        fa.fa_cache_append_fp8(k[:1].expand(40, 2, 64), k, *c.args(), lens, cu, 40)
+    with pytest.raises(ValueError):
+        fa.fa_cache_append_fp8(k, k, *c.args(), lens, cu[:1], 40)
