@@ -28,6 +28,7 @@ __all__ = [
     "fa_fwd_window", "fa_fwd_varlen_window", "fa_fwd_paged_window", "fa_decode_paged_window",
     "fa_decode_window_workspace_size", "fa_bwd_window", "fa_bwd_varlen_window",
     "fa_bwd_window_workspace_size", "fa_cache_append_fp8", "fa_decode_paged_fp8",
+    "fa_fwd_paged_fp8",
     "fa_status_string", "fa_device_status", "fa_last_device_status", "new_workspace",
     "FA_WORKSPACE_HEADER_BYTES",
     "fa_version", "FA_DEV_TIMEOUT", "FA_DEV_BAD_BLOCK", "FA_DEV_BAD_CTX", "FA_DEV_BAD_SEQLEN",
@@ -133,6 +134,9 @@ def load_library() -> ctypes.CDLL:
         lib.fa_decode_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, i, i, i, i, i, i, i, f,
                                             i, i, vp, vp, vp, sz, vp]
         lib.fa_decode_paged_fp8.restype = i
+        lib.fa_fwd_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, i,
+                                         i, f, i, i, vp, vp, vp]
+        lib.fa_fwd_paged_fp8.restype = i
         lib.fa_status_string.argtypes = [i]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i]
@@ -955,4 +959,37 @@ def fa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_le
             workspace.numel(), handle)
     if rc != FA_OK:
         raise FaError("fa_decode_paged_fp8", rc)
+    return out, lse
+
+
+def fa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_lens, cu_seqlens_q,
+                     max_seqlen_q, max_ctx_len, window=0, sinks=0, scale=None, out=None, lse=None,
+                     want_lse=True, stream=None):
+    """Query chunks [Tq,H,d] (causal) against an 8-bit cache, every key up to
+    each query's own (window 0) or the last ``window`` and the first ``sinks``.
+
+    Pools and scales as in :func:`fa_cache_append_fp8`; ctx_lens int32 [batch]
+    and cu_seqlens_q int32 [batch+1] as in :func:`fa_fwd_paged`.
+    Returns (out [Tq,H,d] bf16, lse [H,Tq] fp32 or None).
+    """
+    _check_bf16_cuda("q", q, 3)
+    dev = q.device
+    num_blocks, block_size, Hkv, dp = _check_cache(k_pool, v_pool, k_scale, v_scale, dev)
+    _check_int32("block_table", block_table, dev, ndim=2)
+    batch = block_table.shape[0]
+    _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
+    _check_int32("cu_seqlens_q", cu_seqlens_q, dev, numel=batch + 1)
+    window, sinks = _check_cache_window(window, sinks)
+    Tq, H, d = q.shape
+    if dp != d:
+        raise ValueError("the pools' head size must match q")
+    with _Launch(stream, dev) as handle:
+        out, lse = _outputs(q.shape, (H, Tq), out, lse, want_lse, dev)
+        rc = load_library().fa_fwd_paged_fp8(
+            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+            block_table.shape[1], _ptr(ctx_lens), _ptr(cu_seqlens_q), batch, Tq,
+            int(max_seqlen_q), int(max_ctx_len), H, Hkv, d, block_size, num_blocks,
+            _scale(scale, d), window, sinks, _ptr(out), _ptr(lse), handle)
+    if rc != FA_OK:
+        raise FaError("fa_fwd_paged_fp8", rc)
     return out, lse

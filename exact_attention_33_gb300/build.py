@@ -26,8 +26,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libfa_checked.so")
-SOURCES = ["fa_api.cu", "fa_cache_api.cu", "prefill.cu", "prefill_window.cu", "decode.cu",
-           "decode_fp8.cu", "cache_append.cu", "backward.cu", "backward_window.cu"]
+SOURCES = ["fa_api.cu", "fa_cache_api.cu", "prefill.cu", "prefill_window.cu", "prefill_fp8cache.cu",
+           "decode.cu", "decode_fp8.cu", "cache_append.cu", "backward.cu", "backward_window.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

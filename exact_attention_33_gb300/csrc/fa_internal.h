@@ -43,13 +43,21 @@ constexpr int kPrefill1SoftmaxRegs = 168;
 constexpr int kPrefill1CtlRegs = 88;
 static_assert(128 * kPrefill1SoftmaxRegs + 128 * kPrefill1CtlRegs <= 256 * kPrefill1LaunchRegs,
               "one-tile prefill register split exceeds the launch allocation");
+static_assert(256 * kPrefill1SoftmaxRegs + 256 * kPrefill1CtlRegs <= 512 * kPrefill1LaunchRegs,
+              "8-bit cache prefill register split exceeds the launch allocation");
 
-// Shape of a prefill CTA with QT query tiles.
-template <int QT>
+// Shape of a prefill CTA with QT query tiles.  Over an 8-bit cache (KV8) two
+// query tiles take 512 threads: the softmax warps, a warpgroup of the MMA and
+// the Q copy (warps 10 and 11 idle), and the four warps from kConvWarp on that
+// widen keys and values; the register split is that of the one-tile kernel.
+template <int QT, bool KV8 = false>
 struct PrefillShape {
   static_assert(QT == 1 || QT == 2, "one or two query tiles per CTA");
+  static_assert(!KV8 || QT == 2, "8-bit caches run two query tiles per CTA");
   static constexpr int kRows = kPrefillBM * QT;
-  static constexpr int kThreads = QT == 2 ? kPrefillThreads : 256;
+  static constexpr int kThreads = KV8 ? 512 : QT == 2 ? kPrefillThreads : 256;
+  static constexpr int kConvWarp = 12;
+  static constexpr bool kSplitRegs = QT == 1 || KV8;  // registers move with setmaxnreg
   static constexpr int kSoftmaxWarps = 4 * QT;
   static constexpr int kMmaWarp = kSoftmaxWarps;
   static constexpr int kTmaWarp = kSoftmaxWarps + 1;   // Q and K/V copies (K only when paged)
@@ -109,6 +117,10 @@ struct PrefillParams {
   int max_blocks_per_seq;
   int max_ctx_len;
   int num_blocks;
+  // paged kinds over an 8-bit cache only: e4m3 codes [num_blocks, 16, Hkv, d]
+  // and their scales [num_blocks, Hkv]
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
 };
 
 // ------------------------------------------------------------------- decode

@@ -175,15 +175,24 @@ __device__ __forceinline__ bool varlen_compact_item(const PrefillParams &p, int 
 // WIN: a query at position i sees key j <= i when j > i - p.window or
 // j < p.sinks.  The CTA then streams the key tiles of the sinks and those from
 // the window of its first row on, and leaves the ones between out.
-template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false>
-__global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::kMinBlocks)
+//
+// KV8 (paged kinds, windowed): the cache holds e4m3 codes with a scale per
+// block and KV head.  Warps 12-15 take the place of the K and V copies: they
+// load a tile's codes (16 bytes a lane, the next K and V tile in registers
+// while one is widened), multiply them by their block's scale and store bf16
+// rows in the swizzled layout that the MMAs read.  Widening is exact for
+// scales that are powers of two, else one bf16 rounding of K and V.
+template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false,
+          bool KV8 = false>
+__global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<QT, KV8>::kMinBlocks)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_v1,
                    const __grid_constant__ CUtensorMap tm_o, const PrefillParams p) {
   using L = PrefillLayout<D, FP8, QT>;
-  using Sh = PrefillShape<QT>;
+  using Sh = PrefillShape<QT, KV8>;
+  static_assert(!KV8 || (WIN && (KIND == kKindPaged || KIND == kKindPagedHeads)), "8-bit caches");
   static_assert(!(FP8 && KIND == kKindDenseSplit), "the split-KV layout is bf16 only");
   constexpr int SK = L::kStagesK;
   constexpr int SV = L::kStagesV;
@@ -295,8 +304,10 @@ __global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::
   // Windowed: the first n_sink tiles and, `gap` tiles later, those from the
   // window of the CTA's first row on; key tile j (counted over both) is tile
   // key_tile(j) of the sequence.  A query tile's rows are the CTA's rows (one
-  // query tile, or two heads over the same rows), so one list serves both.
-  static_assert(!WIN || (CAUSAL && !FP8 && (HP || QT == 1) && KIND != kKindDenseSplit),
+  // query tile, or two heads over the same rows), so one list serves both; the
+  // row pairs of an 8-bit cache take the first tile's, and the second tile
+  // meets up to one tile in which it sees nothing.
+  static_assert(!WIN || (CAUSAL && !FP8 && (HP || QT == 1 || KV8) && KIND != kKindDenseSplit),
                 "windowed layouts");
   int n_sink = 0, gap = 0;
   const int win_lo = WIN ? row0 + offset + 1 - p.window : 0;  // first key of row0's window
@@ -355,11 +366,11 @@ __global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::
     // (and K(0)) right away; the other warps wait for it at __syncthreads.
     mbar_init(q_full, 1);
     for (int s = 0; s < SK; ++s) {
-      mbar_init(&k_full[s], 1);
+      mbar_init(&k_full[s], KV8 ? 128 : 1);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < SV; ++s) {
-      mbar_init(&v_full[s], 1);
+      mbar_init(&v_full[s], KV8 ? 128 : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -372,9 +383,11 @@ __global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::
     fence_mbar_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-    if (PAGED) tma_prefetch_desc(&tm_v1);
+    if (!KV8) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      if (PAGED) tma_prefetch_desc(&tm_v1);
+    }
     const int nq = live1 ? 2 : 1;
     mbar_arrive_expect_tx(q_full, nq * L::kTileBytes);
     for (int i = 0; i < nq; ++i) {
@@ -396,7 +409,7 @@ __global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
-  if (PAGED) {
+  if (PAGED && !KV8) {
     // Rows of a V stage that no load fills (keys past the context in the last
     // key tile) must hold finite values: P is 0 there, but 0 * NaN is NaN.
     uint4 *z = reinterpret_cast<uint4 *>(smem + L::kV);
@@ -419,9 +432,127 @@ __global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::
   if (warp >= Sh::kSoftmaxWarps) {
   // One query tile per CTA: this warpgroup (MMA, TMA, two idle warps) hands
   // registers to the softmax warpgroup.
-  if constexpr (QT == 1) setmaxnreg_dec<kPrefill1CtlRegs>();
+  if constexpr (Sh::kSplitRegs) setmaxnreg_dec<kPrefill1CtlRegs>();
   const bool k_producer = warp == Sh::kTmaWarp;  // else the V producer
-  if ((warp == Sh::kTmaWarp || warp == Sh::kTmaVWarp) && PAGED) {
+  if (KV8 && warp == Sh::kTmaWarp) {
+    if (lane == 0) mbar_drain(q_full, 0, p.status);  // no copy outlives the CTA
+  } else if (KV8 && warp >= Sh::kConvWarp) {
+    if constexpr (KV8) {
+      // ---------------------------------------------------- 8-bit K and V
+      // A warp iteration covers 4 rows of d = 128 (8 of d = 64): lane bits 0-1
+      // are the 16-code unit in a 64-column chunk, bit 2 the row's parity, then
+      // (d = 128) the chunk, then the rows above.  So each quarter of the
+      // warp's 16-byte stores is two adjacent rows of one chunk, whose swizzled
+      // units are 8 different ones: no bank conflicts.
+      constexpr int kRowsWarp = 32 / (D / 16);
+      constexpr int kIters = kPrefillBN / (4 * kRowsWarp);
+      const int cw = warp - Sh::kConvWarp;
+      const int c_unit = lane & 3;
+      const int c_chunk = (D == 128) ? (lane >> 3) & 1 : 0;
+      const int c_row = cw * kRowsWarp +
+                        ((D == 128) ? ((lane >> 2) & 1) + 2 * (lane >> 4) : (lane >> 2));
+      const int32_t *trow = p.block_table + static_cast<size_t>(unit) * p.max_blocks_per_seq;
+      constexpr int kBlkPerTile = kPrefillBN / kDecodeBlock;
+      constexpr int kWin = 32 / kBlkPerTile;  // key tiles whose block ids a warp holds
+      const int total_blk = (kv_len + kDecodeBlock - 1) / kDecodeBlock;
+      const size_t n_pool = static_cast<size_t>(p.num_blocks) * kDecodeBlock * p.Hkv * D;
+      // the ids and scales of the blocks of key tiles w .. w + 3 (lane = 8 *
+      // tile + block); -1 for a block that no row sees, or a bad one
+      auto fetch = [&](int w, int &phys, float &ks, float &vs) {
+        phys = -1;
+        ks = vs = 0.f;
+        const int blk = key_tile(w + lane / kBlkPerTile) * kBlkPerTile + lane % kBlkPerTile;
+        if (w + lane / kBlkPerTile >= n_kv || blk >= total_blk) return;
+        if ((blk + 1) * kDecodeBlock <= win_lo && blk * kDecodeBlock >= p.sinks) return;
+        if (!in_bounds(static_cast<size_t>(trow - p.block_table) + blk, 1,
+                       static_cast<size_t>(p.B) * p.max_blocks_per_seq, p.status))
+          return;
+        const int id = trow[blk];
+        if (id < 0 || id >= p.num_blocks) {
+          if (cw == 0) raise_status(p.status, FA_DEV_BAD_BLOCK);
+          return;
+        }
+        phys = id;
+        const size_t sidx = static_cast<size_t>(id) * p.Hkv + kvh;
+        const size_t n = static_cast<size_t>(p.num_blocks) * p.Hkv;
+        ks = checked_load(p.k_scale, sidx, n, p.status);
+        vs = checked_load(p.v_scale, sidx, n, p.status);
+      };
+      int cur, nxt;
+      float cur_k, cur_v, nxt_k, nxt_v;
+      int win_base = 0;
+      fetch(0, cur, cur_k, cur_v);
+      fetch(kWin, nxt, nxt_k, nxt_v);
+      // Loads and widens tile j of K or V.  Tiles are visited in the order
+      // K(0), V(0), K(1), V(1), ...; K(j + 1) is the first to need a new window
+      // of ids, while V(j), already loaded, needs only its scales: each load
+      // keeps the window's scales and its tile's place in them.
+      uint4 kx[kIters], vx[kIters];
+      float k_sc = 0.f, v_sc = 0.f;
+      int k_at = 0, v_at = 0;
+      auto load = [&](int j, bool is_v, uint4(&x)[kIters], float &scl, int &at) {
+        if (j >= win_base + kWin) {
+          win_base += kWin;
+          cur = nxt, cur_k = nxt_k, cur_v = nxt_v;
+          fetch(win_base + kWin, nxt, nxt_k, nxt_v);
+        }
+        const uint8_t *codes = is_v ? p.v_codes : p.k_codes;
+        scl = is_v ? cur_v : cur_k;
+        at = (j - win_base) * kBlkPerTile;
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          const int r = it * 4 * kRowsWarp + c_row;  // row of the tile
+          const int phys = __shfl_sync(0xffffffffu, cur, at + r / kDecodeBlock);
+          const size_t off =
+              ((static_cast<size_t>(phys) * kDecodeBlock + r % kDecodeBlock) * p.Hkv + kvh) * D +
+              c_chunk * 64 + c_unit * 16;
+          // rows past the context (stale slots) and of skipped blocks are 0
+          const bool live = phys >= 0 && key_tile(j) * kPrefillBN + r < kv_len &&
+                            in_bounds(off, 16, n_pool, p.status);
+          x[it] = make_uint4(0u, 0u, 0u, 0u);
+          if (live) x[it] = __ldg(reinterpret_cast<const uint4 *>(codes + off));
+        }
+      };
+      auto widen = [&](uint8_t *tile, const uint4(&x)[kIters], float scl, int at) {
+#pragma unroll
+        for (int it = 0; it < kIters; ++it) {
+          const int r = it * 4 * kRowsWarp + c_row;
+          const uint32_t w[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+          uint32_t o[8];
+          const float sr = __shfl_sync(0xffffffffu, scl, at + r / kDecodeBlock);
+          const float2 s2 = make_float2(sr, sr);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = fmul2(e4m3x2_to_float2(w[e]), s2);
+            const float2 b2 = fmul2(e4m3x2_to_float2(w[e] >> 16), s2);
+            o[2 * e] = pack_bf16x2(a.x, a.y);
+            o[2 * e + 1] = pack_bf16x2(b2.x, b2.y);
+          }
+          uint8_t *row = tile + c_chunk * L::kChunkBytes + r * 128;
+          *reinterpret_cast<uint4 *>(row + (((2 * c_unit) ^ (r & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(row + (((2 * c_unit + 1) ^ (r & 7)) << 4)) =
+              make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_smem();
+      };
+      load(0, false, kx, k_sc, k_at);
+      load(0, true, vx, v_sc, v_at);
+      for (int j = 0; j < n_kv; ++j) {
+        const int sk = j % SK, sv = j % SV;
+        if (j >= SK && !mbar_wait_warp(&k_empty[sk], ((j / SK) - 1) & 1, abort_flag, p.status))
+          break;
+        widen(sK + sk * L::kTileBytes, kx, k_sc, k_at);
+        mbar_arrive(&k_full[sk]);
+        if (j + 1 < n_kv) load(j + 1, false, kx, k_sc, k_at);
+        if (j >= SV && !mbar_wait_warp(&v_empty[sv], ((j / SV) - 1) & 1, abort_flag, p.status))
+          break;
+        widen(sV + sv * L::kTileBytes, vx, v_sc, v_at);
+        mbar_arrive(&v_full[sv]);
+        if (j + 1 < n_kv) load(j + 1, true, vx, v_sc, v_at);
+      }
+    }
+  } else if (!KV8 && (warp == Sh::kTmaWarp || warp == Sh::kTmaVWarp) && PAGED) {
     // ------------------------------------------------------ TMA producer, paged
     // The warp runs converged: lanes 0..7 look up the 8 physical blocks of a
     // 128-key tile in the block table, lane 0 issues the copies.  A block
@@ -538,7 +669,7 @@ __global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::
           mbar_drain(&v_full[j % SV], (j / SV) & 1, p.status);
       }
     }
-  } else if (warp == Sh::kTmaWarp) {
+  } else if (!KV8 && warp == Sh::kTmaWarp) {
     // ------------------------------------------------------ TMA producer
     // The Q tiles of the work item that starts about a wave after this one
     // are read from HBM once: prefetch them into L2 now, so that CTA's first
@@ -740,7 +871,7 @@ __global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::
     }
   }
   } else {
-    if constexpr (QT == 1) setmaxnreg_inc<kPrefill1SoftmaxRegs>();
+    if constexpr (Sh::kSplitRegs) setmaxnreg_inc<kPrefill1SoftmaxRegs>();
     // ------------------------------------------------------ softmax warpgroups
     const int i = warp >> 2;
     const int quad = warp & 3;
@@ -1101,15 +1232,16 @@ __global__ void __launch_bounds__(PrefillShape<QT>::kThreads, PrefillShape<QT>::
 
 // ------------------------------------------------------------------ launch
 
-template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false>
+template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false,
+          bool KV8 = false>
 static cudaError_t launch_prefill_t(const CUtensorMap &tq, const CUtensorMap &tk,
                                     const CUtensorMap &tv, const CUtensorMap &tv1,
                                     const CUtensorMap &to, const PrefillParams &p, int grid,
                                     cudaStream_t stream) {
   using L = PrefillLayout<D, FP8, QT>;
-  using Sh = PrefillShape<QT>;
-  auto kern = prefill_kernel<D, CAUSAL, KIND, FP8, QT, WIN>;
-  if constexpr (QT == 1) {
+  using Sh = PrefillShape<QT, KV8>;
+  auto kern = prefill_kernel<D, CAUSAL, KIND, FP8, QT, WIN, KV8>;
+  if constexpr (Sh::kSplitRegs) {
     // The setmaxnreg split assumes kPrefill1LaunchRegs registers per thread
     // at launch; with fewer, the register increase could never be granted,
     // so such a build is refused instead of launched.

@@ -74,6 +74,23 @@ int fa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
                         float scale, int window, int sinks, void *out, float *lse,
                         void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
+/*
+ * fa_fwd_paged (causal) over the 8-bit cache: query chunks, the last rows of
+ * each sequence's context.  K and V are widened to bf16 on chip and the
+ * products run as in fa_fwd_paged: exactly where a block's scale is a power of
+ * two, with one bf16 rounding of the scaled values where it is not.
+ *   q, out : [total_q, H, d] bf16;  lse : [H, total_q] fp32, may be NULL
+ * Slots past the context never reach the result; a block that no query of a
+ * 128-row tile sees (a window's) is not read and may be freed.  A query that
+ * sees no key gets out = 0 and lse = -inf.
+ */
+int fa_fwd_paged_fp8(const void *q, const void *k_pool, const void *v_pool, const float *k_scale,
+                     const float *v_scale, const int32_t *block_table, int max_blocks_per_seq,
+                     const int32_t *ctx_lens, const int32_t *cu_seqlens_q, int batch, int total_q,
+                     int max_seqlen_q, int max_ctx_len, int H, int Hkv, int d, int block_size,
+                     int num_blocks, float scale, int window, int sinks, void *out, float *lse,
+                     fa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -289,6 +289,92 @@ class _Only:
         self.pool, self.rows = c.pool, lambda x, _, n: c.rows(x, b, n)
 
 
+# ------------------------------------------------------------------ chunks
+
+CHUNKS = [
+    ([1], [1], 1, 1, 64, 0, 0),
+    ([5, 200], [5, 129], 2, 1, 64, 0, 0),
+    ([300, 129, 40], [100, 129, 1], 4, 2, 128, 0, 0),
+    ([700, 16, 0], [300, 3, 2], 3, 1, 64, 0, 0),      # row pairs; no context at all
+    ([1000, 30], [260, 40], 6, 2, 128, 0, 0),         # a chunk longer than its context
+    ([2050], [17], 16, 1, 128, 0, 0),
+    ([900, 41], [400, 20], 3, 1, 128, 128, 0),        # row pairs with a window
+    ([1500, 77], [256, 77], 4, 1, 64, 200, 140),
+    ([2000, 15], [300, 15], 8, 2, 128, 500, 4),
+    ([640], [384], 5, 5, 128, 1, 0),
+]
+
+
+@pytest.mark.parametrize("ctx,new,H,Hkv,d,window,sinks", CHUNKS)
+def test_chunks(fa, ctx, new, H, Hkv, d, window, sinks):
+    """Stale slots hold NaN codes; blocks behind the first query's window have
+    no table entry."""
+    c = Cache(ctx, Hkv, d, seed=80 + d)
+    table = c.table.copy()
+    for b, (n, m) in enumerate(zip(ctx, new)):
+        if n % 16:
+            for x in "kv":
+                c.dpool[x][int(c.table[b, n // 16]), n % 16:] = 0x7F
+        for blk in range((n + 15) // 16):
+            if window and blk * 16 >= sinks and blk * 16 + 16 <= n - m + 1 - window:
+                table[b, blk] = 1 << 29
+    cu = cu_of(new)
+    q = bf16(cr.bf16(np.random.default_rng(d), cu[-1], H, d))
+    out, lse = fa.fa_fwd_paged_fp8(q, *c.args()[:4], dev(table), dev(np.int32(ctx)), dev(cu),
+                                   max(new), max(ctx), window, sinks)
+    assert_device_clean()
+    check_chunks(out, lse, q, c, ctx, cu, window, sinks)
+
+
+def check_chunks(out, lse, q, c, ctx, cu, window, sinks, rounded=False):
+    torch = torch_mod()
+    H, Hkv = q.shape[1], c.pool["k"].shape[2]
+    for b, n in enumerate(ctx):
+        a, e = int(cu[b]), int(cu[b + 1])
+        k, v = c.rows("k", b, n), c.rows("v", b, n)
+        if rounded:
+            k, v = k.to(torch.bfloat16).double(), v.to(torch.bfloat16).double()
+        for h in range(H):
+            kv = h // (H // Hkv)
+            o, l, tol = ref.forward(q[a:e, h].double(), k[:, kv], v[:, kv], window, sinks)
+            ref.assert_within(out[a:e, h], o, tol, f"seq {b} head {h}")
+            ref.assert_lse(lse[h, a:e], l, f"seq {b} head {h}")
+
+
+def test_chunks_with_any_scale(fa):
+    """Scales that are no powers of two: K and V rounded to bf16 once."""
+    torch = torch_mod()
+    ctx, new, H, Hkv, d = [333, 90], [140, 90], 4, 2, 128
+    c = Cache(ctx, Hkv, d, seed=90)
+    rng = np.random.default_rng(91)
+    for x in "kv":
+        c.scale[x] = (0.002 + 0.01 * rng.random(c.scale[x].shape)).astype(np.float32)
+        c.dscale[x].copy_(dev(c.scale[x]))
+    cu = cu_of(new)
+    q = bf16(cr.bf16(rng, cu[-1], H, d))
+    out, lse = fa.fa_fwd_paged_fp8(q, *c.args(), dev(np.int32(ctx)), dev(cu), max(new), max(ctx))
+    assert_device_clean()
+    check_chunks(out, lse, q, c, ctx, cu, 0, 0, rounded=True)
+
+
+def test_chunks_report_bad_blocks(fa):
+    torch = torch_mod()
+    ctx, new, H, Hkv, d = [200, 100], [50, 20], 4, 2, 64
+    c = Cache(ctx, Hkv, d, seed=92)
+    table, lens = c.table.copy(), np.int32(ctx)
+    table[0, 3] = -1
+    cu = cu_of(new)
+    q = bf16(cr.bf16(np.random.default_rng(93), cu[-1], H, d))
+    out, lse = fa.fa_fwd_paged_fp8(q, *c.args()[:4], dev(table), dev(lens), dev(cu), 50, 200)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_DEV_BAD_BLOCK
+    check_chunks(out[50:], lse[:, 50:], q[50:], _Only(c, 1), [100], [0, 20], 0, 0)
+    lens[1] = 10 ** 6
+    fa.fa_fwd_paged_fp8(q, *c.args(), dev(lens), dev(cu), 50, 200)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_DEV_BAD_CTX
+
+
 # ------------------------------------------------------------------ together
 
 def test_serving_run(fa):
@@ -302,6 +388,11 @@ def test_serving_run(fa):
     S = len(prompts)
     c.append(fa, *(cr.bf16(rng, sum(prompts), Hkv, d) for _ in "kv"), prompts, prompts)
     c.check("prompts")
+    # the prompts' own attention, as chunks over what was written
+    q = bf16(cr.bf16(rng, sum(prompts), H, d))
+    got = fa.fa_fwd_paged_fp8(q, *c.args(), dev(np.int32(prompts)), dev(cu_of(prompts)),
+                              max(prompts), max(prompts))
+    check_chunks(*got, q, c, prompts, cu_of(prompts), 0, 0)
     for window, sinks in ((0, 0), (40, 4)):
         q, k, v = (bf16(cr.bf16(rng, S, h, d)) for h in (H, Hkv, Hkv))
         lens, cu = dev(np.int32(prompts)), dev(cu_of([1] * S))
@@ -380,6 +471,11 @@ def test_binding_refuses(fa):
         fa.fa_decode_paged_fp8(q, kp, vp, ks.double(), vs, table, lens, 40)
     with pytest.raises(fa.FaError):
         fa.fa_decode_paged_fp8(q, *c.args(), lens, 4000)
+    for window, sinks in ((-1, 0), (0, 3)):
+        with pytest.raises(ValueError):
+            fa.fa_fwd_paged_fp8(q, *c.args(), lens, dev(np.int32([0, 1])), 1, 40, window, sinks)
+    with pytest.raises(ValueError):
+        fa.fa_fwd_paged_fp8(q, *c.args(), lens, dev(np.int32([0])), 1, 40)
     k = bf16(np.zeros((40, 2, 64), np.float32))
     cu = dev(np.int32([0, 40]))
     with pytest.raises(ValueError):

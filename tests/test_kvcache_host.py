@@ -29,7 +29,7 @@ def test_header_is_exported_and_bound(lib):
     import exact_attention_33_gb300 as fa
     text = open(os.path.join(ROOT, "include", "fa_kvcache.h")).read()
     names = set(re.findall(r"\b(fa_[a-z0-9_]+)\s*\(", re.sub(r"/\*.*?\*/", "", text, flags=re.S)))
-    assert len(names) >= 2
+    assert names == {"fa_cache_append_fp8", "fa_decode_paged_fp8", "fa_fwd_paged_fp8"}
     for name in names:
         assert hasattr(lib, name) and callable(getattr(fa, name)) and name in fa.__all__, name
 
@@ -60,6 +60,15 @@ def test_decode_refusals(lib):
     assert call(ws=NULL) == -4 and call(size=64) == -4 and call(batch=0) == 0
 
 
+def test_chunk_refusals(lib):
+    def call(q=P, scale_ptr=P, cu=P, total=4, max_ctx=64, H=8, d=128, window=0, sinks=0):
+        return lib.fa_fwd_paged_fp8(q, P, P, scale_ptr, P, P, 4, P, cu, 2, total, 4, max_ctx, H, 2, d,
+                                    16, 8, 0.1, window, sinks, P, NULL, NULL)
+    assert call(q=NULL) == -1 and call(q=P_BAD) == -1 and call(scale_ptr=NULL) == -1
+    assert call(cu=NULL) == -1 and call(max_ctx=65) == -1 and call(H=7) == -1
+    assert call(window=-2) == -1 and call(sinks=1) == -1 and call(d=96) == -2 and call(total=0) == 0
+
+
 def test_binding_rejects_host_tensors():
     torch = pytest.importorskip("torch")
     import exact_attention_33_gb300 as fa
@@ -69,6 +78,8 @@ def test_binding_rejects_host_tensors():
     q = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         fa.fa_decode_paged_fp8(q, pool, pool, scale, scale, i[None], i, 1)
+    with pytest.raises(ValueError):
+        fa.fa_fwd_paged_fp8(q, pool, pool, scale, scale, i[None], i, i, 1, 1)
     with pytest.raises(ValueError):
         fa.fa_cache_append_fp8(q, q, pool, pool, scale, scale, i[None], i, i, 1)
 
