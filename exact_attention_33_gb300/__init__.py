@@ -47,6 +47,7 @@ FA_WORKSPACE_HEADER_BYTES = 256   # control block at the start of a decode / spl
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
 _lib = None
+_torch_module = None   # imported by the first call that needs it
 
 
 class FaError(RuntimeError):
@@ -207,8 +208,11 @@ def new_workspace(nbytes: int, device=None):
 # ----------------------------------------------------------------- helpers
 
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream=None, device=None):
@@ -641,23 +645,87 @@ def _check_window(window, sinks):
 class _Launch:
     """``with _Launch(stream, dev) as handle``: the call's device is current,
     and so is ``stream`` where one is given, so that what the call allocates
-    (outputs, workspace) belongs to the stream that it runs on."""
+    (outputs, workspace) belongs to the stream that it runs on.  ``handle`` is
+    the stream's address."""
 
     __slots__ = ("context", "stream", "device")
 
     def __init__(self, stream, device):
         cuda = _torch().cuda
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream must be a stream of {device}")
-        self.context = cuda.device(device) if stream is None else cuda.stream(stream)
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream must be a stream of {device}")
+            self.context = cuda.stream(stream)
+        else:  # entering a device costs more than asking which one is current
+            self.context = None if cuda.current_device() == device.index else cuda.device(device)
         self.stream, self.device = stream, device
 
     def __enter__(self):
-        self.context.__enter__()
-        return _stream_handle(self.stream, self.device)
+        if self.context is not None:
+            self.context.__enter__()
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return _current_stream(self.device)
 
     def __exit__(self, *exc):
-        return self.context.__exit__(*exc)
+        return self.context.__exit__(*exc) if self.context is not None else None
+
+
+def _current_stream(device):
+    """Address of the device's current stream, without a Stream object where
+    torch offers that."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
+
+
+def _are(dtype, index, *pairs):
+    """Every (tensor, shape) of ``pairs`` is a contiguous tensor of this type
+    and shape on CUDA device ``index``.  The calls ask this first; the checks
+    that name what is wrong run only when the answer is no."""
+    try:
+        for t, shape in pairs:
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != index \
+                    or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return True
+
+
+def _addr(t):
+    """Device address of a tensor, 0 for None (the C arguments take an int)."""
+    return 0 if t is None else t.data_ptr()
+
+
+def _results(q, lse_shape, out, lse, want_lse):
+    """The output tensors: the caller's, checked, or new ones."""
+    if out is not None or lse is not None:
+        return _outputs(q.shape, lse_shape, out, lse, want_lse, q.device)
+    torch = _torch()
+    return torch.empty(q.shape, dtype=q.dtype, device=q.device), \
+        torch.empty(lse_shape, dtype=torch.float32, device=q.device) if want_lse else None
+
+
+def _check_table(block_table, ctx_lens, batch, dev):
+    i32 = _torch().int32
+    if not _are(i32, dev.index, (block_table, (batch, *block_table.shape[1:])), (ctx_lens, (batch,))) \
+            or block_table.dim() != 2:
+        _check_int32("block_table", block_table, dev, ndim=2)
+        _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
+        raise ValueError("block_table must have one row per sequence")
+
+
+def _check_sequences(block_table, ctx_lens, cu_seqlens, cu_name, dev):
+    """Checks the int32 arrays of a call on packed rows over a cache; returns
+    the number of sequences."""
+    shape = getattr(block_table, "shape", ())
+    if len(shape) != 2 or not _are(_torch().int32, dev.index, (block_table, shape),
+                                   (ctx_lens, shape[:1]), (cu_seqlens, (shape[0] + 1,))):
+        _check_int32("block_table", block_table, dev, ndim=2)
+        _check_int32("ctx_lens", ctx_lens, dev, numel=block_table.shape[0])
+        _check_int32(cu_name, cu_seqlens, dev, numel=block_table.shape[0] + 1)
+    return block_table.shape[0]
 
 
 def fa_fwd_window(q, k, v, window, sinks=0, scale=None, out=None, lse=None, want_lse=True,
@@ -669,16 +737,17 @@ def fa_fwd_window(q, k, v, window, sinks=0, scale=None, out=None, lse=None, want
     """
     _check_bf16_cuda("q", q, 4)
     dev = q.device
-    for name, t in (("k", k), ("v", v)):
-        _check_bf16_cuda(name, t, 4, dev)
-    window, sinks = _check_window(window, sinks)
     B, N, H, d = q.shape
-    Hkv = k.shape[2]
-    if k.shape != (B, N, Hkv, d) or v.shape != k.shape:
+    if not _are(q.dtype, dev.index, (k, v.shape), (v, k.shape)) or k.dim() != 4 \
+            or k.shape[:2] != (B, N) or k.shape[3] != d:
+        for name, t in (("k", k), ("v", v)):
+            _check_bf16_cuda(name, t, 4, dev)
         raise ValueError("k and v must be [B, N, Hkv, d] matching q")
+    Hkv = k.shape[2]
+    window, sinks = _check_window(window, sinks)
     with _Launch(stream, dev) as handle:
-        out, lse = _outputs(q.shape, (B, H, N), out, lse, want_lse, dev)
-        rc = load_library().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H,
+        out, lse = _results(q, (B, H, N), out, lse, want_lse)
+        rc = load_library().fa_fwd_window(_addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), B, H,
                                           Hkv, N, d, _scale(scale, d), window, sinks,
                                           handle)
     if rc != FA_OK:
@@ -695,20 +764,21 @@ def fa_fwd_varlen_window(q, k, v, cu_seqlens, max_seqlen, window, sinks=0, scale
     """
     _check_bf16_cuda("q", q, 3)
     dev = q.device
-    for name, t in (("k", k), ("v", v)):
-        _check_bf16_cuda(name, t, 3, dev)
+    T, H, d = q.shape
+    if not _are(q.dtype, dev.index, (k, v.shape), (v, k.shape)) or k.dim() != 3 \
+            or k.shape[0] != T or k.shape[2] != d:
+        for name, t in (("k", k), ("v", v)):
+            _check_bf16_cuda(name, t, 3, dev)
+        raise ValueError("k and v must be [T, Hkv, d] matching q")
+    Hkv = k.shape[1]
     _check_int32("cu_seqlens", cu_seqlens, dev)
     if cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must hold num_seqs + 1 offsets")
     window, sinks = _check_window(window, sinks)
-    T, H, d = q.shape
-    Hkv = k.shape[1]
-    if k.shape != (T, Hkv, d) or v.shape != k.shape:
-        raise ValueError("k and v must be [T, Hkv, d] matching q")
     with _Launch(stream, dev) as handle:
-        out, lse = _outputs(q.shape, (H, T), out, lse, want_lse, dev)
+        out, lse = _results(q, (H, T), out, lse, want_lse)
         rc = load_library().fa_fwd_varlen_window(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
+            _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), _addr(cu_seqlens),
             cu_seqlens.numel() - 1, T, int(max_seqlen), H, Hkv, d, _scale(scale, d), window, sinks,
             handle)
     if rc != FA_OK:
@@ -725,20 +795,17 @@ def fa_fwd_paged_window(q, k_pool, v_pool, block_table, ctx_lens, cu_seqlens_q, 
     _check_bf16_cuda("q", q, 3)
     dev = q.device
     num_blocks, block_size, Hkv, dp = _check_pools(k_pool, v_pool, dev)
-    _check_int32("block_table", block_table, dev, ndim=2)
-    batch = block_table.shape[0]
-    _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
-    _check_int32("cu_seqlens_q", cu_seqlens_q, dev, numel=batch + 1)
+    batch = _check_sequences(block_table, ctx_lens, cu_seqlens_q, "cu_seqlens_q", dev)
     window, sinks = _check_window(window, sinks)
     Tq, H, d = q.shape
     if dp != d:
         raise ValueError("the pools' head size must match q")
     with _Launch(stream, dev) as handle:
-        out, lse = _outputs(q.shape, (H, Tq), out, lse, want_lse, dev)
+        out, lse = _results(q, (H, Tq), out, lse, want_lse)
         rc = load_library().fa_fwd_paged_window(
-            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), block_table.shape[1],
-            _ptr(ctx_lens), _ptr(cu_seqlens_q), batch, Tq, int(max_seqlen_q), int(max_ctx_len), H,
-            Hkv, d, block_size, num_blocks, _scale(scale, d), window, sinks, _ptr(out), _ptr(lse),
+            _addr(q), _addr(k_pool), _addr(v_pool), _addr(block_table), block_table.shape[1],
+            _addr(ctx_lens), _addr(cu_seqlens_q), batch, Tq, int(max_seqlen_q), int(max_ctx_len), H,
+            Hkv, d, block_size, num_blocks, _scale(scale, d), window, sinks, _addr(out), _addr(lse),
             handle)
     if rc != FA_OK:
         raise FaError("fa_fwd_paged_window", rc)
@@ -758,18 +825,25 @@ def fa_decode_paged_window(q, k_pool, v_pool, block_table, ctx_lens, max_ctx_len
                            stream=None):
     """:func:`fa_decode_paged` over the last ``window`` keys and the first
     ``sinks`` keys of each sequence; other blocks are not read."""
-    dev, batch, H, Hkv, d, num_blocks, block_size = _decode_args(q, k_pool, v_pool,
-                                                                 block_table, ctx_lens)
+    _check_bf16_cuda("q", q, 3)
+    dev = q.device
+    batch, H, d = q.shape
+    if not _are(q.dtype, dev.index, (k_pool, v_pool.shape), (v_pool, k_pool.shape)) \
+            or k_pool.dim() != 4 or k_pool.shape[3] != d:
+        _check_pools(k_pool, v_pool, dev)
+        raise ValueError("the pools' head size must match q")
+    num_blocks, block_size, Hkv, _ = k_pool.shape
+    _check_table(block_table, ctx_lens, batch, dev)
     window, sinks = _check_window(window, sinks)
     with _Launch(stream, dev) as handle:
         need = 0 if workspace is not None else fa_decode_window_workspace_size(
             batch, H, Hkv, d, max_ctx_len, window, sinks, block_size)
         workspace = _workspace(workspace, need, dev, 256, zero=True)
-        out, lse = _outputs(q.shape, (batch, H), out, lse, want_lse, dev)
+        out, lse = _results(q, (batch, H), out, lse, want_lse)
         rc = load_library().fa_decode_paged_window(
-            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(block_table), block_table.shape[1],
-            _ptr(ctx_lens), int(max_ctx_len), batch, H, Hkv, d, block_size, num_blocks,
-            _scale(scale, d), window, sinks, _ptr(out), _ptr(lse), _ptr(workspace),
+            _addr(q), _addr(k_pool), _addr(v_pool), _addr(block_table), block_table.shape[1],
+            _addr(ctx_lens), int(max_ctx_len), batch, H, Hkv, d, block_size, num_blocks,
+            _scale(scale, d), window, sinks, _addr(out), _addr(lse), _addr(workspace),
             workspace.numel(), handle)
     if rc != FA_OK:
         raise FaError("fa_decode_paged_window", rc)
@@ -820,8 +894,8 @@ def fa_bwd_window(q, k, v, out, lse, dout, window, sinks=0, scale=None, dq=None,
             B, H, Hkv, N, d, window, sinks)
         workspace = _workspace(workspace, need, dev)
         rc = load_library().fa_bwd_window(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
-            _ptr(dv), B, H, Hkv, N, d, _scale(scale, d), window, sinks, _ptr(workspace),
+            _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), _addr(dout), _addr(dq), _addr(dk),
+            _addr(dv), B, H, Hkv, N, d, _scale(scale, d), window, sinks, _addr(workspace),
             workspace.numel(), handle)
     if rc != FA_OK:
         raise FaError("fa_bwd_window", rc)
@@ -847,9 +921,9 @@ def fa_bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window
             S, H, Hkv, min(int(max_seqlen), T), d, window, sinks)
         workspace = _workspace(workspace, need, dev)
         rc = load_library().fa_bwd_varlen_window(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
-            _ptr(dv), _ptr(cu_seqlens), S, T, int(max_seqlen), H, Hkv, d, _scale(scale, d), window,
-            sinks, _ptr(workspace), workspace.numel(), handle)
+            _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), _addr(dout), _addr(dq), _addr(dk),
+            _addr(dv), _addr(cu_seqlens), S, T, int(max_seqlen), H, Hkv, d, _scale(scale, d), window,
+            sinks, _addr(workspace), workspace.numel(), handle)
     if rc != FA_OK:
         raise FaError("fa_bwd_varlen_window", rc)
     return dq, dk, dv
@@ -861,14 +935,18 @@ def fa_bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window
 # KV head (include/fa_kvcache.h).
 
 def _check_cache(k_pool, v_pool, k_scale, v_scale, dev):
-    _check_fp8("k_pool", k_pool, 4, dev)
-    _check_fp8("v_pool", v_pool, 4, dev)
-    if v_pool.shape != k_pool.shape:
-        raise ValueError("k_pool and v_pool must have the same shape [num_blocks,16,Hkv,d]")
-    num_blocks, _, Hkv, _ = k_pool.shape
-    f32 = _torch().float32
-    _check_tensor("k_scale", k_scale, (num_blocks, Hkv), f32, dev)
-    _check_tensor("v_scale", v_scale, (num_blocks, Hkv), f32, dev)
+    torch = _torch()
+    shape = getattr(k_pool, "shape", ())
+    if len(shape) != 4 or k_pool.dtype not in (torch.uint8, torch.float8_e4m3fn) \
+            or not _are(k_pool.dtype, dev.index, (k_pool, shape), (v_pool, shape)) \
+            or not _are(torch.float32, dev.index, (k_scale, shape[::2]), (v_scale, shape[::2])):
+        _check_fp8("k_pool", k_pool, 4, dev)
+        _check_fp8("v_pool", v_pool, 4, dev)
+        if v_pool.shape != k_pool.shape:
+            raise ValueError("k_pool and v_pool must have the same shape [num_blocks,16,Hkv,d]")
+        num_blocks, _, Hkv, _ = k_pool.shape
+        _check_tensor("k_scale", k_scale, (num_blocks, Hkv), torch.float32, dev)
+        _check_tensor("v_scale", v_scale, (num_blocks, Hkv), torch.float32, dev)
     return k_pool.shape
 
 
@@ -911,15 +989,12 @@ def fa_cache_append_fp8(k, v, k_pool, v_pool, k_scale, v_scale, block_table, ctx
     v_stride = _check_token_rows("v", v, Hkv, d)
     if v.shape[0] != k.shape[0] or v.device != dev:
         raise ValueError("k and v must have the same tokens on one device")
-    _check_int32("block_table", block_table, dev, ndim=2)
-    batch = block_table.shape[0]
-    _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
-    _check_int32("cu_seqlens", cu_seqlens, dev, numel=batch + 1)
+    batch = _check_sequences(block_table, ctx_lens, cu_seqlens, "cu_seqlens", dev)
     with _Launch(stream, dev) as handle:
         rc = load_library().fa_cache_append_fp8(
-            _ptr(k), _ptr(v), k_stride, v_stride, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
-            _ptr(v_scale), _ptr(block_table), block_table.shape[1], _ptr(ctx_lens),
-            _ptr(cu_seqlens), batch, k.shape[0], int(max_new), Hkv, d, block_size, num_blocks,
+            _addr(k), _addr(v), k_stride, v_stride, _addr(k_pool), _addr(v_pool), _addr(k_scale),
+            _addr(v_scale), _addr(block_table), block_table.shape[1], _addr(ctx_lens),
+            _addr(cu_seqlens), batch, k.shape[0], int(max_new), Hkv, d, block_size, num_blocks,
             handle)
     if rc != FA_OK:
         raise FaError("fa_cache_append_fp8", rc)
@@ -940,10 +1015,7 @@ def fa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_le
     batch, H, d = q.shape
     if dp != d:
         raise ValueError("the pools' head size must match q")
-    _check_int32("block_table", block_table, dev, ndim=2)
-    if block_table.shape[0] != batch:
-        raise ValueError("block_table must have one row per sequence of q")
-    _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
+    _check_table(block_table, ctx_lens, batch, dev)
     window, sinks = _check_cache_window(window, sinks)
     with _Launch(stream, dev) as handle:
         need = 0
@@ -951,11 +1023,11 @@ def fa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_le
             need = fa_decode_window_workspace_size(batch, H, Hkv, d, max_ctx_len, window, sinks,
                                                    block_size)
         workspace = _workspace(workspace, need, dev, 256, zero=True)
-        out, lse = _outputs(q.shape, (batch, H), out, lse, want_lse, dev)
+        out, lse = _results(q, (batch, H), out, lse, want_lse)
         rc = load_library().fa_decode_paged_fp8(
-            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-            block_table.shape[1], _ptr(ctx_lens), int(max_ctx_len), batch, H, Hkv, d, block_size,
-            num_blocks, _scale(scale, d), window, sinks, _ptr(out), _ptr(lse), _ptr(workspace),
+            _addr(q), _addr(k_pool), _addr(v_pool), _addr(k_scale), _addr(v_scale), _addr(block_table),
+            block_table.shape[1], _addr(ctx_lens), int(max_ctx_len), batch, H, Hkv, d, block_size,
+            num_blocks, _scale(scale, d), window, sinks, _addr(out), _addr(lse), _addr(workspace),
             workspace.numel(), handle)
     if rc != FA_OK:
         raise FaError("fa_decode_paged_fp8", rc)
@@ -975,21 +1047,18 @@ def fa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_lens,
     _check_bf16_cuda("q", q, 3)
     dev = q.device
     num_blocks, block_size, Hkv, dp = _check_cache(k_pool, v_pool, k_scale, v_scale, dev)
-    _check_int32("block_table", block_table, dev, ndim=2)
-    batch = block_table.shape[0]
-    _check_int32("ctx_lens", ctx_lens, dev, numel=batch)
-    _check_int32("cu_seqlens_q", cu_seqlens_q, dev, numel=batch + 1)
+    batch = _check_sequences(block_table, ctx_lens, cu_seqlens_q, "cu_seqlens_q", dev)
     window, sinks = _check_cache_window(window, sinks)
     Tq, H, d = q.shape
     if dp != d:
         raise ValueError("the pools' head size must match q")
     with _Launch(stream, dev) as handle:
-        out, lse = _outputs(q.shape, (H, Tq), out, lse, want_lse, dev)
+        out, lse = _results(q, (H, Tq), out, lse, want_lse)
         rc = load_library().fa_fwd_paged_fp8(
-            _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-            block_table.shape[1], _ptr(ctx_lens), _ptr(cu_seqlens_q), batch, Tq,
+            _addr(q), _addr(k_pool), _addr(v_pool), _addr(k_scale), _addr(v_scale), _addr(block_table),
+            block_table.shape[1], _addr(ctx_lens), _addr(cu_seqlens_q), batch, Tq,
             int(max_seqlen_q), int(max_ctx_len), H, Hkv, d, block_size, num_blocks,
-            _scale(scale, d), window, sinks, _ptr(out), _ptr(lse), handle)
+            _scale(scale, d), window, sinks, _addr(out), _addr(lse), handle)
     if rc != FA_OK:
         raise FaError("fa_fwd_paged_fp8", rc)
     return out, lse

@@ -13,7 +13,8 @@ cudaError_t launch_cache_append(const AppendParams &p, int d, cudaStream_t strea
 cudaError_t launch_decode_fp8(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeParams &p,
                               const CacheScales &sc, int d, cudaStream_t stream);
 
-cudaError_t launch_prefill_fp8cache(const CUtensorMap &tq, const CUtensorMap &to,
+cudaError_t launch_prefill_fp8cache(const CUtensorMap &tq, const CUtensorMap &tk,
+                                    const CUtensorMap &tv, const CUtensorMap &to,
                                     const PrefillParams &p, int d, bool head_pairs, int grid,
                                     cudaStream_t stream);
 
@@ -188,8 +189,12 @@ int fa_fwd_paged_fp8(const void *q, const void *k_pool, const void *v_pool, cons
   if (grid > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(total_q) * H * d * 2 >= (1LL << 40)) return FA_ERR_UNSUPPORTED;
 
-  CUtensorMap tq, to;
+  CUtensorMap tq, tk, tv, to;
+  const long long tokens = static_cast<long long>(num_blocks) * block_size;
   int rc = make_map(&tq, q, d, H, total_q, 1, kPrefillBM);
+  // (the widening warps read the codes themselves: rows as they are)
+  if (rc == FA_OK) rc = make_pool_map(&tk, k_pool, d, Hkv, tokens, kDecodeBlock, 1, false);
+  if (rc == FA_OK) rc = make_pool_map(&tv, v_pool, d, Hkv, tokens, kDecodeBlock, 1, false);
   if (rc == FA_OK) rc = make_map(&to, out, d, H, total_q, 1, kPrefillBM);
   if (rc != FA_OK) return rc;
 
@@ -215,8 +220,6 @@ int fa_fwd_paged_fp8(const void *q, const void *k_pool, const void *v_pool, cons
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.max_ctx_len = max_ctx_len;
   p.num_blocks = num_blocks;
-  p.k_codes = static_cast<const uint8_t *>(k_pool);
-  p.v_codes = static_cast<const uint8_t *>(v_pool);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   // without a window: one that reaches over any context
@@ -224,7 +227,7 @@ int fa_fwd_paged_fp8(const void *q, const void *k_pool, const void *v_pool, cons
       clamp_window({window == 0 ? std::max(1, max_ctx_len) : window, sinks}, max_ctx_len);
   p.window = win.window;
   p.sinks = win.sinks;
-  return launch_prefill_fp8cache(tq, to, p, d, head_pairs, static_cast<int>(grid),
+  return launch_prefill_fp8cache(tq, tk, tv, to, p, d, head_pairs, static_cast<int>(grid),
                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;

@@ -72,9 +72,9 @@ inline int fp8_swz(int d) { return d < 128 ? d : 128; }
 // Paged pool [num_blocks * block_size tokens][Hkv][d] of bf16 values or e4m3
 // codes as a 3-D map; each copy moves one swizzled row per token, {64, 1,
 // box_rows} bf16 values (a whole 16-token block, or one token row), or {d, 1,
-// box_rows} codes with the 128- or 64-byte swizzle.
+// box_rows} codes with the 128- or 64-byte swizzle, or without one.
 inline int make_pool_map(CUtensorMap *map, const void *base, int d, int heads, long long tokens,
-                  int box_rows = kDecodeBlock, int elem_bytes = 2) {
+                  int box_rows = kDecodeBlock, int elem_bytes = 2, bool swizzled = true) {
   auto fn = encode_fn();
   if (fn == nullptr) return FA_ERR_CUDA;
   const cuuint64_t eb = static_cast<cuuint64_t>(elem_bytes);
@@ -89,7 +89,9 @@ inline int make_pool_map(CUtensorMap *map, const void *base, int d, int heads, l
   CUresult r = fn(map,
                   elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                   3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swz == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  !swizzled   ? CU_TENSOR_MAP_SWIZZLE_NONE
+                  : swz == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                              : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }

@@ -48,7 +48,7 @@ static_assert(256 * kPrefill1SoftmaxRegs + 256 * kPrefill1CtlRegs <= 512 * kPref
 
 // Shape of a prefill CTA with QT query tiles.  Over an 8-bit cache (KV8) two
 // query tiles take 512 threads: the softmax warps, a warpgroup of the MMA and
-// the Q copy (warps 10 and 11 idle), and the four warps from kConvWarp on that
+// the copies (warp 11 idles), and the four warps from kConvWarp on that
 // widen keys and values; the register split is that of the one-tile kernel.
 template <int QT, bool KV8 = false>
 struct PrefillShape {
@@ -117,9 +117,7 @@ struct PrefillParams {
   int max_blocks_per_seq;
   int max_ctx_len;
   int num_blocks;
-  // paged kinds over an 8-bit cache only: e4m3 codes [num_blocks, 16, Hkv, d]
-  // and their scales [num_blocks, Hkv]
-  const uint8_t *k_codes, *v_codes;
+  // paged kinds over an 8-bit cache only: the codes' scales [num_blocks, Hkv]
   const float *k_scale, *v_scale;
 };
 

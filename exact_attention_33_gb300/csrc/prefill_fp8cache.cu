@@ -11,22 +11,23 @@
 namespace fa {
 
 template <int D>
-static cudaError_t launch_prefill_fp8cache_d(const CUtensorMap &tq, const CUtensorMap &to,
+static cudaError_t launch_prefill_fp8cache_d(const CUtensorMap &tq, const CUtensorMap &tk,
+                                             const CUtensorMap &tv, const CUtensorMap &to,
                                              const PrefillParams &p, bool head_pairs, int grid,
                                              cudaStream_t stream) {
-  // (the kernel has no use for K and V maps)
   return head_pairs
-             ? launch_prefill_t<D, true, kKindPagedHeads, false, 2, true, true>(tq, tq, tq, tq, to, p,
+             ? launch_prefill_t<D, true, kKindPagedHeads, false, 2, true, true>(tq, tk, tv, tv, to, p,
                                                                                grid, stream)
-             : launch_prefill_t<D, true, kKindPaged, false, 2, true, true>(tq, tq, tq, tq, to, p,
+             : launch_prefill_t<D, true, kKindPaged, false, 2, true, true>(tq, tk, tv, tv, to, p,
                                                                           grid, stream);
 }
 
-cudaError_t launch_prefill_fp8cache(const CUtensorMap &tq, const CUtensorMap &to,
+cudaError_t launch_prefill_fp8cache(const CUtensorMap &tq, const CUtensorMap &tk,
+                                    const CUtensorMap &tv, const CUtensorMap &to,
                                     const PrefillParams &p, int d, bool head_pairs, int grid,
                                     cudaStream_t stream) {
-  return d == 64 ? launch_prefill_fp8cache_d<64>(tq, to, p, head_pairs, grid, stream)
-                 : launch_prefill_fp8cache_d<128>(tq, to, p, head_pairs, grid, stream);
+  return d == 64 ? launch_prefill_fp8cache_d<64>(tq, tk, tv, to, p, head_pairs, grid, stream)
+                 : launch_prefill_fp8cache_d<128>(tq, tk, tv, to, p, head_pairs, grid, stream);
 }
 
 }  // namespace fa

@@ -52,7 +52,7 @@ constexpr float kRescaleLog2 = 8.f;
 
 
 
-template <int D, bool FP8 = false, int QT = 2>
+template <int D, bool FP8 = false, int QT = 2, bool KV8 = false>
 struct PrefillLayout {
   static constexpr int kElemBytes = FP8 ? 1 : 2;
   // Rows are copied and read in swizzled rows of 128 bytes, or of 64 bytes
@@ -71,9 +71,11 @@ struct PrefillLayout {
 #define FA_PREFILL_STAGES_V128 2
 #endif
   // With one query tile per CTA two CTAs share an SM's shared memory, so
-  // 32 KiB tiles get one stage each.
+  // 32 KiB tiles get one stage each.  Over an 8-bit cache a tile of codes of
+  // each of K and V is staged too, at the cost of a third K stage.
   static constexpr int kStagesK =
-      (QT == 1) ? ((kTileBytes == 32768) ? 1 : 2) : ((kTileBytes == 32768) ? FA_PREFILL_STAGES_K128 : 5);
+      (QT == 1) ? ((kTileBytes == 32768) ? 1 : 2)
+                : ((kTileBytes == 32768) ? (KV8 ? 2 : FA_PREFILL_STAGES_K128) : 5);
   static constexpr int kStagesV =
       (QT == 1) ? ((kTileBytes == 32768) ? 1 : 2) : ((kTileBytes == 32768) ? FA_PREFILL_STAGES_V128 : 5);
   // Row sums on the tensor cores (d = 64): the P V product also multiplies
@@ -87,11 +89,14 @@ struct PrefillLayout {
   static constexpr int kK = kQ + QT * kTileBytes;
   static constexpr int kV = kK + kStagesK * kTileBytes;
   static constexpr int kOnesOff = kV + kStagesV * kTileBytes;  // 128 x 64 bf16 ones (one chunk)
-  static constexpr int kBar = kOnesOff + (kOnes ? kChunkBytes : 0);
+  static constexpr int kCodes = kOnesOff + (kOnes ? kChunkBytes : 0);  // e4m3 codes of K, then V
+  static constexpr int kCodeBytes = KV8 ? 128 * D : 0;                 // one tile of codes
+  static constexpr int kBar = kCodes + 2 * kCodeBytes;
   // q_full, k_full[SK], k_empty[SK], v_full[SV], s_full[2], p_full[2],
-  // o_done[2], drain, v_empty[SV].  A V stage is released as soon as the
+  // o_done[2], drain, v_empty[SV], and over an 8-bit cache c_full[2],
+  // c_empty[2] of the staged codes.  A V stage is released as soon as the
   // P V products of its key tile are done.
-  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7;
+  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7 + (KV8 ? 4 : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kSmemAlloc = kBytes + 1024;     // base is aligned up to 1024 in-kernel
@@ -177,11 +182,17 @@ __device__ __forceinline__ bool varlen_compact_item(const PrefillParams &p, int 
 // the window of its first row on, and leaves the ones between out.
 //
 // KV8 (paged kinds, windowed): the cache holds e4m3 codes with a scale per
-// block and KV head.  Warps 12-15 take the place of the K and V copies: they
-// load a tile's codes (16 bytes a lane, the next K and V tile in registers
-// while one is widened), multiply them by their block's scale and store bf16
-// rows in the swizzled layout that the MMAs read.  Widening is exact for
-// scales that are powers of two, else one bf16 rounding of K and V.
+// block and KV head.  Warps 9 and 10 copy the codes of a K and a V tile into
+// staging buffers; warps 12-15 multiply them by their block's scale and store
+// bf16 rows in the swizzled layout that the MMAs read, handing each buffer
+// back at once, so the next tile's codes arrive while this one is multiplied.
+// Bound by these warps' conversions and shared-memory traffic (codes in and
+// out, bf16 rows in, beside the MMAs' operand reads): 4 x 512 rows over 8192
+// keys, 32 / 8 heads of d = 128 take 315 us against 206 us over a bf16 cache
+// (264 us with the conversions' arithmetic left out).  Codes loaded straight
+// into registers, 32 or 64 of a thread's 88 in flight, took 470 to 620 us.
+// Widening is exact for scales that are powers of two, else one bf16 rounding
+// of K and V.
 template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false,
           bool KV8 = false>
 __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<QT, KV8>::kMinBlocks)
@@ -190,7 +201,8 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
                    const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_v1,
                    const __grid_constant__ CUtensorMap tm_o, const PrefillParams p) {
-  using L = PrefillLayout<D, FP8, QT>;
+  using L = PrefillLayout<D, FP8, QT, KV8>;
+  static_assert(L::kSmemAlloc <= 232448, "prefill shared memory exceeds 227 KiB");
   using Sh = PrefillShape<QT, KV8>;
   static_assert(!KV8 || (WIN && (KIND == kKindPaged || KIND == kKindPagedHeads)), "8-bit caches");
   static_assert(!(FP8 && KIND == kKindDenseSplit), "the split-KV layout is bf16 only");
@@ -347,6 +359,8 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
   uint64_t *o_done = p_full + 2;
   uint64_t *drain = o_done + 2;
   uint64_t *v_empty = drain + 1;  // V-stage releases
+  uint64_t *c_full = v_empty + SV;  // 8-bit caches: codes of K [0] and V [1] staged
+  uint64_t *c_empty = c_full + 2;   // and read by the four widening warps
   constexpr bool ONES = L::kOnes;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
@@ -379,15 +393,19 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     }
     mbar_init(drain, 1);
     for (int s = 0; s < SV; ++s) mbar_init(&v_empty[s], 1);
+    if (KV8) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&c_full[i], 1);
+        mbar_init(&c_empty[i], 4);
+      }
+    }
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&tm_q);
-    if (!KV8) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-      if (PAGED) tma_prefetch_desc(&tm_v1);
-    }
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    if (PAGED && !KV8) tma_prefetch_desc(&tm_v1);
     const int nq = live1 ? 2 : 1;
     mbar_arrive_expect_tx(q_full, nq * L::kTileBytes);
     for (int i = 0; i < nq; ++i) {
@@ -434,122 +452,140 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
   // registers to the softmax warpgroup.
   if constexpr (Sh::kSplitRegs) setmaxnreg_dec<kPrefill1CtlRegs>();
   const bool k_producer = warp == Sh::kTmaWarp;  // else the V producer
-  if (KV8 && warp == Sh::kTmaWarp) {
-    if (lane == 0) mbar_drain(q_full, 0, p.status);  // no copy outlives the CTA
+  constexpr int kTileBlocks = kPrefillBN / kDecodeBlock;  // cache blocks of a key tile
+  constexpr int kIdTiles = 32 / kTileBlocks;              // key tiles whose ids a warp holds
+  // Physical block of lane % 8 of key tile w + lane / 8 (8-bit caches): -1
+  // past this CTA's tiles or the context, for a block that no row of the CTA
+  // sees (its id is not looked at: it may be freed), and for a bad id.
+  auto cache_block = [&](int w, bool report) -> int {
+    const int blk = key_tile(w + lane / kTileBlocks) * kTileBlocks + lane % kTileBlocks;
+    if (w + lane / kTileBlocks >= n_kv || blk * kDecodeBlock >= kv_len) return -1;
+    if ((blk + 1) * kDecodeBlock <= win_lo && blk * kDecodeBlock >= p.sinks) return -1;
+    const size_t at = static_cast<size_t>(unit) * p.max_blocks_per_seq + blk;
+    if (!in_bounds(at, 1, static_cast<size_t>(p.B) * p.max_blocks_per_seq, p.status)) return -1;
+    const int id = p.block_table[at];
+    if (id >= 0 && id < p.num_blocks) return id;
+    if (report) raise_status(p.status, FA_DEV_BAD_BLOCK);
+    return -1;
+  };
+  if (KV8 && (warp == Sh::kTmaWarp || warp == Sh::kTmaVWarp)) {
+    if constexpr (KV8) {
+      // ------------------------------------------------- copies of codes
+      // One copy per block, issued by lanes 0 .. 7 after lane 0 has posted the
+      // byte count.  Block ids are read four tiles ahead of their use.
+      const int which = k_producer ? 0 : 1;
+      uint8_t *stage = smem + L::kCodes + which * L::kCodeBytes;
+      const CUtensorMap *map = k_producer ? &tm_k : &tm_v;
+      int cur = cache_block(0, k_producer), nxt = cache_block(kIdTiles, k_producer);
+      int issued = 0;
+      for (int j = 0; j < n_kv; ++j) {
+        if (j > 0 && j % kIdTiles == 0) {
+          cur = nxt;
+          nxt = cache_block(j + kIdTiles, k_producer);
+        }
+        const int phys = __shfl_sync(0xffffffffu, cur, (j % kIdTiles) * kTileBlocks + (lane & 7));
+        const bool mine = lane < kTileBlocks && phys >= 0;
+        const unsigned live = __ballot_sync(0xffffffffu, mine);
+        if (j > 0 && !mbar_wait_warp(&c_empty[which], (j - 1) & 1, abort_flag, p.status)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&c_full[which], __popc(live) * kDecodeBlock * D);
+        __syncwarp();
+        if (mine)
+          tma_load_3d(stage + lane * kDecodeBlock * D, map, &c_full[which], 0, kvh,
+                      phys * kDecodeBlock);
+        issued = j + 1;
+      }
+      if (lane == 0) {  // no copy outlives the CTA
+        if (k_producer) mbar_drain(q_full, 0, p.status);
+        if (issued > 0) mbar_drain(&c_full[which], (issued - 1) & 1, p.status);
+      }
+    }
   } else if (KV8 && warp >= Sh::kConvWarp) {
     if constexpr (KV8) {
       // ---------------------------------------------------- 8-bit K and V
-      // A warp iteration covers 4 rows of d = 128 (8 of d = 64): lane bits 0-1
-      // are the 16-code unit in a 64-column chunk, bit 2 the row's parity, then
-      // (d = 128) the chunk, then the rows above.  So each quarter of the
-      // warp's 16-byte stores is two adjacent rows of one chunk, whose swizzled
-      // units are 8 different ones: no bank conflicts.
+      // A warp iteration covers 4 rows of d = 128 (8 of d = 64), one 16-code
+      // unit a lane: lane bits 0-1 are the unit in a 64-column chunk, bit 2 the
+      // row's parity, bit 3 (d = 128) the chunk, exchanged on odd rows, then
+      // the rows above.  So a quarter of the warp reads two rows of different
+      // halves, and its stores, units 2c (+ 1) ^ row of those rows, fall on 8
+      // different 16-byte places: no bank conflicts either way.
       constexpr int kRowsWarp = 32 / (D / 16);
       constexpr int kIters = kPrefillBN / (4 * kRowsWarp);
       const int cw = warp - Sh::kConvWarp;
       const int c_unit = lane & 3;
-      const int c_chunk = (D == 128) ? (lane >> 3) & 1 : 0;
       const int c_row = cw * kRowsWarp +
                         ((D == 128) ? ((lane >> 2) & 1) + 2 * (lane >> 4) : (lane >> 2));
-      const int32_t *trow = p.block_table + static_cast<size_t>(unit) * p.max_blocks_per_seq;
-      constexpr int kBlkPerTile = kPrefillBN / kDecodeBlock;
-      constexpr int kWin = 32 / kBlkPerTile;  // key tiles whose block ids a warp holds
-      const int total_blk = (kv_len + kDecodeBlock - 1) / kDecodeBlock;
-      const size_t n_pool = static_cast<size_t>(p.num_blocks) * kDecodeBlock * p.Hkv * D;
-      // the ids and scales of the blocks of key tiles w .. w + 3 (lane = 8 *
-      // tile + block); -1 for a block that no row sees, or a bad one
-      auto fetch = [&](int w, int &phys, float &ks, float &vs) {
-        phys = -1;
-        ks = vs = 0.f;
-        const int blk = key_tile(w + lane / kBlkPerTile) * kBlkPerTile + lane % kBlkPerTile;
-        if (w + lane / kBlkPerTile >= n_kv || blk >= total_blk) return;
-        if ((blk + 1) * kDecodeBlock <= win_lo && blk * kDecodeBlock >= p.sinks) return;
-        if (!in_bounds(static_cast<size_t>(trow - p.block_table) + blk, 1,
-                       static_cast<size_t>(p.B) * p.max_blocks_per_seq, p.status))
-          return;
-        const int id = trow[blk];
-        if (id < 0 || id >= p.num_blocks) {
-          if (cw == 0) raise_status(p.status, FA_DEV_BAD_BLOCK);
-          return;
-        }
-        phys = id;
-        const size_t sidx = static_cast<size_t>(id) * p.Hkv + kvh;
+      const int c_chunk = (D == 128) ? ((lane >> 3) ^ (lane >> 2)) & 1 : 0;
+      // The block scales of four tiles, read four tiles ahead; 0 for a block
+      // that was not copied.
+      auto scales = [&](int w, float &ks, float &vs) {
+        const int id = cache_block(w, false);
+        const size_t at = static_cast<size_t>(max(id, 0)) * p.Hkv + kvh;
         const size_t n = static_cast<size_t>(p.num_blocks) * p.Hkv;
-        ks = checked_load(p.k_scale, sidx, n, p.status);
-        vs = checked_load(p.v_scale, sidx, n, p.status);
+        ks = id < 0 ? -1.f : checked_load(p.k_scale, at, n, p.status);
+        vs = id < 0 ? -1.f : checked_load(p.v_scale, at, n, p.status);
       };
-      int cur, nxt;
       float cur_k, cur_v, nxt_k, nxt_v;
-      int win_base = 0;
-      fetch(0, cur, cur_k, cur_v);
-      fetch(kWin, nxt, nxt_k, nxt_v);
-      // Loads and widens tile j of K or V.  Tiles are visited in the order
-      // K(0), V(0), K(1), V(1), ...; K(j + 1) is the first to need a new window
-      // of ids, while V(j), already loaded, needs only its scales: each load
-      // keeps the window's scales and its tile's place in them.
-      uint4 kx[kIters], vx[kIters];
-      float k_sc = 0.f, v_sc = 0.f;
-      int k_at = 0, v_at = 0;
-      auto load = [&](int j, bool is_v, uint4(&x)[kIters], float &scl, int &at) {
-        if (j >= win_base + kWin) {
-          win_base += kWin;
-          cur = nxt, cur_k = nxt_k, cur_v = nxt_v;
-          fetch(win_base + kWin, nxt, nxt_k, nxt_v);
+      scales(0, cur_k, cur_v);
+      scales(kIdTiles, nxt_k, nxt_v);
+      // Turn t is tile t / 2 of K (t even) or V (odd): wait for its codes and a
+      // free stage, write the tile's bf16 rows, handing the buffer back to the
+      // copies once the last codes are read, and hand the rows on.  Rows past
+      // the context (stale slots) and of blocks that were not copied become 0.
+      // One copy of this code serves K and V, four units at a time: unrolled
+      // for both whole tiles it took 472 us instead of 315 (the instruction
+      // streams of these warps and of the softmax warps beside them outgrow
+      // the instruction cache).
+      for (int t = 0; t < 2 * n_kv; ++t) {
+        const int j = t >> 1, i = t & 1;
+        if (i == 0 && j > 0 && j % kIdTiles == 0) {
+          cur_k = nxt_k, cur_v = nxt_v;
+          scales(j + kIdTiles, nxt_k, nxt_v);
         }
-        const uint8_t *codes = is_v ? p.v_codes : p.k_codes;
-        scl = is_v ? cur_v : cur_k;
-        at = (j - win_base) * kBlkPerTile;
+        const int stages = i ? SV : SK, st = j % stages;
+        uint64_t *full = (i ? v_full : k_full) + st, *empty = (i ? v_empty : k_empty) + st;
+        if (j >= stages && !mbar_wait_warp(empty, ((j / stages) - 1) & 1, abort_flag, p.status))
+          break;
+        if (!mbar_wait_warp(&c_full[i], j & 1, abort_flag, p.status)) break;
+        const uint8_t *codes = smem + L::kCodes + i * L::kCodeBytes + c_row * D + c_chunk * 64 +
+                               c_unit * 16;
+        const float sc = i ? cur_v : cur_k;
+        const int rows = kv_len - key_tile(j) * kPrefillBN;
+        uint8_t *tile = (i ? sV : sK) + st * L::kTileBytes + c_chunk * L::kChunkBytes;
+        constexpr int kUnits = 4;
+#pragma unroll 1
+        for (int u0 = 0; u0 < kIters; u0 += kUnits) {
+          uint4 x[kUnits];
 #pragma unroll
-        for (int it = 0; it < kIters; ++it) {
-          const int r = it * 4 * kRowsWarp + c_row;  // row of the tile
-          const int phys = __shfl_sync(0xffffffffu, cur, at + r / kDecodeBlock);
-          const size_t off =
-              ((static_cast<size_t>(phys) * kDecodeBlock + r % kDecodeBlock) * p.Hkv + kvh) * D +
-              c_chunk * 64 + c_unit * 16;
-          // rows past the context (stale slots) and of skipped blocks are 0
-          const bool live = phys >= 0 && key_tile(j) * kPrefillBN + r < kv_len &&
-                            in_bounds(off, 16, n_pool, p.status);
-          x[it] = make_uint4(0u, 0u, 0u, 0u);
-          if (live) x[it] = __ldg(reinterpret_cast<const uint4 *>(codes + off));
-        }
-      };
-      auto widen = [&](uint8_t *tile, const uint4(&x)[kIters], float scl, int at) {
-#pragma unroll
-        for (int it = 0; it < kIters; ++it) {
-          const int r = it * 4 * kRowsWarp + c_row;
-          const uint32_t w[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
-          uint32_t o[8];
-          const float sr = __shfl_sync(0xffffffffu, scl, at + r / kDecodeBlock);
-          const float2 s2 = make_float2(sr, sr);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = fmul2(e4m3x2_to_float2(w[e]), s2);
-            const float2 b2 = fmul2(e4m3x2_to_float2(w[e] >> 16), s2);
-            o[2 * e] = pack_bf16x2(a.x, a.y);
-            o[2 * e + 1] = pack_bf16x2(b2.x, b2.y);
+          for (int it = 0; it < kUnits; ++it)
+            x[it] = *reinterpret_cast<const uint4 *>(codes + (u0 + it) * 4 * kRowsWarp * D);
+          if (u0 + kUnits == kIters) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_empty[i]);
           }
-          uint8_t *row = tile + c_chunk * L::kChunkBytes + r * 128;
-          *reinterpret_cast<uint4 *>(row + (((2 * c_unit) ^ (r & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4 *>(row + (((2 * c_unit + 1) ^ (r & 7)) << 4)) =
-              make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+          for (int it = 0; it < kUnits; ++it) {
+            const int r = (u0 + it) * 4 * kRowsWarp + c_row;
+            float s = __shfl_sync(0xffffffffu, sc, (j % kIdTiles) * kTileBlocks + r / kDecodeBlock);
+            const uint32_t keep = (s >= 0.f && r < rows) ? 0xFFFFFFFFu : 0u;
+            const uint32_t w[4] = {x[it].x & keep, x[it].y & keep, x[it].z & keep, x[it].w & keep};
+            const float2 s2 = make_float2(s, s);
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 a = fmul2(e4m3x2_to_float2(w[e]), s2);
+              const float2 b2 = fmul2(e4m3x2_to_float2(w[e] >> 16), s2);
+              o[2 * e] = pack_bf16x2(a.x, a.y);
+              o[2 * e + 1] = pack_bf16x2(b2.x, b2.y);
+            }
+            uint8_t *row = tile + r * 128;
+            *reinterpret_cast<uint4 *>(row + (((2 * c_unit) ^ (r & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(row + (((2 * c_unit + 1) ^ (r & 7)) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
+          }
         }
         fence_proxy_async_smem();
-      };
-      load(0, false, kx, k_sc, k_at);
-      load(0, true, vx, v_sc, v_at);
-      for (int j = 0; j < n_kv; ++j) {
-        const int sk = j % SK, sv = j % SV;
-        if (j >= SK && !mbar_wait_warp(&k_empty[sk], ((j / SK) - 1) & 1, abort_flag, p.status))
-          break;
-        widen(sK + sk * L::kTileBytes, kx, k_sc, k_at);
-        mbar_arrive(&k_full[sk]);
-        if (j + 1 < n_kv) load(j + 1, false, kx, k_sc, k_at);
-        if (j >= SV && !mbar_wait_warp(&v_empty[sv], ((j / SV) - 1) & 1, abort_flag, p.status))
-          break;
-        widen(sV + sv * L::kTileBytes, vx, v_sc, v_at);
-        mbar_arrive(&v_full[sv]);
-        if (j + 1 < n_kv) load(j + 1, true, vx, v_sc, v_at);
+        mbar_arrive(full);
       }
     }
   } else if (!KV8 && (warp == Sh::kTmaWarp || warp == Sh::kTmaVWarp) && PAGED) {
@@ -1238,7 +1274,7 @@ static cudaError_t launch_prefill_t(const CUtensorMap &tq, const CUtensorMap &tk
                                     const CUtensorMap &tv, const CUtensorMap &tv1,
                                     const CUtensorMap &to, const PrefillParams &p, int grid,
                                     cudaStream_t stream) {
-  using L = PrefillLayout<D, FP8, QT>;
+  using L = PrefillLayout<D, FP8, QT, KV8>;
   using Sh = PrefillShape<QT, KV8>;
   auto kern = prefill_kernel<D, CAUSAL, KIND, FP8, QT, WIN, KV8>;
   if constexpr (Sh::kSplitRegs) {
