@@ -8,21 +8,29 @@
 // of token j's block and c = scale log2(e):
 //   x_j = (q . code_j) ks c,  p_j = 2^(x_j - m),  l = sum p_j,
 //   o = sum p_j vs code'_j,   out = o / l.
-// The codes become fp16 exactly (one conversion for two codes), so both
-// products run on m16n8k16 fp16 MMAs with fp32 sums:
-//   S^T [16 tokens x 8 heads] += K [16 x 16 of d] Q^T.  Which of d's values
-//     stand in which k-slots is free as long as K and Q agree, so a thread
-//     takes 32 (d = 64: 16) consecutive codes of a row and feeds them to the
-//     MMAs four at a time: whole 16-byte reads, no shuffles.  Q is scaled per
-//     head by a power of two that puts its largest value at 2^10..2^11, so
-//     fp16 keeps bf16's bits down to 2^-25 of it; ks and c are applied to S.
-//   O^T [16 of d x 8 heads] += V^T P^T.  V's rows come through a transposing
-//     16-bit ldmatrix, whose elements are pairs of codes: the two halves of a
-//     pair are the accumulator rows g and g + 8, so row g of tile u is
-//     d = 16 u + 2 g, and row g + 8 the next one.
-// vs goes into the weights: o is kept relative to mo, the running maximum of
-// x_j + log2 vs, so the fp16 weights 2^(x_j + log2 vs - mo) are at most 1
-// whatever the scales, and each is rounded to 11 bits (2^-12 of itself).
+//   S^T [16 tokens x 4 heads x 2] += K [16 x 32 of d] [Qh | Ql]^T on e4m3
+//     MMAs (fp32 sums), on the codes as they are; Q goes in as two e4m3 terms.
+//     It is scaled per head by a power of two that puts its largest value at
+//     2^7..2^8; Qh = e4m3(Q) takes its upper four significand bits and Ql =
+//     e4m3(16 (Q - Qh)) the other four, exactly down to 2^-14 of the largest
+//     value and to within 2^-21 of it below.  A head's terms are neighbouring
+//     columns, so a thread holds both sums and adds them: s = S_h + S_l / 16.
+//     Which of d's values stand in which k-slots is free as long as K and Q
+//     agree, so a thread takes 32 (d = 64: 16) consecutive codes of a row:
+//     whole 16-byte reads.  (With K's codes widened for fp16 MMAs instead,
+//     twice as many at half the rate, the benchmark's batch took 544 us where
+//     this takes 383.)
+//   O^T [16 of d x 8 heads] += V^T P^T on fp16 MMAs: weights are rounded to 11
+//     bits and V's codes widened exactly.  V's rows come through a transposing
+//     16-bit ldmatrix, whose elements are pairs of codes: the two values of a
+//     pair are accumulator rows g and g + 8, so row g of tile u is d = 16 u +
+//     2 g, and row g + 8 the next one.  Two e4m3 terms of P would save the
+//     widening, but lose weights below 2^-19 of the largest, which a long
+//     context has enough of to matter.
+// vs goes into the weights: o is kept relative to mo, a running reference of
+// x_j + log2 vs, so the weights 2^(x_j + log2 vs - mo) stay in fp16's range
+// whatever the scales; the references move only when a maximum grows by more
+// than kSlackLog2, which leaves the accumulators alone in most steps.
 // Bound by HBM: half of decode.cu's bytes for the same products.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -42,7 +50,11 @@ namespace fa {
 namespace {
 
 constexpr int kStepBlocks = 2;   // blocks of a step
-constexpr int kF8Stages = 4;     // steps in flight per warp
+constexpr int kF8Stages = 3;     // steps in flight per warp
+// A weight is 2^kTopLog2 when its reference is fresh and at most 2^(kTopLog2 +
+// kSlackLog2) = 2^14 before the reference moves (fp16 ends at 65504, and at
+// 2^-24 below).
+constexpr float kTopLog2 = 12.f, kSlackLog2 = 2.f;
 
 template <int D>
 struct DecodeF8Layout {
@@ -85,7 +97,7 @@ __global__ void __launch_bounds__(32)
                             const CacheScales sc) {
   using L = DecodeF8Layout<D>;
   constexpr int S = kF8Stages;
-  constexpr int W = D / 16;       // words of a K row per thread, MMAs over d
+  constexpr int W = D / 16;       // words of a K row per thread (two to an MMA)
   constexpr int U = D / 16;       // 16-byte units of a V row, accumulator tiles
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x;
@@ -176,13 +188,14 @@ __global__ void __launch_bounds__(32)
     my_lv = __log2f(checked_load(sc.v, sidx, n, p.status));
   }
 
-  // Q^T fragments: column n is query head kvh * G + n; word w of a thread
-  // holds d = 4 W quad + 4 w .. + 3 of its row, as K's words do.
-  uint32_t qf[NT][W][2];
-  float cq[NT][2];  // 2^-e of the heads of this thread's accumulator columns
+  // Q^T fragments: columns 2 h and 2 h + 1 of N tile nt are the two terms of
+  // query head kvh * G + 4 nt + h; word w of a thread holds d = 4 W quad + 4 w
+  // .. + 3 of its column, as K's words do.
+  uint32_t qf[NT][W];
+  float cq[NT];  // 2^-e of the head of this thread's accumulator columns (head quad)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int n = nt * 8 + grp;
+    const int n = nt * 4 + (grp >> 1);
     const bool valid =
         n < G && in_bounds((part_row + n) * D, D, static_cast<size_t>(p.batch) * p.H * D, p.status);
     const uint4 *qrow = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
@@ -202,35 +215,43 @@ __global__ void __launch_bounds__(32)
       top = max(top, max(raw[c] & 0x7FFFu, (raw[c] >> 16) & 0x7FFFu));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // exponent that takes the row to [2^10, 2^11); rows with an infinity or
-    // NaN (or all zero) stay as they are
+    // exponent that takes the row to [2^7, 2^8) (a row of zeros, or with an
+    // infinity or NaN, stays as it is: e4m3 keeps NaN, and an infinite score
+    // has no softmax, so infinities become NaN below)
     const int ex = static_cast<int>(top >> 7);
-    const int e = (ex == 0 || ex == 255) ? 0 : 10 - (ex - 127);
+    const int e = (ex == 0 || ex == 255) ? 0 : 7 - (ex - 127);
     // (two factors: the power itself may exceed fp32's)
     const float f0 = pow2_clamped(e / 2), f1 = pow2_clamped(e - e / 2);
 #pragma unroll
-    for (int w = 0; w < W; ++w)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float2 x = bf16x2_to_float2(raw[2 * w + t]);
-        qf[nt][w][t] = pack_f16x2(x.x * f0 * f1, x.y * f0 * f1);
+    for (int w = 0; w < W; ++w) {
+      const float2 x0 = bf16x2_to_float2(raw[2 * w]), x1 = bf16x2_to_float2(raw[2 * w + 1]);
+      const float a = x0.x * f0 * f1, b2 = x0.y * f0 * f1, c = x1.x * f0 * f1, d = x1.y * f0 * f1;
+      uint32_t h = pack_e4m3x4(a, b2, c, d);
+      if (grp & 1) {  // the second term
+        const float2 h0 = e4m3x2_to_float2(h), h1 = e4m3x2_to_float2(h >> 16);
+        h = pack_e4m3x4((a - h0.x) * 16.f, (b2 - h0.y) * 16.f, (c - h1.x) * 16.f,
+                        (d - h1.y) * 16.f);
       }
-    // column n of this thread's accumulators is head 8 nt + 2 quad + cc
-#pragma unroll
-    for (int cc = 0; cc < 2; ++cc)
-      cq[nt][cc] = pow2_clamped(-__shfl_sync(0xffffffffu, e, (2 * quad + cc) * 4));
+      qf[nt][w] = (ex == 255) ? 0x7F7F7F7Fu : h;
+    }
+    cq[nt] = pow2_clamped(-__shfl_sync(0xffffffffu, e, quad * 8));
   }
 
-  float acc[NT][U][4];
-  float m[NT][2], mo[NT][2], l[NT][2];
+  // O^T: columns 2 h and 2 h + 1 of tile np are heads h of S tiles 2 np and
+  // 2 np + 1, so that the thread with a head's scores has its outputs too.
+  constexpr int NP = (NT + 1) / 2;
+  float acc[NP][U][4];
+  float m[NT], mo[NT], l[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int np = 0; np < NP; ++np)
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) acc[nt][u][x] = 0.f;
-    m[nt][0] = m[nt][1] = mo[nt][0] = mo[nt][1] = -CUDART_INF_F;
-    l[nt][0] = l[nt][1] = 0.f;
+      for (int x = 0; x < 4; ++x) acc[np][u][x] = 0.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = mo[nt] = -CUDART_INF_F;
+    l[nt] = 0.f;
   }
 
   bool ok = true;
@@ -260,13 +281,11 @@ __global__ void __launch_bounds__(32)
         hi[4 * c] = d.x, hi[4 * c + 1] = d.y, hi[4 * c + 2] = d.z, hi[4 * c + 3] = d.w;
       }
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const uint32_t a0 = e4m3x2_to_f16x2(lo[w]), a1 = e4m3x2_to_f16x2(hi[w]);
-        const uint32_t a2 = e4m3x2_hi_to_f16x2(lo[w]), a3 = e4m3x2_hi_to_f16x2(hi[w]);
+      for (int w = 0; w < W; w += 2)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          mma_m16n8k16_f16(s[nt][t], a0, a1, a2, a3, qf[nt][w][0], qf[nt][w][1]);
-      }
+          mma_m16n8k32_e4m3(s[nt][t], lo[w], hi[w], lo[w + 1], hi[w + 1], qf[nt][w],
+                            qf[nt][w + 1]);
     }
 
     // Token masks of the step's blocks: slots past the context (all of them
@@ -288,67 +307,67 @@ __global__ void __launch_bounds__(32)
     auto hidden = [&](int t, int tok) {
       return tok >= n_valid[t] || (tok >= hid0[t] && tok < hid1[t]);
     };
-    // scores in log2 units; rows of the accumulator are tokens grp and grp + 8
+    // Softmax of head quad of each N tile over its tokens grp and grp + 8 of
+    // each block (log2 units).
+    float w[NT][kStepBlocks][2];  // weights times their block's scale
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[kStepBlocks][2];
+      float top = -CUDART_INF_F, top_o = -CUDART_INF_F;
+#pragma unroll
+      for (int t = 0; t < kStepBlocks; ++t) {
+        const float c = ks[t] * cq[nt];
+        x[t][0] = fmaf(s[nt][t][1], 0.0625f, s[nt][t][0]) * c;
+        x[t][1] = fmaf(s[nt][t][3], 0.0625f, s[nt][t][2]) * c;
+        if (masked) {
+          if (hidden(t, grp)) x[t][0] = -CUDART_INF_F;
+          if (hidden(t, grp + 8)) x[t][1] = -CUDART_INF_F;
+        }
+        float mx = fmaxf(x[t][0], x[t][1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        top = fmaxf(top, mx);
+        top_o = fmaxf(top_o, mx + lv[t]);
+      }
+      // references that a maximum has outgrown move to it (from -inf, where
+      // nothing was seen, to the first one)
+      const bool grow = top > m[nt] + kSlackLog2 || top_o > mo[nt] + kSlackLog2;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float m_new = grow ? fmaxf(m[nt], top) : m[nt];
+        const float mo_new = grow ? fmaxf(mo[nt], top_o) : mo[nt];
+        l[nt] *= (m[nt] == m_new) ? 1.f : ex2(m[nt] - m_new);
+        const float alpha = (mo[nt] == mo_new) ? 1.f : ex2(mo[nt] - mo_new);
+        m[nt] = m_new;
+        mo[nt] = mo_new;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          acc[nt / 2][u][nt % 2] *= alpha;
+          acc[nt / 2][u][2 + nt % 2] *= alpha;
+        }
+      }
+      // (nothing seen yet: finite references, every weight is 0)
+      const float m_use = (m[nt] == -CUDART_INF_F) ? 0.f : m[nt];
+      const float mo_use = ((mo[nt] == -CUDART_INF_F) ? 0.f : mo[nt]) - kTopLog2;
+#pragma unroll
+      for (int t = 0; t < kStepBlocks; ++t) {
+        l[nt] += ex2(x[t][0] - m_use) + ex2(x[t][1] - m_use);
+        const float off = lv[t] - mo_use;
+        w[nt][t][0] = ex2(x[t][0] + off);
+        w[nt][t][1] = ex2(x[t][1] + off);
+      }
+    }
+    // rows grp: tokens grp (grp + 8), columns the heads of two S tiles;
+    // transposed: tokens 2 q and 2 q + 1 (+ 8) of column grp
+    uint32_t pb[NP][kStepBlocks][2];
+#pragma unroll
+    for (int np = 0; np < NP; ++np)
 #pragma unroll
       for (int t = 0; t < kStepBlocks; ++t)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[nt][t][x] *= ks[t] * cq[nt][x & 1];
-    if (masked) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int t = 0; t < kStepBlocks; ++t) {
-          if (hidden(t, grp)) s[nt][t][0] = s[nt][t][1] = -CUDART_INF_F;
-          if (hidden(t, grp + 8)) s[nt][t][2] = s[nt][t][3] = -CUDART_INF_F;
-        }
-    }
-    // column-wise (per query head) online softmax
-    uint32_t pb[NT][kStepBlocks][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float w[kStepBlocks][4];
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        float m_new = m[nt][cc], mo_new = mo[nt][cc];
-#pragma unroll
-        for (int t = 0; t < kStepBlocks; ++t) {
-          float mx = fmaxf(s[nt][t][cc], s[nt][t][2 + cc]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          m_new = fmaxf(m_new, mx);
-          mo_new = fmaxf(mo_new, mx + lv[t]);
-        }
-        // (nothing seen yet: both references stay finite, every weight is 0)
-        const float m_use = (m_new == -CUDART_INF_F) ? 0.f : m_new;
-        const float mo_use = (mo_new == -CUDART_INF_F) ? 0.f : mo_new;
-        const float alpha = ex2(mo[nt][cc] - mo_use);
-        float sum = 0.f;
-#pragma unroll
-        for (int t = 0; t < kStepBlocks; ++t) {
-          const float p0 = ex2(s[nt][t][cc] - m_use), p1 = ex2(s[nt][t][2 + cc] - m_use);
-          sum += p0 + p1;
-          // a weight and its block's scale, relative to mo
-          w[t][cc] = ex2(s[nt][t][cc] + (lv[t] - mo_use));
-          w[t][2 + cc] = ex2(s[nt][t][2 + cc] + (lv[t] - mo_use));
-        }
-        l[nt][cc] = fmaf(l[nt][cc], ex2(m[nt][cc] - m_use), sum);
-        m[nt][cc] = m_new;
-        mo[nt][cc] = mo_new;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          acc[nt][u][cc] *= alpha;
-          acc[nt][u][2 + cc] *= alpha;
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < kStepBlocks; ++t) {
-        pb[nt][t][0] = movmatrix_trans(pack_f16x2(w[t][0], w[t][1]));
-        pb[nt][t][1] = movmatrix_trans(pack_f16x2(w[t][2], w[t][3]));
-      }
-    }
+        for (int x = 0; x < 2; ++x)
+          pb[np][t][x] = movmatrix_trans(
+              pack_f16x2(w[2 * np][t][x], 2 * np + 1 < NT ? w[(2 * np + 1) % NT][t][x] : 0.f));
     // O^T += V^T P^T: matrix mi of the transposing load holds tokens
     // 8 mi .. + 7 of the step's 32, 16 values of d as pairs
     const int mi = lane >> 3, mr = lane & 7;
@@ -356,27 +375,28 @@ __global__ void __launch_bounds__(32)
     const int vtok = mr + 8 * (mi & 1);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      // r[mi]: codes (tok, d), (tok, d + 1), (tok + 1, d), (tok + 1, d + 1)
       uint32_t r[4];
       ldmatrix_x4_trans(vrow + f8_off<D>(vtok, u), r[0], r[1], r[2], r[3]);
+      if (masked) {
+        // never let a stale or hidden slot reach the accumulator
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int tok = 8 * (x & 1) + 2 * quad;
+          r[x] &= (hidden(x >> 1, tok) ? 0u : 0x0000FFFFu) |
+                  (hidden(x >> 1, tok + 1) ? 0u : 0xFFFF0000u);
+        }
+      }
 #pragma unroll
       for (int t = 0; t < kStepBlocks; ++t) {
-        uint32_t a[2][2];  // [token half][even or odd value of the pair]
+        // (tok, d), (tok + 1, d), then the same of d + 1
+        const uint32_t y0 = __byte_perm(r[2 * t], 0, 0x3120);
+        const uint32_t y1 = __byte_perm(r[2 * t + 1], 0, 0x3120);
+        const uint32_t a0 = e4m3x2_to_f16x2(y0), a1 = e4m3x2_hi_to_f16x2(y0);
+        const uint32_t a2 = e4m3x2_to_f16x2(y1), a3 = e4m3x2_hi_to_f16x2(y1);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t x = r[2 * t + hf];  // codes (tok, d), (tok, d + 1), (tok + 1, d), (tok + 1, d + 1)
-          if (masked) {
-            // never let a stale or hidden slot reach the accumulator
-            const int tok = 8 * hf + 2 * quad;
-            x &= (hidden(t, tok) ? 0u : 0x0000FFFFu) | (hidden(t, tok + 1) ? 0u : 0xFFFF0000u);
-          }
-          const uint32_t y = __byte_perm(x, 0, 0x3120);  // (tok, d), (tok + 1, d), then d + 1
-          a[hf][0] = e4m3x2_to_f16x2(y);
-          a[hf][1] = e4m3x2_hi_to_f16x2(y);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_m16n8k16_f16(acc[nt][u], a[0][0], a[0][1], a[1][0], a[1][1], pb[nt][t][0],
-                           pb[nt][t][1]);
+        for (int np = 0; np < NP; ++np)
+          mma_m16n8k16_f16(acc[np][u], a0, a1, a2, a3, pb[np][t][0], pb[np][t][1]);
       }
     }
     __syncwarp();
@@ -396,28 +416,26 @@ __global__ void __launch_bounds__(32)
   }
   // write the partial state of every query head of the group
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-      float lt = l[nt][cc];
-      lt += __shfl_xor_sync(0xffffffffu, lt, 4);
-      lt += __shfl_xor_sync(0xffffffffu, lt, 8);
-      lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-      const int g = nt * 8 + 2 * quad + cc;
-      if (g >= G) continue;
-      const size_t row = (part_row + g) * p.max_splits + split;
-      if (!in_bounds(row, 1, part_rows, p.status)) continue;
-      if (grp == 0) {
-        p.ml_part[row * 2 + 0] = m[nt][cc];
-        p.ml_part[row * 2 + 1] = lt;
-      }
-      // o back from its own reference to m's
-      const float f = (mo[nt][cc] == -CUDART_INF_F) ? 0.f : exp2f(mo[nt][cc] - m[nt][cc]);
-      float2 *orow = reinterpret_cast<float2 *>(p.o_part + row * D);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        orow[u * 8 + grp] = make_float2(acc[nt][u][cc] * f, acc[nt][u][2 + cc] * f);
+  for (int nt = 0; nt < NT; ++nt) {
+    float lt = l[nt];
+    lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+    lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+    lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+    const int g = nt * 4 + quad;
+    if (g >= G) continue;
+    const size_t row = (part_row + g) * p.max_splits + split;
+    if (!in_bounds(row, 1, part_rows, p.status)) continue;
+    if (grp == 0) {
+      p.ml_part[row * 2 + 0] = m[nt];
+      p.ml_part[row * 2 + 1] = lt;
     }
+    // o back from its own reference to m's
+    const float f = (mo[nt] == -CUDART_INF_F) ? 0.f : exp2f(mo[nt] - m[nt] - kTopLog2);
+    float2 *orow = reinterpret_cast<float2 *>(p.o_part + row * D);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      orow[u * 8 + grp] = make_float2(acc[nt / 2][u][nt % 2] * f, acc[nt / 2][u][2 + nt % 2] * f);
+  }
 }
 
 template <int D, int NT>
@@ -445,11 +463,13 @@ static cudaError_t launch_decode_fp8_t(const CUtensorMap &tk, const CUtensorMap 
 
 cudaError_t launch_decode_fp8(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeParams &p,
                               const CacheScales &sc, int d, cudaStream_t stream) {
-  const bool two = p.group > 8;
-  if (d == 64) return two ? launch_decode_fp8_t<64, 2>(tk, tv, p, sc, stream)
-                          : launch_decode_fp8_t<64, 1>(tk, tv, p, sc, stream);
-  return two ? launch_decode_fp8_t<128, 2>(tk, tv, p, sc, stream)
-             : launch_decode_fp8_t<128, 1>(tk, tv, p, sc, stream);
+  const int nt = p.group <= 4 ? 1 : p.group <= 8 ? 2 : 4;  // N tiles of four heads
+  if (d == 64) return nt == 1   ? launch_decode_fp8_t<64, 1>(tk, tv, p, sc, stream)
+                      : nt == 2 ? launch_decode_fp8_t<64, 2>(tk, tv, p, sc, stream)
+                                : launch_decode_fp8_t<64, 4>(tk, tv, p, sc, stream);
+  return nt == 1   ? launch_decode_fp8_t<128, 1>(tk, tv, p, sc, stream)
+         : nt == 2 ? launch_decode_fp8_t<128, 2>(tk, tv, p, sc, stream)
+                   : launch_decode_fp8_t<128, 4>(tk, tv, p, sc, stream);
 }
 
 }  // namespace fa

@@ -57,9 +57,9 @@ int fa_cache_append_fp8(const void *k, const void *v, int64_t k_stride, int64_t 
 
 /*
  * fa_decode_paged over the 8-bit cache: one query token per sequence.  The
- * codes are widened to fp16 exactly, Q is scaled per head to fp16's range by
- * a power of two, P V is formed with fp16 weights relative to the largest
- * p * scale so far; sums are fp32.
+ * scores are formed from the codes and from Q in two 8-bit terms, exact to
+ * 2^-21 of a query row's largest value; weights are rounded to 11 bits; sums
+ * are fp32.
  *   q, out    : [batch, H, d] bf16;  lse : [batch, H] fp32, may be NULL
  *   workspace : fa_decode_workspace_size(), or with a window
  *               fa_decode_window_workspace_size() bytes (fa_window.h);
