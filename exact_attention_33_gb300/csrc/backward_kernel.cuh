@@ -79,7 +79,7 @@ struct BwdLayout {
   static constexpr int kNumBars = 1 + 2 * kStagesQ + 2 * kStagesO + 9;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kItem = kMisc + 16;  // the work item slot
-  static constexpr int kBytes = kItem + 32;
+  static constexpr int kBytes = kItem + 48;
   // Room to align the base up to 1 KiB, as much as the 227 KiB limit leaves
   // at d = 128 (the dynamic shared memory of a kernel without static
   // shared memory starts 1 KiB aligned; the kernel checks).
@@ -106,7 +106,7 @@ struct BwdDqLayout {
   static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 9;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kItem = kMisc + 16;  // the work item slot
-  static constexpr int kVec = kItem + 32;   // the item's -lse2 and -D vectors (128 floats each)
+  static constexpr int kVec = kItem + 48;   // the item's -lse2 and -D vectors (128 floats each)
   static constexpr int kBytes = kVec + 1024;
   static constexpr int kSmemAlloc = kBytes + 1024;
   static_assert(kSmemAlloc <= 232448, "dQ shared memory exceeds 227 KiB");
@@ -336,8 +336,20 @@ struct BwdItem {
   int start;  // the sequence's first row in a packed batch (0 when dense)
   int len;    // its rows
   int valid;  // 0: no work left
+  // dK / dV of a windowed call: the item's query tiles [i0, i1), and its slot
+  // of partial sums (see BwdParams) or -1
+  int i0, i1;
+  int part;
 };
-static_assert(sizeof(BwdItem) <= 32, "work item slot");
+static_assert(sizeof(BwdItem) <= 48, "work item slot");
+
+// One past the last query tile whose window holds a key of tile t, of n_q.
+__device__ __forceinline__ int window_queries(const BwdParams &p, int t, int n_q) {
+  return min(n_q, (t * 128 + 127 + p.window - 1) / 128 + 1);
+}
+
+template <bool CAUSAL, bool VARLEN, bool KEY_TILES, bool WIN, typename Next>
+__device__ BwdItem next_item(const BwdParams &p, int heads, Next next);
 
 // Claims the next work item from the call's counter (lane 0 takes an index,
 // the whole warp decodes it) and returns it, or an item with valid = 0 once
@@ -347,18 +359,46 @@ static_assert(sizeof(BwdItem) <= 32, "work item slot");
 // longest-first; a packed batch of more sequences than that order covers
 // takes sequence by sequence and claims again past a sequence's last tile.
 // Run by whole warps.
-template <bool CAUSAL, bool VARLEN, bool KEY_TILES>
+// WIN: the query tiles of a dK / dV item (window_queries), and before the tiles
+// the slices of the sinks' other queries (p.sink_slices of each of the first
+// p.sink_tiles tiles of each sequence).
+template <bool CAUSAL, bool VARLEN, bool KEY_TILES, bool WIN = false>
 __device__ BwdItem claim_item(const BwdParams &p, unsigned int *counter, int heads) {
-  BwdItem it{};
-  const long long total = static_cast<long long>(p.B) * p.n_tiles * heads;
-  for (;;) {
+  return next_item<CAUSAL, VARLEN, KEY_TILES, WIN>(p, heads, [&]() -> long long {
     unsigned int w = 0;
     if ((threadIdx.x & 31) == 0) w = atomicAdd(counter, 1u);
-    w = __shfl_sync(0xffffffffu, w, 0);
+    return __shfl_sync(0xffffffffu, w, 0);
+  });
+}
+
+// The same with the indexes that `next` returns.
+template <bool CAUSAL, bool VARLEN, bool KEY_TILES, bool WIN, typename Next>
+__device__ BwdItem next_item(const BwdParams &p, int heads, Next next) {
+  BwdItem it{};
+  it.part = -1;
+  const int slices = (WIN && KEY_TILES) ? p.B * p.sink_tiles * p.sink_slices : 0;
+  const long long total = (static_cast<long long>(p.B) * p.n_tiles + slices) * heads;
+  for (;;) {
+    const long long w = next();
     if (w >= total) return it;
     const int h = static_cast<int>(w % heads);
-    const int r = static_cast<int>(w / heads);
+    int r = static_cast<int>(w / heads);
     int b, rank, t;
+    if constexpr (WIN && KEY_TILES) {
+      if (r < slices) {
+        const int slice = r % p.sink_slices;
+        t = r / p.sink_slices % p.sink_tiles;
+        b = r / p.sink_slices / p.sink_tiles;
+        int start, len;
+        bwd_seq<VARLEN>(p, b, start, len, false);
+        const int n_q = (len + 127) / 128;
+        const int i0 = window_queries(p, t, n_q) + slice * p.sink_slice;
+        if (t >= n_q || i0 >= n_q) continue;  // the sequence ends before
+        it = {b, t, h, start, len, 1, i0, min(n_q, i0 + p.sink_slice), 1 + slice};
+        return it;
+      }
+      r -= slices;
+    }
     if (VARLEN && p.longest_first) {
       b = longest_first_item<CAUSAL, KEY_TILES>(p, r, t);
       if (b < 0) return it;
@@ -378,6 +418,13 @@ __device__ BwdItem claim_item(const BwdParams &p, unsigned int *counter, int hea
       it.start = start;
       it.len = len;
       it.valid = 1;
+      if constexpr (WIN && KEY_TILES) {
+        // a tile with sinks that is not sliced is seen by every later query
+        const int n_q = (len + 127) / 128;
+        it.i0 = t;
+        it.i1 = (t * 128 < p.sinks && t >= p.sink_tiles) ? n_q : window_queries(p, t, n_q);
+        it.part = t < p.sink_tiles ? 0 : -1;
+      }
       return it;
     }
   }
@@ -442,6 +489,366 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const BwdParams p) 
       p.nlse2[vec] = -CUDART_INF_F;
       p.ndsum[vec] = 0.f;
     }
+  }
+}
+
+// ----------------------------------------------------------------- row sums
+// The row vectors of a windowed call: -log-sum-exp in log2 units and -D, with
+// D = sum_j P_ij dP_ij from the same S and dP products that the gradients use.
+// D = rowsum(dO * O) of the forward's output, which the calls without a window
+// take, carries O's rounding to bf16 into every dS of the row; where a row has
+// few keys that matter, P (dP - D) is a small difference and that error is the
+// largest of all (relative RMS of dQ 4.6e-3 that way against 2.4e-3 this way, of
+// which 2.3e-3 are dS's and dQ's own roundings).  The two products of a tile are
+// 2 / 7 of the backward pass's, and neither O nor a second read of dO is needed.
+// One CTA per SM; query tile and head items in a fixed order (the CTA's index,
+// then every grid-th).  S and dP of a key tile go to one of two TMEM buffers,
+// [0, 256) or [256, 512), so the products of the next tile run while the
+// elementwise warps (roles as in the dQ kernel) work on this one.
+template <int D>
+struct BwdSumsLayout {
+  static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int kChunks = D / 64;
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  static constexpr int kStages = 2;  // of K and of V
+  static constexpr int kQ = 0;
+  static constexpr int kDO = kQ + kTileBytes;
+  static constexpr int kK = kDO + kTileBytes;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kBar = kV + kStages * kTileBytes;
+  // in_full, taken, in_empty, drain, kv_full[2], kv_empty[2], sd_full[2],
+  // sd_free[2], sum_full[2], sum_free[2]
+  static constexpr int kNumBars = 12 + 2 * kStages;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kItem = kMisc + 16;
+  static constexpr int kSum = kItem + 48;            // two items' sums of the upper columns
+  static constexpr int kBytes = kSum + 2 * 128 * 4;
+  static constexpr int kSmemAlloc = kBytes + 1024;
+  static_assert(kSmemAlloc <= 232448, "row sum shared memory exceeds 227 KiB");
+};
+
+template <int D, bool VARLEN>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    bwd_sums_kernel(const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const BwdParams p) {
+  using L = BwdSumsLayout<D>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBar);
+  uint64_t *in_full = bars;         // Q and dO of the item (and its slot)
+  uint64_t *taken = bars + 1;       // the MMA and elementwise warps have read the slot
+  uint64_t *in_empty = bars + 2;    // the item's last products have read Q and dO
+  uint64_t *drain = bars + 3;
+  uint64_t *kv_full = bars + 4;     // K and V of a key tile
+  uint64_t *kv_empty = kv_full + S;
+  uint64_t *sd_full = kv_empty + S;  // S and dP of a key tile are in TMEM
+  uint64_t *sd_free = sd_full + 2;   // and read
+  uint64_t *sum_full = sd_free + 2;  // an item's sums of the upper columns are in shared memory
+  uint64_t *sum_free = sum_full + 2;  // and read
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
+  volatile BwdItem *slot = reinterpret_cast<volatile BwdItem *>(smem + L::kItem);
+  float *sums = reinterpret_cast<float *>(smem + L::kSum);
+  uint8_t *sQ = smem + L::kQ, *sDO = smem + L::kDO, *sK = smem + L::kK, *sV = smem + L::kV;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) {
+    // the counters of the gradient kernels, and the sequences with bad bounds
+    if (threadIdx.x < 2) p.work[threadIdx.x] = 0u;
+    for (int b = threadIdx.x; b < p.B; b += kBwdThreads) {
+      int start, len;
+      bwd_seq<VARLEN>(p, b, start, len, true);
+    }
+  }
+  if (warp == 9 && lane == 0) {
+    mbar_init(in_full, 1);
+    mbar_init(taken, 9);
+    mbar_init(in_empty, 1);
+    mbar_init(drain, 1);
+    for (int x = 0; x < S; ++x) {
+      mbar_init(&kv_full[x], 1);
+      mbar_init(&kv_empty[x], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sd_full[x], 1);
+      mbar_init(&sd_free[x], 256);
+      mbar_init(&sum_full[x], 128);
+      mbar_init(&sum_free[x], 128);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto take = [&](int m, BwdItem &it) -> bool {
+    bool ok = mbar_wait(in_full, m & 1, abort_flag, p.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    it.b = slot->b;
+    it.tile = slot->tile;
+    it.h = slot->h;
+    it.start = slot->start;
+    it.len = slot->len;
+    it.valid = slot->valid;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(taken);
+    return true;
+  };
+
+  if (warp == 9) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_do);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    bool ok = true;
+    int g = 0;      // key tiles issued so far
+    int last = -1;  // the last item whose Q and dO were issued
+    long long index = blockIdx.x;
+    for (int m = 0;; ++m) {
+      const BwdItem it = next_item<false, VARLEN, false, true>(p, p.H, [&]() -> long long {
+        const long long w = index;
+        index += gridDim.x;
+        return w;
+      });
+      if (lane == 0 && m > 0)
+        ok = mbar_wait(taken, (m - 1) & 1, abort_flag, p.status) &&
+             mbar_wait(in_empty, (m - 1) & 1, abort_flag, p.status);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      const int row0 = VARLEN ? it.start : 0, bc = VARLEN ? 0 : it.b;
+      if (lane == 0) {
+        slot->b = it.b;
+        slot->tile = it.tile;
+        slot->h = it.h;
+        slot->start = it.start;
+        slot->len = it.len;
+        slot->valid = it.valid;
+        if (it.valid) {
+          mbar_arrive_expect_tx(in_full, 2 * L::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c) {
+            tma_load_4d(sQ + c * L::kChunkBytes, &tm_q, in_full, c * 64, it.h, row0 + it.tile * 128, bc);
+            tma_load_4d(sDO + c * L::kChunkBytes, &tm_do, in_full, c * 64, it.h, row0 + it.tile * 128,
+                        bc);
+          }
+        } else {
+          mbar_arrive(in_full);  // no work left: publishes the empty slot
+        }
+      }
+      if (!it.valid) break;
+      last = m;
+      if (lane == 0) {
+        const int kvh = it.h / p.group;
+        const WindowTiles wt(p, it.tile, it.len);
+        for (int j = 0; j < wt.n; ++j, ++g) {
+          const int st = g % S, row = row0 + wt.key_tile(j) * 128;
+          if (g >= S && !mbar_wait(&kv_empty[st], ((g / S) - 1) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&kv_full[st], 2 * L::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c) {
+            tma_load_4d(sK + st * L::kTileBytes + c * L::kChunkBytes, &tm_k, &kv_full[st], c * 64, kvh,
+                        row, bc);
+            tma_load_4d(sV + st * L::kTileBytes + c * L::kChunkBytes, &tm_v, &kv_full[st], c * 64, kvh,
+                        row, bc);
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) {
+      // a wait ran out: let the copies still in flight land
+      if (last >= 0) mbar_drain(in_full, last & 1, p.status);
+      for (int x = max(0, g - S); x < g; ++x) mbar_drain(&kv_full[x % S], (x / S) & 1, p.status);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t q_base = smem_u32(sQ), do_base = smem_u32(sDO);
+    bool ok = true;
+    int g = 0;
+    for (int m = 0; ok; ++m) {
+      BwdItem it;
+      if (!take(m, it) || !it.valid) break;
+      const WindowTiles wt(p, it.tile, it.len);
+      for (int j = 0; j < wt.n; ++j, ++g) {
+        const int st = g % S, buf = g & 1;
+        ok = mbar_wait_warp(&kv_full[st], (g / S) & 1, abort_flag, p.status) &&
+             (g < 2 || mbar_wait_warp(&sd_free[buf], ((g >> 1) - 1) & 1, abort_flag, p.status));
+        if (!ok) break;
+        // V rows of another sequence meet weights of 0
+        const int inside = it.len - wt.key_tile(j) * 128;
+        if (VARLEN && inside < 128) zero_rows<D>(sV + st * L::kTileBytes, inside);
+        tc_fence_after();
+        mma_tile_ss<D>(tmem + buf * 256, q_base, smem_u32(sK + st * L::kTileBytes));
+        mma_tile_ss<D>(tmem + buf * 256 + 128, do_base, smem_u32(sV + st * L::kTileBytes));
+        mma_commit_elect(&sd_full[buf]);
+        mma_commit_elect(&kv_empty[st]);
+      }
+      if (!ok) break;
+      mma_commit_elect(in_empty);
+    }
+    mma_commit_elect(drain);
+    mbar_drain(drain, 0, p.status);
+  } else {
+    // ------------------------------------------------------------ elementwise
+    const int quad = warp & 3, hf = warp >> 2;  // TMEM lane group, column half
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const float2 sl2x2 = make_float2(p.scale_log2, p.scale_log2);
+    const size_t n_vec = static_cast<size_t>(p.B) * p.H * p.Npad;
+    const size_t n_rows =
+        VARLEN ? static_cast<size_t>(p.total_tokens) * p.H : static_cast<size_t>(p.B) * p.N * p.H;
+    bool ok = true;
+    int g = 0;
+    for (int m = 0; ok; ++m) {
+      BwdItem it;
+      if (!take(m, it) || !it.valid) break;
+      const int qi = it.tile * 128 + row;
+      const size_t lidx = VARLEN ? static_cast<size_t>(it.h) * p.total_tokens + it.start + qi
+                                 : (static_cast<size_t>(it.b) * p.H + it.h) * p.N + qi;
+      float nlse2 = -CUDART_INF_F;  // rows past the sequence, or without a visible key: P = 0
+      if (qi < it.len) {
+        const float l = checked_load(p.lse, lidx, n_rows, p.status);
+        if (l != -CUDART_INF_F) nlse2 = -(l * kLog2eF);
+      }
+      const float2 nl2 = make_float2(nlse2, nlse2);
+      const WindowTiles wt(p, it.tile, it.len);
+      float2 d0 = make_float2(0.f, 0.f), d1 = make_float2(0.f, 0.f);
+      for (int j = 0; j < wt.n; ++j, ++g) {
+        const int buf = g & 1, kt = wt.key_tile(j);
+        ok = mbar_wait(&sd_full[buf], (g >> 1) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int nvis = min(128, min(it.len, qi + 1) - kt * 128);
+        const int lo_c = qi + 1 - p.window - kt * 128, sink_c = p.sinks - kt * 128;
+        const uint32_t tS = tmem + buf * 256 + lane_off;
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          const int c = 32 * (2 * hf + cc);
+          // a chunk that no row of the warp sees adds nothing
+          if (__all_sync(0xffffffffu, c >= nvis || (c >= sink_c && c + 32 <= lo_c))) continue;
+          const bool part = c + 32 > nvis || (c < lo_c && c + 32 > sink_c);
+          uint32_t sv[32], dp[32];
+          tmem_ld32_wait(tS + c, sv);
+          tmem_ld32_wait(tS + 128 + c, dp);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float2 x0 =
+                ffma2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, nl2);
+            const float2 x1 = ffma2(
+                make_float2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sl2x2, nl2);
+            float w[4] = {ex2(x0.x), ex2(x0.y), ex2(x1.x), ex2(x1.y)};
+            if (part) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int k = c + e + y;
+                if (k >= nvis || (k < lo_c && k >= sink_c)) w[y] = 0.f;
+              }
+            }
+            d0 = ffma2(make_float2(w[0], w[1]),
+                       make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), d0);
+            d1 = ffma2(make_float2(w[2], w[3]),
+                       make_float2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])), d1);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&sd_free[buf]);
+      }
+      if (!ok) break;
+      // the upper columns' sums go to the lower columns' warps through shared
+      // memory (one of two buffers, by the item's parity)
+      const float mine = (d0.x + d0.y) + (d1.x + d1.y);
+      const int sb = m & 1;
+      float *sum = sums + 128 * sb;
+      if (hf == 1) {
+        ok = m < 2 || mbar_wait(&sum_free[sb], ((m >> 1) - 1) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        sum[row] = mine;
+        mbar_arrive(&sum_full[sb]);
+      } else {
+        ok = mbar_wait(&sum_full[sb], (m >> 1) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const float other = sum[row];
+        mbar_arrive(&sum_free[sb]);
+        const size_t vec = (static_cast<size_t>(it.b) * p.H + it.h) * p.Npad + qi;
+        if (in_bounds(vec, 1, n_vec, p.status)) {
+          p.nlse2[vec] = nlse2;
+          p.ndsum[vec] = qi < it.len ? -(mine + other) : 0.f;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------- sinks' sums
+// dV and dK of the sliced sink rows: the slots of a row are added in their
+// order, so the result does not depend on the order of the items.  One warp
+// per (sequence, KV head, row).
+template <int D, bool VARLEN>
+__global__ void __launch_bounds__(128) bwd_sink_sum_kernel(const BwdParams p) {
+  const int lane = threadIdx.x & 31;
+  const int rows = min(p.sinks, p.sink_tiles * 128);
+  const long long gw = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (gw >= static_cast<long long>(p.B) * p.Hkv * rows) return;
+  const int kj = static_cast<int>(gw % rows);
+  const int h = static_cast<int>(gw / rows % p.Hkv), b = static_cast<int>(gw / rows / p.Hkv);
+  int start, len;
+  bwd_seq<VARLEN>(p, b, start, len, false);
+  if (kj >= len) return;
+  const int t = kj / 128, n_q = (len + 127) / 128;
+  const int rest = n_q - window_queries(p, t, n_q);  // query tiles in slices
+  const int slots = 1 + (rest + p.sink_slice - 1) / p.sink_slice;
+  const size_t slot0 = ((static_cast<size_t>(b) * p.Hkv + h) * p.sink_tiles + t) * (1 + p.sink_slices);
+  const size_t n = static_cast<size_t>(p.B) * p.Hkv * p.sink_tiles * (1 + p.sink_slices) * 256 * D;
+  const size_t grow = VARLEN ? static_cast<size_t>(start) + kj : static_cast<size_t>(b) * p.N + kj;
+  const size_t total = VARLEN ? static_cast<size_t>(p.total_tokens) : static_cast<size_t>(p.B) * p.N;
+  constexpr int E = D / 32;
+  const size_t dst = (grow * p.Hkv + h) * D + lane * E;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float sum[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.f;
+    for (int x = 0; x < slots; ++x) {
+      const size_t at = ((slot0 + x) * 2 + which) * 128 * D + (kj % 128) * D + lane * E;
+      if (!in_bounds(at, E, n, p.status)) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] += p.sink_part[at + e];
+    }
+    uint16_t *out = static_cast<uint16_t *>(which ? p.dk : p.dv) + dst;
+    if (!in_bounds(dst, E, total * p.Hkv * D, p.status)) return;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t *>(out + e) = pack_bf16x2(sum[e], sum[e + 1]);
   }
 }
 
@@ -562,7 +969,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int gk = 0, gv = 0;  // K and V tiles issued so far
     int last = -1;       // the last item whose Q and dO were issued
     for (int m = 0;; ++m) {
-      const BwdItem it = claim_item<CAUSAL && !WIN, VARLEN, false>(p, p.work + 0, p.H);
+      const BwdItem it = claim_item<CAUSAL && !WIN, VARLEN, false, WIN>(p, p.work + 0, p.H);
       if (lane == 0 && m > 0)
         ok = mbar_wait(taken, (m - 1) & 1, abort_flag, p.status) &&
              mbar_wait(qdo_empty, (m - 1) & 1, abort_flag, p.status);
@@ -746,7 +1153,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // P = exp(S * scale - lse) of this half's 64 keys, kept as bf16 pairs
         // (the values the dQ product uses through dS)
         // (packed pairs; the mask is applied only in chunks that reach past nvis)
-        uint32_t pp[32];
+        // (windowed: kept in fp32, so that dS is rounded once)
+        uint32_t pp[WIN ? 64 : 32];
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
@@ -763,7 +1171,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               w0 = seen(c * 32 + e) ? w0 : 0.f;
               w1 = seen(c * 32 + e + 1) ? w1 : 0.f;
             }
-            pp[cc * 16 + (e >> 1)] = pack_bf16x2(w0, w1);
+            if constexpr (WIN) {
+              pp[cc * 32 + e] = __float_as_uint(w0);
+              pp[cc * 32 + e + 1] = __float_as_uint(w1);
+            } else {
+              pp[cc * 16 + (e >> 1)] = pack_bf16x2(w0, w1);
+            }
           }
         }
         tc_fence_before();
@@ -782,7 +1195,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tmem_ld32_wait(tP + c * 32, dp);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float2 w = bf16x2_to_float2(pp[cc * 16 + (e >> 1)]);
+            const float2 w = WIN ? make_float2(__uint_as_float(pp[(WIN ? cc * 32 + e : 0)]),
+                                               __uint_as_float(pp[(WIN ? cc * 32 + e + 1 : 0)]))
+                                 : bf16x2_to_float2(pp[cc * 16 + (e >> 1)]);
             const float2 r = fmul2(
                 w, fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), nd2));
             pk[e >> 1] = pack_bf16x2(r.x, r.y);
@@ -919,6 +1334,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     it.start = slot->start;
     it.len = slot->len;
     it.valid = slot->valid;
+    if constexpr (WIN) {
+      it.i0 = slot->i0;
+      it.i1 = slot->i1;
+      it.part = slot->part;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(taken);
     return true;
@@ -927,13 +1347,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // (from the key tile on, causal) times the query heads of the KV head;
   // iteration it is query head kvh * group + it % group, query tile
   // i0 + it / group
-  // (windowed: to the last query tile whose window holds a key of the tile,
-  // or to the last of all for a tile with sinks)
+  // (windowed: those of its range [i0, i1))
+  auto first_tile = [&](const BwdItem &it) { return WIN ? it.i0 : CAUSAL ? it.tile : 0; };
   auto iterations = [&](const BwdItem &it) {
-    int end = (it.len + 127) / 128;
-    if (WIN && it.tile * 128 >= p.sinks)
-      end = min(end, (it.tile * 128 + 127 + p.window - 1) / 128 + 1);
-    return (end - (CAUSAL ? it.tile : 0)) * p.group;
+    return ((WIN ? it.i1 : (it.len + 127) / 128) - first_tile(it)) * p.group;
   };
 
   if (warp == 9) {
@@ -948,7 +1365,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int gq = 0, go = 0;  // Q and dO stages issued so far
     int last = -1;       // the last item whose K and V were issued
     for (int m = 0;; ++m) {
-      const BwdItem it = claim_item<CAUSAL && !WIN, VARLEN, true>(p, p.work + 1, p.Hkv);
+      const BwdItem it = claim_item<CAUSAL && !WIN, VARLEN, true, WIN>(p, p.work + 1, p.Hkv);
       if (lane == 0 && m > 0)
         ok = mbar_wait(taken, (m - 1) & 1, abort_flag, p.status) &&
              mbar_wait(kv_empty, (m - 1) & 1, abort_flag, p.status);
@@ -961,6 +1378,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         slot->start = it.start;
         slot->len = it.len;
         slot->valid = it.valid;
+        if constexpr (WIN) {
+          slot->i0 = it.i0;
+          slot->i1 = it.i1;
+          slot->part = it.part;
+        }
         if (it.valid) {
           const int row0 = VARLEN ? it.start : 0, bc = VARLEN ? 0 : it.b;
           mbar_arrive_expect_tx(in_full, 2 * L::kTileBytes);
@@ -977,7 +1399,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       last = m;
       if (lane == 0) {
         const int row0 = VARLEN ? it.start : 0, bc = VARLEN ? 0 : it.b;
-        const int i0 = CAUSAL ? it.tile : 0;
+        const int i0 = first_tile(it);
         const int n_it = iterations(it);
         for (int x = 0; x < n_it; ++x) {
           const int hq = it.h * p.group + x % p.group;
@@ -1042,7 +1464,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int n_it = iterations(it);
       // query rows past a packed sequence are made 0 (windowed calls)
       auto trim = [&](uint8_t *tile, int x) {
-        const int inside = it.len - ((CAUSAL ? it.tile : 0) + x / p.group) * 128;
+        const int inside = it.len - (first_tile(it) + x / p.group) * 128;
         if (WIN && VARLEN && inside < 128) zero_rows<D>(tile, inside);
       };
       ok = mbar_wait_warp(&q_full[g0 % SQ], (g0 / SQ) & 1, abort_flag, p.status) &&
@@ -1123,7 +1545,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!take(m, itm) || !itm.valid) break;
       const int kj = itm.tile * 128 + row;
       const int len = itm.len;
-      const int i0 = CAUSAL ? itm.tile : 0;
+      const int i0 = first_tile(itm);
       const int n_it = iterations(itm);
       for (int x = 0; x < n_it; ++x) {
         const int g = g0 + x;
@@ -1147,7 +1569,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // pairs, stored over S^T (packed pairs; the mask is applied only in
         // chunks that start before qfirst)
         auto seen = [&](int q0) { return q0 >= qfirst && !(WIN && q0 >= qlast); };
+        // (windowed: also kept in fp32, so that dS^T is rounded once)
         uint32_t pp[32];
+        float pf[WIN ? 64 : 1];
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
@@ -1168,6 +1592,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               w1 = seen(q0 + 1) ? w1 : 0.f;
               w2 = seen(q0 + 2) ? w2 : 0.f;
               w3 = seen(q0 + 3) ? w3 : 0.f;
+            }
+            if constexpr (WIN) {
+              pf[cc * 32 + e] = w0;
+              pf[cc * 32 + e + 1] = w1;
+              pf[cc * 32 + e + 2] = w2;
+              pf[cc * 32 + e + 3] = w3;
             }
             pp[cc * 16 + (e >> 1)] = pack_bf16x2(w0, w1);
             pp[cc * 16 + (e >> 1) + 1] = pack_bf16x2(w2, w3);
@@ -1195,8 +1625,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int e = 0; e < 32; e += 4) {
             const int q0 = c * 32 + e;
             const float4 d4 = *reinterpret_cast<const float4 *>(vd + q0);
-            const float2 wa = bf16x2_to_float2(pp[cc * 16 + (e >> 1)]);
-            const float2 wb = bf16x2_to_float2(pp[cc * 16 + (e >> 1) + 1]);
+            const int f = WIN ? cc * 32 + e : 0;
+            const float2 wa = WIN ? make_float2(pf[f], pf[WIN ? f + 1 : 0])
+                                  : bf16x2_to_float2(pp[cc * 16 + (e >> 1)]);
+            const float2 wb = WIN ? make_float2(pf[WIN ? f + 2 : 0], pf[WIN ? f + 3 : 0])
+                                  : bf16x2_to_float2(pp[cc * 16 + (e >> 1) + 1]);
             const float2 ra = fmul2(
                 wa, fadd2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])),
                           make_float2(d4.x, d4.y)));
@@ -1223,17 +1656,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           VARLEN ? static_cast<size_t>(itm.start) + kj : static_cast<size_t>(itm.b) * p.N + kj;
       const size_t orow = (grow * p.Hkv + itm.h) * D;
       const size_t rows = VARLEN ? static_cast<size_t>(p.total_tokens) : static_cast<size_t>(p.B) * p.N;
-      const bool row_ok = kj < len && in_bounds(orow, D, rows * p.Hkv * D, p.status);
+      // windowed tiles of sliced sinks: the sinks' rows leave as fp32 partial
+      // sums, the others only from the item of the tile's own window
+      const bool sink = WIN && itm.part >= 0 && kj < p.sinks;
+      const bool row_ok = kj < len && !sink && !(WIN && itm.part > 0) &&
+                          in_bounds(orow, D, rows * p.Hkv * D, p.status);
+      const size_t n_part = static_cast<size_t>(p.B) * p.Hkv * p.sink_tiles * (1 + p.sink_slices);
+      auto store_part = [&](int which, const uint32_t(&v)[D / 64][32], float mul) {
+        const size_t at =
+            ((((static_cast<size_t>(itm.b) * p.Hkv + itm.h) * p.sink_tiles + itm.tile) *
+                  (1 + p.sink_slices) + itm.part) * 2 + which) * 128 * D +
+            row * D + hf * (D / 2);
+        if (!sink || kj >= len || !in_bounds(at, D / 2, n_part * 256 * D, p.status)) return;
+        float4 *dst = reinterpret_cast<float4 *>(p.sink_part + at);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          dst[c] = make_float4(__uint_as_float(v[c / 8][c % 8 * 4]) * mul,
+                               __uint_as_float(v[c / 8][c % 8 * 4 + 1]) * mul,
+                               __uint_as_float(v[c / 8][c % 8 * 4 + 2]) * mul,
+                               __uint_as_float(v[c / 8][c % 8 * 4 + 3]) * mul);
+      };
       const size_t step = static_cast<size_t>(p.Hkv) * D;
       uint32_t o[D / 64][32];
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) tmem_ld32_wait(tV + (hf * (D / 64) + c) * 32, o[c]);
+      if constexpr (WIN) store_part(0, o, 1.f);
       store_half_rows_bf16<D>(static_cast<uint16_t *>(p.dv) + orow + hf * (D / 2), step, row_ok, o,
                               1.f);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) tmem_ld32_wait(tK + (hf * (D / 64) + c) * 32, o[c]);
       tc_fence_before();
       mbar_arrive(kv_free);
+      if constexpr (WIN) store_part(1, o, p.scale);
       store_half_rows_bf16<D>(static_cast<uint16_t *>(p.dk) + orow + hf * (D / 2), step, row_ok, o,
                               p.scale);
       g0 += n_it;
@@ -1255,12 +1709,28 @@ static cudaError_t launch_bwd_d(const CUtensorMap &tq, const CUtensorMap &tdo,
                                 const CUtensorMap &tk, const CUtensorMap &tv, const BwdParams &p,
                                 bool causal, cudaStream_t stream) {
   using L = BwdLayout<D>;
-  const long long pre_rows = static_cast<long long>(p.B) * p.Npad * p.H;
-  const long long rows_per_block = 256 / (D / 8);
-  bwd_preprocess_kernel<D, VARLEN>
-      <<<static_cast<unsigned>((pre_rows + rows_per_block - 1) / rows_per_block), 256, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if constexpr (WIN) {
+    // work items: every (sequence, 128-row tile), as below
+    long long tiles = static_cast<long long>(p.B) * p.n_tiles;
+    if (VARLEN && p.longest_first) tiles = std::min(tiles, (p.total_tokens + 127LL) / 128 + p.B);
+    auto sums = bwd_sums_kernel<D, VARLEN>;
+    e = cudaFuncSetAttribute(sums, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             BwdSumsLayout<D>::kSmemAlloc);
+    if (e != cudaSuccess) return e;
+    sums<<<static_cast<unsigned>(std::min<long long>(tiles * p.H, p.num_ctas)), kBwdThreads,
+           BwdSumsLayout<D>::kSmemAlloc, stream>>>(tq, tdo, tk, tv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  } else {
+    const long long pre_rows = static_cast<long long>(p.B) * p.Npad * p.H;
+    const long long rows_per_block = 256 / (D / 8);
+    bwd_preprocess_kernel<D, VARLEN>
+        <<<static_cast<unsigned>((pre_rows + rows_per_block - 1) / rows_per_block), 256, 0,
+           stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   auto dq = causal ? bwd_dq_kernel<D, true, VARLEN, WIN> : bwd_dq_kernel<D, WIN, VARLEN, WIN>;
   auto dkdv = causal ? bwd_dkdv_kernel<D, true, VARLEN, WIN> : bwd_dkdv_kernel<D, WIN, VARLEN, WIN>;
   e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1273,10 +1743,22 @@ static cudaError_t launch_bwd_d(const CUtensorMap &tq, const CUtensorMap &tdo,
   long long items = static_cast<long long>(p.B) * p.n_tiles;
   if (VARLEN && p.longest_first)
     items = std::min(items, (p.total_tokens + 127LL) / 128 + p.B);
-  const unsigned grid_kv = static_cast<unsigned>(std::min<long long>(items * p.Hkv, p.num_ctas));
+  const long long slices = WIN ? static_cast<long long>(p.B) * p.sink_tiles * p.sink_slices : 0;
+  const unsigned grid_kv =
+      static_cast<unsigned>(std::min<long long>((items + slices) * p.Hkv, p.num_ctas));
   dkdv<<<grid_kv, kBwdThreads, L::kSmemAlloc, stream>>>(tq, tdo, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if constexpr (WIN) {
+    if (p.sink_tiles > 0) {
+      const long long rows =
+          static_cast<long long>(p.B) * p.Hkv * std::min(p.sinks, p.sink_tiles * 128);
+      bwd_sink_sum_kernel<D, VARLEN>
+          <<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+  }
   // persistent: one CTA per SM at most
   const unsigned grid_q = static_cast<unsigned>(std::min<long long>(items * p.H, p.num_ctas));
   dq<<<grid_q, kBwdThreads, BwdDqLayout<D>::kSmemAlloc, stream>>>(tq, tdo, tk, tv, p);

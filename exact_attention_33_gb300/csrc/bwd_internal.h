@@ -33,8 +33,16 @@ struct BwdParams {
   unsigned int *work;         // workspace: work counters of the dQ [0] and dK/dV [1] kernels
                               // (zeroed by the preprocess kernel)
   int num_ctas;               // CTAs of a persistent kernel (the SM count)
-  int window, sinks;          // windowed kernels only: query i sees key j <= i when
-                              // j > i - window or j < sinks
+  // windowed kernels only
+  int window, sinks;          // query i sees key j <= i when j > i - window or j < sinks
+  // The sinks' other queries (those whose window lies behind them) are as many
+  // as the sequence is long: the dK / dV of the first sink_tiles key tiles takes
+  // them in up to sink_slices slices of sink_slice query tiles, each a work
+  // item, and the sinks' rows are added up from fp32 partial sums
+  // [B, Hkv, sink_tiles, 1 + sink_slices, 2 (dV, dK), 128, d] (the first slot
+  // is the tile's own window).  0 tiles: one item takes them all.
+  int sink_tiles, sink_slices, sink_slice;
+  float *sink_part;
 };
 
 }  // namespace fa
