@@ -162,6 +162,11 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int from) {
   __syncwarp();
 }
 
+// Bits [0, n) of a 32-bit mask, any n.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // The key tiles of a windowed query tile: the first n_sink tiles of the
 // sequence and, `gap` tiles later, those from the window of the tile's first
 // row to its diagonal, n in all.
@@ -745,9 +750,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 32 * (2 * hf + cc);
+          const uint32_t bits = low_bits(nvis - c) & (~low_bits(lo_c - c) | low_bits(sink_c - c));
           // a chunk that no row of the warp sees adds nothing
-          if (__all_sync(0xffffffffu, c >= nvis || (c >= sink_c && c + 32 <= lo_c))) continue;
-          const bool part = c + 32 > nvis || (c < lo_c && c + 32 > sink_c);
+          if (__all_sync(0xffffffffu, bits == 0u)) continue;
+          const bool part = __any_sync(0xffffffffu, ~bits != 0u);
           uint32_t sv[32], dp[32];
           tmem_ld32_wait(tS + c, sv);
           tmem_ld32_wait(tS + 128 + c, dp);
@@ -760,10 +766,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             float w[4] = {ex2(x0.x), ex2(x0.y), ex2(x1.x), ex2(x1.y)};
             if (part) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int k = c + e + y;
-                if (k >= nvis || (k < lo_c && k >= sink_c)) w[y] = 0.f;
-              }
+              for (int y = 0; y < 4; ++y)
+                if (!(bits & (1u << (e + y)))) w[y] = 0.f;
             }
             d0 = ffma2(make_float2(w[0], w[1]),
                        make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), d0);
@@ -1149,19 +1153,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // windowed: nor are keys [sink_c, lo_c), between sinks and window
         const int lo_c = WIN ? qi + 1 - p.window - kt * 128 : 0;
         const int sink_c = WIN ? p.sinks - kt * 128 : 0;
-        auto seen = [&](int c) { return c < nvis && !(WIN && c < lo_c && c >= sink_c); };
         // P = exp(S * scale - lse) of this half's 64 keys, kept as bf16 pairs
         // (the values the dQ product uses through dS)
         // (packed pairs; the mask is applied only in chunks that reach past nvis)
         // (windowed: kept in fp32, so that dS is rounded once)
         uint32_t pp[WIN ? 64 : 32];
+        bool hid[2] = {false, false};  // windowed: chunks that no row of the warp sees
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
+          const uint32_t bits =
+              WIN ? low_bits(nvis - c * 32) & (~low_bits(lo_c - c * 32) | low_bits(sink_c - c * 32))
+                  : 0u;
+          if constexpr (WIN) {
+            hid[cc] = __all_sync(0xffffffffu, bits == 0u);
+            if (hid[cc]) continue;
+          }
           uint32_t sv[32];
           tmem_ld32_wait(tS + c * 32, sv);
-          const bool part =
-              c * 32 + 32 > nvis || (WIN && c * 32 < lo_c && c * 32 + 32 > sink_c);
+          const bool part = WIN ? __any_sync(0xffffffffu, ~bits != 0u) : c * 32 + 32 > nvis;
+          auto seen = [&](int k) { return WIN ? ((bits >> (k & 31)) & 1u) != 0u : k < nvis; };
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float2 x =
@@ -1191,6 +1202,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
+          if (WIN && hid[cc]) {
+            uint32_t zero[16] = {};
+            tmem_st16(tP + hf * 64 + cc * 16, zero);
+            continue;
+          }
           uint32_t dp[32], pk[16];
           tmem_ld32_wait(tP + c * 32, dp);
 #pragma unroll
@@ -1568,16 +1584,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // P^T = exp(S^T * scale - lse[q]) of this half's 64 queries as bf16
         // pairs, stored over S^T (packed pairs; the mask is applied only in
         // chunks that start before qfirst)
-        auto seen = [&](int q0) { return q0 >= qfirst && !(WIN && q0 >= qlast); };
-        // (windowed: also kept in fp32, so that dS^T is rounded once)
+        // (windowed: also kept in fp32, so that dS^T is rounded once; a chunk
+        // in which no row of the warp sees a query takes no part, and at a
+        // short window's two edges that is half of the tile)
         uint32_t pp[32];
         float pf[WIN ? 64 : 1];
+        bool hid[2] = {false, false};
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
+          const uint32_t bits =
+              WIN ? low_bits(qlast - c * 32) & ~low_bits(qfirst - c * 32) : ~low_bits(qfirst - c * 32);
+          if constexpr (WIN) {
+            hid[cc] = __all_sync(0xffffffffu, bits == 0u);
+            if (hid[cc]) {
+              uint32_t zero[16] = {};
+              tmem_st16(tS + hf * 64 + cc * 16, zero);
+              continue;
+            }
+          }
           uint32_t sv[32];
           tmem_ld32_wait(tS + c * 32, sv);
-          const bool part = c * 32 < qfirst || (WIN && c * 32 + 32 > qlast);
+          const bool part = WIN ? __any_sync(0xffffffffu, ~bits != 0u) : c * 32 < qfirst;
+          auto seen = [&](int q0) { return WIN ? ((bits >> (q0 & 31)) & 1u) != 0u : q0 >= qfirst; };
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const int q0 = c * 32 + e;
@@ -1619,6 +1648,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
+          if (WIN && hid[cc]) {
+            uint32_t zero[16] = {};
+            tmem_st16(tP + hf * 64 + cc * 16, zero);
+            continue;
+          }
           uint32_t dp[32], pd[16];
           tmem_ld32_wait(tP + c * 32, dp);
 #pragma unroll
