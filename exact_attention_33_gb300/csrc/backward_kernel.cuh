@@ -509,24 +509,27 @@ __global__ void __launch_bounds__(256) bwd_preprocess_kernel(const BwdParams p) 
 // One CTA per SM; query tile and head items in a fixed order (the CTA's index,
 // then every grid-th).  S and dP of a key tile go to one of two TMEM buffers,
 // [0, 256) or [256, 512), so the products of the next tile run while the
-// elementwise warps (roles as in the dQ kernel) work on this one.
+// elementwise warps (roles as in the dQ kernel) work on this one.  At d = 64 Q
+// and dO have two buffers as well (33 -> 30 us for 64 heads of 2048 rows, window
+// 500); at d = 128 the room serves a longer ring instead (197 us against 212 us
+// on 16 packed documents of 35 k rows, 16 / 4 heads, window 512: there the 64 KiB
+// that a tile's 0.5 us of products read through L2 are the limit).
 template <int D>
 struct BwdSumsLayout {
   static constexpr int kChunkBytes = 128 * 128;
   static constexpr int kChunks = D / 64;
   static constexpr int kTileBytes = kChunks * kChunkBytes;
-  static constexpr int kStages = 2;  // of K and of V
-  static constexpr int kQ = 0;
-  static constexpr int kDO = kQ + kTileBytes;
-  static constexpr int kK = kDO + kTileBytes;
-  static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kBar = kV + kStages * kTileBytes;
-  // in_full, taken, in_empty, drain, kv_full[2], kv_empty[2], sd_full[2],
-  // sd_free[2], sum_full[2], sum_free[2]
-  static constexpr int kNumBars = 12 + 2 * kStages;
+  static constexpr int kStages = (D == 128) ? 4 : 6;  // ring of K(0), V(0), K(1), V(1), ...
+  static constexpr int kBufs = (D == 128) ? 1 : 2;    // items whose Q and dO are held
+  static constexpr int kIn = 0;
+  static constexpr int kRing = kIn + 2 * kBufs * kTileBytes;
+  static constexpr int kBar = kRing + kStages * kTileBytes;
+  // drain, in_full[2], taken[2], in_empty[2], sd_full[2], sd_free[2],
+  // sum_full[2], sum_free[2], ring_full[], ring_empty[]
+  static constexpr int kNumBars = 15 + 2 * kStages;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kItem = kMisc + 16;
-  static constexpr int kSum = kItem + 48;            // two items' sums of the upper columns
+  static constexpr int kItem = kMisc + 16;           // two work item slots
+  static constexpr int kSum = kItem + 96;            // two items' sums of the upper columns
   static constexpr int kBytes = kSum + 2 * 128 * 4;
   static constexpr int kSmemAlloc = kBytes + 1024;
   static_assert(kSmemAlloc <= 232448, "row sum shared memory exceeds 227 KiB");
@@ -540,25 +543,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const __grid_constant__ CUtensorMap tm_v, const BwdParams p) {
   using L = BwdSumsLayout<D>;
   constexpr int S = L::kStages;
+  constexpr int NB = L::kBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBar);
-  uint64_t *in_full = bars;         // Q and dO of the item (and its slot)
-  uint64_t *taken = bars + 1;       // the MMA and elementwise warps have read the slot
-  uint64_t *in_empty = bars + 2;    // the item's last products have read Q and dO
-  uint64_t *drain = bars + 3;
-  uint64_t *kv_full = bars + 4;     // K and V of a key tile
-  uint64_t *kv_empty = kv_full + S;
-  uint64_t *sd_full = kv_empty + S;  // S and dP of a key tile are in TMEM
+  uint64_t *drain = bars;
+  // of item m: in_full, taken and in_empty m % NB
+  uint64_t *in_full = bars + 1;      // Q and dO (and the slot)
+  uint64_t *taken = in_full + 2;     // the MMA and elementwise warps have read the slot
+  uint64_t *in_empty = taken + 2;    // the last products have read Q and dO
+  uint64_t *sd_full = in_empty + 2;  // S and dP of a key tile are in TMEM (either buffer)
   uint64_t *sd_free = sd_full + 2;   // and read
   uint64_t *sum_full = sd_free + 2;  // an item's sums of the upper columns are in shared memory
   uint64_t *sum_free = sum_full + 2;  // and read
+  uint64_t *ring_full = sum_free + 2;
+  uint64_t *ring_empty = ring_full + S;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
-  volatile BwdItem *slot = reinterpret_cast<volatile BwdItem *>(smem + L::kItem);
   float *sums = reinterpret_cast<float *>(smem + L::kSum);
-  uint8_t *sQ = smem + L::kQ, *sDO = smem + L::kDO, *sK = smem + L::kK, *sV = smem + L::kV;
+  auto slot_of = [&](int m) {
+    return reinterpret_cast<volatile BwdItem *>(smem + L::kItem + 48 * (m % NB));
+  };
+  auto in_tile = [&](int m, int which) {  // Q (0) or dO (1) of item m
+    return smem + L::kIn + (2 * (m % NB) + which) * L::kTileBytes;
+  };
+  auto ring_tile = [&](int x) { return smem + L::kRing + (x % S) * L::kTileBytes; };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -571,19 +581,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   }
   if (warp == 9 && lane == 0) {
-    mbar_init(in_full, 1);
-    mbar_init(taken, 9);
-    mbar_init(in_empty, 1);
     mbar_init(drain, 1);
-    for (int x = 0; x < S; ++x) {
-      mbar_init(&kv_full[x], 1);
-      mbar_init(&kv_empty[x], 1);
-    }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&in_full[x], 1);
+      mbar_init(&taken[x], 9);
+      mbar_init(&in_empty[x], 1);
       mbar_init(&sd_full[x], 1);
       mbar_init(&sd_free[x], 256);
       mbar_init(&sum_full[x], 128);
       mbar_init(&sum_free[x], 128);
+    }
+    for (int x = 0; x < S; ++x) {
+      mbar_init(&ring_full[x], 1);
+      mbar_init(&ring_empty[x], 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -599,9 +609,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto take = [&](int m, BwdItem &it) -> bool {
-    bool ok = mbar_wait(in_full, m & 1, abort_flag, p.status);
+    bool ok = mbar_wait(&in_full[m % NB], (m / NB) & 1, abort_flag, p.status);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
+    volatile BwdItem *slot = slot_of(m);
     it.b = slot->b;
     it.tile = slot->tile;
     it.h = slot->h;
@@ -609,7 +620,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     it.len = slot->len;
     it.valid = slot->valid;
     __syncwarp();
-    if (lane == 0) mbar_arrive(taken);
+    if (lane == 0) mbar_arrive(&taken[m % NB]);
     return true;
   };
 
@@ -622,8 +633,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tma_prefetch_desc(&tm_v);
     }
     bool ok = true;
-    int g = 0;      // key tiles issued so far
-    int last = -1;  // the last item whose Q and dO were issued
+    int x = 0;      // tiles of the ring issued so far
+    int items = 0;  // items whose Q and dO were issued
     long long index = blockIdx.x;
     for (int m = 0;; ++m) {
       const BwdItem it = next_item<false, VARLEN, false, true>(p, p.H, [&]() -> long long {
@@ -631,50 +642,50 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         index += gridDim.x;
         return w;
       });
-      if (lane == 0 && m > 0)
-        ok = mbar_wait(taken, (m - 1) & 1, abort_flag, p.status) &&
-             mbar_wait(in_empty, (m - 1) & 1, abort_flag, p.status);
+      if (lane == 0 && m >= NB)
+        ok = mbar_wait(&taken[m % NB], ((m / NB) - 1) & 1, abort_flag, p.status) &&
+             mbar_wait(&in_empty[m % NB], ((m / NB) - 1) & 1, abort_flag, p.status);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       const int row0 = VARLEN ? it.start : 0, bc = VARLEN ? 0 : it.b;
       if (lane == 0) {
+        volatile BwdItem *slot = slot_of(m);
         slot->b = it.b;
         slot->tile = it.tile;
         slot->h = it.h;
         slot->start = it.start;
         slot->len = it.len;
         slot->valid = it.valid;
+        uint64_t *bar = &in_full[m % NB];
         if (it.valid) {
-          mbar_arrive_expect_tx(in_full, 2 * L::kTileBytes);
+          mbar_arrive_expect_tx(bar, 2 * L::kTileBytes);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c) {
-            tma_load_4d(sQ + c * L::kChunkBytes, &tm_q, in_full, c * 64, it.h, row0 + it.tile * 128, bc);
-            tma_load_4d(sDO + c * L::kChunkBytes, &tm_do, in_full, c * 64, it.h, row0 + it.tile * 128,
-                        bc);
+            tma_load_4d(in_tile(m, 0) + c * L::kChunkBytes, &tm_q, bar, c * 64, it.h,
+                        row0 + it.tile * 128, bc);
+            tma_load_4d(in_tile(m, 1) + c * L::kChunkBytes, &tm_do, bar, c * 64, it.h,
+                        row0 + it.tile * 128, bc);
           }
         } else {
-          mbar_arrive(in_full);  // no work left: publishes the empty slot
+          mbar_arrive(bar);  // no work left: publishes the empty slot
         }
       }
       if (!it.valid) break;
-      last = m;
+      items = m + 1;
       if (lane == 0) {
         const int kvh = it.h / p.group;
         const WindowTiles wt(p, it.tile, it.len);
-        for (int j = 0; j < wt.n; ++j, ++g) {
-          const int st = g % S, row = row0 + wt.key_tile(j) * 128;
-          if (g >= S && !mbar_wait(&kv_empty[st], ((g / S) - 1) & 1, abort_flag, p.status)) {
+        for (int j = 0; ok && j < 2 * wt.n; ++j, ++x) {  // K and V in turn
+          const int st = x % S;
+          if (x >= S && !mbar_wait(&ring_empty[st], ((x / S) - 1) & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&kv_full[st], 2 * L::kTileBytes);
+          mbar_arrive_expect_tx(&ring_full[st], L::kTileBytes);
 #pragma unroll
-          for (int c = 0; c < L::kChunks; ++c) {
-            tma_load_4d(sK + st * L::kTileBytes + c * L::kChunkBytes, &tm_k, &kv_full[st], c * 64, kvh,
-                        row, bc);
-            tma_load_4d(sV + st * L::kTileBytes + c * L::kChunkBytes, &tm_v, &kv_full[st], c * 64, kvh,
-                        row, bc);
-          }
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_4d(ring_tile(x) + c * L::kChunkBytes, (j & 1) ? &tm_v : &tm_k, &ring_full[st],
+                        c * 64, kvh, row0 + wt.key_tile(j >> 1) * 128, bc);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -682,34 +693,42 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (!ok && lane == 0) {
       // a wait ran out: let the copies still in flight land
-      if (last >= 0) mbar_drain(in_full, last & 1, p.status);
-      for (int x = max(0, g - S); x < g; ++x) mbar_drain(&kv_full[x % S], (x / S) & 1, p.status);
+      for (int y = max(0, items - NB); y < items; ++y)
+        mbar_drain(&in_full[y % NB], (y / NB) & 1, p.status);
+      for (int y = max(0, x - S); y < x; ++y) mbar_drain(&ring_full[y % S], (y / S) & 1, p.status);
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t q_base = smem_u32(sQ), do_base = smem_u32(sDO);
     bool ok = true;
-    int g = 0;
+    int g = 0;  // key tiles of the earlier items
+    auto arrived = [&](int x) -> bool {
+      return mbar_wait_warp(&ring_full[x % S], (x / S) & 1, abort_flag, p.status);
+    };
     for (int m = 0; ok; ++m) {
       BwdItem it;
       if (!take(m, it) || !it.valid) break;
+      const uint32_t q_base = smem_u32(in_tile(m, 0)), do_base = smem_u32(in_tile(m, 1));
       const WindowTiles wt(p, it.tile, it.len);
       for (int j = 0; j < wt.n; ++j, ++g) {
-        const int st = g % S, buf = g & 1;
-        ok = mbar_wait_warp(&kv_full[st], (g / S) & 1, abort_flag, p.status) &&
+        const int xk = 2 * g, xv = 2 * g + 1, buf = g & 1;
+        ok = arrived(xk) &&
              (g < 2 || mbar_wait_warp(&sd_free[buf], ((g >> 1) - 1) & 1, abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        mma_tile_ss<D>(tmem + buf * 256, q_base, smem_u32(ring_tile(xk)));
+        mma_commit_elect(&ring_empty[xk % S]);
+        ok = arrived(xv);
         if (!ok) break;
         // V rows of another sequence meet weights of 0
         const int inside = it.len - wt.key_tile(j) * 128;
-        if (VARLEN && inside < 128) zero_rows<D>(sV + st * L::kTileBytes, inside);
+        if (VARLEN && inside < 128) zero_rows<D>(ring_tile(xv), inside);
         tc_fence_after();
-        mma_tile_ss<D>(tmem + buf * 256, q_base, smem_u32(sK + st * L::kTileBytes));
-        mma_tile_ss<D>(tmem + buf * 256 + 128, do_base, smem_u32(sV + st * L::kTileBytes));
+        mma_tile_ss<D>(tmem + buf * 256 + 128, do_base, smem_u32(ring_tile(xv)));
         mma_commit_elect(&sd_full[buf]);
-        mma_commit_elect(&kv_empty[st]);
+        mma_commit_elect(&ring_empty[xv % S]);
       }
       if (!ok) break;
-      mma_commit_elect(in_empty);
+      mma_commit_elect(&in_empty[m % NB]);
     }
     mma_commit_elect(drain);
     mbar_drain(drain, 0, p.status);
