@@ -951,58 +951,40 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
       // 64-key halves of P are zero without exponentials
       const int nvis_w = (D == 64 && !WIN) ? __reduce_max_sync(0xffffffffu, nvis) : kPrefillBN;
       auto f = [&](int c) { return __uint_as_float(sr[c]); };
-      float mx0, mx1, mx2, mx3;
-      // Windowed: a third to all of a window's tiles hold masked scores, and at
-      // an edge most 32-key chunks are seen by every row of the warp or by
-      // none.  Each chunk of an edge tile is masked only where some row sees
-      // part of it, and a hidden one takes no part at all; the other tiles
-      // run without these branches (W 500 of N 2048, B4 H16 d64: 110 us with
-      // every edge tile masked column by column, 48 us by chunks).
-      const bool edge = WIN && __any_sync(0xffffffffu, nvis < kPrefillBN ||
-                                                           (lo_c > 0 && sink_c < kPrefillBN));
-      bool hid[4] = {false, false, false, false};
-      if (WIN && edge) {
-        mx0 = mx1 = mx2 = mx3 = -CUDART_INF_F;
+      // Windowed: masks as bits, a test and a select a score (three compares a
+      // score took 110 us where this takes 44 us: N 2048, window 500, B4 H16
+      // d64).  Leaving out the 32-key chunks that no row of the warp sees saves
+      // exponentials but was slower (48 us; 598 against 567 us on packed
+      // prompts with a window of 1024): the branches double the code, and the
+      // instruction cache is what a CTA of few key tiles runs short of.
+      if (WIN) {
+        if (__any_sync(0xffffffffu, nvis < kPrefillBN || (lo_c > 0 && sink_c < kPrefillBN))) {
+          auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          const int nv = nvis - 32 * cc, lo = lo_c - 32 * cc, sk = sink_c - 32 * cc;
-          hid[cc] = __all_sync(0xffffffffu, nv <= 0 || (sk <= 0 && lo >= 32));
-          const bool part = __any_sync(0xffffffffu, nv < 32 || (lo > 0 && sk < 32));
-          if (hid[cc]) continue;
-          if (part) {
-            // bit c: column c of the chunk is seen
-            auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
-            const uint32_t seen = below(nv) & (~below(lo) | below(sk));
+          for (int cc = 0; cc < 4; ++cc) {
+            const uint32_t seen = below(nvis - 32 * cc) &
+                                  (~below(lo_c - 32 * cc) | below(sink_c - 32 * cc));
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!(seen & (1u << c))) sr[32 * cc + c] = 0xff800000u;  // -inf
           }
-#pragma unroll
-          for (int c = 32 * cc; c < 32 * cc + 32; c += 8) {
-            mx0 = fmax3(mx0, f(c), f(c + 1));
-            mx1 = fmax3(mx1, f(c + 2), f(c + 3));
-            mx2 = fmax3(mx2, f(c + 4), f(c + 5));
-            mx3 = fmax3(mx3, f(c + 6), f(c + 7));
-          }
         }
-      } else {
-        if (!WIN && __any_sync(0xffffffffu, nvis < kPrefillBN)) {
+      } else if (__any_sync(0xffffffffu, nvis < kPrefillBN)) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= nvis) sr[c] = 0xff800000u;  // -inf
-        }
-        // four independent three-input max chains over the 128 scores
-        mx0 = f(0), mx1 = f(1), mx2 = f(2), mx3 = f(3);
-#pragma unroll
-        for (int c = 4; c < 124; c += 8) {
-          mx0 = fmax3(mx0, f(c), f(c + 1));
-          mx1 = fmax3(mx1, f(c + 2), f(c + 3));
-          mx2 = fmax3(mx2, f(c + 4), f(c + 5));
-          mx3 = fmax3(mx3, f(c + 6), f(c + 7));
-        }
-        mx0 = fmax3(mx0, f(124), f(125));
-        mx1 = fmax3(mx1, f(126), f(127));
+        for (int c = 0; c < 128; ++c)
+          if (c >= nvis) sr[c] = 0xff800000u;  // -inf
       }
+      // four independent three-input max chains over the 128 scores
+      float mx0 = f(0), mx1 = f(1), mx2 = f(2), mx3 = f(3);
+#pragma unroll
+      for (int c = 4; c < 124; c += 8) {
+        mx0 = fmax3(mx0, f(c), f(c + 1));
+        mx1 = fmax3(mx1, f(c + 2), f(c + 3));
+        mx2 = fmax3(mx2, f(c + 4), f(c + 5));
+        mx3 = fmax3(mx3, f(c + 6), f(c + 7));
+      }
+      mx0 = fmax3(mx0, f(124), f(125));
+      mx1 = fmax3(mx1, f(126), f(127));
       const float m_new = fmaxf(m_ref, fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
       // false while nothing visible has been seen (both -inf)
       const bool grow = m_new > m_ref + kRescaleLog2;
@@ -1021,36 +1003,8 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
       // fp32 exponentials and gives the log-sum-exp.
       float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
       float2 re0 = make_float2(0.f, 0.f), re1 = make_float2(0.f, 0.f);
-      // P in two halves of 64 keys (windowed edges: four chunks of 32), each
-      // stored to TMEM as soon as it is packed
-      if (WIN && edge) {
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t pk[16];
-          if (hid[cc]) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) pk[c] = 0u;
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-              const int e = cc * 32 + 2 * c;
-              const float2 x0 = ffma2(make_float2(f(e), f(e + 1)), sl2x2, negm);
-              const float2 x1 = ffma2(make_float2(f(e + 2), f(e + 3)), sl2x2, negm);
-              const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
-              const float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
-              pk[c] = pack_bf16x2(p0.x, p0.y);
-              pk[c + 1] = pack_bf16x2(p1.x, p1.y);
-              re0 = fadd2(re0, p0);
-              re1 = fadd2(re1, p1);
-              if (!ONES) {
-                add_bf16x2_to(rs0, pk[c]);
-                add_bf16x2_to(rs1, pk[c + 1]);
-              }
-            }
-          }
-          tmem_st16(tS + cc * 16, pk);
-        }
-      } else if (!FP8) {
+      // P in two halves of 64 keys, each stored to TMEM as soon as it is packed
+      if (!FP8) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t pk[32];
