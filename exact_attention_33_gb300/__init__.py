@@ -693,6 +693,36 @@ def _are(dtype, index, *pairs):
     return True
 
 
+_calls = None   # the extension module, or False where it has not been built
+
+# the library's functions that the extension calls, in its order
+_BOUND = ("fa_fwd_window", "fa_fwd_varlen_window", "fa_fwd_paged_window", "fa_decode_paged_window",
+          "fa_bwd_window", "fa_bwd_varlen_window", "fa_cache_append_fp8", "fa_decode_paged_fp8",
+          "fa_fwd_paged_fp8")
+
+
+def _short():
+    """The extension module (csrc/torch_calls.cpp) whose functions make a call
+    on the current stream when all its tensors are as they should be, and
+    return None otherwise; the functions here go on from there.  False where it
+    has not been built: the calls are then made from here, which takes longer."""
+    global _calls
+    if _calls is None:
+        lib = load_library()
+        _torch()   # its libraries first
+        path = os.path.join(_PKG, "_torch_calls.so")
+        if not os.path.exists(path):
+            _calls = False
+            return _calls
+        import importlib.util
+        spec = importlib.util.spec_from_file_location(__name__ + "._torch_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BOUND))
+        _calls = module
+    return _calls
+
+
 def _addr(t):
     """Device address of a tensor, 0 for None (the C arguments take an int)."""
     return 0 if t is None else t.data_ptr()
@@ -735,6 +765,11 @@ def fa_fwd_window(q, k, v, window, sinks=0, scale=None, out=None, lse=None, want
 
     Returns (out [B,N,H,d] bf16, lse [B,H,N] fp32 or None).
     """
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.fwd_window(q, k, v, window, sinks, scale, want_lse, out, lse)
+        if done is not None:
+            return done
     _check_bf16_cuda("q", q, 4)
     dev = q.device
     B, N, H, d = q.shape
@@ -762,6 +797,12 @@ def fa_fwd_varlen_window(q, k, v, cu_seqlens, max_seqlen, window, sinks=0, scale
 
     Returns (out [T,H,d] bf16, lse [H,T] fp32 or None).
     """
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.fwd_varlen_window(q, k, v, cu_seqlens, max_seqlen, window, sinks, scale, want_lse,
+                                       out, lse)
+        if done is not None:
+            return done
     _check_bf16_cuda("q", q, 3)
     dev = q.device
     T, H, d = q.shape
@@ -792,6 +833,13 @@ def fa_fwd_paged_window(q, k_pool, v_pool, block_table, ctx_lens, cu_seqlens_q, 
     """:func:`fa_fwd_paged` (causal) over each query's last ``window`` keys and
     the first ``sinks`` keys.  Blocks behind the window of a chunk's first
     query, but for those of the sinks, are not read and may have been freed."""
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.fwd_paged_window(q, k_pool, v_pool, block_table, ctx_lens, cu_seqlens_q,
+                                      max_seqlen_q, max_ctx_len, window, sinks, scale, want_lse, out,
+                                      lse)
+        if done is not None:
+            return done
     _check_bf16_cuda("q", q, 3)
     dev = q.device
     num_blocks, block_size, Hkv, dp = _check_pools(k_pool, v_pool, dev)
@@ -825,6 +873,12 @@ def fa_decode_paged_window(q, k_pool, v_pool, block_table, ctx_lens, max_ctx_len
                            stream=None):
     """:func:`fa_decode_paged` over the last ``window`` keys and the first
     ``sinks`` keys of each sequence; other blocks are not read."""
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.decode_paged_window(q, k_pool, v_pool, block_table, ctx_lens, max_ctx_len, window,
+                                         sinks, scale, want_lse, out, lse, workspace)
+        if done is not None:
+            return done
     _check_bf16_cuda("q", q, 3)
     dev = q.device
     batch, H, d = q.shape
@@ -884,6 +938,11 @@ def fa_bwd_window(q, k, v, out, lse, dout, window, sinks=0, scale=None, dq=None,
                   workspace=None, stream=None):
     """Gradient of :func:`fa_fwd_window`.  q, out, dout [B,N,H,d]; k, v
     [B,N,Hkv,d] bf16 CUDA tensors; lse [B,H,N] fp32.  Returns (dq, dk, dv)."""
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.bwd_window(q, k, v, out, lse, dout, window, sinks, scale, dq, dk, dv, workspace)
+        if done is not None:
+            return done
     _check_bwd(q, k, v, out, dout, 4)
     window, sinks = _check_window(window, sinks)
     dev, (B, N, H, d), Hkv = q.device, q.shape, k.shape[2]
@@ -907,6 +966,12 @@ def fa_bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window
     """Gradient of :func:`fa_fwd_varlen_window`.  q, out, dout [T,H,d]; k, v
     [T,Hkv,d] bf16 CUDA tensors; lse [H,T] fp32; cu_seqlens int32 [S+1].
     Returns (dq, dk, dv); rows outside every sequence are left as they were."""
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window, sinks,
+                                       scale, dq, dk, dv, workspace)
+        if done is not None:
+            return done
     _check_bwd(q, k, v, out, dout, 3)
     window, sinks = _check_window(window, sinks)
     dev, (T, H, d), Hkv = q.device, q.shape, k.shape[1]
@@ -980,6 +1045,12 @@ def fa_cache_append_fp8(k, v, k_pool, v_pool, k_scale, v_scale, block_table, ctx
     [batch], the new tokens counted; cu_seqlens int32 [batch+1]: sequence b's
     new tokens; max_new bounds their number per sequence.  Returns None.
     """
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.cache_append_fp8(k_pool, v_pool, k_scale, v_scale, k, v, block_table, ctx_lens,
+                                      cu_seqlens, max_new)
+        if done is not None:
+            return
     torch = _torch()
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise ValueError("k must be a CUDA tensor")
@@ -1009,6 +1080,12 @@ def fa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_le
     q [batch,H,d] bf16; pools and scales as in :func:`fa_cache_append_fp8`.
     Returns (out [batch,H,d] bf16, lse [batch,H] fp32 or None).
     """
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.decode_paged_fp8(k_pool, v_pool, k_scale, v_scale, q, block_table, ctx_lens,
+                                      max_ctx_len, window, sinks, scale, want_lse, out, lse, workspace)
+        if done is not None:
+            return done
     _check_bf16_cuda("q", q, 3)
     dev = q.device
     num_blocks, block_size, Hkv, dp = _check_cache(k_pool, v_pool, k_scale, v_scale, dev)
@@ -1044,6 +1121,13 @@ def fa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_lens,
     and cu_seqlens_q int32 [batch+1] as in :func:`fa_fwd_paged`.
     Returns (out [Tq,H,d] bf16, lse [H,Tq] fp32 or None).
     """
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.fwd_paged_fp8(k_pool, v_pool, k_scale, v_scale, q, block_table, ctx_lens,
+                                   cu_seqlens_q, max_seqlen_q, max_ctx_len, window, sinks, scale,
+                                   want_lse, out, lse)
+        if done is not None:
+            return done
     _check_bf16_cuda("q", q, 3)
     dev = q.device
     num_blocks, block_size, Hkv, dp = _check_cache(k_pool, v_pool, k_scale, v_scale, dev)

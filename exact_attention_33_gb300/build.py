@@ -26,6 +26,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libfa_checked.so")
+# the binding's short way for calls on torch tensors (csrc/torch_calls.cpp)
+TORCH_CALLS = os.path.join(PKG, "_torch_calls.so")
 SOURCES = ["fa_api.cu", "fa_cache_api.cu", "prefill.cu", "prefill_window.cu", "prefill_fp8cache.cu",
            "decode.cu", "decode_fp8.cu", "cache_append.cu", "backward.cu", "backward_window.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -41,6 +43,25 @@ def nvcc_path() -> str:
 def common_flags():
     return ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
                    "-I" + os.path.join(PKG, "..", "include"), "--expt-relaxed-constexpr"]
+
+
+def torch_calls_command(out):
+    """g++ command for the extension module: torch's and Python's headers, no
+    nvcc.  It needs no symbols of libfa.so (their addresses are bound at run
+    time)."""
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    lib = os.path.join(root, "lib")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", os.path.join(root, "include"),
+            "-isystem", sysconfig.get_paths()["include"],
+            "-isystem", os.path.join(cuda, "include"),
+            "-I", os.path.join(PKG, "..", "include"),
+            os.path.join(CSRC, "torch_calls.cpp"), "-o", out,
+            "-L", lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _run(cmd, verbose):
@@ -63,11 +84,13 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
     defines = ["-DFA_DEBUG_CHECKS"] if checked else []
     os.makedirs(build_dir, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    deps = srcs + [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))]
+    deps = srcs + [os.path.join(CSRC, h) for h in os.listdir(CSRC)
+                   if h.endswith((".h", ".cuh", ".cpp"))]
     inc = os.path.join(PKG, "..", "include")
     deps += [os.path.join(inc, h) for h in os.listdir(inc)]
-    if not force and os.path.exists(lib):
-        lib_t = os.path.getmtime(lib)
+    if not force and os.path.exists(lib) and os.path.exists(TORCH_CALLS):
+        lib_t = min(os.path.getmtime(lib), os.path.getmtime(TORCH_CALLS)) \
+            if not checked else os.path.getmtime(lib)
         if all(os.path.getmtime(d) <= lib_t for d in deps):
             return lib
 
@@ -81,8 +104,17 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
             print(out, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    def compile_torch_calls():
+        tmp = TORCH_CALLS + ".tmp"
+        _run(torch_calls_command(tmp), verbose)
+        os.replace(tmp, TORCH_CALLS)
+
+    with ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        # (one module serves both builds)
+        calls = None if checked and os.path.exists(TORCH_CALLS) else ex.submit(compile_torch_calls)
         objs = list(ex.map(compile_one, srcs))
+        if calls is not None:
+            calls.result()
     tmp = lib + ".tmp"
     _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs, verbose)
     os.replace(tmp, lib)
