@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   using L = BwdSumsLayout<D>;
   constexpr int S = L::kStages;
   constexpr int NB = L::kBufs;
+  pdl_launch_dependents();  // dK / dV sets itself up meanwhile
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1271,6 +1272,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // (what follows in the stream waits for this grid: not before dK / dV, which
+  // it overlaps, is complete too)
+  if constexpr (WIN) pdl_wait_primary();
 }
 
 // ----------------------------------------------------------------------- dK dV
@@ -1356,6 +1360,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (WIN) {
+    // launched as a programmatic dependent of the row sums, whose vectors and
+    // counters are complete from here on; dQ, which needs no more than they,
+    // may take over SMs as this kernel's CTAs leave them
+    pdl_wait_primary();
+    pdl_launch_dependents();
+  }
 
   // reads the slot of item m once its barrier phase is complete, then tells
   // the producer (one arrival per warp)
@@ -1799,21 +1810,38 @@ static cudaError_t launch_bwd_d(const CUtensorMap &tq, const CUtensorMap &tdo,
   const long long slices = WIN ? static_cast<long long>(p.B) * p.sink_tiles * p.sink_slices : 0;
   const unsigned grid_kv =
       static_cast<unsigned>(std::min<long long>((items + slices) * p.Hkv, p.num_ctas));
-  dkdv<<<grid_kv, kBwdThreads, L::kSmemAlloc, stream>>>(tq, tdo, tk, tv, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // persistent: one CTA per SM at most
+  const unsigned grid_q = static_cast<unsigned>(std::min<long long>(items * p.H, p.num_ctas));
   if constexpr (WIN) {
+    // each a programmatic dependent of the kernel before it
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kBwdThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(grid_kv);
+    cfg.dynamicSmemBytes = L::kSmemAlloc;
+    e = cudaLaunchKernelEx(&cfg, dkdv, tq, tdo, tk, tv, p);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(grid_q);
+    cfg.dynamicSmemBytes = BwdDqLayout<D>::kSmemAlloc;
+    e = cudaLaunchKernelEx(&cfg, dq, tq, tdo, tk, tv, p);
+    if (e != cudaSuccess) return e;
     if (p.sink_tiles > 0) {
       const long long rows =
           static_cast<long long>(p.B) * p.Hkv * std::min(p.sinks, p.sink_tiles * 128);
       bwd_sink_sum_kernel<D, VARLEN>
           <<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
       e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
     }
+    return e;
   }
-  // persistent: one CTA per SM at most
-  const unsigned grid_q = static_cast<unsigned>(std::min<long long>(items * p.H, p.num_ctas));
+  dkdv<<<grid_kv, kBwdThreads, L::kSmemAlloc, stream>>>(tq, tdo, tk, tv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   dq<<<grid_q, kBwdThreads, BwdDqLayout<D>::kSmemAlloc, stream>>>(tq, tdo, tk, tv, p);
   return cudaGetLastError();
 }
