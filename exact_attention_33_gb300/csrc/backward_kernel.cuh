@@ -766,32 +766,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         const int nvis = min(128, min(it.len, qi + 1) - kt * 128);
         const int lo_c = qi + 1 - p.window - kt * 128, sink_c = p.sinks - kt * 128;
-        const uint32_t tS = tmem + buf * 256 + lane_off;
+        const uint32_t tS = tmem + buf * 256 + hf * 64 + lane_off;
+        // the half's weights, then its products with dP: each one load of 64
+        // columns; a half that no row of the warp sees adds nothing
+        uint32_t bits[2];
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 32 * (2 * hf + cc);
-          const uint32_t bits = low_bits(nvis - c) & (~low_bits(lo_c - c) | low_bits(sink_c - c));
-          // a chunk that no row of the warp sees adds nothing
-          if (__all_sync(0xffffffffu, bits == 0u)) continue;
-          const bool part = __any_sync(0xffffffffu, ~bits != 0u);
-          uint32_t sv[32], dp[32];
-          tmem_ld32_wait(tS + c, sv);
-          tmem_ld32_wait(tS + 128 + c, dp);
+          bits[cc] = low_bits(nvis - c) & (~low_bits(lo_c - c) | low_bits(sink_c - c));
+        }
+        if (__any_sync(0xffffffffu, (bits[0] | bits[1]) != 0u)) {
+          uint32_t w[64], dp[64];
+          tmem_ld64_wait(tS, w);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float2 x0 =
-                ffma2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sl2x2, nl2);
-            const float2 x1 = ffma2(
-                make_float2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sl2x2, nl2);
-            float w[4] = {ex2(x0.x), ex2(x0.y), ex2(x1.x), ex2(x1.y)};
-            if (part) {
+          for (int e = 0; e < 64; e += 2) {
+            const float2 x =
+                ffma2(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), sl2x2, nl2);
+            w[e] = __float_as_uint(ex2(x.x));
+            w[e + 1] = __float_as_uint(ex2(x.y));
+          }
+          if (__any_sync(0xffffffffu, (bits[0] & bits[1]) != ~0u)) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                if (!(bits & (1u << (e + y)))) w[y] = 0.f;
-            }
-            d0 = ffma2(make_float2(w[0], w[1]),
+            for (int e = 0; e < 64; ++e)
+              if (!(bits[e >> 5] & (1u << (e & 31)))) w[e] = 0u;
+          }
+          tmem_ld64_wait(tS + 128, dp);
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            d0 = ffma2(make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])),
                        make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), d0);
-            d1 = ffma2(make_float2(w[2], w[3]),
+            d1 = ffma2(make_float2(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3])),
                        make_float2(__uint_as_float(dp[e + 2]), __uint_as_float(dp[e + 3])), d1);
           }
         }
@@ -1179,6 +1183,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // (windowed: kept in fp32, so that dS is rounded once)
         uint32_t pp[WIN ? 64 : 32];
         bool hid[2] = {false, false};  // windowed: chunks that no row of the warp sees
+        uint32_t s64[64];              // and both chunks in one load
+        if constexpr (WIN) tmem_ld64_wait(tS + hf * 64, s64);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
@@ -1190,7 +1196,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (hid[cc]) continue;
           }
           uint32_t sv[32];
-          tmem_ld32_wait(tS + c * 32, sv);
+          if constexpr (WIN) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sv[e] = s64[cc * 32 + e];
+          } else {
+            tmem_ld32_wait(tS + c * 32, sv);
+          }
           const bool part = WIN ? __any_sync(0xffffffffu, ~bits != 0u) : c * 32 + 32 > nvis;
           auto seen = [&](int k) { return WIN ? ((bits >> (k & 31)) & 1u) != 0u : k < nvis; };
 #pragma unroll
@@ -1219,6 +1230,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // dS = P (dP - D), written over this half's dP columns (dP_j in the
         // buffer of key tile j's parity)
         const uint32_t tP = tmem + ((g & 1) ? 384 : 128) + lane_off;
+        if constexpr (WIN) tmem_ld64_wait(tP + hf * 64, s64);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
@@ -1228,7 +1240,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             continue;
           }
           uint32_t dp[32], pk[16];
-          tmem_ld32_wait(tP + c * 32, dp);
+          if constexpr (WIN) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) dp[e] = s64[cc * 32 + e];
+          } else {
+            tmem_ld32_wait(tP + c * 32, dp);
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float2 w = WIN ? make_float2(__uint_as_float(pp[(WIN ? cc * 32 + e : 0)]),
@@ -1620,6 +1637,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         uint32_t pp[32];
         float pf[WIN ? 64 : 1];
         bool hid[2] = {false, false};
+        uint32_t s64[64];  // windowed: both chunks in one load
+        if constexpr (WIN) tmem_ld64_wait(tS + hf * 64, s64);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
@@ -1634,7 +1653,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
           }
           uint32_t sv[32];
-          tmem_ld32_wait(tS + c * 32, sv);
+          if constexpr (WIN) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sv[e] = s64[cc * 32 + e];
+          } else {
+            tmem_ld32_wait(tS + c * 32, sv);
+          }
           const bool part = WIN ? __any_sync(0xffffffffu, ~bits != 0u) : c * 32 < qfirst;
           auto seen = [&](int q0) { return WIN ? ((bits >> (q0 & 31)) & 1u) != 0u : q0 >= qfirst; };
 #pragma unroll
@@ -1675,6 +1699,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
         tc_fence_after();
         // dS^T = P^T (dP^T - D[q]), stored over this half's dP^T columns
+        if constexpr (WIN) tmem_ld64_wait(tP + hf * 64, s64);
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const int c = 2 * hf + cc;
@@ -1684,7 +1709,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             continue;
           }
           uint32_t dp[32], pd[16];
-          tmem_ld32_wait(tP + c * 32, dp);
+          if constexpr (WIN) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) dp[e] = s64[cc * 32 + e];
+          } else {
+            tmem_ld32_wait(tP + c * 32, dp);
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const int q0 = c * 32 + e;
