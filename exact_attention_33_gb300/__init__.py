@@ -782,6 +782,8 @@ def fa_fwd_window(q, k, v, window, sinks=0, scale=None, out=None, lse=None, want
     window, sinks = _check_window(window, sinks)
     with _Launch(stream, dev) as handle:
         out, lse = _results(q, (B, H, N), out, lse, want_lse)
+        if not B * N:   # (an empty tensor has no address)
+            return out, lse
         rc = load_library().fa_fwd_window(_addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), B, H,
                                           Hkv, N, d, _scale(scale, d), window, sinks,
                                           handle)
@@ -818,6 +820,8 @@ def fa_fwd_varlen_window(q, k, v, cu_seqlens, max_seqlen, window, sinks=0, scale
     window, sinks = _check_window(window, sinks)
     with _Launch(stream, dev) as handle:
         out, lse = _results(q, (H, T), out, lse, want_lse)
+        if not T:
+            return out, lse
         rc = load_library().fa_fwd_varlen_window(
             _addr(q), _addr(k), _addr(v), _addr(out), _addr(lse), _addr(cu_seqlens),
             cu_seqlens.numel() - 1, T, int(max_seqlen), H, Hkv, d, _scale(scale, d), window, sinks,
@@ -850,6 +854,8 @@ def fa_fwd_paged_window(q, k_pool, v_pool, block_table, ctx_lens, cu_seqlens_q, 
         raise ValueError("the pools' head size must match q")
     with _Launch(stream, dev) as handle:
         out, lse = _results(q, (H, Tq), out, lse, want_lse)
+        if not Tq:
+            return out, lse
         rc = load_library().fa_fwd_paged_window(
             _addr(q), _addr(k_pool), _addr(v_pool), _addr(block_table), block_table.shape[1],
             _addr(ctx_lens), _addr(cu_seqlens_q), batch, Tq, int(max_seqlen_q), int(max_ctx_len), H,
@@ -894,6 +900,8 @@ def fa_decode_paged_window(q, k_pool, v_pool, block_table, ctx_lens, max_ctx_len
             batch, H, Hkv, d, max_ctx_len, window, sinks, block_size)
         workspace = _workspace(workspace, need, dev, 256, zero=True)
         out, lse = _results(q, (batch, H), out, lse, want_lse)
+        if not batch:
+            return out, lse
         rc = load_library().fa_decode_paged_window(
             _addr(q), _addr(k_pool), _addr(v_pool), _addr(block_table), block_table.shape[1],
             _addr(ctx_lens), int(max_ctx_len), batch, H, Hkv, d, block_size, num_blocks,
@@ -949,6 +957,8 @@ def fa_bwd_window(q, k, v, out, lse, dout, window, sinks=0, scale=None, dq=None,
     _check_tensor("lse", lse, (B, H, N), _torch().float32, dev)
     with _Launch(stream, dev) as handle:
         dq, dk, dv = _grads(q, k, v, dq, dk, dv)
+        if not B * N:
+            return dq, dk, dv
         need = 0 if workspace is not None else fa_bwd_window_workspace_size(
             B, H, Hkv, N, d, window, sinks)
         workspace = _workspace(workspace, need, dev)
@@ -982,6 +992,8 @@ def fa_bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window
     S = cu_seqlens.numel() - 1
     with _Launch(stream, dev) as handle:
         dq, dk, dv = _grads(q, k, v, dq, dk, dv)
+        if not T:
+            return dq, dk, dv
         need = 0 if workspace is not None else fa_bwd_window_workspace_size(
             S, H, Hkv, min(int(max_seqlen), T), d, window, sinks)
         workspace = _workspace(workspace, need, dev)
@@ -1061,6 +1073,8 @@ def fa_cache_append_fp8(k, v, k_pool, v_pool, k_scale, v_scale, block_table, ctx
     if v.shape[0] != k.shape[0] or v.device != dev:
         raise ValueError("k and v must have the same tokens on one device")
     batch = _check_sequences(block_table, ctx_lens, cu_seqlens, "cu_seqlens", dev)
+    if not k.shape[0]:
+        return
     with _Launch(stream, dev) as handle:
         rc = load_library().fa_cache_append_fp8(
             _addr(k), _addr(v), k_stride, v_stride, _addr(k_pool), _addr(v_pool), _addr(k_scale),
@@ -1101,6 +1115,8 @@ def fa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_le
                                                    block_size)
         workspace = _workspace(workspace, need, dev, 256, zero=True)
         out, lse = _results(q, (batch, H), out, lse, want_lse)
+        if not batch:
+            return out, lse
         rc = load_library().fa_decode_paged_fp8(
             _addr(q), _addr(k_pool), _addr(v_pool), _addr(k_scale), _addr(v_scale), _addr(block_table),
             block_table.shape[1], _addr(ctx_lens), int(max_ctx_len), batch, H, Hkv, d, block_size,
@@ -1138,6 +1154,8 @@ def fa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_lens,
         raise ValueError("the pools' head size must match q")
     with _Launch(stream, dev) as handle:
         out, lse = _results(q, (H, Tq), out, lse, want_lse)
+        if not Tq:
+            return out, lse
         rc = load_library().fa_fwd_paged_fp8(
             _addr(q), _addr(k_pool), _addr(v_pool), _addr(k_scale), _addr(v_scale), _addr(block_table),
             block_table.shape[1], _addr(ctx_lens), _addr(cu_seqlens_q), batch, Tq,

@@ -331,6 +331,8 @@ def check_chunks(out, lse, q, c, ctx, cu, window, sinks, rounded=False):
     H, Hkv = q.shape[1], c.pool["k"].shape[2]
     for b, n in enumerate(ctx):
         a, e = int(cu[b]), int(cu[b + 1])
+        if a == e:
+            continue
         k, v = c.rows("k", b, n), c.rows("v", b, n)
         if rounded:
             k, v = k.to(torch.bfloat16).double(), v.to(torch.bfloat16).double()
@@ -339,6 +341,21 @@ def check_chunks(out, lse, q, c, ctx, cu, window, sinks, rounded=False):
             o, l, tol = ref.forward(q[a:e, h].double(), k[:, kv], v[:, kv], window, sinks)
             ref.assert_within(out[a:e, h], o, tol, f"seq {b} head {h}")
             ref.assert_lse(lse[h, a:e], l, f"seq {b} head {h}")
+
+
+@pytest.mark.parametrize("batch", [1, 32, 33])
+def test_chunks_of_many_sequences(fa, batch):
+    """Each sequence gets its own rows whatever order the sequences start in:
+    ascending, equal and empty contexts, up to and past a warp's 32."""
+    H, Hkv, d = 2, 1, 64
+    ctx = [40] if batch == 1 else [(7 * b) // 3 * 5 for b in range(batch)]
+    new = [min(n, 1 + b % 4) for b, n in enumerate(ctx)]
+    c = Cache(ctx, Hkv, d, seed=95 + batch)
+    cu = cu_of(new)
+    q = bf16(cr.bf16(np.random.default_rng(batch), cu[-1], H, d))
+    out, lse = fa.fa_fwd_paged_fp8(q, *c.args(), dev(np.int32(ctx)), dev(cu), max(new), max(ctx))
+    assert_device_clean()
+    check_chunks(out, lse, q, c, ctx, cu, 0, 0)
 
 
 def test_chunks_with_any_scale(fa):
@@ -488,3 +505,52 @@ def test_binding_refuses(fa):
         fa.fa_cache_append_fp8(k[:1].expand(40, 2, 64), k, *c.args(), lens, cu, 40)
     with pytest.raises(ValueError):
         fa.fa_cache_append_fp8(k, k, *c.args(), lens, cu[:1], 40)
+
+
+def test_no_rows(fa):
+    """A step without tokens does nothing."""
+    c = Cache([40], 2, 64, seed=1)
+    q, k, lens = bf16(np.zeros((0, 4, 64))), bf16(np.zeros((0, 2, 64))), dev(np.int32([40]))
+    cu = dev(np.int32([0, 0]))
+    fa.fa_cache_append_fp8(k, k, *c.args(), lens, cu, 0)
+    c.check()
+    out, lse = fa.fa_fwd_paged_fp8(q, *c.args(), lens, cu, 0, 40)
+    assert out.shape == q.shape and lse.shape == (4, 0)
+    out, lse = fa.fa_decode_paged_fp8(q, *c.args()[:4], c.dtable[:0], lens[:0], 40)
+    assert out.shape == q.shape and lse.shape == (0, 4)
+    assert_device_clean()
+
+
+def test_blocks_past_32_bits(fa):
+    """Blocks whose codes lie past 2^31 and 2^32 bytes of the pool."""
+    torch = torch_mod()
+    H, Hkv, d, n, new = 16, 8, 128, 155, 30
+    c = Cache([n], Hkv, d, seed=130)
+    near = c.table.copy()
+    base = (1 << 32) // (16 * Hkv * d) - 5   # the ten blocks lie on both sides of 2^32
+    size = base + 1 + int(near.max())
+    for x in "kv":
+        pool = torch.zeros(size, 16, Hkv, d, dtype=torch.uint8, device="cuda")
+        pool[base:] = c.dpool[x][:size - base]
+        scale = torch.ones(size, Hkv, dtype=torch.float32, device="cuda")
+        scale[base:] = c.dscale[x][:size - base]
+        c.dpool[x], c.dscale[x] = pool, scale
+    c.dtable = dev((near + base).astype(np.int32))
+    rng = np.random.default_rng(131)
+    k, v = (cr.bf16(rng, new, Hkv, d) for _ in "kv")
+    c.append(fa, k, v, [n], [new])
+    far = c.dpool, c.dscale
+    c.dpool = {x: far[0][x][base:] for x in "kv"}
+    c.dscale = {x: far[1][x][base:] for x in "kv"}
+    for x in "kv":   # (the twin's blocks behind the table's are not in the pool)
+        c.pool[x], c.scale[x] = c.pool[x][:size - base], c.scale[x][:size - base]
+    c.check("far blocks")
+    assert not any(int(far[0][x][:base].count_nonzero()) for x in "kv")
+    c.dpool, c.dscale = far
+    q = bf16(cr.bf16(rng, new, H, d))
+    lens, cu = dev(np.int32([n])), dev(np.int32([0, new]))
+    out, lse = fa.fa_fwd_paged_fp8(q, *c.args(), lens, cu, new, n)
+    check_chunks(out, lse, q, c, [n], [0, new], 0, 0)
+    out, lse = fa.fa_decode_paged_fp8(q[-1:].contiguous(), *c.args(), lens, n)
+    check_decode(out, lse, q[-1:], c, [n], 0, 0, "far blocks")
+    assert_device_clean()

@@ -392,3 +392,54 @@ def test_binding_refuses(fa):
                          workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         fa.fa_bwd_window(q, k, k, out, lse[:, :, :4], out, 4)
+
+
+def test_no_rows(fa):
+    """Empty batches and prompts are calls that do nothing."""
+    torch = torch_mod()
+    for shape in ((0, 5), (3, 0)):
+        q, k = normal(1, *shape, 4, 64), normal(2, *shape, 2, 64)
+        out, lse = fa.fa_fwd_window(q, k, k, 4)
+        assert out.shape == q.shape and lse.shape == (shape[0], 4, shape[1])
+        dq, dk, dv = fa.fa_bwd_window(q, k, k, out, lse, q, 4)
+        assert dq.shape == q.shape and dk.shape == k.shape and dv.shape == k.shape
+    q, k, cu = normal(1, 0, 4, 64), normal(2, 0, 2, 64), i32([0, 0])
+    out, lse = fa.fa_fwd_varlen_window(q, k, k, cu, 0, 4, 1)
+    assert out.shape == q.shape and lse.shape == (4, 0)
+    assert fa.fa_bwd_varlen_window(q, k, k, out, lse, q, cu, 0, 4, 1)[1].shape == k.shape
+    pool, table = normal(3, 4, 16, 2, 64), i32([[0, 1]])
+    out, lse = fa.fa_fwd_paged_window(q, pool, pool, table, i32([20]), cu, 0, 20, 4)
+    assert out.shape == q.shape and lse.shape == (4, 0)
+    out, lse = fa.fa_decode_paged_window(q, pool, pool, table[:0], i32([]), 20, 4)
+    assert out.shape == q.shape and lse.shape == (0, 4)
+    assert_device_clean()
+
+
+def test_rows_past_32_bits(fa):
+    """Rows of q, out and their gradients whose offsets pass 2^31 elements, and
+    cache blocks whose offsets do."""
+    torch = torch_mod()
+    H, Hkv, d, window, sinks = 128, 1, 128, 70, 3
+    lens = [(1 << 31) // (H * d) + 5, 260]   # the second sequence lies past 2^31
+    cu = cu_of(lens)
+    q = normal(120, 4096, H, d).repeat(cu[-1] // 4096 + 1, 1, 1)[:cu[-1]]
+    k, v = normal(121, cu[-1], Hkv, d), normal(122, cu[-1], Hkv, d)
+    args = (i32(cu), max(lens), window, sinks)
+    out, lse = fa.fa_fwd_varlen_window(q, k, v, *args)
+    a = cu[1]
+    check_rows(out[a:, ::32], lse[::32, a:], q[a:, ::32], k[a:], v[a:], window, sinks, "far rows")
+    g = q.flip(0)
+    dq, dk, dv = fa.fa_bwd_varlen_window(q, k, v, out, lse, g, *args)
+    check_gradient(dq[a:], dk[a:], dv[a:], q[a:], k[a:], v[a:], g[a:], window, sinks, "far rows")
+    del q, out, g, dq
+    blocks = (1 << 31) // (16 * 8 * d) + 40
+    pool = torch.zeros(blocks, 16, 8, d, dtype=torch.bfloat16, device="cuda")
+    pool[-20:] = normal(123, 20, 16, 8, d)
+    table, n = i32([list(range(blocks - 10, blocks))]), 155
+    rows = pool[-10:].reshape(-1, 8, d)[:n]
+    tok = normal(124, 30, 16, d)
+    o, l = fa.fa_decode_paged_window(tok[-1:], pool, pool, table, i32([n]), n, 100, 2)
+    check_rows(o, l[0][:, None], tok[-1:], rows, rows, 100, 2, "far blocks, token")
+    o, l = fa.fa_fwd_paged_window(tok, pool, pool, table, i32([n]), i32([0, 30]), 30, n, 100, 2)
+    check_rows(o, l, tok, rows, rows, 100, 2, "far blocks, chunk")
+    assert_device_clean()
