@@ -83,11 +83,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
-// 2^e with e clamped to the normal range
-__device__ __forceinline__ float pow2_clamped(int e) {
-  return __int_as_float((min(max(e, -126), 127) + 127) << 23);
-}
-
 }  // namespace
 
 template <int D, int NT>

@@ -192,8 +192,8 @@ int fa_fwd_paged_fp8(const void *q, const void *k_pool, const void *v_pool, cons
   CUtensorMap tq, tk, tv, to;
   const long long tokens = static_cast<long long>(num_blocks) * block_size;
   int rc = make_map(&tq, q, d, H, total_q, 1, kPrefillBM);
-  // (the widening warps read the codes themselves: rows as they are)
-  if (rc == FA_OK) rc = make_pool_map(&tk, k_pool, d, Hkv, tokens, kDecodeBlock, 1, false);
+  // (K's codes are MMA operands; V's are read by the widening warps: rows as they are)
+  if (rc == FA_OK) rc = make_pool_map(&tk, k_pool, d, Hkv, tokens, kDecodeBlock, 1);
   if (rc == FA_OK) rc = make_pool_map(&tv, v_pool, d, Hkv, tokens, kDecodeBlock, 1, false);
   if (rc == FA_OK) rc = make_map(&to, out, d, H, total_q, 1, kPrefillBM);
   if (rc != FA_OK) return rc;

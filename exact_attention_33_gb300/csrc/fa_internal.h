@@ -43,13 +43,17 @@ constexpr int kPrefill1SoftmaxRegs = 168;
 constexpr int kPrefill1CtlRegs = 88;
 static_assert(128 * kPrefill1SoftmaxRegs + 128 * kPrefill1CtlRegs <= 256 * kPrefill1LaunchRegs,
               "one-tile prefill register split exceeds the launch allocation");
-static_assert(256 * kPrefill1SoftmaxRegs + 256 * kPrefill1CtlRegs <= 512 * kPrefill1LaunchRegs,
+// Two tiles over an 8-bit cache: 512 threads of 128 (168 / 88 spilled 100 bytes
+// of the softmax at d = 128, 192 / 64 as many of the other warps at d = 64).
+constexpr int kPrefill8SoftmaxRegs = 176;
+constexpr int kPrefill8CtlRegs = 80;
+static_assert(256 * kPrefill8SoftmaxRegs + 256 * kPrefill8CtlRegs <= 512 * kPrefill1LaunchRegs,
               "8-bit cache prefill register split exceeds the launch allocation");
 
 // Shape of a prefill CTA with QT query tiles.  Over an 8-bit cache (KV8) two
 // query tiles take 512 threads: the softmax warps, a warpgroup of the MMA and
 // the copies (warp 11 idles), and the four warps from kConvWarp on that
-// widen keys and values; the register split is that of the one-tile kernel.
+// widen values.
 template <int QT, bool KV8 = false>
 struct PrefillShape {
   static_assert(QT == 1 || QT == 2, "one or two query tiles per CTA");

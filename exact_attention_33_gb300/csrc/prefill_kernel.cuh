@@ -72,11 +72,10 @@ struct PrefillLayout {
 #define FA_PREFILL_STAGES_V128 2
 #endif
   // With one query tile per CTA two CTAs share an SM's shared memory, so
-  // 32 KiB tiles get one stage each.  Over an 8-bit cache a tile of codes of
-  // each of K and V is staged too, at the cost of a third K stage.
+  // 32 KiB tiles get one stage each.
   static constexpr int kStagesK =
       (QT == 1) ? ((kTileBytes == 32768) ? 1 : 2)
-                : ((kTileBytes == 32768) ? (KV8 ? 2 : FA_PREFILL_STAGES_K128) : 5);
+                : ((kTileBytes == 32768) ? FA_PREFILL_STAGES_K128 : 5);
   static constexpr int kStagesV =
       (QT == 1) ? ((kTileBytes == 32768) ? 1 : 2) : ((kTileBytes == 32768) ? FA_PREFILL_STAGES_V128 : 5);
   // Row sums on the tensor cores (d = 64): the P V product also multiplies
@@ -88,16 +87,27 @@ struct PrefillLayout {
   static constexpr int kOCols = kOnes ? D + 16 : D;  // TMEM columns of O
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + QT * kTileBytes;
-  static constexpr int kV = kK + kStagesK * kTileBytes;
+  // Over an 8-bit cache K stays e4m3 codes (rows of D bytes, in the swizzle of
+  // that width), and so do the two terms of a Q tile, one behind the other.
+  static constexpr int kKStage = KV8 ? 128 * D : kTileBytes;
+  static constexpr int kK8Swz = (D == 128) ? 128 : 64;
+  static constexpr int kV = kK + kStagesK * kKStage;
   static constexpr int kOnesOff = kV + kStagesV * kTileBytes;  // 128 x 64 bf16 ones (one chunk)
-  static constexpr int kCodes = kOnesOff + (kOnes ? kChunkBytes : 0);  // e4m3 codes of K, then V
+  static constexpr int kCodes = kOnesOff + (kOnes ? kChunkBytes : 0);  // two tiles of V's codes
   static constexpr int kCodeBytes = KV8 ? 128 * D : 0;                 // one tile of codes
-  static constexpr int kBar = kCodes + 2 * kCodeBytes;
+  // Block scales of K, 8 floats a key tile, written beside the tile's copies
+  // and read by the softmax.  The copies of tile t wait for the products of
+  // tile t - kStagesK, which follow the softmax of the tile before it: so
+  // kStagesK + 1 slots would do.
+  static constexpr int kScaleSlots = 8;
+  static_assert(!KV8 || kStagesK + 1 <= kScaleSlots, "slots of block scales");
+  static constexpr int kScales = kCodes + 2 * kCodeBytes;
+  static constexpr int kBar = kScales + (KV8 ? kScaleSlots * 8 * 4 : 0);
   // q_full, k_full[SK], k_empty[SK], v_full[SV], s_full[2], p_full[2],
   // o_done[2], drain, v_empty[SV], and over an 8-bit cache c_full[2],
-  // c_empty[2] of the staged codes.  A V stage is released as soon as the
-  // P V products of its key tile are done.
-  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7 + (KV8 ? 4 : 0);
+  // c_empty[2] of V's staged codes and q_ready.  A V stage is released as soon
+  // as the P V products of its key tile are done.
+  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7 + (KV8 ? 5 : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kSmemAlloc = kBytes + 1024;     // base is aligned up to 1024 in-kernel
@@ -176,6 +186,58 @@ __device__ __forceinline__ bool varlen_compact_item(const PrefillParams &p, int 
   return false;
 }
 
+// Row `row` of a bf16 Q tile (128 rows of D values as swizzled 128-byte rows
+// of 64) becomes two 8-bit terms, tiles of 128 rows of D codes in the swizzle of
+// that width, one behind the other in the tile's place: x 2^e = h + l with the
+// row's largest magnitude in [2^7, 2^8).  h (e4m3) holds the upper 4 of a
+// bf16's 8 significant bits; what is left is at most half a step of h and a
+// multiple of 2^-4 of that step, 3 significant bits, which l (e5m2) holds
+// exactly.  Values below 2^-6, where h's step stays 2^-9, leave up to 2^-10
+// with more bits than l's 3: off by at most 2^-14, 2^-21 of the row's largest
+// magnitude.  A row with an infinity or a NaN becomes NaN (an infinite score
+// has no softmax).  The tile's 128 threads call this together (at d = 64 a row
+// of codes lies in other rows' values; they meet at barrier `bar`).  Returns
+// 2^-e.
+template <int D>
+__device__ __forceinline__ float split_q_row(uint8_t *tile, int row, int bar) {
+  constexpr int kUnits = D / 8;   // 16-byte units of a bf16 row
+  uint4 raw[kUnits];
+  uint32_t top = 0;  // largest magnitude, bf16 bits
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) {
+    raw[u] = *reinterpret_cast<const uint4 *>(tile + (u / 8) * 16384 + row * 128 +
+                                              (((u % 8) ^ (row & 7)) << 4));
+    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) top = max(top, max(w[x] & 0x7FFFu, (w[x] >> 16) & 0x7FFFu));
+  }
+  const int ex = static_cast<int>(top >> 7);
+  const int e = (ex == 0 || ex == 255) ? 0 : 7 - (ex - 127);
+  // (two factors: the power itself may exceed fp32's)
+  const float f0 = pow2_clamped(e / 2), f1 = pow2_clamped(e - e / 2);
+  if (D == 64) named_bar_sync(bar, 128);
+#pragma unroll
+  for (int u = 0; u < kUnits / 2; ++u) {
+    const uint32_t w[8] = {raw[2 * u].x,     raw[2 * u].y,     raw[2 * u].z,     raw[2 * u].w,
+                           raw[2 * u + 1].x, raw[2 * u + 1].y, raw[2 * u + 1].z, raw[2 * u + 1].w};
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float2 a = bf16x2_to_float2(w[2 * x]), b = bf16x2_to_float2(w[2 * x + 1]);
+      const float v0 = a.x * f0 * f1, v1 = a.y * f0 * f1, v2 = b.x * f0 * f1, v3 = b.y * f0 * f1;
+      h[x] = pack_e4m3x4(v0, v1, v2, v3);
+      const float2 h0 = e4m3x2_to_float2(h[x]), h1 = e4m3x2_to_float2(h[x] >> 16);
+      l[x] = pack_e5m2x4(v0 - h0.x, v1 - h0.y, v2 - h1.x, v3 - h1.y);
+      if (ex == 255) h[x] = l[x] = 0x7F7F7F7Fu;
+    }
+    const int at = (D == 128) ? row * 128 + ((u ^ (row & 7)) << 4)
+                              : row * 64 + ((u ^ ((row >> 1) & 3)) << 4);
+    *reinterpret_cast<uint4 *>(tile + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(tile + 128 * D + at) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+  return pow2_clamped(-e);
+}
+
 // The sequence with the rank-th longest context of p.B <= 32 (equal ones in
 // order), for an order of the work items that starts the longest first (all
 // lanes active).
@@ -198,17 +260,18 @@ __device__ __forceinline__ int longest_context(const PrefillParams &p, int rank)
 // the window of its first row on, and leaves the ones between out.
 //
 // KV8 (paged kinds, windowed): the cache holds e4m3 codes with a scale per
-// block and KV head.  Warps 9 and 10 copy the codes of a K and a V tile into
-// staging buffers; warps 12-15 multiply them by their block's scale and store
-// bf16 rows in the swizzled layout that the MMAs read, handing each buffer
-// back at once, so the next tile's codes arrive while this one is multiplied.
-// Bound by these warps' conversions and shared-memory traffic (codes in and
-// out, bf16 rows in, beside the MMAs' operand reads): 4 x 512 rows over 8192
-// keys, 32 / 8 heads of d = 128 take 315 us against 206 us over a bf16 cache
-// (264 us with the conversions' arithmetic left out).  Codes loaded straight
-// into registers, 32 or 64 of a thread's 88 in flight, took 470 to 620 us.
-// Widening is exact for scales that are powers of two, else one bf16 rounding
-// of K and V.
+// block and KV head.  K's codes are operands as they are: S = (Qh + Ql) K^T
+// with Q in two 8-bit terms (split_q_row), at twice bf16's rate for twice the
+// products, and the scores are multiplied by their block's scale.  V would need
+// weights of 3 mantissa bits, so it is widened: warp 10 copies its codes into
+// staging buffers, and warps 12-15 multiply them by their block's scale (exact
+// for powers of two, else one bf16 rounding) and store bf16 rows in the
+// swizzled layout that the MMAs read.  4 x 512 rows over 2196 to 8269 keys, 32
+// / 8 heads of d = 128 take 226 us; with K widened like V 257 us, bound by
+// those warps' conversions and shared-memory traffic; without V's arithmetic
+// 226, so now the softmax and the products set the pace, as over a bf16 cache,
+// and the longest CTAs' 112 steps against 85 on average.  (Codes loaded
+// straight into registers, 32 or 64 of a thread's 88 in flight: 470 to 620 us.)
 template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false,
           bool KV8 = false>
 __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<QT, KV8>::kMinBlocks)
@@ -264,8 +327,8 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     // Few sequences make few rounds of CTAs, and a long one that starts last is
     // waited for: sequences of an 8-bit cache (whose window mostly reaches over
     // all of them) go longest first.  4 x 512 rows over 3469 / 4020 / 2381 / 7444
-    // keys take 169 us against 213 us in their own order, over 8035 / 6236 /
-    // 8269 / 2196 keys 257 against 268, 16 sequences 691 against 730.  Past one
+    // keys take 156 us against 188 us in their own order, over 8035 / 6236 /
+    // 8269 / 2196 keys 226 against 234, 16 sequences 613 against 645.  Past one
     // warp's 32 sequences the rounds are many and the order matters little.
     if constexpr (KV8)
       if (p.B <= 32) unit_x = longest_context(p, unit_x);
@@ -383,8 +446,9 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
   uint64_t *o_done = p_full + 2;
   uint64_t *drain = o_done + 2;
   uint64_t *v_empty = drain + 1;  // V-stage releases
-  uint64_t *c_full = v_empty + SV;  // 8-bit caches: codes of K [0] and V [1] staged
+  uint64_t *c_full = v_empty + SV;  // 8-bit caches: codes of V staged
   uint64_t *c_empty = c_full + 2;   // and read by the four widening warps
+  uint64_t *q_ready = c_empty + 2;  // 8-bit caches: Q in two 8-bit terms
   constexpr bool ONES = L::kOnes;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
@@ -404,7 +468,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     // (and K(0)) right away; the other warps wait for it at __syncthreads.
     mbar_init(q_full, 1);
     for (int s = 0; s < SK; ++s) {
-      mbar_init(&k_full[s], KV8 ? 128 : 1);
+      mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
     }
     for (int s = 0; s < SV; ++s) {
@@ -422,6 +486,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
         mbar_init(&c_full[i], 1);
         mbar_init(&c_empty[i], 4);
       }
+      mbar_init(q_ready, live1 ? 256 : 128);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -474,13 +539,13 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
   if (warp >= Sh::kSoftmaxWarps) {
   // One query tile per CTA: this warpgroup (MMA, TMA, two idle warps) hands
   // registers to the softmax warpgroup.
-  if constexpr (Sh::kSplitRegs) setmaxnreg_dec<kPrefill1CtlRegs>();
+  if constexpr (Sh::kSplitRegs) setmaxnreg_dec<KV8 ? kPrefill8CtlRegs : kPrefill1CtlRegs>();
   const bool k_producer = warp == Sh::kTmaWarp;  // else the V producer
   constexpr int kTileBlocks = kPrefillBN / kDecodeBlock;  // cache blocks of a key tile
   constexpr int kIdTiles = 32 / kTileBlocks;              // key tiles whose ids a warp holds
   // Physical block of lane % 8 of key tile w + lane / 8 (8-bit caches): -1
-  // past this CTA's tiles or the context, for a block that no row of the CTA
-  // sees (its id is not looked at: it may be freed), and for a bad id.
+  // past this CTA's tiles or the context and for a block that no row of the CTA
+  // sees (its id is not looked at: it may be freed), -2 for a bad id.
   auto cache_block = [&](int w, bool report) -> int {
     const int blk = key_tile(w + lane / kTileBlocks) * kTileBlocks + lane % kTileBlocks;
     if (w + lane / kTileBlocks >= n_kv || blk * kDecodeBlock >= kv_len) return -1;
@@ -490,42 +555,65 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     const int id = p.block_table[at];
     if (id >= 0 && id < p.num_blocks) return id;
     if (report) raise_status(p.status, FA_DEV_BAD_BLOCK);
-    return -1;
+    return -2;
   };
   if (KV8 && (warp == Sh::kTmaWarp || warp == Sh::kTmaVWarp)) {
     if constexpr (KV8) {
       // ------------------------------------------------- copies of codes
-      // One copy per block, issued by lanes 0 .. 7 after lane 0 has posted the
-      // byte count.  Block ids are read four tiles ahead of their use.
-      const int which = k_producer ? 0 : 1;
-      uint8_t *stage = smem + L::kCodes + which * L::kCodeBytes;
+      // K's go to the stages that the products read, V's to two staging
+      // buffers.  One copy per block, issued by lanes 0 .. 7 after lane 0 has
+      // posted the byte count.  Block ids, and K's block scales, are read four
+      // tiles ahead of their use.
+      auto scale_of = [&](int id) {
+        if (!k_producer || id < 0) return 0.f;
+        return checked_load(p.k_scale, static_cast<size_t>(id) * p.Hkv + kvh,
+                            static_cast<size_t>(p.num_blocks) * p.Hkv, p.status);
+      };
       const CUtensorMap *map = k_producer ? &tm_k : &tm_v;
+      const int stages = k_producer ? SK : 2;
+      uint64_t *full = k_producer ? k_full : c_full, *empty = k_producer ? k_empty : c_empty;
+      uint8_t *stage0 = k_producer ? sK : smem + L::kCodes;
       int cur = cache_block(0, k_producer), nxt = cache_block(kIdTiles, k_producer);
+      float cur_s = scale_of(cur), nxt_s = scale_of(nxt);
       int issued = 0;
       for (int j = 0; j < n_kv; ++j) {
         if (j > 0 && j % kIdTiles == 0) {
-          cur = nxt;
+          cur = nxt, cur_s = nxt_s;
           nxt = cache_block(j + kIdTiles, k_producer);
+          nxt_s = scale_of(nxt);
         }
-        const int phys = __shfl_sync(0xffffffffu, cur, (j % kIdTiles) * kTileBlocks + (lane & 7));
+        const int st = j % stages, from = (j % kIdTiles) * kTileBlocks + (lane & 7);
+        const int phys = __shfl_sync(0xffffffffu, cur, from);
+        const float sc = __shfl_sync(0xffffffffu, cur_s, from);
         const bool mine = lane < kTileBlocks && phys >= 0;
         const unsigned live = __ballot_sync(0xffffffffu, mine);
-        if (j > 0 && !mbar_wait_warp(&c_empty[which], (j - 1) & 1, abort_flag, p.status)) break;
-        if (lane == 0) mbar_arrive_expect_tx(&c_full[which], __popc(live) * kDecodeBlock * D);
+        if (j >= stages && !mbar_wait_warp(&empty[st], ((j / stages) - 1) & 1, abort_flag, p.status))
+          break;
+        uint8_t *dst = stage0 + st * 128 * D + lane * kDecodeBlock * D;
+        if (k_producer && lane < kTileBlocks) {
+          reinterpret_cast<float *>(smem + L::kScales)[(j % L::kScaleSlots) * kTileBlocks + lane] =
+              sc;
+          if (phys == -2) {  // a bad id's keys are 0
+            for (int t = 0; t < kDecodeBlock * D / 16; ++t)
+              reinterpret_cast<uint4 *>(dst)[t] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+        }
         __syncwarp();
-        if (mine)
-          tma_load_3d(stage + lane * kDecodeBlock * D, map, &c_full[which], 0, kvh,
-                      phys * kDecodeBlock);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(live) * kDecodeBlock * D);
+        __syncwarp();
+        if (mine) tma_load_3d(dst, map, &full[st], 0, kvh, phys * kDecodeBlock);
         issued = j + 1;
       }
       if (lane == 0) {  // no copy outlives the CTA
         if (k_producer) mbar_drain(q_full, 0, p.status);
-        if (issued > 0) mbar_drain(&c_full[which], (issued - 1) & 1, p.status);
+        for (int j = max(0, issued - stages); j < issued; ++j)
+          mbar_drain(&full[j % stages], (j / stages) & 1, p.status);
       }
     }
   } else if (KV8 && warp >= Sh::kConvWarp) {
     if constexpr (KV8) {
-      // ---------------------------------------------------- 8-bit K and V
+      // ---------------------------------------------------- 8-bit V
       // A warp iteration covers 4 rows of d = 128 (8 of d = 64), one 16-code
       // unit a lane: lane bits 0-1 are the unit in a 64-column chunk, bit 2 the
       // row's parity, bit 3 (d = 128) the chunk, exchanged on odd rows, then
@@ -539,43 +627,35 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
       const int c_row = cw * kRowsWarp +
                         ((D == 128) ? ((lane >> 2) & 1) + 2 * (lane >> 4) : (lane >> 2));
       const int c_chunk = (D == 128) ? ((lane >> 3) ^ (lane >> 2)) & 1 : 0;
-      // The block scales of four tiles, read four tiles ahead; 0 for a block
+      // The block scales of four tiles, read four tiles ahead; -1 for a block
       // that was not copied.
-      auto scales = [&](int w, float &ks, float &vs) {
+      auto scales = [&](int w) {
         const int id = cache_block(w, false);
         const size_t at = static_cast<size_t>(max(id, 0)) * p.Hkv + kvh;
         const size_t n = static_cast<size_t>(p.num_blocks) * p.Hkv;
-        ks = id < 0 ? -1.f : checked_load(p.k_scale, at, n, p.status);
-        vs = id < 0 ? -1.f : checked_load(p.v_scale, at, n, p.status);
+        return id < 0 ? -1.f : checked_load(p.v_scale, at, n, p.status);
       };
-      float cur_k, cur_v, nxt_k, nxt_v;
-      scales(0, cur_k, cur_v);
-      scales(kIdTiles, nxt_k, nxt_v);
-      // Turn t is tile t / 2 of K (t even) or V (odd): wait for its codes and a
-      // free stage, write the tile's bf16 rows, handing the buffer back to the
-      // copies once the last codes are read, and hand the rows on.  Rows past
-      // the context (stale slots) and of blocks that were not copied become 0.
-      // One copy of this code serves K and V, four units at a time: unrolled
-      // for both whole tiles it took 472 us instead of 315 (the instruction
-      // streams of these warps and of the softmax warps beside them outgrow
-      // the instruction cache).
-      for (int t = 0; t < 2 * n_kv; ++t) {
-        const int j = t >> 1, i = t & 1;
-        if (i == 0 && j > 0 && j % kIdTiles == 0) {
-          cur_k = nxt_k, cur_v = nxt_v;
-          scales(j + kIdTiles, nxt_k, nxt_v);
+      float cur_s = scales(0), nxt_s = scales(kIdTiles);
+      // Wait for the tile's codes and a free stage, write the tile's bf16 rows,
+      // handing the buffer back to the copies once the last codes are read, and
+      // hand the rows on.  Rows past the context (stale slots) and of blocks
+      // that were not copied become 0.  Four units at a time: the instruction
+      // streams of these warps and of the softmax warps beside them outgrow the
+      // instruction cache when the whole tile is unrolled.
+      for (int j = 0; j < n_kv; ++j) {
+        if (j > 0 && j % kIdTiles == 0) {
+          cur_s = nxt_s;
+          nxt_s = scales(j + kIdTiles);
         }
-        const int stages = i ? SV : SK, st = j % stages;
-        uint64_t *full = (i ? v_full : k_full) + st, *empty = (i ? v_empty : k_empty) + st;
-        if (j >= stages && !mbar_wait_warp(empty, ((j / stages) - 1) & 1, abort_flag, p.status))
-          break;
-        if (!mbar_wait_warp(&c_full[i], j & 1, abort_flag, p.status)) break;
-        const uint8_t *codes = smem + L::kCodes + i * L::kCodeBytes + c_row * D + c_chunk * 64 +
+        const int st = j % SV, cb = j & 1;
+        if (j >= SV && !mbar_wait_warp(&v_empty[st], ((j / SV) - 1) & 1, abort_flag, p.status)) break;
+        if (!mbar_wait_warp(&c_full[cb], (j >> 1) & 1, abort_flag, p.status)) break;
+        const uint8_t *codes = smem + L::kCodes + cb * L::kCodeBytes + c_row * D + c_chunk * 64 +
                                c_unit * 16;
-        const float sc = i ? cur_v : cur_k;
         const int rows = kv_len - key_tile(j) * kPrefillBN;
-        uint8_t *tile = (i ? sV : sK) + st * L::kTileBytes + c_chunk * L::kChunkBytes;
+        uint8_t *tile = sV + st * L::kTileBytes + c_chunk * L::kChunkBytes;
         constexpr int kUnits = 4;
+        static_assert(kIters % kUnits == 0, "whole groups of units");
 #pragma unroll 1
         for (int u0 = 0; u0 < kIters; u0 += kUnits) {
           uint4 x[kUnits];
@@ -584,12 +664,12 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
             x[it] = *reinterpret_cast<const uint4 *>(codes + (u0 + it) * 4 * kRowsWarp * D);
           if (u0 + kUnits == kIters) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c_empty[i]);
+            if (lane == 0) mbar_arrive(&c_empty[cb]);
           }
 #pragma unroll
           for (int it = 0; it < kUnits; ++it) {
             const int r = (u0 + it) * 4 * kRowsWarp + c_row;
-            float s = __shfl_sync(0xffffffffu, sc, (j % kIdTiles) * kTileBlocks + r / kDecodeBlock);
+            float s = __shfl_sync(0xffffffffu, cur_s, (j % kIdTiles) * kTileBlocks + r / kDecodeBlock);
             const uint32_t keep = (s >= 0.f && r < rows) ? 0xFFFFFFFFu : 0u;
             const uint32_t w[4] = {x[it].x & keep, x[it].y & keep, x[it].z & keep, x[it].w & keep};
             const float2 s2 = make_float2(s, s);
@@ -609,7 +689,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(full);
+        mbar_arrive(&v_full[st]);
       }
     }
   } else if (!KV8 && (warp == Sh::kTmaWarp || warp == Sh::kTmaVWarp) && PAGED) {
@@ -820,6 +900,25 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
       // address fields (address / 16) by constants.
       auto issue_s = [&](int i, int st) {
         const uint32_t d_t = tmem + i * 128;
+        if constexpr (KV8) {
+          // both terms of Q times the codes, one sum: 32 codes an MMA
+          if (elect_one()) {
+            constexpr uint32_t kIdesc8 = idesc_e4m3_f32(kPrefillBM, kPrefillBN, false, false);
+            constexpr uint32_t kIdesc8l = kIdesc8 | kIdescAE5m2;
+            constexpr int kSbo8 = 8 * L::kK8Swz;
+            const uint64_t a0 = sdesc_swz<L::kK8Swz>(q_base + i * L::kTileBytes, 16, kSbo8);
+            const uint64_t b0 = sdesc_swz<L::kK8Swz>(k_base + st * L::kKStage, 16, kSbo8);
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_ss_f8(d_t, a0 + ((term * L::kKStage + kk * 32) >> 4), b0 + ((kk * 32) >> 4),
+                          term ? kIdesc8l : kIdesc8, term + kk > 0 ? 1u : 0u);
+            mma_commit(&s_full[i]);
+          }
+          __syncwarp();
+          return;
+        }
         if (elect_one()) {
           const uint64_t a0 = sdesc_swz<L::kSwz>(q_base + i * L::kTileBytes, 16, L::kSbo);
           const uint64_t b0 = sdesc_swz<L::kSwz>(k_base + st * L::kTileBytes, 16, L::kSbo);
@@ -867,7 +966,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
       // issued just before it by this thread, reads P_i(j) from; tcgen05 MMAs
       // issued by one thread execute in order.
       // (a split that owns no key tile issues nothing)
-      bool ok = n_kv > 0 && mbar_wait_warp(q_full, 0, abort_flag, p.status) &&
+      bool ok = n_kv > 0 && mbar_wait_warp(KV8 ? q_ready : q_full, 0, abort_flag, p.status) &&
                 mbar_wait_warp(&k_full[0], 0, abort_flag, p.status);
       if (ok) {
         tc_fence_after();
@@ -931,7 +1030,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     }
   }
   } else {
-    if constexpr (Sh::kSplitRegs) setmaxnreg_inc<kPrefill1SoftmaxRegs>();
+    if constexpr (Sh::kSplitRegs) setmaxnreg_inc<KV8 ? kPrefill8SoftmaxRegs : kPrefill1SoftmaxRegs>();
     // ------------------------------------------------------ softmax warpgroups
     const int i = warp >> 2;
     const int quad = warp & 3;
@@ -942,7 +1041,20 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     const int qi = tile_row(i) + row;  // query row within the sequence
     const int hi = tile_head(i);       // query head of this tile
     const int my_end = kv_end[i];
-    const float sl2 = p.scale_log2;
+    float q_scale = 1.f;  // 8-bit caches: what the scores of this row's codes are multiplied by
+    if constexpr (KV8) {
+      if (my_end > 0) {
+        // Q as two 8-bit terms, each thread its own row, in the tile's place
+        if (mbar_wait_warp(q_full, 0, abort_flag, p.status))
+          q_scale = p.scale_log2 * split_q_row<D>(sQ + i * L::kTileBytes, row, 1 + i);
+        else if (D == 64)
+          named_bar_sync(1 + i, 128);  // (split_q_row's)
+        fence_proxy_async_smem();
+        mbar_arrive(q_ready);
+      }
+    }
+    // (the scores of codes get their scales before the softmax)
+    const float sl2 = KV8 ? 1.f : p.scale_log2;
     const float2 sl2x2 = make_float2(sl2, sl2);
     // Reference maximum of the exponentials, log2 units.  It follows the row
     // maximum, but moves only when the maximum grows by more than
@@ -966,6 +1078,23 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
 
       uint32_t sr[128];
       tmem_ld128_wait(tS, sr);
+      if constexpr (KV8) {
+        const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kScales) +
+                           (j % L::kScaleSlots) * 2;
+        const float4 k0 = ks[0], k1 = ks[1];
+        const float s8[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+        for (int blk = 0; blk < 8; ++blk) {
+          const float2 c2 = make_float2(s8[blk] * q_scale, s8[blk] * q_scale);
+#pragma unroll
+          for (int c = blk * 16; c < blk * 16 + 16; c += 2) {
+            const float2 x =
+                fmul2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2);
+            sr[c] = __float_as_uint(x.x);
+            sr[c + 1] = __float_as_uint(x.y);
+          }
+        }
+      }
       const int nvis = limit - key_tile(j) * kPrefillBN;
       // windowed: keys [sink_c, lo_c) of the tile lie between sinks and window
       const int lo_c = WIN ? limit_lo - key_tile(j) * kPrefillBN : 0;

@@ -76,9 +76,11 @@ int fa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
 
 /*
  * fa_fwd_paged (causal) over the 8-bit cache: query chunks, the last rows of
- * each sequence's context.  K and V are widened to bf16 on chip and the
- * products run as in fa_fwd_paged: exactly where a block's scale is a power of
- * two, with one bf16 rounding of the scaled values where it is not.
+ * each sequence's context.  The products run as in fa_fwd_paged: on K's codes
+ * as they are, with q exact down to 2^-13 of its row's largest value and off
+ * by at most 2^-21 of that below, and on V widened to bf16, exactly where a
+ * block's scale is a power of two, with one bf16 rounding where it is not.  An
+ * infinite or NaN value of q makes its row's result NaN.
  *   q, out : [total_q, H, d] bf16;  lse : [H, total_q] fp32, may be NULL
  * Slots past the context never reach the result; a block that no query of a
  * 128-row tile sees (a window's) is not read and may be freed.  A query that

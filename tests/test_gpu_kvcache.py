@@ -335,7 +335,7 @@ def check_chunks(out, lse, q, c, ctx, cu, window, sinks, rounded=False):
             continue
         k, v = c.rows("k", b, n), c.rows("v", b, n)
         if rounded:
-            k, v = k.to(torch.bfloat16).double(), v.to(torch.bfloat16).double()
+            v = v.to(torch.bfloat16).double()
         for h in range(H):
             kv = h // (H // Hkv)
             o, l, tol = ref.forward(q[a:e, h].double(), k[:, kv], v[:, kv], window, sinks)
@@ -359,7 +359,7 @@ def test_chunks_of_many_sequences(fa, batch):
 
 
 def test_chunks_with_any_scale(fa):
-    """Scales that are no powers of two: K and V rounded to bf16 once."""
+    """Scales that are no powers of two: V rounded to bf16 once."""
     torch = torch_mod()
     ctx, new, H, Hkv, d = [333, 90], [140, 90], 4, 2, 128
     c = Cache(ctx, Hkv, d, seed=90)
@@ -553,4 +553,49 @@ def test_blocks_past_32_bits(fa):
     check_chunks(out, lse, q, c, [n], [0, new], 0, 0)
     out, lse = fa.fa_decode_paged_fp8(q[-1:].contiguous(), *c.args(), lens, n)
     check_decode(out, lse, q[-1:], c, [n], 0, 0, "far blocks")
+    assert_device_clean()
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(4, 4, 64), (6, 3, 128)])
+def test_chunks_of_any_size_of_row(fa, H, Hkv, d):
+    """Queries of 2^-60 to 2^100 over keys whose block scales make up for it,
+    values 2^-8 and 2^-12 of their row's largest, zero rows; rows with an
+    infinity or a NaN become NaN and leave the others alone.
+
+    The products hold q to 2^-21 of its row's largest value: a score is off by
+    2^-21 max|q| sum|k| of its scale, and the output by twice that (in its
+    weights and in their sum) of sum P |v|."""
+    torch = torch_mod()
+    ctx, new = [300, 170], [150, 40]
+    c = Cache(ctx, Hkv, d, seed=140)
+    rng = np.random.default_rng(141)
+    G = H // Hkv
+    size = np.exp2([(-60, 0, 100, 37)[h] for h in range(Hkv)]).astype(np.float32)
+    c.scale["k"] = (c.scale["k"] / size).astype(np.float32)
+    c.dscale["k"].copy_(dev(c.scale["k"]))
+    cu = cu_of(new)
+    q = cr.bf16(rng, cu[-1], H, d) * np.repeat(size, G)[:, None]
+    q[:, :, 5:] *= np.float32(2.0 ** -8)
+    q[:, :, 9:] *= np.float32(2.0 ** -4)
+    q[7], q[160] = 0, 0
+    q = bf16(q)
+    out, lse = fa.fa_fwd_paged_fp8(q, *c.args(), dev(np.int32(ctx)), dev(cu), max(new), max(ctx))
+    assert_device_clean()
+    for b, n in enumerate(ctx):
+        a, e = int(cu[b]), int(cu[b + 1])
+        k, v = c.rows("k", b, n), c.rows("v", b, n)
+        for h in range(H):
+            x, kh, vh = q[a:e, h].double(), k[:, h // G], v[:, h // G]
+            o, l, tol = ref.forward(x, kh, vh, 0, 0)
+            off = 2.0 ** -21 * x.abs().amax(1) * kh.abs().sum(1).max() / math.sqrt(d)
+            size_v = torch.softmax((x @ kh.T / math.sqrt(d)).masked_fill(
+                ~ref.visible(e - a, n, n - (e - a), 0, 0, x.device), -math.inf), 1) @ vh.abs()
+            ref.assert_within(out[a:e, h], o, tol + 2 * off[:, None] * size_v, f"seq {b} head {h}")
+            assert bool(((lse[h, a:e].double() - l).abs() <= ref.LSE_TOL + off).all()), (b, h)
+    bad = q.clone()
+    bad[3, 0, 1], bad[151, :, d - 1] = math.inf, math.nan
+    got, _ = fa.fa_fwd_paged_fp8(bad, *c.args(), dev(np.int32(ctx)), dev(cu), max(new), max(ctx))
+    assert bool(got[3, 0].isnan().all()) and bool(got[151].isnan().all())
+    got[3, 0], got[151] = out[3, 0], out[151]
+    assert torch.equal(got, out)
     assert_device_clean()
