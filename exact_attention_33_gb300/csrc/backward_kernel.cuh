@@ -103,7 +103,7 @@ struct BwdDqLayout {
   static constexpr int kK = kDO + kTileBytes;
   static constexpr int kV = kK + kStagesK * kTileBytes;
   static constexpr int kBar = kV + kStagesV * kTileBytes;
-  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 9;
+  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 11;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kItem = kMisc + 16;  // the work item slot
   static constexpr int kVec = kItem + 48;   // the item's -lse2 and -D vectors (128 floats each)
@@ -909,9 +909,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t *v_empty = v_full + SV;
   uint64_t *s_full = v_empty + SV;
   uint64_t *s_read = s_full + 1;    // the elementwise warps have read S_j
+  // dP_j, and dS_j (bf16) in its place, of even and of odd key tiles.  dP_{j+1}
+  // waits for S_j to be read, not for dP_j to be seen, and tile j + 1 may be done
+  // while the MMA warp still looks for dS_j: on one barrier a waiter that wakes
+  // only after both phases waits for the phase after them, for ever (short
+  // windows, whose tiles are mostly hidden and quickly done, did so)
   uint64_t *dp_full = s_read + 1;
-  uint64_t *p_full = dp_full + 1;   // dS_j (bf16) is in TMEM
-  uint64_t *dq_done = p_full + 1;   // the item's dQ is complete in TMEM
+  uint64_t *p_full = dp_full + 2;
+  uint64_t *dq_done = p_full + 2;   // the item's dQ is complete in TMEM
   uint64_t *drain = dq_done + 1;
   uint64_t *qdo_empty = drain + 1;  // the item's last products that read Q and dO are done
   uint64_t *dq_free = qdo_empty + 1;  // the elementwise warps have read the item's dQ
@@ -939,8 +944,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(s_read, 256);
-    mbar_init(dp_full, 1);
-    mbar_init(p_full, 256);
+    mbar_init(&dp_full[0], 1);
+    mbar_init(&dp_full[1], 1);
+    mbar_init(&p_full[0], 256);
+    mbar_init(&p_full[1], 256);
     mbar_init(dq_done, 1);
     mbar_init(drain, 1);
     mbar_init(qdo_empty, 1);
@@ -1102,7 +1109,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (WIN && VARLEN && inside < 128) zero_rows<D>(sV + sv * L::kTileBytes, inside);
       tc_fence_after();
       mma_tile_ss<D>(tmem + ((g & 1) ? 384 : 128), do_base, v_ring + sv * L::kTileBytes);
-      mma_commit_elect(dp_full);
+      mma_commit_elect(&dp_full[g & 1]);
       mma_commit_elect(&v_empty[sv]);
       return true;
     };
@@ -1126,7 +1133,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         } else {
           mma_commit_elect(qdo_empty);  // the item's last S and dP read Q and dO
         }
-        if (!mbar_wait_warp(p_full, g & 1, abort_flag, p.status)) {
+        if (!mbar_wait_warp(&p_full[g & 1], (g >> 1) & 1, abort_flag, p.status)) {
           ok = false;
           break;
         }
@@ -1223,7 +1230,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(s_read);
-        ok = mbar_wait(dp_full, g & 1, abort_flag, p.status);
+        ok = mbar_wait(&dp_full[g & 1], (g >> 1) & 1, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -1259,7 +1266,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(p_full);
+        mbar_arrive(&p_full[g & 1]);
       }
       if (!ok) break;
       ok = mbar_wait(dq_done, m & 1, abort_flag, p.status);

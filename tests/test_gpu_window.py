@@ -443,3 +443,21 @@ def test_rows_past_32_bits(fa):
     o, l = fa.fa_fwd_paged_window(tok, pool, pool, table, i32([n]), i32([0, 30]), 30, n, 100, 2)
     check_rows(o, l, tok, rows, rows, 100, 2, "far blocks, chunk")
     assert_device_clean()
+
+
+def test_gradient_under_load(fa):
+    """Many short work items behind one another, again and again: no wait of the
+    pipeline may miss its turn (a missed one raises the status word after a
+    second)."""
+    torch = torch_mod()
+    H, d, lens = 64, 128, [40000, 260]
+    q, g = normal(130, sum(lens), H, d), normal(131, sum(lens), H, d)
+    k, v = normal(132, sum(lens), 1, d), normal(133, sum(lens), 1, d)
+    args = (i32(cu_of(lens)), max(lens), 70, 3)
+    out, lse = fa.fa_fwd_varlen_window(q, k, v, *args)
+    first = None
+    for _ in range(12):
+        grads = fa.fa_bwd_varlen_window(q, k, v, out, lse, g, *args)
+        first = first or grads
+        assert_device_clean()
+    assert all(torch.equal(a, b) for a, b in zip(grads, first))
