@@ -54,12 +54,14 @@ static_assert(256 * kPrefill8SoftmaxRegs + 256 * kPrefill8CtlRegs <= 512 * kPref
 // query tiles take 512 threads: the softmax warps, a warpgroup of the MMA and
 // the copies (warp 11 idles), and the four warps from kConvWarp on that
 // widen values.
-template <int QT, bool KV8 = false>
+// A persistent CTA (PERS) has no second copy warp, so that its softmax gets 200
+// registers.
+template <int QT, bool KV8 = false, bool PERS = false>
 struct PrefillShape {
   static_assert(QT == 1 || QT == 2, "one or two query tiles per CTA");
   static_assert(!KV8 || QT == 2, "8-bit caches run two query tiles per CTA");
   static constexpr int kRows = kPrefillBM * QT;
-  static constexpr int kThreads = KV8 ? 512 : QT == 2 ? kPrefillThreads : 256;
+  static constexpr int kThreads = KV8 ? 512 : PERS ? 320 : QT == 2 ? kPrefillThreads : 256;
   static constexpr int kConvWarp = 12;
   static constexpr bool kSplitRegs = QT == 1 || KV8;  // registers move with setmaxnreg
   static constexpr int kSoftmaxWarps = 4 * QT;
@@ -107,6 +109,7 @@ struct PrefillParams {
   // item (its own + prefetch_ahead), the one that starts about a wave later
   // (0: none)
   int prefetch_ahead;
+  int num_items;  // work items (a persistent CTA takes more than one)
   // windowed kernels only: the query at position i sees key j <= i when
   // j > i - window or j < sinks
   int window;

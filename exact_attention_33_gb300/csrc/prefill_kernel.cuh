@@ -41,8 +41,11 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "fa_internal.h"
 #include "ptx.cuh"
+#include "store.cuh"
 #include "checks.cuh"
 
 namespace fa {
@@ -53,7 +56,7 @@ constexpr float kRescaleLog2 = 8.f;
 
 
 
-template <int D, bool FP8 = false, int QT = 2, bool KV8 = false>
+template <int D, bool FP8 = false, int QT = 2, bool KV8 = false, bool PERS = false>
 struct PrefillLayout {
   static constexpr int kElemBytes = FP8 ? 1 : 2;
   // Rows are copied and read in swizzled rows of 128 bytes, or of 64 bytes
@@ -105,9 +108,10 @@ struct PrefillLayout {
   static constexpr int kBar = kScales + (KV8 ? kScaleSlots * 8 * 4 : 0);
   // q_full, k_full[SK], k_empty[SK], v_full[SV], s_full[2], p_full[2],
   // o_done[2], drain, v_empty[SV], and over an 8-bit cache c_full[2],
-  // c_empty[2] of V's staged codes and q_ready.  A V stage is released as soon
+  // c_empty[2] of V's staged codes and q_ready, in a persistent CTA q_free.  A V
+  // stage is released as soon
   // as the P V products of its key tile are done.
-  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7 + (KV8 ? 5 : 0);
+  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7 + (KV8 ? 5 : 0) + (PERS ? 1 : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kSmemAlloc = kBytes + 1024;     // base is aligned up to 1024 in-kernel
@@ -259,6 +263,13 @@ __device__ __forceinline__ int longest_context(const PrefillParams &p, int rank)
 // j < p.sinks.  The CTA then streams the key tiles of the sinks and those from
 // the window of its first row on, and leaves the ones between out.
 //
+// PERS (windowed head pairs): the CTA takes work items blockIdx.x, blockIdx.x +
+// gridDim.x, ... one behind the other (prefill_window.cu says when).  Every
+// barrier of the key loop counts key tiles over all of them; the copies of the
+// next item's K(0), and of its Q as soon as the last S products have read this
+// one's, run beside the last softmax and the epilogue, which writes its rows from
+// registers because the Q tile is taken.
+//
 // KV8 (paged kinds, windowed): the cache holds e4m3 codes with a scale per
 // block and KV head.  K's codes are operands as they are: S = (Qh + Ql) K^T
 // with Q in two 8-bit terms (split_q_row), at twice bf16's rate for twice the
@@ -273,16 +284,19 @@ __device__ __forceinline__ int longest_context(const PrefillParams &p, int rank)
 // and the longest CTAs' 112 steps against 85 on average.  (Codes loaded
 // straight into registers, 32 or 64 of a thread's 88 in flight: 470 to 620 us.)
 template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false,
-          bool KV8 = false>
-__global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<QT, KV8>::kMinBlocks)
+          bool KV8 = false, bool PERS = false>
+__global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
+                                  PrefillShape<QT, KV8, PERS>::kMinBlocks)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_v1,
                    const __grid_constant__ CUtensorMap tm_o, const PrefillParams p) {
-  using L = PrefillLayout<D, FP8, QT, KV8>;
+  using L = PrefillLayout<D, FP8, QT, KV8, PERS>;
   static_assert(L::kSmemAlloc <= 232448, "prefill shared memory exceeds 227 KiB");
-  using Sh = PrefillShape<QT, KV8>;
+  using Sh = PrefillShape<QT, KV8, PERS>;
+  static_assert(!PERS || (WIN && (KIND == kKindDenseHeads || KIND == kKindVarlenHeads)),
+                "persistent kinds");
   static_assert(!KV8 || (WIN && (KIND == kKindPaged || KIND == kKindPagedHeads)), "8-bit caches");
   static_assert(!(FP8 && KIND == kKindDenseSplit), "the split-KV layout is bf16 only");
   constexpr int SK = L::kStagesK;
@@ -335,101 +349,132 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     pair_x = CAUSAL ? (p.max_pairs - 1 - pair_rank) : pair_rank;
     return true;
   };
+  int item = lin;
   int h, unit, pair;  // unit: batch element or sequence
-  if (!decode_item(lin, unit, pair, h)) return;  // past the last item
   // len: query rows of the unit; kv_len: its keys; offset = kv_len - len
   // aligns causal masking to the bottom right (query i sees keys
   // j <= i + offset).
   int b, seq_start, len, kv_len, offset;
-  if (DENSE || KIND == kKindDenseSplit) {
-    b = unit;
-    seq_start = 0;
-    len = p.N;
-    kv_len = len;
-    offset = 0;
-  } else {
-    seq_start = checked_load(p.cu_seqlens, unit, p.B + 1, p.status);
-    const int seq_end = checked_load(p.cu_seqlens, unit + 1, p.B + 1, p.status);
-    if (seq_start < 0 || seq_end < seq_start || seq_end > p.total_tokens) {
-      if (pair == 0 && h == 0) raise_status(p.status, FA_DEV_BAD_SEQLEN);
-      return;
-    }
-    len = seq_end - seq_start;
-    // Longer than max_seqlen: a grid sized from it cannot cover the sequence.
-    // Any item of head 0 reports it; the sequence's first item, which is one,
-    // is launched whenever the sequences before it respect max_seqlen.
-    if (len > p.max_pairs * kCtaRows && h == 0) raise_status(p.status, FA_DEV_BAD_SEQLEN);
-    b = 0;
-    if (KIND == kKindVarlen || KIND == kKindVarlenHeads) {
-      kv_len = len;
-      offset = 0;
-    } else {
-      kv_len = checked_load(p.ctx_lens, unit, p.B, p.status);
-      if (kv_len < 0 || kv_len > p.max_ctx_len ||
-          kv_len > p.max_blocks_per_seq * kDecodeBlock) {
-        if (pair == 0 && h == 0) raise_status(p.status, FA_DEV_BAD_CTX);
-        return;
-      }
-      offset = kv_len - len;
-    }
-  }
-  const int row0 = pair * kCtaRows;
-  if (row0 >= len) return;  // no padding work: the whole CTA leaves before any set-up
-  // first query row (within the sequence) and head of query tile i
-  auto tile_row = [&](int i) { return HP ? row0 : row0 + i * kPrefillBM; };
-  auto tile_head = [&](int i) { return HP ? h + i : h; };
-
-  const int n_kv_all = (kv_len + kPrefillBN - 1) / kPrefillBN;
-  int kv_end[kPrefillQTiles];
-#pragma unroll
-  for (int i = 0; i < kPrefillQTiles; ++i) {
-    const int t0 = tile_row(i);
-    if (i >= QT || t0 >= len) {
-      kv_end[i] = 0;
-    } else {
-      int e = n_kv_all;
-      if (CAUSAL) {
-        const int last_key = min(t0 + kPrefillBM - 1, len - 1) + offset;
-        e = (last_key < 0) ? 0 : min(n_kv_all, last_key / kPrefillBN + 1);
-      }
-      // a live tile runs at least one key tile (possibly fully masked), so
-      // that rows which see no key are still written (O = 0, LSE = -inf)
-      kv_end[i] = max(e, 1);
-    }
-  }
-  // This CTA's key tiles are [kv0, kv0 + n_kv); from here on kv_end[i] counts
-  // the tiles of query tile i inside that range.
-  int kv0 = 0;
-  // Windowed: the first n_sink tiles and, `gap` tiles later, those from the
-  // window of the CTA's first row on; key tile j (counted over both) is tile
-  // key_tile(j) of the sequence.  A query tile's rows are the CTA's rows (one
-  // query tile, or two heads over the same rows), so one list serves both; the
-  // row pairs of an 8-bit cache take the first tile's, and the second tile
+  int kvh;   // KV head
+  int row0;  // first query row of the item
+  // The item's key tiles are [kv0, kv0 + n_kv), kv_end[i] of them for query
+  // tile i.  Windowed: the first n_sink tiles and, `gap` tiles later, those from
+  // the window of the item's first row on; key tile j (counted over both) is
+  // tile key_tile(j) of the sequence.  A query tile's rows are the item's rows
+  // (one query tile, or two heads over the same rows), so one list serves both;
+  // the row pairs of an 8-bit cache take the first tile's, and the second tile
   // meets up to one tile in which it sees nothing.
   static_assert(!WIN || (CAUSAL && !FP8 && (HP || QT == 1 || KV8) && KIND != kKindDenseSplit),
                 "windowed layouts");
-  int n_sink = 0, gap = 0;
-  const int win_lo = WIN ? row0 + offset + 1 - p.window : 0;  // first key of row0's window
-  if constexpr (WIN) {
-    const int w0 = max(win_lo, 0) / kPrefillBN;
-    const int ns = (min(p.sinks, kv_len) + kPrefillBN - 1) / kPrefillBN;
-    if (ns < w0) {
-      n_sink = ns;
-      gap = w0 - ns;
-#pragma unroll
-      for (int i = 0; i < kPrefillQTiles; ++i) kv_end[i] = max(0, kv_end[i] - gap);
-    }
-  }
+  int kv0, n_kv, kv_end[kPrefillQTiles];
+  int n_sink, gap;
+  int win_lo;  // first key of row0's window
+  // first query row (within the sequence) and head of query tile i
+  auto tile_row = [&](int i) { return HP ? row0 : row0 + i * kPrefillBM; };
+  auto tile_head = [&](int i) { return HP ? h + i : h; };
   auto key_tile = [&](int j) { return WIN ? (j < n_sink ? j : j + gap) : kv0 + j; };
-  if (KIND == kKindDenseSplit) {
-    const int total = max(kv_end[0], kv_end[1]);
-    const int per = (total + p.num_splits - 1) / p.num_splits;
-    kv0 = split * per;
-    const int stop = min(total, kv0 + per);
+  // Sets all of these for the work item; kItemRun unless it has no rows
+  // (kItemNone) or lies past the last one (kItemEnd).  Collective over the warp.
+  constexpr int kItemRun = 0, kItemNone = 1, kItemEnd = 2;
+  auto load_item = [&]() -> int {
+    if (!decode_item(item, unit, pair, h)) return kItemEnd;
+    kvh = h / p.group;
+    if (DENSE || KIND == kKindDenseSplit) {
+      b = unit;
+      seq_start = 0;
+      len = p.N;
+      kv_len = len;
+      offset = 0;
+    } else {
+      seq_start = checked_load(p.cu_seqlens, unit, p.B + 1, p.status);
+      const int seq_end = checked_load(p.cu_seqlens, unit + 1, p.B + 1, p.status);
+      if (seq_start < 0 || seq_end < seq_start || seq_end > p.total_tokens) {
+        if (pair == 0 && h == 0) raise_status(p.status, FA_DEV_BAD_SEQLEN);
+        return kItemNone;
+      }
+      len = seq_end - seq_start;
+      // Longer than max_seqlen: a grid sized from it cannot cover the sequence.
+      // Any item of head 0 reports it; the sequence's first item, which is one,
+      // is launched whenever the sequences before it respect max_seqlen.
+      if (len > p.max_pairs * kCtaRows && h == 0) raise_status(p.status, FA_DEV_BAD_SEQLEN);
+      b = 0;
+      if (KIND == kKindVarlen || KIND == kKindVarlenHeads) {
+        kv_len = len;
+        offset = 0;
+      } else {
+        kv_len = checked_load(p.ctx_lens, unit, p.B, p.status);
+        if (kv_len < 0 || kv_len > p.max_ctx_len ||
+            kv_len > p.max_blocks_per_seq * kDecodeBlock) {
+          if (pair == 0 && h == 0) raise_status(p.status, FA_DEV_BAD_CTX);
+          return kItemNone;
+        }
+        offset = kv_len - len;
+      }
+    }
+    row0 = pair * kCtaRows;
+    if (row0 >= len) return kItemNone;  // no padding work
+    const int n_kv_all = (kv_len + kPrefillBN - 1) / kPrefillBN;
 #pragma unroll
-    for (int i = 0; i < kPrefillQTiles; ++i) kv_end[i] = max(0, min(kv_end[i], stop) - kv0);
-  }
-  const int n_kv = max(kv_end[0], kv_end[1]);
+    for (int i = 0; i < kPrefillQTiles; ++i) {
+      const int t0 = tile_row(i);
+      if (i >= QT || t0 >= len) {
+        kv_end[i] = 0;
+      } else {
+        int e = n_kv_all;
+        if (CAUSAL) {
+          const int last_key = min(t0 + kPrefillBM - 1, len - 1) + offset;
+          e = (last_key < 0) ? 0 : min(n_kv_all, last_key / kPrefillBN + 1);
+        }
+        // a live tile runs at least one key tile (possibly fully masked), so
+        // that rows which see no key are still written (O = 0, LSE = -inf)
+        kv_end[i] = max(e, 1);
+      }
+    }
+    kv0 = n_sink = gap = 0;
+    win_lo = WIN ? row0 + offset + 1 - p.window : 0;
+    if constexpr (WIN) {
+      const int w0 = max(win_lo, 0) / kPrefillBN;
+      const int ns = (min(p.sinks, kv_len) + kPrefillBN - 1) / kPrefillBN;
+      if (ns < w0) {
+        n_sink = ns;
+        gap = w0 - ns;
+#pragma unroll
+        for (int i = 0; i < kPrefillQTiles; ++i) kv_end[i] = max(0, kv_end[i] - gap);
+      }
+    }
+    if (KIND == kKindDenseSplit) {
+      const int total = max(kv_end[0], kv_end[1]);
+      const int per = (total + p.num_splits - 1) / p.num_splits;
+      kv0 = split * per;
+      const int stop = min(total, kv0 + per);
+#pragma unroll
+      for (int i = 0; i < kPrefillQTiles; ++i) kv_end[i] = max(0, min(kv_end[i], stop) - kv0);
+    }
+    n_kv = max(kv_end[0], kv_end[1]);
+    return kItemRun;
+  };
+  // A persistent CTA runs items blockIdx.x, blockIdx.x + gridDim.x, ...: every
+  // warp walks them by itself.  tiles0 counts the key tiles of the items before
+  // this one (the same for both query tiles, whose rows see the same keys), and
+  // `turn` those items, for the phases of the barriers.
+  int tiles0 = 0, turn = 0;
+  // the first item with rows from `item` on, by this CTA's steps
+  auto find_item = [&]() -> bool {
+    for (;;) {
+      const int rc = load_item();
+      if (rc != kItemNone || !PERS) return rc == kItemRun;
+      if (item >= p.num_items - static_cast<int>(gridDim.x)) return false;
+      item += gridDim.x;
+    }
+  };
+  auto next_item = [&]() -> bool {
+    if (!PERS || item >= p.num_items - static_cast<int>(gridDim.x)) return false;
+    tiles0 += n_kv;
+    ++turn;
+    item += gridDim.x;
+    return find_item();
+  };
+  if (!find_item()) return;  // the whole CTA leaves before any set-up
   const bool live1 = QT == 2 && tile_row(1) < len;  // the second query tile has rows
 
   // ---------------------------------------------------------- shared memory
@@ -449,6 +494,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
   uint64_t *c_full = v_empty + SV;  // 8-bit caches: codes of V staged
   uint64_t *c_empty = c_full + 2;   // and read by the four widening warps
   uint64_t *q_ready = c_empty + 2;  // 8-bit caches: Q in two 8-bit terms
+  uint64_t *q_free = v_empty + SV;  // persistent: the item's last S products have read Q
   constexpr bool ONES = L::kOnes;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
@@ -459,10 +505,20 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
   uint8_t *sQ = smem + L::kQ;
   uint8_t *sK = smem + L::kK;
   uint8_t *sV = smem + L::kV;
-  const int kvh = h / p.group;
   // Dense kinds: K(0) is copied with Q, before the block-wide set-up ends.
   const bool k0_early = !PAGED && n_kv > 0;
 
+  auto load_q = [&]() {
+    const int nq = live1 ? 2 : 1;
+    mbar_arrive_expect_tx(q_full, nq * L::kTileBytes);
+    for (int i = 0; i < nq; ++i) {
+      const int qrow = seq_start + tile_row(i);
+#pragma unroll
+      for (int c = 0; c < L::kChunks; ++c)
+        tma_load_4d(sQ + i * L::kTileBytes + c * L::kChunkBytes, &tm_q, q_full,
+                    c * L::kChunkElems, tile_head(i), qrow, b);
+    }
+  };
   if (warp == Sh::kTmaWarp && lane == 0) {
     // The producer thread initialises the barriers and starts the Q copies
     // (and K(0)) right away; the other warps wait for it at __syncthreads.
@@ -488,6 +544,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
       }
       mbar_init(q_ready, live1 ? 256 : 128);
     }
+    if (PERS) mbar_init(q_free, 1);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -495,15 +552,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     if (PAGED && !KV8) tma_prefetch_desc(&tm_v1);
-    const int nq = live1 ? 2 : 1;
-    mbar_arrive_expect_tx(q_full, nq * L::kTileBytes);
-    for (int i = 0; i < nq; ++i) {
-      const int qrow = seq_start + tile_row(i);
-#pragma unroll
-      for (int c = 0; c < L::kChunks; ++c)
-        tma_load_4d(sQ + i * L::kTileBytes + c * L::kChunkBytes, &tm_q, q_full,
-                    c * L::kChunkElems, tile_head(i), qrow, b);
-    }
+    load_q();
     if (k0_early) {
       mbar_arrive_expect_tx(&k_full[0], L::kTileBytes);
 #pragma unroll
@@ -811,70 +860,81 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     }
   } else if (!KV8 && warp == Sh::kTmaWarp) {
     // ------------------------------------------------------ TMA producer
-    // The Q tiles of the work item that starts about a wave after this one
-    // are read from HBM once: prefetch them into L2 now, so that CTA's first
-    // S waits for L2 instead of HBM.
-    if (KIND != kKindDenseSplit && p.prefetch_ahead > 0) {
-      const long long ahead = static_cast<long long>(lin) + p.prefetch_ahead;
-      int unit2 = 0, pair2 = 0, h2 = 0;
-      if (ahead < static_cast<long long>(gridDim.x) &&
-          decode_item(static_cast<int>(ahead), unit2, pair2, h2)) {
-        int start2 = 0, len2 = p.N;
-        if (!DENSE) {
-          start2 = checked_load(p.cu_seqlens, unit2, p.B + 1, p.status);
-          len2 = min(checked_load(p.cu_seqlens, unit2 + 1, p.B + 1, p.status), p.total_tokens) -
-                 start2;
-        }
-        const int r2 = pair2 * kCtaRows;
-        if (lane == 0 && start2 >= 0 && r2 < len2) {
-          for (int i = 0; i < QT; ++i) {
-            const int t2 = HP ? r2 : r2 + i * kPrefillBM;
-            if (t2 >= len2) break;
+    int k_issued = k0_early ? 1 : 0, v_issued = 0, q_issued = 0;  // over all items
+    bool ok = true;
+    do {
+      // The Q tiles of the work item that starts about a wave after this one
+      // are read from HBM once: prefetch them into L2 now, so that its first
+      // S waits for L2 instead of HBM.
+      if (KIND != kKindDenseSplit && p.prefetch_ahead > 0) {
+        const long long ahead = static_cast<long long>(item) + p.prefetch_ahead;
+        int unit2 = 0, pair2 = 0, h2 = 0;
+        if (ahead < static_cast<long long>(PERS ? p.num_items : gridDim.x) &&
+            decode_item(static_cast<int>(ahead), unit2, pair2, h2)) {
+          int start2 = 0, len2 = p.N;
+          if (!DENSE) {
+            start2 = checked_load(p.cu_seqlens, unit2, p.B + 1, p.status);
+            len2 = min(checked_load(p.cu_seqlens, unit2 + 1, p.B + 1, p.status), p.total_tokens) -
+                   start2;
+          }
+          const int r2 = pair2 * kCtaRows;
+          if (lane == 0 && start2 >= 0 && r2 < len2) {
+            for (int i = 0; i < QT; ++i) {
+              const int t2 = HP ? r2 : r2 + i * kPrefillBM;
+              if (t2 >= len2) break;
 #pragma unroll
-            for (int c = 0; c < L::kChunks; ++c)
-              tma_prefetch_4d(&tm_q, c * L::kChunkElems, HP ? h2 + i : h2, start2 + t2,
-                              DENSE ? unit2 : 0);
+              for (int c = 0; c < L::kChunks; ++c)
+                tma_prefetch_4d(&tm_q, c * L::kChunkElems, HP ? h2 + i : h2, start2 + t2,
+                                DENSE ? unit2 : 0);
+            }
           }
         }
       }
-    }
-    if (lane == 0) {
-      // Issue order K(0) (already issued with Q), then V(j), K(j+1) for
-      // every j: a V load never waits behind a K stage that frees later.
-      int k_issued = k0_early ? 1 : 0, v_issued = 0;
-      auto load_k = [&](int j) -> bool {
-        const int sk = j % SK;
-        if (j >= SK && !mbar_wait(&k_empty[sk], ((j / SK) - 1) & 1, abort_flag, p.status))
-          return false;
-        mbar_arrive_expect_tx(&k_full[sk], L::kTileBytes);
+      if (lane == 0) {
+        // Issue order K(0) (the first item's was issued with Q), Q, then V(j),
+        // K(j+1) for every j: a V load never waits behind a K stage that frees
+        // later.
+        auto load_k = [&](int j) -> bool {
+          const int g = tiles0 + j, sk = g % SK;
+          if (g >= SK && !mbar_wait(&k_empty[sk], ((g / SK) - 1) & 1, abort_flag, p.status))
+            return false;
+          mbar_arrive_expect_tx(&k_full[sk], L::kTileBytes);
 #pragma unroll
-        for (int c = 0; c < L::kChunks; ++c)
-          tma_load_4d(sK + sk * L::kTileBytes + c * L::kChunkBytes, &tm_k, &k_full[sk], c * L::kChunkElems,
-                      kvh, seq_start + key_tile(j) * kPrefillBN, b);
-        k_issued = j + 1;
-        return true;
-      };
-      auto load_v = [&](int j) -> bool {
-        const int sv = j % SV;
-        if (j >= SV && !mbar_wait(&v_empty[sv], ((j / SV) - 1) & 1, abort_flag, p.status))
-          return false;
-        mbar_arrive_expect_tx(&v_full[sv], L::kTileBytes);
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_4d(sK + sk * L::kTileBytes + c * L::kChunkBytes, &tm_k, &k_full[sk],
+                        c * L::kChunkElems, kvh, seq_start + key_tile(j) * kPrefillBN, b);
+          k_issued = g + 1;
+          return true;
+        };
+        auto load_v = [&](int j) -> bool {
+          const int g = tiles0 + j, sv = g % SV;
+          if (g >= SV && !mbar_wait(&v_empty[sv], ((g / SV) - 1) & 1, abort_flag, p.status))
+            return false;
+          mbar_arrive_expect_tx(&v_full[sv], L::kTileBytes);
 #pragma unroll
-        for (int c = 0; c < L::kChunks; ++c)
-          tma_load_4d(sV + sv * L::kTileBytes + c * L::kChunkBytes, &tm_v, &v_full[sv], c * L::kChunkElems,
-                      kvh, seq_start + key_tile(j) * kPrefillBN, b);
-        v_issued = j + 1;
-        return true;
-      };
-      if (n_kv > 0 && (k0_early || load_k(0))) {
-        for (int j = 0; j < n_kv; ++j) {
-          if (!load_v(j)) break;
-          if (j + 1 < n_kv && !load_k(j + 1)) break;
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_4d(sV + sv * L::kTileBytes + c * L::kChunkBytes, &tm_v, &v_full[sv],
+                        c * L::kChunkElems, kvh, seq_start + key_tile(j) * kPrefillBN, b);
+          v_issued = g + 1;
+          return true;
+        };
+        ok = n_kv > 0 && ((turn == 0 && k0_early) || load_k(0));
+        if (PERS && turn > 0 && ok) {
+          ok = mbar_wait(q_free, (turn - 1) & 1, abort_flag, p.status);
+          if (ok) {
+            load_q();
+            q_issued = turn;
+          }
         }
+        for (int j = 0; ok && j < n_kv; ++j)
+          ok = load_v(j) && (j + 1 >= n_kv || load_k(j + 1));
       }
+      if (PERS) ok = __shfl_sync(0xffffffffu, ok, 0);
+    } while (PERS && ok && next_item());
+    if (lane == 0) {
       // Never leave copies in flight into shared memory that is about to be
       // released: wait for the last load of every stage.
-      mbar_drain(q_full, 0, p.status);
+      mbar_drain(q_full, q_issued & 1, p.status);
       for (int j = max(0, k_issued - SK); j < k_issued; ++j)
         mbar_drain(&k_full[j % SK], (j / SK) & 1, p.status);
       for (int j = max(0, v_issued - SV); j < v_issued; ++j)
@@ -966,64 +1026,72 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
       // issued just before it by this thread, reads P_i(j) from; tcgen05 MMAs
       // issued by one thread execute in order.
       // (a split that owns no key tile issues nothing)
-      bool ok = n_kv > 0 && mbar_wait_warp(KV8 ? q_ready : q_full, 0, abort_flag, p.status) &&
-                mbar_wait_warp(&k_full[0], 0, abort_flag, p.status);
-      if (ok) {
-        tc_fence_after();
-        for (int i = 0; i < 2; ++i)
-          if (kv_end[i] > 0) issue_s(i, 0);
-        mma_commit_elect(&k_empty[0]);
-      }
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int sv = j % SV;
-        const int sk1 = (j + 1) % SK;
-        bool k_next = false;
-        auto wait_k_next = [&]() -> bool {
-          if (k_next) return true;
-          if (!mbar_wait_warp(&k_full[sk1], ((j + 1) / SK) & 1, abort_flag, p.status)) return false;
+      bool ok;
+      do {
+        ok = n_kv > 0 && mbar_wait_warp(KV8 ? q_ready : q_full, turn & 1, abort_flag, p.status) &&
+             mbar_wait_warp(&k_full[tiles0 % SK], (tiles0 / SK) & 1, abort_flag, p.status);
+        if (ok) {
           tc_fence_after();
-          k_next = true;
-          return true;
-        };
-        // With dense K/V, V(j) and K(j+1) are usually resident before P_0(j)
-        // is ready: waiting for them first keeps both waits off the path
-        // from P_i(j) to S_i(j+1).  (Their loads never depend on this
-        // iteration's releases, so the order cannot deadlock.)  Gathered
-        // paged K may still be in flight, so that kind waits for K(j+1)
-        // only before the S MMAs that read it.
-        if (!mbar_wait_warp(&v_full[sv], (j / SV) & 1, abort_flag, p.status)) break;
-        if (!PAGED && SK > 1 && j + 1 < n_kv && !wait_k_next()) break;
-        if constexpr (WIN && !PAGED && !DENSE) {
-          // V rows past a packed sequence belong to the next one, or to none:
-          // their weights are 0, but 0 * NaN is NaN, so they are made 0 too
-          const int inside = kv_len - key_tile(j) * kPrefillBN;
-          if (inside < kPrefillBN)
-            zero_tile_rows<L::kChunks, L::kChunkBytes>(sV + sv * L::kTileBytes, inside);
+          for (int i = 0; i < 2; ++i)
+            if (kv_end[i] > 0) issue_s(i, tiles0 % SK);
+          mma_commit_elect(&k_empty[tiles0 % SK]);
+          if (PERS && n_kv == 1) mma_commit_elect(q_free);
         }
-        tc_fence_after();
-        if (j < kv_end[0]) {
-          if (!mbar_wait_warp(&p_full[0], j & 1, abort_flag, p.status)) break;
+        int j = 0;
+        for (; ok && j < n_kv; ++j) {
+          const int g = tiles0 + j;
+          const int sv = g % SV;
+          const int sk1 = (g + 1) % SK;
+          bool k_next = false;
+          auto wait_k_next = [&]() -> bool {
+            if (k_next) return true;
+            if (!mbar_wait_warp(&k_full[sk1], ((g + 1) / SK) & 1, abort_flag, p.status)) return false;
+            tc_fence_after();
+            k_next = true;
+            return true;
+          };
+          // With dense K/V, V(j) and K(j+1) are usually resident before P_0(j)
+          // is ready: waiting for them first keeps both waits off the path
+          // from P_i(j) to S_i(j+1).  (Their loads never depend on this
+          // iteration's releases, so the order cannot deadlock.)  Gathered
+          // paged K may still be in flight, so that kind waits for K(j+1)
+          // only before the S MMAs that read it.
+          if (!mbar_wait_warp(&v_full[sv], (g / SV) & 1, abort_flag, p.status)) break;
+          if (!PAGED && SK > 1 && j + 1 < n_kv && !wait_k_next()) break;
+          if constexpr (WIN && !PAGED && !DENSE) {
+            // V rows past a packed sequence belong to the next one, or to none:
+            // their weights are 0, but 0 * NaN is NaN, so they are made 0 too
+            const int inside = kv_len - key_tile(j) * kPrefillBN;
+            if (inside < kPrefillBN)
+              zero_tile_rows<L::kChunks, L::kChunkBytes>(sV + sv * L::kTileBytes, inside);
+          }
           tc_fence_after();
-          issue_o(0, sv, j);
+          if (j < kv_end[0]) {
+            if (!mbar_wait_warp(&p_full[0], g & 1, abort_flag, p.status)) break;
+            tc_fence_after();
+            issue_o(0, sv, j);
+          }
+          if (j + 1 < kv_end[0]) {
+            if (!wait_k_next()) break;
+            issue_s(0, sk1);
+          }
+          if (j < kv_end[1]) {
+            if (!mbar_wait_warp(&p_full[1], g & 1, abort_flag, p.status)) break;
+            tc_fence_after();
+            issue_o(1, sv, j);
+          }
+          // the V stage of key tile j is free once its P V products are done
+          mma_commit_elect(&v_empty[sv]);
+          if (j + 1 < kv_end[1]) {
+            if (!wait_k_next()) break;
+            issue_s(1, sk1);
+          }
+          // the stage of K(j+1) is free once S_0(j+1) and S_1(j+1) are done
+          if (j + 1 < n_kv) mma_commit_elect(&k_empty[sk1]);
+          if (PERS && j + 2 == n_kv) mma_commit_elect(q_free);  // the last S products are issued
         }
-        if (j + 1 < kv_end[0]) {
-          if (!wait_k_next()) break;
-          issue_s(0, sk1);
-        }
-        if (j < kv_end[1]) {
-          if (!mbar_wait_warp(&p_full[1], j & 1, abort_flag, p.status)) break;
-          tc_fence_after();
-          issue_o(1, sv, j);
-        }
-        // the V stage of key tile j is free once its P V products are done
-        mma_commit_elect(&v_empty[sv]);
-        if (j + 1 < kv_end[1]) {
-          if (!wait_k_next()) break;
-          issue_s(1, sk1);
-        }
-        // the stage of K(j+1) is free once S_0(j+1) and S_1(j+1) are done
-        if (j + 1 < n_kv) mma_commit_elect(&k_empty[sk1]);
-      }
+        ok = ok && j == n_kv;
+      } while (PERS && ok && next_item());
       // Everything this thread issued must finish before TMEM is released.
       mma_commit_elect(drain);
       mbar_drain(drain, 0, p.status);
@@ -1038,393 +1106,407 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + i * 128 + lane_off;
     const uint32_t tO = tmem + L::kTmemO + i * L::kOCols + lane_off;
-    const int qi = tile_row(i) + row;  // query row within the sequence
-    const int hi = tile_head(i);       // query head of this tile
-    const int my_end = kv_end[i];
-    float q_scale = 1.f;  // 8-bit caches: what the scores of this row's codes are multiplied by
-    if constexpr (KV8) {
-      if (my_end > 0) {
-        // Q as two 8-bit terms, each thread its own row, in the tile's place
-        if (mbar_wait_warp(q_full, 0, abort_flag, p.status))
-          q_scale = p.scale_log2 * split_q_row<D>(sQ + i * L::kTileBytes, row, 1 + i);
-        else if (D == 64)
-          named_bar_sync(1 + i, 128);  // (split_q_row's)
-        fence_proxy_async_smem();
-        mbar_arrive(q_ready);
-      }
-    }
-    // (the scores of codes get their scales before the softmax)
-    const float sl2 = KV8 ? 1.f : p.scale_log2;
-    const float2 sl2x2 = make_float2(sl2, sl2);
-    // Reference maximum of the exponentials, log2 units.  It follows the row
-    // maximum, but moves only when the maximum grows by more than
-    // kRescaleLog2: until then every p stays below 2^kRescaleLog2, which the
-    // fp32 sum and the bf16 P operand hold as well as values below 1.  o and
-    // l always share the reference, so o / l is the same result; O in TMEM
-    // is rescaled only when the reference moves.
-    float m_ref = -CUDART_INF_F;
-    float l = 0.f;        // running sum of the bf16 P values, relative to m_ref
-    float l_exact = 0.f;  // running sum of the fp32 exponentials, relative to m_ref
     bool ok = true;
-    // keys [0, limit) are visible to this row (bottom-right causal alignment)
-    const int limit = CAUSAL ? min(kv_len, qi + 1 + offset) : kv_len;
-    const int limit_lo = WIN ? qi + offset + 1 - p.window : 0;  // windowed: and only from here on
-
-    for (int j = 0; j < my_end; ++j) {
-      ok = mbar_wait(&s_full[i], j & 1, abort_flag, p.status);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-
-      uint32_t sr[128];
-      tmem_ld128_wait(tS, sr);
+    do {
+      const int qi = tile_row(i) + row;  // query row within the sequence
+      const int hi = tile_head(i);       // query head of this tile
+      const int my_end = kv_end[i];
+      float q_scale = 1.f;  // 8-bit caches: what the scores of this row's codes are multiplied by
       if constexpr (KV8) {
-        const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kScales) +
-                           (j % L::kScaleSlots) * 2;
-        const float4 k0 = ks[0], k1 = ks[1];
-        const float s8[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-        for (int blk = 0; blk < 8; ++blk) {
-          const float2 c2 = make_float2(s8[blk] * q_scale, s8[blk] * q_scale);
-#pragma unroll
-          for (int c = blk * 16; c < blk * 16 + 16; c += 2) {
-            const float2 x =
-                fmul2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2);
-            sr[c] = __float_as_uint(x.x);
-            sr[c + 1] = __float_as_uint(x.y);
-          }
+        if (my_end > 0) {
+          // Q as two 8-bit terms, each thread its own row, in the tile's place
+          if (mbar_wait_warp(q_full, 0, abort_flag, p.status))
+            q_scale = p.scale_log2 * split_q_row<D>(sQ + i * L::kTileBytes, row, 1 + i);
+          else if (D == 64)
+            named_bar_sync(1 + i, 128);  // (split_q_row's)
+          fence_proxy_async_smem();
+          mbar_arrive(q_ready);
         }
       }
-      const int nvis = limit - key_tile(j) * kPrefillBN;
-      // windowed: keys [sink_c, lo_c) of the tile lie between sinks and window
-      const int lo_c = WIN ? limit_lo - key_tile(j) * kPrefillBN : 0;
-      const int sink_c = WIN ? p.sinks - key_tile(j) * kPrefillBN : 0;
-      // keys past the last one any row of this warp sees (the causal
-      // diagonal): at d = 64, where the softmax bounds the key loop, their
-      // 64-key halves of P are zero without exponentials
-      const int nvis_w = (D == 64 && !WIN) ? __reduce_max_sync(0xffffffffu, nvis) : kPrefillBN;
-      auto f = [&](int c) { return __uint_as_float(sr[c]); };
-      // Windowed: masks as bits, a test and a select a score (three compares a
-      // score took 110 us where this takes 44 us: N 2048, window 500, B4 H16
-      // d64).  Leaving out the 32-key chunks that no row of the warp sees saves
-      // exponentials but was slower (48 us; 598 against 567 us on packed
-      // prompts with a window of 1024): the branches double the code, and the
-      // instruction cache is what a CTA of few key tiles runs short of.
-      if (WIN) {
-        if (__any_sync(0xffffffffu, nvis < kPrefillBN || (lo_c > 0 && sink_c < kPrefillBN))) {
-          auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
+      // (the scores of codes get their scales before the softmax)
+      const float sl2 = KV8 ? 1.f : p.scale_log2;
+      const float2 sl2x2 = make_float2(sl2, sl2);
+      // Reference maximum of the exponentials, log2 units.  It follows the row
+      // maximum, but moves only when the maximum grows by more than
+      // kRescaleLog2: until then every p stays below 2^kRescaleLog2, which the
+      // fp32 sum and the bf16 P operand hold as well as values below 1.  o and
+      // l always share the reference, so o / l is the same result; O in TMEM
+      // is rescaled only when the reference moves.
+      float m_ref = -CUDART_INF_F;
+      float l = 0.f;        // running sum of the bf16 P values, relative to m_ref
+      float l_exact = 0.f;  // running sum of the fp32 exponentials, relative to m_ref
+      // keys [0, limit) are visible to this row (bottom-right causal alignment)
+      const int limit = CAUSAL ? min(kv_len, qi + 1 + offset) : kv_len;
+      const int limit_lo = WIN ? qi + offset + 1 - p.window : 0;  // windowed: and only from here on
+
+      for (int j = 0; j < my_end; ++j) {
+        ok = mbar_wait(&s_full[i], (tiles0 + j) & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+
+        uint32_t sr[128];
+        tmem_ld128_wait(tS, sr);
+        if constexpr (KV8) {
+          const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kScales) +
+                             (j % L::kScaleSlots) * 2;
+          const float4 k0 = ks[0], k1 = ks[1];
+          const float s8[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            const uint32_t seen = below(nvis - 32 * cc) &
-                                  (~below(lo_c - 32 * cc) | below(sink_c - 32 * cc));
+          for (int blk = 0; blk < 8; ++blk) {
+            const float2 c2 = make_float2(s8[blk] * q_scale, s8[blk] * q_scale);
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(seen & (1u << c))) sr[32 * cc + c] = 0xff800000u;  // -inf
-          }
-        }
-      } else if (__any_sync(0xffffffffu, nvis < kPrefillBN)) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= nvis) sr[c] = 0xff800000u;  // -inf
-      }
-      // four independent three-input max chains over the 128 scores
-      float mx0 = f(0), mx1 = f(1), mx2 = f(2), mx3 = f(3);
-#pragma unroll
-      for (int c = 4; c < 124; c += 8) {
-        mx0 = fmax3(mx0, f(c), f(c + 1));
-        mx1 = fmax3(mx1, f(c + 2), f(c + 3));
-        mx2 = fmax3(mx2, f(c + 4), f(c + 5));
-        mx3 = fmax3(mx3, f(c + 6), f(c + 7));
-      }
-      mx0 = fmax3(mx0, f(124), f(125));
-      mx1 = fmax3(mx1, f(126), f(127));
-      const float m_new = fmaxf(m_ref, fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
-      // false while nothing visible has been seen (both -inf)
-      const bool grow = m_new > m_ref + kRescaleLog2;
-      float alpha = 1.f;
-      if (grow) {
-        alpha = ex2(m_ref - m_new);  // 0 on the first visible tile
-        m_ref = m_new;
-      }
-      // NaN guard ("exp(-inf - -inf) is NaN"): a row that has seen no
-      // visible key yet uses the finite reference 0, so every p is 0.
-      const float m_use = (m_ref == -CUDART_INF_F) ? 0.f : m_ref;
-      const float2 negm = make_float2(-m_use, -m_use);
-      // Two row sums: l sums the bf16 values that the P V product multiplies,
-      // so o / l is a weighted mean with consistent weights (with the ones
-      // block, the tensor cores form it in column D of O); l_exact sums the
-      // fp32 exponentials and gives the log-sum-exp.
-      float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
-      float2 re0 = make_float2(0.f, 0.f), re1 = make_float2(0.f, 0.f);
-      // P in two halves of 64 keys, each stored to TMEM as soon as it is packed
-      if (!FP8) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-          if (D == 64 && half * 64 >= nvis_w) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) pk[c] = 0u;
-            tmem_st32(tS + half * 32, pk);
-            continue;
-          }
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const int e = half * 64 + 2 * c;
-            const float2 x0 = ffma2(
-                make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2x2, negm);
-            const float2 x1 = ffma2(
-                make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), sl2x2, negm);
-            const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
-            const float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
-            pk[c] = pack_bf16x2(p0.x, p0.y);
-            pk[c + 1] = pack_bf16x2(p1.x, p1.y);
-            re0 = fadd2(re0, p0);
-            re1 = fadd2(re1, p1);
-            if (!ONES) {
-              add_bf16x2_to(rs0, pk[c]);
-              add_bf16x2_to(rs1, pk[c + 1]);
+            for (int c = blk * 16; c < blk * 16 + 16; c += 2) {
+              const float2 x =
+                  fmul2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), c2);
+              sr[c] = __float_as_uint(x.x);
+              sr[c + 1] = __float_as_uint(x.y);
             }
           }
-          tmem_st32(tS + half * 32, pk);
         }
-      } else {
-        // e4m3 P, four keys per TMEM column.  Its 3-bit mantissa leaves the
-        // weights as they are rounded; both sums use the fp32 exponentials.
+        const int nvis = limit - key_tile(j) * kPrefillBN;
+        // windowed: keys [sink_c, lo_c) of the tile lie between sinks and window
+        const int lo_c = WIN ? limit_lo - key_tile(j) * kPrefillBN : 0;
+        const int sink_c = WIN ? p.sinks - key_tile(j) * kPrefillBN : 0;
+        // keys past the last one any row of this warp sees (the causal
+        // diagonal): at d = 64, where the softmax bounds the key loop, their
+        // 64-key halves of P are zero without exponentials
+        const int nvis_w = (D == 64 && !WIN) ? __reduce_max_sync(0xffffffffu, nvis) : kPrefillBN;
+        auto f = [&](int c) { return __uint_as_float(sr[c]); };
+        // Windowed: masks as bits, a test and a select a score (three compares a
+        // score took 110 us where this takes 44 us: N 2048, window 500, B4 H16
+        // d64).  Leaving out the 32-key chunks that no row of the warp sees saves
+        // exponentials but was slower (48 us; 598 against 567 us on packed
+        // prompts with a window of 1024): the branches double the code, and the
+        // instruction cache is what a CTA of few key tiles runs short of.
+        if (WIN) {
+          if (__any_sync(0xffffffffu, nvis < kPrefillBN || (lo_c > 0 && sink_c < kPrefillBN))) {
+            auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[16];
+            for (int cc = 0; cc < 4; ++cc) {
+              const uint32_t seen = below(nvis - 32 * cc) &
+                                    (~below(lo_c - 32 * cc) | below(sink_c - 32 * cc));
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int e = half * 64 + 4 * c;
-            const float2 x0 = ffma2(
-                make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2x2, negm);
-            const float2 x1 = ffma2(
-                make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), sl2x2, negm);
-            const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
-            const float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
-            pk[c] = pack_e4m3x4(p0.x, p0.y, p1.x, p1.y);
-            re0 = fadd2(re0, p0);
-            re1 = fadd2(re1, p1);
+              for (int c = 0; c < 32; ++c)
+                if (!(seen & (1u << c))) sr[32 * cc + c] = 0xff800000u;  // -inf
+            }
           }
-          tmem_st16(tS + half * 16, pk);
+        } else if (__any_sync(0xffffffffu, nvis < kPrefillBN)) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= nvis) sr[c] = 0xff800000u;  // -inf
         }
-        rs0 = re0;
-        rs1 = re1;
-      }
-      const float2 rs = fadd2(rs0, rs1);
-      const float2 re = fadd2(re0, re1);
-      if (!ONES) l = l * alpha + (rs.x + rs.y);
-      l_exact = l_exact * alpha + (re.x + re.y);
-      if (j > 0 && __any_sync(0xffffffffu, grow)) {
-        const float2 a2 = make_float2(alpha, alpha);
+        // four independent three-input max chains over the 128 scores
+        float mx0 = f(0), mx1 = f(1), mx2 = f(2), mx3 = f(3);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32_wait(tO + c * 32, o);
+        for (int c = 4; c < 124; c += 8) {
+          mx0 = fmax3(mx0, f(c), f(c + 1));
+          mx1 = fmax3(mx1, f(c + 2), f(c + 3));
+          mx2 = fmax3(mx2, f(c + 4), f(c + 5));
+          mx3 = fmax3(mx3, f(c + 6), f(c + 7));
+        }
+        mx0 = fmax3(mx0, f(124), f(125));
+        mx1 = fmax3(mx1, f(126), f(127));
+        const float m_new = fmaxf(m_ref, fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
+        // false while nothing visible has been seen (both -inf)
+        const bool grow = m_new > m_ref + kRescaleLog2;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2(m_ref - m_new);  // 0 on the first visible tile
+          m_ref = m_new;
+        }
+        // NaN guard ("exp(-inf - -inf) is NaN"): a row that has seen no
+        // visible key yet uses the finite reference 0, so every p is 0.
+        const float m_use = (m_ref == -CUDART_INF_F) ? 0.f : m_ref;
+        const float2 negm = make_float2(-m_use, -m_use);
+        // Two row sums: l sums the bf16 values that the P V product multiplies,
+        // so o / l is a weighted mean with consistent weights (with the ones
+        // block, the tensor cores form it in column D of O); l_exact sums the
+        // fp32 exponentials and gives the log-sum-exp.
+        float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
+        float2 re0 = make_float2(0.f, 0.f), re1 = make_float2(0.f, 0.f);
+        // P in two halves of 64 keys, each stored to TMEM as soon as it is packed
+        if (!FP8) {
 #pragma unroll
-          for (int t = 0; t < 32; t += 2) {
-            const float2 v = fmul2(make_float2(__uint_as_float(o[t]), __uint_as_float(o[t + 1])), a2);
-            o[t] = __float_as_uint(v.x);
-            o[t + 1] = __float_as_uint(v.y);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+            if (D == 64 && half * 64 >= nvis_w) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) pk[c] = 0u;
+              tmem_st32(tS + half * 32, pk);
+              continue;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const int e = half * 64 + 2 * c;
+              const float2 x0 = ffma2(
+                  make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2x2, negm);
+              const float2 x1 = ffma2(
+                  make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), sl2x2, negm);
+              const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
+              const float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
+              pk[c] = pack_bf16x2(p0.x, p0.y);
+              pk[c + 1] = pack_bf16x2(p1.x, p1.y);
+              re0 = fadd2(re0, p0);
+              re1 = fadd2(re1, p1);
+              if (!ONES) {
+                add_bf16x2_to(rs0, pk[c]);
+                add_bf16x2_to(rs1, pk[c + 1]);
+              }
+            }
+            tmem_st32(tS + half * 32, pk);
           }
-          tmem_st32(tO + c * 32, o);
-        }
-        if (ONES) {  // the row-sum columns follow O
-          uint32_t o[16];
-          tmem_ld16_wait(tO + D, o);
+        } else {
+          // e4m3 P, four keys per TMEM column.  Its 3-bit mantissa leaves the
+          // weights as they are rounded; both sums use the fp32 exponentials.
 #pragma unroll
-          for (int t = 0; t < 16; t += 2) {
-            const float2 v = fmul2(make_float2(__uint_as_float(o[t]), __uint_as_float(o[t + 1])), a2);
-            o[t] = __float_as_uint(v.x);
-            o[t + 1] = __float_as_uint(v.y);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const int e = half * 64 + 4 * c;
+              const float2 x0 = ffma2(
+                  make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sl2x2, negm);
+              const float2 x1 = ffma2(
+                  make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), sl2x2, negm);
+              const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
+              const float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
+              pk[c] = pack_e4m3x4(p0.x, p0.y, p1.x, p1.y);
+              re0 = fadd2(re0, p0);
+              re1 = fadd2(re1, p1);
+            }
+            tmem_st16(tS + half * 16, pk);
           }
-          tmem_st16(tO + D, o);
+          rs0 = re0;
+          rs1 = re1;
         }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[i]);
-    }
-    const float m = m_ref;
-
-    // ---------------------------------------------------- epilogue
-    if constexpr (KIND == kKindDenseSplit) {
-      // Partial state of this split: o unnormalised (fp32), m (log2 units),
-      // l over the bf16 weights and l over the fp32 exponentials.  A row of
-      // a live tile that got no key tile stores the neutral state.
-      const bool tile_live = row0 + i * kPrefillBM < len;
-      bool have = ok && my_end > 0;
-      if (have) {
-        have = mbar_wait(&o_done[i], 0, abort_flag, p.status);
-        have = __all_sync(0xffffffffu, have);
-      }
-      if (ONES && have) {  // the sum of the bf16 weights, from column D of O
-        tc_fence_after();
-        uint32_t lr[16];
-        tmem_ld16_wait(tO + D, lr);
-        l = __uint_as_float(lr[0]);
-      }
-      if (tile_live && my_end > 0) {
-        // The fp32 tile goes out through the warpgroup's free Q tile (it
-        // holds half of an fp32 tile), half of the columns at a time, with
-        // one TMA store per 32-column chunk of 128-byte swizzled rows; rows
-        // past N are clipped by the tensor bounds.  All four warps meet at
-        // the barriers (the conditions above are the same for the whole
-        // tile); a warp whose wait gave up writes nothing, and the status
-        // word already marks the call as failed.
-        if (have) tc_fence_after();
-        uint8_t *stile = sQ + i * L::kTileBytes;
-        constexpr int kHalfChunks = D / 64;
-        static_assert(kHalfChunks * L::kChunkBytes <= L::kTileBytes, "staging tile too small");
+        const float2 rs = fadd2(rs0, rs1);
+        const float2 re = fadd2(re0, re1);
+        if (!ONES) l = l * alpha + (rs.x + rs.y);
+        l_exact = l_exact * alpha + (re.x + re.y);
+        if (j > 0 && __any_sync(0xffffffffu, grow)) {
+          const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-          for (int cc = 0; have && cc < kHalfChunks; ++cc) {
-            const int c = half * kHalfChunks + cc;  // columns [32 c, 32 c + 32)
+          for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32_wait(tO + c * 32, o);
-            uint8_t *srow = stile + cc * L::kChunkBytes + row * 128;
-            // 128-byte swizzle: 16-byte unit u of row r sits at u ^ (r % 8)
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<uint4 *>(srow + ((u ^ (row & 7)) * 16)) =
-                  make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+            for (int t = 0; t < 32; t += 2) {
+              const float2 v = fmul2(make_float2(__uint_as_float(o[t]), __uint_as_float(o[t + 1])), a2);
+              o[t] = __float_as_uint(v.x);
+              o[t + 1] = __float_as_uint(v.y);
+            }
+            tmem_st32(tO + c * 32, o);
           }
-          fence_proxy_async_smem();
-          named_bar_sync(1 + i, 128);
-          if (row == 0 && have) {
+          if (ONES) {  // the row-sum columns follow O
+            uint32_t o[16];
+            tmem_ld16_wait(tO + D, o);
 #pragma unroll
-            for (int cc = 0; cc < kHalfChunks; ++cc)
-              tma_store_4d(&tm_o, stile + cc * L::kChunkBytes, (half * kHalfChunks + cc) * 32,
-                           h, row0 + i * kPrefillBM, split * p.B + b);
-            tma_store_commit();
-            tma_store_wait_read();
+            for (int t = 0; t < 16; t += 2) {
+              const float2 v = fmul2(make_float2(__uint_as_float(o[t]), __uint_as_float(o[t + 1])), a2);
+              o[t] = __float_as_uint(v.x);
+              o[t + 1] = __float_as_uint(v.y);
+            }
+            tmem_st16(tO + D, o);
           }
-          // the second half reuses the staging tile once the copies have read it
-          if (half == 0) named_bar_sync(1 + i, 128);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[i]);
       }
-      if (tile_live && (have || my_end == 0) && qi < len) {
-        const size_t prow = (static_cast<size_t>(split) * p.B + b) * p.N + qi;
-        if (in_bounds(prow * p.H + h, 1,
-                      static_cast<size_t>(p.num_splits) * p.B * p.N * p.H, p.status))
-          reinterpret_cast<float4 *>(p.ml_part)[prow * p.H + h] =
-            have ? make_float4(m, l, l_exact, 0.f) : make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
-      }
-    } else if (my_end > 0) {
-      if (ok) {
-        ok = mbar_wait(&o_done[i], 0, abort_flag, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      {
-        if (ok) tc_fence_after();
-        if (ONES && ok) {  // the sum of the bf16 weights, from column D of O
+      const float m = m_ref;
+
+      // ---------------------------------------------------- epilogue
+      if constexpr (KIND == kKindDenseSplit) {
+        // Partial state of this split: o unnormalised (fp32), m (log2 units),
+        // l over the bf16 weights and l over the fp32 exponentials.  A row of
+        // a live tile that got no key tile stores the neutral state.
+        const bool tile_live = row0 + i * kPrefillBM < len;
+        bool have = ok && my_end > 0;
+        if (have) {
+          have = mbar_wait(&o_done[i], 0, abort_flag, p.status);
+          have = __all_sync(0xffffffffu, have);
+        }
+        if (ONES && have) {  // the sum of the bf16 weights, from column D of O
+          tc_fence_after();
           uint32_t lr[16];
           tmem_ld16_wait(tO + D, lr);
           l = __uint_as_float(lr[0]);
         }
-        const bool live = qi < len;
-        const float inv_l = (l > 0.f) ? p.v_descale / l : 0.f;
-        // A whole bf16 tile goes out through shared memory and one TMA store
-        // per 64-column chunk (rows past the end of a dense sequence are
-        // clipped by the tensor bounds).  The warpgroup's Q tile is free: its
-        // last S MMA completed before the last S tile was handed over.  An
-        // fp8 Q tile holds half of the bf16 output tile at d = 128, so the
-        // tile leaves in two passes of 64 columns; at d = 64 (a quarter) and
-        // for a partial tile of a packed layout, whose tail rows belong to
-        // the next sequence, the rows are written one by one instead.
-        constexpr int kOutChunkBytes = 128 * 128;  // 128 rows x 64 bf16 columns
-        constexpr int kPasses = FP8 ? 2 : 1;
-        constexpr int kPassCols = D / 32 / kPasses;  // 32-column TMEM chunks per pass
-        const bool tma_out =
-            (!FP8 || D == 128) && (DENSE || tile_row(i) + kPrefillBM <= len);
-        if (tma_out) {
-          // All four warps of the tile meet at the barriers below (my_end and
-          // tma_out are the same for the whole tile); a warp whose wait gave
-          // up writes nothing, and the status word already marks the call as
-          // failed.
+        if (tile_live && my_end > 0) {
+          // The fp32 tile goes out through the warpgroup's free Q tile (it
+          // holds half of an fp32 tile), half of the columns at a time, with
+          // one TMA store per 32-column chunk of 128-byte swizzled rows; rows
+          // past N are clipped by the tensor bounds.  All four warps meet at
+          // the barriers (the conditions above are the same for the whole
+          // tile); a warp whose wait gave up writes nothing, and the status
+          // word already marks the call as failed.
+          if (have) tc_fence_after();
           uint8_t *stile = sQ + i * L::kTileBytes;
-          static_assert(kPassCols / 2 * kOutChunkBytes <= L::kTileBytes, "output staging tile");
+          constexpr int kHalfChunks = D / 64;
+          static_assert(kHalfChunks * L::kChunkBytes <= L::kTileBytes, "staging tile too small");
 #pragma unroll
-          for (int pass = 0; pass < kPasses; ++pass) {
+          for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int cc = 0; ok && cc < kPassCols; ++cc) {
-            const int c = pass * kPassCols + cc;
-            uint32_t o[32];
-            tmem_ld32_wait(tO + c * 32, o);
-            uint8_t *srow = stile + (cc >> 1) * kOutChunkBytes + row * 128;
-#pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(o[v4 * 8 + 0]) * inv_l,
-                                __uint_as_float(o[v4 * 8 + 1]) * inv_l);
-              w.y = pack_bf16x2(__uint_as_float(o[v4 * 8 + 2]) * inv_l,
-                                __uint_as_float(o[v4 * 8 + 3]) * inv_l);
-              w.z = pack_bf16x2(__uint_as_float(o[v4 * 8 + 4]) * inv_l,
-                                __uint_as_float(o[v4 * 8 + 5]) * inv_l);
-              w.w = pack_bf16x2(__uint_as_float(o[v4 * 8 + 6]) * inv_l,
-                                __uint_as_float(o[v4 * 8 + 7]) * inv_l);
+            for (int cc = 0; have && cc < kHalfChunks; ++cc) {
+              const int c = half * kHalfChunks + cc;  // columns [32 c, 32 c + 32)
+              uint32_t o[32];
+              tmem_ld32_wait(tO + c * 32, o);
+              uint8_t *srow = stile + cc * L::kChunkBytes + row * 128;
               // 128-byte swizzle: 16-byte unit u of row r sits at u ^ (r % 8)
-              const int u = ((c & 1) * 4 + v4) ^ (row & 7);
-              *reinterpret_cast<uint4 *>(srow + u * 16) = w;
-            }
-          }
-          fence_proxy_async_smem();
-          named_bar_sync(1 + i, 128);
-          if (row == 0 && ok) {
-            const int orow = (DENSE ? 0 : seq_start) + tile_row(i);
 #pragma unroll
-            for (int c = 0; c < kPassCols / 2; ++c)
-              tma_store_4d(&tm_o, stile + c * kOutChunkBytes, (pass * kPassCols / 2 + c) * 64, hi,
-                           orow, b);
-            tma_store_commit();
-            tma_store_wait_read();
-          }
-          // the next pass reuses the staging tile once the copies have read it
-          if (pass + 1 < kPasses) named_bar_sync(1 + i, 128);
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<uint4 *>(srow + ((u ^ (row & 7)) * 16)) =
+                    make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(1 + i, 128);
+            if (row == 0 && have) {
+#pragma unroll
+              for (int cc = 0; cc < kHalfChunks; ++cc)
+                tma_store_4d(&tm_o, stile + cc * L::kChunkBytes, (half * kHalfChunks + cc) * 32,
+                             h, row0 + i * kPrefillBM, split * p.B + b);
+              tma_store_commit();
+              tma_store_wait_read();
+            }
+            // the second half reuses the staging tile once the copies have read it
+            if (half == 0) named_bar_sync(1 + i, 128);
           }
         }
-        size_t out_row;
-        if (!DENSE)
-          out_row = static_cast<size_t>(seq_start + qi);
-        else
-          out_row = static_cast<size_t>(b) * p.N + qi;
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) +
-                                               ((out_row * p.H + hi) * D) * 2);
-        // rows of the output (and of the log-sum-exp) the call owns
-        const size_t out_rows =
-            DENSE ? static_cast<size_t>(p.B) * p.N : static_cast<size_t>(p.total_tokens);
-        const bool row_ok =
-            !live || tma_out || in_bounds((out_row * p.H + hi) * D, D, out_rows * p.H * D, p.status);
+        if (tile_live && (have || my_end == 0) && qi < len) {
+          const size_t prow = (static_cast<size_t>(split) * p.B + b) * p.N + qi;
+          if (in_bounds(prow * p.H + h, 1,
+                        static_cast<size_t>(p.num_splits) * p.B * p.N * p.H, p.status))
+            reinterpret_cast<float4 *>(p.ml_part)[prow * p.H + h] =
+              have ? make_float4(m, l, l_exact, 0.f) : make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+        }
+      } else if (my_end > 0) {
+        if (ok) {
+          ok = mbar_wait(&o_done[i], turn & 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        {
+          if (ok) tc_fence_after();
+          if (ONES && ok) {  // the sum of the bf16 weights, from column D of O
+            uint32_t lr[16];
+            tmem_ld16_wait(tO + D, lr);
+            l = __uint_as_float(lr[0]);
+          }
+          const bool live = qi < len;
+          const float inv_l = (l > 0.f) ? p.v_descale / l : 0.f;
+          // A whole bf16 tile goes out through shared memory and one TMA store
+          // per 64-column chunk (rows past the end of a dense sequence are
+          // clipped by the tensor bounds).  The warpgroup's Q tile is free: its
+          // last S MMA completed before the last S tile was handed over.  An
+          // fp8 Q tile holds half of the bf16 output tile at d = 128, so the
+          // tile leaves in two passes of 64 columns; at d = 64 (a quarter) and
+          // for a partial tile of a packed layout, whose tail rows belong to
+          // the next sequence, the rows are written one by one instead.
+          constexpr int kOutChunkBytes = 128 * 128;  // 128 rows x 64 bf16 columns
+          // A persistent CTA's Q tile is the next item's by then: its rows are
+          // exchanged between lanes and written from registers.
+          constexpr int kPasses = FP8 ? 2 : 1;
+          constexpr int kPassCols = D / 32 / kPasses;  // 32-column TMEM chunks per pass
+          const bool tma_out =
+              !PERS && (!FP8 || D == 128) && (DENSE || tile_row(i) + kPrefillBM <= len);
+          if (tma_out) {
+            // All four warps of the tile meet at the barriers below (my_end and
+            // tma_out are the same for the whole tile); a warp whose wait gave
+            // up writes nothing, and the status word already marks the call as
+            // failed.
+            uint8_t *stile = sQ + i * L::kTileBytes;
+            static_assert(kPassCols / 2 * kOutChunkBytes <= L::kTileBytes, "output staging tile");
 #pragma unroll
-        for (int c = 0; ok && !tma_out && c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32_wait(tO + c * 32, o);  // warp-wide: every lane loads
-          if (live && row_ok) {
+            for (int pass = 0; pass < kPasses; ++pass) {
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(o[v4 * 8 + 0]) * inv_l,
-                                __uint_as_float(o[v4 * 8 + 1]) * inv_l);
-              w.y = pack_bf16x2(__uint_as_float(o[v4 * 8 + 2]) * inv_l,
-                                __uint_as_float(o[v4 * 8 + 3]) * inv_l);
-              w.z = pack_bf16x2(__uint_as_float(o[v4 * 8 + 4]) * inv_l,
-                                __uint_as_float(o[v4 * 8 + 5]) * inv_l);
-              w.w = pack_bf16x2(__uint_as_float(o[v4 * 8 + 6]) * inv_l,
-                                __uint_as_float(o[v4 * 8 + 7]) * inv_l);
-              dst[c * 4 + v4] = w;
+            for (int cc = 0; ok && cc < kPassCols; ++cc) {
+              const int c = pass * kPassCols + cc;
+              uint32_t o[32];
+              tmem_ld32_wait(tO + c * 32, o);
+              uint8_t *srow = stile + (cc >> 1) * kOutChunkBytes + row * 128;
+#pragma unroll
+              for (int v4 = 0; v4 < 4; ++v4) {
+                uint4 w;
+                w.x = pack_bf16x2(__uint_as_float(o[v4 * 8 + 0]) * inv_l,
+                                  __uint_as_float(o[v4 * 8 + 1]) * inv_l);
+                w.y = pack_bf16x2(__uint_as_float(o[v4 * 8 + 2]) * inv_l,
+                                  __uint_as_float(o[v4 * 8 + 3]) * inv_l);
+                w.z = pack_bf16x2(__uint_as_float(o[v4 * 8 + 4]) * inv_l,
+                                  __uint_as_float(o[v4 * 8 + 5]) * inv_l);
+                w.w = pack_bf16x2(__uint_as_float(o[v4 * 8 + 6]) * inv_l,
+                                  __uint_as_float(o[v4 * 8 + 7]) * inv_l);
+                // 128-byte swizzle: 16-byte unit u of row r sits at u ^ (r % 8)
+                const int u = ((c & 1) * 4 + v4) ^ (row & 7);
+                *reinterpret_cast<uint4 *>(srow + u * 16) = w;
+              }
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(1 + i, 128);
+            if (row == 0 && ok) {
+              const int orow = (DENSE ? 0 : seq_start) + tile_row(i);
+#pragma unroll
+              for (int c = 0; c < kPassCols / 2; ++c)
+                tma_store_4d(&tm_o, stile + c * kOutChunkBytes, (pass * kPassCols / 2 + c) * 64, hi,
+                             orow, b);
+              tma_store_commit();
+              tma_store_wait_read();
+            }
+            // the next pass reuses the staging tile once the copies have read it
+            if (pass + 1 < kPasses) named_bar_sync(1 + i, 128);
             }
           }
-        }
-        const size_t lse_idx = !DENSE
-                                   ? static_cast<size_t>(hi) * p.total_tokens + seq_start + qi
-                                   : (static_cast<size_t>(b) * p.H + hi) * p.N + qi;
-        if (ok && live && p.lse != nullptr && in_bounds(lse_idx, 1, out_rows * p.H, p.status)) {
-          p.lse[lse_idx] = (l_exact > 0.f) ? (m + __log2f(l_exact)) * 0.69314718055994530942f
-                                           : -CUDART_INF_F;
+          size_t out_row;
+          if (!DENSE)
+            out_row = static_cast<size_t>(seq_start + qi);
+          else
+            out_row = static_cast<size_t>(b) * p.N + qi;
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) +
+                                                 ((out_row * p.H + hi) * D) * 2);
+          // rows of the output (and of the log-sum-exp) the call owns
+          const size_t out_rows =
+              DENSE ? static_cast<size_t>(p.B) * p.N : static_cast<size_t>(p.total_tokens);
+          const bool row_ok =
+              !live || tma_out || in_bounds((out_row * p.H + hi) * D, D, out_rows * p.H * D, p.status);
+          if constexpr (PERS) {
+#pragma unroll
+            for (int half = 0; ok && half < 2; ++half) {
+              uint32_t o[D / 64][32];
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) tmem_ld32_wait(tO + (half * (D / 64) + c) * 32, o[c]);
+              store_half_rows_bf16<D>(reinterpret_cast<uint16_t *>(dst) + half * (D / 2),
+                                      static_cast<size_t>(p.H) * D, live && row_ok, o, inv_l);
+            }
+          }
+#pragma unroll
+          for (int c = 0; !PERS && ok && !tma_out && c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32_wait(tO + c * 32, o);  // warp-wide: every lane loads
+            if (live && row_ok) {
+#pragma unroll
+              for (int v4 = 0; v4 < 4; ++v4) {
+                uint4 w;
+                w.x = pack_bf16x2(__uint_as_float(o[v4 * 8 + 0]) * inv_l,
+                                  __uint_as_float(o[v4 * 8 + 1]) * inv_l);
+                w.y = pack_bf16x2(__uint_as_float(o[v4 * 8 + 2]) * inv_l,
+                                  __uint_as_float(o[v4 * 8 + 3]) * inv_l);
+                w.z = pack_bf16x2(__uint_as_float(o[v4 * 8 + 4]) * inv_l,
+                                  __uint_as_float(o[v4 * 8 + 5]) * inv_l);
+                w.w = pack_bf16x2(__uint_as_float(o[v4 * 8 + 6]) * inv_l,
+                                  __uint_as_float(o[v4 * 8 + 7]) * inv_l);
+                dst[c * 4 + v4] = w;
+              }
+            }
+          }
+          const size_t lse_idx = !DENSE
+                                     ? static_cast<size_t>(hi) * p.total_tokens + seq_start + qi
+                                     : (static_cast<size_t>(b) * p.H + hi) * p.N + qi;
+          if (ok && live && p.lse != nullptr && in_bounds(lse_idx, 1, out_rows * p.H, p.status)) {
+            p.lse[lse_idx] = (l_exact > 0.f) ? (m + __log2f(l_exact)) * 0.69314718055994530942f
+                                             : -CUDART_INF_F;
+          }
         }
       }
-    }
+    } while (PERS && ok && next_item());
   }
 
   __syncwarp();
@@ -1439,14 +1521,14 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8>::kThreads, PrefillShape<
 // ------------------------------------------------------------------ launch
 
 template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false,
-          bool KV8 = false>
+          bool KV8 = false, bool PERS = false>
 static cudaError_t launch_prefill_t(const CUtensorMap &tq, const CUtensorMap &tk,
                                     const CUtensorMap &tv, const CUtensorMap &tv1,
                                     const CUtensorMap &to, const PrefillParams &p, int grid,
                                     cudaStream_t stream) {
-  using L = PrefillLayout<D, FP8, QT, KV8>;
-  using Sh = PrefillShape<QT, KV8>;
-  auto kern = prefill_kernel<D, CAUSAL, KIND, FP8, QT, WIN, KV8>;
+  using L = PrefillLayout<D, FP8, QT, KV8, PERS>;
+  using Sh = PrefillShape<QT, KV8, PERS>;
+  auto kern = prefill_kernel<D, CAUSAL, KIND, FP8, QT, WIN, KV8, PERS>;
   if constexpr (Sh::kSplitRegs) {
     // The setmaxnreg split assumes kPrefill1LaunchRegs registers per thread
     // at launch; with fewer, the register increase could never be granted,
@@ -1460,7 +1542,10 @@ static cudaError_t launch_prefill_t(const CUtensorMap &tq, const CUtensorMap &tk
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
   if (e != cudaSuccess) return e;
-  kern<<<grid, Sh::kThreads, L::kSmemAlloc, stream>>>(tq, tk, tv, tv1, to, p);
+  PrefillParams pp = p;
+  pp.num_items = grid;
+  if (PERS) grid = std::min(grid, std::max(1, p.prefetch_ahead));  // (one CTA an SM)
+  kern<<<grid, Sh::kThreads, L::kSmemAlloc, stream>>>(tq, tk, tv, tv1, to, pp);
   return cudaGetLastError();
 }
 

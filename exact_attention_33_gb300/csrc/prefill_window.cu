@@ -12,18 +12,39 @@
 
 namespace fa {
 
+// A head-pair item of a short window is a few key tiles long, and what a CTA
+// spends before and after them (set-up, the first copies, the epilogue) a
+// quarter of its time.  Persistent CTAs, one an SM, take the items in turn, and
+// the next item's copies and first products run beside the last softmax and the
+// epilogue.  They take fixed shares, so the items have to be alike: sequences of
+// some windows' length.  In us, one CTA an item / persistent (32 / 8 heads,
+// N = 16384, B = 1; the last two 16 / 4 heads, B = 8):
+//   d    window 512   1024        2048        4096        N 2048, 512  N 2048, 1024
+//   128  187 / 165    261 / 246   400 / 400   658 / 687   98 / 93      119 / 121
+//   64   160 / 138    222 / 202   341 / 325   558 / 556   83 / 78      101 / 101
+constexpr int kPersistentKeys = 1536;
+
 template <int D>
 static cudaError_t launch_prefill_window_d(const CUtensorMap &tq, const CUtensorMap &tk,
                                            const CUtensorMap &tv, const CUtensorMap &tv1,
                                            const CUtensorMap &to, const PrefillParams &p, int kind,
                                            int grid, cudaStream_t stream) {
+  const long long reach = static_cast<long long>(p.window) + p.sinks;
+  const bool persistent = grid > p.prefetch_ahead && reach <= kPersistentKeys &&
+                          3 * reach <= static_cast<long long>(p.max_pairs) * kPrefillBM;
   switch (kind) {
     case kKindDenseHeads:
-      return launch_prefill_t<D, true, kKindDenseHeads, false, 2, true>(tq, tk, tv, tv1, to, p, grid,
-                                                                       stream);
+      return persistent
+                 ? launch_prefill_t<D, true, kKindDenseHeads, false, 2, true, false, true>(
+                       tq, tk, tv, tv1, to, p, grid, stream)
+                 : launch_prefill_t<D, true, kKindDenseHeads, false, 2, true>(tq, tk, tv, tv1, to, p,
+                                                                             grid, stream);
     case kKindVarlenHeads:
-      return launch_prefill_t<D, true, kKindVarlenHeads, false, 2, true>(tq, tk, tv, tv1, to, p,
-                                                                        grid, stream);
+      return persistent
+                 ? launch_prefill_t<D, true, kKindVarlenHeads, false, 2, true, false, true>(
+                       tq, tk, tv, tv1, to, p, grid, stream)
+                 : launch_prefill_t<D, true, kKindVarlenHeads, false, 2, true>(tq, tk, tv, tv1, to, p,
+                                                                              grid, stream);
     case kKindPagedHeads:
       return launch_prefill_t<D, true, kKindPagedHeads, false, 2, true>(tq, tk, tv, tv1, to, p, grid,
                                                                        stream);

@@ -151,6 +151,56 @@ def test_packed_with_gradient(fa, lens, H, Hkv, d, window, sinks):
         check_gradient(dq[r], dk[r], dv[r], q[r], k[r], v[r], g[r], window, sinks, f"rows {a}:{b}")
 
 
+# more work items than SMs, behind one another in the same CTAs
+MANY = [
+    ([2048, 2048], 16, 4, 128, 200, 5),
+    ([4096], 32, 8, 64, 129, 0),
+    ([1500, 3, 0, 700, 2900, 1, 129, 128], 16, 4, 128, 300, 140),
+    ([3000] + [40] * 140, 8, 2, 64, 100, 3),        # beyond the padding-free order
+    ([1300, 1, 1291], 24, 4, 128, 1, 0),
+]
+
+
+@pytest.mark.parametrize("lens,H,Hkv,d,window,sinks", MANY)
+def test_many_items(fa, lens, H, Hkv, d, window, sinks):
+    torch = torch_mod()
+    cu = cu_of(lens)
+    q, k, v = (normal(140 + i, cu[-1] + 3, h, d) for i, h in enumerate((H, Hkv, Hkv)))
+    q[-3:], k[-3:], v[-3:] = math.nan, math.nan, math.nan     # of no sequence
+    out = torch.full_like(q, 7.0)
+    _, lse = fa.fa_fwd_varlen_window(q, k, v, i32(cu), max(lens), window, sinks, out=out)
+    assert_device_clean()
+    assert bool((out[-3:] == 7.0).all())
+    for n in sorted(set(lens)):
+        a = cu[lens.index(n)]
+        if n:
+            check_rows(out[a:a + n], lse[:, a:a + n], q[a:a + n], k[a:a + n], v[a:a + n], window,
+                       sinks, f"{n} rows")
+    if lens[0] == lens[-1]:
+        q, k, v = (t[:-3].reshape(len(lens), lens[0], -1, d) for t in (q, k, v))
+        dense, dlse = fa.fa_fwd_window(q, k, v, window, sinks)
+        assert_device_clean()
+        for b in range(len(lens)):
+            check_rows(dense[b], dlse[b], q[b], k[b], v[b], window, sinks, f"dense {b}")
+
+
+def test_bad_sequence_among_many(fa):
+    """A sequence with bad bounds is reported and passed over; the CTAs that meet
+    it go on."""
+    torch = torch_mod()
+    for count in (3, 140):                       # with and beyond the padding-free order
+        lens = [1500] + [30] * (count - 3) + [1500, 300]
+        cu = cu_of(lens)
+        q, k, v = (normal(150 + i, cu[-1], h, 128) for i, h in enumerate((16, 4, 4)))
+        bad = list(cu)
+        bad[-1] += 1                             # the last ends past the rows
+        out, lse = fa.fa_fwd_varlen_window(q, k, v, i32(bad), 1500, 200, 4)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status(clear=True) == fa.FA_DEV_BAD_SEQLEN
+        for a, e in ((cu[0], cu[1]), (cu[-3], cu[-2])):
+            check_rows(out[a:e], lse[:, a:e], q[a:e], k[a:e], v[a:e], 200, 4, f"{count}, row {a}")
+
+
 def test_values_of_another_sequence_do_not_matter(fa):
     """A sequence next to one of infinities and NaN gives the same bits."""
     torch = torch_mod()
