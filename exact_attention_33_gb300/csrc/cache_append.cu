@@ -25,7 +25,7 @@ namespace fa {
 
 namespace {
 
-// Small CTAs at high occupancy: 43 us for 34.8 k tokens of 8 heads of d = 128
+// Small CTAs at high occupancy: 44 us for 34.8 k tokens of 8 heads of d = 128
 // (214 MB; 4 warps, 10 CTAs per SM) against 47-49 us for 8 warps and 63 us for
 // 16, whose slowest warp holds the others' registers.
 constexpr int kAppendWarps = 4;

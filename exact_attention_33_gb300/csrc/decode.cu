@@ -24,7 +24,8 @@
 // A windowed call (WIN) reads the blocks of the sinks and of the window alone
 // and masks the hidden tokens of the first window block and the last sink
 // block as it masks slots past the context; its splits run over the blocks
-// that are read.
+// that are read (64 sequences of 512 to 32768 keys, 32 / 8 heads of d = 128,
+// window 4096: 165 us for 1.02 GB, 6.2 TB/s).
 //
 // decode_combine_kernel: one CTA per (sequence, query head) merges the
 // partial states: M = max m_i, L = sum 2^(m_i - M) l_i,

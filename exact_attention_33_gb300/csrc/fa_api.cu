@@ -386,9 +386,13 @@ namespace {
 // BwdParams).  One item over all of them would run for as long as the sequence
 // (N 16384, 16 sinks, window 500: 1390 us for the whole backward pass against
 // 632 us without sinks); a slice is as long as a tile's own window, so that
-// items are alike.  Beyond kSinkTiles tiles of sinks there are enough of them
-// to fill the GPU, and their partial sums would outgrow the gradients.
+// items are alike, but the slices of all sequences are at most kSinkSlots (or 4
+// of each): with that many the GPU is full, and a slot takes 1 KiB d of
+// workspace for every sequence, however short.  Beyond kSinkTiles tiles of
+// sinks there are enough of them to fill the GPU, and their partial sums would
+// outgrow the gradients.
 constexpr int kSinkTiles = 2;
+constexpr long long kSinkSlots = 4096;
 struct SinkSlices {
   int tiles = 0, slices = 0, slice = 0;
   size_t part_bytes = 0;
@@ -401,7 +405,9 @@ SinkSlices sink_slices(int B, int Hkv, int N, int d, WindowSpec w) {
   const int span = static_cast<int>(std::min<long long>(n_q, (w.window + 126LL) / 128 + 1));
   if (tiles == 0 || tiles > kSinkTiles || n_q <= span) return s;
   s.tiles = tiles;
-  s.slice = std::max(4, span);
+  const long long most =
+      std::max(4LL, kSinkSlots / (static_cast<long long>(B) * Hkv * tiles));
+  s.slice = static_cast<int>(std::max<long long>(std::max(4, span), (n_q - span + most - 1) / most));
   s.slices = (n_q - span + s.slice - 1) / s.slice;
   s.part_bytes = static_cast<size_t>(B) * Hkv * tiles * (1 + s.slices) * 2 * 128 * d * sizeof(float);
   return s;

@@ -109,8 +109,7 @@ struct PrefillLayout {
   // q_full, k_full[SK], k_empty[SK], v_full[SV], s_full[2], p_full[2],
   // o_done[2], drain, v_empty[SV], and over an 8-bit cache c_full[2],
   // c_empty[2] of V's staged codes and q_ready, in a persistent CTA q_free.  A V
-  // stage is released as soon
-  // as the P V products of its key tile are done.
+  // stage is released as soon as the P V products of its key tile are done.
   static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7 + (KV8 ? 5 : 0) + (PERS ? 1 : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;

@@ -511,3 +511,17 @@ def test_gradient_under_load(fa):
         first = first or grads
         assert_device_clean()
     assert all(torch.equal(a, b) for a, b in zip(grads, first))
+
+
+def test_sinks_of_one_long_sequence_among_many(fa):
+    """Few slices of the sinks' queries for each sequence: longer ones."""
+    H, Hkv, d, window, sinks, n = 2, 2, 64, 16, 2, 4000
+    lens = [n] + [1] * 599
+    cu = cu_of(lens)
+    q, k, v, g = (normal(160 + i, cu[-1], h, d) for i, h in enumerate((H, Hkv, Hkv, H)))
+    args = (i32(cu), n, window, sinks)
+    out, lse = fa.fa_fwd_varlen_window(q, k, v, *args)
+    dq, dk, dv = fa.fa_bwd_varlen_window(q, k, v, out, lse, g, *args)
+    assert_device_clean()
+    for a, e in ((0, n), (n, n + 1), (cu[-2], cu[-1])):
+        check_gradient(*(t[a:e] for t in (dq, dk, dv, q, k, v, g)), window, sinks, f"row {a}")

@@ -88,6 +88,11 @@ def test_workspace_sizes(lib):
     assert fa.fa_bwd_window_workspace_size(1, 4, 2, 256, 64, 100) >= fa.fa_bwd_workspace_size(1, 4, 256)
     with pytest.raises(ValueError):
         fa.fa_bwd_window_workspace_size(1, 4, 2, 256, 64, 0)
+    # the sinks' partial sums do not grow with sequences that are there already
+    long, many = (fa.fa_bwd_window_workspace_size(n, 8, 8, 65536, 128, 64, 4) for n in (1, 1000))
+    vectors = fa.fa_bwd_workspace_size(1000, 8, 65536)
+    assert many - vectors < 8 * 1000 * 6 * 2 * 128 * 128 * 4
+    assert long < 1 << 30
 
 
 def test_binding_rejects_host_tensors():
