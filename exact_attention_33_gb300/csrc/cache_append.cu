@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
   }
   const int first = ctx - n;  // position of the first new token
   const int blk = first / kDecodeBlock + nth;
+  if (n == 0 || blk > (ctx - 1) / kDecodeBlock) return;
   const int pos0 = blk * kDecodeBlock;
-  if (n == 0 || pos0 >= ctx) return;
   const int s0 = max(0, first - pos0), s1 = min(kDecodeBlock, ctx - pos0);  // new slots
 
   // the new rows: lane reads values [8 c, 8 c + 8) of rows kRows i + r
