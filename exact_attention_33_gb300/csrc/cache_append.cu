@@ -25,9 +25,10 @@ namespace fa {
 
 namespace {
 
-// Small CTAs at high occupancy: 44 us for 34.8 k tokens of 8 heads of d = 128
-// (214 MB; 4 warps, 10 CTAs per SM) against 47-49 us for 8 warps and 63 us for
-// 16, whose slowest warp holds the others' registers.
+// Small CTAs at high occupancy, 4 warps and 10 CTAs per SM: 34.8 k tokens of 8
+// heads of d = 128 (214 MB) take 41 us.  (With an older maximum and division, 47
+// us, 8 warps took 50 us and 16 took 66, whose slowest warp holds the others'
+// registers; 8 or 9 CTAs take as long as 10 at d = 128 and 2 us more at d = 64.)
 constexpr int kAppendWarps = 4;
 constexpr int kAppendCtas = 10;
 constexpr int kMinScaleExp = -100;
@@ -114,15 +115,28 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
   const size_t n_scales = static_cast<size_t>(p.num_blocks) * p.Hkv;
   const float old = s0 > 0 ? checked_load(scales, sidx, n_scales, p.status) : 0.f;
 
-  uint32_t m = 0;
+  // largest magnitude, both halves of a word at once; a warp that meets an
+  // infinity or a NaN looks again at the finite ones
+  uint32_t m2 = 0;
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    m = finite_max(m, x[i].x);
-    m = finite_max(m, x[i].y);
-    m = finite_max(m, x[i].z);
-    m = finite_max(m, x[i].w);
+    m2 = __vmaxu2(m2, x[i].x & 0x7FFF7FFFu);
+    m2 = __vmaxu2(m2, x[i].y & 0x7FFF7FFFu);
+    m2 = __vmaxu2(m2, x[i].z & 0x7FFF7FFFu);
+    m2 = __vmaxu2(m2, x[i].w & 0x7FFF7FFFu);
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+  if (m >= 0x7F80u) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      m = finite_max(m, x[i].x);
+      m = finite_max(m, x[i].y);
+      m = finite_max(m, x[i].z);
+      m = finite_max(m, x[i].w);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+  }
   const float need = pow2(scale_exponent(m));
   const float scale = fmaxf(old, need);  // (a NaN or negative old scale counts as none)
 
@@ -153,18 +167,24 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
   // A power of two is divided by through its reciprocal, which is exact; a
   // scale that someone else wrote may be none.
   const bool is_pow2 = (__float_as_uint(scale) & 0x007FFFFFu) == 0u;
-  const float inv = 1.f / scale;
-  auto code = [&](float v) { return is_pow2 ? v * inv : v / scale; };
+  auto write = [&](auto code) {
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const int slot = i * kRows + r;
-    if (slot < s0 || slot >= s1) continue;
-    const float2 a = bf16x2_to_float2(x[i].x), e = bf16x2_to_float2(x[i].y);
-    const float2 f = bf16x2_to_float2(x[i].z), g = bf16x2_to_float2(x[i].w);
-    uint2 w;
-    w.x = pack_e4m3x4(code(a.x), code(a.y), code(e.x), code(e.y));
-    w.y = pack_e4m3x4(code(f.x), code(f.y), code(g.x), code(g.y));
-    if (in_bounds(at(slot), 8, n_pool, p.status)) *reinterpret_cast<uint2 *>(pool + at(slot)) = w;
+    for (int i = 0; i < kIter; ++i) {
+      const int slot = i * kRows + r;
+      if (slot < s0 || slot >= s1) continue;
+      const float2 a = code(bf16x2_to_float2(x[i].x)), e = code(bf16x2_to_float2(x[i].y));
+      const float2 f = code(bf16x2_to_float2(x[i].z)), g = code(bf16x2_to_float2(x[i].w));
+      uint2 w;
+      w.x = pack_e4m3x4(a.x, a.y, e.x, e.y);
+      w.y = pack_e4m3x4(f.x, f.y, g.x, g.y);
+      if (in_bounds(at(slot), 8, n_pool, p.status)) *reinterpret_cast<uint2 *>(pool + at(slot)) = w;
+    }
+  };
+  if (is_pow2) {
+    const float2 inv = make_float2(1.f / scale, 1.f / scale);
+    write([&](float2 v) { return fmul2(v, inv); });
+  } else {
+    write([&](float2 v) { return make_float2(v.x / scale, v.y / scale); });
   }
   if (lane == 0 && scale != old && in_bounds(sidx, 1, n_scales, p.status)) scales[sidx] = scale;
 }
