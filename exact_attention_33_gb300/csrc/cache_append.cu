@@ -26,9 +26,10 @@ namespace fa {
 namespace {
 
 // Small CTAs at high occupancy, 4 warps and 10 CTAs per SM: 34.8 k tokens of 8
-// heads of d = 128 (214 MB) take 41 us.  (With an older maximum and division, 47
-// us, 8 warps took 50 us and 16 took 66, whose slowest warp holds the others'
-// registers; 8 or 9 CTAs take as long as 10 at d = 128 and 2 us more at d = 64.)
+// heads of d = 128 (214 MB) take 37 us, 33 of them in the kernel.  (With an older
+// maximum and division, 45 us, 8 warps took 49 us and 16 took 63, whose slowest
+// warp holds the others' registers; 8 or 9 CTAs take as long as 10 at d = 128
+// and 2 us more at d = 64.)
 constexpr int kAppendWarps = 4;
 constexpr int kAppendCtas = 10;
 constexpr int kMinScaleExp = -100;

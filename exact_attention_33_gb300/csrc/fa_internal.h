@@ -54,8 +54,7 @@ static_assert(256 * kPrefill8SoftmaxRegs + 256 * kPrefill8CtlRegs <= 512 * kPref
 // query tiles take 512 threads: the softmax warps, a warpgroup of the MMA and
 // the copies (warp 11 idles), and the four warps from kConvWarp on that
 // widen values.
-// A persistent CTA (PERS) has no second copy warp, so that its softmax gets 200
-// registers.
+// A persistent CTA (PERS) has no second copy warp (dense and packed kinds).
 template <int QT, bool KV8 = false, bool PERS = false>
 struct PrefillShape {
   static_assert(QT == 1 || QT == 2, "one or two query tiles per CTA");

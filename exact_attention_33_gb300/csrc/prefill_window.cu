@@ -20,7 +20,8 @@ namespace fa {
 // quarter of its time.  Persistent CTAs, one an SM, take the items in turn, and
 // the next item's copies and first products run beside the last softmax and the
 // epilogue.  They take fixed shares, so the items have to be alike: sequences of
-// some windows' length.  In us, one CTA an item / persistent (32 / 8 heads,
+// some windows' length.  (One-tile CTAs, two an SM, overlap already: persistent
+// ones took 5 to 17% longer.)  In us, one CTA an item / persistent (32 / 8 heads,
 // N = 16384, B = 1; the last two 16 / 4 heads, B = 8):
 //   d    window 512   1024        2048        4096        N 2048, 512  N 2048, 1024
 //   128  187 / 165    261 / 246   400 / 400   658 / 687   98 / 93      119 / 121
