@@ -599,3 +599,35 @@ def test_chunks_of_any_size_of_row(fa, H, Hkv, d):
     got[3, 0], got[151] = out[3, 0], out[151]
     assert torch.equal(got, out)
     assert_device_clean()
+
+
+def test_padded_serving_batch(fa):
+    """Slots of a batch without a sequence (no tokens, empty context, table row
+    of no ids) and rows behind the last sequence: nothing of them is written,
+    whatever their rows hold; pools as e4m3 tensors give the same bits."""
+    torch = torch_mod()
+    H, Hkv, d = 4, 2, 128
+    ctx, new = [0, 70, 0, 33, 0], [0, 5, 0, 33, 0]
+    c = Cache(ctx, Hkv, d, seed=150)
+    rng = np.random.default_rng(151)
+    T = sum(new)
+    k, v = cr.bf16(rng, T + 4, Hkv, d), cr.bf16(rng, T + 4, Hkv, d)
+    k[T:], v[T:] = np.nan, np.nan
+    c.append(fa, k, v, ctx, new)
+    c.check("padded")
+    q = bf16(cr.bf16(rng, T + 4, H, d))
+    q[T:] = math.nan
+    lens, cu = dev(np.int32(ctx)), dev(cu_of(new))
+    for window, sinks in ((0, 0), (20, 3)):
+        out = torch.full_like(q, 7.0)
+        lse = torch.full((H, T + 4), 7.0, device="cuda")
+        fa.fa_fwd_paged_fp8(q, *c.args(), lens, cu, max(new), max(ctx), window, sinks, out=out, lse=lse)
+        assert bool((out[T:] == 7.0).all()) and bool((lse[:, T:] == 7.0).all())
+        check_chunks(out[:T], lse[:, :T], q[:T], c, ctx, cu_of(new), window, sinks)
+        tok = bf16(cr.bf16(rng, len(ctx), H, d))
+        got = fa.fa_decode_paged_fp8(tok, *c.args(), lens, max(ctx), window, sinks)
+        check_decode(*got, tok, c, ctx, window, sinks, "padded")
+        e4m3 = [t.view(torch.float8_e4m3fn) for t in c.args()[:2]]
+        same = fa.fa_decode_paged_fp8(tok, *e4m3, *c.args()[2:], lens, max(ctx), window, sinks)
+        assert torch.equal(got[0], same[0]) and torch.equal(got[1], same[1])
+    assert_device_clean()

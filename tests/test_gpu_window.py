@@ -525,3 +525,39 @@ def test_sinks_of_one_long_sequence_among_many(fa):
     assert_device_clean()
     for a, e in ((0, n), (n, n + 1), (cu[-2], cu[-1])):
         check_gradient(*(t[a:e] for t in (dq, dk, dv, q, k, v, g)), window, sinks, f"row {a}")
+
+
+def test_padded_chunks_and_gradients(fa):
+    """Rows behind the last sequence, of chunks and of gradients, stay as they
+    were, and what they hold reaches nothing."""
+    torch = torch_mod()
+    H, Hkv, d, window, sinks, pad = 4, 2, 64, 30, 3, 5
+    ctx, new = [0, 150, 40], [0, 60, 1]
+    kp, vp, table, rows = pages(ctx, Hkv, d, 170)
+    q = normal(171, sum(new) + pad, H, d)
+    q[-pad:] = math.nan
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((H, q.shape[0]), 7.0, device="cuda")
+    fa.fa_fwd_paged_window(q, kp, vp, table.cuda(), i32(ctx), i32(cu_of(new)), max(new), max(ctx),
+                           window, sinks, out=out, lse=lse)
+    assert bool((out[-pad:] == 7.0).all()) and bool((lse[:, -pad:] == 7.0).all())
+    a = 0
+    for n, kv in zip(new, rows):
+        if n:
+            check_rows(out[a:a + n], lse[:, a:a + n], q[a:a + n], *kv, window, sinks, f"chunk of {n}")
+        a += n
+    lens = [200, 0, 131]
+    cu, T = cu_of(lens), sum(lens)
+    q, k, v, g = (normal(172 + i, T + pad, h, d) for i, h in enumerate((H, Hkv, Hkv, H)))
+    for t in (q, k, v, g):
+        t[-pad:] = math.nan
+    out = torch.full_like(q, math.nan)
+    _, lse = fa.fa_fwd_varlen_window(q, k, v, i32(cu), 200, window, sinks, out=out)
+    grads = [torch.full_like(t, 7.0) for t in (q, k, v)]
+    fa.fa_bwd_varlen_window(q, k, v, out, lse, g, i32(cu), 200, window, sinks,
+                            dq=grads[0], dk=grads[1], dv=grads[2])
+    assert_device_clean()
+    assert all(bool((t[-pad:] == 7.0).all()) for t in grads)
+    for a, e in zip(cu, cu[1:]):
+        if e > a:
+            check_gradient(*(t[a:e] for t in (*grads, q, k, v, g)), window, sinks, f"rows {a}")
