@@ -69,6 +69,7 @@ KERNEL_SOURCES = {
     "prefill": ["exact_attention_33_gb300/csrc/prefill.cu",
                 "exact_attention_33_gb300/csrc/prefill_kernel.cuh",
                 "exact_attention_33_gb300/csrc/store.cuh",
+                "exact_attention_33_gb300/csrc/launch.h",
                 "exact_attention_33_gb300/csrc/ptx.cuh",
                 "exact_attention_33_gb300/csrc/fa_internal.h",
                 "exact_attention_33_gb300/csrc/checks.cuh"],

@@ -47,6 +47,7 @@
 
 #include "bwd_internal.h"
 #include "fa_internal.h"
+#include "launch.h"
 #include "ptx.cuh"
 #include "store.cuh"
 #include "checks.cuh"
@@ -1763,8 +1764,8 @@ static cudaError_t launch_bwd_d(const CUtensorMap &tq, const CUtensorMap &tdo,
     long long tiles = static_cast<long long>(p.B) * p.n_tiles;
     if (VARLEN && p.longest_first) tiles = std::min(tiles, (p.total_tokens + 127LL) / 128 + p.B);
     auto sums = bwd_sums_kernel<D, VARLEN>;
-    e = cudaFuncSetAttribute(sums, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             BwdSumsLayout<D>::kSmemAlloc);
+    static std::atomic<unsigned long long> smem_set{0};
+    e = allow_smem(sums, BwdSumsLayout<D>::kSmemAlloc, smem_set);
     if (e != cudaSuccess) return e;
     sums<<<static_cast<unsigned>(std::min<long long>(tiles * p.H, p.num_ctas)), kBwdThreads,
            BwdSumsLayout<D>::kSmemAlloc, stream>>>(tq, tdo, tk, tv, p);
@@ -1781,10 +1782,10 @@ static cudaError_t launch_bwd_d(const CUtensorMap &tq, const CUtensorMap &tdo,
   }
   auto dq = causal ? bwd_dq_kernel<D, true, VARLEN, WIN> : bwd_dq_kernel<D, WIN, VARLEN, WIN>;
   auto dkdv = causal ? bwd_dkdv_kernel<D, true, VARLEN, WIN> : bwd_dkdv_kernel<D, WIN, VARLEN, WIN>;
-  e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           BwdDqLayout<D>::kSmemAlloc);
+  static std::atomic<unsigned long long> dq_set[2], dkdv_set[2];  // not causal, causal
+  e = allow_smem(dq, BwdDqLayout<D>::kSmemAlloc, dq_set[causal]);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
+  e = allow_smem(dkdv, L::kSmemAlloc, dkdv_set[causal]);
   if (e != cudaSuccess) return e;
   // work items: every (sequence, 128-row tile); the longest-first order of a
   // packed batch enumerates only real tiles, at most ceil(T / 128) + B

@@ -43,6 +43,7 @@
 #include "checks.cuh"
 #include "decode_common.cuh"
 #include "fa_internal.h"
+#include "launch.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -439,18 +440,9 @@ static cudaError_t launch_decode_fp8_t(const CUtensorMap &tk, const CUtensorMap 
                                        cudaStream_t stream) {
   using L = DecodeF8Layout<D>;
   auto kern = decode_fp8_split_kernel<D, NT>;
-  // the shared-memory attribute is per device: set once on each (one bit per
-  // device id; ids past 63 set it on every launch)
-  static std::atomic<unsigned long long> attr_set{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t e = allow_smem(kern, L::kSmemAlloc, smem_set);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? (1ull << dev) : 0ull;
-  if (bit == 0ull || (attr_set.load(std::memory_order_acquire) & bit) == 0ull) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
-    if (e != cudaSuccess) return e;
-    attr_set.fetch_or(bit, std::memory_order_release);
-  }
   kern<<<dim3(p.max_splits, p.Hkv, p.batch), 32, L::kSmemAlloc, stream>>>(tk, tv, p, sc);
   e = cudaGetLastError();
   return e == cudaSuccess ? launch_decode_combine(p, D, stream) : e;

@@ -44,6 +44,7 @@
 #include <algorithm>
 
 #include "fa_internal.h"
+#include "launch.h"
 #include "ptx.cuh"
 #include "store.cuh"
 #include "checks.cuh"
@@ -1538,8 +1539,8 @@ static cudaError_t launch_prefill_t(const CUtensorMap &tq, const CUtensorMap &tk
     }();
     if (launch_regs != kPrefill1LaunchRegs) return cudaErrorInvalidKernelImage;
   }
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemAlloc);
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t e = allow_smem(kern, L::kSmemAlloc, smem_set);
   if (e != cudaSuccess) return e;
   PrefillParams pp = p;
   pp.num_items = grid;
