@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(32)
         const size_t row = (part_row + g) * p.max_splits + split;
         if (!in_bounds(row, 1, part_rows, p.status)) continue;
         if (grp == 0) {
-          p.ml_part[row * 2 + 0] = st.mcol[nt][cc];
+          p.ml_part[row * 2 + 0] = split_max(st.mcol[nt][cc], lt);
           p.ml_part[row * 2 + 1] = lt;
         }
         float *orow = p.o_part + row * D;
@@ -510,7 +510,8 @@ __global__ void __launch_bounds__(32 * combine_cta_warps<W>())
     for (int w = 0; w < W; ++w) t += s_acc[r0 + w][lane * E + e];
     acc[e] = t;
   }
-  const float inv = (Lsum > 0.f) ? 1.f / Lsum : 0.f;
+  // (0: no key seen; NaN goes on to the row)
+  const float inv = (Lsum == 0.f) ? 0.f : 1.f / Lsum;
   uint16_t *dst = static_cast<uint16_t *>(p.out) + static_cast<size_t>(gw) * D + lane * E;
   const bool out_ok = in_bounds(static_cast<size_t>(gw) * D + lane * E, E,
                                 static_cast<size_t>(p.batch) * p.H * D, status);
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(32 * combine_cta_warps<W>())
   }
   if (lane == 0 && p.lse != nullptr &&
       in_bounds(gw, 1, static_cast<size_t>(p.batch) * p.H, status))
-    p.lse[gw] = (Lsum > 0.f) ? (M + __log2f(Lsum)) * 0.69314718055994530942f : -CUDART_INF_F;
+    p.lse[gw] = (Lsum == 0.f) ? -CUDART_INF_F : (M + __log2f(Lsum)) * 0.69314718055994530942f;
   if (publisher) publish_call_status(p.call, call_bits, p.dev_status);
 }
 

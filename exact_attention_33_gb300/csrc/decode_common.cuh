@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include "fa_internal.h"
@@ -24,6 +25,13 @@ struct WindowBlocks {
   // block of the sequence that is the v-th to be read
   __device__ __forceinline__ int logical(int v) const { return v < nsb ? v : v - nsb + wb0; }
 };
+
+// The maximum that a split reports for a row, m with sum l.  A row whose scores
+// are all NaN leaves its maximum at -inf, which the combine takes for a split
+// without keys: it reports 0, so that its NaN sums make the row NaN.
+__device__ __forceinline__ float split_max(float m, float l) {
+  return (m == -CUDART_INF_F && l != l) ? 0.f : m;
+}
 
 // The (m, l, o) combine of a split decode call (decode.cu), launched as a
 // programmatic dependent of the split grid on the same stream.

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(32)
     const size_t row = (part_row + g) * p.max_splits + split;
     if (!in_bounds(row, 1, part_rows, p.status)) continue;
     if (grp == 0) {
-      p.ml_part[row * 2 + 0] = m[nt];
+      p.ml_part[row * 2 + 0] = split_max(m[nt], lt);
       p.ml_part[row * 2 + 1] = lt;
     }
     // o back from its own reference to m's

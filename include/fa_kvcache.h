@@ -65,7 +65,9 @@ int fa_cache_append_fp8(const void *k, const void *v, int64_t k_stride, int64_t 
  *               fa_decode_window_workspace_size() bytes (fa_window.h);
  *               the conventions of fa_decode_paged
  * Slots outside the context and hidden ones never reach the result; blocks
- * without a visible key are not read.  Supported: H / Hkv <= 16.
+ * without a visible key are not read.  An infinite or NaN value of q makes its
+ * row's out and lse NaN (0 and -inf stand for a context without keys alone).
+ * Supported: H / Hkv <= 16.
  */
 int fa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
                         const float *k_scale, const float *v_scale, const int32_t *block_table,

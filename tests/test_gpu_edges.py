@@ -1,0 +1,90 @@
+"""Calls at the edges of what the windowed and 8-bit cache calls document:
+rows that are not finite, very wide block tables, sequences longer than said,
+workspaces sized for longer calls, tiny and subnormal queries."""
+import math
+
+import numpy as np
+import pytest
+
+import cache_reference as cr
+import window_reference as ref
+from gpu_helpers import assert_device_clean, torch_mod
+from test_gpu_kvcache import Cache, bf16, cu_of, dev
+from test_gpu_window import check_gradient, check_rows, i32, normal, pages
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    from exact_attention_33_gb300.build import build
+    build()
+    import exact_attention_33_gb300 as fa_mod
+    fa_mod.fa_device_status(clear=True)
+    return fa_mod
+
+
+def assert_poisoned(got, want, rows):
+    """(out, lse) [rows.., H, d], [rows.., H]: NaN at the (row, head) pairs of
+    `rows`, the bits of `want` elsewhere."""
+    torch = torch_mod()
+    (out, lse), (o, l) = got, want
+    for r, h in rows:
+        assert bool(out[r, h].isnan().all()), (r, h)
+        assert bool(lse[r, h].isnan()), (r, h, float(lse[r, h]))
+        out[r, h], lse[r, h] = o[r, h], l[r, h]
+    assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+# ------------------------------------------------------------------ rows that are not finite
+
+@pytest.mark.parametrize("H,Hkv,d,window,sinks", [(4, 2, 64, 0, 0), (32, 2, 128, 0, 0),
+                                                  (8, 1, 128, 600, 4), (3, 1, 64, 5, 0)])
+def test_tokens_over_codes_with_bad_queries(fa, H, Hkv, d, window, sinks):
+    """A query with a NaN or an infinity gets NaN, not what an empty context
+    gets; in contexts of one key, one split and many."""
+    ctx = [1, 60, 0, 3000]
+    c = Cache(ctx, Hkv, d, seed=200)
+    q = bf16(cr.bf16(np.random.default_rng(d), len(ctx), H, d))
+    args = (*c.args(), dev(np.int32(ctx)), max(ctx), window, sinks)
+    want = fa.fa_decode_paged_fp8(q, *args)
+    for value in (math.nan, math.inf, -math.inf):
+        bad = q.clone()
+        rows = [(0, 0), (1, H - 1), (3, 1), (3, 2)]
+        for i, (r, h) in enumerate(rows):
+            bad[r, h, (7 * i) % d] = value
+        assert_poisoned(fa.fa_decode_paged_fp8(bad, *args), want, rows)
+    bad = q.clone()
+    bad[2] = math.nan     # over no keys: still an empty row
+    assert_poisoned(fa.fa_decode_paged_fp8(bad, *args), want, [])
+    assert_device_clean()
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 64), (32, 2, 128)])
+@pytest.mark.parametrize("window", [0, 50, 2000])
+def test_tokens_over_bf16_with_bad_queries(fa, H, Hkv, d, window):
+    ctx = [1, 60, 0, 3000]
+    kp, vp, table, _ = pages(ctx, Hkv, d, 210)
+    q = normal(212, len(ctx), H, d)
+
+    def call(q):
+        args = (q, kp, vp, table.cuda(), i32(ctx), max(ctx))
+        return fa.fa_decode_paged_window(*args, window, 3) if window else fa.fa_decode_paged(*args)
+    want = call(q)
+    bad = q.clone()
+    bad[0, 0, 1] = bad[1, H - 1, 0] = bad[3, 1, d - 1] = bad[2] = math.nan
+    assert_poisoned(call(bad), want, [(0, 0), (1, H - 1), (3, 1)])
+    assert_device_clean()
+
+
+def test_a_bad_key_reaches_its_log_sum_too(fa):
+    """A NaN code in a visible key makes the token's output NaN, and its
+    log-sum-exp with it."""
+    ctx, H, Hkv, d = [100, 100], 4, 2, 64
+    c = Cache(ctx, Hkv, d, seed=215)
+    q = bf16(cr.bf16(np.random.default_rng(1), 2, H, d))
+    args = (*c.args(), dev(np.int32(ctx)), 100)
+    want = fa.fa_decode_paged_fp8(q, *args)
+    c.dpool["k"][int(c.table[1, 3]), 5, 0, 9] = 0x7F
+    assert_poisoned(fa.fa_decode_paged_fp8(q, *args), want, [(1, 0), (1, 1)])
+    assert_device_clean()
