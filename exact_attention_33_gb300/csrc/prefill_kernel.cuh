@@ -1501,8 +1501,9 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
                                      ? static_cast<size_t>(hi) * p.total_tokens + seq_start + qi
                                      : (static_cast<size_t>(b) * p.H + hi) * p.N + qi;
           if (ok && live && p.lse != nullptr && in_bounds(lse_idx, 1, out_rows * p.H, p.status)) {
-            p.lse[lse_idx] = (l_exact > 0.f) ? (m + __log2f(l_exact)) * 0.69314718055994530942f
-                                             : -CUDART_INF_F;
+            // (a sum of 0: no key seen; NaN scores make it NaN)
+            p.lse[lse_idx] = (l_exact == 0.f) ? -CUDART_INF_F
+                                              : (m + __log2f(l_exact)) * 0.69314718055994530942f;
           }
         }
       }

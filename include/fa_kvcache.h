@@ -82,7 +82,7 @@ int fa_decode_paged_fp8(const void *q, const void *k_pool, const void *v_pool,
  * as they are, with q exact down to 2^-13 of its row's largest value and off
  * by at most 2^-21 of that below, and on V widened to bf16, exactly where a
  * block's scale is a power of two, with one bf16 rounding where it is not.  An
- * infinite or NaN value of q makes its row's result NaN.
+ * infinite or NaN value of q makes its row's out and lse NaN.
  *   q, out : [total_q, H, d] bf16;  lse : [H, total_q] fp32, may be NULL
  * Slots past the context never reach the result; a block that no query of a
  * 128-row tile sees (a window's) is not read and may be freed.  A query that

@@ -26,6 +26,7 @@
  * also K, Q and dO) that is infinite or NaN reaches the rows of its sequence
  * whose tiles hold it, as in fa.h's calls; rows of other sequences, and
  * packed rows behind the last sequence, never reach a sequence's results.
+ * A query with a NaN gets out = NaN and lse = NaN.
  */
 #ifndef FA_WINDOW_H_
 #define FA_WINDOW_H_

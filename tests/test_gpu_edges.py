@@ -88,3 +88,35 @@ def test_a_bad_key_reaches_its_log_sum_too(fa):
     c.dpool["k"][int(c.table[1, 3]), 5, 0, 9] = 0x7F
     assert_poisoned(fa.fa_decode_paged_fp8(q, *args), want, [(1, 0), (1, 1)])
     assert_device_clean()
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 64), (6, 2, 128)])
+def test_chunks_and_prompts_with_bad_queries(fa, H, Hkv, d):
+    """Rows with a NaN are NaN in out and lse alike, in every windowed and
+    8-bit form; so are rows with an infinity over the 8-bit cache."""
+    ctx, new = [300, 170], [150, 40]
+    cu, T = cu_of(new), sum(new)
+    rows = [(3, 0), (151, 1), (151, 2), (189, H - 1)]
+    c = Cache(ctx, Hkv, d, seed=220)
+    kp, vp, table, _ = pages(ctx, Hkv, d, 221)
+    q, k, v = (normal(222 + i, T, h, d) for i, h in enumerate((H, Hkv, Hkv)))
+    bad = q.clone()
+    for r, h in rows:
+        bad[r, h, r % d] = math.nan
+    lens, dcu = dev(np.int32(ctx)), dev(cu)
+    calls = [
+        lambda q: fa.fa_fwd_paged_fp8(q, *c.args(), lens, dcu, max(new), max(ctx)),
+        lambda q: fa.fa_fwd_paged_fp8(q, *c.args(), lens, dcu, max(new), max(ctx), 40, 3),
+        lambda q: fa.fa_fwd_paged_window(q, kp, vp, table.cuda(), lens, dcu, max(new), max(ctx), 40, 3),
+        lambda q: fa.fa_fwd_varlen_window(q, k, v, dcu, max(new), 40, 3),
+        lambda q: [t[0] for t in fa.fa_fwd_window(q[None], k[None], v[None], 40, 3)],
+    ]
+    for i, call in enumerate(calls):
+        (out, lse), (o, l) = call(bad), call(q)
+        assert_poisoned((out, lse.T.contiguous()), (o, l.T.contiguous()), rows)
+        if i < 2:
+            inf = q.clone()
+            inf[bad.isnan()] = math.inf
+            out, lse = call(inf)
+            assert_poisoned((out, lse.T.contiguous()), (o, l.T.contiguous()), rows)
+    assert_device_clean()
