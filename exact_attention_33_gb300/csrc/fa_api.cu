@@ -391,11 +391,16 @@ namespace {
 // workspace for every sequence, however short.  Beyond kSinkTiles tiles of
 // sinks there are enough of them to fill the GPU, and their partial sums would
 // outgrow the gradients.
+// Which form a call takes follows from the window and sinks as the caller gave
+// them and from N, so that part_bound, the size for B and N, covers every
+// smaller batch and shorter sequence.
 constexpr int kSinkTiles = 2;
 constexpr long long kSinkSlots = 4096;
+constexpr int kSinkSlice = 4;   // query tiles of a slice, at least
 struct SinkSlices {
   int tiles = 0, slices = 0, slice = 0;
-  size_t part_bytes = 0;
+  size_t part_bytes = 0;   // of this call
+  size_t part_bound = 0;   // of every call of at most B sequences of at most N rows
 };
 SinkSlices sink_slices(int B, int Hkv, int N, int d, WindowSpec w) {
   SinkSlices s;
@@ -403,13 +408,21 @@ SinkSlices sink_slices(int B, int Hkv, int N, int d, WindowSpec w) {
   const int tiles = (std::min(w.sinks, N) + 127) / 128;
   // query tiles whose windows hold a key of tile 0 (window_queries of the kernels)
   const int span = static_cast<int>(std::min<long long>(n_q, (w.window + 126LL) / 128 + 1));
-  if (tiles == 0 || tiles > kSinkTiles || n_q <= span) return s;
+  if (tiles == 0 || w.sinks > kSinkTiles * 128 || n_q <= span) return s;
+  const long long units = static_cast<long long>(B) * Hkv * tiles;
+  const long long most = std::max(4LL, kSinkSlots / units);
+  const int least = std::max(kSinkSlice, span);
   s.tiles = tiles;
-  const long long most =
-      std::max(4LL, kSinkSlots / (static_cast<long long>(B) * Hkv * tiles));
-  s.slice = static_cast<int>(std::max<long long>(std::max(4, span), (n_q - span + most - 1) / most));
+  s.slice = static_cast<int>(std::max<long long>(least, (n_q - span + most - 1) / most));
   s.slices = (n_q - span + s.slice - 1) / s.slice;
-  s.part_bytes = static_cast<size_t>(B) * Hkv * tiles * (1 + s.slices) * 2 * 128 * d * sizeof(float);
+  const size_t slot = 2 * 128 * static_cast<size_t>(d) * sizeof(float);
+  s.part_bytes = static_cast<size_t>(units) * (1 + s.slices) * slot;
+  // slices <= (n_q - span) / least, rounded up, and units * slices <= max(4
+  // units, kSinkSlots): each rises with B and N (span and least do not depend on
+  // N where there are slices)
+  const long long slices = std::min(units * ((n_q - span + least - 1) / least),
+                                    std::max(4 * units, kSinkSlots));
+  s.part_bound = static_cast<size_t>(units + slices) * slot;
   return s;
 }
 
@@ -419,7 +432,7 @@ size_t fa_bwd_window_workspace_size(int B, int H, int Hkv, int N, int d, int win
   if (!window_ok(window, sinks) || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
   const size_t base = fa_bwd_workspace_size(B, H, N);
   if (base == 0) return 0;
-  return base + sink_slices(B, Hkv, N, d, clamp_window({window, sinks}, N)).part_bytes;
+  return base + sink_slices(B, Hkv, N, d, {window, sinks}).part_bound;
 }
 
 // Gradient of dense attention, causal or not or windowed.
@@ -437,8 +450,8 @@ static int bwd_dense(const void *q, const void *k, const void *v, const void *ou
   if (!scale_ok(scale)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (B == 0 || N == 0) return FA_OK;
-  const size_t need = win.window ? fa_bwd_window_workspace_size(B, H, Hkv, N, d, win.window, win.sinks)
-                                 : fa_bwd_workspace_size(B, H, N);
+  const SinkSlices sl = win.window ? sink_slices(B, Hkv, N, d, win) : SinkSlices{};
+  const size_t need = fa_bwd_workspace_size(B, H, N) + sl.part_bytes;
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
     return FA_ERR_WORKSPACE;
   const long long n_tiles = (N + 127) / 128;
@@ -478,7 +491,6 @@ static int bwd_dense(const void *q, const void *k, const void *v, const void *ou
   p.window = win.window;
   p.sinks = win.sinks;
   if (win.window) {
-    const SinkSlices sl = sink_slices(p.B, Hkv, p.N, d, win);
     p.sink_tiles = sl.tiles;
     p.sink_slices = sl.slices;
     p.sink_slice = sl.slice;
@@ -528,9 +540,8 @@ static int bwd_varlen(const void *q, const void *k, const void *v, const void *o
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (num_seqs == 0 || total_tokens == 0 || max_seqlen == 0) return FA_OK;
   const int n_max = std::min(max_seqlen, total_tokens);
-  const size_t need =
-      win.window ? fa_bwd_window_workspace_size(num_seqs, H, Hkv, n_max, d, win.window, win.sinks)
-                 : fa_bwd_workspace_size(num_seqs, H, n_max);
+  const SinkSlices sl = win.window ? sink_slices(num_seqs, Hkv, n_max, d, win) : SinkSlices{};
+  const size_t need = fa_bwd_workspace_size(num_seqs, H, n_max) + sl.part_bytes;
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256))
     return FA_ERR_WORKSPACE;
   const long long n_tiles = (n_max + 127) / 128;
@@ -575,7 +586,6 @@ static int bwd_varlen(const void *q, const void *k, const void *v, const void *o
   p.window = win.window;
   p.sinks = win.sinks;
   if (win.window) {
-    const SinkSlices sl = sink_slices(p.B, Hkv, p.N, d, win);
     p.sink_tiles = sl.tiles;
     p.sink_slices = sl.slices;
     p.sink_slice = sl.slice;

@@ -80,7 +80,9 @@ int fa_decode_paged_window(const void *q, const void *k_pool, const void *v_pool
    over the visible pairs); out and lse as those calls wrote them, with the
    same window and sinks.  The workspace has
    fa_bwd_window_workspace_size() bytes (a packed batch: B = num_seqs,
-   N = max_seqlen), 256-byte aligned, overwritten, one call at a time.
+   N = max_seqlen), 256-byte aligned, overwritten, one call at a time.  One sized
+   for some B and N serves every smaller B and N with the same H, Hkv, d, window
+   and sinks.
    A packed batch with a bad cu_seqlens entry: as fa_bwd_varlen. */
 size_t fa_bwd_window_workspace_size(int B, int H, int Hkv, int N, int d, int window, int sinks);
 int fa_bwd_window(const void *q, const void *k, const void *v, const void *out, const float *lse,

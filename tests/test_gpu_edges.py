@@ -120,3 +120,20 @@ def test_chunks_and_prompts_with_bad_queries(fa, H, Hkv, d):
             out, lse = call(inf)
             assert_poisoned((out, lse.T.contiguous()), (o, l.T.contiguous()), rows)
     assert_device_clean()
+
+
+# ------------------------------------------------------------------ sizes
+
+def test_documented_workspace_of_a_gradient(fa):
+    """A gradient's workspace sized with the longest sequence, which a batch of
+    fewer rows than that does not reach."""
+    torch = torch_mod()
+    H, Hkv, d, window, sinks, T, said = 4, 4, 128, 1, 300, 256, 257
+    cu = i32([0, T])
+    q, k, v, g = (normal(250 + i, T, h, d) for i, h in enumerate((H, Hkv, Hkv, H)))
+    out, lse = fa.fa_fwd_varlen_window(q, k, v, cu, said, window, sinks)
+    ws = torch.empty(fa.fa_bwd_window_workspace_size(1, H, Hkv, said, d, window, sinks),
+                     dtype=torch.uint8, device="cuda")
+    grads = fa.fa_bwd_varlen_window(q, k, v, out, lse, g, cu, said, window, sinks, workspace=ws)
+    assert_device_clean()
+    check_gradient(*grads, q, k, v, g, window, sinks, "shorter than said")
