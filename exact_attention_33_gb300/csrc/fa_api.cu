@@ -795,8 +795,7 @@ size_t fa_decode_workspace_size(int batch, int H, int Hkv, int d, int max_ctx_le
   if (batch < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || max_ctx_len < 0) return 0;
   if ((d != 64 && d != 128) || block_size != kDecodeBlock) return 0;
   if (max_ctx_len > kMaxCtxLen) return 0;
-  const DecodeWs w = decode_ws(batch, H, Hkv, d, max_ctx_len);
-  return FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes;
+  return FA_WORKSPACE_HEADER_BYTES + decode_ws_bound(batch, H, Hkv, d, max_ctx_len);
 }
 
 size_t fa_decode_window_workspace_size(int batch, int H, int Hkv, int d, int max_ctx_len,

@@ -131,12 +131,17 @@ inline int sm_count() {
 #define FA_DECODE_WAVE_CTAS 14
 #endif
 constexpr int kDecodeWaveCtas = FA_DECODE_WAVE_CTAS;
-inline int decode_split_tokens(int batch, int Hkv, int max_ctx_len) {
+constexpr int kDecodeMinSplitTokens = 64;
+// Work items that a decode call wants at least.
+inline long long decode_want_items() {
   int sms = sm_count();
   if (sms <= 0) sms = 148;
-  const long long want = static_cast<long long>(kDecodeWaveCtas) * sms;
+  return static_cast<long long>(kDecodeWaveCtas) * sms;
+}
+inline int decode_split_tokens(int batch, int Hkv, int max_ctx_len) {
+  const long long want = decode_want_items();
   int split = kDecodeMaxSplitTokens;
-  while (split > 64) {
+  while (split > kDecodeMinSplitTokens) {
     const long long items = static_cast<long long>(batch) * Hkv *
                             ((static_cast<long long>(max_ctx_len) + split - 1) / split);
     if (items >= want) break;
@@ -221,6 +226,23 @@ inline DecodeWs decode_ws(int batch, int H, int Hkv, int d, int max_ctx_len) {
   w.o_bytes = round_up(rows * d * sizeof(float), 256);
   w.ml_bytes = round_up(rows * 2 * sizeof(float), 256);
   return w;
+}
+
+// Workspace bytes that every decode call of at most `batch` sequences of at most
+// max_ctx_len keys fits into.  The split size falls as the batch or the context
+// does, so what a call needs rises with neither.  Its splits of one head are at
+// most ceil(keys / 512) of each sequence or, where they are shorter than that,
+// at most ceil(keys / 64) of each, and all of them (on every KV head) fewer than
+// twice the wanted items, because splits of twice the size were fewer than those.
+inline size_t decode_ws_bound(int batch, int H, int Hkv, int d, int max_ctx_len) {
+  auto splits = [&](int tokens) {
+    return batch * std::max(1LL, (static_cast<long long>(max_ctx_len) + tokens - 1) / tokens);
+  };
+  const long long rows =
+      H * std::max(splits(kDecodeMaxSplitTokens),
+                   std::min(splits(kDecodeMinSplitTokens), 2 * decode_want_items() / Hkv));
+  return round_up(static_cast<size_t>(rows) * d * sizeof(float), 256) +
+         round_up(static_cast<size_t>(rows) * 2 * sizeof(float), 256);
 }
 
 }  // namespace fa

@@ -258,7 +258,9 @@ int fa_fwd_paged(const void *q, const void *k_pool, const void *v_pool,
 /*
  * Bytes of caller-owned workspace that fa_decode_paged needs: the control
  * block plus the split partial states (m, l, o) of every (sequence, query
- * head, key split).  Returns 0 for invalid arguments.  The split size
+ * head, key split).  Returns 0 for invalid arguments.  A workspace of this size
+ * serves every call of at most `batch` sequences and at most max_ctx_len with
+ * the same other arguments.  The split size
  * depends only on these arguments and on the current device's SM count; Hkv
  * is among them because the number of splits is chosen so that the
  * (sequence, KV head, split) work items fill the GPU.
@@ -307,9 +309,10 @@ int fa_decode_paged(const void *q, const void *k_pool, const void *v_pool,
  * workspace.  The split partial states live in a library-owned static device
  * array of FA_DECODE_NOALLOC_SCRATCH_BYTES bytes, which every GPU that loads
  * the library holds until the process exits.
- *  - A request whose partial states would need more than that (compare
- *    fa_decode_workspace_size() with FA_DECODE_NOALLOC_SCRATCH_BYTES) returns
- *    FA_ERR_WORKSPACE and launches nothing.
+ *  - A request whose own partial states need more than that returns
+ *    FA_ERR_WORKSPACE and launches nothing (one whose
+ *    fa_decode_workspace_size() is at most FA_DECODE_NOALLOC_SCRATCH_BYTES
+ *    never does).
  *  - The first call on a device looks up the array's device address on that
  *    device (with it current); make that first call before any stream
  *    capture.

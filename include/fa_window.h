@@ -65,8 +65,8 @@ int fa_fwd_paged_window(const void *q, const void *k_pool, const void *v_pool,
    the first window block and of the last sink block, never reach the result,
    whatever they hold.
    The workspace has fa_decode_window_workspace_size() bytes (window and
-   sinks 0: those of a call over every key); it and its control block are
-   those of fa_decode_paged. */
+   sinks 0: those of a call over every key), which serve smaller batches and
+   contexts too; it and its control block are those of fa_decode_paged. */
 size_t fa_decode_window_workspace_size(int batch, int H, int Hkv, int d, int max_ctx_len,
                                        int block_size, int window, int sinks);
 int fa_decode_paged_window(const void *q, const void *k_pool, const void *v_pool,

@@ -137,3 +137,22 @@ def test_documented_workspace_of_a_gradient(fa):
     grads = fa.fa_bwd_varlen_window(q, k, v, out, lse, g, cu, said, window, sinks, workspace=ws)
     assert_device_clean()
     check_gradient(*grads, q, k, v, g, window, sinks, "shorter than said")
+
+
+def test_documented_workspace_of_single_tokens(fa):
+    """Workspaces sized with the longest context, while contexts are short."""
+    H, Hkv, batch = 8, 8, 64
+    for window, limit in ((0, 2049), (2040, 8000)):
+        sized = fa.fa_decode_window_workspace_size(batch, H, Hkv, 64, limit, window)
+        ctx = [40] * batch
+        c = Cache(ctx, Hkv, 64, seed=253, width=500)
+        q = normal(254, batch, H, 64)
+        for longest in (40, 1024, 2048, limit):
+            ws = fa.new_workspace(sized)
+            got = fa.fa_decode_paged_fp8(q, *c.args(), dev(np.int32(ctx)), longest, window,
+                                         workspace=ws)
+            for h in range(H):
+                o, l, tol = cr.decode_rows(q[:1, h].double(), c.rows("k", 0, 40)[:, h],
+                                           c.rows("v", 0, 40)[:, h], window, 0)
+                ref.assert_within(got[0][:1, h], o, tol, f"longest {longest}")
+    assert_device_clean()
