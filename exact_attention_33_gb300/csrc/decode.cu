@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(32)
   if (!WIN && lane < p.split_tokens / kDecodeBlock && lb0 + lane < p.max_blocks_per_seq)
     read_block_id(lb0 + lane);
   const int ctx = checked_load(p.ctx_lens, b, p.batch, p.status);
-  if (ctx < 0 || ctx > p.max_ctx_len || ctx > p.max_blocks_per_seq * kDecodeBlock) {
+  if (ctx < 0 || ctx > p.max_ctx_len ||
+      ctx > p.max_blocks_per_seq * static_cast<long long>(kDecodeBlock)) {
     if (split == 0 && kvh == 0 && lane == 0) raise_status(p.status, FA_DEV_BAD_CTX);
     return;
   }
@@ -416,7 +417,9 @@ __global__ void __launch_bounds__(32 * combine_cta_warps<W>())
   const bool row_live = gw < p.batch * p.H;
   const int b = row_live ? gw / p.H : 0;
   int ctx = row_live ? checked_load(p.ctx_lens, b, p.batch, status) : 0;
-  if (ctx < 0 || ctx > p.max_ctx_len || ctx > p.max_blocks_per_seq * kDecodeBlock) ctx = 0;
+  if (ctx < 0 || ctx > p.max_ctx_len ||
+      ctx > p.max_blocks_per_seq * static_cast<long long>(kDecodeBlock))
+    ctx = 0;
   const int keys = p.window > 0 ? WindowBlocks(ctx, p.window, p.sinks).nvb * kDecodeBlock : ctx;
   const int ns = (keys + p.split_tokens - 1) / p.split_tokens;
   const size_t row0 = static_cast<size_t>(gw) * p.max_splits;

@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
       } else {
         kv_len = checked_load(p.ctx_lens, unit, p.B, p.status);
         if (kv_len < 0 || kv_len > p.max_ctx_len ||
-            kv_len > p.max_blocks_per_seq * kDecodeBlock) {
+            kv_len > p.max_blocks_per_seq * static_cast<long long>(kDecodeBlock)) {
           if (pair == 0 && h == 0) raise_status(p.status, FA_DEV_BAD_CTX);
           return kItemNone;
         }

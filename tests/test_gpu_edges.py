@@ -156,3 +156,30 @@ def test_documented_workspace_of_single_tokens(fa):
                                            c.rows("v", 0, 40)[:, h], window, 0)
                 ref.assert_within(got[0][:1, h], o, tol, f"longest {longest}")
     assert_device_clean()
+
+
+def test_tables_of_many_columns(fa):
+    """A table whose columns hold 2^31 tokens and more."""
+    torch = torch_mod()
+    ctx, H, Hkv, d, width = [90], 4, 2, 64, (1 << 27) + 8
+    lens, cu = dev(np.int32(ctx)), dev(np.int32([0, 20]))
+    q = normal(231, 20, H, d)
+    c = Cache(ctx, Hkv, d, seed=230)
+    kp, vp, table, _ = pages(ctx, Hkv, d, 232)
+    codes, bf = c.args()[:4], (kp, vp)
+    calls = [
+        (c.dtable, lambda t: fa.fa_decode_paged_fp8(q[-1:], *codes, t, lens, 90)),
+        (c.dtable, lambda t: fa.fa_decode_paged_fp8(q[-1:], *codes, t, lens, 90, 30, 2)),
+        (c.dtable, lambda t: fa.fa_fwd_paged_fp8(q, *codes, t, lens, cu, 20, 90)),
+        (table.cuda(), lambda t: fa.fa_decode_paged_window(q[-1:], *bf, t, lens, 90, 30, 2)),
+        (table.cuda(), lambda t: fa.fa_fwd_paged_window(q, *bf, t, lens, cu, 20, 90, 30, 2)),
+        (table.cuda(), lambda t: fa.fa_decode_paged(q[-1:], *bf, t, lens, 90)),
+        (table.cuda(), lambda t: fa.fa_fwd_paged(q, *bf, t, lens, cu, 20, 90)),
+    ]
+    wide = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    for i, (few, call) in enumerate(calls):
+        wide[:, :6] = few[:, :6]
+        want, got = call(few), call(wide)
+        assert_device_clean()
+        assert all(torch.equal(x, y) for x, y in zip(want, got)), i
+        assert bool(torch.isfinite(got[1]).all()), i
