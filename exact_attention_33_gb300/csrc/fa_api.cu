@@ -33,7 +33,7 @@ cudaError_t launch_prefill(const CUtensorMap &tq, const CUtensorMap &tk, const C
 cudaError_t launch_prefill_window(const CUtensorMap &tq, const CUtensorMap &tk,
                                   const CUtensorMap &tv, const CUtensorMap &tv1,
                                   const CUtensorMap &to, const PrefillParams &p, int d, int kind,
-                                  int grid, cudaStream_t stream);
+                                  int grid, int longest, cudaStream_t stream);
 cudaError_t launch_prefill_split_combine(const PrefillParams &p, int d, cudaStream_t stream);
 cudaError_t launch_bwd(const CUtensorMap &tq, const CUtensorMap &tdo, const CUtensorMap &tk,
                        const CUtensorMap &tv, const BwdParams &p, int d, bool causal,
@@ -193,7 +193,7 @@ static int fwd_dense(const void *q, const void *k, const void *v, void *out, flo
   p.window = win.window;
   p.sinks = win.sinks;
   cudaError_t e = win.window ? launch_prefill_window(tq, tk, tv, tv, to, p, d, kind,
-                                                     static_cast<int>(grid), st)
+                                                     static_cast<int>(grid), N, st)
                              : launch_prefill(tq, tk, tv, tv, to, p, d, causal != 0, kind,
                                               static_cast<int>(grid), st);
   if (e == cudaSuccess && call != nullptr)
@@ -286,12 +286,13 @@ static int fwd_varlen(const void *q, const void *k, const void *v, void *out, fl
   p.prefetch_ahead = std::max(0, sm_count()) * (qtiles == 1 ? 2 : 1);  // CTAs resident at once
   const int kind = layout == kHeadPairs ? kKindVarlenHeads : kKindVarlen;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  win = clamp_window(win, max_seqlen);
+  // (not to max_seqlen: a longer sequence that the grid covers keeps its window)
+  win = clamp_window(win, total_tokens);
   p.window = win.window;
   p.sinks = win.sinks;
   if (win.window)
-    return launch_prefill_window(tq, tk, tv, tv, to, p, d, kind, static_cast<int>(grid), st) ==
-                   cudaSuccess
+    return launch_prefill_window(tq, tk, tv, tv, to, p, d, kind, static_cast<int>(grid),
+                                 max_seqlen, st) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
   cudaError_t e = fp8 ? launch_prefill_fp8(tq, tk, tv, to, p, causal != 0, static_cast<int>(grid), st,
@@ -762,7 +763,7 @@ static int fwd_paged(const void *q, const void *k_pool, const void *v_pool,
   p.window = win.window;
   p.sinks = win.sinks;
   cudaError_t e = win.window ? launch_prefill_window(tq, tk, tv, tv1, to, p, d, kind,
-                                                     static_cast<int>(grid), st)
+                                                     static_cast<int>(grid), max_ctx_len, st)
                              : launch_prefill(tq, tk, tv, tv1, to, p, d, causal != 0, kind,
                                               static_cast<int>(grid), st);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

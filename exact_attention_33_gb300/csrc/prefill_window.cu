@@ -32,8 +32,9 @@ template <int D>
 static cudaError_t launch_prefill_window_d(const CUtensorMap &tq, const CUtensorMap &tk,
                                            const CUtensorMap &tv, const CUtensorMap &tv1,
                                            const CUtensorMap &to, const PrefillParams &p, int kind,
-                                           int grid, cudaStream_t stream) {
-  const long long reach = static_cast<long long>(p.window) + p.sinks;
+                                           int grid, int longest, cudaStream_t stream) {
+  const long long reach =
+      static_cast<long long>(std::min(p.window, longest)) + std::min(p.sinks, longest);
   const bool persistent = grid > p.prefetch_ahead && reach <= kPersistentKeys &&
                           3 * reach <= static_cast<long long>(p.max_pairs) * kPrefillBM;
   switch (kind) {
@@ -66,13 +67,13 @@ static cudaError_t launch_prefill_window_d(const CUtensorMap &tq, const CUtensor
 
 // Head-pair kinds run two heads of a KV group over the same 128 rows per CTA;
 // the others one query tile per CTA, so that every tile of a CTA has the same
-// key tiles.
+// key tiles.  longest: the caller's bound on the sequences' keys.
 cudaError_t launch_prefill_window(const CUtensorMap &tq, const CUtensorMap &tk,
                                   const CUtensorMap &tv, const CUtensorMap &tv1,
                                   const CUtensorMap &to, const PrefillParams &p, int d, int kind,
-                                  int grid, cudaStream_t stream) {
-  return d == 64 ? launch_prefill_window_d<64>(tq, tk, tv, tv1, to, p, kind, grid, stream)
-                 : launch_prefill_window_d<128>(tq, tk, tv, tv1, to, p, kind, grid, stream);
+                                  int grid, int longest, cudaStream_t stream) {
+  return d == 64 ? launch_prefill_window_d<64>(tq, tk, tv, tv1, to, p, kind, grid, longest, stream)
+                 : launch_prefill_window_d<128>(tq, tk, tv, tv1, to, p, kind, grid, longest, stream);
 }
 
 }  // namespace fa

@@ -183,3 +183,16 @@ def test_tables_of_many_columns(fa):
         assert_device_clean()
         assert all(torch.equal(x, y) for x, y in zip(want, got)), i
         assert bool(torch.isfinite(got[1]).all()), i
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(4, 2, 64), (3, 3, 128)])
+def test_a_sequence_longer_than_said(fa, H, Hkv, d):
+    """max_seqlen is a bound on every length; a longer sequence that the launch
+    covers all the same keeps its own window."""
+    lens, said, window, sinks = [100, 60], 50, 80, 2
+    cu = [0, 100, 160]
+    q, k, v = (normal(240 + i, 160, h, d) for i, h in enumerate((H, Hkv, Hkv)))
+    out, lse = fa.fa_fwd_varlen_window(q, k, v, i32(cu), said, window, sinks)
+    assert fa.fa_device_status(clear=True) in (0, fa.FA_DEV_BAD_SEQLEN)
+    for a, e in zip(cu, cu[1:]):
+        check_rows(out[a:e], lse[:, a:e], q[a:e], k[a:e], v[a:e], window, sinks, f"row {a}")
