@@ -100,7 +100,8 @@ struct PrefillLayout {
   static constexpr int kCodes = kOnesOff + (kOnes ? kChunkBytes : 0);  // two tiles of V's codes
   static constexpr int kCodeBytes = KV8 ? 128 * D : 0;                 // one tile of codes
   // Block scales of K, 8 floats a key tile, written beside the tile's copies
-  // and read by the softmax.  The copies of tile t wait for the products of
+  // and read by the softmax, which waits for them at a barrier of theirs: the
+  // products that it waits for as well do not read them.  The copies of tile t wait for the products of
   // tile t - kStagesK, which follow the softmax of the tile before it: so
   // kStagesK + 1 slots would do.
   static constexpr int kScaleSlots = 8;
@@ -109,9 +110,11 @@ struct PrefillLayout {
   static constexpr int kBar = kScales + (KV8 ? kScaleSlots * 8 * 4 : 0);
   // q_full, k_full[SK], k_empty[SK], v_full[SV], s_full[2], p_full[2],
   // o_done[2], drain, v_empty[SV], and over an 8-bit cache c_full[2],
-  // c_empty[2] of V's staged codes and q_ready, in a persistent CTA q_free.  A V
-  // stage is released as soon as the P V products of its key tile are done.
-  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7 + (KV8 ? 5 : 0) + (PERS ? 1 : 0);
+  // c_empty[2] of V's staged codes, q_ready and ks_full[] of K's block scales, in
+  // a persistent CTA q_free.  A V stage is released as soon as the P V products
+  // of its key tile are done.
+  static constexpr int kNumBars = 1 + 2 * kStagesK + 2 * kStagesV + 7 +
+                                  (KV8 ? 5 + kScaleSlots : 0) + (PERS ? 1 : 0);
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kSmemAlloc = kBytes + 1024;     // base is aligned up to 1024 in-kernel
@@ -494,6 +497,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
   uint64_t *c_full = v_empty + SV;  // 8-bit caches: codes of V staged
   uint64_t *c_empty = c_full + 2;   // and read by the four widening warps
   uint64_t *q_ready = c_empty + 2;  // 8-bit caches: Q in two 8-bit terms
+  uint64_t *ks_full = q_ready + 1;  // 8-bit caches: K's block scales of a key tile, by slot
   uint64_t *q_free = v_empty + SV;  // persistent: the item's last S products have read Q
   constexpr bool ONES = L::kOnes;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
@@ -543,6 +547,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
         mbar_init(&c_empty[i], 4);
       }
       mbar_init(q_ready, live1 ? 256 : 128);
+      for (int x = 0; x < L::kScaleSlots; ++x) mbar_init(&ks_full[x], kPrefillBN / kDecodeBlock);
     }
     if (PERS) mbar_init(q_free, 1);
     *abort_flag = 0;
@@ -642,6 +647,7 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
         if (k_producer && lane < kTileBlocks) {
           reinterpret_cast<float *>(smem + L::kScales)[(j % L::kScaleSlots) * kTileBlocks + lane] =
               sc;
+          mbar_arrive(&ks_full[j % L::kScaleSlots]);
           if (phys == -2) {  // a bad id's keys are 0
             for (int t = 0; t < kDecodeBlock * D / 16; ++t)
               reinterpret_cast<uint4 *>(dst)[t] = make_uint4(0u, 0u, 0u, 0u);
@@ -1140,6 +1146,19 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
       const int limit_lo = WIN ? qi + offset + 1 - p.window : 0;  // windowed: and only from here on
 
       for (int j = 0; j < my_end; ++j) {
+        // 8-bit caches: the tile's block scales, there before its scores are
+        float s8[KV8 ? 8 : 1];
+        if constexpr (KV8) {
+          ok = mbar_wait_warp(&ks_full[j % L::kScaleSlots], (j / L::kScaleSlots) & 1, abort_flag,
+                              p.status);
+          if (!ok) break;
+          const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kScales) +
+                             (j % L::kScaleSlots) * 2;
+          const float4 k0 = ks[0], k1 = ks[1];
+          const float x8[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int blk = 0; blk < 8; ++blk) s8[blk] = x8[blk] * q_scale;
+        }
         ok = mbar_wait(&s_full[i], (tiles0 + j) & 1, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -1148,13 +1167,9 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
         uint32_t sr[128];
         tmem_ld128_wait(tS, sr);
         if constexpr (KV8) {
-          const float4 *ks = reinterpret_cast<const float4 *>(smem + L::kScales) +
-                             (j % L::kScaleSlots) * 2;
-          const float4 k0 = ks[0], k1 = ks[1];
-          const float s8[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
           for (int blk = 0; blk < 8; ++blk) {
-            const float2 c2 = make_float2(s8[blk] * q_scale, s8[blk] * q_scale);
+            const float2 c2 = make_float2(s8[blk], s8[blk]);
 #pragma unroll
             for (int c = blk * 16; c < blk * 16 + 16; c += 2) {
               const float2 x =
