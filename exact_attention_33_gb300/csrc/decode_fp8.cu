@@ -214,9 +214,7 @@ __global__ void __launch_bounds__(32)
     // exponent that takes the row to [2^7, 2^8) (a row of zeros, or with an
     // infinity or NaN, stays as it is: e4m3 keeps NaN, and an infinite score
     // has no softmax, so infinities become NaN below)
-    const int ex = static_cast<int>(top >> 7);
-    const int e = (ex == 0 || ex == 255) ? 0 : 7 - (ex - 127);
-    // (two factors: the power itself may exceed fp32's)
+    const int e = exponent_to_2_7(top);
     const float f0 = pow2_clamped(e / 2), f1 = pow2_clamped(e - e / 2);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -228,9 +226,9 @@ __global__ void __launch_bounds__(32)
         h = pack_e4m3x4((a - h0.x) * 16.f, (b2 - h0.y) * 16.f, (c - h1.x) * 16.f,
                         (d - h1.y) * 16.f);
       }
-      qf[nt][w] = (ex == 255) ? 0x7F7F7F7Fu : h;
+      qf[nt][w] = (top >= 0x7F80u) ? 0x7F7F7F7Fu : h;
     }
-    cq[nt] = pow2_clamped(-__shfl_sync(0xffffffffu, e, quad * 8));
+    cq[nt] = pow2_exact(-__shfl_sync(0xffffffffu, e, quad * 8));
   }
 
   // O^T: columns 2 h and 2 h + 1 of tile np are heads h of S tiles 2 np and

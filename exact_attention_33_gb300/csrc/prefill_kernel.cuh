@@ -218,9 +218,7 @@ __device__ __forceinline__ float split_q_row(uint8_t *tile, int row, int bar) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) top = max(top, max(w[x] & 0x7FFFu, (w[x] >> 16) & 0x7FFFu));
   }
-  const int ex = static_cast<int>(top >> 7);
-  const int e = (ex == 0 || ex == 255) ? 0 : 7 - (ex - 127);
-  // (two factors: the power itself may exceed fp32's)
+  const int e = exponent_to_2_7(top);
   const float f0 = pow2_clamped(e / 2), f1 = pow2_clamped(e - e / 2);
   if (D == 64) named_bar_sync(bar, 128);
 #pragma unroll
@@ -235,14 +233,14 @@ __device__ __forceinline__ float split_q_row(uint8_t *tile, int row, int bar) {
       h[x] = pack_e4m3x4(v0, v1, v2, v3);
       const float2 h0 = e4m3x2_to_float2(h[x]), h1 = e4m3x2_to_float2(h[x] >> 16);
       l[x] = pack_e5m2x4(v0 - h0.x, v1 - h0.y, v2 - h1.x, v3 - h1.y);
-      if (ex == 255) h[x] = l[x] = 0x7F7F7F7Fu;
+      if (top >= 0x7F80u) h[x] = l[x] = 0x7F7F7F7Fu;
     }
     const int at = (D == 128) ? row * 128 + ((u ^ (row & 7)) << 4)
                               : row * 64 + ((u ^ ((row >> 1) & 3)) << 4);
     *reinterpret_cast<uint4 *>(tile + at) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4 *>(tile + 128 * D + at) = make_uint4(l[0], l[1], l[2], l[3]);
   }
-  return pow2_clamped(-e);
+  return pow2_exact(-e);
 }
 
 // The sequence with the rank-th longest context of p.B <= 32 (equal ones in
@@ -617,11 +615,11 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
       // K's go to the stages that the products read, V's to two staging
       // buffers.  One copy per block, issued by lanes 0 .. 7 after lane 0 has
       // posted the byte count.  Block ids, and K's block scales, are read four
-      // tiles ahead of their use.
+      // tiles ahead of their use.  The softmax scale goes into them.
       auto scale_of = [&](int id) {
         if (!k_producer || id < 0) return 0.f;
-        return checked_load(p.k_scale, static_cast<size_t>(id) * p.Hkv + kvh,
-                            static_cast<size_t>(p.num_blocks) * p.Hkv, p.status);
+        return p.scale_log2 * checked_load(p.k_scale, static_cast<size_t>(id) * p.Hkv + kvh,
+                                           static_cast<size_t>(p.num_blocks) * p.Hkv, p.status);
       };
       const CUtensorMap *map = k_producer ? &tm_k : &tm_v;
       const int stages = k_producer ? SK : 2;
@@ -1117,12 +1115,15 @@ __global__ void __launch_bounds__(PrefillShape<QT, KV8, PERS>::kThreads,
       const int qi = tile_row(i) + row;  // query row within the sequence
       const int hi = tile_head(i);       // query head of this tile
       const int my_end = kv_end[i];
-      float q_scale = 1.f;  // 8-bit caches: what the scores of this row's codes are multiplied by
+      // 8-bit caches: the scores of this row's codes are multiplied by this and by their
+      // block's scale (the softmax scale is in that one: this may be a subnormal
+      // power of two, which holds no factor more)
+      float q_scale = 1.f;
       if constexpr (KV8) {
         if (my_end > 0) {
           // Q as two 8-bit terms, each thread its own row, in the tile's place
           if (mbar_wait_warp(q_full, 0, abort_flag, p.status))
-            q_scale = p.scale_log2 * split_q_row<D>(sQ + i * L::kTileBytes, row, 1 + i);
+            q_scale = split_q_row<D>(sQ + i * L::kTileBytes, row, 1 + i);
           else if (D == 64)
             named_bar_sync(1 + i, 128);  // (split_q_row's)
           fence_proxy_async_smem();

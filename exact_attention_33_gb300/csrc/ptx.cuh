@@ -615,6 +615,21 @@ __device__ __forceinline__ float pow2_clamped(int e) {
   return __int_as_float((min(max(e, -126), 127) + 127) << 23);
 }
 
+// 2^e, -149 <= e <= 127, subnormals among them.
+__device__ __forceinline__ float pow2_exact(int e) {
+  return __int_as_float(e >= -126 ? (e + 127) << 23 : 1 << (e + 149));
+}
+
+// Exponent e that takes a bf16 magnitude (its bits, also of a subnormal) into
+// [2^7, 2^8), -120 <= e <= 140; 0 for zero, infinities and NaN.  (2^e may exceed
+// fp32: multiply by 2^(e / 2) and 2^(e - e / 2) in turn.)
+__device__ __forceinline__ int exponent_to_2_7(uint32_t bits) {
+  if (bits == 0u || bits >= 0x7F80u) return 0;
+  // (a subnormal is its bits times 2^-133)
+  const int biased = bits < 0x80u ? 25 - __clz(bits) : static_cast<int>(bits >> 7);
+  return 7 + 127 - biased;
+}
+
 // Pack two fp32 values into bf16x2 (round to nearest even); `lo` goes to
 // the low half.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

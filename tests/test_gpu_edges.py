@@ -196,3 +196,36 @@ def test_a_sequence_longer_than_said(fa, H, Hkv, d):
     assert fa.fa_device_status(clear=True) in (0, fa.FA_DEV_BAD_SEQLEN)
     for a, e in zip(cu, cu[1:]):
         check_rows(out[a:e], lse[:, a:e], q[a:e], k[a:e], v[a:e], window, sinks, f"row {a}")
+
+
+# ------------------------------------------------------------------ tiny queries
+
+@pytest.mark.parametrize("top", [-100, -119, -122, -126, -128, -133])
+def test_tiny_queries_over_large_keys(fa, top):
+    """Queries of 2^top, down to bf16's smallest subnormal, over blocks whose
+    scales make up for it."""
+    ctx, H, Hkv, d, n = [90], 2, 1, 64, 20
+    c = Cache(ctx, Hkv, d, seed=260)
+    rng = np.random.default_rng(261)
+    c.scale["k"] = np.full_like(c.scale["k"], 2.0 ** min(-top - 8, 118))
+    c.dscale["k"].copy_(dev(c.scale["k"]))
+    # few significand bits: also the subnormal ones are exact
+    x = rng.integers(-3, 4, (n, H, d)).astype(np.float64) * 2.0 ** top
+    q = bf16(x.astype(np.float32))
+    assert np.array_equal(q.float().cpu().numpy().astype(np.float64), x)
+    lens, cu = dev(np.int32(ctx)), dev(np.int32([0, n]))
+    out, lse = fa.fa_fwd_paged_fp8(q, *c.args(), lens, cu, n, 90)
+    tok, tlse = fa.fa_decode_paged_fp8(q[-1:], *c.args(), lens, 90)
+    assert_device_clean()
+    k, v = c.rows("k", 0, 90)[:, 0], c.rows("v", 0, 90)[:, 0]
+    for h in range(H):
+        qh = dev(x[:, h])
+        o, l, tol = ref.forward(qh, k, v, 0, 0)
+        # scores: fp32 sums of exact products
+        off = 2.0 ** -18 * float((qh.abs() @ k.T.abs()).max()) / math.sqrt(d)
+        size = 2 * off * float(v.abs().max())
+        ref.assert_within(out[:, h], o, tol + size, f"chunk head {h}")
+        assert float((lse[h].double() - l).abs().max()) <= ref.LSE_TOL + off
+        o, l, tol = cr.decode_rows(qh[-1:], k, v, 0, 0)
+        ref.assert_within(tok[:, h], o, tol + size, f"token head {h}")
+        assert abs(float(tlse[0, h]) - float(l)) <= ref.LSE_TOL + off
