@@ -18,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -75,24 +76,44 @@ def _run(cmd, verbose):
     return r.stdout
 
 
+def _newer(path, deps):
+    """``path`` exists and is no older than any of ``deps``."""
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
+
+
+def _build_torch_calls(verbose):
+    """The extension module, or a warning: the binding makes its calls without it."""
+    tmp = TORCH_CALLS + ".tmp"
+    try:
+        _run(torch_calls_command(tmp), verbose)
+        os.replace(tmp, TORCH_CALLS)
+    except Exception as e:
+        if os.path.exists(TORCH_CALLS):  # made from older headers: not to be bound
+            os.remove(TORCH_CALLS)
+        warnings.warn(f"calls on torch tensors take longer without {TORCH_CALLS}: {e}",
+                      RuntimeWarning)
+
+
 def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = False,
           checked: bool = False) -> str:
     """Compile every CUDA source and link libfa.so (libfa_checked.so with
-    ``checked``); returns the library path."""
+    ``checked``); returns the library path.  The library needs nvcc alone; the
+    extension module beside it is left out with a warning where it does not
+    compile."""
     nvcc = nvcc_path()
     build_dir, lib = (BUILD_CHECKED, LIB_CHECKED) if checked else (BUILD, LIB)
     defines = ["-DFA_DEBUG_CHECKS"] if checked else []
     os.makedirs(build_dir, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    deps = srcs + [os.path.join(CSRC, h) for h in os.listdir(CSRC)
-                   if h.endswith((".h", ".cuh", ".cpp"))]
     inc = os.path.join(PKG, "..", "include")
-    deps += [os.path.join(inc, h) for h in os.listdir(inc)]
-    if not force and os.path.exists(lib) and os.path.exists(TORCH_CALLS):
-        lib_t = min(os.path.getmtime(lib), os.path.getmtime(TORCH_CALLS)) \
-            if not checked else os.path.getmtime(lib)
-        if all(os.path.getmtime(d) <= lib_t for d in deps):
-            return lib
+    api = [os.path.join(inc, h) for h in os.listdir(inc)]
+    deps = api + srcs + [os.path.join(CSRC, h) for h in os.listdir(CSRC)
+                         if h.endswith((".h", ".cuh"))]
+    lib_ready = not force and _newer(lib, deps)
+    if checked:   # (one module serves both builds)
+        calls_ready = os.path.exists(TORCH_CALLS)
+    else:
+        calls_ready = not force and _newer(TORCH_CALLS, api + [os.path.join(CSRC, "torch_calls.cpp")])
 
     def compile_one(src):
         obj = os.path.join(build_dir, os.path.basename(src).replace(".cu", ".o"))
@@ -104,20 +125,15 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
             print(out, flush=True)
         return obj
 
-    def compile_torch_calls():
-        tmp = TORCH_CALLS + ".tmp"
-        _run(torch_calls_command(tmp), verbose)
-        os.replace(tmp, TORCH_CALLS)
-
     with ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        # (one module serves both builds)
-        calls = None if checked and os.path.exists(TORCH_CALLS) else ex.submit(compile_torch_calls)
-        objs = list(ex.map(compile_one, srcs))
+        calls = None if calls_ready else ex.submit(_build_torch_calls, verbose)
+        if not lib_ready:
+            objs = list(ex.map(compile_one, srcs))
+            tmp = lib + ".tmp"
+            _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs, verbose)
+            os.replace(tmp, lib)
         if calls is not None:
             calls.result()
-    tmp = lib + ".tmp"
-    _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs, verbose)
-    os.replace(tmp, lib)
     return lib
 
 
