@@ -110,10 +110,8 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
     deps = api + srcs + [os.path.join(CSRC, h) for h in os.listdir(CSRC)
                          if h.endswith((".h", ".cuh"))]
     lib_ready = not force and _newer(lib, deps)
-    if checked:   # (one module serves both builds)
-        calls_ready = os.path.exists(TORCH_CALLS)
-    else:
-        calls_ready = not force and _newer(TORCH_CALLS, api + [os.path.join(CSRC, "torch_calls.cpp")])
+    # (one module serves both builds)
+    calls_ready = not force and _newer(TORCH_CALLS, api + [os.path.join(CSRC, "torch_calls.cpp")])
 
     def compile_one(src):
         obj = os.path.join(build_dir, os.path.basename(src).replace(".cu", ".o"))

@@ -48,6 +48,17 @@ def test_library_without_the_module(tree, monkeypatch):
         b.build(force=True)
 
 
+def test_checked_build_renews_the_module(tree):
+    (tree / "csrc" / "torch_calls.cpp").write_text("old")
+    b.build(checked=True)
+    assert (tree / "_torch_calls.so").read_text() == "old"
+    (tree / "csrc" / "torch_calls.cpp").write_text("new")
+    for f in ("libfa_checked.so", "_torch_calls.so"):
+        age(tree / f, 60)
+    b.build(checked=True)
+    assert (tree / "_torch_calls.so").read_text() == "new"
+
+
 def test_a_lost_module_is_made_again(tree):
     b.build()
     os.remove(tree / "_torch_calls.so")
