@@ -19,6 +19,7 @@ import ctypes
 import math
 import os
 import threading
+import warnings
 
 __all__ = [
     "FaError", "library_path", "load_library", "fa_fwd", "fa_fwd_varlen", "fa_fwd_paged",
@@ -705,7 +706,8 @@ def _short():
     """The extension module (csrc/torch_calls.cpp) whose functions make a call
     on the current stream when all its tensors are as they should be, and
     return None otherwise; the functions here go on from there.  False where it
-    has not been built: the calls are then made from here, which takes longer."""
+    has not been built or does not load: the calls are then made from here, which
+    takes longer."""
     global _calls
     if _calls is None:
         lib = load_library()
@@ -715,11 +717,16 @@ def _short():
             _calls = False
             return _calls
         import importlib.util
-        spec = importlib.util.spec_from_file_location(__name__ + "._torch_calls", path)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BOUND))
-        _calls = module
+        try:
+            spec = importlib.util.spec_from_file_location(__name__ + "._torch_calls", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BOUND))
+            _calls = module
+        except Exception as e:  # made for another torch or Python
+            _calls = False
+            warnings.warn(f"calls on torch tensors take longer: {path} does not load ({e})",
+                          RuntimeWarning)
     return _calls
 
 

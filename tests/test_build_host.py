@@ -1,6 +1,7 @@
 """The build and the binding's extension module (no GPU): the C library does
 not depend on the module, and no module outlives the headers it was made from."""
 import os
+import shutil
 
 import pytest
 
@@ -67,3 +68,21 @@ def test_a_lost_module_is_made_again(tree):
     b.build()
     assert (tree / "_torch_calls.so").exists()
     assert os.stat(tree / "libfa.so").st_mtime_ns == before   # not linked again
+
+
+def test_a_module_that_does_not_load(tmp_path, monkeypatch):
+    """The calls are then made from Python."""
+    import exact_attention_33_gb300 as fa
+    b.build()
+    fa.load_library()
+    (tmp_path / "_torch_calls.so").write_text("made for another torch")
+    monkeypatch.setattr(fa, "_PKG", str(tmp_path))
+    monkeypatch.setattr(fa, "_calls", None)
+    with pytest.warns(RuntimeWarning):
+        assert fa._short() is False
+    assert fa._short() is False
+    shutil.rmtree(tmp_path)
+    torch = pytest.importorskip("torch")
+    q = torch.zeros((1, 8, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        fa.fa_fwd_window(q, q, q, 4)
