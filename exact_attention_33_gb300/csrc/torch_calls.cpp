@@ -46,6 +46,7 @@ struct {
 // the call wants it; the caller looks at `ok` before it uses any of them.
 struct Args {
   PyObject *const *v;
+  int n;   // arguments
   int at = 0;
   bool ok = true;
   int dev = -1;
@@ -77,6 +78,15 @@ struct Args {
     if (!THPVariable_CheckExact(o)) return fail();
     const ScalarType type = THPVariable_Unpack(o).scalar_type();
     return tensor(type == ScalarType::Byte ? type : ScalarType::Float8_e4m3fn, dim);
+  }
+  // the workspace, the last argument: asked for before there are outputs, so that
+  // a call without one, which is made from Python, allocates nothing here
+  const Tensor *workspace() {
+    const int here = at;
+    at = n - 1;
+    const Tensor *t = tensor(ScalarType::Byte, 1);
+    at = here;
+    return t;
   }
   // the caller's tensor of this type and shape, or a new one
   Tensor output(ScalarType type, at::IntArrayRef shape) {
@@ -170,7 +180,7 @@ template <typename Body>
 PyObject *call(PyObject *const *v, Py_ssize_t given, Py_ssize_t n, Body body) {
   if (given != n) Py_RETURN_NONE;
   try {
-    Args a{v};
+    Args a{v, static_cast<int>(n)};
     return body(a);
   } catch (...) {
     PyErr_Clear();
@@ -263,10 +273,10 @@ PyObject *decode_paged_window(PyObject *, PyObject *const *v, Py_ssize_t given) 
     const int window = a.integer(1, INT_MAX), sinks = a.integer(0, INT_MAX);
     const float scale = a.scale(q->size(2));
     const bool want = a.flag();
+    const Tensor *ws = a.workspace();
     NEED(a.ok);
     const Tensor out = a.output(kBf16, q->sizes());
     const Tensor lse = lse_output(a, {q->size(0), q->size(1)}, want);
-    const Tensor *ws = a.tensor(ScalarType::Byte, 1);
     NEED(a.ok);
     return results(
         lib.decode_paged_window(ptr(q), ptr(k), ptr(w), ints(table), size(table, 1), ints(ctx),
@@ -288,10 +298,10 @@ PyObject *bwd_window(PyObject *, PyObject *const *v, Py_ssize_t given) {
     const Tensor *dout = a.tensor(kBf16, q->sizes());
     const int window = a.integer(1, INT_MAX), sinks = a.integer(0, INT_MAX);
     const float scale = a.scale(q->size(3));
+    const Tensor *ws = a.workspace();
     NEED(a.ok);
     const Tensor dq = a.output(kBf16, q->sizes()), dk = a.output(kBf16, k->sizes());
     const Tensor dv = a.output(kBf16, k->sizes());
-    const Tensor *ws = a.tensor(ScalarType::Byte, 1);
     NEED(a.ok);
     return results(lib.bwd_window(ptr(q), ptr(k), ptr(w), ptr(out), floats(lse), ptr(dout), ptr(dq),
                                   ptr(dk), ptr(dv), size(q, 0), size(q, 2), size(k, 2), size(q, 1),
@@ -314,10 +324,10 @@ PyObject *bwd_varlen_window(PyObject *, PyObject *const *v, Py_ssize_t given) {
     const int longest = a.integer(INT_MIN, INT_MAX);
     const int window = a.integer(1, INT_MAX), sinks = a.integer(0, INT_MAX);
     const float scale = a.scale(q->size(2));
+    const Tensor *ws = a.workspace();
     NEED(a.ok && cu->numel() >= 1 && small(cu));
     const Tensor dq = a.output(kBf16, q->sizes()), dk = a.output(kBf16, k->sizes());
     const Tensor dv = a.output(kBf16, k->sizes());
-    const Tensor *ws = a.tensor(ScalarType::Byte, 1);
     NEED(a.ok);
     return results(
         lib.bwd_varlen_window(ptr(q), ptr(k), ptr(w), ptr(out), floats(lse), ptr(dout), ptr(dq),
@@ -396,10 +406,10 @@ PyObject *decode_paged_fp8(PyObject *, PyObject *const *v, Py_ssize_t given) {
     NEED(cache_window(a, window, sinks));
     const float scale = a.scale(q->size(2));
     const bool want = a.flag();
+    const Tensor *ws = a.workspace();
     NEED(a.ok);
     const Tensor out = a.output(kBf16, q->sizes());
     const Tensor lse = lse_output(a, {q->size(0), q->size(1)}, want);
-    const Tensor *ws = a.tensor(ScalarType::Byte, 1);
     NEED(a.ok);
     return results(
         lib.decode_paged_fp8(ptr(q), ptr(c.k), ptr(c.v), floats(c.k_scale), floats(c.v_scale),

@@ -229,3 +229,35 @@ def test_tiny_queries_over_large_keys(fa, top):
         o, l, tol = cr.decode_rows(qh[-1:], k, v, 0, 0)
         ref.assert_within(tok[:, h], o, tol + size, f"token head {h}")
         assert abs(float(tlse[0, h]) - float(l)) <= ref.LSE_TOL + off
+
+
+# ------------------------------------------------------------------ what a call takes
+
+def allocations(call):
+    torch = torch_mod()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_stats().get("allocation.all.allocated", 0)
+    keep = call()
+    return torch.cuda.memory_stats()["allocation.all.allocated"] - before, keep
+
+
+def test_calls_allocate_their_outputs_once(fa):
+    ctx, H, Hkv, d = [90, 40], 4, 2, 64
+    c = Cache(ctx, Hkv, d, seed=270)
+    kp, vp, table, _ = pages(ctx, Hkv, d, 271)
+    table, lens = table.cuda(), i32(ctx)
+    tok = normal(272, 2, H, d)
+    q, k, v, g = (normal(273 + i, 1, 90, h, d) for i, h in enumerate((H, Hkv, Hkv, H)))
+    cu = i32([0, 90])
+    out, lse = fa.fa_fwd_window(q, k, v, 30, 2)
+    calls = [   # outputs and the workspace
+        (3, lambda: fa.fa_decode_paged_fp8(tok, *c.args(), lens, 90)),
+        (3, lambda: fa.fa_decode_paged_window(tok, kp, vp, table, lens, 90, 30, 2)),
+        (4, lambda: fa.fa_bwd_window(q, k, v, out, lse, g, 30, 2)),
+        (4, lambda: fa.fa_bwd_varlen_window(q[0], k[0], v[0], out[0], lse[0], g[0], cu, 90, 30, 2)),
+    ]
+    for i, (most, call) in enumerate(calls):
+        call()
+        n, _ = allocations(call)
+        assert n <= most, (i, n)
+    assert_device_clean()
