@@ -927,8 +927,9 @@ def fa_bwd_window_workspace_size(B, H, Hkv, N, d, window, sinks=0) -> int:
 
 
 def _check_bwd(q, k, v, out, dout, ndim):
-    """Checks the inputs of a backward call."""
+    """Checks the inputs of a windowed backward call (out may be None)."""
     _check_bf16_cuda("q", q, ndim)
+    out = dout if out is None else out
     for name, t in (("k", k), ("v", v), ("out", out), ("dout", dout)):
         _check_bf16_cuda(name, t, ndim, q.device)
     if k.shape != (*q.shape[:-2], k.shape[-2], q.shape[-1]) or v.shape != k.shape \
@@ -952,7 +953,8 @@ def _grads(q, k, v, dq, dk, dv):
 def fa_bwd_window(q, k, v, out, lse, dout, window, sinks=0, scale=None, dq=None, dk=None, dv=None,
                   workspace=None, stream=None):
     """Gradient of :func:`fa_fwd_window`.  q, out, dout [B,N,H,d]; k, v
-    [B,N,Hkv,d] bf16 CUDA tensors; lse [B,H,N] fp32.  Returns (dq, dk, dv)."""
+    [B,N,Hkv,d] bf16 CUDA tensors; lse [B,H,N] fp32.  out is not read and may
+    be None.  Returns (dq, dk, dv)."""
     short = _calls or _short()
     if short and stream is None:
         done = short.bwd_window(q, k, v, out, lse, dout, window, sinks, scale, dq, dk, dv, workspace)
@@ -981,8 +983,9 @@ def fa_bwd_window(q, k, v, out, lse, dout, window, sinks=0, scale=None, dq=None,
 def fa_bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window, sinks=0,
                          scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Gradient of :func:`fa_fwd_varlen_window`.  q, out, dout [T,H,d]; k, v
-    [T,Hkv,d] bf16 CUDA tensors; lse [H,T] fp32; cu_seqlens int32 [S+1].
-    Returns (dq, dk, dv); rows outside every sequence are left as they were."""
+    [T,Hkv,d] bf16 CUDA tensors; lse [H,T] fp32; cu_seqlens int32 [S+1].  out is
+    not read and may be None.  Returns (dq, dk, dv); rows outside every sequence
+    are left as they were."""
     short = _calls or _short()
     if short and stream is None:
         done = short.bwd_varlen_window(q, k, v, out, lse, dout, cu_seqlens, max_seqlen, window, sinks,

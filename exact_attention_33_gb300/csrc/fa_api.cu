@@ -441,7 +441,8 @@ static int bwd_dense(const void *q, const void *k, const void *v, const void *ou
                      const float *lse, const void *dout, void *dq, void *dk, void *dv, int B,
                      int H, int Hkv, int N, int d, float scale, int causal, void *workspace,
                      size_t workspace_bytes, fa_stream_t stream, WindowSpec win) {
-  if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
+  if (!q || !k || !v || !lse || !dout || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
+  if (!out && !win.window) return FA_ERR_INVALID_ARG;  // (a windowed call does not read it)
   for (const void *ptr : {q, k, v, out, dout, static_cast<const void *>(dq),
                           static_cast<const void *>(dk), static_cast<const void *>(dv)})
     if (!aligned(ptr, 16)) return FA_ERR_INVALID_ARG;
@@ -528,8 +529,9 @@ static int bwd_varlen(const void *q, const void *k, const void *v, const void *o
                       const int32_t *cu_seqlens, int num_seqs, int total_tokens, int max_seqlen,
                       int H, int Hkv, int d, float scale, int causal, void *workspace,
                       size_t workspace_bytes, fa_stream_t stream, WindowSpec win) {
-  if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv || !cu_seqlens)
+  if (!q || !k || !v || !lse || !dout || !dq || !dk || !dv || !cu_seqlens)
     return FA_ERR_INVALID_ARG;
+  if (!out && !win.window) return FA_ERR_INVALID_ARG;  // (a windowed call does not read it)
   for (const void *ptr : {q, k, v, out, dout, static_cast<const void *>(dq),
                           static_cast<const void *>(dk), static_cast<const void *>(dv)})
     if (!aligned(ptr, 16)) return FA_ERR_INVALID_ARG;

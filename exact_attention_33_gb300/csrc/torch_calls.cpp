@@ -79,6 +79,12 @@ struct Args {
     const ScalarType type = THPVariable_Unpack(o).scalar_type();
     return tensor(type == ScalarType::Byte ? type : ScalarType::Float8_e4m3fn, dim);
   }
+  // a tensor that the call does not read, or None
+  const Tensor *unread(ScalarType type, at::IntArrayRef shape) {
+    if (v[at] != Py_None) return tensor(type, shape);
+    ++at;
+    return nullptr;
+  }
   // the workspace, the last argument: asked for before there are outputs, so that
   // a call without one, which is made from Python, allocates nothing here
   const Tensor *workspace() {
@@ -131,7 +137,7 @@ const auto kInt = ScalarType::Int;
 const auto kF32 = ScalarType::Float;
 
 void *ptr(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
-void *ptr(const Tensor *t) { return t->data_ptr(); }
+void *ptr(const Tensor *t) { return t ? t->data_ptr() : nullptr; }
 int size(const Tensor *t, int i) { return static_cast<int>(t->size(i)); }
 const int32_t *ints(const Tensor *t) { return static_cast<const int32_t *>(t->data_ptr()); }
 float *floats(const Tensor *t) { return static_cast<float *>(t->data_ptr()); }
@@ -293,7 +299,7 @@ PyObject *bwd_window(PyObject *, PyObject *const *v, Py_ssize_t given) {
     const Tensor *q = a.tensor(kBf16, 4), *k = a.tensor(kBf16, 4), *w = a.tensor(kBf16, 4);
     NEED(a.ok && small(q) && k->sizes() == w->sizes() && k->size(0) == q->size(0) &&
          k->size(1) == q->size(1) && k->size(3) == q->size(3) && k->size(2) <= INT_MAX);
-    const Tensor *out = a.tensor(kBf16, q->sizes());
+    const Tensor *out = a.unread(kBf16, q->sizes());
     const Tensor *lse = a.tensor(kF32, {q->size(0), q->size(2), q->size(1)});
     const Tensor *dout = a.tensor(kBf16, q->sizes());
     const int window = a.integer(1, INT_MAX), sinks = a.integer(0, INT_MAX);
@@ -318,7 +324,7 @@ PyObject *bwd_varlen_window(PyObject *, PyObject *const *v, Py_ssize_t given) {
     const Tensor *q = a.tensor(kBf16, 3), *k = a.tensor(kBf16, 3), *w = a.tensor(kBf16, 3);
     NEED(a.ok && small(q) && k->sizes() == w->sizes() && k->size(0) == q->size(0) &&
          k->size(2) == q->size(2) && k->size(1) <= INT_MAX);
-    const Tensor *out = a.tensor(kBf16, q->sizes());
+    const Tensor *out = a.unread(kBf16, q->sizes());
     const Tensor *lse = a.tensor(kF32, {q->size(1), q->size(0)});
     const Tensor *dout = a.tensor(kBf16, q->sizes()), *cu = a.tensor(kInt, 1);
     const int longest = a.integer(INT_MIN, INT_MAX);

@@ -77,8 +77,9 @@ int fa_decode_paged_window(const void *q, const void *k_pool, const void *v_pool
                            size_t workspace_bytes, fa_stream_t stream);
 
 /* Gradients of fa_fwd_window and fa_fwd_varlen_window (the products of fa_bwd
-   over the visible pairs); out and lse as those calls wrote them, with the
-   same window and sinks.  The workspace has
+   over the visible pairs); lse as those calls wrote it, with the same window and
+   sinks.  out is not read (the row sums of dS come from P and dP) and may be
+   NULL.  The workspace has
    fa_bwd_window_workspace_size() bytes (a packed batch: B = num_seqs,
    N = max_seqlen), 256-byte aligned, overwritten, one call at a time.  One sized
    for some B and N serves every smaller B and N with the same H, Hkv, d, window

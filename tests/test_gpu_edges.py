@@ -261,3 +261,27 @@ def test_calls_allocate_their_outputs_once(fa):
         n, _ = allocations(call)
         assert n <= most, (i, n)
     assert_device_clean()
+
+
+def test_gradient_without_the_output(fa):
+    """The windowed gradient forms its row sums itself: O may be gone."""
+    torch = torch_mod()
+    lens, H, Hkv, d, window, sinks = [90, 200], 4, 2, 64, 30, 2
+    cu = i32([0, 90, 290])
+    q, k, v, g = (normal(280 + i, 290, h, d) for i, h in enumerate((H, Hkv, Hkv, H)))
+    out, lse = fa.fa_fwd_varlen_window(q, k, v, cu, 200, window, sinks)
+    want = fa.fa_bwd_varlen_window(q, k, v, out, lse, g, cu, 200, window, sinks)
+    got = fa.fa_bwd_varlen_window(q, k, v, None, lse, g, cu, 200, window, sinks)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    ws = torch.empty(fa.fa_bwd_window_workspace_size(2, H, Hkv, 200, d, window, sinks),
+                     dtype=torch.uint8, device="cuda")
+    got = fa.fa_bwd_varlen_window(q, k, v, None, lse, g, cu, 200, window, sinks, workspace=ws)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    q, k, v, g = (t[None, :200].contiguous() for t in (q, k, v, g))
+    out, lse = fa.fa_fwd_window(q, k, v, window, sinks)
+    want = fa.fa_bwd_window(q, k, v, out, lse, g, window, sinks)
+    got = fa.fa_bwd_window(q, k, v, None, lse, g, window, sinks)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    with pytest.raises(ValueError):
+        fa.fa_bwd_window(q, k, v, out[:, :50], lse, g, window, sinks)
+    assert_device_clean()
