@@ -2,10 +2,12 @@
 // = sum_j P_ij dP_ij, then dK / dV = sums of P^T dO and scale dS^T Q, then dQ =
 // scale dS K with dS = P (dP - D), over the tiles that the window and the sinks
 // leave.  Nine products where five are the gradient's, so that no kernel adds into
-// another's results.  Bound by the elementwise work on S and dP between the
-// products: 16 packed documents of up to 4096 rows, 16 / 4 heads of d = 128,
-// window 512, 16 sinks take 1.0 ms with the forward pass, 472 TFLOP/s of the
-// seven products that forward and gradient cannot do without.
+// another's results.  16 packed documents of up to 4096 rows, 16 / 4 heads of
+// d = 128, window 512, 16 sinks take 1.0 ms with the forward pass, 474 TFLOP/s of
+// the seven products that forward and gradient cannot do without.  No pipe is
+// full: the tensor pipe is busy 43 to 48% of the cycles (23 to 25% at d = 64), the
+// issue slots 29 to 36% (35 to 40%), the exponential's unit 12 to 26%.  Each step
+// waits in turn for scores, weights, dP and dS, mostly for loads from TMEM.
 #include "backward_kernel.cuh"
 
 namespace fa {

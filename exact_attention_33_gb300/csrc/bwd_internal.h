@@ -15,11 +15,13 @@ constexpr int kBwdOrderMaxSeqs = 128;  // multiple of 32
 
 struct BwdParams {
   unsigned int *status;   // per-device sticky FA_DEV_* word
-  const void *out;        // forward output O, bf16 [B, N, H, d] (packed: [T, H, d])
+  const void *out;        // forward output O, bf16 [B, N, H, d] (packed: [T, H, d]); a windowed
+                          // call does not read it (it may be null)
   const void *dout;       // upstream gradient dO, layout of out
   const float *lse;       // forward log-sum-exp, fp32 [B, H, N] (packed: [H, T]) (natural log)
   float *nlse2;           // workspace: -lse in log2 units, [B, H, Npad]
-  float *ndsum;           // workspace: -D = -rowsum(dO * O), [B, H, Npad]
+  float *ndsum;           // workspace: -D, [B, H, Npad], with D = rowsum(dO * O), in windowed
+                          // calls sum_j P_ij dP_ij
   void *dq, *dk, *dv;     // bf16, layouts of q, k, v
   int B, H, Hkv, group, N;  // packed batches: B sequences of at most N (max_seqlen) rows
   int Npad;               // N rounded up to 128

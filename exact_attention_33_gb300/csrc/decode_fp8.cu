@@ -12,7 +12,7 @@
 //     MMAs (fp32 sums), on the codes as they are; Q goes in as two e4m3 terms.
 //     It is scaled per head by a power of two that puts its largest value at
 //     2^7..2^8; Qh = e4m3(Q) takes its upper four significand bits and Ql =
-//     e4m3(16 (Q - Qh)) the other four, exactly down to 2^-14 of the largest
+//     e4m3(16 (Q - Qh)) the other four, exactly down to 2^-13 of the largest
 //     value and to within 2^-21 of it below.  A head's terms are neighbouring
 //     columns, so a thread holds both sums and adds them: s = S_h + S_l / 16.
 //     Which of d's values stand in which k-slots is free as long as K and Q

@@ -279,10 +279,10 @@ __device__ __forceinline__ int longest_context(const PrefillParams &p, int rank)
 // staging buffers, and warps 12-15 multiply them by their block's scale (exact
 // for powers of two, else one bf16 rounding) and store bf16 rows in the
 // swizzled layout that the MMAs read.  4 x 512 rows over 2196 to 8269 keys, 32
-// / 8 heads of d = 128 take 226 us; with K widened like V 257 us, bound by
+// / 8 heads of d = 128 take 224 us; with K widened like V 257 us, bound by
 // those warps' conversions and shared-memory traffic; without V's arithmetic
-// 226, so now the softmax and the products set the pace, as over a bf16 cache,
-// and the longest CTAs' 112 steps against 85 on average.  (Codes loaded
+// they take as long, so now the softmax and the products set the pace, as over a
+// bf16 cache, and the longest CTAs' 112 steps against 85 on average.  (Codes loaded
 // straight into registers, 32 or 64 of a thread's 88 in flight: 470 to 620 us.)
 template <int D, bool CAUSAL, int KIND, bool FP8 = false, int QT = 2, bool WIN = false,
           bool KV8 = false, bool PERS = false>

@@ -4,9 +4,11 @@
 // row to its diagonal, so the work grows with N (window + sinks) instead of
 // N^2.  Only the first window tile, the diagonal tile and the last sink tile
 // hold masked scores.  32 packed prompts of 64 to 4096 rows, 16 / 4 heads of
-// d = 128, window 1024, 4 sinks: 541 us, 901 TFLOP/s of visible scores, bound
-// by the softmax of a tile beside its products, the masked halves of the edge
-// tiles and what a CTA spends around a few key tiles.
+// d = 128, window 1024, 4 sinks: 547 us, 892 TFLOP/s of visible scores.  No pipe
+// is full (8 sequences of 2048, window 512: tensor 38%, issue slots 49% of the
+// cycles): a tile's softmax waits for its scores and its products for the weights,
+// and the masked halves of the edge tiles and what a CTA spends around a few key
+// tiles come on top.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -19,13 +21,20 @@ namespace fa {
 // spends before and after them (set-up, the first copies, the epilogue) a
 // quarter of its time.  Persistent CTAs, one an SM, take the items in turn, and
 // the next item's copies and first products run beside the last softmax and the
-// epilogue.  They take fixed shares, so the items have to be alike: sequences of
-// some windows' length.  (One-tile CTAs, two an SM, overlap already: persistent
-// ones took 5 to 17% longer.)  In us, one CTA an item / persistent (32 / 8 heads,
-// N = 16384, B = 1; the last two 16 / 4 heads, B = 8):
+// epilogue.  They take fixed shares, and long items level out badly.  (One-tile
+// CTAs, two an SM, overlap already: persistent ones took 5 to 17% longer.)  The
+// rule asks for the caller's bound on the lengths to be some windows; one limit
+// serves both head sizes, though at d = 64 it leaves 5% of window 2048.  In us,
+// one CTA an item / persistent (32 / 8 heads, N = 16384, B = 1; the last two 16 / 4
+// heads, B = 8):
 //   d    window 512   1024        2048        4096        N 2048, 512  N 2048, 1024
 //   128  187 / 165    261 / 246   400 / 400   658 / 687   98 / 93      119 / 121
 //   64   160 / 138    222 / 202   341 / 325   558 / 556   83 / 78      101 / 101
+// Items that are not alike and bounds that are loose gain as well (16 / 4 heads,
+// d = 128, windows 128, 512, 1024): 32 sequences of 64 to 4096 226 / 193, 312 /
+// 287, 404 / 406; 64 of 256 to 512 with a bound of 16384 111 / 97, 119 / 105, 119 /
+// 105; one of 16384 and 200 of 1 to 256, whose grid of one CTA an item is mostly
+// empty, 1365 / 614, 1393 / 644, 1432 / 689.
 constexpr int kPersistentKeys = 1536;
 
 template <int D>

@@ -286,7 +286,8 @@ size_t fa_decode_workspace_size(int batch, int H, int Hkv, int d, int max_ctx_le
  *                 owned by the caller; zero-filled before its first call
  *                 (the control block, see the conventions above); past the
  *                 control block its contents on entry are ignored.
- * A sequence with ctx_len 0 gets out = 0 and lse = -inf.  Slots of the last
+ * A sequence with ctx_len 0 gets out = 0 and lse = -inf, a query with a NaN
+ * NaN in both.  Slots of the last
  * block past ctx_len are never read into the result.  Supported: block_size
  * == 16, H / Hkv <= 16.  Two kernels run in stream order: the split kernel
  * and the (m, l, o) combine.
