@@ -29,7 +29,8 @@
 //     context has enough of to matter.
 // vs goes into the weights: o is kept relative to mo, a running reference of
 // x_j + log2 vs, so the weights 2^(x_j + log2 vs - mo) stay in fp16's range
-// whatever the scales; the references move only when a maximum grows by more
+// whatever the scales (the largest at 2^12 to 2^14: 11 bits down to 2^-26 of it,
+// multiples of 2^-36 below); the references move only when a maximum grows by more
 // than kSlackLog2, which leaves the accumulators alone in most steps.
 // Bound by HBM: half of decode.cu's bytes for the same products.
 #include <cuda.h>

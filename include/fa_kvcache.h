@@ -58,8 +58,9 @@ int fa_cache_append_fp8(const void *k, const void *v, int64_t k_stride, int64_t 
 /*
  * fa_decode_paged over the 8-bit cache: one query token per sequence.  The
  * scores are formed from the codes and from Q in two 8-bit terms, exact to
- * 2^-21 of a query row's largest value; weights are rounded to 11 bits; sums
- * are fp32.
+ * 2^-21 of a query row's largest value; weights (times their blocks' v_scale) are
+ * rounded to 11 bits, below 2^-26 of a head's largest to multiples of 2^-36 of it;
+ * sums are fp32.
  *   q, out    : [batch, H, d] bf16;  lse : [batch, H] fp32, may be NULL
  *   workspace : fa_decode_workspace_size(), or with a window
  *               fa_decode_window_workspace_size() bytes (fa_window.h);
