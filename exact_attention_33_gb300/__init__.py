@@ -1,8 +1,8 @@
 """Exact attention for GB300 (sm_103a): thin Python binding of libfa.so.
 
 Every function here only marshals torch tensors into the C ABI declared in
-``include/fa.h``, ``fa_window.h`` and ``fa_kvcache.h`` (device pointers, sizes, the current CUDA stream) and checks
-the returned status; all arithmetic runs in the library's CUDA kernels.  There
+``include/fa.h``, ``fa_window.h``, ``fa_kvcache.h`` and ``fa_rope.h`` (device pointers, sizes,
+the current CUDA stream) and checks the returned status; all arithmetic runs in the library's CUDA kernels.  There
 is no fallback: if ``libfa.so`` is missing or a call fails, an exception is
 raised.
 
@@ -30,6 +30,8 @@ __all__ = [
     "fa_decode_window_workspace_size", "fa_bwd_window", "fa_bwd_varlen_window",
     "fa_bwd_window_workspace_size", "fa_cache_append_fp8", "fa_decode_paged_fp8",
     "fa_fwd_paged_fp8",
+    "fa_rope_frequencies", "fa_rope", "fa_rope_bwd", "fa_cache_append_rope",
+    "fa_cache_append_rope_fp8",
     "fa_status_string", "fa_device_status", "fa_last_device_status", "new_workspace",
     "FA_WORKSPACE_HEADER_BYTES",
     "fa_version", "FA_DEV_TIMEOUT", "FA_DEV_BAD_BLOCK", "FA_DEV_BAD_CTX", "FA_DEV_BAD_SEQLEN",
@@ -139,6 +141,18 @@ def load_library() -> ctypes.CDLL:
         lib.fa_fwd_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, i,
                                          i, f, i, i, vp, vp, vp]
         lib.fa_fwd_paged_fp8.restype = i
+        lib.fa_rope.argtypes = [vp, vp, i64, i64, vp, vp, i64, i64, vp, i, f, i, vp, i, i, i, i, i,
+                                vp]
+        lib.fa_rope.restype = i
+        lib.fa_rope_bwd.argtypes = lib.fa_rope.argtypes
+        lib.fa_rope_bwd.restype = i
+        lib.fa_cache_append_rope.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, vp, i, f, i, vp, vp,
+                                             vp, i, vp, vp, i, i, i, i, i, i, i, i, vp]
+        lib.fa_cache_append_rope.restype = i
+        lib.fa_cache_append_rope_fp8.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, vp, i, f, i, vp,
+                                                 vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, i,
+                                                 vp]
+        lib.fa_cache_append_rope_fp8.restype = i
         lib.fa_status_string.argtypes = [i]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i]
@@ -1174,3 +1188,240 @@ def fa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, ctx_lens,
     if rc != FA_OK:
         raise FaError("fa_fwd_paged_fp8", rc)
     return out, lse
+
+
+# ---------------------------------------------------------- rotary positions
+#
+# include/fa_rope.h
+
+def fa_rope_frequencies(rot_dim, base=10000.0, stretch=1.0, method="parts", trained_len=8192,
+                        slow_turns=1.0, fast_turns=32.0, device=None):
+    """Frequencies and factor of a rotation: (inv_freq fp64 [rot_dim/2] on the
+    device, factor), for the calls below.
+
+    Pair i turns base^(-2i/rot_dim) radians a position.  ``stretch`` > 1 makes a
+    model that was trained on contexts of ``trained_len`` serve contexts
+    ``stretch`` times as long:
+
+    * ``"linear"``: every pair is slowed by ``stretch``;
+    * ``"base"``: the base grows by stretch^(rot_dim/(rot_dim-2)), which slows the
+      slowest pair by ``stretch`` and leaves the fastest as it is;
+    * ``"parts"``: pairs that turn fewer than ``slow_turns`` times over the trained
+      length are slowed by ``stretch``, those that turn more than ``fast_turns``
+      times are left, in between linearly; the factor is 0.1 ln(stretch) + 1.
+    """
+    torch = _torch()
+    rot_dim, base, stretch = int(rot_dim), float(base), float(stretch)
+    if rot_dim < 16 or rot_dim % 16:
+        raise ValueError("rot_dim must be a positive multiple of 16")
+    if not (base > 1.0 and math.isfinite(base) and stretch >= 1.0 and math.isfinite(stretch)):
+        raise ValueError("base must be above 1 and stretch at least 1")
+    if method not in ("linear", "base", "parts"):
+        raise ValueError("method must be 'linear', 'base' or 'parts'")
+    factor = 1.0
+    if method == "base":
+        base *= stretch ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2.0 * j / rot_dim) for j in range(rot_dim // 2)]
+    if method == "linear":
+        freq = [f / stretch for f in freq]
+    elif method == "parts" and stretch > 1.0:
+        if not 0 <= slow_turns < fast_turns or trained_len < 1:
+            raise ValueError("0 <= slow_turns < fast_turns and a positive trained_len are wanted")
+        keep = [min(1.0, max(0.0, (trained_len * f / (2 * math.pi) - slow_turns)
+                             / (fast_turns - slow_turns))) for f in freq]
+        freq = [f * w + f / stretch * (1.0 - w) for f, w in zip(freq, keep)]
+        factor = 0.1 * math.log(stretch) + 1.0
+    return torch.tensor(freq, dtype=torch.float64,
+                        device=device if device is not None else "cuda"), factor
+
+
+def _check_rope_rows(name, t, lead, heads, d, dev):
+    """bf16 rows [*lead, heads, d] on ``dev`` whose tokens may lie apart (None for
+    heads: any); returns the token stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    n = t.dim() - 2
+    if n != len(lead) or tuple(t.shape[:n]) != tuple(lead) or t.shape[-1] != d \
+            or (heads is not None and t.shape[-2] != heads) or not t.shape[-2]:
+        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, heads, {d}]")
+    row = t.shape[-2] * d
+    if not t.numel():
+        return row
+    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != d):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    tokens = t.shape[n - 1] * (t.shape[0] if n == 2 else 1)
+    if tokens == 1:
+        return row
+    stride = t.stride(n - 1) if t.shape[n - 1] > 1 else t.stride(0)
+    if n == 2 and t.shape[0] > 1 and t.stride(0) != stride * t.shape[1]:
+        raise ValueError(f"{name}: all tokens must lie equally far apart")
+    if stride < row or stride % 8:
+        raise ValueError(f"{name}: tokens must lie a multiple of 8 elements apart, not overlapping")
+    return stride
+
+
+def _check_freq(inv_freq, d, dev):
+    """The frequencies of a rotation; returns rot_dim."""
+    torch = _torch()
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.device != dev \
+            or inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 \
+            or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous 1-D float64 tensor on {dev}")
+    rot = 2 * inv_freq.numel()
+    if not 0 < rot <= d:
+        raise ValueError("inv_freq must hold 1 to d / 2 values")
+    return rot
+
+
+def _rope(name, q, k, inv_freq, positions, factor, interleaved, q_out, k_out, stream):
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev = q.device
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [T, H, d] or [B, N, H, d]")
+    lead, (H, d) = q.shape[:-2], q.shape[-2:]
+    strides = [_check_rope_rows("q", q, lead, None, d, dev), 0]
+    Hkv = 0
+    if k is not None:
+        strides[1] = _check_rope_rows("k", k, lead, None, d, dev)
+        Hkv = k.shape[-2]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    rot = _check_freq(inv_freq, d, dev)
+    if positions is not None:
+        _check_tensor("positions", positions, lead, torch.int32, dev)
+    with _Launch(stream, dev) as handle:
+        outs = []
+        for what, x, out in (("q_out", q, q_out), ("k_out", k, k_out)):
+            if x is None:
+                outs.append((None, 0))
+            elif out is None:
+                outs.append((torch.empty(x.shape, dtype=x.dtype, device=dev), x.shape[-2] * d))
+            else:
+                outs.append((out, _check_rope_rows(what, out, lead, x.shape[-2], d, dev)))
+        (q_out, qs), (k_out, ks) = outs
+        if not q.numel():
+            return q_out, k_out
+        rc = getattr(load_library(), name)(
+            _addr(q), _addr(k), *strides, _addr(q_out), _addr(k_out), qs, ks, _addr(inv_freq), rot,
+            float(factor), 1 if interleaved else 0, _addr(positions), lead[-1], math.prod(lead), H,
+            Hkv, d, handle)
+    if rc != FA_OK:
+        raise FaError(name, rc)
+    return q_out, k_out
+
+
+def fa_rope(q, k, inv_freq, positions=None, factor=1.0, interleaved=False, q_out=None, k_out=None,
+            stream=None):
+    """Queries and keys rotated by their positions.
+
+    q [T,H,d] or [B,N,H,d], k the same with Hkv heads (or None) bf16; tokens may
+    lie apart (views of a fused projection).  inv_freq fp64 [rot_dim/2]
+    (:func:`fa_rope_frequencies`); positions int32 [T] or [B,N], None for a
+    token's index in its sequence ([B,N,..]) or in the batch ([T,..]).  Pairs
+    are (x[i], x[i + rot_dim/2]), or neighbours with ``interleaved``.  q_out and
+    k_out may be q and k themselves.  Returns (q_out, k_out).
+    """
+    return _rope("fa_rope", q, k, inv_freq, positions, factor, interleaved, q_out, k_out, stream)
+
+
+def fa_rope_bwd(dq, dk, inv_freq, positions=None, factor=1.0, interleaved=False, dq_out=None,
+                dk_out=None, stream=None):
+    """Gradient of :func:`fa_rope`: from dq, dk of its outputs (as fa_bwd gives
+    them) those of its inputs.  Arguments as there; dq_out and dk_out may be dq
+    and dk themselves.  Returns (dq_out, dk_out)."""
+    return _rope("fa_rope_bwd", dq, dk, inv_freq, positions, factor, interleaved, dq_out, dk_out,
+                 stream)
+
+
+def _append_rope(q, k, v, inv_freq, q_out, block_table, ctx_lens, cu_seqlens, pool_shape, dev):
+    """Checks what the two writes share; returns the token strides of k, v, q and
+    q_out, q's heads, the tokens, rot_dim and the batch."""
+    _, _, Hkv, d = pool_shape
+    T = k.shape[0] if isinstance(k, _torch().Tensor) and k.dim() == 3 else -1
+    ks = _check_rope_rows("k", k, (T,), Hkv, d, dev)
+    vs = _check_rope_rows("v", v, (T,), Hkv, d, dev)
+    H = qs = qos = 0
+    if q is not None:
+        qs = _check_rope_rows("q", q, (T,), None, d, dev)
+        H = q.shape[1]
+        if q_out is not None:
+            qos = _check_rope_rows("q_out", q_out, (T,), H, d, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = 0 if inv_freq is None else _check_freq(inv_freq, d, dev)
+    batch = _check_sequences(block_table, ctx_lens, cu_seqlens, "cu_seqlens", dev)
+    return ks, vs, qs, qos, H, T, rot, batch
+
+
+def fa_cache_append_rope(q, k, v, inv_freq, k_pool, v_pool, block_table, ctx_lens, cu_seqlens,
+                         max_new, factor=1.0, interleaved=False, q_out=None, stream=None):
+    """Write new keys, rotated by their positions, and values into the bf16
+    cache of :func:`fa_fwd_paged` and :func:`fa_decode_paged`, and rotate the
+    queries that come with them.
+
+    q [T,H,d] (or None), k, v [T,Hkv,d] bf16 (tokens may lie apart: views of a
+    fused projection); inv_freq fp64 [rot_dim/2], or None to write the rows as
+    they are; pools [num_blocks,16,Hkv,d] bf16, written in place; block_table
+    int32 [batch,max_blocks]; ctx_lens int32 [batch], the new tokens counted;
+    cu_seqlens int32 [batch+1]: sequence b's new tokens; max_new bounds their
+    number per sequence.  Returns the rotated queries (q_out, which may be q;
+    new rows behind the last sequence hold nothing of use), None without q.
+    """
+    torch = _torch()
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor")
+    dev = k.device
+    shape = _check_pools(k_pool, v_pool, dev)
+    ks, vs, qs, qos, H, T, rot, batch = _append_rope(
+        q, k, v, inv_freq, q_out, block_table, ctx_lens, cu_seqlens, shape, dev)
+    num_blocks, block_size, Hkv, d = shape
+    with _Launch(stream, dev) as handle:
+        if q is not None and q_out is None:
+            q_out, qos = torch.empty(q.shape, dtype=q.dtype, device=dev), H * d
+        if not T:
+            return q_out
+        rc = load_library().fa_cache_append_rope(
+            _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), qos, _addr(inv_freq), rot,
+            float(factor), 1 if interleaved else 0, _addr(k_pool), _addr(v_pool),
+            _addr(block_table), block_table.shape[1], _addr(ctx_lens), _addr(cu_seqlens), batch, T,
+            int(max_new), H, Hkv, d, block_size, num_blocks, handle)
+    if rc != FA_OK:
+        raise FaError("fa_cache_append_rope", rc)
+    return q_out
+
+
+def fa_cache_append_rope_fp8(q, k, v, inv_freq, k_pool, v_pool, k_scale, v_scale, block_table,
+                             ctx_lens, cu_seqlens, max_new, factor=1.0, interleaved=False,
+                             q_out=None, stream=None):
+    """:func:`fa_cache_append_rope` into the 8-bit cache of
+    :func:`fa_cache_append_fp8` (pools uint8/e4m3, scales [num_blocks,Hkv] fp32);
+    inv_freq is wanted.  A block's scale comes from its keys before the
+    rotation.  Returns the rotated queries, None without q."""
+    torch = _torch()
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor")
+    if inv_freq is None:
+        raise ValueError("inv_freq is wanted (fa_cache_append_fp8 writes rows as they are)")
+    dev = k.device
+    shape = _check_cache(k_pool, v_pool, k_scale, v_scale, dev)
+    ks, vs, qs, qos, H, T, rot, batch = _append_rope(
+        q, k, v, inv_freq, q_out, block_table, ctx_lens, cu_seqlens, shape, dev)
+    num_blocks, block_size, Hkv, d = shape
+    with _Launch(stream, dev) as handle:
+        if q is not None and q_out is None:
+            q_out, qos = torch.empty(q.shape, dtype=q.dtype, device=dev), H * d
+        if not T:
+            return q_out
+        rc = load_library().fa_cache_append_rope_fp8(
+            _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(q_out), qos, _addr(inv_freq), rot,
+            float(factor), 1 if interleaved else 0, _addr(k_pool), _addr(v_pool), _addr(k_scale),
+            _addr(v_scale), _addr(block_table), block_table.shape[1], _addr(ctx_lens),
+            _addr(cu_seqlens), batch, T, int(max_new), H, Hkv, d, block_size, num_blocks, handle)
+    if rc != FA_OK:
+        raise FaError("fa_cache_append_rope_fp8", rc)
+    return q_out
