@@ -1,8 +1,8 @@
 """Exact attention for GB300 (sm_103a): thin Python binding of libfa.so.
 
 Every function here only marshals torch tensors into the C ABI declared in
-``include/fa.h``, ``fa_window.h``, ``fa_kvcache.h`` and ``fa_rope.h`` (device pointers, sizes,
-the current CUDA stream) and checks the returned status; all arithmetic runs in the library's CUDA kernels.  There
+``include/fa.h``, ``fa_window.h``, ``fa_kvcache.h``, ``fa_rope.h`` and ``fa_prefix.h`` (device
+pointers, sizes, the current CUDA stream) and checks the returned status; all arithmetic runs in the library's CUDA kernels.  There
 is no fallback: if ``libfa.so`` is missing or a call fails, an exception is
 raised.
 
@@ -31,7 +31,7 @@ __all__ = [
     "fa_bwd_window_workspace_size", "fa_cache_append_fp8", "fa_decode_paged_fp8",
     "fa_fwd_paged_fp8",
     "fa_rope_frequencies", "fa_rope", "fa_rope_bwd", "fa_cache_append_rope",
-    "fa_cache_append_rope_fp8",
+    "fa_cache_append_rope_fp8", "fa_decode_paged_prefix", "fa_decode_prefix_workspace_size",
     "fa_status_string", "fa_device_status", "fa_last_device_status", "new_workspace",
     "FA_WORKSPACE_HEADER_BYTES",
     "fa_version", "FA_DEV_TIMEOUT", "FA_DEV_BAD_BLOCK", "FA_DEV_BAD_CTX", "FA_DEV_BAD_SEQLEN",
@@ -153,6 +153,11 @@ def load_library() -> ctypes.CDLL:
                                                  vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, i, i,
                                                  vp]
         lib.fa_cache_append_rope_fp8.restype = i
+        lib.fa_decode_prefix_workspace_size.argtypes = [i, i, i, i, i, i, i]
+        lib.fa_decode_prefix_workspace_size.restype = sz
+        lib.fa_decode_paged_prefix.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i, i,
+                                               i, f, vp, vp, vp, sz, vp]
+        lib.fa_decode_paged_prefix.restype = i
         lib.fa_status_string.argtypes = [i]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), i]
@@ -1425,3 +1430,55 @@ def fa_cache_append_rope_fp8(q, k, v, inv_freq, k_pool, v_pool, k_scale, v_scale
     if rc != FA_OK:
         raise FaError("fa_cache_append_rope_fp8", rc)
     return q_out
+
+
+# ------------------------------------------------------------ shared prefixes
+#
+# include/fa_prefix.h
+
+def fa_decode_prefix_workspace_size(batch, H, Hkv, d, max_prefix_len, max_own_len,
+                                    block_size=16) -> int:
+    """Bytes of workspace of :func:`fa_decode_paged_prefix`."""
+    return int(load_library().fa_decode_prefix_workspace_size(batch, H, Hkv, d, max_prefix_len,
+                                                              max_own_len, block_size))
+
+
+def fa_decode_paged_prefix(q, k_pool, v_pool, block_table, ctx_lens, cu_groups, prefix_lens,
+                           max_prefix_len, max_own_len, scale=None, out=None, lse=None,
+                           workspace=None, want_lse=True, stream=None):
+    """:func:`fa_decode_paged` for a batch in which groups of neighbouring
+    sequences share the cache blocks of their first keys: those are read and
+    multiplied once for a group.
+
+    q [batch,H,d] bf16; pools [num_blocks,16,Hkv,d] bf16; block_table int32
+    [batch,max_blocks] with all blocks of each sequence, shared ones first;
+    ctx_lens int32 [batch] all keys of each; cu_groups int32 [groups+1]: group g
+    is sequences cu_groups[g] to cu_groups[g+1]; prefix_lens int32 [groups]: the
+    keys that its sequences have in common (whole blocks of them are shared).
+    max_prefix_len bounds prefix_lens, max_own_len the keys of a sequence behind
+    its prefix.  Returns (out [batch,H,d] bf16, lse [batch,H] fp32 or None).
+    """
+    _check_bf16_cuda("q", q, 3)
+    dev = q.device
+    num_blocks, block_size, Hkv, dp = _check_pools(k_pool, v_pool, dev)
+    batch, H, d = q.shape
+    if dp != d:
+        raise ValueError("the pools' head size must match q")
+    _check_table(block_table, ctx_lens, batch, dev)
+    _check_int32("prefix_lens", prefix_lens, dev)
+    _check_int32("cu_groups", cu_groups, dev, numel=prefix_lens.numel() + 1)
+    with _Launch(stream, dev) as handle:
+        need = 0 if workspace is not None else fa_decode_prefix_workspace_size(
+            batch, H, Hkv, d, int(max_prefix_len), int(max_own_len), block_size)
+        workspace = _workspace(workspace, need, dev, 256, zero=True)
+        out, lse = _results(q, (batch, H), out, lse, want_lse)
+        if not batch:
+            return out, lse
+        rc = load_library().fa_decode_paged_prefix(
+            _addr(q), _addr(k_pool), _addr(v_pool), _addr(block_table), block_table.shape[1],
+            _addr(ctx_lens), _addr(cu_groups), _addr(prefix_lens), prefix_lens.numel(),
+            int(max_prefix_len), int(max_own_len), batch, H, Hkv, d, block_size, num_blocks,
+            _scale(scale, d), _addr(out), _addr(lse), _addr(workspace), workspace.numel(), handle)
+    if rc != FA_OK:
+        raise FaError("fa_decode_paged_prefix", rc)
+    return out, lse

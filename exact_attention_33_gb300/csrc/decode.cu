@@ -41,6 +41,8 @@
 
 #include "decode_common.cuh"
 #include "fa_internal.h"
+#include "launch.h"
+#include "prefix_internal.h"
 #include "ptx.cuh"
 #include "checks.cuh"
 
@@ -290,11 +292,64 @@ __device__ __forceinline__ int decode_range(const CUtensorMap &tm_k, const CUten
   return kRangeFailed;
 }
 
+// Writes the partial states of the group's query heads, rows part_row, ... of
+// [batch * H, max_splits], for split `split`.
+template <int D, int NT>
+__device__ __forceinline__ void store_range(const DecodeParams &p, size_t part_row, int split,
+                                            const WarpRange<D, NT> &st) {
+  constexpr int KC = D / 16;
+  const int lane = threadIdx.x & 31;
+  const int G = p.group;
+  const size_t part_rows = static_cast<size_t>(p.batch) * p.H * p.max_splits;
+  const int quad = lane & 3;
+  const int grp = lane >> 2;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc) {
+      float lt = st.lcol[nt][cc];
+      lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+      lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+      lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+      const int g = nt * 8 + 2 * quad + cc;
+      if (g < G) {
+        const size_t row = (part_row + g) * p.max_splits + split;
+        if (!in_bounds(row, 1, part_rows, p.status)) continue;
+        if (grp == 0) {
+          p.ml_part[row * 2 + 0] = split_max(st.mcol[nt][cc], lt);
+          p.ml_part[row * 2 + 1] = lt;
+        }
+        float *orow = p.o_part + row * D;
+#pragma unroll
+        for (int mt = 0; mt < KC; ++mt) {
+          orow[mt * 16 + grp] = st.acc[nt][mt][cc];
+          orow[mt * 16 + 8 + grp] = st.acc[nt][mt][2 + cc];
+        }
+      }
+    }
+  }
+}
+
+// Leaves a neutral partial state, so that the combine ignores the split.
+template <int D>
+__device__ __forceinline__ void store_neutral(const DecodeParams &p, size_t part_row, int split) {
+  const int lane = threadIdx.x & 31;
+  const size_t part_rows = static_cast<size_t>(p.batch) * p.H * p.max_splits;
+  for (int g = 0; g < p.group; ++g) {
+    const size_t row = (part_row + g) * p.max_splits + split;
+    if (!in_bounds(row, 1, part_rows, p.status)) continue;
+    for (int c = lane; c < D; c += 32) p.o_part[row * D + c] = 0.f;
+    if (lane == 0) {
+      p.ml_part[row * 2 + 0] = -CUDART_INF_F;
+      p.ml_part[row * 2 + 1] = 0.f;
+    }
+  }
+}
+
 template <int D, int NT, bool WIN>
 __global__ void __launch_bounds__(32)
     decode_split_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
-  constexpr int KC = D / 16;
   const int split = blockIdx.x;
   const int kvh = blockIdx.y;
   const int b = blockIdx.z;
@@ -326,10 +381,7 @@ __global__ void __launch_bounds__(32)
   const int t1 = min(keys, t0 + p.split_tokens);
   // (which blocks a window reads depends on the context length)
   if (WIN && lane < (t1 - t0) / kDecodeBlock) read_block_id(wb.logical(lb0 + lane));
-  const int G = p.group;
-  // partial-state rows of the call: [batch, H, max_splits]
-  const size_t part_rows = static_cast<size_t>(p.batch) * p.H * p.max_splits;
-  const size_t part_row = static_cast<size_t>(b) * p.H + static_cast<size_t>(kvh) * G;
+  const size_t part_row = static_cast<size_t>(b) * p.H + static_cast<size_t>(kvh) * p.group;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -337,48 +389,42 @@ __global__ void __launch_bounds__(32)
   WarpRange<D, NT> st;
   const int rc =
       decode_range<D, NT, WIN>(tm_k, tm_v, p, b, kvh, t0, t1, my_blk, smem, st, wb, ctx);
-  if (rc == kRangeBadBlock) {
-    // Leave a neutral partial state so that the combine ignores this split.
-    for (int g = 0; g < G; ++g) {
-      const size_t row = (part_row + g) * p.max_splits + split;
-      if (!in_bounds(row, 1, part_rows, p.status)) continue;
-      for (int c = lane; c < D; c += 32) p.o_part[row * D + c] = 0.f;
-      if (lane == 0) {
-        p.ml_part[row * 2 + 0] = -CUDART_INF_F;
-        p.ml_part[row * 2 + 1] = 0.f;
-      }
-    }
-    return;
+  if (rc == kRangeBadBlock) store_neutral<D>(p, part_row, split);
+  if (rc == kRangeOk) store_range<D, NT>(p, part_row, split, st);
+}
+
+// The keys that a sequence has for itself behind a shared prefix (prefix.cu):
+// as decode_split_kernel over keys [whole, ctx).
+template <int D, int NT>
+__global__ void __launch_bounds__(32)
+    decode_own_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const PrefixParams pp) {
+  const DecodeParams &p = pp.own;
+  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x;
+  pdl_launch_dependents();
+  PrefixGroup group{};
+  long long start;
+  const int whole = prefix_find(pp, b, true, group, start) ? group.whole : 0;
+  const int ctx = prefix_ctx(pp, b, whole, split == 0 && kvh == 0 && lane == 0);
+  const int t0 = whole + split * p.split_tokens;
+  if (t0 >= ctx) return;
+  const int t1 = min(ctx, t0 + p.split_tokens);
+  int my_blk = -1;
+  if (lane < (t1 - t0 + kDecodeBlock - 1) / kDecodeBlock) {
+    const size_t tidx = static_cast<size_t>(b) * p.max_blocks_per_seq + t0 / kDecodeBlock + lane;
+    if (in_bounds(tidx, 1, static_cast<size_t>(p.batch) * p.max_blocks_per_seq, p.status))
+      my_blk = p.block_table[tidx];
   }
-  if (rc != kRangeOk) return;
-  // write the partial state of every query head of the group
-  const int quad = lane & 3;
-  const int grp = lane >> 2;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
-      float lt = st.lcol[nt][cc];
-      lt += __shfl_xor_sync(0xffffffffu, lt, 4);
-      lt += __shfl_xor_sync(0xffffffffu, lt, 8);
-      lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-      const int g = nt * 8 + 2 * quad + cc;
-      if (g < G) {
-        const size_t row = (part_row + g) * p.max_splits + split;
-        if (!in_bounds(row, 1, part_rows, p.status)) continue;
-        if (grp == 0) {
-          p.ml_part[row * 2 + 0] = split_max(st.mcol[nt][cc], lt);
-          p.ml_part[row * 2 + 1] = lt;
-        }
-        float *orow = p.o_part + row * D;
-#pragma unroll
-        for (int mt = 0; mt < KC; ++mt) {
-          orow[mt * 16 + grp] = st.acc[nt][mt][cc];
-          orow[mt * 16 + 8 + grp] = st.acc[nt][mt][2 + cc];
-        }
-      }
-    }
-  }
+  const size_t part_row = static_cast<size_t>(b) * p.H + static_cast<size_t>(kvh) * p.group;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  WarpRange<D, NT> st;
+  const int rc = decode_range<D, NT, false>(tm_k, tm_v, p, b, kvh, t0, t1, my_blk, smem, st,
+                                            WindowBlocks(ctx, 0, 0), ctx);
+  if (rc == kRangeBadBlock) store_neutral<D>(p, part_row, split);
+  if (rc == kRangeOk) store_range<D, NT>(p, part_row, split, st);
 }
 
 // Warps per merged row: one for rows of at most kCombineFewSplits splits
@@ -601,6 +647,30 @@ cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const De
                           : launch_decode_w<64, 1>(tk, tv, p, stream);
   return two ? launch_decode_w<128, 2>(tk, tv, p, stream)
              : launch_decode_w<128, 1>(tk, tv, p, stream);
+}
+
+namespace {
+
+template <int D, int NT>
+cudaError_t launch_own_t(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixParams &p,
+                         cudaStream_t stream) {
+  using L = DecodeLayout<D>;
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e = allow_smem(decode_own_kernel<D, NT>, L::kSmemAlloc, smem_set);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.own.max_splits, p.own.Hkv, p.own.batch);
+  decode_own_kernel<D, NT><<<grid, 32, L::kSmemAlloc, stream>>>(tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode_own(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixParams &p,
+                              int d, cudaStream_t stream) {
+  const bool two = p.own.group > 8;
+  if (d == 64) return two ? launch_own_t<64, 2>(tk, tv, p, stream)
+                          : launch_own_t<64, 1>(tk, tv, p, stream);
+  return two ? launch_own_t<128, 2>(tk, tv, p, stream) : launch_own_t<128, 1>(tk, tv, p, stream);
 }
 
 }  // namespace fa

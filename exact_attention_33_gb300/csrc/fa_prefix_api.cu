@@ -1,0 +1,167 @@
+// fa_prefix_api.cu - the C ABI of decoding over shared prefixes
+// (include/fa_prefix.h): argument validation, tensor maps and dispatch, as
+// fa_api.cu for fa.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/fa_prefix.h"
+#include "fa_host.h"
+#include "prefix_internal.h"
+
+namespace fa {
+
+cudaError_t launch_prefix(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                          const PrefixParams &p, int d, cudaStream_t stream);
+
+namespace {
+
+struct PrefixWs {
+  int max_slots;
+  size_t o_bytes, ml_bytes;
+};
+
+int prefix_ctas() {
+  const int sms = sm_count();
+  return sms > 0 ? sms : 148;
+}
+
+// positions stay in int
+bool lengths_ok(int max_prefix, int max_own) {
+  return static_cast<long long>(max_prefix) + max_own <= kMaxCtxLen - kDecodeBlock;
+}
+
+// Partial states over shared keys.  A run of a CTA is at least one key tile,
+// and a CTA's share of the tiles at least the CTAs' part of one group's on all
+// KV heads, so a row meets at most CTAs / Hkv shares of it and two cut ones.
+PrefixWs prefix_ws(int batch, int H, int Hkv, int d, int max_prefix) {
+  PrefixWs w;
+  const int tiles = (max_prefix / kDecodeBlock * kDecodeBlock + kPrefixTileKeys - 1) / kPrefixTileKeys;
+  w.max_slots = std::max(1, std::min(tiles, prefix_ctas() / Hkv + 2));
+  const size_t rows = static_cast<size_t>(batch) * H * w.max_slots;
+  w.o_bytes = round_up(rows * d * sizeof(float), 256);
+  w.ml_bytes = round_up(rows * 4 * sizeof(float), 256);
+  return w;
+}
+
+// The tensor map of Q [batch, H, d] for boxes of `seqs` sequences x the heads
+// of one KV group x 64 values.
+int make_q_map(CUtensorMap *map, const void *q, int batch, int H, int group, int d, int seqs) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return FA_ERR_CUDA;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(H) * d * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(seqs)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_decode_prefix_workspace_size(int batch, int H, int Hkv, int d, int max_prefix_len,
+                                       int max_own_len, int block_size) {
+  if (batch < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || max_prefix_len < 0 || max_own_len < 0)
+    return 0;
+  if ((d != 64 && d != 128) || block_size != kDecodeBlock) return 0;
+  if (!lengths_ok(max_prefix_len, max_own_len)) return 0;
+  const PrefixWs w = prefix_ws(batch, H, Hkv, d, max_prefix_len);
+  return FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes +
+         decode_ws_bound(batch, H, Hkv, d, max_own_len + kDecodeBlock - 1);
+}
+
+int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool,
+                           const int32_t *block_table, int max_blocks_per_seq,
+                           const int32_t *ctx_lens, const int32_t *cu_groups,
+                           const int32_t *prefix_lens, int num_groups, int max_prefix_len,
+                           int max_own_len, int batch, int H, int Hkv, int d, int block_size,
+                           int num_blocks, float scale, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, fa_stream_t stream) {
+  if (!q || !k_pool || !v_pool || !block_table || !ctx_lens || !out) return FA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(ctx_lens, 4) || (lse && !aligned(lse, 4)))
+    return FA_ERR_INVALID_ARG;
+  if (num_groups < 0 || (num_groups > 0 && (!cu_groups || !prefix_lens || !aligned(cu_groups, 4) ||
+                                            !aligned(prefix_lens, 4))))
+    return FA_ERR_INVALID_ARG;
+  if (batch < 0 || H < 1 || Hkv < 1 || H % Hkv != 0 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+      max_prefix_len < 0 || max_own_len < 0)
+    return FA_ERR_INVALID_ARG;
+  if (!scale_ok(scale)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (block_size != kDecodeBlock) return FA_ERR_UNSUPPORTED;
+  if (H / Hkv > 16) return FA_ERR_UNSUPPORTED;
+  const long long reach = static_cast<long long>(max_blocks_per_seq) * block_size;
+  if (reach < std::max(max_prefix_len, max_own_len)) return FA_ERR_INVALID_ARG;
+  if (!lengths_ok(max_prefix_len, max_own_len)) return FA_ERR_UNSUPPORTED;
+  if (batch > 65535 || Hkv > 65535 || static_cast<long long>(batch) * H > 0x7fffffffLL)
+    return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_blocks) * block_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  if (batch == 0) return FA_OK;
+  const int group = H / Hkv, seqs = kPrefillBM / group;
+  // key tiles of all groups: they are counted in int
+  const long long tiles = (max_prefix_len + kPrefixTileKeys - 1LL) / kPrefixTileKeys;
+  if (tiles * Hkv * (batch / (2 * seqs) + std::min(num_groups, batch)) > 0x7fffffffLL)
+    return FA_ERR_UNSUPPORTED;
+  const int max_own = max_own_len + kDecodeBlock - 1;
+  const DecodeWs w = decode_ws(batch, H, Hkv, d, max_own);
+  const PrefixWs s = prefix_ws(batch, H, Hkv, d, max_prefix_len);
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes + s.o_bytes + s.ml_bytes)
+    return FA_ERR_WORKSPACE;
+  CallStatus *call = static_cast<CallStatus *>(workspace);
+  uint8_t *parts = static_cast<uint8_t *>(workspace) + FA_WORKSPACE_HEADER_BYTES;
+
+  CUtensorMap tq, tk, tv;
+  const long long tokens = static_cast<long long>(num_blocks) * block_size;
+  int rc = make_q_map(&tq, q, batch, H, group, d, seqs);
+  if (rc == FA_OK) rc = make_pool_map(&tk, k_pool, d, Hkv, tokens);
+  if (rc == FA_OK) rc = make_pool_map(&tv, v_pool, d, Hkv, tokens);
+  if (rc != FA_OK) return rc;
+
+  PrefixParams p{};
+  p.own.dev_status = status_ptr();
+  if (p.own.dev_status == nullptr) return FA_ERR_CUDA;
+  p.own.status = &call->acc;
+  p.own.call = call;
+  p.own.q = q;
+  p.own.block_table = block_table;
+  p.own.ctx_lens = ctx_lens;
+  p.own.o_part = reinterpret_cast<float *>(parts);
+  p.own.ml_part = reinterpret_cast<float *>(parts + w.o_bytes);
+  p.own.out = out;
+  p.own.lse = lse;
+  p.own.batch = batch;
+  p.own.H = H;
+  p.own.Hkv = Hkv;
+  p.own.group = group;
+  p.own.max_blocks_per_seq = max_blocks_per_seq;
+  p.own.max_ctx_len = static_cast<int>(std::min<long long>(reach, 0x7fffffff));
+  p.own.num_blocks = num_blocks;
+  p.own.split_tokens = w.split_tokens;
+  p.own.max_splits = w.max_splits;
+  p.own.scale_log2 = scale * kLog2e;
+  p.cu_groups = cu_groups;
+  p.prefix_lens = prefix_lens;
+  p.num_groups = num_groups;
+  p.max_prefix = max_prefix_len;
+  p.max_own = max_own;
+  p.seqs_per_tile = seqs;
+  p.ctas = prefix_ctas();
+  p.max_slots = s.max_slots;
+  p.po_part = reinterpret_cast<float *>(parts + w.o_bytes + w.ml_bytes);
+  p.pml_part = reinterpret_cast<float4 *>(parts + w.o_bytes + w.ml_bytes + s.o_bytes);
+  return launch_prefix(tq, tk, tv, p, d, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+}  // extern "C"
