@@ -718,7 +718,8 @@ _calls = None   # the extension module, or False where it has not been built
 # the library's functions that the extension calls, in its order
 _BOUND = ("fa_fwd_window", "fa_fwd_varlen_window", "fa_fwd_paged_window", "fa_decode_paged_window",
           "fa_bwd_window", "fa_bwd_varlen_window", "fa_cache_append_fp8", "fa_decode_paged_fp8",
-          "fa_fwd_paged_fp8")
+          "fa_fwd_paged_fp8", "fa_rope", "fa_rope_bwd", "fa_cache_append_rope",
+          "fa_cache_append_rope_fp8", "fa_decode_paged_prefix")
 
 
 def _short():
@@ -1331,6 +1332,11 @@ def fa_rope(q, k, inv_freq, positions=None, factor=1.0, interleaved=False, q_out
     are (x[i], x[i + rot_dim/2]), or neighbours with ``interleaved``.  q_out and
     k_out may be q and k themselves.  Returns (q_out, k_out).
     """
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.rope(q, k, inv_freq, positions, factor, interleaved, q_out, k_out)
+        if done is not None:
+            return done
     return _rope("fa_rope", q, k, inv_freq, positions, factor, interleaved, q_out, k_out, stream)
 
 
@@ -1339,6 +1345,11 @@ def fa_rope_bwd(dq, dk, inv_freq, positions=None, factor=1.0, interleaved=False,
     """Gradient of :func:`fa_rope`: from dq, dk of its outputs (as fa_bwd gives
     them) those of its inputs.  Arguments as there; dq_out and dk_out may be dq
     and dk themselves.  Returns (dq_out, dk_out)."""
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.rope_bwd(dq, dk, inv_freq, positions, factor, interleaved, dq_out, dk_out)
+        if done is not None:
+            return done
     return _rope("fa_rope_bwd", dq, dk, inv_freq, positions, factor, interleaved, dq_out, dk_out,
                  stream)
 
@@ -1377,6 +1388,12 @@ def fa_cache_append_rope(q, k, v, inv_freq, k_pool, v_pool, block_table, ctx_len
     number per sequence.  Returns the rotated queries (q_out, which may be q;
     new rows behind the last sequence hold nothing of use), None without q.
     """
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.cache_append_rope(k_pool, v_pool, q, k, v, inv_freq, block_table, ctx_lens,
+                                       cu_seqlens, max_new, factor, interleaved, q_out)
+        if done is not None:
+            return None if done is True else done
     torch = _torch()
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise ValueError("k must be a CUDA tensor")
@@ -1407,6 +1424,13 @@ def fa_cache_append_rope_fp8(q, k, v, inv_freq, k_pool, v_pool, k_scale, v_scale
     :func:`fa_cache_append_fp8` (pools uint8/e4m3, scales [num_blocks,Hkv] fp32);
     inv_freq is wanted.  A block's scale comes from its keys before the
     rotation.  Returns the rotated queries, None without q."""
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.cache_append_rope_fp8(k_pool, v_pool, k_scale, v_scale, q, k, v, inv_freq,
+                                           block_table, ctx_lens, cu_seqlens, max_new, factor,
+                                           interleaved, q_out)
+        if done is not None:
+            return None if done is True else done
     torch = _torch()
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise ValueError("k must be a CUDA tensor")
@@ -1458,6 +1482,13 @@ def fa_decode_paged_prefix(q, k_pool, v_pool, block_table, ctx_lens, cu_groups, 
     max_prefix_len bounds prefix_lens, max_own_len the keys of a sequence behind
     its prefix.  Returns (out [batch,H,d] bf16, lse [batch,H] fp32 or None).
     """
+    short = _calls or _short()
+    if short and stream is None:
+        done = short.decode_paged_prefix(q, k_pool, v_pool, block_table, ctx_lens, cu_groups,
+                                         prefix_lens, max_prefix_len, max_own_len, scale, want_lse,
+                                         out, lse, workspace)
+        if done is not None:
+            return done
     _check_bf16_cuda("q", q, 3)
     dev = q.device
     num_blocks, block_size, Hkv, dp = _check_pools(k_pool, v_pool, dev)

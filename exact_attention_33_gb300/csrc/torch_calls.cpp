@@ -21,6 +21,8 @@
 #include <cmath>
 
 #include "fa_kvcache.h"
+#include "fa_prefix.h"
+#include "fa_rope.h"
 #include "fa_window.h"
 
 namespace {
@@ -40,6 +42,11 @@ struct {
   decltype(&fa_cache_append_fp8) cache_append_fp8;
   decltype(&fa_decode_paged_fp8) decode_paged_fp8;
   decltype(&fa_fwd_paged_fp8) fwd_paged_fp8;
+  decltype(&fa_rope) rope;
+  decltype(&fa_rope_bwd) rope_bwd;
+  decltype(&fa_cache_append_rope) cache_append_rope;
+  decltype(&fa_cache_append_rope_fp8) cache_append_rope_fp8;
+  decltype(&fa_decode_paged_prefix) decode_paged_prefix;
 } lib;
 
 // One call's arguments.  Every getter clears `ok` when its argument is not as
@@ -115,6 +122,11 @@ struct Args {
   float scale(int64_t d) {
     PyObject *o = next();
     if (o == Py_None) return static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
+    if (!PyFloat_CheckExact(o)) return ok = false, 0.f;
+    return static_cast<float>(PyFloat_AS_DOUBLE(o));
+  }
+  float number() {
+    PyObject *o = next();
     if (!PyFloat_CheckExact(o)) return ok = false, 0.f;
     return static_cast<float>(PyFloat_AS_DOUBLE(o));
   }
@@ -455,6 +467,201 @@ PyObject *fwd_paged_fp8(PyObject *, PyObject *const *v, Py_ssize_t given) {
   });
 }
 
+// Rows [lead.., heads, d] of bf16 whose tokens may lie apart (heads or d below
+// 0: any), on the call's device; `stride` is their distance.
+struct Rows {
+  const Tensor *t = nullptr;
+  int64_t stride = 0;
+  Rows() = default;
+  Rows(Args &a, at::IntArrayRef lead, int64_t heads, int64_t d) {
+    PyObject *o = a.next();
+    a.ok = a.ok && THPVariable_CheckExact(o);
+    if (!a.ok) return;
+    const Tensor &x = THPVariable_Unpack(o);
+    const int64_t n = x.dim() - 2;
+    a.ok = x.defined() && x.is_cuda() && x.scalar_type() == kBf16 && (n == 1 || n == 2) &&
+           x.numel() > 0 && small(&x) && (heads < 0 || x.size(n) == heads) &&
+           (d < 0 || x.size(n + 1) == d) && (lead.empty() || x.sizes().slice(0, n) == lead) &&
+           x.stride(n + 1) == 1 && (x.size(n) == 1 || x.stride(n) == x.size(n + 1));
+    if (!a.ok) return;
+    if (a.dev < 0) {
+      a.dev = x.get_device();
+      a.ok = a.dev == c10::cuda::current_device();
+    } else {
+      a.ok = x.get_device() == a.dev;
+    }
+    const int64_t row = x.size(n) * x.size(n + 1);
+    stride = x.size(n - 1) > 1 ? x.stride(n - 1) : n == 2 && x.size(0) > 1 ? x.stride(0) : row;
+    a.ok = a.ok && stride >= row && stride % 8 == 0 &&
+           (n == 1 || x.size(0) == 1 || x.stride(0) == stride * x.size(1));
+    if (a.ok) t = &x;
+  }
+  int heads() const { return t ? static_cast<int>(t->size(t->dim() - 2)) : 0; }
+};
+
+// The caller's rows like x's, or new ones; `keep` holds them.
+Rows rows_like(Args &a, const Rows &x, Tensor &keep) {
+  Rows r;
+  if (a.v[a.at] == Py_None) {
+    ++a.at;
+    if (!a.ok || !x.t) return r;
+    keep = at::empty(x.t->sizes(), at::TensorOptions().dtype(kBf16).device(at::kCUDA, a.dev));
+    r.stride = static_cast<int64_t>(x.heads()) * x.t->size(x.t->dim() - 1);
+    r.t = &keep;
+    return r;
+  }
+  if (!x.t) return a.ok = false, r;
+  const int64_t n = x.t->dim() - 2;
+  r = Rows(a, x.t->sizes().slice(0, n), x.t->size(n), x.t->size(n + 1));
+  if (a.ok) keep = *r.t;
+  return r;
+}
+
+// fp64 [rot_dim / 2]; rot is rot_dim
+const double *frequencies(Args &a, int64_t d, int &rot) {
+  const Tensor *t = a.tensor(ScalarType::Double, 1);
+  rot = t && t->numel() > 0 && 2 * t->numel() <= d ? static_cast<int>(2 * t->numel()) : 0;
+  a.ok = a.ok && rot > 0;
+  return a.ok ? static_cast<const double *>(t->data_ptr()) : nullptr;
+}
+
+// q, k, inv_freq, positions, factor, interleaved, q_out, k_out
+PyObject *turn(PyObject *const *v, Py_ssize_t given, decltype(&fa_rope) f) {
+  return call(v, given, 8, [f](Args &a) -> PyObject * {
+    const Rows q(a, {}, -1, -1);
+    NEED(a.ok);
+    const int64_t n = q.t->dim() - 2, d = q.t->size(n + 1);
+    const at::IntArrayRef lead = q.t->sizes().slice(0, n);
+    Rows k;
+    if (a.v[a.at] == Py_None)
+      ++a.at;
+    else
+      k = Rows(a, lead, -1, d);
+    int rot;
+    const double *freq = frequencies(a, d, rot);
+    const Tensor *pos = a.unread(kInt, lead);
+    const float factor = a.number();
+    const bool interleaved = a.flag();
+    const int64_t tokens = n == 2 ? lead[0] * lead[1] : lead[0];
+    NEED(a.ok && tokens <= INT_MAX);
+    Tensor keep_q, keep_k;
+    const Rows qo = rows_like(a, q, keep_q), ko = rows_like(a, k, keep_k);
+    NEED(a.ok);
+    return results(f(ptr(q.t), ptr(k.t), q.stride, k.stride, ptr(qo.t), ptr(ko.t), qo.stride,
+                     ko.stride, freq, rot, factor, interleaved, pos ? ints(pos) : nullptr,
+                     static_cast<int>(lead[n - 1]), static_cast<int>(tokens), q.heads(), k.heads(),
+                     static_cast<int>(d), a.stream()),
+                   keep_q, keep_k);
+  });
+}
+PyObject *rope(PyObject *, PyObject *const *v, Py_ssize_t given) { return turn(v, given, lib.rope); }
+PyObject *rope_bwd(PyObject *, PyObject *const *v, Py_ssize_t given) {
+  return turn(v, given, lib.rope_bwd);
+}
+
+// What a write with rotation takes behind its pools: q, k, v, inv_freq,
+// block_table, ctx_lens, cu_seqlens, max_new, factor, interleaved, q_out.
+struct Write {
+  Rows q, k, v, qo;
+  Tensor keep;
+  const double *freq = nullptr;
+  int rot = 0, most = 0;
+  const Tensor *table, *ctx, *cu;
+  float factor = 1.f;
+  bool interleaved = false;
+  Write(Args &a, const Tensor *pool) {
+    if (!a.ok) return;
+    const int64_t Hkv = pool->size(2), d = pool->size(3);
+    if (a.v[a.at] == Py_None)
+      ++a.at;
+    else
+      q = Rows(a, {}, -1, d);
+    k = Rows(a, {}, Hkv, d);
+    v = Rows(a, {}, Hkv, d);
+    if (!a.ok) return;
+    a.ok = k.t->dim() == 3 && v.t->dim() == 3 && v.t->size(0) == k.t->size(0) &&
+           (!q.t || (q.t->dim() == 3 && q.t->size(0) == k.t->size(0)));
+    if (a.v[a.at] == Py_None)
+      ++a.at;
+    else
+      freq = frequencies(a, d, rot);
+    table = a.tensor(kInt, 2);
+    ctx = a.tensor(kInt, 1);
+    cu = a.tensor(kInt, 1);
+    most = a.integer(INT_MIN, INT_MAX);
+    factor = a.number();
+    interleaved = a.flag();
+    if (!a.ok) return;
+    a.ok = small(table) && ctx->size(0) == table->size(0) && cu->size(0) == table->size(0) + 1;
+    qo = rows_like(a, q, keep);
+  }
+  // the queries, or True where there are none
+  PyObject *result(int rc) const {
+    NEED(rc == FA_OK);
+    if (!q.t) Py_RETURN_TRUE;
+    return wrap(keep);
+  }
+};
+
+// k_pool, v_pool, then a Write's
+PyObject *cache_append_rope(PyObject *, PyObject *const *v, Py_ssize_t given) {
+  return call(v, given, 13, [](Args &a) -> PyObject * {
+    const Tensor *kp = a.tensor(kBf16, 4), *vp = a.tensor(kBf16, 4);
+    NEED(a.ok && small(kp) && kp->sizes() == vp->sizes());
+    const Write w(a, kp);
+    NEED(a.ok);
+    return w.result(lib.cache_append_rope(
+        ptr(w.q.t), ptr(w.k.t), ptr(w.v.t), w.q.stride, w.k.stride, w.v.stride, ptr(w.qo.t),
+        w.qo.stride, w.freq, w.rot, w.factor, w.interleaved, ptr(kp), ptr(vp), ints(w.table),
+        size(w.table, 1), ints(w.ctx), ints(w.cu), size(w.table, 0), size(w.k.t, 0), w.most,
+        w.q.heads(), size(kp, 2), size(kp, 3), size(kp, 1), size(kp, 0), a.stream()));
+  });
+}
+
+// k_pool, v_pool, k_scale, v_scale, then a Write's
+PyObject *cache_append_rope_fp8(PyObject *, PyObject *const *v, Py_ssize_t given) {
+  return call(v, given, 15, [](Args &a) -> PyObject * {
+    const Cache c(a);
+    NEED(a.ok);
+    const Write w(a, c.k);
+    NEED(a.ok && w.freq);
+    return w.result(lib.cache_append_rope_fp8(
+        ptr(w.q.t), ptr(w.k.t), ptr(w.v.t), w.q.stride, w.k.stride, w.v.stride, ptr(w.qo.t),
+        w.qo.stride, w.freq, w.rot, w.factor, w.interleaved, ptr(c.k), ptr(c.v), floats(c.k_scale),
+        floats(c.v_scale), ints(w.table), size(w.table, 1), ints(w.ctx), ints(w.cu),
+        size(w.table, 0), size(w.k.t, 0), w.most, w.q.heads(), size(c.k, 2), size(c.k, 3),
+        size(c.k, 1), size(c.k, 0), a.stream()));
+  });
+}
+
+// q, k_pool, v_pool, block_table, ctx_lens, cu_groups, prefix_lens,
+// max_prefix_len, max_own_len, scale, want_lse, out, lse, workspace
+PyObject *decode_paged_prefix(PyObject *, PyObject *const *v, Py_ssize_t given) {
+  return call(v, given, 14, [](Args &a) -> PyObject * {
+    const Tensor *q = a.tensor(kBf16, 3), *k = a.tensor(kBf16, 4), *w = a.tensor(kBf16, 4);
+    const Tensor *table = a.tensor(kInt, 2), *ctx = a.tensor(kInt, 1);
+    const Tensor *cu = a.tensor(kInt, 1), *pre = a.tensor(kInt, 1);
+    NEED(a.ok && small(q) && small(k) && small(table) && small(pre) && k->sizes() == w->sizes() &&
+         k->size(3) == q->size(2) && table->size(0) == q->size(0) && ctx->size(0) == q->size(0) &&
+         cu->size(0) == pre->size(0) + 1);
+    const int most = a.integer(INT_MIN, INT_MAX), most_own = a.integer(INT_MIN, INT_MAX);
+    const float scale = a.scale(q->size(2));
+    const bool want = a.flag();
+    const Tensor *ws = a.workspace();
+    NEED(a.ok);
+    const Tensor out = a.output(kBf16, q->sizes());
+    const Tensor lse = lse_output(a, {q->size(0), q->size(1)}, want);
+    NEED(a.ok);
+    return results(
+        lib.decode_paged_prefix(ptr(q), ptr(k), ptr(w), ints(table), size(table, 1), ints(ctx),
+                                ints(cu), ints(pre), size(pre, 0), most, most_own, size(q, 0),
+                                size(q, 1), size(k, 2), size(q, 2), size(k, 1), size(k, 0), scale,
+                                ptr(out), floats(lse), ptr(ws), static_cast<size_t>(ws->numel()),
+                                a.stream()),
+        out, lse);
+  });
+}
+
 // the library's functions' addresses, in the order of `lib`
 PyObject *bind(PyObject *, PyObject *const *v, Py_ssize_t given) {
   constexpr Py_ssize_t kCalls = sizeof(lib) / sizeof(void *);
@@ -485,6 +692,11 @@ PyMethodDef methods[] = {METHOD(bind),
                          METHOD(cache_append_fp8),
                          METHOD(decode_paged_fp8),
                          METHOD(fwd_paged_fp8),
+                         METHOD(rope),
+                         METHOD(rope_bwd),
+                         METHOD(cache_append_rope),
+                         METHOD(cache_append_rope_fp8),
+                         METHOD(decode_paged_prefix),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
