@@ -31,7 +31,7 @@ LIB_CHECKED = os.path.join(PKG, "libfa_checked.so")
 TORCH_CALLS = os.path.join(PKG, "_torch_calls.so")
 SOURCES = ["fa_api.cu", "fa_cache_api.cu", "prefill.cu", "prefill_window.cu", "prefill_fp8cache.cu",
            "decode.cu", "decode_fp8.cu", "cache_append.cu", "backward.cu", "backward_window.cu",
-           "fa_rope_api.cu", "rope.cu", "fa_prefix_api.cu", "prefix.cu",
+           "fa_rope_api.cu", "rope.cu", "cache_append_rope.cu", "fa_prefix_api.cu", "prefix.cu",
            "decode_own.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -13,15 +13,6 @@
 // filled token by token differs from one filled at once by no more than that.
 // It costs up to one of the nearly 15 binades of e4m3's normal values, and no
 // precision above the smallest.
-//
-// With rotary positions (ROPE) keys are rotated between their registers and
-// their codes, and further warps rotate the queries' heads, 16 tokens each.  A
-// lane's pairs keep their frequencies while its rows walk through the block,
-// so it forms cos and sin of its first row and of one step, and turns them on
-// from row to row (4 multiplications; after the 7 steps of d = 128 off by
-// less than 2^-20, where bf16 and e4m3 keep 2^-9 and 2^-4).  In the half layout
-// the other half of a pair lies in another lane of the row and comes by a
-// shuffle.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -29,8 +20,6 @@
 #include "checks.cuh"
 #include "fa_internal.h"
 #include "ptx.cuh"
-#include "rope_common.cuh"
-#include "rope_internal.h"
 
 namespace fa {
 
@@ -43,23 +32,13 @@ namespace {
 // and 2 us more at d = 64.)
 constexpr int kAppendWarps = 4;
 constexpr int kAppendCtas = 10;
-// Rotating warps hold cos, sin and their steps too: 2.5 times the registers.
-constexpr int kAppendRopeCtas = 4;
 constexpr int kMinScaleExp = -100;
-constexpr int kRopeNone = 0, kRopeHalf = 1, kRopeInterleaved = 2;
 
 // Smallest e >= kMinScaleExp with the bf16 magnitude `bits` (finite) at most
 // 448 * 2^e: 448 = 1.75 * 2^8, so e is the value's exponent - 8, or - 7
 // when its significand is above 1.75.
 __device__ __forceinline__ int scale_exponent(uint32_t bits) {
   const int e = static_cast<int>(bits >> 7) - 127 - 8 + ((bits & 0x7Fu) > 0x60u ? 1 : 0);
-  return max(e, kMinScaleExp);
-}
-
-// The same of an fp32 magnitude (an infinite one is above every bf16's).
-__device__ __forceinline__ int scale_exponent_f32(float x) {
-  const uint32_t bits = __float_as_uint(x);
-  const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return max(e, kMinScaleExp);
 }
 
@@ -72,85 +51,22 @@ __device__ __forceinline__ uint32_t finite_max(uint32_t m, uint32_t word) {
   return max(m, hi < 0x7F80u ? hi : 0u);
 }
 
-// A lane's 8 values of a row, rotated as the row's position wants it.
-// ROPE: the lane's pairs are its own neighbours (4 of them), or its values are
-// one half of 8 pairs, whose other half lane `partner` holds.
-template <int ROPE>
-struct LaneTurn {
-  static constexpr int kPairs = ROPE == kRopeInterleaved ? 4 : 8;
-  float c[kPairs], s[kPairs];    // of the row's position, with the factor
-  float dc[kPairs], ds[kPairs];  // of one step
-  bool on, second;  // the lane's values turn; they are the second half of their pairs
-  int partner;
-
-  // lane column col of a row of D values, rows at positions pos, pos + step, ...
-  __device__ __forceinline__ LaneTurn(const RopeSpec &r, int col, int row_lane0, int pos, int step,
-                                      unsigned int *status) {
-    const int first = ROPE == kRopeInterleaved ? 4 * col : 8 * col % max(r.pairs, 1);
-    on = 8 * col < 2 * r.pairs;
-    second = ROPE == kRopeHalf && on && 8 * col >= r.pairs;
-    partner = row_lane0 + col + (ROPE == kRopeHalf && on ? (second ? -1 : 1) * (r.pairs / 8) : 0);
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      c[i] = dc[i] = 1.f;
-      s[i] = ds[i] = 0.f;
-      if (!on) continue;
-      const uint64_t turns = rope_turns(checked_load(r.inv_freq, first + i, r.pairs, status));
-      const float2 a = rope_cos_sin(turns, pos), d = rope_cos_sin(turns, step);
-      c[i] = a.x * r.factor;
-      s[i] = a.y * r.factor;
-      dc[i] = d.x;
-      ds[i] = d.y;
-    }
-  }
-  __device__ __forceinline__ void advance() {
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const float x = fmaf(c[i], dc[i], -(s[i] * ds[i]));
-      s[i] = fmaf(c[i], ds[i], s[i] * dc[i]);
-      c[i] = x;
-    }
-  }
-  // all lanes of the warp; v: the 8 values in fp32
-  __device__ __forceinline__ void row(const uint4 &x, float2 (&v)[4]) const {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 own = bf16x2_to_float2(w[i]);
-      v[i] = own;
-      if constexpr (ROPE == kRopeInterleaved) {
-        if (on)
-          v[i] = make_float2(fmaf(own.x, c[i], -(own.y * s[i])), fmaf(own.x, s[i], own.y * c[i]));
-      } else {
-        const float2 other = bf16x2_to_float2(__shfl_sync(0xffffffffu, w[i], partner));
-        const float s0 = second ? s[2 * i] : -s[2 * i], s1 = second ? s[2 * i + 1] : -s[2 * i + 1];
-        if (on)
-          v[i] = make_float2(fmaf(own.x, c[2 * i], other.x * s0),
-                             fmaf(own.y, c[2 * i + 1], other.y * s1));
-      }
-    }
-  }
-};
-
 }  // namespace
 
-template <int D, int ROPE>
-__global__ void __launch_bounds__(32 * kAppendWarps, ROPE ? kAppendRopeCtas : kAppendCtas)
-    cache_append_kernel(const AppendParams p, const RopeAppend rope) {
+template <int D>
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
+    cache_append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 8;        // lanes of a row: 8 values (16 bytes of bf16) each
   constexpr int kRows = 32 / kLanes;   // rows a warp loads at once
   constexpr int kIter = kDecodeBlock / kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y;
   // unit: (block of the sequence's new tokens, head, K or V), K and V of a
-  // head side by side; with rotary positions the queries' heads behind them
+  // head side by side
   const long long unit = static_cast<long long>(blockIdx.x) * kAppendWarps + warp;
-  const int units = ROPE ? 2 * p.Hkv + rope.q.heads : 2 * p.Hkv;  // of a block
-  const int nth = static_cast<int>(unit / units);
-  const int of_block = static_cast<int>(unit % units);
-  const bool is_q = ROPE && of_block >= 2 * p.Hkv;
-  const int h = is_q ? of_block - 2 * p.Hkv : of_block >> 1;
-  const bool is_v = !is_q && ((ROPE ? of_block : unit) & 1) != 0;
+  const int nth = static_cast<int>(unit / (2 * p.Hkv));
+  const int h = static_cast<int>(unit % (2 * p.Hkv)) >> 1;
+  const bool is_v = (unit & 1) != 0;
   const bool report = unit == 0 && lane == 0;
 
   const int start = checked_load(p.cu_seqlens, b, p.batch + 1, p.status);
@@ -173,11 +89,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps, ROPE ? kAppendRopeCtas : kA
 
   // the new rows: lane reads values [8 c, 8 c + 8) of rows kRows i + r
   const int c = lane % kLanes, r = lane / kLanes;
-  const uint16_t *src = static_cast<const uint16_t *>(is_q ? rope.q.src : is_v ? p.v : p.k);
-  const int64_t stride = ROPE && is_q ? rope.q.src_stride : is_v ? p.v_stride : p.k_stride;
-  // extent of the input in elements (its last row ends after its heads)
-  const size_t n_src = static_cast<size_t>(p.total_tokens - 1) * stride +
-                       static_cast<size_t>(is_q ? rope.q.heads : p.Hkv) * D;
+  const uint16_t *src = static_cast<const uint16_t *>(is_v ? p.v : p.k);
+  const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  // extent of the input in elements (its last row ends after Hkv * D of them)
+  const size_t n_src = static_cast<size_t>(p.total_tokens - 1) * stride + p.Hkv * D;
   uint4 x[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
@@ -188,29 +103,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps, ROPE ? kAppendRopeCtas : kA
                          static_cast<size_t>(h) * D + c * 8;
       if (in_bounds(off, 8, n_src, p.status)) x[i] = __ldcs(reinterpret_cast<const uint4 *>(src + off));  // read once
     }
-  }
-  if (is_q) {
-    if constexpr (ROPE != kRopeNone) {
-      LaneTurn<ROPE> turn(rope.rope, c, r * kLanes, pos0 + r, kRows, p.status);
-      uint16_t *dst = static_cast<uint16_t *>(rope.q.dst);
-      const size_t n_dst = static_cast<size_t>(p.total_tokens - 1) * rope.q.dst_stride +
-                           static_cast<size_t>(rope.q.heads) * D;
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int slot = i * kRows + r;
-        float2 v[4];
-        turn.row(x[i], v);
-        turn.advance();
-        if (slot < s0 || slot >= s1) continue;
-        const size_t off = static_cast<size_t>(start + pos0 + slot - first) * rope.q.dst_stride +
-                           static_cast<size_t>(h) * D + c * 8;
-        if (in_bounds(off, 8, n_dst, p.status))
-          *reinterpret_cast<uint4 *>(dst + off) =
-              make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                         pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
-      }
-    }
-    return;
   }
   const size_t tidx = static_cast<size_t>(b) * p.max_blocks_per_seq + blk;
   const int phys = checked_load(p.block_table, tidx,
@@ -246,9 +138,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, ROPE ? kAppendRopeCtas : kA
     }
     m = __reduce_max_sync(0xffffffffu, m);
   }
-  const float need =
-      ROPE && !is_v ? pow2(scale_exponent_f32(__uint_as_float(m << 16) * rope.grow))  // (its bound)
-                    : pow2(scale_exponent(m));
+  const float need = pow2(scale_exponent(m));
   const float scale = fmaxf(old, need);  // (a NaN or negative old scale counts as none)
 
   // row `slot` of the block's head, this lane's 8 codes
@@ -279,26 +169,6 @@ __global__ void __launch_bounds__(32 * kAppendWarps, ROPE ? kAppendRopeCtas : kA
   // scale that someone else wrote may be none.
   const bool is_pow2 = (__float_as_uint(scale) & 0x007FFFFFu) == 0u;
   auto write = [&](auto code) {
-    if constexpr (ROPE != kRopeNone) {
-      if (!is_v) {
-        LaneTurn<ROPE> turn(rope.rope, c, r * kLanes, pos0 + r, kRows, p.status);
-#pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const int slot = i * kRows + r;
-          float2 v[4];
-          turn.row(x[i], v);
-          turn.advance();
-          if (slot < s0 || slot >= s1) continue;
-          const float2 a = code(v[0]), e = code(v[1]), f = code(v[2]), g = code(v[3]);
-          uint2 w;
-          w.x = pack_e4m3x4(a.x, a.y, e.x, e.y);
-          w.y = pack_e4m3x4(f.x, f.y, g.x, g.y);
-          if (in_bounds(at(slot), 8, n_pool, p.status))
-            *reinterpret_cast<uint2 *>(pool + at(slot)) = w;
-        }
-        return;
-      }
-    }
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int slot = i * kRows + r;
@@ -320,33 +190,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps, ROPE ? kAppendRopeCtas : kA
   if (lane == 0 && scale != old && in_bounds(sidx, 1, n_scales, p.status)) scales[sidx] = scale;
 }
 
-namespace {
-
-template <int D, int ROPE>
-cudaError_t launch_append_t(const AppendParams &p, const RopeAppend &r, cudaStream_t stream) {
+cudaError_t launch_cache_append(const AppendParams &p, int d, cudaStream_t stream) {
   // the new tokens of a sequence may begin inside a block
   const long long blocks = (p.max_new + 2LL * kDecodeBlock - 2) / kDecodeBlock;
-  const long long units = blocks * (p.Hkv * 2 + (ROPE ? r.q.heads : 0));
+  const long long units = blocks * p.Hkv * 2;
   const dim3 grid(static_cast<unsigned>((units + kAppendWarps - 1) / kAppendWarps),
                   static_cast<unsigned>(p.batch));
-  cache_append_kernel<D, ROPE><<<grid, 32 * kAppendWarps, 0, stream>>>(p, r);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_cache_append(const AppendParams &p, int d, cudaStream_t stream) {
-  return d == 64 ? launch_append_t<64, kRopeNone>(p, {}, stream)
-                 : launch_append_t<128, kRopeNone>(p, {}, stream);
-}
-
-cudaError_t launch_cache_append_rope(const AppendParams &p, const RopeAppend &r, int d,
-                                     bool interleaved, cudaStream_t stream) {
   if (d == 64)
-    return interleaved ? launch_append_t<64, kRopeInterleaved>(p, r, stream)
-                       : launch_append_t<64, kRopeHalf>(p, r, stream);
-  return interleaved ? launch_append_t<128, kRopeInterleaved>(p, r, stream)
-                     : launch_append_t<128, kRopeHalf>(p, r, stream);
+    cache_append_kernel<64><<<grid, 32 * kAppendWarps, 0, stream>>>(p);
+  else
+    cache_append_kernel<128><<<grid, 32 * kAppendWarps, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace fa

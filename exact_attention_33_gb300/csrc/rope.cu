@@ -1,12 +1,10 @@
 // rope.cu - rotary positions: queries and keys rotated in place or from rows
 // to rows, and on the way into a bf16 paged cache.
 //
-// A head row of d values is d / 16 units of 16 values: two 16-byte pieces that
-// hold 8 pairs (half layout: one piece of each half; interleaved: neighbours),
-// or 16 values that pass through.  A thread owns one unit of one token: it
-// forms the 8 angles once and walks over the token's heads with them, q's and
-// k's (and copies v's), 4 rows in flight.  `head_lanes` threads share the
-// heads of a unit; the host takes more of them the fewer tokens there are.
+// A thread owns one unit of one token (rope_common.cuh): it forms the 8 angles
+// once and walks over the token's heads with them, q's and k's (and copies
+// v's), 4 rows in flight.  `head_lanes` threads share the heads of a unit; the
+// host takes more of them the fewer tokens there are.
 // Bound by HBM: 2 bytes read and 2 written for each value.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -23,73 +21,6 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-
-// The 8 pairs of a unit: cos and sin (times the factor), in two's.
-struct UnitAngles {
-  float2 c[4], s[4];
-};
-
-// One unit rotated in fp32.  INTER: word w is pair w; else word w of x holds
-// the a's of pairs 2w and 2w + 1 and that of y their b's.
-template <bool INTER>
-__device__ __forceinline__ void rotate_unit(const UnitAngles &t, uint4 &x, uint4 &y) {
-  uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    if (INTER) {
-      // pairs w (of x) and 4 + w (of y)
-      const float2 p = bf16x2_to_float2(a[w]), q = bf16x2_to_float2(b[w]);
-      const float pc = w & 1 ? t.c[w / 2].y : t.c[w / 2].x, ps = w & 1 ? t.s[w / 2].y : t.s[w / 2].x;
-      const float qc = w & 1 ? t.c[2 + w / 2].y : t.c[2 + w / 2].x;
-      const float qs = w & 1 ? t.s[2 + w / 2].y : t.s[2 + w / 2].x;
-      a[w] = pack_bf16x2(fmaf(p.x, pc, -(p.y * ps)), fmaf(p.x, ps, p.y * pc));
-      b[w] = pack_bf16x2(fmaf(q.x, qc, -(q.y * qs)), fmaf(q.x, qs, q.y * qc));
-    } else {
-      const float2 u = bf16x2_to_float2(a[w]), v = bf16x2_to_float2(b[w]);
-      const float2 ns = make_float2(-t.s[w].x, -t.s[w].y);
-      const float2 r0 = ffma2(u, t.c[w], fmul2(v, ns));
-      const float2 r1 = ffma2(u, t.s[w], fmul2(v, t.c[w]));
-      a[w] = pack_bf16x2(r0.x, r0.y);
-      b[w] = pack_bf16x2(r1.x, r1.y);
-    }
-  }
-  x = make_uint4(a[0], a[1], a[2], a[3]);
-  y = make_uint4(b[0], b[1], b[2], b[3]);
-}
-
-// Pieces [lo, hi) of the heads h0, h0 + step, ... of one token: rotated with
-// `t` where `turn`, copied otherwise.  src and dst point to the token's first
-// head; a piece's values start at o0 and at o1 of a head.  `extent` is what a
-// buffer holds from those pointers on (checked build).
-template <int D, bool INTER>
-__device__ __forceinline__ void walk_heads(const uint16_t *src, uint16_t *dst, int h0, int heads,
-                                           int step, int o0, int o1, bool turn,
-                                           const UnitAngles &t, size_t src_extent,
-                                           size_t dst_extent, unsigned int *status) {
-  constexpr int kFlight = 4;
-  for (int h = h0; h < heads; h += kFlight * step) {
-    uint4 x[kFlight], y[kFlight];
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int hh = h + i * step;
-      x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (hh < heads && in_bounds(static_cast<size_t>(hh) * D + max(o0, o1), 8, src_extent, status)) {
-        x[i] = *reinterpret_cast<const uint4 *>(src + hh * D + o0);
-        y[i] = *reinterpret_cast<const uint4 *>(src + hh * D + o1);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int hh = h + i * step;
-      if (hh >= heads) break;
-      if (turn) rotate_unit<INTER>(t, x[i], y[i]);
-      if (in_bounds(static_cast<size_t>(hh) * D + max(o0, o1), 8, dst_extent, status)) {
-        *reinterpret_cast<uint4 *>(dst + hh * D + o0) = x[i];
-        *reinterpret_cast<uint4 *>(dst + hh * D + o1) = y[i];
-      }
-    }
-  }
-}
 
 // What is left of [tokens, heads, D] rows from token t on, in elements.
 __device__ __forceinline__ size_t rows_left(int tokens, int t, int64_t stride, int heads, int d) {
@@ -143,46 +74,71 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     pos = p.positions ? checked_load(p.positions, t, p.total_tokens, p.status) : t % p.seq_len;
   }
 
-  const int pairs = p.rope.pairs;
-  const bool turn = u < pairs / 8;
-  // the unit's two pieces of a head
-  const int o0 = turn && !INTER ? 8 * u : 16 * u;
-  const int o1 = turn && !INTER ? pairs + 8 * u : 16 * u + 8;
-  UnitAngles a{};
-  if (turn) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 cs = rope_cos_sin(
-          rope_turns(checked_load(p.rope.inv_freq, u * 8 + i, pairs, p.status)), pos);
-      const float c = cs.x * p.rope.factor, s = (BACK ? -cs.y : cs.y) * p.rope.factor;
-      if (i & 1)
-        a.c[i / 2].y = c, a.s[i / 2].y = s;
-      else
-        a.c[i / 2].x = c, a.s[i / 2].x = s;
-    }
-  }
-  auto rows = [&](const RopeRows &r) {
-    if (r.src == nullptr) return;
-    walk_heads<D, INTER>(static_cast<const uint16_t *>(r.src) + t * r.src_stride,
-                         static_cast<uint16_t *>(r.dst) + t * r.dst_stride, hl, r.heads,
-                         p.head_lanes, o0, o1, turn, a,
-                         rows_left(p.total_tokens, t, r.src_stride, r.heads, D),
-                         rows_left(p.total_tokens, t, r.dst_stride, r.heads, D), p.status);
+  // The token's heads in a row: q's, k's and, into a cache, v's.  A row whose
+  // block is bad keeps its queries.
+  const int hq = p.q.src ? p.q.heads : 0;
+  const int hk = !APPEND ? (p.k.src ? p.k.heads : 0) : k_dst ? p.k.heads : 0;
+  const int heads = hq + hk + (APPEND ? hk : 0);
+  const uint16_t *src_q = static_cast<const uint16_t *>(p.q.src) + t * p.q.src_stride;
+  const uint16_t *src_k = static_cast<const uint16_t *>(p.k.src) + t * p.k.src_stride;
+  const uint16_t *src_v = static_cast<const uint16_t *>(p.v.src) + t * p.v.src_stride;
+  uint16_t *dst_q = static_cast<uint16_t *>(p.q.dst) + t * p.q.dst_stride;
+  if constexpr (!APPEND) k_dst = static_cast<uint16_t *>(p.k.dst) + t * p.k.dst_stride;
+  auto src = [&](int h) {
+    return h < hq ? src_q + h * D : h < hq + hk ? src_k + (h - hq) * D : src_v + (h - hq - hk) * D;
   };
-  rows(p.q);
-  if constexpr (APPEND) {
-    if (k_dst == nullptr) return;
-    const size_t left = (static_cast<size_t>(p.num_blocks) * kDecodeBlock) * p.k.heads * D -
-                        (k_dst - static_cast<uint16_t *>(p.k_pool));
-    auto cache = [&](const RopeRows &r, uint16_t *dst, bool rotated) {
-      walk_heads<D, INTER>(static_cast<const uint16_t *>(r.src) + t * r.src_stride, dst, hl, r.heads,
-                           p.head_lanes, o0, o1, rotated, a,
-                           rows_left(p.total_tokens, t, r.src_stride, r.heads, D), left, p.status);
-    };
-    cache(p.k, k_dst, turn);
-    cache(p.v, v_dst, false);
-  } else {
-    rows(p.k);
+  auto dst = [&](int h) {
+    return h < hq ? dst_q + h * D : h < hq + hk ? k_dst + (h - hq) * D : v_dst + (h - hq - hk) * D;
+  };
+  // (checked build) both pieces of head h lie in their buffers
+  auto inside = [&](int h, bool write) {
+    const RopeRows &r = h < hq ? p.q : h < hq + hk ? p.k : p.v;
+    const uint16_t *base = static_cast<const uint16_t *>(
+        !write ? r.src : !APPEND || h < hq ? r.dst : h < hq + hk ? p.k_pool : p.v_pool);
+    const size_t n = write && APPEND && h >= hq
+                         ? static_cast<size_t>(p.num_blocks) * kDecodeBlock * r.heads * D
+                         : rows_left(p.total_tokens, 0, write ? r.dst_stride : r.src_stride, r.heads, D);
+    return in_bounds((write ? dst(h) : src(h)) - base, D, n, p.status);
+  };
+
+  const RopeUnit unit(u, p.rope.pairs, INTER);
+  UnitAngles a{};
+  constexpr int kFlight = 4;
+  uint4 x[kFlight], y[kFlight];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      const int hh = h + i * p.head_lanes;
+      x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (hh < heads && inside(hh, false)) {
+        x[i] = *reinterpret_cast<const uint4 *>(src(hh) + unit.o0);
+        y[i] = *reinterpret_cast<const uint4 *>(src(hh) + unit.o1);
+      }
+    }
+  };
+  load(hl);  // in flight while the angles are formed
+  if (unit.turns)
+    a.set([&](int i) {
+      return rope_turns(checked_load(p.rope.inv_freq, u * 8 + i, p.rope.pairs, p.status));
+    }, pos, p.rope.factor, BACK);
+  for (int h = hl; h < heads;) {
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      const int hh = h + i * p.head_lanes;
+      if (hh >= heads) break;
+      if (unit.turns && hh < hq + hk) {
+        float2 v[8];
+        rotate_unit<INTER>(a, x[i], y[i], v);
+        x[i] = pack_bf16x8(v);
+        y[i] = pack_bf16x8(v + 4);
+      }
+      if (inside(hh, true)) {
+        *reinterpret_cast<uint4 *>(dst(hh) + unit.o0) = x[i];
+        *reinterpret_cast<uint4 *>(dst(hh) + unit.o1) = y[i];
+      }
+    }
+    h += kFlight * p.head_lanes;
+    if (h < heads) load(h);
   }
 }
 
@@ -191,7 +147,7 @@ namespace {
 template <int D, bool INTER, bool BACK, bool APPEND>
 cudaError_t launch_rope_t(RopeParams p, cudaStream_t stream) {
   constexpr int kUnits = D / 16;
-  const int heads = std::max(p.q.src ? p.q.heads : 0, p.k.heads);
+  const int heads = (p.q.src ? p.q.heads : 0) + (APPEND ? 2 : 1) * (p.k.src ? p.k.heads : 0);
   // Threads for the GPU: heads are shared among more of them until there are
   // enough, or every head has its own.
   const long long rows = APPEND ? static_cast<long long>(p.batch) * p.max_new : p.total_tokens;

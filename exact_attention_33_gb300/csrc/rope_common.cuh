@@ -1,22 +1,41 @@
-// rope_common.cuh - angles of rotary positions.
+// rope_common.cuh - angles of rotary positions, and rows turned by them.
 //
 // p * inv_freq is wanted to about 2^-24 of a radian at any position, and the
-// product in fp32 is off by 2^-24 of itself (at position 10^6 by 0.06 rad);
-// fp64 is slow on this GPU.  So turns a position, inv_freq / 2 pi, are made a
-// 64-bit fraction of a turn once for a thread, and the product with a position
-// is one integer multiplication: it wraps at whole turns by itself and is
-// exact.  Its upper half, 2^-32 of a turn, goes to sincospi.
+// product in fp32 is off by 2^-24 of itself (at position 10^6 by 0.06 rad).
+// So turns a position, inv_freq / 2 pi, are made a 64-bit fraction of a turn,
+// and the product with a position is one integer multiplication: it wraps at
+// whole turns by itself and is exact.  Its upper half, 2^-32 of a turn, goes to
+// sincospi.  The fraction is formed in integers too: with the few fp64
+// instructions that it takes otherwise, this GPU's fp64 rate bound every kernel
+// here (a packed training batch 261 us against 232, 16 prompts into the 8-bit
+// cache 343 us).
 #pragma once
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ptx.cuh"
+
 namespace fa {
 
-// Turns a position as a fraction of 2^64 (whole turns left out).
+// Turns a position, inv_freq / (2 pi), as a fraction of 2^64, whole turns left
+// out.  inv_freq = m 2^(e - 1075) with a 53-bit m, 1 / (2 pi) = K 2^-66.
 __device__ __forceinline__ uint64_t rope_turns(double inv_freq) {
-  const double t = inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
-  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+  constexpr uint64_t K = 0xa2f9836e4e44152aull;  // 2^65 / pi
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(inv_freq));
+  const int e = static_cast<int>(bits >> 52) & 0x7FF;
+  uint64_t m = bits & 0xFFFFFFFFFFFFFull;
+  if (e != 0) m |= 1ull << 52;
+  const uint64_t hi = __umul64hi(m, K), lo = m * K;
+  const int s = 1077 - max(e, 1);  // turns 2^64 = (hi 2^64 + lo) 2^-s
+  uint64_t t = 0;
+  if (s >= 64)
+    t = s < 128 ? hi >> (s - 64) : 0;
+  else if (s > 0)
+    t = (hi << (64 - s)) | (lo >> s);
+  else if (s > -64)
+    t = lo << -s;
+  return bits >> 63 ? 0 - t : t;
 }
 
 // cos and sin of p positions' turns.
@@ -26,6 +45,77 @@ __device__ __forceinline__ float2 rope_cos_sin(uint64_t turns, int p) {
   // (as a signed fraction: half a turn either way, in units of half a turn)
   sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f, &s, &c);
   return make_float2(c, s);
+}
+
+// A head row of D values is D / 16 units of two 16-byte pieces: 8 pairs (half
+// layout: a piece of each half; interleaved: neighbours), or 16 values that pass
+// through.
+struct RopeUnit {
+  bool turns;  // the unit's values are rotated
+  int o0, o1;  // where its pieces start in the row
+  __device__ __forceinline__ RopeUnit(int u, int pairs, bool interleaved) {
+    turns = u < pairs / 8;
+    o0 = turns && !interleaved ? 8 * u : 16 * u;
+    o1 = turns && !interleaved ? pairs + 8 * u : 16 * u + 8;
+  }
+};
+
+// cos and sin of a unit's 8 pairs, by two's.
+struct UnitAngles {
+  float2 c[4], s[4];
+
+  // of pairs [8 u, 8 u + 8) at position p, times `factor`
+  template <typename Frequency>
+  __device__ __forceinline__ void set(Frequency turns_of, int p, float factor, bool back) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = rope_cos_sin(turns_of(2 * i), p), y = rope_cos_sin(turns_of(2 * i + 1), p);
+      c[i] = make_float2(x.x * factor, y.x * factor);
+      s[i] = make_float2(x.y * factor, y.y * factor);
+      if (back) s[i] = make_float2(-s[i].x, -s[i].y);
+    }
+  }
+  // on by the angles of d
+  __device__ __forceinline__ void advance(const UnitAngles &d) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 ns = make_float2(-s[i].x, -s[i].y);
+      const float2 x = ffma2(c[i], d.c[i], fmul2(ns, d.s[i]));
+      s[i] = ffma2(c[i], d.s[i], fmul2(s[i], d.c[i]));
+      c[i] = x;
+    }
+  }
+};
+
+// A unit's pieces x and y, rotated in fp32: v[0..3] are piece x's values by
+// two's, v[4..7] piece y's.
+template <bool INTER>
+__device__ __forceinline__ void rotate_unit(const UnitAngles &t, const uint4 &x, const uint4 &y,
+                                            float2 (&v)[8]) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (INTER) {
+      // word w of x is pair w, of y pair 4 + w
+      const float2 p = bf16x2_to_float2(a[w]), q = bf16x2_to_float2(b[w]);
+      const float pc = w & 1 ? t.c[w / 2].y : t.c[w / 2].x, ps = w & 1 ? t.s[w / 2].y : t.s[w / 2].x;
+      const float qc = w & 1 ? t.c[2 + w / 2].y : t.c[2 + w / 2].x;
+      const float qs = w & 1 ? t.s[2 + w / 2].y : t.s[2 + w / 2].x;
+      v[w] = make_float2(fmaf(p.x, pc, -(p.y * ps)), fmaf(p.x, ps, p.y * pc));
+      v[4 + w] = make_float2(fmaf(q.x, qc, -(q.y * qs)), fmaf(q.x, qs, q.y * qc));
+    } else {
+      // word w of x holds the a's of pairs 2w and 2w + 1, that of y their b's
+      const float2 p = bf16x2_to_float2(a[w]), q = bf16x2_to_float2(b[w]);
+      const float2 ns = make_float2(-t.s[w].x, -t.s[w].y);
+      v[w] = ffma2(p, t.c[w], fmul2(q, ns));
+      v[4 + w] = ffma2(p, t.s[w], fmul2(q, t.c[w]));
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float2 *v) {
+  return make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                    pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
 }
 
 }  // namespace fa
