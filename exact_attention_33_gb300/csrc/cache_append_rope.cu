@@ -1,9 +1,10 @@
 // cache_append_rope.cu - quantises new keys, rotated by their positions, and
 // values into a paged e4m3 cache, and rotates the queries that come with them.
 //
-// A warp takes a block of a sequence's new tokens (16 at most) and some of its
-// heads, K's, V's and q's, one after the other.  A lane owns one unit of a row
-// (rope_common.cuh) and walks through the rows with it.  Its pairs keep their
+// The first CTAs of a sequence rotate its queries as rope.cu does.  In the
+// others a warp takes a block of the sequence's new tokens (16 at most) and
+// some of its heads, K's or V's, one after the other.  A lane owns one unit of
+// a row (rope_common.cuh) and walks through the rows with it.  Its pairs keep their
 // frequencies, so it forms cos and sin of its first row and of one step once
 // for all heads, and turns them on from row to row (2 packed multiplications a
 // pair; after at most 3 steps off by less than 2^-21, where bf16 and e4m3 keep
@@ -23,12 +24,13 @@
 #include "ptx.cuh"
 #include "rope_common.cuh"
 #include "rope_internal.h"
+#include "rope_walk.cuh"
 
 namespace fa {
 
 namespace {
 
-constexpr int kAppendWarps = 4;
+constexpr int kAppendWarps = kRopeThreads / 32;
 constexpr int kMinScaleExp = -100;
 
 // Smallest e >= kMinScaleExp with x <= 448 * 2^e (x >= 0, fp32; 2^120 for what
@@ -61,15 +63,20 @@ __device__ __forceinline__ uint2 encode8(const float2 *v, float scale, float inv
 }  // namespace
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(32 * kAppendWarps, 4)
-    cache_append_rope_kernel(const AppendParams p, const RopeAppend rope, const int block_warps) {
+__global__ void __launch_bounds__(kRopeThreads, 2)
+    cache_append_rope_kernel(const AppendParams p, const RopeParams rp, const float grow,
+                             const int q_ctas, const int block_warps) {
+  if (static_cast<int>(blockIdx.x) < q_ctas) {
+    rope_walk<D, INTER, false, kRopeQueries>(rp, blockIdx.x);
+    return;
+  }
   constexpr int kLanes = D / 16;       // lanes of a row, one unit each
   constexpr int kRows = 32 / kLanes;   // rows at once
   constexpr int kIter = kDecodeBlock / kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y;
-  // warp w of the nth block takes heads w, w + block_warps, ... of K's, V's, q's
-  const long long id = static_cast<long long>(blockIdx.x) * kAppendWarps + warp;
+  // warp w of the nth block takes heads w, w + block_warps, ... of K's and V's
+  const long long id = static_cast<long long>(blockIdx.x - q_ctas) * kAppendWarps + warp;
   const int nth = static_cast<int>(id / block_warps);
   const int w = static_cast<int>(id % block_warps);
   const bool report = id == 0 && lane == 0;
@@ -94,23 +101,25 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 4)
   const int row0 = start + pos0 - first;  // the token of slot 0 (may lie before the new ones)
   const int phys = checked_load(p.block_table, static_cast<size_t>(b) * p.max_blocks_per_seq + blk,
                                 static_cast<size_t>(p.batch) * p.max_blocks_per_seq, p.status);
-  const bool bad = phys < 0 || phys >= p.num_blocks;
-  if (bad && w == 0 && lane == 0) raise_status(p.status, FA_DEV_BAD_BLOCK);
+  if (phys < 0 || phys >= p.num_blocks) {
+    if (w == 0 && lane == 0) raise_status(p.status, FA_DEV_BAD_BLOCK);
+    return;
+  }
 
   const int u = lane % kLanes, r = lane / kLanes;
-  const RopeUnit unit(u, rope.rope.pairs, INTER);
-  const int kv = 2 * p.Hkv, heads = kv + rope.q.heads;
+  const RopeUnit unit(u, rp.rope.pairs, INTER);
+  const int heads = 2 * p.Hkv;
   const size_t n_scales = static_cast<size_t>(p.num_blocks) * p.Hkv;
   const size_t n_pool = n_scales * kDecodeBlock * D;
 
   uint4 x[kIter], y[kIter];
   auto load = [&](int h) {
-    const bool is_q = h >= kv, is_v = !is_q && h >= p.Hkv;
-    const uint16_t *src = static_cast<const uint16_t *>(is_q ? rope.q.src : is_v ? p.v : p.k);
-    const int64_t stride = is_q ? rope.q.src_stride : is_v ? p.v_stride : p.k_stride;
-    const int hh = is_q ? h - kv : is_v ? h - p.Hkv : h;
-    const size_t n_src = static_cast<size_t>(p.total_tokens - 1) * stride +
-                         static_cast<size_t>(is_q ? rope.q.heads : p.Hkv) * D;
+    const bool is_v = h >= p.Hkv;
+    const uint16_t *src = static_cast<const uint16_t *>(is_v ? p.v : p.k);
+    const int64_t stride = is_v ? p.v_stride : p.k_stride;
+    const int hh = is_v ? h - p.Hkv : h;
+    const size_t n_src =
+        static_cast<size_t>(p.total_tokens - 1) * stride + static_cast<size_t>(p.Hkv) * D;
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int slot = i * kRows + r;
@@ -125,23 +134,20 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 4)
     }
   };
   int h = w;
-  if (bad)
-    while (h < kv) h += block_warps;  // queries have no block
-  if (h >= heads) return;
   load(h);
   // cos and sin of the lane's first row and of one step
   UnitAngles at_first{}, step{};
-  if (unit.turns) {
+  if (unit.turns && w < p.Hkv) {
     uint64_t turns[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      turns[i] = rope_turns(checked_load(rope.rope.inv_freq, u * 8 + i, rope.rope.pairs, p.status));
-    at_first.set([&](int i) { return turns[i]; }, pos0 + r, rope.rope.factor, false);
+      turns[i] = rope_turns(checked_load(rp.rope.inv_freq, u * 8 + i, rp.rope.pairs, p.status));
+    at_first.set([&](int i) { return turns[i]; }, pos0 + r, rp.rope.factor, false);
     step.set([&](int i) { return turns[i]; }, kRows, 1.f, false);
   }
 
-  for (;; load(h)) {
-    const bool is_q = h >= kv, is_v = !is_q && h >= p.Hkv;
+  for (;;) {
+    const bool is_v = h >= p.Hkv;
     const bool turned = !is_v && unit.turns;
     // the rows of this head, in fp32, one after the other
     UnitAngles a = at_first;
@@ -155,114 +161,103 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 4)
         for (int e = 0; e < 8; ++e) v[e] = bf16x2_to_float2(word[e]);
       }
     };
-    if (is_q) {
-      uint16_t *dst = static_cast<uint16_t *>(rope.q.dst);
-      const size_t n_dst = static_cast<size_t>(p.total_tokens - 1) * rope.q.dst_stride +
-                           static_cast<size_t>(rope.q.heads) * D;
+    const int hh = is_v ? h - p.Hkv : h;
+    float *scales = is_v ? p.v_scale : p.k_scale;
+    const size_t sidx = static_cast<size_t>(phys) * p.Hkv + hh;
+    const float old = s0 > 0 ? checked_load(scales, sidx, n_scales, p.status) : 0.f;
+    // largest magnitude, both halves of a word at once; a warp that meets an
+    // infinity or a NaN looks again at the finite ones
+    uint32_t m2 = 0;
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int slot = i * kRows + r;
-        float2 v[8];
-        row(i, v);
-        const size_t off = static_cast<size_t>(row0 + slot) * rope.q.dst_stride +
-                           static_cast<size_t>(h - kv) * D;
-        if (slot < s0 || slot >= s1 || !in_bounds(off, D, n_dst, p.status)) continue;
-        *reinterpret_cast<uint4 *>(dst + off + unit.o0) = pack_bf16x8(v);
-        *reinterpret_cast<uint4 *>(dst + off + unit.o1) = pack_bf16x8(v + 4);
-      }
-    } else {
-      const int hh = is_v ? h - p.Hkv : h;
-      float *scales = is_v ? p.v_scale : p.k_scale;
-      const size_t sidx = static_cast<size_t>(phys) * p.Hkv + hh;
-      const float old = s0 > 0 ? checked_load(scales, sidx, n_scales, p.status) : 0.f;
-      // largest magnitude, both halves of a word at once; a warp that meets an
-      // infinity or a NaN looks again at the finite ones
-      uint32_t m2 = 0;
+    for (int i = 0; i < kIter; ++i) {
+      const uint32_t word[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m2 = __vmaxu2(m2, word[e] & 0x7FFF7FFFu);
+    }
+    uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+    if (m >= 0x7F80u) {
+      m = 0;
 #pragma unroll
       for (int i = 0; i < kIter; ++i) {
         const uint32_t word[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m2 = __vmaxu2(m2, word[e] & 0x7FFF7FFFu);
+        for (int e = 0; e < 8; ++e) m = finite_max(m, word[e]);
       }
-      uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
-      if (m >= 0x7F80u) {
-        m = 0;
-#pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-          const uint32_t word[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = finite_max(m, word[e]);
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-      }
-      const float top = __uint_as_float(m << 16);
-      const float need = pow2(scale_exponent(is_v ? top : top * rope.grow));
-      const float scale = fmaxf(old, need);  // (a NaN or negative old scale counts as none)
-      uint8_t *pool = static_cast<uint8_t *>(is_v ? p.v_pool : p.k_pool);
-      auto at = [&](int slot) {
-        return ((static_cast<size_t>(phys) * kDecodeBlock + slot) * p.Hkv + hh) * D;
-      };
-      if (s0 > 0 && !(scale <= old)) {
-        // the block's older codes at its new scale
-        const float ratio = old > 0.f ? old / scale : 0.f;
-        for (int slot = r; slot < s0; slot += kRows) {
-          if (!in_bounds(at(slot), D, n_pool, p.status)) continue;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t *code =
-                reinterpret_cast<uint32_t *>(pool + at(slot) + (e < 2 ? unit.o0 : unit.o1)) + e % 2;
-            const float2 lo = e4m3x2_to_float2(*code), hi = e4m3x2_to_float2(*code >> 16);
-            *code = pack_e4m3x4(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
-          }
-        }
-      }
-      // A power of two is divided by through its reciprocal, which is exact; a
-      // scale that someone else wrote may be none.
-      const bool is_pow2 = (__float_as_uint(scale) & 0x007FFFFFu) == 0u;
-      const float inv = 1.f / scale;
-#pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        const int slot = i * kRows + r;
-        float2 v[8];
-        row(i, v);
-        if (slot < s0 || slot >= s1 || !in_bounds(at(slot), D, n_pool, p.status)) continue;
-        *reinterpret_cast<uint2 *>(pool + at(slot) + unit.o0) = encode8(v, scale, inv, is_pow2);
-        *reinterpret_cast<uint2 *>(pool + at(slot) + unit.o1) = encode8(v + 4, scale, inv, is_pow2);
-      }
-      if (lane == 0 && scale != old && in_bounds(sidx, 1, n_scales, p.status)) scales[sidx] = scale;
+      m = __reduce_max_sync(0xffffffffu, m);
     }
+    const float top = __uint_as_float(m << 16);
+    const float need = pow2(scale_exponent(is_v ? top : top * grow));
+    const float scale = fmaxf(old, need);  // (a NaN or negative old scale counts as none)
+    uint8_t *pool = static_cast<uint8_t *>(is_v ? p.v_pool : p.k_pool);
+    auto at = [&](int slot) {
+      return ((static_cast<size_t>(phys) * kDecodeBlock + slot) * p.Hkv + hh) * D;
+    };
+    if (s0 > 0 && !(scale <= old)) {
+      // the block's older codes at its new scale
+      const float ratio = old > 0.f ? old / scale : 0.f;
+      for (int slot = r; slot < s0; slot += kRows) {
+        if (!in_bounds(at(slot), D, n_pool, p.status)) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t *code =
+              reinterpret_cast<uint32_t *>(pool + at(slot) + (e < 2 ? unit.o0 : unit.o1)) + e % 2;
+          const float2 lo = e4m3x2_to_float2(*code), hi = e4m3x2_to_float2(*code >> 16);
+          *code = pack_e4m3x4(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
+        }
+      }
+    }
+    // A power of two is divided by through its reciprocal, which is exact; a
+    // scale that someone else wrote may be none.
+    const bool is_pow2 = (__float_as_uint(scale) & 0x007FFFFFu) == 0u;
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int slot = i * kRows + r;
+      float2 v[8];
+      row(i, v);
+      if (slot < s0 || slot >= s1 || !in_bounds(at(slot), D, n_pool, p.status)) continue;
+      *reinterpret_cast<uint2 *>(pool + at(slot) + unit.o0) = encode8(v, scale, inv, is_pow2);
+      *reinterpret_cast<uint2 *>(pool + at(slot) + unit.o1) = encode8(v + 4, scale, inv, is_pow2);
+    }
+    if (lane == 0 && scale != old && in_bounds(sidx, 1, n_scales, p.status)) scales[sidx] = scale;
     h += block_warps;
     if (h >= heads) return;
+    load(h);
   }
 }
 
 namespace {
 
 template <int D, bool INTER>
-cudaError_t launch_append_t(const AppendParams &p, const RopeAppend &r, cudaStream_t stream) {
+cudaError_t launch_append_t(const AppendParams &p, RopeParams rp, float grow, cudaStream_t stream) {
+  int q_ctas = 0;
+  if (rp.q.src) {
+    rp.head_lanes = rope_head_lanes<D>(static_cast<long long>(p.batch) * p.max_new, rp.q.heads);
+    q_ctas = static_cast<int>(rope_ctas<D>(p.max_new, rp.head_lanes));
+  }
   // the new tokens of a sequence may begin inside a block
   const long long blocks = (p.max_new + 2LL * kDecodeBlock - 2) / kDecodeBlock;
-  const int heads = 2 * p.Hkv + r.q.heads;
-  // a warp takes up to 8 heads of its block, for whom it forms the angles once,
+  // a warp takes up to 4 heads of its block, for whom it forms the angles once,
   // where that leaves two rounds of warps for the GPU
-  const long long rounds = blocks * p.batch * heads / (2LL * 152 * 16);
-  const int per_warp = static_cast<int>(std::min(8LL, std::max(1LL, rounds)));
-  const int block_warps = (heads + per_warp - 1) / per_warp;
-  const dim3 grid(static_cast<unsigned>((blocks * block_warps + kAppendWarps - 1) / kAppendWarps),
+  const long long rounds = blocks * p.batch * 2 * p.Hkv / (2LL * 152 * 16);
+  const int per_warp = static_cast<int>(std::min(4LL, std::max(1LL, rounds)));
+  const int block_warps = (2 * p.Hkv + per_warp - 1) / per_warp;
+  const dim3 grid(static_cast<unsigned>(q_ctas + (blocks * block_warps + kAppendWarps - 1) / kAppendWarps),
                   static_cast<unsigned>(p.batch));
-  cache_append_rope_kernel<D, INTER><<<grid, 32 * kAppendWarps, 0, stream>>>(p, r, block_warps);
+  cache_append_rope_kernel<D, INTER>
+      <<<grid, kRopeThreads, 0, stream>>>(p, rp, grow, q_ctas, block_warps);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache_append_rope(const AppendParams &p, const RopeAppend &r, int d,
+cudaError_t launch_cache_append_rope(const AppendParams &p, const RopeParams &rp, float grow, int d,
                                      bool interleaved, cudaStream_t stream) {
   if (d == 64)
-    return interleaved ? launch_append_t<64, true>(p, r, stream)
-                       : launch_append_t<64, false>(p, r, stream);
-  return interleaved ? launch_append_t<128, true>(p, r, stream)
-                     : launch_append_t<128, false>(p, r, stream);
+    return interleaved ? launch_append_t<64, true>(p, rp, grow, stream)
+                       : launch_append_t<64, false>(p, rp, grow, stream);
+  return interleaved ? launch_append_t<128, true>(p, rp, grow, stream)
+                     : launch_append_t<128, false>(p, rp, grow, stream);
 }
 
 }  // namespace fa

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/fa_rope.h"
+#include "cache_internal.h"
 #include "fa_host.h"
 #include "rope_internal.h"
 
@@ -11,7 +12,7 @@ namespace fa {
 cudaError_t launch_rope(const RopeParams &p, int d, bool interleaved, bool back,
                         cudaStream_t stream);
 cudaError_t launch_append_rope(const RopeParams &p, int d, bool interleaved, cudaStream_t stream);
-cudaError_t launch_cache_append_rope(const AppendParams &p, const RopeAppend &r, int d,
+cudaError_t launch_cache_append_rope(const AppendParams &p, const RopeParams &rp, float grow, int d,
                                      bool interleaved, cudaStream_t stream);
 
 namespace {
@@ -160,9 +161,9 @@ int fa_cache_append_rope_fp8(const void *q, const void *k, const void *v, int64_
                              const int32_t *cu_seqlens, int batch, int total_tokens, int max_new,
                              int H, int Hkv, int d, int block_size, int num_blocks,
                              fa_stream_t stream) {
-  RopeAppend r{};
+  RopeParams r{};
   r.rope = {inv_freq, rot_dim / 2, factor};
-  r.q = {q, q_out, q_stride, q_out_stride, q ? H : 0};
+  r.q = {q, q_out, q_stride, q_out_stride, H};
   const RopeRows kr = {k, nullptr, k_stride, 0, Hkv}, vr = {v, nullptr, v_stride, 0, Hkv};
   if (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !inv_freq)
     return FA_ERR_INVALID_ARG;
@@ -172,9 +173,10 @@ int fa_cache_append_rope_fp8(const void *q, const void *k, const void *v, int64_
                            d, block_size, num_blocks, run);
   if (rc != FA_OK || !run) return rc;
   max_new = std::min(max_new, total_tokens);
-  if ((max_new / kDecodeBlock + 2LL) * (Hkv * 2LL + (q ? H : 0)) > 0x7fffffffLL)
+  if ((max_new / kDecodeBlock + 2LL) * Hkv * 2 + max_new > 0x7fffffffLL)
     return FA_ERR_UNSUPPORTED;
-  r.grow = std::max(1.f, static_cast<float>(1.4142135623730951 * factor));
+  // what a rotated key may grow by
+  const float grow = std::max(1.f, static_cast<float>(1.4142135623730951 * factor));
   AppendParams p{};
   p.status = status_ptr();
   if (p.status == nullptr) return FA_ERR_CUDA;
@@ -195,7 +197,14 @@ int fa_cache_append_rope_fp8(const void *q, const void *k, const void *v, int64_
   p.Hkv = Hkv;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_blocks = num_blocks;
-  return launch_cache_append_rope(p, r, d, interleaved != 0,
+  r.status = p.status;
+  r.ctx_lens = ctx_lens;
+  r.cu_seqlens = cu_seqlens;
+  r.batch = batch;
+  r.total_tokens = total_tokens;
+  r.max_new = max_new;
+  r.max_blocks_per_seq = max_blocks_per_seq;
+  return launch_cache_append_rope(p, r, grow, d, interleaved != 0,
                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;

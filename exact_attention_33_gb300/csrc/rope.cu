@@ -9,179 +9,51 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
-
-#include "checks.cuh"
-#include "ptx.cuh"
-#include "rope_common.cuh"
 #include "rope_internal.h"
+#include "rope_walk.cuh"
 
 namespace fa {
 
-namespace {
+constexpr int kRopeCtas = 3;
 
-constexpr int kRopeThreads = 256;
-
-// What is left of [tokens, heads, D] rows from token t on, in elements.
-__device__ __forceinline__ size_t rows_left(int tokens, int t, int64_t stride, int heads, int d) {
-  return static_cast<size_t>(tokens - 1 - t) * stride + static_cast<size_t>(heads) * d;
-}
-
-}  // namespace
-
-template <int D, bool INTER, bool BACK, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-  constexpr int kUnits = D / 16;
-  const int u = threadIdx.x % kUnits;
-  const int hl = (threadIdx.x / kUnits) % p.head_lanes;
-  const int tokens = kRopeThreads / (kUnits * p.head_lanes);  // of a CTA
-  const long long mine =
-      static_cast<long long>(blockIdx.x) * tokens + threadIdx.x / (kUnits * p.head_lanes);
-  int t, pos;  // the row and its position
-  uint16_t *k_dst = nullptr, *v_dst = nullptr;
-  if constexpr (APPEND) {
-    const int b = blockIdx.y;
-    const bool report = blockIdx.x == 0 && threadIdx.x == 0;
-    const int start = checked_load(p.cu_seqlens, b, p.batch + 1, p.status);
-    const int end = checked_load(p.cu_seqlens, b + 1, p.batch + 1, p.status);
-    const int ctx = checked_load(p.ctx_lens, b, p.batch, p.status);
-    if (start < 0 || end < start || end > p.total_tokens || end - start > p.max_new) {
-      if (report) raise_status(p.status, FA_DEV_BAD_SEQLEN);
-      return;
-    }
-    const int n = end - start;
-    if (ctx < n || ctx > p.max_blocks_per_seq * static_cast<long long>(kDecodeBlock)) {
-      if (report) raise_status(p.status, FA_DEV_BAD_CTX);
-      return;
-    }
-    if (mine >= n) return;
-    t = start + static_cast<int>(mine);
-    pos = ctx - n + static_cast<int>(mine);
-    const size_t at = static_cast<size_t>(b) * p.max_blocks_per_seq + pos / kDecodeBlock;
-    const int phys = checked_load(p.block_table, at,
-                                  static_cast<size_t>(p.batch) * p.max_blocks_per_seq, p.status);
-    if (phys >= 0 && phys < p.num_blocks) {
-      const size_t row = (static_cast<size_t>(phys) * kDecodeBlock + pos % kDecodeBlock) *
-                         p.k.heads * D;
-      k_dst = static_cast<uint16_t *>(p.k_pool) + row;
-      v_dst = static_cast<uint16_t *>(p.v_pool) + row;
-    } else if (hl == 0 && u == 0) {
-      raise_status(p.status, FA_DEV_BAD_BLOCK);
-    }
-  } else {
-    if (mine >= p.total_tokens) return;
-    t = static_cast<int>(mine);
-    pos = p.positions ? checked_load(p.positions, t, p.total_tokens, p.status) : t % p.seq_len;
-  }
-
-  // The token's heads in a row: q's, k's and, into a cache, v's.  A row whose
-  // block is bad keeps its queries.
-  const int hq = p.q.src ? p.q.heads : 0;
-  const int hk = !APPEND ? (p.k.src ? p.k.heads : 0) : k_dst ? p.k.heads : 0;
-  const int heads = hq + hk + (APPEND ? hk : 0);
-  const uint16_t *src_q = static_cast<const uint16_t *>(p.q.src) + t * p.q.src_stride;
-  const uint16_t *src_k = static_cast<const uint16_t *>(p.k.src) + t * p.k.src_stride;
-  const uint16_t *src_v = static_cast<const uint16_t *>(p.v.src) + t * p.v.src_stride;
-  uint16_t *dst_q = static_cast<uint16_t *>(p.q.dst) + t * p.q.dst_stride;
-  if constexpr (!APPEND) k_dst = static_cast<uint16_t *>(p.k.dst) + t * p.k.dst_stride;
-  auto src = [&](int h) {
-    return h < hq ? src_q + h * D : h < hq + hk ? src_k + (h - hq) * D : src_v + (h - hq - hk) * D;
-  };
-  auto dst = [&](int h) {
-    return h < hq ? dst_q + h * D : h < hq + hk ? k_dst + (h - hq) * D : v_dst + (h - hq - hk) * D;
-  };
-  // (checked build) both pieces of head h lie in their buffers
-  auto inside = [&](int h, bool write) {
-    const RopeRows &r = h < hq ? p.q : h < hq + hk ? p.k : p.v;
-    const uint16_t *base = static_cast<const uint16_t *>(
-        !write ? r.src : !APPEND || h < hq ? r.dst : h < hq + hk ? p.k_pool : p.v_pool);
-    const size_t n = write && APPEND && h >= hq
-                         ? static_cast<size_t>(p.num_blocks) * kDecodeBlock * r.heads * D
-                         : rows_left(p.total_tokens, 0, write ? r.dst_stride : r.src_stride, r.heads, D);
-    return in_bounds((write ? dst(h) : src(h)) - base, D, n, p.status);
-  };
-
-  const RopeUnit unit(u, p.rope.pairs, INTER);
-  UnitAngles a{};
-  constexpr int kFlight = 4;
-  uint4 x[kFlight], y[kFlight];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int hh = h + i * p.head_lanes;
-      x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (hh < heads && inside(hh, false)) {
-        x[i] = *reinterpret_cast<const uint4 *>(src(hh) + unit.o0);
-        y[i] = *reinterpret_cast<const uint4 *>(src(hh) + unit.o1);
-      }
-    }
-  };
-  load(hl);  // in flight while the angles are formed
-  if (unit.turns)
-    a.set([&](int i) {
-      return rope_turns(checked_load(p.rope.inv_freq, u * 8 + i, p.rope.pairs, p.status));
-    }, pos, p.rope.factor, BACK);
-  for (int h = hl; h < heads;) {
-#pragma unroll
-    for (int i = 0; i < kFlight; ++i) {
-      const int hh = h + i * p.head_lanes;
-      if (hh >= heads) break;
-      if (unit.turns && hh < hq + hk) {
-        float2 v[8];
-        rotate_unit<INTER>(a, x[i], y[i], v);
-        x[i] = pack_bf16x8(v);
-        y[i] = pack_bf16x8(v + 4);
-      }
-      if (inside(hh, true)) {
-        *reinterpret_cast<uint4 *>(dst(hh) + unit.o0) = x[i];
-        *reinterpret_cast<uint4 *>(dst(hh) + unit.o1) = y[i];
-      }
-    }
-    h += kFlight * p.head_lanes;
-    if (h < heads) load(h);
-  }
+template <int D, bool INTER, bool BACK, int MODE>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeParams p) {
+  rope_walk<D, INTER, BACK, MODE>(p, blockIdx.x);
 }
 
 namespace {
 
-template <int D, bool INTER, bool BACK, bool APPEND>
+template <int D, bool INTER, bool BACK, int MODE>
 cudaError_t launch_rope_t(RopeParams p, cudaStream_t stream) {
-  constexpr int kUnits = D / 16;
+  constexpr bool APPEND = MODE == kRopeCache;
   const int heads = (p.q.src ? p.q.heads : 0) + (APPEND ? 2 : 1) * (p.k.src ? p.k.heads : 0);
-  // Threads for the GPU: heads are shared among more of them until there are
-  // enough, or every head has its own.
-  const long long rows = APPEND ? static_cast<long long>(p.batch) * p.max_new : p.total_tokens;
-  int lanes = 1;
-  while (lanes * 2 * kUnits <= kRopeThreads && lanes < heads && rows * kUnits * lanes < 512 * 1024)
-    lanes *= 2;
-  p.head_lanes = lanes;
-  const int tokens = kRopeThreads / (kUnits * lanes);
-  const long long per = APPEND ? p.max_new : p.total_tokens;
-  const dim3 grid(static_cast<unsigned>((per + tokens - 1) / tokens),
+  p.head_lanes = rope_head_lanes<D>(
+      APPEND ? static_cast<long long>(p.batch) * p.max_new : p.total_tokens, heads);
+  const dim3 grid(rope_ctas<D>(APPEND ? p.max_new : p.total_tokens, p.head_lanes),
                   static_cast<unsigned>(APPEND ? p.batch : 1));
-  rope_kernel<D, INTER, BACK, APPEND><<<grid, kRopeThreads, 0, stream>>>(p);
+  rope_kernel<D, INTER, BACK, MODE><<<grid, kRopeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <bool BACK, bool APPEND>
+template <bool BACK, int MODE>
 cudaError_t launch_rope_d(const RopeParams &p, int d, bool interleaved, cudaStream_t stream) {
   if (d == 64)
-    return interleaved ? launch_rope_t<64, true, BACK, APPEND>(p, stream)
-                       : launch_rope_t<64, false, BACK, APPEND>(p, stream);
-  return interleaved ? launch_rope_t<128, true, BACK, APPEND>(p, stream)
-                     : launch_rope_t<128, false, BACK, APPEND>(p, stream);
+    return interleaved ? launch_rope_t<64, true, BACK, MODE>(p, stream)
+                       : launch_rope_t<64, false, BACK, MODE>(p, stream);
+  return interleaved ? launch_rope_t<128, true, BACK, MODE>(p, stream)
+                     : launch_rope_t<128, false, BACK, MODE>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeParams &p, int d, bool interleaved, bool back,
                         cudaStream_t stream) {
-  return back ? launch_rope_d<true, false>(p, d, interleaved, stream)
-              : launch_rope_d<false, false>(p, d, interleaved, stream);
+  return back ? launch_rope_d<true, kRopeRows>(p, d, interleaved, stream)
+              : launch_rope_d<false, kRopeRows>(p, d, interleaved, stream);
 }
 
 cudaError_t launch_append_rope(const RopeParams &p, int d, bool interleaved, cudaStream_t stream) {
-  return launch_rope_d<false, true>(p, d, interleaved, stream);
+  return launch_rope_d<false, kRopeCache>(p, d, interleaved, stream);
 }
 
 }  // namespace fa

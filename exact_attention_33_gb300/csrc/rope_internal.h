@@ -4,7 +4,6 @@
 
 #include <stdint.h>
 
-#include "cache_internal.h"
 #include "fa_internal.h"
 
 namespace fa {
@@ -31,20 +30,13 @@ struct RopeParams {
   const int32_t *positions;  // [total_tokens], or null: token t at t % seq_len
   int seq_len, total_tokens;
   int head_lanes;  // threads that share a token's heads for each 16-value unit
-  // append only
+  // packed tokens of a cache write
   RopeRows v;
   void *k_pool, *v_pool;       // bf16 [num_blocks, 16, Hkv, d]
   const int32_t *block_table;  // [batch, max_blocks_per_seq]
   const int32_t *ctx_lens;     // [batch], the new tokens counted
   const int32_t *cu_seqlens;   // [batch + 1]
   int batch, max_new, max_blocks_per_seq, num_blocks;
-};
-
-// The 8-bit append's additions to AppendParams.
-struct RopeAppend {
-  RopeSpec rope;
-  RopeRows q;
-  float grow;  // bound of a key's growth by the rotation
 };
 
 }  // namespace fa
