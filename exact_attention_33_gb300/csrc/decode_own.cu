@@ -1,5 +1,10 @@
 // decode_own.cu - the keys that a sequence has for itself behind a shared
-// prefix (prefix.cu): decode.cu's split kernel from the prefix on.
+// prefix: decode.cu's split kernel from the prefix on.
+//
+// Launched behind prefix.cu's kernel as its programmatic dependent, which computes
+// while this one reads: its CTAs start once that kernel's have, one on each SM
+// beside them and more as they end.  The combine waits for this grid alone, so
+// its first CTA waits for that kernel.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -16,6 +21,11 @@
 
 namespace fa {
 
+// Blocks in a warp's ring.  A warp takes 0.6 us for a block that is there, so
+// what counts is warps: rings of two blocks let twice as many of them run as
+// decode.cu's of four, on an SM and beside the shared keys' kernel.
+constexpr int kOwnStages = 2;
+
 // One warp per (sequence, KV head, split of keys [whole, ctx)).
 template <int D, int NT>
 __global__ void __launch_bounds__(32)
@@ -25,12 +35,26 @@ __global__ void __launch_bounds__(32)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x;
   pdl_launch_dependents();
+  const bool first = split == 0 && kvh == 0 && b == 0;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (lane == 0) raise_status(p.status, FA_DEV_SMEM_ALIGN);
+    if (first) pdl_wait_primary();
+    return;
+  }
   PrefixGroup group{};
-  long long start;
-  const int whole = prefix_find(pp, b, true, group, start) ? group.whole : 0;
+  const int whole = prefix_walk<kPrefixBySeq>(pp, b, false, group, nullptr) ? group.whole : 0;
   const int ctx = prefix_ctx(pp, b, whole, split == 0 && kvh == 0 && lane == 0);
-  const int t0 = whole + split * p.split_tokens;
-  if (t0 >= ctx) return;
+  if (pp.alone && first) {  // nobody else looks at the groups
+    PrefixSums sums;
+    PrefixGroup none{};
+    prefix_walk<kPrefixNone>(pp, 0, true, none, &sums);
+  }
+  const int t0 = prefix_own_from(pp, group) + split * p.split_tokens;
+  if (t0 >= ctx) {
+    if (first) pdl_wait_primary();
+    return;
+  }
   const int t1 = min(ctx, t0 + p.split_tokens);
   int my_blk = -1;
   if (lane < (t1 - t0 + kDecodeBlock - 1) / kDecodeBlock) {
@@ -39,14 +63,12 @@ __global__ void __launch_bounds__(32)
       my_blk = p.block_table[tidx];
   }
   const size_t part_row = static_cast<size_t>(b) * p.H + static_cast<size_t>(kvh) * p.group;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   WarpRange<D, NT> st;
-  const int rc = decode_range<D, NT, false>(tm_k, tm_v, p, b, kvh, t0, t1, my_blk, smem, st,
+  const int rc = decode_range<D, NT, false, kOwnStages>(tm_k, tm_v, p, b, kvh, t0, t1, my_blk, smem, st,
                                             WindowBlocks(ctx, 0, 0), ctx);
   if (rc == kRangeBadBlock) store_neutral<D>(p, part_row, split);
   if (rc == kRangeOk) store_range<D, NT>(p, part_row, split, st);
+  if (first) pdl_wait_primary();
 }
 
 namespace {
@@ -54,12 +76,20 @@ namespace {
 template <int D, int NT>
 cudaError_t launch_own_t(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixParams &p,
                          cudaStream_t stream) {
-  using L = DecodeLayout<D>;
+  using L = DecodeLayout<D, kOwnStages>;
   static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = allow_smem(decode_own_kernel<D, NT>, L::kSmemAlloc, smem_set);
+  cudaError_t e = allow_smem(decode_own_kernel<D, NT>, L::kBytes, smem_set);
+  // An SM changes its share of shared memory only while it is empty: both
+  // kernels ask for all of it, or this one's CTAs wait for the other's to end.
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(decode_own_kernel<D, NT>,
+                             cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.own.max_splits, p.own.Hkv, p.own.batch);
-  decode_own_kernel<D, NT><<<grid, 32, L::kSmemAlloc, stream>>>(tk, tv, p);
+  if (!p.alone)
+    return launch_dependent(decode_own_kernel<D, NT>, grid, dim3(32), L::kBytes, stream, tk, tv, p);
+  decode_own_kernel<D, NT><<<grid, 32, L::kBytes, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }
 

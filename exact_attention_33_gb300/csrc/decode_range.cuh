@@ -14,14 +14,15 @@
 
 namespace fa {
 
-template <int D>
+// A warp's ring of STAGES blocks.
+template <int D, int STAGES = kDecodeStages>
 struct DecodeLayout {
   static constexpr int kChunks = D / 64;
   static constexpr int kChunkBytes = kDecodeBlock * 128;   // 16 tokens x 64 bf16
   static constexpr int kBlockBytes = kChunks * kChunkBytes;  // one KV head of one block
   static constexpr int kStageBytes = 2 * kBlockBytes;        // K then V
-  static constexpr int kBar = kDecodeStages * kStageBytes;
-  static constexpr int kMisc = kBar + kDecodeStages * 8;
+  static constexpr int kBar = STAGES * kStageBytes;
+  static constexpr int kMisc = kBar + STAGES * 8;
   static constexpr int kBytes = kMisc + 16;
   static constexpr int kSmemAlloc = kBytes + 1024;
 };
@@ -53,7 +54,7 @@ constexpr int kRangeOk = 0, kRangeBadBlock = 1, kRangeFailed = 2;
 
 // A converged warp streams keys [t0, t1) (at most kDecodeMaxSplitTokens) of
 // sequence b and KV head kvh through its own ring of TMA stages at `smem`
-// (DecodeLayout<D>::kBytes, 1024-byte aligned) and leaves its state in st.
+// (DecodeLayout<D, STAGES>::kBytes, 1024-byte aligned) and leaves its state in st.
 // Lane i holds the physical id of logical block t0 / 16 + i in my_blk (-1
 // when it could not be read).  WIN: t0 and t1 count the keys of the blocks
 // that the windowed query reads (wb), and the hidden ones among them are
@@ -61,13 +62,13 @@ constexpr int kRangeOk = 0, kRangeBadBlock = 1, kRangeFailed = 2;
 // status raised) when a block id of the range is outside the pool,
 // kRangeFailed when a wait gave up (copies in flight are drained before it
 // returns).
-template <int D, int NT, bool WIN>
+template <int D, int NT, bool WIN, int STAGES = kDecodeStages>
 __device__ __forceinline__ int decode_range(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                             const DecodeParams &p, int b, int kvh, int t0, int t1,
                                             int my_blk, uint8_t *smem, WarpRange<D, NT> &st,
                                             const WindowBlocks &wb, int ctx) {
-  using L = DecodeLayout<D>;
-  constexpr int S = kDecodeStages;
+  using L = DecodeLayout<D, STAGES>;
+  constexpr int S = STAGES;
   constexpr int KC = D / 16;  // 16-wide k chunks of the head dimension
   const int lane = threadIdx.x & 31;
   const int nblk = (t1 - t0 + kDecodeBlock - 1) / kDecodeBlock;  // <= 32

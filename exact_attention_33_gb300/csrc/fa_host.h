@@ -132,14 +132,14 @@ inline int sm_count() {
 #endif
 constexpr int kDecodeWaveCtas = FA_DECODE_WAVE_CTAS;
 constexpr int kDecodeMinSplitTokens = 64;
-// Work items that a decode call wants at least.
-inline long long decode_want_items() {
+// Work items that a decode call wants at least (`times` as many as usual).
+inline long long decode_want_items(int times = 1) {
   int sms = sm_count();
   if (sms <= 0) sms = 148;
-  return static_cast<long long>(kDecodeWaveCtas) * sms;
+  return static_cast<long long>(kDecodeWaveCtas) * sms * times;
 }
-inline int decode_split_tokens(int batch, int Hkv, int max_ctx_len) {
-  const long long want = decode_want_items();
+inline int decode_split_tokens(int batch, int Hkv, int max_ctx_len, int times = 1) {
+  const long long want = decode_want_items(times);
   int split = kDecodeMaxSplitTokens;
   while (split > kDecodeMinSplitTokens) {
     const long long items = static_cast<long long>(batch) * Hkv *
@@ -217,9 +217,9 @@ struct DecodeWs {
 };
 
 // Decode workspace: control block, fp32 partial o rows, (m, l) pairs.
-inline DecodeWs decode_ws(int batch, int H, int Hkv, int d, int max_ctx_len) {
+inline DecodeWs decode_ws(int batch, int H, int Hkv, int d, int max_ctx_len, int times = 1) {
   DecodeWs w;
-  w.split_tokens = decode_split_tokens(batch, Hkv, max_ctx_len);
+  w.split_tokens = decode_split_tokens(batch, Hkv, max_ctx_len, times);
   w.max_splits = static_cast<int>(std::max(
       1LL, (static_cast<long long>(max_ctx_len) + w.split_tokens - 1) / w.split_tokens));
   const size_t rows = static_cast<size_t>(batch) * H * w.max_splits;
@@ -234,13 +234,13 @@ inline DecodeWs decode_ws(int batch, int H, int Hkv, int d, int max_ctx_len) {
 // most ceil(keys / 512) of each sequence or, where they are shorter than that,
 // at most ceil(keys / 64) of each, and all of them (on every KV head) fewer than
 // twice the wanted items, because splits of twice the size were fewer than those.
-inline size_t decode_ws_bound(int batch, int H, int Hkv, int d, int max_ctx_len) {
+inline size_t decode_ws_bound(int batch, int H, int Hkv, int d, int max_ctx_len, int times = 1) {
   auto splits = [&](int tokens) {
     return batch * std::max(1LL, (static_cast<long long>(max_ctx_len) + tokens - 1) / tokens);
   };
   const long long rows =
       H * std::max(splits(kDecodeMaxSplitTokens),
-                   std::min(splits(kDecodeMinSplitTokens), 2 * decode_want_items() / Hkv));
+                   std::min(splits(kDecodeMinSplitTokens), 2 * decode_want_items(times) / Hkv));
   return round_up(static_cast<size_t>(rows) * d * sizeof(float), 256) +
          round_up(static_cast<size_t>(rows) * 2 * sizeof(float), 256);
 }

@@ -15,9 +15,43 @@ cudaError_t launch_prefix(const CUtensorMap &tq, const CUtensorMap &tk, const CU
 
 namespace {
 
+// Twice the ordinary work items: sequences' own keys mostly stay well below
+// max_own_len, and a call of few rounds of CTAs waits for the last of them.
+constexpr int kOwnItems = 2;
+
+// Calls that read less than this (K and V of every sequence up to its largest
+// length) take every key as its sequence's own: two kernels instead of three,
+// and the shared blocks come from L2.  Measured with 32 / 8 heads of d = 128, us
+// as own keys and as shared ones: 3 sequences over 1001 keys (two heads of 64)
+// 9 and 14, 8 over 1024 keys (36 MB) 14.4 and 16.0, 4 over 4096 (68 MB) 18.5 and
+// 19.2, 16 over 1024 (71 MB) 18.5 and 17.2, 8 over 4096 (136 MB) 27 and 21.
+constexpr long long kAloneBytes = 64LL << 20;
+
+// Most keys of a sequence.
+int longest(int max_prefix, int max_own) { return max_prefix + max_own + kDecodeBlock - 1; }
+
+bool prefix_alone(int batch, int Hkv, int d, int max_prefix, int max_own) {
+  return static_cast<long long>(batch) * longest(max_prefix, max_own) * Hkv * d * 4 <= kAloneBytes;
+}
+
+// Bytes of the partial states that such calls of at most this batch and these
+// lengths need: a call of b sequences of c keys each, b c <= keys, has at most
+// ceil(c / 512) states of each head and sequence, or, where its splits are
+// shorter, fewer than twice the wanted items and at most ceil(c / 64) of each.
+size_t alone_bound(int batch, int H, int Hkv, int d, int max_prefix, int max_own, int times) {
+  const long long keys = std::min(static_cast<long long>(batch) * longest(max_prefix, max_own),
+                                  kAloneBytes / (4LL * Hkv * d));
+  const long long rows =
+      H * std::max(keys / kDecodeMaxSplitTokens + batch,
+                   std::min(keys / kDecodeMinSplitTokens + batch, 2 * decode_want_items(times) / Hkv));
+  return round_up(static_cast<size_t>(rows) * d * sizeof(float), 256) +
+         round_up(static_cast<size_t>(rows) * 2 * sizeof(float), 256);
+}
+
 struct PrefixWs {
   int max_slots;
   size_t o_bytes, ml_bytes;
+  size_t bytes() const { return o_bytes + ml_bytes; }
 };
 
 int prefix_ctas() {
@@ -73,8 +107,10 @@ size_t fa_decode_prefix_workspace_size(int batch, int H, int Hkv, int d, int max
   if ((d != 64 && d != 128) || block_size != kDecodeBlock) return 0;
   if (!lengths_ok(max_prefix_len, max_own_len)) return 0;
   const PrefixWs w = prefix_ws(batch, H, Hkv, d, max_prefix_len);
-  return FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes +
-         decode_ws_bound(batch, H, Hkv, d, max_own_len + kDecodeBlock - 1);
+  return FA_WORKSPACE_HEADER_BYTES +
+         std::max(alone_bound(batch, H, Hkv, d, max_prefix_len, max_own_len, kOwnItems),
+                  w.bytes() + decode_ws_bound(batch, H, Hkv, d, max_own_len + kDecodeBlock - 1,
+                                              kOwnItems));
 }
 
 int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool,
@@ -107,15 +143,22 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   if (static_cast<long long>(num_blocks) * block_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (batch == 0) return FA_OK;
   const int group = H / Hkv, seqs = kPrefillBM / group;
-  // key tiles of all groups: they are counted in int
+  // Key tiles are counted in int, whatever groups the arrays name: a batch's
+  // worth for each.
   const long long tiles = (max_prefix_len + kPrefixTileKeys - 1LL) / kPrefixTileKeys;
-  if (tiles * Hkv * (batch / (2 * seqs) + std::min(num_groups, batch)) > 0x7fffffffLL)
+  const long long pairs = (batch + 2LL * seqs - 1) / (2 * seqs);
+  if (num_groups > batch || tiles * Hkv * pairs > 0x7fffffffLL / std::max(1, num_groups))
     return FA_ERR_UNSUPPORTED;
   const int max_own = max_own_len + kDecodeBlock - 1;
-  const DecodeWs w = decode_ws(batch, H, Hkv, d, max_own);
-  const PrefixWs s = prefix_ws(batch, H, Hkv, d, max_prefix_len);
+  const bool alone = prefix_alone(batch, Hkv, d, max_prefix_len, max_own_len);
+  const DecodeWs w = decode_ws(
+      batch, H, Hkv, d,
+      alone ? static_cast<int>(std::min<long long>(reach, longest(max_prefix_len, max_own_len)))
+            : max_own,
+      kOwnItems);
+  const PrefixWs s = alone ? PrefixWs{1, 0, 0} : prefix_ws(batch, H, Hkv, d, max_prefix_len);
   if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes + s.o_bytes + s.ml_bytes)
+      workspace_bytes < FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes + s.bytes())
     return FA_ERR_WORKSPACE;
   CallStatus *call = static_cast<CallStatus *>(workspace);
   uint8_t *parts = static_cast<uint8_t *>(workspace) + FA_WORKSPACE_HEADER_BYTES;
@@ -154,8 +197,20 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   p.num_groups = num_groups;
   p.max_prefix = max_prefix_len;
   p.max_own = max_own;
+  p.alone = alone;
   p.seqs_per_tile = seqs;
   p.ctas = prefix_ctas();
+  // Measured on one GB300.  A key tile of 128: 2.1 us with two row tiles of d =
+  // 128 and 1.3 with one, 6 us before and after; the own keys' CTAs read 15 GB/s
+  // each, 6 (d = 64: 13) on an SM of their own, one (d = 64: three) beside.
+  p.tile_ns2 = d == 128 ? 2200.f : 1500.f;
+  p.tile_ns1 = d == 128 ? 1300.f : 900.f;
+  p.fixed_ns = 6000.f;
+  p.state_ns = d == 128 ? 50.f : 25.f;
+  p.key_bytes = 4.f * d * Hkv;
+  p.max_rate = 5000.f;
+  p.free_rate = 130.f;
+  p.beside_rate = d == 128 ? 5.f : 10.f;
   p.max_slots = s.max_slots;
   p.po_part = reinterpret_cast<float *>(parts + w.o_bytes + w.ml_bytes);
   p.pml_part = reinterpret_cast<float4 *>(parts + w.o_bytes + w.ml_bytes + s.o_bytes);

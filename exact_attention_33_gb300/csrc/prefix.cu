@@ -13,14 +13,22 @@
 // after pair; a CTA takes an equal stretch of it, that is one or more runs of
 // key tiles over one pair of row tiles each, and leaves a partial state (m, l,
 // o) for every row and run.
-//   warps 0-7  softmax, one row a thread, two tiles of 128 rows
+//   warps 0-7  softmax, one row a thread, in two streams of four warps
 //   warp 8     MMA issuer: S_i = Q_i K^T, O_i += P_i V (tcgen05, TMEM)
 //   warp 9     TMA of Q (a box of sequences x heads) and, block by block, K
 //   warp 10    TMA of V
-// A tile's rows are whole sequences, 128 / G of them with G heads each.
+// A tile's rows are whole sequences, 128 / G of them with G heads each.  With
+// two row tiles stream i is row tile i over every key tile.  A run with one
+// row tile would have one stream wait for its own products in turn; there
+// stream i takes the key tiles j0 + i, j0 + i + 2, ... of the same rows, and the
+// two states are merged as they leave TMEM.
 //
-// prefix_combine_kernel: W warps per (sequence, query head) merge the partial
-// states of its own keys and of the shared ones, as decode_combine_kernel.
+// It takes less than the SM: the own keys' CTAs, launched as programmatic
+// dependents, run beside it (one on an SM with it, more as it ends) and read
+// their keys while it computes.
+//
+// prefix_combine_kernel: one, two or four warps per (sequence, query head) merge
+// the states of its own keys and of the shared ones, as decode_combine_kernel.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -38,7 +46,14 @@ namespace fa {
 
 namespace {
 
-constexpr int kPrefixThreads = 352;
+// 12 warps of 128 registers, so that the own keys' CTAs find registers too; the
+// softmax warps take some of the others' (256 * 168 + 128 * 48 = 384 * 128).
+constexpr int kPrefixThreads = 384;
+constexpr int kPrefixLaunchRegs = 128;
+constexpr int kPrefixSoftmaxRegs = 168;
+constexpr int kPrefixCtlRegs = 48;
+static_assert(256 * kPrefixSoftmaxRegs + 128 * kPrefixCtlRegs <= kPrefixThreads * kPrefixLaunchRegs,
+              "prefix register split exceeds the launch allocation");
 constexpr float kPrefixRescaleLog2 = 8.f;  // as the prefill kernel's
 
 template <int D>
@@ -50,21 +65,40 @@ struct PrefixLayout {
   static constexpr int kQ = 0;                       // two tiles
   static constexpr int kK = 2 * kTileBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
-  static constexpr int kOut = kV + kStages * kTileBytes;  // 32 rows x 128 bytes a softmax warp
-  static constexpr int kBar = kOut + 8 * 32 * 128;
+  static constexpr int kStates = kV + kStages * kTileBytes;  // 3 x 128 floats
+  static constexpr int kBar = kStates + 3 * 128 * 4;
   // q_full, q_free, drain, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_done[2]
   static constexpr int kNumBars = 3 + 4 * kStages + 6;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16;
-  static constexpr int kSmemAlloc = kBytes + 1024;
-  static_assert(kSmemAlloc <= 232448, "prefix shared memory exceeds 227 KiB");
   static constexpr int kTmemO = 256;
 };
+
+// named_bar_sync of `count` threads that tells all of them whether any says so.
+__device__ __forceinline__ bool named_bar_any(int id, int count, bool x) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, %2, %3, q;\n\t"
+      "selp.s32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<int>(x)), "r"(id), "r"(count)
+      : "memory");
+  return any != 0;
+}
+
+// 8 floats to a 32-byte aligned address: a whole sector
+__device__ __forceinline__ void store8(float *to, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(kPrefixThreads, 1)
+__global__ void __maxnreg__(kPrefixLaunchRegs)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
@@ -77,21 +111,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   pdl_launch_dependents();
 
   // ---------------------------------------------------------------- work
-  long long total;
-  const int per = prefix_share(p, blockIdx.x == 0 && warp == 0, total);
-  if (static_cast<long long>(blockIdx.x) * per >= total) return;  // the whole CTA
+  PrefixSums sums;
+  PrefixGroup g{};
+  prefix_walk<kPrefixNone>(p, 0, blockIdx.x == 0 && warp == 0, g, &sums);
+  const PrefixPlan plan = prefix_plan(p, sums);
+  const int per = plan.per;
+  if (static_cast<long long>(blockIdx.x) * per >= plan.total) return;  // the whole CTA
   int at = blockIdx.x * per;
-  const int stop = static_cast<int>(min(total, static_cast<long long>(at) + per));
+  const int stop = static_cast<int>(min(static_cast<long long>(plan.total),
+                                        static_cast<long long>(at) + per));
 
   // A run: key tiles [j0, j0 + n) of KV head kvh for the row tiles of the
-  // sequences from seq0 on; rows[i] of tile i belong to the group.
+  // sequences from seq0 on; rows0 and rows1 of the two belong to the group.
   int kvh, j0, n, seq0, slot, lead, whole;
-  int rows[2];
+  int rows0, rows1;
   auto load_run = [&]() {
-    PrefixGroup g;
-    long long start = 0;
-    prefix_find(p, at, false, g, start);
-    const int rel = at - static_cast<int>(start);
+    prefix_walk<kPrefixByTile>(p, at, false, g, nullptr);
+    const int rel = at - g.start;
     const int unit = rel / g.tiles;
     j0 = rel - unit * g.tiles;
     n = min(g.tiles - j0, stop - at);
@@ -99,21 +135,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     lead = g.a;
     whole = g.whole;
     seq0 = g.a + (unit - kvh * g.pairs) * 2 * p.seqs_per_tile;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      rows[i] = max(0, min(p.seqs_per_tile, g.e - seq0 - i * p.seqs_per_tile)) * G;
+    rows0 = min(p.seqs_per_tile, g.e - seq0) * G;
+    rows1 = max(0, min(p.seqs_per_tile, g.e - seq0 - p.seqs_per_tile)) * G;
     slot = at / per - (at - j0) / per;
   };
-  // k tiles, key tiles of tile 1 and runs so far, for the barriers' phases
-  int tiles0 = 0, tiles1 = 0, turn = 0, turn1 = 0;
+  // Key tiles and runs so far, and those of each stream, for the barriers' phases.
+  int tiles = 0, turn = 0;
+  int tiles_0 = 0, tiles_1 = 0, turns_0 = 0, turns_1 = 0;
+  // key tiles of stream i in this run; those and its runs before
+  auto stream_tiles = [&](int i) { return rows1 > 0 ? n : (n + 1 - i) / 2; };
+  auto tiles_of = [&](int i) { return i ? tiles_1 : tiles_0; };
+  auto turns_of = [&](int i) { return i ? turns_1 : turns_0; };
   auto next_run = [&]() -> bool {
     at += n;
-    tiles0 += n;
+    tiles += n;
     ++turn;
-    if (rows[1] > 0) {
-      tiles1 += n;
-      ++turn1;
-    }
+    tiles_0 += stream_tiles(0);
+    tiles_1 += stream_tiles(1);
+    ++turns_0;
+    turns_1 += stream_tiles(1) > 0 ? 1 : 0;
     if (at >= stop) return false;
     load_run();
     return true;
@@ -121,9 +161,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   load_run();
 
   // ------------------------------------------------------- shared memory
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (threadIdx.x == 0) raise_status(status, FA_DEV_SMEM_ALIGN);
+    return;
+  }
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L::kBar);
   uint64_t *q_free = q_full + 1;
   uint64_t *drain = q_full + 2;
@@ -168,6 +210,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if (warp >= 8) {
+  setmaxnreg_dec<kPrefixCtlRegs>();
   if (warp == 9 || warp == 10) {
     // ------------------------------------------------------ copies
     // Lanes 0..7 hold a tile's 8 block ids; the ids of 4 tiles come with one
@@ -201,7 +245,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           cur = nxt;
           nxt = fetch(j + kIdTiles);
         }
-        const int x = tiles0 + j, st = x % S;
+        const int x = tiles + j, st = x % S;
         if (x >= S && !mbar_wait_warp(&empty[st], ((x / S) - 1) & 1, abort_flag, status)) return false;
         uint8_t *stage = stage0 + st * L::kTileBytes;
         // lane = block * chunks + chunk issues that copy
@@ -228,9 +272,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // Q's place is free once the last run's S products have read it
         if (turn > 0) ok = mbar_wait_warp(q_free, (turn - 1) & 1, abort_flag, status);
         if (ok && lane == 0) {
-          const int tiles = rows[1] > 0 ? 2 : 1;
-          mbar_arrive_expect_tx(q_full, tiles * p.seqs_per_tile * G * 128 * L::kChunks);
-          for (int i = 0; i < tiles; ++i)
+          const int loads = rows1 > 0 ? 2 : 1;
+          mbar_arrive_expect_tx(q_full, loads * p.seqs_per_tile * G * 128 * L::kChunks);
+          for (int i = 0; i < loads; ++i)
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c)
               tma_load_3d(smem + L::kQ + i * L::kTileBytes + c * L::kChunkBytes, &tm_q, q_full, c * 64,
@@ -251,9 +295,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const uint32_t q_base = smem_u32(smem + L::kQ);
     const uint32_t k_base = smem_u32(smem + L::kK);
     const uint32_t v_base = smem_u32(smem + L::kV);
-    auto issue_s = [&](int i, int st) {
+    // S of stream i: row tile `tile` over the K stage st
+    auto issue_s = [&](int i, int tile, int st) {
       if (elect_one()) {
-        const uint64_t a0 = sdesc_swz<128>(q_base + i * L::kTileBytes, 16, 1024);
+        const uint64_t a0 = sdesc_swz<128>(q_base + tile * L::kTileBytes, 16, 1024);
         const uint64_t b0 = sdesc_swz<128>(k_base + st * L::kTileBytes, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -264,54 +309,83 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       }
       __syncwarp();
     };
-    auto issue_o = [&](int i, int st, int j) {
+    // O of stream i, its first or last key tile of the run
+    auto issue_o = [&](int i, int st, bool first, bool last) {
       if (elect_one()) {
         const uint64_t b0 = sdesc_swz<128>(v_base + st * L::kTileBytes, L::kChunkBytes, 1024);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + L::kTmemO + i * D, tmem + i * 128 + kk * 8,
                  b0 + static_cast<uint64_t>((kk * 16 * 128) >> 4), kIdescO,
-                 (j > 0 || kk > 0) ? 1u : 0u);
-        if (j == n - 1) mma_commit(&o_done[i]);
+                 (!first || kk > 0) ? 1u : 0u);
+        if (last) mma_commit(&o_done[i]);
       }
       __syncwarp();
     };
-    // Per key tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1), as the prefill kernel.
+    auto wait_k = [&](int x) {
+      const bool done = mbar_wait_warp(&k_full[x % S], (x / S) & 1, abort_flag, status);
+      tc_fence_after();
+      return done;
+    };
+    // V(x) and P of stream i, its t-th key tile
+    auto wait_p = [&](int i, int t) {
+      const bool done = mbar_wait_warp(&p_full[i], (tiles_of(i) + t) & 1, abort_flag, status);
+      tc_fence_after();
+      return done;
+    };
+    auto wait_v = [&](int x) {
+      return mbar_wait_warp(&v_full[x % S], (x / S) & 1, abort_flag, status);
+    };
     bool ok = true;
     do {
-      const bool two = rows[1] > 0;
-      auto wait_k = [&](int x) {
-        const bool done = mbar_wait_warp(&k_full[x % S], (x / S) & 1, abort_flag, status);
-        tc_fence_after();
-        return done;
-      };
-      ok = mbar_wait_warp(q_full, turn & 1, abort_flag, status) && wait_k(tiles0);
+      ok = mbar_wait_warp(q_full, turn & 1, abort_flag, status) && wait_k(tiles);
       if (!ok) break;
-      issue_s(0, tiles0 % S);
-      if (two) issue_s(1, tiles0 % S);
-      mma_commit_elect(&k_empty[tiles0 % S]);
-      if (n == 1) mma_commit_elect(q_free);
       int j = 0;
-      for (; j < n; ++j) {
-        const int x = tiles0 + j;
-        if (!mbar_wait_warp(&v_full[x % S], (x / S) & 1, abort_flag, status)) break;
-        if (!mbar_wait_warp(&p_full[0], x & 1, abort_flag, status)) break;
-        tc_fence_after();
-        issue_o(0, x % S, j);
-        if (j + 1 < n) {
-          if (!wait_k(x + 1)) break;
-          issue_s(0, (x + 1) % S);
+      if (rows1 > 0) {
+        // Per key tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1), as the prefill kernel.
+        issue_s(0, 0, tiles % S);
+        issue_s(1, 1, tiles % S);
+        mma_commit_elect(&k_empty[tiles % S]);
+        if (n == 1) mma_commit_elect(q_free);
+        for (; j < n; ++j) {
+          const int x = tiles + j;
+          if (!wait_v(x) || !wait_p(0, j)) break;
+          issue_o(0, x % S, j == 0, j == n - 1);
+          if (j + 1 < n) {
+            if (!wait_k(x + 1)) break;
+            issue_s(0, 0, (x + 1) % S);
+          }
+          if (!wait_p(1, j)) break;
+          issue_o(1, x % S, j == 0, j == n - 1);
+          mma_commit_elect(&v_empty[x % S]);
+          if (j + 1 < n) {
+            issue_s(1, 1, (x + 1) % S);
+            mma_commit_elect(&k_empty[(x + 1) % S]);
+            if (j + 2 == n) mma_commit_elect(q_free);  // the run's last S products are issued
+          }
         }
-        if (two) {
-          if (!mbar_wait_warp(&p_full[1], (tiles1 + j) & 1, abort_flag, status)) break;
-          tc_fence_after();
-          issue_o(1, x % S, j);
+      } else {
+        // One row tile: key tile j is stream j % 2's, two of them under way.
+        issue_s(0, 0, tiles % S);
+        mma_commit_elect(&k_empty[tiles % S]);
+        if (n > 1) {
+          ok = wait_k(tiles + 1);
+          if (!ok) break;
+          issue_s(1, 0, (tiles + 1) % S);
+          mma_commit_elect(&k_empty[(tiles + 1) % S]);
         }
-        mma_commit_elect(&v_empty[x % S]);
-        if (j + 1 < n) {
-          if (two) issue_s(1, (x + 1) % S);
-          mma_commit_elect(&k_empty[(x + 1) % S]);
-          if (j + 2 == n) mma_commit_elect(q_free);  // the run's last S products are issued
+        if (n <= 2) mma_commit_elect(q_free);
+        for (; j < n; ++j) {
+          const int x = tiles + j;
+          if (!wait_v(x) || !wait_p(j & 1, j / 2)) break;
+          issue_o(j & 1, x % S, j < 2, j + 2 >= n);
+          mma_commit_elect(&v_empty[x % S]);
+          if (j + 2 < n) {
+            if (!wait_k(x + 2)) break;
+            issue_s(j & 1, 0, (x + 2) % S);
+            mma_commit_elect(&k_empty[(x + 2) % S]);
+            if (j + 3 == n) mma_commit_elect(q_free);
+          }
         }
       }
       ok = j == n;
@@ -319,37 +393,41 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // everything issued must finish before TMEM is released
     mma_commit_elect(drain);
     mbar_drain(drain, 0, status);
+  }
   } else {
+    setmaxnreg_inc<kPrefixSoftmaxRegs>();
     // ------------------------------------------------------ softmax
     const int i = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + i * 128 + lane_off;
     const uint32_t tO = tmem + L::kTmemO + i * D + lane_off;
-    uint8_t *out_stage = smem + L::kOut + warp * 32 * 128;
     const float sl2 = p.own.scale_log2;
     const float2 sl2x2 = make_float2(sl2, sl2);
     bool ok = true;
     do {
-      if (rows[i] == 0) continue;
-      const int t0 = i == 0 ? tiles0 : tiles1;
+      const bool two = rows1 > 0;
+      const int tile = two ? i : 0;        // row tile
+      const int tile_rows = tile ? rows1 : rows0;
+      const int step = two ? 1 : 2;        // this stream's key tiles: j, j + step, ...
+      const int count = stream_tiles(i);
       // rows behind the group's last sequence take part in the products and are
       // not written; a warp of them alone only keeps the barriers going
-      const bool live = row < rows[i];
-      const bool warp_live = (warp & 3) * 32 < rows[i];
-      const int seq = seq0 + i * p.seqs_per_tile + row / G;
+      const bool live = row < tile_rows;
+      const bool warp_live = (warp & 3) * 32 < tile_rows;
+      const int seq = seq0 + tile * p.seqs_per_tile + row / G;
       const int head = kvh * G + row % G;
       int limit = whole;
       if (live) limit = min(whole, prefix_ctx(p, seq, whole, false));
       float m_ref = -CUDART_INF_F, l = 0.f, l_exact = 0.f;
-      for (int j = 0; j < n; ++j) {
-        ok = mbar_wait_warp(&s_full[i], (t0 + j) & 1, abort_flag, status);
+      for (int t = 0; t < count; ++t) {
+        ok = mbar_wait_warp(&s_full[i], (tiles_of(i) + t) & 1, abort_flag, status);
         if (!ok) break;
         tc_fence_after();
         if (warp_live) {
           uint32_t sr[128];
           tmem_ld128_wait(tS, sr);
-          const int nvis = limit - (j0 + j) * kPrefixTileKeys;
+          const int nvis = limit - (j0 + (two ? 0 : i) + t * step) * kPrefixTileKeys;
           if (__any_sync(0xffffffffu, nvis < kPrefixTileKeys)) {
 #pragma unroll
             for (int c = 0; c < 128; ++c)
@@ -404,18 +482,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           const float2 rs = fadd2(rs0, rs1), re = fadd2(re0, re1);
           l = l * alpha + (rs.x + rs.y);
           l_exact = l_exact * alpha + (re.x + re.y);
-          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+          if (t > 0 && __any_sync(0xffffffffu, grow)) {
             const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               tmem_ld32_wait(tO + c * 32, o);
 #pragma unroll
-              for (int t = 0; t < 32; t += 2) {
+              for (int e = 0; e < 32; e += 2) {
                 const float2 v =
-                    fmul2(make_float2(__uint_as_float(o[t]), __uint_as_float(o[t + 1])), a2);
-                o[t] = __float_as_uint(v.x);
-                o[t + 1] = __float_as_uint(v.y);
+                    fmul2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), a2);
+                o[e] = __float_as_uint(v.x);
+                o[e + 1] = __float_as_uint(v.y);
               }
               tmem_st32(tO + c * 32, o);
             }
@@ -426,37 +504,76 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         mbar_arrive(&p_full[i]);
       }
       // ---------------------------------------------------- partial state
-      if (ok) ok = mbar_wait_warp(&o_done[i], (i == 0 ? turn : turn1) & 1, abort_flag, status);
-      if (!ok || !warp_live) continue;
-      tc_fence_after();
+      // Stream i of two row tiles writes its tile.  With one row tile each
+      // stream writes half of the columns, from both streams' O, and stream 0
+      // the sums.  Every thread of the streams comes to every barrier here, and
+      // they agree on whether a wait gave up: a stream alone would wait for ever.
+      if (ok && count > 0) ok = mbar_wait_warp(&o_done[i], turns_of(i) & 1, abort_flag, status);
       const size_t n_rows = static_cast<size_t>(p.own.batch) * p.own.H * p.max_slots;
-      const size_t mine = (static_cast<size_t>(seq) * p.own.H + head) * p.max_slots + slot;
-      if (live && in_bounds(mine, 1, n_rows, status))
-        p.pml_part[mine] = make_float4(split_max(m_ref, l), l, l_exact, 0.f);
-      // 32 columns at a time: each thread's row through shared memory (16-byte
-      // unit u of row r at u ^ (r % 8)), then 8 lanes write a row's 128 bytes
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32_wait(tO + c * 32, o);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          *reinterpret_cast<uint4 *>(out_stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-              make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int r4 = 0; r4 < 8; ++r4) {
-          const int r = r4 * 4 + lane / 8, u = lane % 8;
-          const uint4 v =
-              *reinterpret_cast<const uint4 *>(out_stage + r * 128 + ((u ^ (r & 7)) << 4));
-          const size_t to = __shfl_sync(0xffffffffu, mine, r) * D + c * 32 + u * 4;
-          if ((warp & 3) * 32 + r < rows[i] && in_bounds(to, 4, n_rows * D, status))
-            *reinterpret_cast<uint4 *>(p.po_part + to) = v;
+      const size_t to = (static_cast<size_t>(seq) * p.own.H + head) * p.max_slots + slot;
+      const bool write = live && in_bounds(to, 1, n_rows, status);
+      float m = split_max(m_ref, l);
+      float w0 = 1.f, w1 = 0.f;  // weights of O_i and of the other stream's
+      const bool other = !two && stream_tiles(1 - i) > 0;
+      // row r's maxima at [r] and [128 + r]; stream 1's sums replace the first,
+      // which only its own thread reads, and follow at [256 + r]
+      float *state = reinterpret_cast<float *>(smem + L::kStates) + row;
+      if (!two) {
+        state[i * 128] = m;
+        named_bar_sync(1, 256);
+        if (ok && other)
+          ok = mbar_wait_warp(&o_done[1 - i], turns_of(1 - i) & 1, abort_flag, status);
+        const float m1 = state[(1 - i) * 128];
+        const float top = fmaxf(m, m1);
+        w0 = m == -CUDART_INF_F ? 0.f : ex2(m - top);
+        w1 = m1 == -CUDART_INF_F ? 0.f : ex2(m1 - top);
+        l = w0 == 0.f ? 0.f : w0 * l;
+        l_exact = w0 == 0.f ? 0.f : w0 * l_exact;
+        m = top;
+        if (i == 1) {
+          state[0] = l;
+          state[256] = l_exact;
         }
-        __syncwarp();
       }
-      // the next run's products overwrite O once this warp's next p_full arrives
+      if (ok && warp_live) {
+        tc_fence_after();
+        const uint32_t tOther = tmem + L::kTmemO + (1 - i) * D + lane_off;
+        const int c0 = two ? 0 : i * (D / 64), c1 = two ? D / 32 : c0 + D / 64;
+        for (int c = c0; c < c1; ++c) {
+          uint32_t o[32];
+          tmem_ld32_wait(tO + c * 32, o);
+          if (!two) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * w0);
+            if (other) {
+              uint32_t o1[32];
+              tmem_ld32_wait(tOther + c * 32, o1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (w1 != 0.f)
+                  o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
+            }
+          }
+          if (write)
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              const float v[8] = {__uint_as_float(o[e]),     __uint_as_float(o[e + 1]),
+                                  __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]),
+                                  __uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]),
+                                  __uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])};
+              store8(p.po_part + to * D + c * 32 + e, v);
+            }
+        }
+      }
+      // the next run's products overwrite O once both streams are past this
       tc_fence_before();
+      ok = !named_bar_any(1, 256, !ok);
+      if (!two && i == 0) {
+        l += state[0];
+        l_exact += state[256];
+      }
+      if (ok && write && (two || i == 0)) p.pml_part[to] = make_float4(m, l, l_exact, 0.f);
     } while (ok && next_run());
   }
 
@@ -473,83 +590,78 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 
 namespace {
 
-constexpr int kPrefixCombineWarps = 4;
+constexpr int kPrefixCombineWarps = 4;  // of a CTA
+constexpr int kPrefixCombineCtas = 8;   // on an SM
 
 }  // namespace
 
-// A CTA per (sequence, query head).  Its warps find the maximum of all states
-// together, take every fourth state each, and are added through shared memory.
-template <int D>
-__global__ void __launch_bounds__(32 * kPrefixCombineWarps)
-    prefix_combine_kernel(const PrefixParams p) {
-  constexpr int W = kPrefixCombineWarps;
+// W warps per (sequence, query head) row, 4 / W rows a CTA; warp w of a row takes
+// states w, w + W, ..., a lane each for the maxima and weights, eight o rows per
+// memory round trip.  The CTAs are there before the states are and read the plan
+// meanwhile, so a call takes no more of them than the GPU holds at once: with
+// W = 1 a warp takes `rows` rows of a sequence, one after the other.
+template <int D, int W>
+__global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
+    prefix_combine_kernel(const PrefixParams p, const int rows) {
   constexpr int E = D / 32;
-  __shared__ float s_acc[W][D];
-  __shared__ float s_l[W], s_lx[W], s_m[W];
+  constexpr int U = 8;
+  constexpr int R = kPrefixCombineWarps / W;
+  __shared__ float s_acc[kPrefixCombineWarps][D];
+  __shared__ float s_l[kPrefixCombineWarps], s_lx[kPrefixCombineWarps], s_m[kPrefixCombineWarps];
   const DecodeParams &o = p.own;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / o.H, h = blockIdx.x - b * o.H;
-  // the plan of the shared keys, and this row's place in it
+  const int w = warp % W, r0 = warp - w;
+  const int row0 = (blockIdx.x * R + warp / W) * rows;
+  const bool live = row0 < o.batch * o.H;  // (a CTA's last rows may lie past the end)
+  const int b = live ? row0 / o.H : 0;
+  // the plan of the shared keys, and this sequence's place in it
+  PrefixSums sums;
   PrefixGroup g{};
-  long long start = 0, total;
-  const int per = prefix_share(p, false, total);
-  const bool grouped = prefix_find(p, b, true, g, start) && total > 0;
-  const int whole = grouped ? g.whole : 0;
-  const int ctx = prefix_ctx(p, b, whole, blockIdx.x % o.H == 0 && threadIdx.x == 0);
-  int shared = 0;  // partial states over shared keys
-  if (whole > 0 && ctx > 0) {
-    const int first = static_cast<int>(start) +
-                      (h / o.group * g.pairs + (b - g.a) / (2 * p.seqs_per_tile)) * g.tiles;
-    shared = (first + g.tiles - 1) / per - first / per + 1;
-  }
-  const int own = (max(0, ctx - whole) + o.split_tokens - 1) / o.split_tokens;
-  const int ns = own + shared;
-  pdl_wait_primary();  // both kernels' partial states are complete from here on
-  const bool publisher = blockIdx.x == 0 && threadIdx.x == 0;
-  const unsigned int call_bits = publisher ? call_status_bits(o.call) : 0u;
+  if (!prefix_walk<kPrefixBySeq>(p, b, false, g, &sums)) g = PrefixGroup{};
+  const int per = p.alone ? 1 : prefix_plan(p, sums).per;
+  const int ctx = prefix_ctx(p, b, g.whole, false);  // (decode_own.cu reports)
+  const int own = (max(0, ctx - prefix_own_from(p, g)) + o.split_tokens - 1) / o.split_tokens;
   // this kernel's own (checked-build) index errors go to the device word only
   unsigned int *status = o.dev_status;
   const size_t n_own = static_cast<size_t>(o.batch) * o.H * o.max_splits;
   const size_t n_shared = static_cast<size_t>(o.batch) * o.H * p.max_slots;
-  const size_t own0 = static_cast<size_t>(blockIdx.x) * o.max_splits;
-  const size_t shared0 = static_cast<size_t>(blockIdx.x) * p.max_slots;
-  // (m, l, l_exact) of state i
-  auto state = [&](int i) -> float3 {
-    if (i < own) {
-      if (!in_bounds(own0 + i, 1, n_own, status)) return make_float3(-CUDART_INF_F, 0.f, 0.f);
-      const float2 x = reinterpret_cast<const float2 *>(o.ml_part)[own0 + i];
-      return make_float3(x.x, x.y, x.y);
+  pdl_wait_primary();  // both kernels' partial states are complete from here on
+  const bool publisher = blockIdx.x == 0 && threadIdx.x == 0;
+  const unsigned int call_bits = publisher ? call_status_bits(o.call) : 0u;
+  for (int row = row0; row < row0 + rows; ++row) {
+    int shared = 0;  // partial states over shared keys
+    if (g.tiles > 0 && ctx > 0 && !p.alone) {
+      const int first =
+          g.start + ((row - b * o.H) / o.group * g.pairs + (b - g.a) / (2 * p.seqs_per_tile)) * g.tiles;
+      shared = (first + g.tiles - 1) / per - first / per + 1;
     }
-    if (!in_bounds(shared0 + i - own, 1, n_shared, status))
+    const int ns = live ? own + shared : 0;
+    const size_t own0 = static_cast<size_t>(row) * o.max_splits;
+    const size_t shared0 = static_cast<size_t>(row) * p.max_slots;
+    // (m, l, l_exact) of state i, the neutral one past the last
+    auto state = [&](int i) -> float3 {
+      if (i < own && i < ns && in_bounds(own0 + i, 1, n_own, status)) {
+        const float2 x = reinterpret_cast<const float2 *>(o.ml_part)[own0 + i];
+        return make_float3(x.x, x.y, x.y);
+      }
+      if (i >= own && i < ns && in_bounds(shared0 + i - own, 1, n_shared, status)) {
+        const float4 x = p.pml_part[shared0 + i - own];
+        return make_float3(x.x, x.y, x.z);
+      }
       return make_float3(-CUDART_INF_F, 0.f, 0.f);
-    const float4 x = p.pml_part[shared0 + i - own];
-    return make_float3(x.x, x.y, x.z);
-  };
-  float M = -CUDART_INF_F;
-  for (int i = threadIdx.x; i < ns; i += 32 * W) M = fmaxf(M, state(i).x);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  if (lane == 0) s_m[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[w]);
-
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float L = 0.f, Lx = 0.f;
-  if (M != -CUDART_INF_F) {
-    constexpr int U = 4;
-    for (int i0 = warp; i0 < ns; i0 += U * W) {
-      float3 st[U];
-      float v[U][E];
+    };
+    // o of U states from the t-th of this warp on (states w + W t); own_o + i D is
+    // o of state i, from `own` on shared_o + i D
+    const float *own_o = o.o_part + own0 * D + lane * E;
+    const float *shared_o = p.po_part + shared0 * D - own * D + lane * E;
+    float v[U][E];
+    auto load = [&](int t) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * W;
-        st[u] = i < ns ? state(i) : make_float3(-CUDART_INF_F, 0.f, 0.f);
-        const size_t row = i < own ? own0 + i : shared0 + i - own;
-        const float *src = (i < own ? o.o_part : p.po_part) + row * D + lane * E;
-        const bool there = i < ns && in_bounds(row, 1, i < own ? n_own : n_shared, status);
+        const int i = (t + u) * W + w;
+        const bool there = i < ns && (i < own ? in_bounds(own0 + i, 1, n_own, status)
+                                              : in_bounds(shared0 + i - own, 1, n_shared, status));
+        const float *src = (i < own ? own_o : shared_o) + i * D;
         if constexpr (E == 4) {
           const float4 x = there ? *reinterpret_cast<const float4 *>(src) : make_float4(0, 0, 0, 0);
           v[u][0] = x.x;
@@ -562,73 +674,88 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps)
           v[u][1 % E] = x.y;
         }
       }
+    };
+    load(0);
+    float3 st = state(lane * W + w);  // of this warp's first 32 states
+    float M = st.x;
+    for (int i = (lane + 32) * W + w; i < ns; i += 32 * W) M = fmaxf(M, state(i).x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    if constexpr (W > 1) {
+      if (lane == 0) s_m[warp] = M;
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < W; ++x) M = fmaxf(M, s_m[r0 + x]);
+    }
+
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    float L = 0.f, Lx = 0.f;  // this lane's states'
+    float weight = 0.f;       // this lane's state's
+    for (int t = 0; t * W + w < ns; t += U) {
+      if (t % 32 == 0) {
+        if (t > 0) st = state((t + lane) * W + w);
+        // an empty state has weight 0 and is passed over, whatever its o holds
+        weight = st.x == -CUDART_INF_F ? 0.f : ex2(st.x - M);
+        if (weight != 0.f) {
+          L = fmaf(weight, st.y, L);
+          Lx = fmaf(weight, st.z, Lx);
+        }
+      }
+      if (t > 0) load(t);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        // an empty state is passed over, whatever its o holds
-        const bool live = st[u].x != -CUDART_INF_F;
-        const float w = ex2(st[u].x - M);
-        L = live ? fmaf(w, st[u].y, L) : L;
-        Lx = live ? fmaf(w, st[u].z, Lx) : Lx;
+        const float wu = __shfl_sync(0xffffffffu, weight, (t + u) & 31);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = live ? fmaf(w, v[u][e], acc[e]) : acc[e];
+        for (int e = 0; e < E; ++e) acc[e] = wu != 0.f ? fmaf(wu, v[u][e], acc[e]) : acc[e];
       }
     }
-  }
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-  if (lane == 0) {
-    s_l[warp] = L;
-    s_lx[warp] = Lx;
-  }
-  __syncthreads();
-  if (warp != 0) return;
-  L = Lx = 0.f;
+    for (int x = 16; x > 0; x >>= 1) {
+      L += __shfl_xor_sync(0xffffffffu, L, x);
+      Lx += __shfl_xor_sync(0xffffffffu, Lx, x);
+    }
+    if constexpr (W > 1) {
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    L += s_l[w];
-    Lx += s_lx[w];
-  }
+      for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+      if (lane == 0) {
+        s_l[warp] = L;
+        s_lx[warp] = Lx;
+      }
+      __syncthreads();
+      if (w != 0) break;  // (one row)
+      L = Lx = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    float t = 0.f;
+      for (int x = 0; x < W; ++x) {
+        L += s_l[r0 + x];
+        Lx += s_lx[r0 + x];
+      }
 #pragma unroll
-    for (int w = 0; w < W; ++w) t += s_acc[w][lane * E + e];
-    acc[e] = t;
+      for (int e = 0; e < E; ++e) {
+        acc[e] = 0.f;
+#pragma unroll
+        for (int x = 0; x < W; ++x) acc[e] += s_acc[r0 + x][lane * E + e];
+      }
+    }
+    const float inv = (L == 0.f) ? 0.f : 1.f / L;
+    const size_t at = static_cast<size_t>(row) * D + lane * E;
+    uint16_t *dst = static_cast<uint16_t *>(o.out) + at;
+    if (live && in_bounds(at, E, static_cast<size_t>(o.batch) * o.H * D, status)) {
+      if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1 % E] * inv),
+                                                     pack_bf16x2(acc[2 % E] * inv, acc[3 % E] * inv));
+      else
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1 % E] * inv);
+    }
+    if (live && lane == 0 && o.lse != nullptr &&
+        in_bounds(row, 1, static_cast<size_t>(o.batch) * o.H, status))
+      o.lse[row] = (Lx == 0.f) ? -CUDART_INF_F : (M + __log2f(Lx)) * 0.69314718055994530942f;
   }
-  const float inv = (L == 0.f) ? 0.f : 1.f / L;
-  const size_t at = static_cast<size_t>(blockIdx.x) * D + lane * E;
-  uint16_t *dst = static_cast<uint16_t *>(o.out) + at;
-  if (in_bounds(at, E, static_cast<size_t>(o.batch) * o.H * D, status)) {
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1 % E] * inv),
-                                                   pack_bf16x2(acc[2 % E] * inv, acc[3 % E] * inv));
-    else
-      *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1 % E] * inv);
-  }
-  if (lane == 0 && o.lse != nullptr &&
-      in_bounds(blockIdx.x, 1, static_cast<size_t>(o.batch) * o.H, status))
-    o.lse[blockIdx.x] = (Lx == 0.f) ? -CUDART_INF_F : (M + __log2f(Lx)) * 0.69314718055994530942f;
   if (publisher) publish_call_status(o.call, call_bits, o.dev_status);
 }
 
 // ------------------------------------------------------------------ launch
-
-// a kernel launched as a programmatic dependent of the one before it
-template <typename Kernel, typename... Args>
-static cudaError_t launch_dependent(Kernel kern, dim3 grid, dim3 block, size_t smem,
-                                    cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
 
 cudaError_t launch_decode_own(const CUtensorMap &tk, const CUtensorMap &tv, const PrefixParams &p,
                               int d, cudaStream_t stream);
@@ -639,14 +766,32 @@ static cudaError_t launch_prefix_d(const CUtensorMap &tq, const CUtensorMap &tk,
                                    cudaStream_t stream) {
   using L = PrefixLayout<D>;
   static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t e = allow_smem(prefix_kernel<D>, L::kSmemAlloc, smem_set);
+  cudaError_t e = allow_smem(prefix_kernel<D>, L::kBytes, smem_set);
+  // (the own keys' kernel wants the same, see there)
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  prefix_kernel<D><<<p.ctas, kPrefixThreads, L::kSmemAlloc, stream>>>(tq, tk, tv, p);
-  e = cudaGetLastError();
+  if (!p.alone) {
+    prefix_kernel<D><<<p.ctas, kPrefixThreads, L::kBytes, stream>>>(tq, tk, tv, p);
+    e = cudaGetLastError();
+  }
   if (e == cudaSuccess) e = launch_decode_own(tk, tv, p, D, stream);
   if (e != cudaSuccess) return e;
-  return launch_dependent(prefix_combine_kernel<D>, dim3(static_cast<unsigned>(p.own.batch * p.own.H)),
-                          dim3(32 * kPrefixCombineWarps), 0, stream, p);
+  // as many warps a row, and then as few rows a warp, as the GPU holds at once
+  const int rows = p.own.batch * p.own.H, ctas = p.ctas * kPrefixCombineCtas;
+  const dim3 block(32 * kPrefixCombineWarps);
+  if (rows <= ctas)
+    return launch_dependent(prefix_combine_kernel<D, 4>, dim3(static_cast<unsigned>(rows)), block, 0,
+                            stream, p, 1);
+  if (rows <= 2 * ctas)
+    return launch_dependent(prefix_combine_kernel<D, 2>,
+                            dim3(static_cast<unsigned>((rows + 1) / 2)), block, 0, stream, p, 1);
+  int each = 1;
+  while (rows > 4LL * each * ctas && p.own.H % (2 * each) == 0) each *= 2;
+  return launch_dependent(prefix_combine_kernel<D, 1>,
+                          dim3(static_cast<unsigned>((rows / each + 3) / 4)), block, 0, stream, p,
+                          each);
 }
 
 cudaError_t launch_prefix(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,

@@ -23,8 +23,15 @@ struct PrefixParams {
   const int32_t *prefix_lens;  // [num_groups]
   int num_groups;
   int max_prefix, max_own;     // keys; max_own counts the prefix's last part block
+  int alone;                   // every key as a sequence's own (small calls)
   int seqs_per_tile;           // sequences whose group of heads fills a 128-row tile
-  int ctas;                    // CTAs that share the prefix work
+  int ctas;                    // CTAs that share the prefix work at most (one an SM)
+  // What decides how many do: ns of a key tile with two row tiles and with one,
+  // before and after them, and of the partial states that each CTA adds; bytes
+  // a key (all KV heads); bytes a ns that the own keys' CTAs read at most, on an
+  // SM of their own and beside this work.
+  float tile_ns2, tile_ns1, fixed_ns, state_ns;
+  float key_bytes, max_rate, free_rate, beside_rate;
   int max_slots;               // partial states of a row over shared keys
   float *po_part;              // fp32 [batch, H, max_slots, d]
   float4 *pml_part;            // [batch, H, max_slots]: m (log2 units), l, l_exact, 0
@@ -32,10 +39,10 @@ struct PrefixParams {
 
 // One group: its sequences [a, e), the keys of its shared blocks, and the work
 // of it: `pairs` CTA loads of query rows (two tiles) of each KV head, `tiles`
-// key tiles each.
+// key tiles each; `start` key tiles lie before it in the call's line of them.
 struct PrefixGroup {
   int a, e, whole, pairs, tiles;
-  long long work;  // key tiles over all pairs and KV heads
+  int start;
 };
 
 __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams &p, int g, bool report) {
@@ -59,53 +66,116 @@ __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams &p, int g
   r.whole = n / kDecodeBlock * kDecodeBlock;
   r.tiles = (r.whole + kPrefixTileKeys - 1) / kPrefixTileKeys;
   r.pairs = (e - a + 2 * p.seqs_per_tile - 1) / (2 * p.seqs_per_tile);
-  r.work = static_cast<long long>(r.tiles) * r.pairs * p.own.Hkv;
   return r;
 }
 
-// The group that holds key tile `pos` of the call's work (all groups' one
-// after the other), or, with by_seq, the sequence `pos`; its work starts at
-// `start`.  All lanes of a converged warp; false if there is none.
-__device__ __forceinline__ bool prefix_find(const PrefixParams &p, long long pos, bool by_seq,
-                                            PrefixGroup &found, long long &start) {
+// The work of all groups, and how it is shared: CTA c takes key tiles [c per,
+// (c + 1) per) of `total`.  Groups that follow the rules make an int's worth of
+// work (the host looks); others may wrap, and what they write stays in bounds
+// all the same.
+struct PrefixPlan {
+  int total, per;
+};
+
+// What the search is for: the group of a sequence, or of a key tile.
+constexpr int kPrefixNone = 0, kPrefixBySeq = 1, kPrefixByTile = 2;
+
+// Walks over the groups, 32 at a time (all lanes of a converged warp).  Finds
+// the group that `what` and `key` ask for, into `found`; false if there is none.
+// Sums the work, its cost in ns of one SM, and the keys that sequences share.
+struct PrefixSums {
+  int total;
+  float cost;
+  long long shared_keys;
+};
+template <int WHAT>
+__device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool report,
+                                            PrefixGroup &found, PrefixSums *sums) {
   const int lane = threadIdx.x & 31;
-  long long base = 0;
-  for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
-    const PrefixGroup r = prefix_group(p, g0 + lane, false);
-    long long incl = r.work;
+  int base = 0;
+  bool hit = false;
+  if (sums) *sums = {0, 0.f, 0};
+  for (int g0 = 0; g0 < p.num_groups && !(hit && !sums); g0 += 32) {
+    PrefixGroup r = prefix_group(p, g0 + lane, report);
+    const int work = r.tiles * r.pairs * p.own.Hkv;
+    int incl = work;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    const unsigned hit = __ballot_sync(
-        0xffffffffu, by_seq ? (r.a <= pos && pos < r.e) : pos < base + incl);
-    if (hit != 0u) {
-      const int l = __ffs(hit) - 1;
-      found.a = __shfl_sync(0xffffffffu, r.a, l);
-      found.e = __shfl_sync(0xffffffffu, r.e, l);
-      found.whole = __shfl_sync(0xffffffffu, r.whole, l);
-      found.pairs = __shfl_sync(0xffffffffu, r.pairs, l);
-      found.tiles = __shfl_sync(0xffffffffu, r.tiles, l);
-      found.work = __shfl_sync(0xffffffffu, r.work, l);
-      start = base + __shfl_sync(0xffffffffu, incl - r.work, l);
-      return true;
+    r.start = base + incl - work;
+    if (WHAT != kPrefixNone && !hit) {
+      const unsigned at = __ballot_sync(
+          0xffffffffu, WHAT == kPrefixBySeq ? (r.a <= key && key < r.e)
+                                            : (work > 0 && key < r.start + work));
+      if (at != 0u) {
+        const int l = __ffs(at) - 1;
+        found.a = __shfl_sync(0xffffffffu, r.a, l);
+        found.e = __shfl_sync(0xffffffffu, r.e, l);
+        found.whole = __shfl_sync(0xffffffffu, r.whole, l);
+        found.pairs = __shfl_sync(0xffffffffu, r.pairs, l);
+        found.tiles = __shfl_sync(0xffffffffu, r.tiles, l);
+        found.start = __shfl_sync(0xffffffffu, r.start, l);
+        hit = true;
+      }
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
+    if (sums) {
+      // pairs with two row tiles take longer than a single one
+      const int n = r.e - r.a, single = n > 0 && (n - 1) / p.seqs_per_tile % 2 == 0 ? 1 : 0;
+      const float tiles = static_cast<float>(r.tiles * p.own.Hkv);
+      sums->cost = __fadd_rn(
+          sums->cost, __fmul_rn(tiles, __fadd_rn(__fmul_rn(static_cast<float>(r.pairs - single),
+                                                           p.tile_ns2),
+                                                 __fmul_rn(static_cast<float>(single), p.tile_ns1))));
+      sums->shared_keys += static_cast<long long>(r.whole) * n;
+    }
   }
-  return false;
+  if (sums) sums->total = base;
+  return hit;
 }
 
-// Key tiles of a CTA's share: CTA c takes tiles [c per, (c + 1) per) of the
-// call's work.  0 without work (and where groups that overlap against the
-// rules add up to more than an int).  All lanes of a converged warp.
-__device__ __forceinline__ int prefix_share(const PrefixParams &p, bool report, long long &total) {
-  total = 0;
-  for (int g = threadIdx.x & 31; g < p.num_groups; g += 32) total += prefix_group(p, g, report).work;
+// The plan of a call, the same in every warp that asks (integers, and fp32
+// operations that no compiler contracts).  The own keys' CTAs read while this
+// work computes, several on an SM that it leaves to them and some beside it, so it takes as many SMs as let both end together.
+__device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const PrefixSums &s) {
+  const int lane = threadIdx.x & 31;
+  if (s.total <= p.ctas) return {max(0, s.total), 1};
+  float cost = s.cost;
+  // keys of all sequences, from every `skip`-th of a large batch
+  const int skip = (p.own.batch + 1023) / 1024;
+  long long keys = 0;
+  for (int b = lane * skip; b < p.own.batch; b += 32 * skip)
+    keys += max(0, checked_load(p.own.ctx_lens, b, p.own.batch, p.own.status));
+  keys *= skip;
+  float shared = static_cast<float>(s.shared_keys);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (total > 0x7fffffffLL) total = 0;
-  return static_cast<int>((total + p.ctas - 1) / p.ctas);
+  for (int o = 16; o > 0; o >>= 1) {
+    cost = __fadd_rn(cost, __shfl_xor_sync(0xffffffffu, cost, o));
+    shared = __fadd_rn(shared, __shfl_xor_sync(0xffffffffu, shared, o));
+    keys += __shfl_xor_sync(0xffffffffu, keys, o);
+  }
+  // lane l tries ctas - l ctas / 40 SMs
+  const int n = max(1, p.ctas - lane * p.ctas / 40);
+  const float own_bytes =
+      __fmul_rn(fmaxf(0.f, __fadd_rn(static_cast<float>(keys), -shared)), p.key_bytes);
+  const float rate =
+      fminf(p.max_rate, __fadd_rn(__fmul_rn(static_cast<float>(p.ctas - n), p.free_rate),
+                                  __fmul_rn(static_cast<float>(n), p.beside_rate)));
+  const float t = __fadd_rn(fmaxf(__fadd_rn(p.fixed_ns, __fdiv_rn(cost, static_cast<float>(n))),
+                                  __fdiv_rn(own_bytes, rate)),
+                            __fmul_rn(static_cast<float>(n), p.state_ns));
+  const unsigned best = __reduce_min_sync(
+      0xffffffffu, (static_cast<unsigned>(fminf(t, 1.3e8f)) << 5) | static_cast<unsigned>(lane));
+  const int ctas = __shfl_sync(0xffffffffu, n, best & 31);
+  const int total = max(0, s.total);
+  return {total, max(1, (total + ctas - 1) / ctas)};
+}
+
+// The first key that a sequence of a group reads on its own.
+__device__ __forceinline__ int prefix_own_from(const PrefixParams &p, const PrefixGroup &g) {
+  return p.alone ? 0 : g.whole;
 }
 
 // Keys of sequence b, 0 where ctx_lens breaks a rule (`whole` of them shared).
@@ -116,6 +186,24 @@ __device__ __forceinline__ int prefix_ctx(const PrefixParams &p, int b, int whol
     return ctx;
   if (report) raise_status(p.own.status, FA_DEV_BAD_CTX);
   return 0;
+}
+
+// Launches a kernel as a programmatic dependent of the one before it on the
+// stream.
+template <typename Kernel, typename... Args>
+inline cudaError_t launch_dependent(Kernel kern, dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 }  // namespace fa

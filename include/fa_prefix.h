@@ -61,8 +61,12 @@ size_t fa_decode_prefix_workspace_size(int batch, int H, int Hkv, int d, int max
  * or the table: nothing is shared; ctx_lens negative, beyond the table or with
  * more own keys than max_own_len: the row gets out = 0 and lse = -inf),
  * FA_DEV_BAD_BLOCK (rows that need the block hold nothing of use).
- * Supported: d in {64, 128}, H / Hkv <= 16.  Three kernels run in stream order:
- * the shared keys on the tensor cores, the own keys, and the (m, l, o) combine.
+ * Supported: d in {64, 128}, H / Hkv <= 16, num_groups <= batch, and
+ * num_groups * ceil(batch / (2 floor(128 / (H / Hkv)))) * Hkv *
+ * ceil(max_prefix_len / 128) below 2^31.  Three kernels: the shared keys on the
+ * tensor cores, the own keys beside them, and the (m, l, o) combine; a call over
+ * few keys reads them all as own ones (the results are the same up to the order
+ * of the sums).
  */
 int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool,
                            const int32_t *block_table, int max_blocks_per_seq,

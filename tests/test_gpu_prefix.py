@@ -28,9 +28,11 @@ def dev(a):
 
 class Batch:
     """Groups as (prefix, [context lengths]); a context may be shorter than the
-    prefix.  Sequences of a group share the blocks of its whole ones."""
+    prefix.  Sequences of a group share the blocks of its whole ones.  With
+    `shared` the table and max_prefix_len are wide enough that the call does not
+    take every key as a sequence's own, which it does for few of them."""
 
-    def __init__(self, groups, H, Hkv, d, seed, spread=1.0):
+    def __init__(self, groups, H, Hkv, d, seed, spread=1.0, shared=True):
         torch = torch_mod()
         rng = np.random.default_rng(seed)
         g = torch.Generator(device="cuda").manual_seed(seed)
@@ -56,6 +58,10 @@ class Batch:
         self.pre = np.int32([p for p, _ in groups])
         self.max_pre = int(max(self.pre, default=0))
         self.max_own = max([max(0, c - p) for p, cs in groups for c in cs], default=0)
+        if shared:
+            self.max_pre = max(self.max_pre, (64 << 20) // (4 * Hkv * d * len(rows)) + 16)
+            more = (self.max_pre + 15) // 16 - self.table.shape[1]
+            self.table = np.pad(self.table, ((0, 0), (0, max(0, more))), constant_values=-1)
 
     def args(self, **new):
         a = dict(q=self.q, k_pool=self.kp, v_pool=self.vp, block_table=dev(self.table),
@@ -100,9 +106,10 @@ CASES = [  # groups (prefix, contexts), H, Hkv, d
 
 
 @pytest.mark.parametrize("case", range(len(CASES)))
-def test_decode(fa, case):
+@pytest.mark.parametrize("shared", [True, False])
+def test_decode(fa, case, shared):
     groups, H, Hkv, d = CASES[case]
-    x = Batch(groups, H, Hkv, d, seed=case)
+    x = Batch(groups, H, Hkv, d, seed=case, shared=shared)
     out, lse = fa.fa_decode_paged_prefix(**x.args())
     assert_device_clean()
     x.check(out, lse)
@@ -147,7 +154,7 @@ def test_many_rows_deep_prefix(fa):
 def test_repeated_calls_give_the_same_bits(fa):
     torch = torch_mod()
     x = Batch([(3000, [3010] * 20), (700, [900] * 13)], 16, 4, 128, seed=5)
-    ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(33, 16, 4, 128, 3000, 200))
+    ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(33, 16, 4, 128, x.max_pre, x.max_own))
     first = fa.fa_decode_paged_prefix(**x.args(), workspace=ws)
     for _ in range(5):
         ws[256:].random_(0, 255)   # whatever it held before
@@ -157,11 +164,12 @@ def test_repeated_calls_give_the_same_bits(fa):
     assert_device_clean()
 
 
-def test_stale_and_foreign_values(fa):
+@pytest.mark.parametrize("shared", [True, False])
+def test_stale_and_foreign_values(fa, shared):
     """NaN in free blocks, in slots past a context and in another group's keys
     reaches nothing; in shared keys it stays in its group."""
     torch = torch_mod()
-    x = Batch([(200, [210, 230, 199]), (500, [520, 501]), (90, [100])], 8, 2, 64, seed=6)
+    x = Batch([(200, [210, 230, 199]), (500, [520, 501]), (90, [100])], 8, 2, 64, seed=6, shared=shared)
     used = np.zeros(x.kp.shape[0] * 16, dtype=bool)
     for b, c in enumerate(x.ctx):
         for j in range(c):
@@ -178,9 +186,10 @@ def test_stale_and_foreign_values(fa):
     x.check(out, lse, only=[0, 1, 2, 5])
 
 
-def test_nan_query(fa):
+@pytest.mark.parametrize("shared", [True, False])
+def test_nan_query(fa, shared):
     torch = torch_mod()
-    x = Batch([(300, [320] * 6)], 8, 2, 128, seed=7)
+    x = Batch([(300, [320] * 6)], 8, 2, 128, seed=7, shared=shared)
     x.q[2, 3, 17] = math.nan
     out, lse = fa.fa_decode_paged_prefix(**x.args())
     assert torch.isnan(out[2, 3]).all() and torch.isnan(lse[2, 3])
@@ -191,11 +200,12 @@ def test_nan_query(fa):
     assert_device_clean()
 
 
-def test_padded_batch_and_no_groups(fa):
+@pytest.mark.parametrize("shared", [True, False])
+def test_padded_batch_and_no_groups(fa, shared):
     """Idle slots with tables of nothing, a batch behind its groups, and no
     groups at all."""
     torch = torch_mod()
-    x = Batch([(400, [450, 420]), (0, [30, 60])], 8, 2, 64, seed=8)
+    x = Batch([(400, [450, 420]), (0, [30, 60])], 8, 2, 64, seed=8, shared=shared)
     x.cu, x.pre = x.cu[:2], x.pre[:1]          # the last two sequences are in no group
     out, lse = fa.fa_decode_paged_prefix(**x.args())
     assert_device_clean()
@@ -214,13 +224,14 @@ def test_padded_batch_and_no_groups(fa):
     x.check(out, lse)
 
 
-def test_bad_data_is_reported(fa):
-    x = Batch([(300, [320, 350]), (100, [120, 130])], 8, 2, 64, seed=9)
+@pytest.mark.parametrize("shared", [True, False])
+def test_bad_data_is_reported(fa, shared):
+    x = Batch([(300, [320, 350]), (100, [120, 130])], 8, 2, 64, seed=9, shared=shared)
     good, gl = fa.fa_decode_paged_prefix(**x.args())
     assert_device_clean()
 
     def run(**new):
-        ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(4, 8, 2, 64, 320, 400))
+        ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(4, 8, 2, 64, x.max_pre + 20, 400))
         out, lse = fa.fa_decode_paged_prefix(**x.args(**new), workspace=ws)
         torch_mod().cuda.synchronize()
         st = fa.fa_last_device_status(ws)
@@ -236,7 +247,7 @@ def test_bad_data_is_reported(fa):
     out, lse, st = run(ctx_lens=i32(320, 350, 120, 200))      # more than max_own_len keys of its own
     assert st == fa.FA_DEV_BAD_CTX and not out[3].any()
     x.check(out, lse, only=[0, 1, 2])
-    out, lse, st = run(prefix_lens=i32(301, 100))             # beyond max_prefix_len
+    out, lse, st = run(prefix_lens=i32(x.max_pre + 1, 100))   # beyond max_prefix_len
     assert st == fa.FA_DEV_BAD_CTX and not out[:2].any()
     x.check(out, lse, only=[2, 3])
     out, lse, st = run(cu_groups=i32(0, 2, 5))                # a group outside the batch
@@ -264,7 +275,7 @@ def test_workspace_serves_smaller_calls(fa):
     ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(64, 8, 2, 128, 9000, 2000))
     for i, groups in enumerate(([(9000, [9001] * 2)], [(500, [2500] * 64)], [(9000, [11000])],
                                 [(130, [131] * 64)], [(0, [2000] * 3), (8999, [9100] * 5)])):
-        x = Batch(groups, 8, 2, 128, seed=20 + i)
+        x = Batch(groups, 8, 2, 128, seed=20 + i, shared=False)
         out, lse = fa.fa_decode_paged_prefix(**x.args(), workspace=ws)
         x.check(out, lse, only=[0, len(x.ctx) - 1])
     assert_device_clean()
@@ -272,7 +283,7 @@ def test_workspace_serves_smaller_calls(fa):
 
 def test_refusals(fa):
     torch = torch_mod()
-    x = Batch([(64, [70, 80])], 8, 2, 64, seed=10)
+    x = Batch([(64, [70, 80])], 8, 2, 64, seed=10, shared=False)
     for new in (dict(q=x.q[:, :, :32]), dict(cu_groups=dev(np.int32([0]))), dict(q=x.q.float()),
                 dict(prefix_lens=dev(np.int64([64]))), dict(ctx_lens=dev(np.int32([70]))),
                 dict(cu_groups=dev(x.cu).cpu()), dict(q=x.q.transpose(0, 1)), dict(v_pool=x.vp[1:]),
@@ -297,7 +308,7 @@ def test_streams_and_two_calls_at_once(fa):
     xs = [Batch([(2500, [2600] * 24)], 8, 2, 128, seed=30), Batch([(700, [900] * 9)], 8, 2, 128, seed=31)]
     streams = [torch.cuda.Stream() for _ in xs]
     args = [x.args() for x in xs]
-    ws = [fa.new_workspace(fa.fa_decode_prefix_workspace_size(24, 8, 2, 128, 2500, 200)) for _ in xs]
+    ws = [fa.new_workspace(fa.fa_decode_prefix_workspace_size(24, 8, 2, 128, x.max_pre, 200)) for x in xs]
     torch.cuda.synchronize()
     for _ in range(4):
         got = [fa.fa_decode_paged_prefix(**a, workspace=w, stream=s)
@@ -308,25 +319,26 @@ def test_streams_and_two_calls_at_once(fa):
     assert_device_clean()
 
 
-def test_graph_replay_with_new_groups(fa):
+@pytest.mark.parametrize("most", [1000, 20000])   # every key as an own one, and shared
+def test_graph_replay_with_new_groups(fa, most):
     """A captured call replayed on other groups, lengths, queries and blocks
     inside its bounds; two graphs share a workspace one after the other."""
     torch = torch_mod()
     shapes = [[(900, [950] * 6), (0, [40] * 2)], [(100, [150]), (700, [701] * 4 + [800, 0, 650])],
               [(16, [60, 17]), (1000, [1001] * 6)]]
-    xs = [Batch(s, 8, 2, 64, seed=40 + i) for i, s in enumerate(shapes)]
+    xs = [Batch(s, 8, 2, 64, seed=40 + i, shared=False) for i, s in enumerate(shapes)]
     blocks = max(x.kp.shape[0] for x in xs)
-    width = max(x.table.shape[1] for x in xs)
+    width = max([(most + 15) // 16] + [x.table.shape[1] for x in xs])
     z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
     kp, vp, q = z(blocks, 16, 2, 64), z(blocks, 16, 2, 64), z(8, 8, 64)
     table, ctx, cu, pre = (z(8, width, t=torch.int32), z(8, t=torch.int32), z(3, t=torch.int32),
                            z(2, t=torch.int32))
     out, lse = torch.empty_like(q), z(8, 8, t=torch.float32)
-    ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(8, 8, 2, 64, 1000, 100))
+    ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(8, 8, 2, 64, most, 100))
     graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
     for graph in graphs:
         with torch.cuda.graph(graph):
-            fa.fa_decode_paged_prefix(q, kp, vp, table, ctx, cu, pre, 1000, 100, out=out, lse=lse,
+            fa.fa_decode_paged_prefix(q, kp, vp, table, ctx, cu, pre, most, 100, out=out, lse=lse,
                                       workspace=ws)
     for turn, x in enumerate(xs * 2):
         kp[:x.kp.shape[0]] = x.kp
@@ -355,7 +367,8 @@ def test_far_blocks(fa):
     x.check(out, lse)
 
 
-def test_serving_run(fa):
+@pytest.mark.parametrize("most", [300, 20000])   # every key as an own one, and shared
+def test_serving_run(fa, most):
     """One prompt written once, then tokens of several samples of it: each step
     writes rotated keys and reads the shared blocks through
     fa_decode_paged_prefix; every step against attention in 64 bits over rotated
@@ -369,6 +382,7 @@ def test_serving_run(fa):
     own = (prompt + steps + 15) // 16 - whole
     perm = rng.permutation(whole + n * own + 2)
     table = np.int32([[*perm[:whole], *perm[whole + i * own: whole + (i + 1) * own]] for i in range(n)])
+    table = np.pad(table, ((0, 0), (0, max(0, most // 16 - table.shape[1]))), constant_values=-1)
     pools = [torch.zeros((len(perm), 16, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
     bf = lambda a: dev(a).to(torch.bfloat16)  # noqa: E731
     k0, v0 = (cr.bf16(rng, prompt, Hkv, d) for _ in "kv")
@@ -379,14 +393,14 @@ def test_serving_run(fa):
         pool[dev(table[1:, whole].astype(np.int64))] = pool[int(table[0, whole])].clone()
     keys = [[k0] for _ in range(n)]
     vals = [[v0] for _ in range(n)]
-    ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(n, H, Hkv, d, prompt, steps))
+    ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(n, H, Hkv, d, most, steps))
     for step in range(1, steps + 1):
         q, k, v = (cr.bf16(rng, n, h, d) for h in (H, Hkv, Hkv))
         ctx = dev(np.int32([prompt + step] * n))
         qr = fa.fa_cache_append_rope(bf(q), bf(k), bf(v), f, *pools, dev(table), ctx,
                                      dev(np.arange(n + 1, dtype=np.int32)), 1)
         out, lse = fa.fa_decode_paged_prefix(qr, *pools, dev(table), ctx, dev(np.int32([0, n])),
-                                             dev(np.int32([prompt])), prompt, steps, workspace=ws)
+                                             dev(np.int32([prompt])), most, steps, workspace=ws)
         for b in range(n):
             keys[b].append(k[b:b + 1]), vals[b].append(v[b:b + 1])
             kk = rr.rotate(np.concatenate(keys[b]), np.arange(prompt + step), freq)
