@@ -7,8 +7,7 @@
 // a row (rope_common.cuh) and walks through the rows with it.  Its pairs keep their
 // frequencies, so it forms cos and sin of its first row and of one step once
 // for all heads, and turns them on from row to row (2 packed multiplications a
-// pair; after at most 3 steps off by less than 2^-21, where bf16 and e4m3 keep
-// 2^-8 and 2^-4).
+// pair; off by less than 2^-20 in the end, where e4m3 keeps 2^-4).
 //
 // Scales and older codes are cache_append.cu's, with one difference: a key's
 // scale is taken from the block's values before the rotation, times the bound
@@ -135,15 +134,33 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   };
   int h = w;
   load(h);
-  // cos and sin of the lane's first row and of one step
+  // cos and sin of the lane's first row and of kRows rows: the lanes of a unit
+  // form those of the block's first row and of one row together, and each goes
+  // on from there by its own row number
   UnitAngles at_first{}, step{};
-  if (unit.turns && w < p.Hkv) {
-    uint64_t turns[8];
+  if (w < p.Hkv) {
+    float2 base[8 / kRows], one[8 / kRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      turns[i] = rope_turns(checked_load(rp.rope.inv_freq, u * 8 + i, rp.rope.pairs, p.status));
-    at_first.set([&](int i) { return turns[i]; }, pos0 + r, rp.rope.factor, false);
-    step.set([&](int i) { return turns[i]; }, kRows, 1.f, false);
+    for (int i = 0; i < 8 / kRows; ++i) {
+      const int pair = u * 8 + r * (8 / kRows) + i;
+      const uint64_t turns = rope_turns(
+          unit.turns ? checked_load(rp.rope.inv_freq, pair, rp.rope.pairs, p.status) : 0.0);
+      base[i] = rope_cos_sin(turns, pos0);
+      base[i] = make_float2(base[i].x * rp.rope.factor, base[i].y * rp.rope.factor);
+      one[i] = rope_cos_sin(turns, 1);
+    }
+    auto gather = [&](const float2 (&x)[8 / kRows], int i) {
+      const int from = i / (8 / kRows) * kLanes + u;
+      return make_float2(__shfl_sync(0xffffffffu, x[i % (8 / kRows)].x, from),
+                         __shfl_sync(0xffffffffu, x[i % (8 / kRows)].y, from));
+    };
+    at_first.set([&](int i) { return gather(base, i); });
+    step.set([&](int i) { return gather(one, i); });
+#pragma unroll
+    for (int bit = 1; bit < kRows; bit *= 2) {
+      if (r & bit) at_first.advance(step);
+      step.advance(UnitAngles(step));
+    }
   }
 
   for (;;) {

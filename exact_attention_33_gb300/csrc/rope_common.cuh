@@ -64,15 +64,14 @@ struct RopeUnit {
 struct UnitAngles {
   float2 c[4], s[4];
 
-  // of pairs [8 u, 8 u + 8) at position p, times `factor`
-  template <typename Frequency>
-  __device__ __forceinline__ void set(Frequency turns_of, int p, float factor, bool back) {
+  // of_pair(i): (cos, sin) of pair i
+  template <typename OfPair>
+  __device__ __forceinline__ void set(OfPair of_pair) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 x = rope_cos_sin(turns_of(2 * i), p), y = rope_cos_sin(turns_of(2 * i + 1), p);
-      c[i] = make_float2(x.x * factor, y.x * factor);
-      s[i] = make_float2(x.y * factor, y.y * factor);
-      if (back) s[i] = make_float2(-s[i].x, -s[i].y);
+      const float2 x = of_pair(2 * i), y = of_pair(2 * i + 1);
+      c[i] = make_float2(x.x, y.x);
+      s[i] = make_float2(x.y, y.y);
     }
   }
   // on by the angles of d

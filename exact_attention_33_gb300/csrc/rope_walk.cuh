@@ -33,7 +33,8 @@ __device__ __forceinline__ void rope_walk(const RopeParams &p, int cta) {
   const int tokens = kRopeThreads / (kUnits * p.head_lanes);  // of a CTA
   const long long mine =
       static_cast<long long>(cta) * tokens + threadIdx.x / (kUnits * p.head_lanes);
-  int t, pos;  // the row and its position
+  int t = 0, pos = 0;  // the row and its position
+  bool live = true;
   uint16_t *k_dst = nullptr, *v_dst = nullptr;
   if constexpr (PACKED) {
     const int b = blockIdx.y;
@@ -50,10 +51,13 @@ __device__ __forceinline__ void rope_walk(const RopeParams &p, int cta) {
       if (report) raise_status(p.status, FA_DEV_BAD_CTX);
       return;
     }
-    if (mine >= n) return;
-    t = start + static_cast<int>(mine);
-    pos = ctx - n + static_cast<int>(mine);
-    if constexpr (APPEND) {
+    if (static_cast<long long>(cta) * tokens >= n) return;  // the whole CTA
+    live = mine < n;
+    if (live) {
+      t = start + static_cast<int>(mine);
+      pos = ctx - n + static_cast<int>(mine);
+    }
+    if (APPEND && live) {
       const size_t at = static_cast<size_t>(b) * p.max_blocks_per_seq + pos / kDecodeBlock;
       const int phys = checked_load(p.block_table, at,
                                     static_cast<size_t>(p.batch) * p.max_blocks_per_seq, p.status);
@@ -67,8 +71,8 @@ __device__ __forceinline__ void rope_walk(const RopeParams &p, int cta) {
       }
     }
   } else {
-    if (mine >= p.total_tokens) return;
-    t = static_cast<int>(mine);
+    live = mine < p.total_tokens;
+    if (live) t = static_cast<int>(mine);
     pos = p.positions ? checked_load(p.positions, t, p.total_tokens, p.status) : t % p.seq_len;
   }
 
@@ -76,7 +80,7 @@ __device__ __forceinline__ void rope_walk(const RopeParams &p, int cta) {
   // block is bad keeps its queries.
   const int hq = p.q.src ? p.q.heads : 0;
   const int hk = MODE == kRopeQueries ? 0 : (APPEND ? k_dst : p.k.src) ? p.k.heads : 0;
-  const int heads = hq + hk + (APPEND ? hk : 0);
+  const int heads = live ? hq + hk + (APPEND ? hk : 0) : 0;
   const uint16_t *src_q = static_cast<const uint16_t *>(p.q.src) + t * p.q.src_stride;
   const uint16_t *src_k = static_cast<const uint16_t *>(p.k.src) + t * p.k.src_stride;
   const uint16_t *src_v = static_cast<const uint16_t *>(p.v.src) + t * p.v.src_stride;
@@ -115,10 +119,38 @@ __device__ __forceinline__ void rope_walk(const RopeParams &p, int cta) {
     }
   };
   load(hl);  // in flight while the angles are formed
-  if (unit.turns)
-    a.set([&](int i) {
-      return rope_turns(checked_load(p.rope.inv_freq, u * 8 + i, p.rope.pairs, p.status));
-    }, pos, p.rope.factor, BACK);
+  auto angle = [&](int i) {
+    const float2 cs = rope_cos_sin(
+        rope_turns(checked_load(p.rope.inv_freq, u * 8 + i, p.rope.pairs, p.status)), pos);
+    return make_float2(cs.x * p.rope.factor, (BACK ? -cs.y : cs.y) * p.rope.factor);
+  };
+  if (p.head_lanes == 1) {
+    if (unit.turns) a.set(angle);
+  } else {
+    // The threads of a unit form its angles together: cosines at [0, 8), sines
+    // at [8, 16) of a row of 20 floats (16-byte reads of 8 neighbouring rows
+    // then fall on different banks).
+    __shared__ __align__(16) float shared_angles[kRopeThreads / 2][20];
+    float *row = shared_angles[threadIdx.x / (kUnits * p.head_lanes) * kUnits + u];
+    if (unit.turns)
+      for (int i = hl; i < 8; i += p.head_lanes) {
+        const float2 cs = angle(i);
+        row[i] = cs.x;
+        row[8 + i] = cs.y;
+      }
+    __syncthreads();
+    if (unit.turns) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 c = *reinterpret_cast<const float4 *>(row + 4 * i);
+        const float4 s = *reinterpret_cast<const float4 *>(row + 8 + 4 * i);
+        a.c[2 * i] = make_float2(c.x, c.y);
+        a.c[2 * i + 1] = make_float2(c.z, c.w);
+        a.s[2 * i] = make_float2(s.x, s.y);
+        a.s[2 * i + 1] = make_float2(s.z, s.w);
+      }
+    }
+  }
   for (int h = hl; h < heads;) {
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
@@ -140,12 +172,15 @@ __device__ __forceinline__ void rope_walk(const RopeParams &p, int cta) {
   }
 }
 
-// Threads that share a unit's heads: more of them, up to one for each head,
-// until there are enough threads for the GPU.
+// Threads that share a unit's heads: as many as make kRopeWantThreads, and as
+// leave each no more than kRopeMostHeads.
+constexpr long long kRopeWantThreads = 128 * 1024;
+constexpr int kRopeMostHeads = 16;
 template <int D>
 inline int rope_head_lanes(long long rows, int heads) {
   int lanes = 1;
-  while (lanes * 2 * (D / 16) <= kRopeThreads && lanes < heads && rows * (D / 16) * lanes < 512 * 1024)
+  while (lanes * 2 * (D / 16) <= kRopeThreads && 2 * lanes <= heads &&
+         (rows * (D / 16) * lanes < kRopeWantThreads || heads > kRopeMostHeads * lanes))
     lanes *= 2;
   return lanes;
 }
