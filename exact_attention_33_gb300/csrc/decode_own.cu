@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(32)
     decode_own_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PrefixParams pp) {
   const DecodeParams &p = pp.own;
-  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.y, kvh = blockIdx.x, b = blockIdx.z;  // (heads read together)
   const int lane = threadIdx.x;
   pdl_launch_dependents();
   const bool first = split == 0 && kvh == 0 && b == 0;
@@ -86,7 +86,7 @@ cudaError_t launch_own_t(const CUtensorMap &tk, const CUtensorMap &tv, const Pre
                              cudaFuncAttributePreferredSharedMemoryCarveout,
                              cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.own.max_splits, p.own.Hkv, p.own.batch);
+  const dim3 grid(p.own.Hkv, p.own.max_splits, p.own.batch);
   if (!p.alone)
     return launch_dependent(decode_own_kernel<D, NT>, grid, dim3(32), L::kBytes, stream, tk, tv, p);
   decode_own_kernel<D, NT><<<grid, 32, L::kBytes, stream>>>(tk, tv, p);

@@ -64,13 +64,21 @@ bool lengths_ok(int max_prefix, int max_own) {
   return static_cast<long long>(max_prefix) + max_own <= kMaxCtxLen - kDecodeBlock;
 }
 
+// KV heads of a team: the most that divide Hkv and find CTAs.
+int team_heads(int Hkv) {
+  int h = std::min(Hkv, prefix_ctas());
+  while (Hkv % h != 0) --h;
+  return h;
+}
+
 // Partial states over shared keys.  A run of a CTA is at least one key tile,
-// and a CTA's share of the tiles at least the CTAs' part of one group's on all
-// KV heads, so a row meets at most CTAs / Hkv shares of it and two cut ones.
+// and a team's share of the line at least the teams' part of one group's tiles,
+// so a row meets at most as many shares of them as there are teams, and two cut
+// ones.
 PrefixWs prefix_ws(int batch, int H, int Hkv, int d, int max_prefix) {
   PrefixWs w;
   const int tiles = (max_prefix / kDecodeBlock * kDecodeBlock + kPrefixTileKeys - 1) / kPrefixTileKeys;
-  w.max_slots = std::max(1, std::min(tiles, prefix_ctas() / Hkv + 2));
+  w.max_slots = std::max(1, std::min(tiles, prefix_ctas() / team_heads(Hkv) + 2));
   const size_t rows = static_cast<size_t>(batch) * H * w.max_slots;
   w.o_bytes = round_up(rows * d * sizeof(float), 256);
   w.ml_bytes = round_up(rows * 4 * sizeof(float), 256);
@@ -200,6 +208,8 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   p.alone = alone;
   p.seqs_per_tile = seqs;
   p.ctas = prefix_ctas();
+  p.team_heads = team_heads(Hkv);
+  p.head_rounds = Hkv / p.team_heads;
   // Measured on one GB300.  A key tile of 128: 2.1 us with two row tiles of d =
   // 128 and 1.3 with one, 6 us before and after; the own keys' CTAs read 15 GB/s
   // each, 6 (d = 64: 13) on an SM of their own, one (d = 64: three) beside.

@@ -8,11 +8,10 @@
 // the running maximum and sums of the prefill kernel (prefill_kernel.cuh), and
 // no row has a causal limit of its own but its context length.
 //
-// prefix_kernel: one CTA per SM, persistent.  The work is a line of key tiles
-// (128 keys), group after group, KV head after KV head, pair of row tiles
-// after pair; a CTA takes an equal stretch of it, that is one or more runs of
-// key tiles over one pair of row tiles each, and leaves a partial state (m, l,
-// o) for every row and run.
+// prefix_kernel: one CTA per SM, persistent.  A CTA takes a KV head and a
+// stretch of the call's key tiles (128 keys; prefix_internal.h), that is one or
+// more runs of key tiles over one pair of row tiles each, and leaves a partial
+// state (m, l, o) for every row and run.
 //   warps 0-7  softmax, one row a thread, in two streams of four warps
 //   warp 8     MMA issuer: S_i = Q_i K^T, O_i += P_i V (tcgen05, TMEM)
 //   warp 9     TMA of Q (a box of sequences x heads) and, block by block, K
@@ -116,8 +115,9 @@ __global__ void __maxnreg__(kPrefixLaunchRegs)
   prefix_walk<kPrefixNone>(p, 0, blockIdx.x == 0 && warp == 0, g, &sums);
   const PrefixPlan plan = prefix_plan(p, sums);
   const int per = plan.per;
-  if (static_cast<long long>(blockIdx.x) * per >= plan.total) return;  // the whole CTA
-  int at = blockIdx.x * per;
+  const int team = blockIdx.x / p.team_heads;
+  if (static_cast<long long>(team) * per >= plan.total) return;  // the whole CTA
+  int at = team * per;
   const int stop = static_cast<int>(min(static_cast<long long>(plan.total),
                                         static_cast<long long>(at) + per));
 
@@ -131,10 +131,11 @@ __global__ void __maxnreg__(kPrefixLaunchRegs)
     const int unit = rel / g.tiles;
     j0 = rel - unit * g.tiles;
     n = min(g.tiles - j0, stop - at);
-    kvh = unit / g.pairs;
+    const int round = unit / g.pairs;
+    kvh = round * p.team_heads + blockIdx.x % p.team_heads;
     lead = g.a;
     whole = g.whole;
-    seq0 = g.a + (unit - kvh * g.pairs) * 2 * p.seqs_per_tile;
+    seq0 = g.a + (unit - round * g.pairs) * 2 * p.seqs_per_tile;
     rows0 = min(p.seqs_per_tile, g.e - seq0) * G;
     rows1 = max(0, min(p.seqs_per_tile, g.e - seq0 - p.seqs_per_tile)) * G;
     slot = at / per - (at - j0) / per;
@@ -631,8 +632,9 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
   for (int row = row0; row < row0 + rows; ++row) {
     int shared = 0;  // partial states over shared keys
     if (g.tiles > 0 && ctx > 0 && !p.alone) {
+      const int round = (row - b * o.H) / o.group / p.team_heads;
       const int first =
-          g.start + ((row - b * o.H) / o.group * g.pairs + (b - g.a) / (2 * p.seqs_per_tile)) * g.tiles;
+          g.start + (round * g.pairs + (b - g.a) / (2 * p.seqs_per_tile)) * g.tiles;
       shared = (first + g.tiles - 1) / per - first / per + 1;
     }
     const int ns = live ? own + shared : 0;

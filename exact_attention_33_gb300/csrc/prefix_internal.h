@@ -26,6 +26,7 @@ struct PrefixParams {
   int alone;                   // every key as a sequence's own (small calls)
   int seqs_per_tile;           // sequences whose group of heads fills a 128-row tile
   int ctas;                    // CTAs that share the prefix work at most (one an SM)
+  int team_heads, head_rounds; // KV heads that a team does at a time, and how often
   // What decides how many do: ns of a key tile with two row tiles and with one,
   // before and after them, and of the partial states that each CTA adds; bytes
   // a key (all KV heads); bytes a ns that the own keys' CTAs read at most, on an
@@ -37,9 +38,16 @@ struct PrefixParams {
   float4 *pml_part;            // [batch, H, max_slots]: m (log2 units), l, l_exact, 0
 };
 
+// The work is a line of key tiles, group after group and, in a group, pair of
+// row tiles after pair.  Teams of team_heads CTAs share it out in equal
+// stretches; a team's CTAs do the same stretch for a KV head each, so that the
+// heads of a token, which lie side by side in the pools, are read together.
+// (More KV heads than CTAs: a group's pairs come head_rounds times, with other
+// heads each time.)
+//
 // One group: its sequences [a, e), the keys of its shared blocks, and the work
-// of it: `pairs` CTA loads of query rows (two tiles) of each KV head, `tiles`
-// key tiles each; `start` key tiles lie before it in the call's line of them.
+// of it: `pairs` CTA loads of query rows (two tiles), `tiles` key tiles each;
+// `start` key tiles lie before it in the line.
 struct PrefixGroup {
   int a, e, whole, pairs, tiles;
   int start;
@@ -69,8 +77,8 @@ __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams &p, int g
   return r;
 }
 
-// The work of all groups, and how it is shared: CTA c takes key tiles [c per,
-// (c + 1) per) of `total`.  Groups that follow the rules make an int's worth of
+// The line's length, and how it is shared: team t takes key tiles [t per, (t +
+// 1) per) of `total`.  Groups that follow the rules make an int's worth of
 // work (the host looks); others may wrap, and what they write stays in bounds
 // all the same.
 struct PrefixPlan {
@@ -97,7 +105,7 @@ __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool
   if (sums) *sums = {0, 0.f, 0};
   for (int g0 = 0; g0 < p.num_groups && !(hit && !sums); g0 += 32) {
     PrefixGroup r = prefix_group(p, g0 + lane, report);
-    const int work = r.tiles * r.pairs * p.own.Hkv;
+    const int work = r.tiles * r.pairs * p.head_rounds;
     int incl = work;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -141,7 +149,7 @@ __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool
 // work computes, several on an SM that it leaves to them and some beside it, so it takes as many SMs as let both end together.
 __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const PrefixSums &s) {
   const int lane = threadIdx.x & 31;
-  if (s.total <= p.ctas) return {max(0, s.total), 1};
+  if (s.total <= p.ctas / p.team_heads) return {max(0, s.total), 1};
   float cost = s.cost;
   // keys of all sequences, from every `skip`-th of a large batch
   const int skip = (p.own.batch + 1023) / 1024;
@@ -156,8 +164,8 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const P
     shared = __fadd_rn(shared, __shfl_xor_sync(0xffffffffu, shared, o));
     keys += __shfl_xor_sync(0xffffffffu, keys, o);
   }
-  // lane l tries ctas - l ctas / 40 SMs
-  const int n = max(1, p.ctas - lane * p.ctas / 40);
+  // lane l tries whole teams of ctas - l ctas / 40 SMs
+  const int n = max(1, (p.ctas - lane * p.ctas / 40) / p.team_heads) * p.team_heads;
   const float own_bytes =
       __fmul_rn(fmaxf(0.f, __fadd_rn(static_cast<float>(keys), -shared)), p.key_bytes);
   const float rate =
@@ -168,9 +176,9 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const P
                             __fmul_rn(static_cast<float>(n), p.state_ns));
   const unsigned best = __reduce_min_sync(
       0xffffffffu, (static_cast<unsigned>(fminf(t, 1.3e8f)) << 5) | static_cast<unsigned>(lane));
-  const int ctas = __shfl_sync(0xffffffffu, n, best & 31);
+  const int teams = __shfl_sync(0xffffffffu, n / p.team_heads, best & 31);
   const int total = max(0, s.total);
-  return {total, max(1, (total + ctas - 1) / ctas)};
+  return {total, max(1, (total + teams - 1) / teams)};
 }
 
 // The first key that a sequence of a group reads on its own.
