@@ -10,8 +10,7 @@
 
 namespace fa {
 
-cudaError_t launch_prefix(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                          const PrefixParams &p, int d, cudaStream_t stream);
+cudaError_t launch_prefix(const PrefixMaps &m, const PrefixParams &p, int d, cudaStream_t stream);
 
 namespace {
 
@@ -101,6 +100,26 @@ int make_q_map(CUtensorMap *map, const void *q, int batch, int H, int group, int
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
+// A pool's tensor map for whole blocks of one KV head: 16 tokens' rows of d bf16
+// values go to shared memory as 128-byte swizzled rows, 8 tokens x 64 values at
+// a time, the 64-value chunks of 8 tokens one behind the other.  (One copy of 4
+// KB a block: what a copy costs the copy engine does not shrink with it.)
+int make_block_map(CUtensorMap *map, const void *pool, int d, int Hkv, long long tokens) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return FA_ERR_CUDA;
+  const cuuint64_t row = static_cast<cuuint64_t>(Hkv) * d * 2;
+  const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d / 64),
+                              static_cast<cuuint64_t>(tokens / 8), static_cast<cuuint64_t>(Hkv)};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(d) * 2};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d / 64), kDecodeBlock / 8, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(pool), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -171,11 +190,15 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   CallStatus *call = static_cast<CallStatus *>(workspace);
   uint8_t *parts = static_cast<uint8_t *>(workspace) + FA_WORKSPACE_HEADER_BYTES;
 
-  CUtensorMap tq, tk, tv;
+  PrefixMaps m{};
   const long long tokens = static_cast<long long>(num_blocks) * block_size;
-  int rc = make_q_map(&tq, q, batch, H, group, d, seqs);
-  if (rc == FA_OK) rc = make_pool_map(&tk, k_pool, d, Hkv, tokens);
-  if (rc == FA_OK) rc = make_pool_map(&tv, v_pool, d, Hkv, tokens);
+  int rc = make_pool_map(&m.k, k_pool, d, Hkv, tokens);
+  if (rc == FA_OK) rc = make_pool_map(&m.v, v_pool, d, Hkv, tokens);
+  if (!alone) {
+    if (rc == FA_OK) rc = make_q_map(&m.q, q, batch, H, group, d, seqs);
+    if (rc == FA_OK) rc = make_block_map(&m.k_tile, k_pool, d, Hkv, tokens);
+    if (rc == FA_OK) rc = make_block_map(&m.v_tile, v_pool, d, Hkv, tokens);
+  }
   if (rc != FA_OK) return rc;
 
   PrefixParams p{};
@@ -220,11 +243,10 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   p.key_bytes = 4.f * d * Hkv;
   p.max_rate = 5000.f;
   p.free_rate = 130.f;
-  p.beside_rate = d == 128 ? 5.f : 10.f;
   p.max_slots = s.max_slots;
   p.po_part = reinterpret_cast<float *>(parts + w.o_bytes + w.ml_bytes);
   p.pml_part = reinterpret_cast<float4 *>(parts + w.o_bytes + w.ml_bytes + s.o_bytes);
-  return launch_prefix(tq, tk, tv, p, d, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_prefix(m, p, d, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }

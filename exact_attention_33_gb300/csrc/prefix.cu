@@ -22,9 +22,8 @@
 // stream i takes the key tiles j0 + i, j0 + i + 2, ... of the same rows, and the
 // two states are merged as they leave TMEM.
 //
-// It takes less than the SM: the own keys' CTAs, launched as programmatic
-// dependents, run beside it (one on an SM with it, more as it ends) and read
-// their keys while it computes.
+// The own keys' CTAs, launched as programmatic dependents, run on the SMs that it
+// leaves to them (prefix_plan) and on its own as its CTAs end.
 //
 // prefix_combine_kernel: one, two or four warps per (sequence, query head) merge
 // the states of its own keys and of the shared ones, as decode_combine_kernel.
@@ -45,14 +44,7 @@ namespace fa {
 
 namespace {
 
-// 12 warps of 128 registers, so that the own keys' CTAs find registers too; the
-// softmax warps take some of the others' (256 * 168 + 128 * 48 = 384 * 128).
-constexpr int kPrefixThreads = 384;
-constexpr int kPrefixLaunchRegs = 128;
-constexpr int kPrefixSoftmaxRegs = 168;
-constexpr int kPrefixCtlRegs = 48;
-static_assert(256 * kPrefixSoftmaxRegs + 128 * kPrefixCtlRegs <= kPrefixThreads * kPrefixLaunchRegs,
-              "prefix register split exceeds the launch allocation");
+constexpr int kPrefixThreads = 352;
 constexpr float kPrefixRescaleLog2 = 8.f;  // as the prefill kernel's
 
 template <int D>
@@ -87,6 +79,16 @@ __device__ __forceinline__ bool named_bar_any(int id, int count, bool x) {
   return any != 0;
 }
 
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0,
+                                            int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "r"(c4)
+      : "memory");
+}
+
 // 8 floats to a 32-byte aligned address: a whole sector
 __device__ __forceinline__ void store8(float *to, const float (&v)[8]) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(v[0]),
@@ -97,7 +99,7 @@ __device__ __forceinline__ void store8(float *to, const float (&v)[8]) {
 }  // namespace
 
 template <int D>
-__global__ void __maxnreg__(kPrefixLaunchRegs)
+__global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
@@ -211,8 +213,6 @@ __global__ void __maxnreg__(kPrefixLaunchRegs)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 8) {
-  setmaxnreg_dec<kPrefixCtlRegs>();
   if (warp == 9 || warp == 10) {
     // ------------------------------------------------------ copies
     // Lanes 0..7 hold a tile's 8 block ids; the ids of 4 tiles come with one
@@ -221,7 +221,7 @@ __global__ void __maxnreg__(kPrefixLaunchRegs)
     // may be infinite, and 0 times that is NaN).
     constexpr int kTileBlocks = kPrefixTileKeys / kDecodeBlock;
     constexpr int kIdTiles = 32 / kTileBlocks;
-    constexpr int kBlockRows = kDecodeBlock * 128;  // bytes of a block in one chunk
+    constexpr int kBlockBytes = kDecodeBlock * D * 2;
     const bool is_k = warp == 9;
     const CUtensorMap *map = is_k ? &tm_k : &tm_v;
     uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
@@ -249,22 +249,21 @@ __global__ void __maxnreg__(kPrefixLaunchRegs)
         const int x = tiles + j, st = x % S;
         if (x >= S && !mbar_wait_warp(&empty[st], ((x / S) - 1) & 1, abort_flag, status)) return false;
         uint8_t *stage = stage0 + st * L::kTileBytes;
-        // lane = block * chunks + chunk issues that copy
-        const int id = __shfl_sync(0xffffffffu, cur,
-                                   (j % kIdTiles) * kTileBlocks + (lane / L::kChunks) % kTileBlocks);
-        uint8_t *dst = stage + (lane % L::kChunks) * L::kChunkBytes + lane / L::kChunks * kBlockRows;
-        const bool mine = lane < kTileBlocks * L::kChunks;
+        // lane = block issues that copy
+        const int id = __shfl_sync(0xffffffffu, cur, (j % kIdTiles) * kTileBlocks + lane % kTileBlocks);
+        uint8_t *dst = stage + lane * kBlockBytes;
+        const bool mine = lane < kTileBlocks;
         const unsigned live = __ballot_sync(0xffffffffu, mine && id >= 0);
         if (mine && id < 0) {
-          for (int t = 0; t < kBlockRows / 16; ++t)
+          for (int t = 0; t < kBlockBytes / 16; ++t)
             reinterpret_cast<uint4 *>(dst)[t] = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(live) * kBlockRows);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(live) * kBlockBytes);
         __syncwarp();
         if (mine && id >= 0)
-          tma_load_3d(dst, map, &full[st], (lane % L::kChunks) * 64, kvh, id * kDecodeBlock);
+          tma_load_5d(dst, map, &full[st], 0, 0, 0, id * (kDecodeBlock / 8), kvh);
         issued = x + 1;
         return true;
       };
@@ -300,11 +299,12 @@ __global__ void __maxnreg__(kPrefixLaunchRegs)
     auto issue_s = [&](int i, int tile, int st) {
       if (elect_one()) {
         const uint64_t a0 = sdesc_swz<128>(q_base + tile * L::kTileBytes, 16, 1024);
-        const uint64_t b0 = sdesc_swz<128>(k_base + st * L::kTileBytes, 16, 1024);
+        const uint64_t b0 = sdesc_swz<128>(k_base + st * L::kTileBytes, 16, L::kChunks * 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>((kk / 4 * L::kChunkBytes + kk % 4 * 32) >> 4);
-          mma_ss(tmem + i * 128, a0 + off, b0 + off, kIdescS, kk > 0 ? 1u : 0u);
+          const uint64_t a_off = static_cast<uint64_t>((kk / 4 * L::kChunkBytes + kk % 4 * 32) >> 4);
+          const uint64_t b_off = static_cast<uint64_t>((kk / 4 * 1024 + kk % 4 * 32) >> 4);
+          mma_ss(tmem + i * 128, a0 + a_off, b0 + b_off, kIdescS, kk > 0 ? 1u : 0u);
         }
         mma_commit(&s_full[i]);
       }
@@ -313,11 +313,11 @@ __global__ void __maxnreg__(kPrefixLaunchRegs)
     // O of stream i, its first or last key tile of the run
     auto issue_o = [&](int i, int st, bool first, bool last) {
       if (elect_one()) {
-        const uint64_t b0 = sdesc_swz<128>(v_base + st * L::kTileBytes, L::kChunkBytes, 1024);
+        const uint64_t b0 = sdesc_swz<128>(v_base + st * L::kTileBytes, 1024, L::kChunks * 1024);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + L::kTmemO + i * D, tmem + i * 128 + kk * 8,
-                 b0 + static_cast<uint64_t>((kk * 16 * 128) >> 4), kIdescO,
+                 b0 + static_cast<uint64_t>((kk * kDecodeBlock * D * 2) >> 4), kIdescO,
                  (!first || kk > 0) ? 1u : 0u);
         if (last) mma_commit(&o_done[i]);
       }
@@ -394,9 +394,7 @@ __global__ void __maxnreg__(kPrefixLaunchRegs)
     // everything issued must finish before TMEM is released
     mma_commit_elect(drain);
     mbar_drain(drain, 0, status);
-  }
   } else {
-    setmaxnreg_inc<kPrefixSoftmaxRegs>();
     // ------------------------------------------------------ softmax
     const int i = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -763,8 +761,7 @@ cudaError_t launch_decode_own(const CUtensorMap &tk, const CUtensorMap &tv, cons
                               int d, cudaStream_t stream);
 
 template <int D>
-static cudaError_t launch_prefix_d(const CUtensorMap &tq, const CUtensorMap &tk,
-                                   const CUtensorMap &tv, const PrefixParams &p,
+static cudaError_t launch_prefix_d(const PrefixMaps &m, const PrefixParams &p,
                                    cudaStream_t stream) {
   using L = PrefixLayout<D>;
   static std::atomic<unsigned long long> smem_set{0};
@@ -775,10 +772,10 @@ static cudaError_t launch_prefix_d(const CUtensorMap &tq, const CUtensorMap &tk,
                              cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   if (!p.alone) {
-    prefix_kernel<D><<<p.ctas, kPrefixThreads, L::kBytes, stream>>>(tq, tk, tv, p);
+    prefix_kernel<D><<<p.ctas, kPrefixThreads, L::kBytes, stream>>>(m.q, m.k_tile, m.v_tile, p);
     e = cudaGetLastError();
   }
-  if (e == cudaSuccess) e = launch_decode_own(tk, tv, p, D, stream);
+  if (e == cudaSuccess) e = launch_decode_own(m.k, m.v, p, D, stream);
   if (e != cudaSuccess) return e;
   // as many warps a row, and then as few rows a warp, as the GPU holds at once
   const int rows = p.own.batch * p.own.H, ctas = p.ctas * kPrefixCombineCtas;
@@ -796,10 +793,8 @@ static cudaError_t launch_prefix_d(const CUtensorMap &tq, const CUtensorMap &tk,
                           each);
 }
 
-cudaError_t launch_prefix(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                          const PrefixParams &p, int d, cudaStream_t stream) {
-  return d == 64 ? launch_prefix_d<64>(tq, tk, tv, p, stream)
-                 : launch_prefix_d<128>(tq, tk, tv, p, stream);
+cudaError_t launch_prefix(const PrefixMaps &m, const PrefixParams &p, int d, cudaStream_t stream) {
+  return d == 64 ? launch_prefix_d<64>(m, p, stream) : launch_prefix_d<128>(m, p, stream);
 }
 
 }  // namespace fa

@@ -29,13 +29,19 @@ struct PrefixParams {
   int team_heads, head_rounds; // KV heads that a team does at a time, and how often
   // What decides how many do: ns of a key tile with two row tiles and with one,
   // before and after them, and of the partial states that each CTA adds; bytes
-  // a key (all KV heads); bytes a ns that the own keys' CTAs read at most, on an
-  // SM of their own and beside this work.
+  // a key (all KV heads); bytes a ns that the own keys' CTAs read at most, and on
+  // an SM that is left to them.
   float tile_ns2, tile_ns1, fixed_ns, state_ns;
-  float key_bytes, max_rate, free_rate, beside_rate;
+  float key_bytes, max_rate, free_rate;
   int max_slots;               // partial states of a row over shared keys
   float *po_part;              // fp32 [batch, H, max_slots, d]
   float4 *pml_part;            // [batch, H, max_slots]: m (log2 units), l, l_exact, 0
+};
+
+// The maps of Q, of the pools as the own keys' kernel copies them (a block's
+// tokens x 64 values) and as the shared keys' one does (a block's whole rows).
+struct PrefixMaps {
+  CUtensorMap q, k, v, k_tile, v_tile;
 };
 
 // The work is a line of key tiles, group after group and, in a group, pair of
@@ -168,11 +174,13 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const P
   const int n = max(1, (p.ctas - lane * p.ctas / 40) / p.team_heads) * p.team_heads;
   const float own_bytes =
       __fmul_rn(fmaxf(0.f, __fadd_rn(static_cast<float>(keys), -shared)), p.key_bytes);
-  const float rate =
-      fminf(p.max_rate, __fadd_rn(__fmul_rn(static_cast<float>(p.ctas - n), p.free_rate),
-                                  __fmul_rn(static_cast<float>(n), p.beside_rate)));
-  const float t = __fadd_rn(fmaxf(__fadd_rn(p.fixed_ns, __fdiv_rn(cost, static_cast<float>(n))),
-                                  __fdiv_rn(own_bytes, rate)),
+  // (without an SM of their own they come after this work)
+  const float rate = fminf(p.max_rate, __fmul_rn(static_cast<float>(p.ctas - n), p.free_rate));
+  const float mine = __fadd_rn(p.fixed_ns, __fdiv_rn(cost, static_cast<float>(n)));
+  const float all = __fdiv_rn(own_bytes, p.max_rate);
+  // what they have not read by the end of this work they read on every SM
+  const float rest = fmaxf(0.f, __fadd_rn(own_bytes, -__fmul_rn(rate, mine)));
+  const float t = __fadd_rn(fmaxf(all, __fadd_rn(mine, __fdiv_rn(rest, p.max_rate))),
                             __fmul_rn(static_cast<float>(n), p.state_ns));
   const unsigned best = __reduce_min_sync(
       0xffffffffu, (static_cast<unsigned>(fminf(t, 1.3e8f)) << 5) | static_cast<unsigned>(lane));
