@@ -3,11 +3,12 @@
 //
 // The first CTAs of a sequence rotate its queries as rope.cu does.  In the
 // others a warp takes a block of the sequence's new tokens (16 at most) and
-// some of its heads, K's or V's, one after the other.  A lane owns one unit of
-// a row (rope_common.cuh) and walks through the rows with it.  Its pairs keep their
-// frequencies, so it forms cos and sin of its first row and of one step once
-// for all heads, and turns them on from row to row (2 packed multiplications a
-// pair; off by less than 2^-20 in the end, where e4m3 keeps 2^-4).
+// some of its heads, K's or V's, one after the other; a lane owns one unit of a
+// row (rope_common.cuh) and walks through the rows with it.  The warps of a
+// block form cos and sin of its 16 positions together, in shared memory, and
+// read them for every head.  (Angles in registers, turned on from row to row by
+// the angle of a step, take 48 registers more: 144 us for 34.8 k tokens of 32 / 8
+// heads of d = 128 where this takes 131, and they are off by 2^-21.)
 //
 // Scales and older codes are cache_append.cu's, with one difference: a key's
 // scale is taken from the block's values before the rotation, times the bound
@@ -30,6 +31,7 @@ namespace fa {
 namespace {
 
 constexpr int kAppendWarps = kRopeThreads / 32;
+constexpr int kMaxCtaBlocks = 4;
 constexpr int kMinScaleExp = -100;
 
 // Smallest e >= kMinScaleExp with x <= 448 * 2^e (x >= 0, fp32; 2^120 for what
@@ -62,9 +64,9 @@ __device__ __forceinline__ uint2 encode8(const float2 *v, float scale, float inv
 }  // namespace
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 2)
+__global__ void __launch_bounds__(kRopeThreads, 3)
     cache_append_rope_kernel(const AppendParams p, const RopeParams rp, const float grow,
-                             const int q_ctas, const int block_warps) {
+                             const int q_ctas, const int block_warps, const int cta_blocks) {
   if (static_cast<int>(blockIdx.x) < q_ctas) {
     rope_walk<D, INTER, false, kRopeQueries>(rp, blockIdx.x);
     return;
@@ -74,11 +76,15 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   constexpr int kIter = kDecodeBlock / kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y;
-  // warp w of the nth block takes heads w, w + block_warps, ... of K's and V's
-  const long long id = static_cast<long long>(blockIdx.x - q_ctas) * kAppendWarps + warp;
-  const int nth = static_cast<int>(id / block_warps);
-  const int w = static_cast<int>(id % block_warps);
-  const bool report = id == 0 && lane == 0;
+  // A CTA takes cta_blocks blocks with equally many warps each, its part of the
+  // block_warps that share a block's heads: warp w of them heads w, w +
+  // block_warps, ... of K's and V's.
+  const int cta = blockIdx.x - q_ctas, warps = kAppendWarps / cta_blocks;
+  const int parts = (block_warps + warps - 1) / warps;  // CTAs of a block
+  const int mine = warp / warps;                        // block of the CTA
+  const int nth = cta / parts * cta_blocks + mine;
+  const int w = cta % parts * warps + warp % warps;
+  const bool report = cta == 0 && warp == 0 && lane == 0;
 
   const int start = checked_load(p.cu_seqlens, b, p.batch + 1, p.status);
   const int end = checked_load(p.cu_seqlens, b + 1, p.batch + 1, p.status);
@@ -94,17 +100,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
   }
   const int first = ctx - n;  // position of the first new token
   const int blk = first / kDecodeBlock + nth;
-  if (n == 0 || blk > (ctx - 1) / kDecodeBlock) return;
   const int pos0 = blk * kDecodeBlock;
+  if (n == 0 || blk - mine > (ctx - 1) / kDecodeBlock) return;  // the whole CTA
+  const bool active = blk <= (ctx - 1) / kDecodeBlock && w < block_warps;
   const int s0 = max(0, first - pos0), s1 = min(kDecodeBlock, ctx - pos0);  // new slots
   const int row0 = start + pos0 - first;  // the token of slot 0 (may lie before the new ones)
-  const int phys = checked_load(p.block_table, static_cast<size_t>(b) * p.max_blocks_per_seq + blk,
-                                static_cast<size_t>(p.batch) * p.max_blocks_per_seq, p.status);
-  if (phys < 0 || phys >= p.num_blocks) {
-    if (w == 0 && lane == 0) raise_status(p.status, FA_DEV_BAD_BLOCK);
-    return;
-  }
-
   const int u = lane % kLanes, r = lane / kLanes;
   const RopeUnit unit(u, rp.rope.pairs, INTER);
   const int heads = 2 * p.Hkv;
@@ -133,45 +133,51 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     }
   };
   int h = w;
-  load(h);
-  // cos and sin of the lane's first row and of kRows rows: the lanes of a unit
-  // form those of the block's first row and of one row together, and each goes
-  // on from there by its own row number
-  UnitAngles at_first{}, step{};
-  if (w < p.Hkv) {
-    float2 base[8 / kRows], one[8 / kRows];
-#pragma unroll
-    for (int i = 0; i < 8 / kRows; ++i) {
-      const int pair = u * 8 + r * (8 / kRows) + i;
-      const uint64_t turns = rope_turns(
-          unit.turns ? checked_load(rp.rope.inv_freq, pair, rp.rope.pairs, p.status) : 0.0);
-      base[i] = rope_cos_sin(turns, pos0);
-      base[i] = make_float2(base[i].x * rp.rope.factor, base[i].y * rp.rope.factor);
-      one[i] = rope_cos_sin(turns, 1);
-    }
-    auto gather = [&](const float2 (&x)[8 / kRows], int i) {
-      const int from = i / (8 / kRows) * kLanes + u;
-      return make_float2(__shfl_sync(0xffffffffu, x[i % (8 / kRows)].x, from),
-                         __shfl_sync(0xffffffffu, x[i % (8 / kRows)].y, from));
-    };
-    at_first.set([&](int i) { return gather(base, i); });
-    step.set([&](int i) { return gather(one, i); });
-#pragma unroll
-    for (int bit = 1; bit < kRows; bit *= 2) {
-      if (r & bit) at_first.advance(step);
-      step.advance(UnitAngles(step));
-    }
+  if (active) load(h);  // in flight while the angles are formed
+  // cos and sin of pair 8 u + i of row r of the CTA's blocks: floats i and 8 + i
+  // of the 16 of (block, r, u), of which the 16-byte quarter q lies at q ^ (u / 2)
+  // % 4 (so that 8 units' quarters fall on different banks)
+  __shared__ __align__(16) float angles[kMaxCtaBlocks * kDecodeBlock * kLanes * 16];
+  auto place = [&](int row, int unit, int i) {
+    return ((row * kLanes + unit) * 4 + ((i / 4) ^ ((unit / 2) & 3))) * 4 + i % 4;
+  };
+  const int base = pos0 - mine * kDecodeBlock;  // position of the CTA's first row
+  const int rows = min(cta_blocks * kDecodeBlock, ctx - base);
+  for (int x = threadIdx.x + max(0, first - base) * rp.rope.pairs; x < rows * rp.rope.pairs;
+       x += kRopeThreads) {
+    const int pair = x % rp.rope.pairs, row = x / rp.rope.pairs;
+    const float2 cs = rope_cos_sin(
+        rope_turns(checked_load(rp.rope.inv_freq, pair, rp.rope.pairs, p.status)), base + row);
+    angles[place(row, pair / 8, pair % 8)] = cs.x * rp.rope.factor;
+    angles[place(row, pair / 8, 8 + pair % 8)] = cs.y * rp.rope.factor;
+  }
+  __syncthreads();
+  if (!active) return;
+  const int phys = checked_load(p.block_table, static_cast<size_t>(b) * p.max_blocks_per_seq + blk,
+                                static_cast<size_t>(p.batch) * p.max_blocks_per_seq, p.status);
+  if (phys < 0 || phys >= p.num_blocks) {
+    if (w == 0 && lane == 0) raise_status(p.status, FA_DEV_BAD_BLOCK);
+    return;
   }
 
   for (;;) {
     const bool is_v = h >= p.Hkv;
     const bool turned = !is_v && unit.turns;
     // the rows of this head, in fp32, one after the other
-    UnitAngles a = at_first;
     auto row = [&](int i, float2 (&v)[8]) {
       if (turned) {
+        UnitAngles a;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int at = mine * kDecodeBlock + i * kRows + r;
+          const float4 c = *reinterpret_cast<const float4 *>(&angles[place(at, u, 4 * q)]);
+          const float4 s = *reinterpret_cast<const float4 *>(&angles[place(at, u, 8 + 4 * q)]);
+          a.c[2 * q] = make_float2(c.x, c.y);
+          a.c[2 * q + 1] = make_float2(c.z, c.w);
+          a.s[2 * q] = make_float2(s.x, s.y);
+          a.s[2 * q + 1] = make_float2(s.z, s.w);
+        }
         rotate_unit<INTER>(a, x[i], y[i], v);
-        if (i + 1 < kIter) a.advance(step);
       } else {
         const uint32_t word[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
 #pragma unroll
@@ -254,15 +260,20 @@ cudaError_t launch_append_t(const AppendParams &p, RopeParams rp, float grow, cu
   }
   // the new tokens of a sequence may begin inside a block
   const long long blocks = (p.max_new + 2LL * kDecodeBlock - 2) / kDecodeBlock;
-  // a warp takes up to 4 heads of its block, for whom it forms the angles once,
-  // where that leaves two rounds of warps for the GPU
+  // a warp takes two heads of its block where that leaves two rounds of warps for
+  // the GPU (34.8 k tokens of 32 / 8 heads of d = 128: 131 us; four heads 137,
+  // eight 149; with 2 CTAs on an SM instead of 3, 148, with 4, 164)
   const long long rounds = blocks * p.batch * 2 * p.Hkv / (2LL * 152 * 16);
-  const int per_warp = static_cast<int>(std::min(4LL, std::max(1LL, rounds)));
+  const int per_warp = static_cast<int>(std::min(2LL, std::max(1LL, rounds)));
   const int block_warps = (2 * p.Hkv + per_warp - 1) / per_warp;
-  const dim3 grid(static_cast<unsigned>(q_ctas + (blocks * block_warps + kAppendWarps - 1) / kAppendWarps),
+  // 2, 4 or 8 warps of a CTA for a block
+  int warps = 2;
+  while (warps < kAppendWarps && warps < block_warps) warps *= 2;
+  const int cta_blocks = kAppendWarps / warps, parts = (block_warps + warps - 1) / warps;
+  const dim3 grid(static_cast<unsigned>(q_ctas + (blocks + cta_blocks - 1) / cta_blocks * parts),
                   static_cast<unsigned>(p.batch));
   cache_append_rope_kernel<D, INTER>
-      <<<grid, kRopeThreads, 0, stream>>>(p, rp, grow, q_ctas, block_warps);
+      <<<grid, kRopeThreads, 0, stream>>>(p, rp, grow, q_ctas, block_warps, cta_blocks);
   return cudaGetLastError();
 }
 

@@ -1,10 +1,10 @@
 // decode_own.cu - the keys that a sequence has for itself behind a shared
 // prefix: decode.cu's split kernel from the prefix on.
 //
-// Launched behind prefix.cu's kernel as its programmatic dependent, which computes
-// while this one reads: its CTAs start once that kernel's have, one on each SM
-// beside them and more as they end.  The combine waits for this grid alone, so
-// its first CTA waits for that kernel.
+// Launched behind prefix.cu's kernel as its programmatic dependent: its CTAs start
+// once that kernel's have, on the SMs that are left, and on the others as they
+// end.  The combine waits for this grid alone, so its first CTA waits for that
+// kernel.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -23,7 +23,7 @@ namespace fa {
 
 // Blocks in a warp's ring.  A warp takes 0.6 us for a block that is there, so
 // what counts is warps: rings of two blocks let twice as many of them run as
-// decode.cu's of four, on an SM and beside the shared keys' kernel.
+// decode.cu's of four.
 constexpr int kOwnStages = 2;
 
 // One warp per (sequence, KV head, split of keys [whole, ctx)).
@@ -32,9 +32,12 @@ __global__ void __launch_bounds__(32)
     decode_own_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const PrefixParams pp) {
   const DecodeParams &p = pp.own;
-  const int split = blockIdx.y, kvh = blockIdx.x, b = blockIdx.z;  // (heads read together)
+  // the KV heads of a split side by side: their rows lie so in the pools
+  const int split = blockIdx.x / p.Hkv, kvh = blockIdx.x - split * p.Hkv, b = blockIdx.y;
   const int lane = threadIdx.x;
   pdl_launch_dependents();
+  // (a loose max_own_len makes many CTAs without keys: most leave here)
+  if (split > 0 && split * p.split_tokens >= checked_load(p.ctx_lens, b, p.batch, p.status)) return;
   const bool first = split == 0 && kvh == 0 && b == 0;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {
@@ -64,8 +67,8 @@ __global__ void __launch_bounds__(32)
   }
   const size_t part_row = static_cast<size_t>(b) * p.H + static_cast<size_t>(kvh) * p.group;
   WarpRange<D, NT> st;
-  const int rc = decode_range<D, NT, false, kOwnStages>(tm_k, tm_v, p, b, kvh, t0, t1, my_blk, smem, st,
-                                            WindowBlocks(ctx, 0, 0), ctx);
+  const int rc = decode_range<D, NT, false, kOwnStages>(tm_k, tm_v, p, b, kvh, t0, t1, my_blk, smem,
+                                                        st, WindowBlocks(ctx, 0, 0), ctx);
   if (rc == kRangeBadBlock) store_neutral<D>(p, part_row, split);
   if (rc == kRangeOk) store_range<D, NT>(p, part_row, split, st);
   if (first) pdl_wait_primary();
@@ -78,15 +81,9 @@ cudaError_t launch_own_t(const CUtensorMap &tk, const CUtensorMap &tv, const Pre
                          cudaStream_t stream) {
   using L = DecodeLayout<D, kOwnStages>;
   static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t e = allow_smem(decode_own_kernel<D, NT>, L::kBytes, smem_set);
-  // An SM changes its share of shared memory only while it is empty: both
-  // kernels ask for all of it, or this one's CTAs wait for the other's to end.
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(decode_own_kernel<D, NT>,
-                             cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
+  const cudaError_t e = allow_smem(decode_own_kernel<D, NT>, L::kBytes, smem_set);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.own.Hkv, p.own.max_splits, p.own.batch);
+  const dim3 grid(static_cast<unsigned>(p.own.max_splits) * p.own.Hkv, p.own.batch);
   if (!p.alone)
     return launch_dependent(decode_own_kernel<D, NT>, grid, dim3(32), L::kBytes, stream, tk, tv, p);
   decode_own_kernel<D, NT><<<grid, 32, L::kBytes, stream>>>(tk, tv, p);

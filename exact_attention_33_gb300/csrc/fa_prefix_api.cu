@@ -30,7 +30,8 @@ constexpr long long kAloneBytes = 64LL << 20;
 int longest(int max_prefix, int max_own) { return max_prefix + max_own + kDecodeBlock - 1; }
 
 bool prefix_alone(int batch, int Hkv, int d, int max_prefix, int max_own) {
-  return static_cast<long long>(batch) * longest(max_prefix, max_own) * Hkv * d * 4 <= kAloneBytes;
+  return static_cast<long long>(batch) * longest(max_prefix, max_own) <=
+         kAloneBytes / (4LL * Hkv * d);
 }
 
 // Bytes of the partial states that such calls of at most this batch and these
@@ -183,6 +184,7 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
       alone ? static_cast<int>(std::min<long long>(reach, longest(max_prefix_len, max_own_len)))
             : max_own,
       kOwnItems);
+  if (static_cast<long long>(w.max_splits) * Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const PrefixWs s = alone ? PrefixWs{1, 0, 0} : prefix_ws(batch, H, Hkv, d, max_prefix_len);
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < FA_WORKSPACE_HEADER_BYTES + w.o_bytes + w.ml_bytes + s.bytes())

@@ -173,7 +173,7 @@ int fa_cache_append_rope_fp8(const void *q, const void *k, const void *v, int64_
                            d, block_size, num_blocks, run);
   if (rc != FA_OK || !run) return rc;
   max_new = std::min(max_new, total_tokens);
-  if ((max_new / kDecodeBlock + 2LL) * Hkv * 2 + max_new > 0x7fffffffLL)
+  if ((max_new / kDecodeBlock + 6LL) * (Hkv * 2 + 8) + max_new > 0x7fffffffLL)
     return FA_ERR_UNSUPPORTED;
   // what a rotated key may grow by
   const float grow = std::max(1.f, static_cast<float>(1.4142135623730951 * factor));

@@ -766,10 +766,6 @@ static cudaError_t launch_prefix_d(const PrefixMaps &m, const PrefixParams &p,
   using L = PrefixLayout<D>;
   static std::atomic<unsigned long long> smem_set{0};
   cudaError_t e = allow_smem(prefix_kernel<D>, L::kBytes, smem_set);
-  // (the own keys' kernel wants the same, see there)
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(prefix_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   if (!p.alone) {
     prefix_kernel<D><<<p.ctas, kPrefixThreads, L::kBytes, stream>>>(m.q, m.k_tile, m.v_tile, p);

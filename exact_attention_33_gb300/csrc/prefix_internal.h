@@ -84,9 +84,8 @@ __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams &p, int g
 }
 
 // The line's length, and how it is shared: team t takes key tiles [t per, (t +
-// 1) per) of `total`.  Groups that follow the rules make an int's worth of
-// work (the host looks); others may wrap, and what they write stays in bounds
-// all the same.
+// 1) per) of `total`.  (Whatever the arrays hold, it is an int: the host sees to
+// that.)
 struct PrefixPlan {
   int total, per;
 };
@@ -152,7 +151,10 @@ __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool
 
 // The plan of a call, the same in every warp that asks (integers, and fp32
 // operations that no compiler contracts).  The own keys' CTAs read while this
-// work computes, several on an SM that it leaves to them and some beside it, so it takes as many SMs as let both end together.
+// work computes, on the SMs that it leaves to them and then on all of them; it
+// takes as many as let both end first.  (64 sequences over 8192 keys, 300 to
+// 1000 of their own: 64 SMs 42 us, 86 SMs 46, 128 SMs 47; 256 over 16384 keys:
+// 120 SMs 107 us, 152 SMs 124.)
 __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const PrefixSums &s) {
   const int lane = threadIdx.x & 31;
   if (s.total <= p.ctas / p.team_heads) return {max(0, s.total), 1};

@@ -38,13 +38,18 @@ __device__ __forceinline__ uint64_t rope_turns(double inv_freq) {
   return bits >> 63 ? 0 - t : t;
 }
 
-// cos and sin of p positions' turns.
+// cos and sin of p positions' turns: the nearest quarter of a turn by signs and
+// places, the rest, at most an eighth either way, as a float (2^-27 of a turn).
 __device__ __forceinline__ float2 rope_cos_sin(uint64_t turns, int p) {
   const uint64_t a = turns * static_cast<uint64_t>(static_cast<int64_t>(p));
+  const uint32_t hi = static_cast<uint32_t>(a >> 32);  // 2^32 of a turn
+  const uint32_t quarter = (hi + 0x20000000u) >> 30;
   float s, c;
-  // (as a signed fraction: half a turn either way, in units of half a turn)
-  sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f, &s, &c);
-  return make_float2(c, s);
+  // (in units of half a turn)
+  sincospif(static_cast<float>(static_cast<int32_t>(hi - (quarter << 30))) * 4.656612873077393e-10f,
+            &s, &c);
+  const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
+  return make_float2((quarter + 1u) & 2u ? -x : x, quarter & 2u ? -y : y);
 }
 
 // A head row of D values is D / 16 units of two 16-byte pieces: 8 pairs (half
@@ -72,16 +77,6 @@ struct UnitAngles {
       const float2 x = of_pair(2 * i), y = of_pair(2 * i + 1);
       c[i] = make_float2(x.x, y.x);
       s[i] = make_float2(x.y, y.y);
-    }
-  }
-  // on by the angles of d
-  __device__ __forceinline__ void advance(const UnitAngles &d) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 ns = make_float2(-s[i].x, -s[i].y);
-      const float2 x = ffma2(c[i], d.c[i], fmul2(ns, d.s[i]));
-      s[i] = ffma2(c[i], d.s[i], fmul2(s[i], d.c[i]));
-      c[i] = x;
     }
   }
 };
