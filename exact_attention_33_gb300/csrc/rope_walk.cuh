@@ -173,7 +173,10 @@ __device__ __forceinline__ void rope_walk(const RopeParams &p, int cta) {
 }
 
 // Threads that share a unit's heads: as many as make kRopeWantThreads, and as
-// leave each no more than kRopeMostHeads.
+// leave each no more than kRopeMostHeads.  (A thread to itself for all heads
+// forms its angles once and leaves few, long CTAs: 73 k tokens of 16 / 4 heads, two
+// calls, 230 us against 227, 34.8 k of 32 / 8 heads into a cache 133 against 130; with
+// too few threads 20 k tokens of 5 heads took 50 us instead of 21.)
 constexpr long long kRopeWantThreads = 128 * 1024;
 constexpr int kRopeMostHeads = 16;
 template <int D>

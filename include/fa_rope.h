@@ -16,7 +16,7 @@
  *              is in these values and in factor.
  *   factor   : finite and > 0 (1, or what a stretched context wants)
  * The angle is the exact product, reduced to one turn in 64-bit integers
- * (turns a position are held to 2^-53 of themselves): a position of 2^31 costs
+ * (turns a position are held to 2^-53 of themselves or 2^-64): a position of 2^31 costs
  * no accuracy that bf16 values show.  Values are rotated in fp32 and rounded
  * once.
  *
