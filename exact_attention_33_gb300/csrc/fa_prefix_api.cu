@@ -235,17 +235,22 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   p.ctas = prefix_ctas();
   p.team_heads = team_heads(Hkv);
   p.head_rounds = Hkv / p.team_heads;
-  // Measured on one GB300: a key tile of 128 with two row tiles and with one, what
-  // a CTA takes before the first and after the last, what its states cost the
-  // combine; the own keys' CTAs read 130 GB/s on an SM that is left to them and
-  // 5 TB/s together.
-  p.tile_ns2 = d == 128 ? 2200.f : 1500.f;
-  p.tile_ns1 = d == 128 ? 1300.f : 900.f;
-  p.fixed_ns = 6000.f;
-  p.state_ns = d == 128 ? 50.f : 25.f;
-  p.key_bytes = 4.f * d * Hkv;
-  p.max_rate = 5000.f;
-  p.free_rate = 130.f;
+  p.teams = p.ctas / p.team_heads;
+  // Measured on one GB300 (d = 128): a key tile of 128 with two row tiles and with
+  // one, what a CTA takes before its first product and after its last and between
+  // two runs, what one more CTA costs the others (states, loads that contend); the
+  // own keys' CTAs read 62 GB/s on an SM that is left to them while the others
+  // work, and all reads come to 5.6 TB/s at most.  (4 groups over 15 k to 29 k keys: 110
+  // us, with 1400 instead of 1000 for a single row tile 114.)
+  p.tile_ns2 = d == 128 ? 1650.f : 1100.f;
+  p.tile_ns1 = d == 128 ? 1000.f : 650.f;
+  p.fixed_ns = 14500.f;
+  p.run_ns = 8000.f;
+  p.state_ns = d == 128 ? 150.f : 75.f;
+  p.block_bytes = 4.f * kDecodeBlock * d * Hkv;
+  p.max_rate = 5600.f;
+  p.max_rate_inv = 1.f / p.max_rate;
+  p.free_rate = 62.f;
   p.max_slots = s.max_slots;
   p.po_part = reinterpret_cast<float *>(parts + w.o_bytes + w.ml_bytes);
   p.pml_part = reinterpret_cast<float4 *>(parts + w.o_bytes + w.ml_bytes + s.o_bytes);

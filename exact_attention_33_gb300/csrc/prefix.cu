@@ -69,7 +69,8 @@ struct PrefixLayout {
   // q_full, q_free, drain, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_done[2]
   static constexpr int kNumBars = 3 + 4 * kStages + 6;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kBytes = kMisc + 16;
+  static constexpr int kSave = kMisc + 16;  // 12 ints for each of 8 softmax warps
+  static constexpr int kBytes = kSave + 8 * 12 * 4;
   static constexpr int kTmemO = 256;
 };
 
@@ -122,34 +123,37 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   // ---------------------------------------------------------------- work
   PrefixSums sums;
   PrefixGroup g{};
+  const PrefixFirst first = prefix_first(p);
   prefix_walk<kPrefixNone>(p, 0, blockIdx.x == 0 && warp == 0, g, &sums);
-  const PrefixPlan plan = prefix_plan(p, sums);
-  const int per = plan.per;
-  const int team = blockIdx.x / p.team_heads;
-  if (static_cast<long long>(team) * per >= plan.total) return;  // the whole CTA
-  int at = team * per;
-  const int stop = static_cast<int>(min(static_cast<long long>(plan.total),
-                                        static_cast<long long>(at) + per));
+  const PrefixPlan plan = prefix_plan(p, sums, first);
+  const int my_team = blockIdx.x / p.team_heads;
+  if (static_cast<long long>(my_team) * plan.per >= plan.total) return;  // the whole CTA
+  int at = my_team * plan.per;
+  int stop = static_cast<int>(min(static_cast<long long>(plan.total),
+                                  static_cast<long long>(at) + plan.per));
 
   // A run: key tiles [j0, j0 + n) of KV head kvh for the row tiles of the
   // sequences from seq0 on; rows0 and rows1 of the two belong to the group.
   int kvh, j0, n, seq0, slot, lead, whole;
   int rows0, rows1;
-  auto load_run = [&]() {
-    prefix_walk<kPrefixByTile>(p, at, false, g, nullptr);
+  auto load_run = [&](int team, int per, bool apart) {
+    prefix_walk<kPrefixByTile>(p, at, false, g, nullptr, apart ? per : 0);
     const int rel = at - g.start;
-    const int unit = rel / g.tiles;
-    j0 = rel - unit * g.tiles;
+    const int unit = rel / g.span;
+    j0 = rel - unit * g.span;
     n = min(g.tiles - j0, stop - at);
-    const int round = unit / g.pairs;
-    kvh = round * p.team_heads + blockIdx.x % p.team_heads;
+    const int round = p.head_rounds > 1 ? unit / g.pairs : 0;
+    kvh = round * p.team_heads + blockIdx.x - team * p.team_heads;
     lead = g.a;
     whole = g.whole;
     seq0 = g.a + (unit - round * g.pairs) * 2 * p.seqs_per_tile;
     rows0 = min(p.seqs_per_tile, g.e - seq0) * G;
     rows1 = max(0, min(p.seqs_per_tile, g.e - seq0 - p.seqs_per_tile)) * G;
-    slot = at / per - (at - j0) / per;
+    slot = team - (at - j0) / per;
   };
+  // (what later runs want of the plan waits in shared memory: registers are short)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  volatile int *misc = reinterpret_cast<volatile int *>(smem + L::kMisc);
   // Key tiles and runs so far, and those of each stream, for the barriers' phases.
   int tiles = 0, turn = 0;
   int tiles_0 = 0, tiles_1 = 0, turns_0 = 0, turns_1 = 0;
@@ -166,13 +170,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     ++turns_0;
     turns_1 += stream_tiles(1) > 0 ? 1 : 0;
     if (at >= stop) return false;
-    load_run();
+    load_run(misc[2], misc[3], false);
     return true;
   };
-  load_run();
+  load_run(my_team, plan.per, plan.apart);
+  if (plan.apart) stop = at;  // no other run
 
   // ------------------------------------------------------- shared memory
-  extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (threadIdx.x == 0) raise_status(status, FA_DEV_SMEM_ALIGN);
     return;
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   uint64_t *p_full = s_full + 2;
   uint64_t *o_done = p_full + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kMisc + 4);
+  volatile int *abort_flag = misc + 1;
 
   if (warp == 9 && lane == 0) {
     mbar_init(q_full, 1);
@@ -206,6 +210,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       mbar_init(&o_done[i], 1);
     }
     *abort_flag = 0;
+    misc[2] = my_team;
+    misc[3] = plan.per;
     fence_mbar_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&tm_q);
@@ -411,30 +417,39 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const uint32_t tO = tmem + L::kTmemO + i * D + lane_off;
     const float sl2 = p.own.scale_log2;
     const float2 sl2x2 = make_float2(sl2, sl2);
+    volatile int *save = reinterpret_cast<volatile int *>(smem + L::kSave) + warp * 12;
     bool ok = true;
     do {
-      const bool two = rows1 > 0;
-      const int tile = two ? i : 0;        // row tile
-      const int tile_rows = tile ? rows1 : rows0;
-      const int step = two ? 1 : 2;        // this stream's key tiles: j, j + step, ...
-      const int count = stream_tiles(i);
+      bool two = rows1 > 0;
+      const int count = stream_tiles(i);   // its key tiles: j, j + 1 or j + 2, ...
+      const int step = two ? kPrefixTileKeys : 2 * kPrefixTileKeys;
+      int tile = two ? i : 0;              // row tile
+      int tile_rows = tile ? rows1 : rows0;
       // rows behind the group's last sequence take part in the products and are
       // not written; a warp of them alone only keeps the barriers going
-      const bool live = row < tile_rows;
       const bool warp_live = (warp & 3) * 32 < tile_rows;
-      const int seq = seq0 + tile * p.seqs_per_tile + row / G;
-      const int head = kvh * G + row % G;
-      int limit = whole;
-      if (live) limit = min(whole, prefix_ctx(p, seq, whole, false));
+      int nvis = whole;  // visible keys from the stream's next tile on
+      if (row < tile_rows)
+        nvis = min(whole, prefix_ctx(p, seq0 + tile * p.seqs_per_tile + row / G, whole, false));
+      nvis -= (j0 + (two ? 0 : i)) * kPrefixTileKeys;
+      unsigned phase = tiles_of(i) & 1;
+      // what the loop does not need waits in shared memory (with it in registers
+      // the scores do not fit)
+      if (lane == 0) {
+        const int keep[12] = {at, stop, n, seq0, slot, kvh, rows0, rows1, tiles_0, tiles_1, turns_0, turns_1};
+#pragma unroll
+        for (int x = 0; x < 12; ++x) save[x] = keep[x];
+      }
+      __syncwarp();
       float m_ref = -CUDART_INF_F, l = 0.f, l_exact = 0.f;
       for (int t = 0; t < count; ++t) {
-        ok = mbar_wait_warp(&s_full[i], (tiles_of(i) + t) & 1, abort_flag, status);
+        ok = mbar_wait_warp(&s_full[i], phase, abort_flag, status);
         if (!ok) break;
+        phase ^= 1u;
         tc_fence_after();
         if (warp_live) {
           uint32_t sr[128];
           tmem_ld128_wait(tS, sr);
-          const int nvis = limit - (j0 + (two ? 0 : i) + t * step) * kPrefixTileKeys;
           if (__any_sync(0xffffffffu, nvis < kPrefixTileKeys)) {
 #pragma unroll
             for (int c = 0; c < 128; ++c)
@@ -507,15 +522,26 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           }
           tmem_wait_st();
         }
+        nvis -= step;
         tc_fence_before();
         mbar_arrive(&p_full[i]);
       }
+      at = save[0], stop = save[1], n = save[2], seq0 = save[3], slot = save[4], kvh = save[5];
+      rows0 = save[6], rows1 = save[7], tiles_0 = save[8], tiles_1 = save[9];
+      turns_0 = save[10], turns_1 = save[11];
+      __syncwarp();
+      two = rows1 > 0;
+      tile = two ? i : 0;
+      tile_rows = tile ? rows1 : rows0;
+      const bool live = row < tile_rows;
+      const int seq = seq0 + tile * p.seqs_per_tile + row / G;
+      const int head = kvh * G + row % G;
       // ---------------------------------------------------- partial state
       // Stream i of two row tiles writes its tile.  With one row tile each
       // stream writes half of the columns, from both streams' O, and stream 0
       // the sums.  Every thread of the streams comes to every barrier here, and
       // they agree on whether a wait gave up: a stream alone would wait for ever.
-      if (ok && count > 0) ok = mbar_wait_warp(&o_done[i], turns_of(i) & 1, abort_flag, status);
+      if (ok && stream_tiles(i) > 0) ok = mbar_wait_warp(&o_done[i], turns_of(i) & 1, abort_flag, status);
       const size_t n_rows = static_cast<size_t>(p.own.batch) * p.own.H * p.max_slots;
       const size_t to = (static_cast<size_t>(seq) * p.own.H + head) * p.max_slots + slot;
       const bool write = live && in_bounds(to, 1, n_rows, status);
@@ -598,7 +624,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 namespace {
 
 constexpr int kPrefixCombineWarps = 4;  // of a CTA
-constexpr int kPrefixCombineCtas = 8;   // on an SM
+// on an SM: 72 registers a thread.  (8, with 64, spill a few, and what they spill
+// comes from HBM: 1 to 2 us of a call.  6 take two more at the largest batch.)
+constexpr int kPrefixCombineCtas = 7;
 
 }  // namespace
 
@@ -624,8 +652,10 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
   // the plan of the shared keys, and this sequence's place in it
   PrefixSums sums;
   PrefixGroup g{};
+  const PrefixFirst firsts = prefix_first(p);
   if (!prefix_walk<kPrefixBySeq>(p, b, false, g, &sums)) g = PrefixGroup{};
-  const int per = p.alone ? 1 : prefix_plan(p, sums).per;
+  const PrefixPlan plan = p.alone ? PrefixPlan{0, 1, true} : prefix_plan(p, sums, firsts);
+  const int per = plan.per;
   const int ctx = prefix_ctx(p, b, g.whole, false);  // (decode_own.cu reports)
   const int own = (max(0, ctx - prefix_own_from(p, g)) + o.split_tokens - 1) / o.split_tokens;
   // this kernel's own (checked-build) index errors go to the device word only
@@ -641,7 +671,8 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
       const int round = (row - b * o.H) / o.group / p.team_heads;
       const int first =
           g.start + (round * g.pairs + (b - g.a) / (2 * p.seqs_per_tile)) * g.tiles;
-      shared = (first + g.tiles - 1) / per - first / per + 1;
+      shared = plan.apart ? (g.tiles + per - 1) / per
+                          : (first + g.tiles - 1) / per - first / per + 1;
     }
     const int ns = live ? own + shared : 0;
     const size_t own0 = static_cast<size_t>(row) * o.max_splits;

@@ -27,12 +27,13 @@ struct PrefixParams {
   int seqs_per_tile;           // sequences whose group of heads fills a 128-row tile
   int ctas;                    // CTAs that share the prefix work at most (one an SM)
   int team_heads, head_rounds; // KV heads that a team does at a time, and how often
+  int teams;                   // at most
   // What decides how many do: ns of a key tile with two row tiles and with one,
-  // before and after them, and of the partial states that each CTA adds; bytes
-  // a key (all KV heads); bytes a ns that the own keys' CTAs read at most, and on
-  // an SM that is left to them.
-  float tile_ns2, tile_ns1, fixed_ns, state_ns;
-  float key_bytes, max_rate, free_rate;
+  // before and after them, between two runs, and of the partial states that each
+  // CTA adds; bytes of a cache block (all KV heads); bytes a ns that the own keys' CTAs read
+  // at most, and on an SM that is left to them.
+  float tile_ns2, tile_ns1, fixed_ns, run_ns, state_ns;
+  float block_bytes, max_rate, max_rate_inv, free_rate;
   int max_slots;               // partial states of a row over shared keys
   float *po_part;              // fp32 [batch, H, max_slots, d]
   float4 *pml_part;            // [batch, H, max_slots]: m (log2 units), l, l_exact, 0
@@ -49,14 +50,15 @@ struct PrefixMaps {
 // stretches; a team's CTAs do the same stretch for a KV head each, so that the
 // heads of a token, which lie side by side in the pools, are read together.
 // (More KV heads than CTAs: a group's pairs come head_rounds times, with other
-// heads each time.)
+// heads each time.)  Where it pays, a pair's place in the line is rounded up to
+// whole stretches, so that none goes on into another pair (PrefixPlan::apart).
 //
 // One group: its sequences [a, e), the keys of its shared blocks, and the work
-// of it: `pairs` CTA loads of query rows (two tiles), `tiles` key tiles each;
-// `start` key tiles lie before it in the line.
+// of it: `pairs` CTA loads of query rows (two tiles), `tiles` key tiles each,
+// `span` of the line; `start` of the line lies before it.
 struct PrefixGroup {
   int a, e, whole, pairs, tiles;
-  int start;
+  int span, start;
 };
 
 __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams &p, int g, bool report) {
@@ -84,10 +86,12 @@ __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams &p, int g
 }
 
 // The line's length, and how it is shared: team t takes key tiles [t per, (t +
-// 1) per) of `total`.  (Whatever the arrays hold, it is an int: the host sees to
-// that.)
+// 1) per) of `total`; `apart`: a pair's key tiles begin at a multiple of `per`.
+// (Whatever the arrays hold, the line's length without gaps is an int: the host
+// sees to that.  With gaps it is at most per times the teams.)
 struct PrefixPlan {
   int total, per;
+  bool apart;
 };
 
 // What the search is for: the group of a sequence, or of a key tile.
@@ -95,22 +99,27 @@ constexpr int kPrefixNone = 0, kPrefixBySeq = 1, kPrefixByTile = 2;
 
 // Walks over the groups, 32 at a time (all lanes of a converged warp).  Finds
 // the group that `what` and `key` ask for, into `found`; false if there is none.
-// Sums the work, its cost in ns of one SM, and the keys that sequences share.
+// Sums the work; key tiles of pairs with two row tiles and with one, the shared
+// blocks and, once more for each sequence, the blocks that it shares, are this
+// lane's groups' alone.  Of the first 32 groups lane l keeps the l-th one's pairs
+// and their key tiles.  `apart`: 0, or the stretch that pairs are rounded up to.
 struct PrefixSums {
   int total;
-  float cost;
-  long long shared_keys;
+  int tiles2, tiles1;
+  long long blocks, shared_blocks;
+  int pairs, tiles;
 };
 template <int WHAT>
 __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool report,
-                                            PrefixGroup &found, PrefixSums *sums) {
+                                            PrefixGroup &found, PrefixSums *sums, int apart = 0) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   bool hit = false;
-  if (sums) *sums = {0, 0.f, 0};
+  if (sums) *sums = {};
   for (int g0 = 0; g0 < p.num_groups && !(hit && !sums); g0 += 32) {
     PrefixGroup r = prefix_group(p, g0 + lane, report);
-    const int work = r.tiles * r.pairs * p.head_rounds;
+    r.span = apart > 0 ? (r.tiles + apart - 1) / apart * apart : r.tiles;
+    const int work = r.span * r.pairs * p.head_rounds;
     int incl = work;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -129,6 +138,7 @@ __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool
         found.whole = __shfl_sync(0xffffffffu, r.whole, l);
         found.pairs = __shfl_sync(0xffffffffu, r.pairs, l);
         found.tiles = __shfl_sync(0xffffffffu, r.tiles, l);
+        found.span = __shfl_sync(0xffffffffu, r.span, l);
         found.start = __shfl_sync(0xffffffffu, r.start, l);
         hit = true;
       }
@@ -136,59 +146,125 @@ __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool
     base += __shfl_sync(0xffffffffu, incl, 31);
     if (sums) {
       // pairs with two row tiles take longer than a single one
-      const int n = r.e - r.a, single = n > 0 && (n - 1) / p.seqs_per_tile % 2 == 0 ? 1 : 0;
-      const float tiles = static_cast<float>(r.tiles * p.own.Hkv);
-      sums->cost = __fadd_rn(
-          sums->cost, __fmul_rn(tiles, __fadd_rn(__fmul_rn(static_cast<float>(r.pairs - single),
-                                                           p.tile_ns2),
-                                                 __fmul_rn(static_cast<float>(single), p.tile_ns1))));
-      sums->shared_keys += static_cast<long long>(r.whole) * n;
+      const int n = r.e - r.a, single = n <= (2 * r.pairs - 1) * p.seqs_per_tile ? 1 : 0;
+      sums->tiles2 += r.tiles * (r.pairs - single);
+      sums->tiles1 += r.tiles * single;
+      sums->blocks += n > 0 ? r.whole / kDecodeBlock : 0;
+      sums->shared_blocks += static_cast<long long>(r.whole / kDecodeBlock) * n;
+      if (g0 == 0) {
+        sums->pairs = r.pairs * p.head_rounds;
+        sums->tiles = r.tiles;
+      }
     }
   }
   if (sums) sums->total = base;
   return hit;
 }
 
-// The plan of a call, the same in every warp that asks (integers, and fp32
-// operations that no compiler contracts).  The own keys' CTAs read while this
-// work computes, on the SMs that it leaves to them and then on all of them; it
-// takes as many as let both end first.  (64 sequences over 8192 keys, 300 to
-// 1000 of their own: 64 SMs 42 us, 86 SMs 46, 128 SMs 47; 256 over 16384 keys:
-// 120 SMs 107 us, 152 SMs 124.)
-__device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const PrefixSums &s) {
-  const int lane = threadIdx.x & 31;
-  if (s.total <= p.ctas / p.team_heads) return {max(0, s.total), 1};
-  float cost = s.cost;
-  // keys of all sequences, from every `skip`-th of a large batch
-  const int skip = (p.own.batch + 1023) / 1024;
-  long long keys = 0;
-  for (int b = lane * skip; b < p.own.batch; b += 32 * skip)
-    keys += max(0, checked_load(p.own.ctx_lens, b, p.own.batch, p.own.status));
-  keys *= skip;
-  float shared = static_cast<float>(s.shared_keys);
+// 1 / x, to 2^-23, the same in every kernel
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Keys of the batch's first sequences, four a lane: loaded before the walk over
+// the groups, whose loads they then do not wait for.
+constexpr int kPrefixFirst = 4;
+struct PrefixFirst {
+  int keys[kPrefixFirst];
+};
+__device__ __forceinline__ int prefix_skip(const PrefixParams &p) {
+  return (p.own.batch + 1023) / 1024;  // a large batch's every `skip`-th counts
+}
+__device__ __forceinline__ PrefixFirst prefix_first(const PrefixParams &p) {
+  const int lane = threadIdx.x & 31, skip = prefix_skip(p);
+  PrefixFirst f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    cost = __fadd_rn(cost, __shfl_xor_sync(0xffffffffu, cost, o));
-    shared = __fadd_rn(shared, __shfl_xor_sync(0xffffffffu, shared, o));
-    keys += __shfl_xor_sync(0xffffffffu, keys, o);
+  for (int i = 0; i < kPrefixFirst; ++i) {
+    const int b = (lane + 32 * i) * skip;
+    f.keys[i] = b < p.own.batch ? checked_load(p.own.ctx_lens, b, p.own.batch, p.own.status) : 0;
   }
-  // lane l tries whole teams of ctas - l ctas / 40 SMs
-  const int n = max(1, (p.ctas - lane * p.ctas / 40) / p.team_heads) * p.team_heads;
-  const float own_bytes =
-      __fmul_rn(fmaxf(0.f, __fadd_rn(static_cast<float>(keys), -shared)), p.key_bytes);
-  // (without an SM of their own they come after this work)
-  const float rate = fminf(p.max_rate, __fmul_rn(static_cast<float>(p.ctas - n), p.free_rate));
-  const float mine = __fadd_rn(p.fixed_ns, __fdiv_rn(cost, static_cast<float>(n)));
-  const float all = __fdiv_rn(own_bytes, p.max_rate);
-  // what they have not read by the end of this work they read on every SM
-  const float rest = fmaxf(0.f, __fadd_rn(own_bytes, -__fmul_rn(rate, mine)));
-  const float t = __fadd_rn(fmaxf(all, __fadd_rn(mine, __fdiv_rn(rest, p.max_rate))),
-                            __fmul_rn(static_cast<float>(n), p.state_ns));
-  const unsigned best = __reduce_min_sync(
-      0xffffffffu, (static_cast<unsigned>(fminf(t, 1.3e8f)) << 5) | static_cast<unsigned>(lane));
-  const int teams = __shfl_sync(0xffffffffu, n / p.team_heads, best & 31);
-  const int total = max(0, s.total);
-  return {total, max(1, (total + teams - 1) / teams)};
+  return f;
+}
+
+// The plan of a call, the same in every warp that asks (integers, and fp32
+// operations that no compiler contracts, without divisions: a call waits for it).  The own keys' CTAs read while this
+// work computes, on the SMs that it leaves to them and then on all of them; it
+// takes as many as let both end first.  (64 sequences over 8192 keys, 1 to
+// 1024 of their own: 48 SMs 47 us, 64 SMs 42, 88 SMs 47, 128 SMs 49; 256 over 16384
+// keys, 1 to 512 of their own: 64 SMs 136 us, 96 SMs 98, 128 SMs 110, 152 SMs 125.)
+//
+// A stretch that goes from one pair to the next has two runs, and the MMAs rest
+// between them until O has left, Q has come and the first weights are there: 8
+// us that the other teams do not have.  Pairs set apart have no such stretch, but
+// their last ones are shorter; the same estimate decides.
+__device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const PrefixSums &s,
+                                                  const PrefixFirst &f) {
+  const int lane = threadIdx.x & 31;
+  const int total = max(0, s.total), teams = p.teams;
+  if (total <= teams) return {total, 1, false};
+  const int skip = prefix_skip(p);
+  long long keys = 0;
+#pragma unroll
+  for (int i = 0; i < kPrefixFirst; ++i) keys += max(0, f.keys[i]);
+  for (int b = (lane + 32 * kPrefixFirst) * skip; b < p.own.batch; b += 32 * skip)
+    keys += max(0, checked_load(p.own.ctx_lens, b, p.own.batch, p.own.status));
+  // (a lane's blocks are cut off at 2^25: what a cache can hold is below 2^30)
+  constexpr long long kMost = 1 << 25;
+  const int own_blocks = __reduce_add_sync(
+      0xffffffffu, static_cast<int>(min(kMost, keys * skip / kDecodeBlock)) -
+                       static_cast<int>(min(kMost, s.shared_blocks)));
+  const int once = __reduce_add_sync(0xffffffffu, static_cast<int>(min(kMost, s.blocks)));
+  const int tiles2 = __reduce_add_sync(0xffffffffu, s.tiles2);
+  const int tiles1 = __reduce_add_sync(0xffffffffu, s.tiles1);
+  // lane l tries stretches of 1 to 4 times what all teams would take
+  const int least = (total - 1) / teams + 1;
+  int per = static_cast<int>(min(static_cast<long long>(total), least + 3LL * least * lane / 32));
+  // ... and, pairs set apart, the least that cuts none into more parts
+  int parts = 0, even = 1;
+  if (p.num_groups <= 32)
+    for (int g = 0; g < p.num_groups; ++g) {
+      const int tiles = __shfl_sync(0xffffffffu, s.tiles, g);
+      const int pairs = __shfl_sync(0xffffffffu, s.pairs, g);
+      if (tiles > 0 && pairs > 0) {
+        const int n = (tiles - 1) / per + 1;
+        parts += n * pairs;
+        even = max(even, (tiles - 1) / n + 1);
+      }
+    }
+  const float own_bytes = __fmul_rn(static_cast<float>(max(0, own_blocks)), p.block_bytes);
+  const float all_bytes = __fadd_rn(own_bytes, __fmul_rn(static_cast<float>(once), p.block_bytes));
+  const float tiles = __fadd_rn(static_cast<float>(tiles2), static_cast<float>(tiles1));
+  const float tile_ns = __fmul_rn(__fadd_rn(__fmul_rn(static_cast<float>(tiles2), p.tile_ns2),
+                                            __fmul_rn(static_cast<float>(tiles1), p.tile_ns1)),
+                                  rcp_approx(tiles));
+  // ns of the call with stretches of `x` on n SMs, `more` beside what CTAs take anyway
+  auto estimate = [&](int x, int n, float more) {
+    // (without an SM of their own they come after this work)
+    const float rate = fminf(p.max_rate, __fmul_rn(static_cast<float>(p.ctas - n), p.free_rate));
+    const float mine = __fadd_rn(more, __fmul_rn(static_cast<float>(x), tile_ns));
+    // what they have not read by the end of this work they read on every SM
+    const float rest = fmaxf(0.f, __fadd_rn(own_bytes, -__fmul_rn(rate, mine)));
+    const float t = fmaxf(__fmul_rn(all_bytes, p.max_rate_inv),
+                          __fadd_rn(mine, __fmul_rn(rest, p.max_rate_inv)));
+    return static_cast<unsigned>(
+        fminf(__fadd_rn(t, __fmul_rn(static_cast<float>(n), p.state_ns)), 1.3e8f));
+  };
+  const unsigned line = estimate(per, ((total - 1) / per + 1) * p.team_heads,
+                                 __fadd_rn(p.fixed_ns, p.run_ns));
+  const unsigned apart = parts > 0 && parts <= teams
+                             ? estimate(even, parts * p.team_heads, p.fixed_ns)
+                             : 0xffffffffu;
+  const unsigned best =
+      __reduce_min_sync(0xffffffffu, (min(apart, line) << 5) | static_cast<unsigned>(lane));
+  const int l = best & 31;
+  const bool is_apart = __shfl_sync(0xffffffffu, apart <= line ? 1 : 0, l) != 0;
+  per = __shfl_sync(0xffffffffu, is_apart ? even : per, l);
+  if (!is_apart) return {total, per, false};
+  const int mine = __reduce_add_sync(
+      0xffffffffu, s.tiles > 0 ? ((s.tiles - 1) / per + 1) * s.pairs : 0);
+  return {mine * per, per, true};
 }
 
 // The first key that a sequence of a group reads on its own.

@@ -151,6 +151,35 @@ def test_many_rows_deep_prefix(fa):
     x.check(out, lse, only=[0, 1, 31, 32, 63, 64, 100, 255])
 
 
+STRETCHES = [  # groups (prefix, contexts), H, Hkv, d
+    ([(2500, [2501 + i for i in range(70)])], 32, 8, 128),    # two pairs of row tiles, twenty key tiles
+    ([(2500, [2600] * 40), (1300, [1400] * 35), (130, [150] * 3)], 32, 8, 128),  # unlike pairs
+    ([(200 + 40 * g, [260 + 40 * g] * 2) for g in range(33)], 16, 8, 64),        # more than 32 groups
+    ([(400 + 70 * g, [440 + 70 * g] * 2) for g in range(24)], 8, 8, 128),        # more pairs than teams
+    ([(700, [720] * 3), (300, [310] * 2)], 160, 160, 64),     # more KV heads than CTAs
+    ([(1000, [1100] * 9), (260, [300])], 304, 304, 128),
+]
+
+
+@pytest.mark.parametrize("case", range(len(STRETCHES)))
+def test_stretches_of_the_work(fa, case):
+    """Work that CTAs share out in stretches: ends inside a pair of row tiles, at
+    its end and behind it, and KV heads in rounds."""
+    groups, H, Hkv, d = STRETCHES[case]
+    x = Batch(groups, H, Hkv, d, seed=20 + case)
+    out, lse = fa.fa_decode_paged_prefix(**x.args())
+    assert_device_clean()
+    n = len(x.ctx)
+    x.check(out, lse, only=sorted({0, 1, 2, n // 3, n // 2, n - 2, n - 1}))
+    # the same batch over its own keys alone: each result is off by half a step of
+    # its own and half a step of each weight, 2^-8 of sum p |v| <= max |v| each
+    few, _ = fa.fa_decode_paged_prefix(**x.args(
+        cu_groups=dev(np.zeros(1, np.int32)), prefix_lens=dev(np.zeros(0, np.int32)),
+        max_own_len=max(x.ctx)))
+    assert_device_clean()
+    assert (out.float() - few.float()).abs().max() <= 2.0 ** -6 * x.vp.float().abs().max()
+
+
 def test_repeated_calls_give_the_same_bits(fa):
     torch = torch_mod()
     x = Batch([(3000, [3010] * 20), (700, [900] * 13)], 16, 4, 128, seed=5)
