@@ -28,13 +28,13 @@
 // prefix_combine_kernel: one, two or four warps per (sequence, query head) merge
 // the states of its own keys and of the shared ones, as decode_combine_kernel.
 //
-// What bounds it: with many rows the loop over key tiles, 3202 cycles each for
+// What bounds it: with many rows the loop over key tiles, 3200 cycles each for
 // two row tiles of d = 128, of which the products are 2048 (the rest the issuer
-// waits, most for P: 394), 1024 rows and 16384 keys of 8 KV heads 73 us on 120
+// waits, most for P: 394), 1024 rows and 16384 keys of 8 KV heads 85 us on 96
 // SMs; with few rows the feed, 5.2 TB/s.  A call has 9 us before its first product
-// (plan 2.3, block ids 1.3, ring 4.5) and 5 to 7 behind its last in the combine.
-// 64 sequences over 8192 shared keys and 1 to 1024 of their own, 32 / 8 heads: 42 us
-// where the ordinary call takes 216; 256 over 16384 and 1 to 512: 107 and 1537.
+// (plan 3.4, block ids 1.3, ring 4) and 5 to 7 behind its last in the combine.
+// 64 sequences over 8192 shared keys and 1 to 1024 of their own, 32 / 8 heads: 41 us
+// where the ordinary call takes 216; 256 over 16384 and 1 to 512: 97 and 1537.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
