@@ -4,8 +4,8 @@
 // product in fp32 is off by 2^-24 of itself (at position 10^6 by 0.06 rad).
 // So turns a position, inv_freq / 2 pi, are made a 64-bit fraction of a turn,
 // and the product with a position is one integer multiplication: it wraps at
-// whole turns by itself and is exact.  Its upper half, 2^-32 of a turn, goes to
-// sincospi.  The fraction is formed in integers too: with the few fp64
+// whole turns by itself and is exact.  Its upper half, 2^-32 of a turn, goes into
+// sin and cos.  The fraction is formed in integers too: with the few fp64
 // instructions that it takes otherwise, this GPU's fp64 rate bound every kernel
 // here (73 k packed tokens of 16 / 4 heads of d = 128, both directions, 261 us
 // against 232; 34.8 k tokens into the 8-bit cache 343 us against 148).
@@ -38,16 +38,39 @@ __device__ __forceinline__ uint64_t rope_turns(double inv_freq) {
   return bits >> 63 ? 0 - t : t;
 }
 
+// sin and cos of v 2^-32 turns, at most an eighth of a turn either way: the
+// angle in two floats t + tl, the Taylor series' terms behind the first one (of
+// cos: behind 1 - t^2 / 2, also in two floats) with their rounding errors and tl
+// added to it last.  So there is little but the last rounding: 0.29 units in the
+// last place root mean square (sincospi's are about 0.4), at most 0.82.  Of a key on
+// its way to e4m3 those that fp32 gives another code than the exact product has
+// are so one in a million, against 1.6 with sincospi.
+__device__ __forceinline__ void sin_cos_eighth(int32_t v, float &s, float &c) {
+  constexpr float K = 0x1.921fb6p-30f, Kl = -0x1.777a5cp-55f;  // 2 pi 2^-32
+  const float vh = static_cast<float>(v & ~127), vl = static_cast<float>(v & 127);
+  const float t = vh * K;
+  const float tl = fmaf(vh, K, -t) + fmaf(vh, Kl, vl * K);
+  const float w = t * t, wl = fmaf(t, t, -w);
+  const float h = fmaf(-0.5f, w, 1.f);  // 1 - w / 2
+  float q = fmaf(w, 1.f / 362880.f, -1.f / 5040.f);
+  q = fmaf(w, q, 1.f / 120.f);
+  q = fmaf(w, q, -1.f / 6.f);
+  s = t + fmaf(tl, h, t * w * q);
+  q = fmaf(w, -1.f / 3628800.f, 1.f / 40320.f);
+  q = fmaf(w, q, -1.f / 720.f);
+  q = fmaf(w, q, 1.f / 24.f);
+  const float hl = fmaf(-0.5f, w, 1.f - h);
+  c = h + fmaf(w * w, q, fmaf(-t, tl, fmaf(-0.5f, wl, hl)));
+}
+
 // cos and sin of p positions' turns: the nearest quarter of a turn by signs and
-// places, the rest, at most an eighth either way, as a float (2^-27 of a turn).
+// places, the rest as above (2^-32 of a turn).
 __device__ __forceinline__ float2 rope_cos_sin(uint64_t turns, int p) {
   const uint64_t a = turns * static_cast<uint64_t>(static_cast<int64_t>(p));
   const uint32_t hi = static_cast<uint32_t>(a >> 32);  // 2^32 of a turn
   const uint32_t quarter = (hi + 0x20000000u) >> 30;
   float s, c;
-  // (in units of half a turn)
-  sincospif(static_cast<float>(static_cast<int32_t>(hi - (quarter << 30))) * 4.656612873077393e-10f,
-            &s, &c);
+  sin_cos_eighth(static_cast<int32_t>(hi - (quarter << 30)), s, c);
   const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
   return make_float2((quarter + 1u) & 2u ? -x : x, quarter & 2u ? -y : y);
 }

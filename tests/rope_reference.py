@@ -42,10 +42,9 @@ def slack(x, pos, freq, factor=1.0, interleaved=False, steps=1):
     """What fp32 may be off by before the result is rounded, for each value.
 
     The angle: turns a position are held to 2^-52 of themselves, and the NumPy
-    product to 2^-53: 2^-51 |p f|.  As a float of half a turn either way it is
-    rounded by 2^-25 half turns (2^-23.3 rad), and sincospi adds two units of
-    2^-24 and the factor one: 2^-21.5 for each of cos and sin, times (|a| + |b|)
-    factor; the two products and the sum add 3 units of 2^-24, the `steps` turns
+    product to 2^-53: 2^-51 |p f|.  Cut to 2^-32 of a turn it is off by 2^-29.3
+    rad, sin and cos by two units of 2^-24 at most and the factor by one; 2^-21.5
+    is above that for each of cos and sin, times (|a| + |b|) factor; the two products and the sum add 3 units of 2^-24, the `steps` turns
     from row to row 2^-22 each.  Values that pass through are exact."""
     rot = 2 * len(freq)
     x = np.abs(np.asarray(x, dtype=np.float64))

@@ -345,6 +345,62 @@ def test_append_fp8(fa, ctx, new, H, Hkv, d, rot, inter, factor):
     assert np.array_equal(got_k, codes[0]) and np.array_equal(got_ks, scales[0])
 
 
+@pytest.mark.parametrize("inter,factor,d", [(False, 1.0, 128), (True, 1.2, 128), (False, 1.1, 64)])
+def test_append_fp8_few_codes_are_beside_the_nearest(fa, inter, factor, d):
+    """Four million keys, rotated in fp32: where the code is not that of the exact
+    value, that lies as near the border between both as fp32 may be off.  cos and
+    sin are off by 0.82 units in their last place (1.64 x 2^-24 of themselves) and
+    the angle by 2^-32 turns (2^-29 rad), the factor, a product and the sum round
+    once each: 4.7 x 2^-24 of |a cos| + |b sin| and 2^-29 (|a| + |b|).
+
+    With factor 1 there are 1 to 2 in a million of them (codes lie 2^-3 to 2^-4
+    apart): 12 at most here.  With 1.2, which is 6/5, borders m 2^k with m a
+    multiple of 3 are what bf16 values 5 (m/3) 2^(k-1) become at small angles, so
+    their number says nothing there.  Compared are e4m3's normal values whose two
+    terms do not cancel to less than a sixth."""
+    torch = torch_mod()
+    n, Hkv, seqs = 1024, 8, 4 * 128 // d
+    g = torch.Generator(device="cuda").manual_seed(31)
+    k = torch.randn((seqs * n, Hkv, d), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.randperm(seqs * n // 16, generator=g, device="cuda").to(torch.int32).view(seqs, -1)
+    ctx = torch.full((seqs,), n, dtype=torch.int32, device="cuda")
+    cu = torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * n
+    pools = [torch.zeros(seqs * n // 16, 16, Hkv, d, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scales = [torch.zeros(seqs * n // 16, Hkv, device="cuda") for _ in "kv"]
+    freq = dev(rr.frequencies(d))
+    fa.fa_cache_append_rope_fp8(None, k, k, freq, *pools, *scales, table, ctx, cu, n, factor=factor,
+                                interleaved=inter)
+    assert_device_clean()
+    order = table.flatten().long()
+    got = pools[0][order].view(torch.float8_e4m3fn).double().view(seqs * n, Hkv, d)
+    scale = scales[0][order].double().repeat_interleave(16, 0)[..., None]
+    x = k.double()
+    angle = torch.arange(n, dtype=torch.float64, device="cuda").repeat(seqs)[:, None, None] * freq
+    fac = float(np.float32(factor))
+    c, s = angle.cos() * fac, angle.sin() * fac
+    if inter:
+        a, b = x[..., 0::2], x[..., 1::2]
+        join = lambda u, v: torch.stack([u, v], -1).flatten(-2)  # noqa: E731
+    else:
+        a, b = x[..., :d // 2], x[..., d // 2:]
+        join = lambda u, v: torch.cat([u, v], -1)  # noqa: E731
+    y = join(a * c - b * s, a * s + b * c) / scale
+    terms = join((a * c).abs() + (b * s).abs(), (a * s).abs() + (b * c).abs()) / scale
+    q = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
+    want = torch.round(y / q) * q
+    # (the 64-bit angle is off by 2^-43: what is that near a border is left out)
+    clear = ((y / q).abs() % 1 - 0.5).abs() > 2.0 ** -36
+    fair = (y.abs() >= 2.0 ** -6) & (y.abs() * 6 >= terms) & clear
+    assert fair.double().mean() > 0.8
+    far = (got != want) & fair
+    off = 5 * 2.0 ** -24 * terms + 2.0 ** -28 * join(*[(a.abs() + b.abs()) * fac] * 2) / scale
+    border = ((y / q).abs() % 1 - 0.5).abs() * q
+    assert (border <= off)[far].all()
+    if factor == 1.0:
+        assert far.sum() <= 12
+    assert ((got - want).abs()[far] <= q[far] * (1 + 2.0 ** -20)).all()
+
+
 def test_append_fp8_extremes(fa):
     """Zeros, the smallest and largest bf16 values, infinities and NaN, amax at a
     border, and an older scale that is no power of two."""
