@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 
   // A run: key tiles [j0, j0 + n) of KV head kvh for the row tiles of the
   // sequences from seq0 on; rows0 and rows1 of the two belong to the group.
-  int kvh, j0, n, seq0, slot, lead, whole;
+  int kvh, j0, n, seq0, slot, whole;
   int rows0, rows1;
   auto load_run = [&](int team, int per, bool apart) {
     prefix_walk<kPrefixByTile>(p, at, false, g, nullptr, apart ? per : 0);
@@ -144,7 +144,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     n = min(g.tiles - j0, stop - at);
     const int round = p.head_rounds > 1 ? unit / g.pairs : 0;
     kvh = round * p.team_heads + blockIdx.x - team * p.team_heads;
-    lead = g.a;
     whole = g.whole;
     seq0 = g.a + (unit - round * g.pairs) * 2 * p.seqs_per_tile;
     rows0 = min(p.seqs_per_tile, g.e - seq0) * G;
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   if (warp == 9 || warp == 10) {
     // ------------------------------------------------------ copies
     // Lanes 0..7 hold a tile's 8 block ids; the ids of 4 tiles come with one
-    // load, 4 tiles before they are needed.  A block past the prefix or outside
+    // load, 4 tiles before they are needed.  A block past the held keys or outside
     // the pool is not copied: its rows are made 0 (what a stage held before
     // may be infinite, and 0 times that is NaN).
     constexpr int kTileBlocks = kPrefixTileKeys / kDecodeBlock;
@@ -243,10 +242,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     int issued = 0, q_issued = 0;
     bool ok = true;
     do {
+      // The table row to read the blocks through: a sequence's row holds its own
+      // keys' blocks and no more, so the first of the group that has all shared
+      // keys, or the longest if none has (`held` of them; nobody sees the others).
+      int lead = g.a, held = min(whole, prefix_ctx(p, g.a, whole, false));
+      for (int b0 = g.a; held < whole && b0 < g.e; b0 += 32) {
+        const int b = b0 + lane;
+        const int keys = b < g.e ? min(whole, prefix_ctx(p, b, whole, false)) : 0;
+        const int most = __reduce_max_sync(0xffffffffu, keys);
+        if (most > held) {
+          held = most;
+          lead = b0 + __ffs(__ballot_sync(0xffffffffu, keys == most)) - 1;
+        }
+      }
       auto fetch = [&](int w) -> int {
         const int j = w + lane / kTileBlocks;
         const int blk = (j0 + j) * kTileBlocks + lane % kTileBlocks;
-        if (j >= n || blk * kDecodeBlock >= whole) return -1;
+        if (j >= n || blk * kDecodeBlock >= held) return -1;
         const int id = checked_load(
             p.own.block_table, static_cast<size_t>(lead) * p.own.max_blocks_per_seq + blk,
             static_cast<size_t>(p.own.batch) * p.own.max_blocks_per_seq, status);

@@ -43,10 +43,12 @@ size_t fa_decode_prefix_workspace_size(int batch, int H, int Hkv, int d, int max
  *   prefix_lens    : int32 DEVICE array [num_groups]: the first prefix_lens[g]
  *                    keys of every sequence of the group are the same.  Whole
  *                    blocks are shared, 16 * floor(prefix_lens[g] / 16) keys,
- *                    read through the table row of the group's first sequence;
- *                    the keys from there on are read through each sequence's own.
- *                    A sequence may be shorter than its prefix and sees its
- *                    first ctx_lens keys (0 for a padded slot of the batch).
+ *                    read through the table row of the group's first sequence
+ *                    that has them all (of its longest one, where none has); the
+ *                    keys from there on are read through each sequence's own.
+ *                    A sequence may be shorter than its prefix, the first one
+ *                    too, and sees its first ctx_lens keys (0 for a padded slot of
+ *                    the batch); its row holds the blocks of those alone.
  *   max_prefix_len : an upper bound of prefix_lens
  *   max_own_len    : an upper bound of ctx_lens[b] less its group's prefix_lens
  *   workspace      : fa_decode_prefix_workspace_size() bytes, 256-byte aligned;

@@ -447,3 +447,25 @@ def test_serving_run(fa, most):
                 got = out[b, h].double().cpu().numpy()
                 assert (np.abs(got - want) <= tol).all(), (step, b, h)
     assert_device_clean()
+
+
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("rest", [-1, "stale"])
+@pytest.mark.parametrize("groups", [
+    [(400, [0, 450, 420]), (90, [100, 0])],                # a finished sequence comes first
+    [(1001, [100, 0, 1040, 1002])],                        # ... or one of few keys
+    [(700, [0] * 40 + [710, 30, 705]), (0, [50])],         # the 41st has them all
+    [(2048, [2047, 2030, 2048, 2100])],                    # short by one key
+    [(2500, [300, 1234, 0, 1233]), (640, [640])],          # none has them all
+    [(300, [0, 0]), (64, [70])],                           # nobody is there
+])
+def test_rows_hold_the_blocks_of_their_keys_alone(fa, groups, rest, shared):
+    """A group's shared blocks are found whichever of its sequences has them: a
+    row holds nothing, or old ids, behind its own keys."""
+    x = Batch(groups, 8, 2, 128, seed=50, shared=shared)
+    for b, c in enumerate(x.ctx):
+        x.table[b, (c + 15) // 16:] = -1 if rest == -1 else x.table[b, 0] if c else b
+    out, lse = fa.fa_decode_paged_prefix(**x.args())
+    assert_device_clean()
+    x.check(out, lse)
+    assert not out[[b for b, c in enumerate(x.ctx) if c == 0]].any()
