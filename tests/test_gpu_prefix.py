@@ -449,6 +449,14 @@ def test_serving_run(fa, most):
     assert_device_clean()
 
 
+def reaching(x):
+    """The batch's table made as wide as its longest prefix, which the call wants
+    although none of its sequences may be as long."""
+    more = (x.max_pre + 15) // 16 - x.table.shape[1]
+    x.table = np.pad(x.table, ((0, 0), (0, max(0, more))), constant_values=-1)
+    return x
+
+
 @pytest.mark.parametrize("shared", [True, False])
 @pytest.mark.parametrize("rest", [-1, "stale"])
 @pytest.mark.parametrize("groups", [
@@ -462,7 +470,7 @@ def test_serving_run(fa, most):
 def test_rows_hold_the_blocks_of_their_keys_alone(fa, groups, rest, shared):
     """A group's shared blocks are found whichever of its sequences has them: a
     row holds nothing, or old ids, behind its own keys."""
-    x = Batch(groups, 8, 2, 128, seed=50, shared=shared)
+    x = reaching(Batch(groups, 8, 2, 128, seed=50, shared=shared))
     for b, c in enumerate(x.ctx):
         x.table[b, (c + 15) // 16:] = -1 if rest == -1 else x.table[b, 0] if c else b
     out, lse = fa.fa_decode_paged_prefix(**x.args())
