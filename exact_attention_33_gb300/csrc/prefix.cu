@@ -105,6 +105,22 @@ __device__ __forceinline__ void store8(float *to, const float (&v)[8]) {
                : "memory");
 }
 
+// The first of the sequences [a, e) that has all of `whole` shared keys, or else the
+// longest, and how many of them it has (a converged warp).
+__device__ __noinline__ int2 find_lead(const PrefixParams &p, int a, int e, int whole) {
+  int lead = a, held = 0;
+  for (int b0 = a; held < whole && b0 < e; b0 += 32) {
+    const int b = b0 + static_cast<int>(threadIdx.x & 31);
+    const int keys = b < e ? min(whole, prefix_ctx(p, b, whole, false)) : 0;
+    const int most = __reduce_max_sync(0xffffffffu, keys);
+    if (most > held) {
+      held = most;
+      lead = b0 + __ffs(__ballot_sync(0xffffffffu, keys == most)) - 1;
+    }
+  }
+  return make_int2(lead, held);
+}
+
 }  // namespace
 
 template <int D>
@@ -245,28 +261,26 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       // The table row to read the blocks through: a sequence's row holds its own
       // keys' blocks and no more, so the first of the group that has all shared
       // keys, or the longest if none has (`held` of them; nobody sees the others).
-      int lead = g.a, held = min(whole, prefix_ctx(p, g.a, whole, false));
-      for (int b0 = g.a; held < whole && b0 < g.e; b0 += 32) {
-        const int b = b0 + lane;
-        const int keys = b < g.e ? min(whole, prefix_ctx(p, b, whole, false)) : 0;
-        const int most = __reduce_max_sync(0xffffffffu, keys);
-        if (most > held) {
-          held = most;
-          lead = b0 + __ffs(__ballot_sync(0xffffffffu, keys == most)) - 1;
-        }
-      }
+      // That is mostly the first of all, whose ids come while its length is looked
+      // at.  (-1: an id that no pool has, -2: no block wanted)
+      int lead = g.a, held = whole;
       auto fetch = [&](int w) -> int {
         const int j = w + lane / kTileBlocks;
         const int blk = (j0 + j) * kTileBlocks + lane % kTileBlocks;
-        if (j >= n || blk * kDecodeBlock >= held) return -1;
-        const int id = checked_load(
+        if (j >= n || blk * kDecodeBlock >= held) return -2;
+        return max(-1, checked_load(
             p.own.block_table, static_cast<size_t>(lead) * p.own.max_blocks_per_seq + blk,
-            static_cast<size_t>(p.own.batch) * p.own.max_blocks_per_seq, status);
-        if (id >= 0 && id < p.own.num_blocks) return id;
-        if (is_k) raise_status(status, FA_DEV_BAD_BLOCK);
-        return -1;
+            static_cast<size_t>(p.own.batch) * p.own.max_blocks_per_seq, status));
       };
+      const int lead_ctx = prefix_ctx(p, lead, whole, false);
       int cur = fetch(0), nxt = fetch(kIdTiles);
+      if (lead_ctx < whole) {
+        const int2 found = find_lead(p, g.a, g.e, whole);
+        lead = found.x;
+        held = found.y;
+        cur = fetch(0);
+        nxt = fetch(kIdTiles);
+      }
       auto load = [&](int j) -> bool {
         if (j > 0 && j % kIdTiles == 0) {
           cur = nxt;
@@ -278,9 +292,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // lane = block issues that copy
         const int id = __shfl_sync(0xffffffffu, cur, (j % kIdTiles) * kTileBlocks + lane % kTileBlocks);
         uint8_t *dst = stage + lane * kBlockBytes;
-        const bool mine = lane < kTileBlocks;
-        const unsigned live = __ballot_sync(0xffffffffu, mine && id >= 0);
-        if (mine && id < 0) {
+        const bool mine = lane < kTileBlocks, there = mine && id >= 0 && id < p.own.num_blocks;
+        const unsigned live = __ballot_sync(0xffffffffu, there);
+        if (mine && !there) {
+          if (is_k && id != -2) raise_status(status, FA_DEV_BAD_BLOCK);
           for (int t = 0; t < kBlockBytes / 16; ++t)
             reinterpret_cast<uint4 *>(dst)[t] = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
@@ -288,7 +303,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(live) * kBlockBytes);
         __syncwarp();
-        if (mine && id >= 0)
+        if (there)
           tma_load_5d(dst, map, &full[st], 0, 0, 0, id * (kDecodeBlock / 8), kvh);
         issued = x + 1;
         return true;
