@@ -252,6 +252,8 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   p.max_rate_inv = 1.f / p.max_rate;
   p.free_rate = 62.f;
   p.max_slots = s.max_slots;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
   p.po_part = reinterpret_cast<float *>(parts + w.o_bytes + w.ml_bytes);
   p.pml_part = reinterpret_cast<float4 *>(parts + w.o_bytes + w.ml_bytes + s.o_bytes);
   return launch_prefix(m, p, d, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess

@@ -655,6 +655,92 @@ constexpr int kPrefixCombineWarps = 4;  // of a CTA
 // comes from HBM: 1 to 2 us of a call.  6 take two more at the largest batch.)
 constexpr int kPrefixCombineCtas = 7;
 
+// E consecutive bf16 values from element `at` on of an array of n.
+template <int E>
+__device__ __forceinline__ void load_bf16(const void *base, size_t at, size_t n, unsigned int *status,
+                                          float (&v)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.f;
+  if (!in_bounds(at, E, n, status)) return;
+  const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + at);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float2 x = bf16x2_to_float2(src[e / 2]);
+    v[e] = x.x;
+    v[e + 1] = x.y;
+  }
+}
+
+// Rows [row0, row0 + rows) of one sequence over all its keys, one after the other,
+// through its own table row: writes the output alone.  (A converged warp, E values
+// of the head a lane.)
+template <int E>
+__device__ __noinline__ void sum_rows(const PrefixParams &p, int row0, int rows) {
+  constexpr int D = 32 * E, U = 4;
+  const DecodeParams &o = p.own;
+  unsigned int *status = o.dev_status;
+  const int lane = threadIdx.x & 31, b = row0 / o.H;
+  const int ctx = checked_load(o.ctx_lens, b, o.batch, status);
+  const size_t n_pool = static_cast<size_t>(o.num_blocks) * kDecodeBlock * o.Hkv * D;
+  const size_t n_out = static_cast<size_t>(o.batch) * o.H * D;
+  const size_t token = static_cast<size_t>(o.Hkv) * D;  // elements from key to key of a block
+  for (int row = row0; row < row0 + rows; ++row) {
+    const size_t mine = static_cast<size_t>(row) * D + lane * E;
+    const size_t head = static_cast<size_t>((row - b * o.H) / o.group) * D + lane * E;
+    float q[E], acc[E], m = -CUDART_INF_F, l = 0.f;
+    load_bf16<E>(o.q, mine, n_out, status, q);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int t = 0; t < ctx; t += U) {  // U keys of one block
+      const int id = checked_load(
+          o.block_table, static_cast<size_t>(b) * o.max_blocks_per_seq + t / kDecodeBlock,
+          static_cast<size_t>(o.batch) * o.max_blocks_per_seq, status);
+      if (id < 0 || id >= o.num_blocks) {
+        if (lane == 0) raise_status(o.dev_status, FA_DEV_BAD_BLOCK);
+        break;
+      }
+      const size_t at =
+          (static_cast<size_t>(id) * kDecodeBlock + t % kDecodeBlock) * token + head;
+      float s[U], v[U][E];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float k[E];
+        load_bf16<E>(p.k_pool, at + u * token, n_pool, status, k);
+        load_bf16<E>(p.v_pool, at + u * token, n_pool, status, v[u]);
+        s[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[u] = fmaf(q[e], k[e], s[u]);
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
+        s[u] = t + u < ctx ? s[u] * o.scale_log2 : -CUDART_INF_F;
+        top = fmaxf(top, s[u]);
+      }
+      const float ref = top == -CUDART_INF_F ? 0.f : top, alpha = ex2(m - ref);
+      m = top;
+      l *= alpha;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u >= ctx) break;
+        const float w = ex2(s[u] - ref);
+        l += w;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (!in_bounds(mine, E, n_out, status)) continue;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(o.out) + mine);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
 }  // namespace
 
 // W warps per (sequence, query head) row, 4 / W rows a CTA; warp w of a row takes
@@ -685,6 +771,14 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
   const int per = plan.per;
   const int ctx = prefix_ctx(p, b, g.whole, false);  // (decode_own.cu reports)
   const int own = (max(0, ctx - prefix_own_from(p, g)) + o.split_tokens - 1) / o.split_tokens;
+  // A sequence that ends inside the shared keys meets the values behind its own with
+  // weight 0 in the products, and 0 times an infinity or a NaN is a NaN: then its
+  // rows are summed again over its own keys alone.  That takes 0.25 us a key (8000
+  // keys 2 ms), and no cache of finite values comes there.  (Its code costs a call
+  // of 42 or 97 us up to 0.9 by being there, in line or out of it, and 1.3 in the own
+  // keys' kernel: more instructions come through a cold L2.)
+  const bool ends_inside = !p.alone && live && ctx < g.whole;
+  bool again = false;
   // this kernel's own (checked-build) index errors go to the device word only
   unsigned int *status = o.dev_status;
   const size_t n_own = static_cast<size_t>(o.batch) * o.H * o.max_splits;
@@ -804,6 +898,10 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
         for (int x = 0; x < W; ++x) acc[e] += s_acc[r0 + x][lane * E + e];
       }
     }
+    if (ends_inside) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) again = again || !(fabsf(acc[e]) < CUDART_INF_F);
+    }
     const float inv = (L == 0.f) ? 0.f : 1.f / L;
     const size_t at = static_cast<size_t>(row) * D + lane * E;
     uint16_t *dst = static_cast<uint16_t *>(o.out) + at;
@@ -818,6 +916,7 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
         in_bounds(row, 1, static_cast<size_t>(o.batch) * o.H, status))
       o.lse[row] = (Lx == 0.f) ? -CUDART_INF_F : (M + __log2f(Lx)) * 0.69314718055994530942f;
   }
+  if (__any_sync(0xffffffffu, again)) sum_rows<E>(p, row0, rows);
   if (publisher) publish_call_status(o.call, call_bits, o.dev_status);
 }
 

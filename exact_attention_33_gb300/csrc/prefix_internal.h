@@ -37,6 +37,7 @@ struct PrefixParams {
   int max_slots;               // partial states of a row over shared keys
   float *po_part;              // fp32 [batch, H, max_slots, d]
   float4 *pml_part;            // [batch, H, max_slots]: m (log2 units), l, l_exact, 0
+  const void *k_pool, *v_pool; // bf16 [num_blocks, 16, Hkv, d]
 };
 
 // The maps of Q, of the pools as the own keys' kernel copies them (a block's

@@ -55,8 +55,9 @@ size_t fa_decode_prefix_workspace_size(int batch, int H, int Hkv, int d, int max
  *                    with its control block as fa_decode_paged's
  * A sequence with ctx_len 0 gets out = 0 and lse = -inf, a query with a NaN
  * NaN in both.  Shared values (V) that are infinite or NaN reach the rows of
- * their group's sequences, whatever their weight; values past a sequence's own
- * context reach nothing.
+ * the group's sequences that see them, whatever their weight; values past a
+ * sequence's own context reach nothing of it.  (A sequence shorter than its
+ * prefix whose group holds such values behind its keys is summed on its own.)
  * Device-side checks: FA_DEV_BAD_SEQLEN (a group outside the batch or of
  * negative size: it is passed over, and sequences in no other group read all
  * keys as their own), FA_DEV_BAD_CTX (prefix_lens outside [0, max_prefix_len]

@@ -477,3 +477,60 @@ def test_rows_hold_the_blocks_of_their_keys_alone(fa, groups, rest, shared):
     assert_device_clean()
     x.check(out, lse)
     assert not out[[b for b, c in enumerate(x.ctx) if c == 0]].any()
+
+
+@pytest.mark.parametrize("groups,H,Hkv,d", [
+    ([(640, [700, 100, 0, 16, 641, 640, 639, 624])], 4, 2, 64),    # one row tile: both streams
+    ([(2000, [1500, 2010, 700] + [2001] * 60), (320, [330, 15])], 32, 8, 128),   # 2080 rows
+    ([(1000, [1010] * 50 + [129, 990, 500] + [1002] * 20)], 32, 8, 128),   # 2336 rows
+    ([(512, [515] * 140 + [200, 333])], 32, 8, 64),                # 4544 rows
+])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("shared", [True, False])
+def test_values_behind_a_short_sequence(fa, groups, H, Hkv, d, value, shared):
+    """A sequence that ends inside the shared keys meets nothing of those behind
+    its own, whatever they hold; those that see them do."""
+    torch = torch_mod()
+    x = Batch(groups, H, Hkv, d, seed=60, shared=shared)
+    a, e = int(x.cu[0]), int(x.cu[1])
+    long = [b for b in range(a, e) if x.ctx[b] >= groups[0][0]]
+    short = [b for b in range(len(x.ctx)) if b not in long]
+    last = max(x.ctx[b] for b in short if b < e)
+    x.vp[int(x.table[0, last // 16]), last % 16] = value   # the first key that no short one sees
+    out, lse = fa.fa_decode_paged_prefix(**x.args())
+    assert_device_clean()
+    x.check(out, lse, only=short)
+    assert not torch.isfinite(out[long]).any() and torch.isfinite(lse[long]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shared", [True, False])
+def test_slots_that_nobody_wrote(fa, d, shared):
+    """All sequences of a group shorter than its prefix: its other slots are free
+    ones and hold NaN."""
+    x = reaching(Batch([(900, [500, 0, 507, 64]), (300, [17])], 8, 2, d, seed=61, shared=shared))
+    used = np.zeros(x.kp.shape[0] * 16, dtype=bool)
+    for b, c in enumerate(x.ctx):
+        for j in range(c):
+            used[x.table[b, j // 16] * 16 + j % 16] = True
+    for pool in (x.kp, x.vp):
+        pool.view(-1, 2, d)[dev(~used)] = math.nan
+    out, lse = fa.fa_decode_paged_prefix(**x.args())
+    assert_device_clean()
+    x.check(out, lse)
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_short_sequences_keep_what_is_theirs(fa, shared):
+    """Infinite and NaN values that a short sequence does see, and a query of its
+    that holds a NaN, come through as they do for any other."""
+    torch = torch_mod()
+    x = Batch([(800, [810, 300, 400, 200])], 8, 2, 128, seed=62, shared=shared)
+    x.vp[int(x.table[0, 20]), 3] = math.nan      # key 323: sequences 0 and 2 see it
+    x.q[3, 5, 9] = math.nan
+    out, lse = fa.fa_decode_paged_prefix(**x.args())
+    assert_device_clean()
+    assert torch.isnan(out[[0, 2]]).all() and torch.isfinite(lse[[0, 2]]).all()
+    x.check(out, lse, only=[1])
+    assert torch.isnan(out[3, 5]).all() and torch.isnan(lse[3, 5])
+    assert torch.isfinite(out[3, [0, 1, 2, 3, 4, 6, 7]]).all()
