@@ -60,6 +60,7 @@ struct PrefixMaps {
 struct PrefixGroup {
   int a, e, whole, pairs, tiles;
   int span, start;
+  bool bad;  // outside the batch or of negative size (and empty here)
 };
 
 __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams &p, int g, bool report) {
@@ -71,6 +72,7 @@ __device__ __forceinline__ PrefixGroup prefix_group(const PrefixParams &p, int g
   const int n = checked_load(p.prefix_lens, g, p.num_groups, status);
   if (a < 0 || e < a || e > p.own.batch) {
     if (report) raise_status(status, FA_DEV_BAD_SEQLEN);
+    r.bad = true;
     return r;
   }
   r.a = a;
@@ -114,11 +116,29 @@ template <int WHAT>
 __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool report,
                                             PrefixGroup &found, PrefixSums *sums, int apart = 0) {
   const int lane = threadIdx.x & 31;
-  int base = 0;
-  bool hit = false;
+  int base = 0, reached = 0;  // of the groups before these: their work, their largest end
+  bool hit = false, falls = false;
   if (sums) *sums = {};
   for (int g0 = 0; g0 < p.num_groups && !(hit && !sums); g0 += 32) {
     PrefixGroup r = prefix_group(p, g0 + lane, report);
+    // A group begins where the one before it ends, so groups in order do not
+    // overlap.  Behind one that is not, a group that begins inside an earlier one is
+    // passed over too: both would write their sequences' states.
+    falls = falls || __any_sync(0xffffffffu, r.bad);
+    if (falls) {
+      int end = max(reached, r.e);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
+      int before = __shfl_up_sync(0xffffffffu, end, 1);
+      if (lane == 0) before = reached;
+      if (r.a < before && r.a < r.e) {
+        if (report) raise_status(p.own.status, FA_DEV_BAD_SEQLEN);
+        r = PrefixGroup{};
+      }
+      reached = __shfl_sync(0xffffffffu, end, 31);
+    } else {
+      reached = __shfl_sync(0xffffffffu, r.e, 31);  // (the last step's is not looked at)
+    }
     r.span = apart > 0 ? (r.tiles + apart - 1) / apart * apart : r.tiles;
     const int work = r.span * r.pairs * p.head_rounds;
     int incl = work;

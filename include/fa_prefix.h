@@ -58,9 +58,10 @@ size_t fa_decode_prefix_workspace_size(int batch, int H, int Hkv, int d, int max
  * the group's sequences that see them, whatever their weight; values past a
  * sequence's own context reach nothing of it.  (A sequence shorter than its
  * prefix whose group holds such values behind its keys is summed on its own.)
- * Device-side checks: FA_DEV_BAD_SEQLEN (a group outside the batch or of
- * negative size: it is passed over, and sequences in no other group read all
- * keys as their own), FA_DEV_BAD_CTX (prefix_lens outside [0, max_prefix_len]
+ * Device-side checks: FA_DEV_BAD_SEQLEN (a group outside the batch, of
+ * negative size, or, behind such a one, that begins before the end of an earlier
+ * one: it is passed over, and sequences in no other group read all keys as their
+ * own), FA_DEV_BAD_CTX (prefix_lens outside [0, max_prefix_len]
  * or the table: nothing is shared; ctx_lens negative, beyond the table or with
  * more own keys than max_own_len: the row gets out = 0 and lse = -inf),
  * FA_DEV_BAD_BLOCK (rows that need the block hold nothing of use).

@@ -534,3 +534,47 @@ def test_short_sequences_keep_what_is_theirs(fa, shared):
     x.check(out, lse, only=[1])
     assert torch.isnan(out[3, 5]).all() and torch.isnan(lse[3, 5])
     assert torch.isfinite(out[3, [0, 1, 2, 3, 4, 6, 7]]).all()
+
+
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("cu,kept", [
+    ([0, 4, 2, 6], [0]), ([0, 4, 2, 4], [0]), ([0, 6, 5, 3, 6], [0]), ([0, 2, 1, 4, 3, 6], [0]),
+    ([0, 3, 1, 3, 6], [0, 3]), ([2, 0, 4, 4, 6], [1, 2, 3]),
+])
+def test_groups_that_go_back(fa, cu, kept, shared):
+    """cu_groups that falls: a group that would begin inside an earlier one is
+    passed over as the one of negative size is, and its sequences read their keys
+    as own ones."""
+    x = Batch([(700, [720, 705, 710, 800, 777, 701])], 8, 2, 128, seed=70, shared=shared)
+    groups = len(cu) - 1
+    args = x.args(cu_groups=dev(np.int32(cu)), max_own_len=800,
+                  prefix_lens=dev(np.int32([700 - 16 * g for g in range(groups)])))
+    ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(6, 8, 2, 128, x.max_pre, 800))
+    first = fa.fa_decode_paged_prefix(**args, workspace=ws)
+    torch_mod().cuda.synchronize()
+    assert fa.fa_last_device_status(ws) == fa.FA_DEV_BAD_SEQLEN
+    x.check(*first)
+    for _ in range(3):
+        again = fa.fa_decode_paged_prefix(**args, workspace=ws)
+        assert all(torch_mod().equal(p, q) for p, q in zip(again, first))
+    # the groups that stand, alone in the call
+    for g in kept:
+        x.check(*fa.fa_decode_paged_prefix(**{**args, "cu_groups": dev(np.int32(cu[g:g + 2])),
+                                              "prefix_lens": args["prefix_lens"][g:g + 1]}, workspace=ws))
+        assert fa.fa_last_device_status(ws) == 0
+    assert fa.fa_device_status(clear=True) == fa.FA_DEV_BAD_SEQLEN
+
+
+def test_groups_that_go_back_far_down(fa):
+    """The same among more than 32 groups, so that the walk over them has steps."""
+    n = 80
+    x = Batch([(320, [330 + b for b in range(n)])], 4, 2, 64, seed=71)
+    cu = list(range(0, 60)) + [50] + list(range(51, 70))   # group 59 falls, 60 to 68 begin too early
+    args = x.args(cu_groups=dev(np.int32(cu)), prefix_lens=dev(np.int32([320] * (len(cu) - 1))),
+                  max_own_len=410)
+    ws = fa.new_workspace(fa.fa_decode_prefix_workspace_size(n, 4, 2, 64, x.max_pre, 410))
+    out, lse = fa.fa_decode_paged_prefix(**args, workspace=ws)
+    torch_mod().cuda.synchronize()
+    assert fa.fa_last_device_status(ws) == fa.FA_DEV_BAD_SEQLEN
+    assert fa.fa_device_status(clear=True) == fa.FA_DEV_BAD_SEQLEN
+    x.check(out, lse)
