@@ -171,12 +171,15 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   if (static_cast<long long>(num_blocks) * block_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   if (batch == 0) return FA_OK;
   const int group = H / Hkv, seqs = kPrefillBM / group;
-  // Key tiles are counted in int, whatever groups the arrays name: a batch's
-  // worth for each.
+  // Key tiles are counted in int, whatever groups the arrays name: those that stand
+  // do not overlap, so they have at most a batch's worth of pairs of row tiles each,
+  // and all of them one batch's worth and a pair for each group of some sequences.
+  // (Every CTA walks over all groups, hence their limit.)
   const long long tiles = (max_prefix_len + kPrefixTileKeys - 1LL) / kPrefixTileKeys;
   const long long pairs = (batch + 2LL * seqs - 1) / (2 * seqs);
-  if (num_groups > batch || tiles * Hkv * pairs > 0x7fffffffLL / std::max(1, num_groups))
-    return FA_ERR_UNSUPPORTED;
+  const long long all_pairs =
+      std::min(num_groups * pairs, pairs + std::min<long long>(num_groups, batch));
+  if (num_groups > 65535 || tiles * Hkv * all_pairs > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const int max_own = max_own_len + kDecodeBlock - 1;
   const bool alone = prefix_alone(batch, Hkv, d, max_prefix_len, max_own_len);
   const DecodeWs w = decode_ws(

@@ -65,9 +65,10 @@ size_t fa_decode_prefix_workspace_size(int batch, int H, int Hkv, int d, int max
  * or the table: nothing is shared; ctx_lens negative, beyond the table or with
  * more own keys than max_own_len: the row gets out = 0 and lse = -inf),
  * FA_DEV_BAD_BLOCK (rows that need the block hold nothing of use).
- * Supported: d in {64, 128}, H / Hkv <= 16, num_groups <= batch, and
- * num_groups * ceil(batch / (2 floor(128 / (H / Hkv)))) * Hkv *
- * ceil(max_prefix_len / 128) below 2^31.  Three kernels: the shared keys on the
+ * Supported: d in {64, 128}, H / Hkv <= 16, num_groups <= 65535 (above the batch
+ * too: groups may be empty), and, with n = ceil(batch / (2 floor(128 / (H / Hkv)))),
+ * min(num_groups n, n + min(num_groups, batch)) * Hkv * ceil(max_prefix_len / 128)
+ * below 2^31.  Three kernels: the shared keys on the
  * tensor cores, the own keys beside them, and the (m, l, o) combine; a call over
  * few keys reads them all as own ones (the results are the same up to the order
  * of the sums).

@@ -578,3 +578,12 @@ def test_groups_that_go_back_far_down(fa):
     assert fa.fa_last_device_status(ws) == fa.FA_DEV_BAD_SEQLEN
     assert fa.fa_device_status(clear=True) == fa.FA_DEV_BAD_SEQLEN
     x.check(out, lse)
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_more_groups_than_sequences(fa, shared):
+    """An array of groups of a fixed size, empty ones behind and between."""
+    x = Batch([(500, [520, 510]), (0, []), (64, [100]), *[(0, [])] * 60], 8, 2, 64, seed=90, shared=shared)
+    out, lse = fa.fa_decode_paged_prefix(**x.args())
+    assert_device_clean()
+    x.check(out, lse)

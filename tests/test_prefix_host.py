@@ -78,3 +78,20 @@ def test_workspace_sizes_rise(lib):
     assert size(1, 8, 2, 96, 1, 1) == 0 and size(1, 7, 2, 64, 1, 1) == 0 and size(-1, 8, 2, 64, 1, 1) == 0
     assert size(1, 8, 2, 64, -1, 1) == 0 and size(1, 8, 2, 64, 1 << 30, 1 << 30) == 0
     assert size(1, 8, 2, 64, 1, 1, block_size=32) == 0
+
+
+def test_more_groups_than_sequences_are_taken(lib):
+    """Empty groups are no work: up to 65535 of them, whatever the batch, as long as
+    the sequences cannot make too much of it (-4: the call came to its workspace)."""
+    def call(groups, batch=2, mp=64, width=8, Hkv=2):
+        return lib.fa_decode_paged_prefix(P, P, P, P, width, P, P, P, groups, mp, 64, batch, 4 * Hkv,
+                                          Hkv, 128, 16, 8, 0.1, P, NULL, NULL, 0, NULL)
+    assert call(3) == -4 and call(2) == -4 and call(65535) == -4
+    assert call(65536) == -2 and call((1 << 31) - 1) == -2
+    # 4096 sequences, 64 Ki keys shared: 8192 slots for groups are no more work than 4096
+    big = dict(batch=4096, mp=1 << 16, width=1 << 12, Hkv=8)
+    assert call(1, **big) == -4 and call(4096, **big) == -4 and call(8192, **big) == -4
+    assert call(65535, **big) == -4
+    # 60000 sequences that may be a group each, over 2^29 keys
+    assert call(1, batch=60000, mp=1 << 29, width=1 << 26) == -2
+    assert call(60000, batch=60000, mp=1 << 29, width=1 << 26) == -2
