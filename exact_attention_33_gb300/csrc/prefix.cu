@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
     uint8_t *stage0 = smem + (is_k ? L::kK : L::kV);
     int issued = 0, q_issued = 0;
+    unsigned zeros = 0;  // stages whose place for this lane's block holds zeros
     bool ok = true;
     do {
       // The table row to read the blocks through: a sequence's row holds its own
@@ -296,9 +297,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const unsigned live = __ballot_sync(0xffffffffu, there);
         if (mine && !there) {
           if (is_k && id != -2) raise_status(status, FA_DEV_BAD_BLOCK);
-          for (int t = 0; t < kBlockBytes / 16; ++t)
-            reinterpret_cast<uint4 *>(dst)[t] = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
+          if ((zeros >> st & 1u) == 0u) {
+            for (int t = 0; t < kBlockBytes / 16; ++t)
+              reinterpret_cast<uint4 *>(dst)[t] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+          zeros |= 1u << st;
+        } else {
+          zeros &= ~(1u << st);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(live) * kBlockBytes);
