@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   PrefixSums sums;
   PrefixGroup g{};
   const PrefixFirst first = prefix_first(p);
-  prefix_walk<kPrefixNone>(p, 0, blockIdx.x == 0 && warp == 0, g, &sums);
+  prefix_walk<kPrefixNone>(p, 0, blockIdx.x == 0 && warp == 0, g, &sums, 0, &first);
   const PrefixPlan plan = prefix_plan(p, sums, first);
   const int my_team = blockIdx.x / p.team_heads;
   if (static_cast<long long>(my_team) * plan.per >= plan.total) return;  // the whole CTA
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
   PrefixSums sums;
   PrefixGroup g{};
   const PrefixFirst firsts = prefix_first(p);
-  if (!prefix_walk<kPrefixBySeq>(p, b, false, g, &sums)) g = PrefixGroup{};
+  if (!prefix_walk<kPrefixBySeq>(p, b, false, g, &sums, 0, &firsts)) g = PrefixGroup{};
   const PrefixPlan plan = p.alone ? PrefixPlan{0, 1, true} : prefix_plan(p, sums, firsts);
   const int per = plan.per;
   const int ctx = prefix_ctx(p, b, g.whole, false);  // (decode_own.cu reports)

@@ -100,33 +100,57 @@ struct PrefixPlan {
 // What the search is for: the group of a sequence, or of a key tile.
 constexpr int kPrefixNone = 0, kPrefixBySeq = 1, kPrefixByTile = 2;
 
+// Keys of the batch's sequences (of a large batch's every `skip`-th), four a lane:
+// loaded before the walk over the groups, whose loads they then do not wait for.
+constexpr int kPrefixFirst = 4;
+struct PrefixFirst {
+  int keys[kPrefixFirst];
+};
+__device__ __forceinline__ int prefix_skip(const PrefixParams &p) {
+  return (p.own.batch + 32 * kPrefixFirst - 1) / (32 * kPrefixFirst);
+}
+__device__ __forceinline__ PrefixFirst prefix_first(const PrefixParams &p) {
+  const int lane = threadIdx.x & 31, skip = prefix_skip(p);
+  PrefixFirst f;
+#pragma unroll
+  for (int i = 0; i < kPrefixFirst; ++i) {
+    const int b = (lane + 32 * i) * skip;
+    f.keys[i] = b < p.own.batch ? checked_load(p.own.ctx_lens, b, p.own.batch, p.own.status) : 0;
+  }
+  return f;
+}
+
 // Walks over the groups, 32 at a time (all lanes of a converged warp).  Finds
 // the group that `what` and `key` ask for, into `found`; false if there is none.
-// Sums the work; key tiles of pairs with two row tiles and with one, the shared
-// blocks and, once more for each sequence, the blocks that it shares, are this
-// lane's groups' alone.  Of the first 32 groups lane l keeps the l-th one's pairs
-// and their key tiles.  `apart`: 0, or the stretch that pairs are rounded up to.
+// Sums the work; key tiles of pairs with two row tiles and with one and the shared
+// blocks are this lane's groups' alone; with `first`, `covered` is the blocks that
+// this lane's of those sequences share.  Of the first 32 groups lane l keeps the l-th
+// one's pairs and their key tiles.  `apart`: 0, or the stretch that pairs are rounded
+// up to.
 struct PrefixSums {
   int total;
   int tiles2, tiles1;
-  long long blocks, shared_blocks;
+  long long blocks;
+  int covered;
   int pairs, tiles;
 };
 template <int WHAT>
 __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool report,
-                                            PrefixGroup &found, PrefixSums *sums, int apart = 0) {
+                                            PrefixGroup &found, PrefixSums *sums, int apart = 0,
+                                            const PrefixFirst *first = nullptr) {
   const int lane = threadIdx.x & 31;
   int base = 0, reached = 0;  // of the groups before these: their work, their largest end
   bool hit = false, falls = false;
   if (sums) *sums = {};
   for (int g0 = 0; g0 < p.num_groups && !(hit && !sums); g0 += 32) {
     PrefixGroup r = prefix_group(p, g0 + lane, report);
+    int end = g0 + lane < p.num_groups ? r.e : 0x7fffffff;  // the largest up to this group's
     // A group begins where the one before it ends, so groups in order do not
     // overlap.  Behind one that is not, a group that begins inside an earlier one is
     // passed over too: both would write their sequences' states.
     falls = falls || __any_sync(0xffffffffu, r.bad);
     if (falls) {
-      int end = max(reached, r.e);
+      end = max(reached, end);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
       int before = __shfl_up_sync(0xffffffffu, end, 1);
@@ -135,10 +159,8 @@ __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool
         if (report) raise_status(p.own.status, FA_DEV_BAD_SEQLEN);
         r = PrefixGroup{};
       }
-      reached = __shfl_sync(0xffffffffu, end, 31);
-    } else {
-      reached = __shfl_sync(0xffffffffu, r.e, 31);  // (the last step's is not looked at)
     }
+    reached = __shfl_sync(0xffffffffu, end, min(31, p.num_groups - 1 - g0));
     r.span = apart > 0 ? (r.tiles + apart - 1) / apart * apart : r.tiles;
     const int work = r.span * r.pairs * p.head_rounds;
     int incl = work;
@@ -171,7 +193,24 @@ __device__ __forceinline__ bool prefix_walk(const PrefixParams &p, int key, bool
       sums->tiles2 += r.tiles * (r.pairs - single);
       sums->tiles1 += r.tiles * single;
       sums->blocks += n > 0 ? r.whole / kDecodeBlock : 0;
-      sums->shared_blocks += static_cast<long long>(r.whole / kDecodeBlock) * n;
+      if (first) {
+        // (rolled: what is fetched to run once costs more than the loop)
+        const int skip = prefix_skip(p);
+#pragma unroll 1
+        for (int i = 0; i < kPrefixFirst && 32 * i * skip < reached; ++i) {
+          const int b = (lane + 32 * i) * skip;
+          const int keys = i < 2 ? (i == 0 ? first->keys[0] : first->keys[1])
+                                  : (i == 2 ? first->keys[2] : first->keys[3]);
+          int l = 0;  // the first group that ends behind b
+          if (p.num_groups > 1)
+#pragma unroll 1
+            for (int o = 16; o > 0; o >>= 1)
+              if (__shfl_sync(0xffffffffu, end, l + o - 1) <= b) l += o;
+          const int a = __shfl_sync(0xffffffffu, r.a, l), e = __shfl_sync(0xffffffffu, r.e, l);
+          const int whole = __shfl_sync(0xffffffffu, r.whole, l);
+          if (a <= b && b < e) sums->covered += min(max(0, keys), whole) / kDecodeBlock;
+        }
+      }
       if (g0 == 0) {
         sums->pairs = r.pairs * p.head_rounds;
         sums->tiles = r.tiles;
@@ -187,26 +226,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Keys of the batch's first sequences, four a lane: loaded before the walk over
-// the groups, whose loads they then do not wait for.
-constexpr int kPrefixFirst = 4;
-struct PrefixFirst {
-  int keys[kPrefixFirst];
-};
-__device__ __forceinline__ int prefix_skip(const PrefixParams &p) {
-  return (p.own.batch + 1023) / 1024;  // a large batch's every `skip`-th counts
-}
-__device__ __forceinline__ PrefixFirst prefix_first(const PrefixParams &p) {
-  const int lane = threadIdx.x & 31, skip = prefix_skip(p);
-  PrefixFirst f;
-#pragma unroll
-  for (int i = 0; i < kPrefixFirst; ++i) {
-    const int b = (lane + 32 * i) * skip;
-    f.keys[i] = b < p.own.batch ? checked_load(p.own.ctx_lens, b, p.own.batch, p.own.status) : 0;
-  }
-  return f;
 }
 
 // The plan of a call, the same in every warp that asks (integers, and fp32
@@ -225,17 +244,13 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const P
   const int lane = threadIdx.x & 31;
   const int total = max(0, s.total), teams = p.teams;
   if (total <= teams) return {total, 1, false};
-  const int skip = prefix_skip(p);
-  long long keys = 0;
+  // blocks of their own that the sequences read
+  int mine = -s.covered;
 #pragma unroll
-  for (int i = 0; i < kPrefixFirst; ++i) keys += max(0, f.keys[i]);
-  for (int b = (lane + 32 * kPrefixFirst) * skip; b < p.own.batch; b += 32 * skip)
-    keys += max(0, checked_load(p.own.ctx_lens, b, p.own.batch, p.own.status));
-  // (a lane's blocks are cut off at 2^25: what a cache can hold is below 2^30)
+  for (int i = 0; i < kPrefixFirst; ++i) mine += max(0, f.keys[i]) / kDecodeBlock;
+  // (cut off at 2^25 a lane: such a call is bound by its bytes whatever the plan)
   constexpr long long kMost = 1 << 25;
-  const int own_blocks = __reduce_add_sync(
-      0xffffffffu, static_cast<int>(min(kMost, keys * skip / kDecodeBlock)) -
-                       static_cast<int>(min(kMost, s.shared_blocks)));
+  const int own_blocks = __reduce_add_sync(0xffffffffu, min(1 << 25, mine));
   const int once = __reduce_add_sync(0xffffffffu, static_cast<int>(min(kMost, s.blocks)));
   const int tiles2 = __reduce_add_sync(0xffffffffu, s.tiles2);
   const int tiles1 = __reduce_add_sync(0xffffffffu, s.tiles1);
@@ -254,7 +269,8 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const P
         even = max(even, (tiles - 1) / n + 1);
       }
     }
-  const float own_bytes = __fmul_rn(static_cast<float>(max(0, own_blocks)), p.block_bytes);
+  const float own_bytes = __fmul_rn(__fmul_rn(static_cast<float>(own_blocks), p.block_bytes),
+                                    static_cast<float>(prefix_skip(p)));
   const float all_bytes = __fadd_rn(own_bytes, __fmul_rn(static_cast<float>(once), p.block_bytes));
   const float tiles = __fadd_rn(static_cast<float>(tiles2), static_cast<float>(tiles1));
   const float tile_ns = __fmul_rn(__fadd_rn(__fmul_rn(static_cast<float>(tiles2), p.tile_ns2),
@@ -283,9 +299,9 @@ __device__ __forceinline__ PrefixPlan prefix_plan(const PrefixParams &p, const P
   const bool is_apart = __shfl_sync(0xffffffffu, apart <= line ? 1 : 0, l) != 0;
   per = __shfl_sync(0xffffffffu, is_apart ? even : per, l);
   if (!is_apart) return {total, per, false};
-  const int mine = __reduce_add_sync(
+  const int parts_of_all = __reduce_add_sync(
       0xffffffffu, s.tiles > 0 ? ((s.tiles - 1) / per + 1) * s.pairs : 0);
-  return {mine * per, per, true};
+  return {parts_of_all * per, per, true};
 }
 
 // The first key that a sequence of a group reads on its own.

@@ -587,3 +587,17 @@ def test_more_groups_than_sequences(fa, shared):
     out, lse = fa.fa_decode_paged_prefix(**x.args())
     assert_device_clean()
     x.check(out, lse)
+
+
+@pytest.mark.parametrize("members,idle,G", [(48, 16, 4), (100, 28, 4), (50, 14, 8)])
+def test_idle_slots_leave_the_plan_alone(fa, members, idle, G):
+    """Finished slots at a group's end have nothing to read and nothing to share:
+    the work is shared out as if they were in no group, bit for bit."""
+    torch = torch_mod()
+    x = Batch([(8192, [8192 + 37 + (i * 131) % 900 for i in range(members)] + [0] * idle)], 8 * G, 8,
+              128, seed=80)
+    inside = fa.fa_decode_paged_prefix(**x.args())
+    outside = fa.fa_decode_paged_prefix(**x.args(cu_groups=dev(np.int32([0, members]))))
+    assert_device_clean()
+    assert all(torch.equal(a, b) for a, b in zip(inside, outside))
+    x.check(*inside, only=[0, members - 1, members])
