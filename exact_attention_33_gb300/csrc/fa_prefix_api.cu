@@ -239,21 +239,26 @@ int fa_decode_paged_prefix(const void *q, const void *k_pool, const void *v_pool
   p.team_heads = team_heads(Hkv);
   p.head_rounds = Hkv / p.team_heads;
   p.teams = p.ctas / p.team_heads;
-  // Measured on one GB300 (d = 128): a key tile of 128 with two row tiles and with
-  // one, what a CTA takes before its first product and after its last and between
-  // two runs, what one more CTA costs the others (states, loads that contend); the
-  // own keys' CTAs read 62 GB/s on an SM that is left to them while the others
-  // work, and all reads come to 5.6 TB/s at most.  (4 groups over 15 k to 29 k keys: 110
-  // us, with 1400 instead of 1000 for a single row tile 114.)
-  p.tile_ns2 = d == 128 ? 1650.f : 1100.f;
-  p.tile_ns1 = d == 128 ? 1000.f : 650.f;
-  p.fixed_ns = 14500.f;
-  p.run_ns = 8000.f;
-  p.state_ns = d == 128 ? 150.f : 75.f;
+  // What prefix_plan's estimate is made of: ns of a key tile of 128 with two row
+  // tiles and with one, before a CTA's first product and after its last, between two
+  // runs, and what one more CTA costs the others; bytes a ns that the own keys' CTAs
+  // read on an SM that is left to them while the others work, and all at most.  All
+  // ten are fits, no times of anything by themselves (a key tile with two row tiles
+  // takes 1.65 us in a long run without own keys): of 53 batches (d = 64 and 128, 1 to
+  // 16 heads a group, 1 to 20 groups, own keys from none to twice the shared ones,
+  // idle slots) every stretch was timed.  The ones chosen so take 1.6% longer than the
+  // best, 15% at worst (4 unlike groups, d = 64); batches that were left out of the fit
+  // do nearly as well.  The constants before, taken at three batches of one shape,
+  // chose ones that take 6.2% longer, 38% at worst.
+  p.tile_ns2 = d == 128 ? 2600.f : 1500.f;
+  p.tile_ns1 = d == 128 ? 2600.f : 930.f;
+  p.fixed_ns = 6900.f;
+  p.run_ns = 5300.f;
+  p.state_ns = d == 128 ? 160.f : 39.f;
   p.block_bytes = 4.f * kDecodeBlock * d * Hkv;
   p.max_rate = 5600.f;
   p.max_rate_inv = 1.f / p.max_rate;
-  p.free_rate = 62.f;
+  p.free_rate = 51.f;
   p.max_slots = s.max_slots;
   p.k_pool = k_pool;
   p.v_pool = v_pool;
