@@ -4,11 +4,11 @@
 // product in fp32 is off by 2^-24 of itself (at position 10^6 by 0.06 rad).
 // So turns a position, inv_freq / 2 pi, are made a 64-bit fraction of a turn,
 // and the product with a position is one integer multiplication: it wraps at
-// whole turns by itself and is exact.  Its upper half, 2^-32 of a turn, goes into
-// sin and cos.  The fraction is formed in integers too: with the few fp64
-// instructions that it takes otherwise, this GPU's fp64 rate bound every kernel
-// here (73 k packed tokens of 16 / 4 heads of d = 128, both directions, 261 us
-// against 232; 34.8 k tokens into the 8-bit cache 343 us against 148).
+// whole turns by itself and is exact.  Its upper 56 bits go into sin and cos.  The
+// fraction is formed in integers too: with the few fp64 instructions that it takes
+// otherwise, this GPU's fp64 rate bound every kernel here (73 k packed tokens of 16 / 4
+// heads of d = 128, both directions, 261 us against 232; 34.8 k tokens into the 8-bit
+// cache 343 us against 148).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -38,18 +38,25 @@ __device__ __forceinline__ uint64_t rope_turns(double inv_freq) {
   return bits >> 63 ? 0 - t : t;
 }
 
-// sin and cos of v 2^-32 turns, at most an eighth of a turn either way: the
-// angle in two floats t + tl, the Taylor series' terms behind the first one (of
-// cos: behind 1 - t^2 / 2, also in two floats) with their rounding errors and tl
-// added to it last.  So there is little but the last rounding: 0.29 units in the
-// last place root mean square, at most 0.82.  Keys on their way to e4m3 whose code
-// is not that of the exact product are so 1.07 in a million, with sincospif 1.33 (50
-// million counted); the calls take the same time.
-__device__ __forceinline__ void sin_cos_eighth(int32_t v, float &s, float &c) {
+// sin and cos of v + below 2^-32 (2^-32 turns), at most an eighth of a turn either
+// way: the angle in two floats t + tl, the Taylor series' terms behind the first one
+// (of cos: behind 1 - t^2 / 2, also in two floats) with their rounding errors and tl
+// added to it last.  t is of the nearest multiple of 128, so that small angles of
+// either sign lie in tl alone and nothing cancels.  So there is little but the last
+// rounding: 0.29 units in the last place root mean square; sin is within 3.1 x 2^-24
+// of itself from 2^-32 of a turn up (1.2 units above 64 x 2^-32) and within 2^-54 of a
+// turn below, cos within 2^-24.  Keys on their way to e4m3 whose code is not that of
+// the exact product are so 1.09 in a million, with sincospif 1.33 (50 million counted);
+// the calls take the same time.
+__device__ __forceinline__ void sin_cos_eighth(int32_t v, uint32_t below, float &s, float &c) {
   constexpr float K = 0x1.921fb6p-30f, Kl = -0x1.777a5cp-55f;  // 2 pi 2^-32
-  const float vh = static_cast<float>(v & ~127), vl = static_cast<float>(v & 127);
+  const int32_t near = (v + 64) & ~127;
+  const float vh = static_cast<float>(near);
+  // what is left, in 2^-24ths of v's units
+  const float vl = static_cast<float>(static_cast<int32_t>(
+      __funnelshift_l(below, static_cast<uint32_t>(v - near), 24)));
   const float t = vh * K;
-  const float tl = fmaf(vh, K, -t) + fmaf(vh, Kl, vl * K);
+  const float tl = fmaf(vh, K, -t) + fmaf(vh, Kl, vl * (K * 0x1p-24f));
   const float w = t * t, wl = fmaf(t, t, -w);
   const float h = fmaf(-0.5f, w, 1.f);  // 1 - w / 2
   float q = fmaf(w, 1.f / 362880.f, -1.f / 5040.f);
@@ -64,13 +71,13 @@ __device__ __forceinline__ void sin_cos_eighth(int32_t v, float &s, float &c) {
 }
 
 // cos and sin of p positions' turns: the nearest quarter of a turn by signs and
-// places, the rest as above (2^-32 of a turn).
+// places, the rest as above.
 __device__ __forceinline__ float2 rope_cos_sin(uint64_t turns, int p) {
   const uint64_t a = turns * static_cast<uint64_t>(static_cast<int64_t>(p));
   const uint32_t hi = static_cast<uint32_t>(a >> 32);  // 2^32 of a turn
   const uint32_t quarter = (hi + 0x20000000u) >> 30;
   float s, c;
-  sin_cos_eighth(static_cast<int32_t>(hi - (quarter << 30)), s, c);
+  sin_cos_eighth(static_cast<int32_t>(hi - (quarter << 30)), static_cast<uint32_t>(a), s, c);
   const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
   return make_float2((quarter + 1u) & 2u ? -x : x, quarter & 2u ? -y : y);
 }

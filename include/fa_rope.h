@@ -15,10 +15,11 @@
  *              How contexts are stretched (slower frequencies for some pairs)
  *              is in these values and in factor.
  *   factor   : finite and > 0 (1, or what a stretched context wants)
- * The angle is the exact product, reduced to one turn in 64-bit integers
- * (turns a position are held to 2^-53 of themselves or 2^-64): a position of 2^31 costs
- * no accuracy that bf16 values show.  Values are rotated in fp32 and rounded
- * once.
+ * The angle is the exact product, reduced to one turn in 64-bit integers (turns a
+ * position are held to 2^-53 of themselves or 2^-64, the angle to 2^-56 of a turn): a
+ * position of 2^31 costs no accuracy that bf16 values show, and the sine of a small
+ * angle of either sign is as near as that of a large one.  Values are rotated in
+ * fp32 and rounded once.
  *
  * Conventions and statuses are those of fa.h.  Rows of one token are dense
  * ([heads, d]); tokens lie `stride` elements apart, a multiple of 8 and at

@@ -620,3 +620,47 @@ def test_training_run(fa):
             # (its own tests); against a random direction that is 1.5e-2 |grad| and one
             # rounding more, times a normal factor (5 of them: one in a million)
             assert abs(diff - (grad * u).sum()) <= 5 * 2e-2 * np.linalg.norm(grad), i
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_angles_hold_their_last_places(fa, inter, back, sign):
+    """a cos t - b sin t with b t next to a, so that what sin is off by shows: angles
+    from 2^-28 to a quarter, both signs.
+
+    From 2^-32 of a turn up sin is within 3.1 x 2^-24 of itself and cos within 0.98;
+    b sin t and a cos t are about 1, and their products round once each (2^-24 and
+    2^-25; the sum's rounding is of the small result); turns a position are held to
+    2^-64, at most 2^-26 of the angles here: 5.9 x 2^-24 in all, and half a step of
+    bf16."""
+    rng = np.random.default_rng(5)
+    rot, heads = 128, 3
+    for pos, least in [(1, -27), (7, -27), (-1, -27), (-12, -20), (100003, -14)] * 5:
+        mag = np.exp2(rng.uniform(least, -2, rot // 2))
+        b = np.exp2(np.round(-np.log2(mag))) * np.round(rng.uniform(1, 2, rot // 2) * 128) / 128 * sign
+        freq = (1 - 2.0 ** -13) / b / pos
+        x = rr.join(np.ones((1, heads, rot // 2)),
+                    np.broadcast_to(-b if back else b, (1, heads, rot // 2)),
+                    np.zeros((1, heads, rot)), rot, inter)
+        call = fa.fa_rope_bwd if back else fa.fa_rope
+        out, _ = call(bf16(x), None, dev(freq), positions=dev(np.int32([pos])), interleaved=inter)
+        got, _ = rr.split(host(out), rot, inter)
+        t = freq * float(pos)
+        want = np.cos(t) - b * np.sin(t)
+        off = np.abs(got[0] - want) - (rr.U * np.abs(want) + (1 + rr.U) * 5.9 * 2.0 ** -24)
+        assert off.max() <= 0, (pos, t[off.max(0).argmax()], off.max())
+    assert_device_clean()
+
+
+def test_slow_pairs_at_small_positions(fa):
+    """The slowest pair of a stretched context at its first positions: sin is as
+    near as bf16 lets it be."""
+    freq = rr.frequencies(128, base=500000.0) / 32
+    pos = np.arange(-5, 6, dtype=np.int32)
+    x = np.zeros((len(pos), 1, 128))
+    x[..., :64] = 1.0
+    out, _ = fa.fa_rope(bf16(x), None, dev(freq), positions=dev(pos))
+    got = host(out)[:, 0, 64:]
+    want = np.sin(pos[:, None] * freq)
+    assert (np.abs(got - want) <= (rr.U + 4 * 2.0 ** -24) * np.abs(want)).all()
