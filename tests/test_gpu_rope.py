@@ -664,3 +664,37 @@ def test_slow_pairs_at_small_positions(fa):
     got = host(out)[:, 0, 64:]
     want = np.sin(pos[:, None] * freq)
     assert (np.abs(got - want) <= (rr.U + 4 * 2.0 ** -24) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("ctx,new,H,Hkv,d,rot,inter,factor", [a for a in APPEND if a[5]])
+def test_both_writes_turn_alike(fa, ctx, new, H, Hkv, d, rot, inter, factor):
+    """The 8-bit write's queries are the bf16 write's bit for bit, and its keys
+    within half a step of e4m3 and what fp32 may be off by.
+
+    cos and sin are within 2.5 x 2^-24 of themselves (3.1 for the smallest angles),
+    the factor, the products and the sum round once each: 6.1 x 2^-24 of |a cos| + |b
+    sin|; the product of position and frequency is held to 2^-53 of itself here and
+    there, so the angle to 2^-51 (and 2^-50 rad).  Half a step at the value that was rounded is that
+    at the exact one and 2^-4 of what lies between."""
+    torch = torch_mod()
+    r = Run(ctx, new, H, Hkv, d, rot, inter, factor, seed=sum(ctx) + d)
+    pools = [torch.zeros((r.blocks, 16, Hkv, d), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    pools8 = [torch.zeros((r.blocks, 16, Hkv, d), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scales = [torch.zeros((r.blocks, Hkv), device="cuda") for _ in "kv"]
+    q = r.call(fa, pools)
+    q8 = r.call(fa, [*pools8, *scales], fp8=True)
+    assert_device_clean()
+    assert q is None or torch.equal(q.view(torch.int16), q8.view(torch.int16))
+    blk, slot = r.slots()
+    s = scales[0].double().cpu().numpy()[blk][..., None]
+    real = W.e4m3_decode(pools8[0].cpu().numpy()[blk, slot]) * s
+    k64 = r.k[:r.T].astype(np.float64)
+    want = rr.rotate(k64, r.pos, r.freq, r.factor, inter)
+    t = np.asarray(r.pos, np.float64)[:, None, None] * r.freq
+    a, b = (np.abs(z) for z in rr.split(k64, rot, inter))
+    c, sn = np.abs(np.cos(t)), np.abs(np.sin(t))
+    turn = (np.abs(t) * 2.0 ** -51 + 2.0 ** -50) * (a + b)
+    off = float(r.factor) * rr.join(a * c + b * sn, a * sn + b * c, np.zeros_like(k64), rot, inter)
+    off = 6.1 * 2.0 ** -24 * off + float(r.factor) * rr.join(turn, turn, np.zeros_like(k64), rot, inter)
+    tol = np.maximum(rr.HALF_E4M3 * (np.abs(want) + off), s * 2.0 ** -10) + off
+    assert (np.abs(real - want) <= tol * (1 + 2.0 ** -40)).all()
