@@ -1215,6 +1215,8 @@ def fa_rope_frequencies(rot_dim, base=10000.0, stretch=1.0, method="parts", trai
     * ``"parts"``: pairs that turn fewer than ``slow_turns`` times over the trained
       length are slowed by ``stretch``, those that turn more than ``fast_turns``
       times are left, in between linearly; the factor is 0.1 ln(stretch) + 1.
+      (Models that slow their pairs so without a factor pass 1 to the calls below in
+      its place; the frequencies are the same.)
     """
     torch = _torch()
     rot_dim, base, stretch = int(rot_dim), float(base), float(stretch)

@@ -61,9 +61,10 @@ size_t fa_decode_prefix_workspace_size(int batch, int H, int Hkv, int d, int max
  * Device-side checks: FA_DEV_BAD_SEQLEN (a group outside the batch, of
  * negative size, or, behind such a one, that begins before the end of an earlier
  * one: it is passed over, and sequences in no other group read all keys as their
- * own), FA_DEV_BAD_CTX (prefix_lens outside [0, max_prefix_len]
- * or the table: nothing is shared; ctx_lens negative, beyond the table or with
- * more own keys than max_own_len: the row gets out = 0 and lse = -inf),
+ * own), FA_DEV_BAD_CTX (prefix_lens outside [0, max_prefix_len] or the table:
+ * nothing is shared; ctx_lens negative, beyond the table or more than
+ * max_own_len + 15 keys behind the shared blocks: the row gets out = 0 and lse =
+ * -inf),
  * FA_DEV_BAD_BLOCK (rows that need the block hold nothing of use).
  * Supported: d in {64, 128}, H / Hkv <= 16, num_groups <= 65535 (above the batch
  * too: groups may be empty), and, with n = ceil(batch / (2 floor(128 / (H / Hkv)))),

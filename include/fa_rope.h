@@ -72,7 +72,8 @@ int fa_rope_bwd(const void *dq, const void *dk, int64_t dq_stride, int64_t dk_st
  *   inv_freq       : NULL with rot_dim 0: nothing is rotated, rows are copied
  *   k_pool, v_pool : bf16 [num_blocks, block_size, Hkv, d], block_size == 16
  *   cu_seqlens     : int32 DEVICE array [batch + 1] (rules as fa_fwd_varlen)
- *   max_new        : an upper bound of every sequence's n (sizes the launch)
+ *   max_new        : an upper bound of every sequence's n (sizes the launch; 0:
+ *                    nothing is done, nor looked at)
  * Slots behind the new ones, rows of q_out behind the last sequence and every
  * other block stay as they are.  A written block belongs to one sequence.
  * Device-side checks: FA_DEV_BAD_SEQLEN (bad cu_seqlens, or n > max_new),
