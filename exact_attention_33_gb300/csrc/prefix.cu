@@ -34,7 +34,7 @@
 // SMs; with few rows the feed, 5.2 TB/s.  A call has 9 us before its first product
 // (plan 3.4, block ids 1.3, ring 4) and 5 to 7 behind its last in the combine.
 // 64 sequences over 8192 shared keys and 1 to 1024 of their own, 32 / 8 heads: 41 us
-// where the ordinary call takes 216; 256 over 16384 and 1 to 512: 97 and 1537.
+// where the ordinary call takes 216; 256 over 16384 and 1 to 512: 95 and 1537.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -780,9 +780,9 @@ __global__ void __launch_bounds__(32 * kPrefixCombineWarps, kPrefixCombineCtas)
   // A sequence that ends inside the shared keys meets the values behind its own with
   // weight 0 in the products, and 0 times an infinity or a NaN is a NaN: then its
   // rows are summed again over its own keys alone.  That takes 0.25 us a key (8000
-  // keys 2 ms), and no cache of finite values comes there.  (Its code costs a call
-  // of 42 or 97 us up to 0.9 by being there, in line or out of it, and 1.3 in the own
-  // keys' kernel: more instructions come through a cold L2.)
+  // keys 2 ms), and no cache of finite values comes there.  (That the code is there
+  // moved calls of 41 to 97 us by 0 to 1.2 us, in line or out of it, here or in the
+  // own keys' kernel, as any change of what comes through a cold L2 does.)
   const bool ends_inside = !p.alone && live && ctx < g.whole;
   bool again = false;
   // this kernel's own (checked-build) index errors go to the device word only
